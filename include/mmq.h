@@ -48,6 +48,7 @@ typedef struct mmq_weights_s *mmq_weights_t;
 #define MMQ_ERR_UNSUPPORTED -7     /* valid input this build does not handle */
 #define MMQ_ERR_NO_DEVICE -8       /* current device is not a GB300 (sm_103) */
 #define MMQ_ERR_SCRATCH_LIMIT -9   /* problem exceeds mmq_gemm_noalloc's fixed scratch */
+#define MMQ_ERR_DEVICE_INDEX -10   /* an index in device memory was out of range (mmq_last_device_error) */
 
 /* ---- weight types (ggml numbering) ------------------------------------- */
 #define MMQ_Q4_K 12
@@ -315,9 +316,171 @@ int mmq_gemm_noalloc(mmq_weights_t h, const void *Q, int64_t nt, float *Y, mmq_s
  */
 int mmq_debug_chunk_partials(mmq_weights_t h, const void *Q, int64_t nt, float *P, mmq_stream_t stream);
 
+/* ---- the serving step around the projections ---------------------------
+ * Four entry points that hand each other their outputs: page tables and slot
+ * maps from request lengths, the projections' K and V rows into a paged
+ * cache, attention of the new tokens over it, and the verification of drafted
+ * tokens, whose accepted counts give the next step's lengths.  Lengths stay
+ * on the device: nothing here synchronizes or reads them back, so every call
+ * can be captured into a CUDA graph and replayed on other lengths.
+ *
+ * Element types.  The values of MMQ_OUT_F16 / MMQ_OUT_F32, and bf16. */
+#define MMQ_DT_F16 1
+#define MMQ_DT_F32 2
+#define MMQ_DT_BF16 3
+
+/* A paged cache of keys and values.  Row (page, token, head) of K begins at
+ * element page*k_page + token*k_token + head*k_head and holds head_dim
+ * contiguous elements; V the same with its own strides.  So both
+ * [page][token][head][d] and [page][head][token][d] are strides of this.
+ * Slot s is token s % page_size of page s / page_size. */
+typedef struct mmq_paged_cache {
+  void *k, *v;                      /* device, 16-byte aligned */
+  int64_t k_page, k_token, k_head;  /* strides in elements, multiples of 8 */
+  int64_t v_page, v_token, v_head;
+  int64_t pages;                    /* >= 1 */
+  int32_t page_size;                /* >= 1, any size */
+  int32_t heads;                    /* K/V heads */
+  int32_t head_dim;                 /* a multiple of 8, at most 256 */
+  int32_t type;                     /* MMQ_DT_F16 or MMQ_DT_BF16 */
+} mmq_paged_cache;
+
+/*
+ * mmq_page_tables -- page tables, slot map and row starts of a step, built on
+ * the device from the requests' lengths.  Request b has cached[b] tokens in
+ * the cache, brings fresh[b] new ones and holds held[b] pages (it may hold
+ * more than its tokens fill, after refused drafted tokens).  With
+ *   need[b] = ceil((cached[b] + fresh[b]) / page_size)
+ * it takes need[b] - held[b] pages, if positive, from free_pages, in the
+ * order of the requests; table[b][held[b]..] receives them (the other entries
+ * are left as they are).
+ *   cached, fresh, held  device, int32, nreq each; negative counts as 0.
+ *   table       device, int32, nreq rows of table_width, row pitch
+ *               table_stride; read and extended in place.  Running the call
+ *               again on the same inputs writes the same.
+ *   free_pages  device, int32, nfree page ids (nfree >= 0).
+ *   q_start     device, int32, nreq + 1: the new tokens' first rows and their
+ *               total.   seq_lens  device, int32, nreq: cached + fresh.
+ *   held_out    device, int32, nreq: pages held now.
+ *   slots       device, int64, max_tokens: slot of every new token; -1 for a
+ *               token that found no page and behind the last token.
+ *   positions   device, int32, max_tokens: place of the token in its request;
+ *               -1 behind the last token.
+ *   taken       device, int32, 2: pages taken from the front of free_pages;
+ *               pages missing (free_pages too short or need > table_width;
+ *               their table entries are -1).
+ * New tokens past max_tokens get no slot.  nreq in 0..8192 (more:
+ * MMQ_ERR_UNSUPPORTED).  One kernel, no scratch.  Errors: MMQ_ERR_ARG,
+ * MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
+ */
+int mmq_page_tables(const int32_t *cached, const int32_t *fresh, const int32_t *held, int64_t nreq,
+                    int32_t *table, int64_t table_width, int64_t table_stride, const int32_t *free_pages,
+                    int64_t nfree, int32_t page_size, int64_t max_tokens, int32_t *q_start, int32_t *seq_lens,
+                    int32_t *held_out, int64_t *slots, int32_t *positions, int32_t *taken, mmq_stream_t stream);
+
+/*
+ * mmq_kv_write -- rows of K and V into their slots of a paged cache.
+ *   k, v     device, 16-byte aligned; element (t, head, i) at t*k_token +
+ *            head*k_head + i (strides multiples of 8 elements, so K and V may
+ *            be columns of a fused projection's output), cache->heads heads.
+ *   src_type MMQ_DT_F32, MMQ_DT_F16 or MMQ_DT_BF16; rounded to the cache's
+ *            type to nearest even, once.
+ *   slots    device, int64, ntok: a negative slot writes nothing; a slot past
+ *            the cache writes nothing and is reported by
+ *            mmq_last_device_error; a slot twice leaves either row.
+ *   ntok     >= 0; 0 is a no-op.
+ * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN, MMQ_ERR_TYPE, MMQ_ERR_NO_DEVICE,
+ * MMQ_ERR_CUDA.
+ */
+int mmq_kv_write(const mmq_paged_cache *cache, const void *k, int64_t k_token, int64_t k_head, const void *v,
+                 int64_t v_token, int64_t v_head, int src_type, const int64_t *slots, int64_t ntok,
+                 mmq_stream_t stream);
+
+/* Arguments of mmq_paged_attention. */
+typedef struct mmq_attention {
+  const void *q;             /* device, 16-byte aligned, the cache's type: (t, head, i) at t*q_token + head*q_head + i */
+  void *out;                 /* device, 16-byte aligned: (t, head, i) at t*out_token + head*out_head + i */
+  float *lse;                /* device, ntok x q_heads, or NULL */
+  const int32_t *table;      /* device, nreq rows of table_width page ids, row pitch table_stride */
+  const int32_t *seq_lens;   /* device, nreq: keys of each request, its new tokens among them */
+  const int32_t *q_start;    /* device, nreq + 1: first row of each request's new tokens, ascending from 0 */
+  int64_t q_token, q_head;   /* strides in elements, multiples of 8 */
+  int64_t out_token, out_head;
+  int64_t table_stride;
+  int64_t nreq, ntok;        /* requests; rows of q */
+  int32_t table_width;
+  int32_t q_heads;           /* a multiple of cache->heads: q head h reads K/V head h / (q_heads / heads) */
+  int32_t out_type;          /* the cache's type or MMQ_DT_F32 */
+  int32_t causal;            /* nonzero: a token sees no later one */
+  int32_t window;            /* > 0: a token sees the last `window` keys up to itself; 0: no window */
+  float scale;               /* of q . k; positive */
+} mmq_attention;
+
+/*
+ * mmq_paged_attention -- attention of each request's new tokens over its
+ * pages.  Token i of request b is at position p = seq_lens[b] - n + i, n =
+ * q_start[b+1] - q_start[b]; it sees keys j < seq_lens[b] with j <= p (causal)
+ * and j > p - window (window > 0).  out = softmax(scale q.k) v over them, lse
+ * the natural logarithm of their sum of exponentials; a row that sees no key
+ * gets out = 0, lse = -inf.  One token a request (a decode step), a few (drafted
+ * tokens) or thousands (a prompt's chunk) go through this one call, in any
+ * mixture.
+ *   Rows of q past q_start[nreq] belong to no request; their out and lse are
+ * not written.  seq_lens[b] = 0 and n = 0 are allowed.  Keys past seq_lens[b]
+ * are not used, whatever their memory holds, and table entries past the last
+ * key's page are not read.  A non-finite V row that some row of a chunk sees
+ * may also make rows of that chunk non-finite that do not see it.
+ *   A page id outside the cache, or seq_lens[b] past table_width*page_size, is
+ * reported by mmq_last_device_error; that request's rows are then unspecified.
+ *   Products and sums are fp32; the softmax weights are rounded to the
+ * cache's type before they multiply V.  The results of one problem do not
+ * change from call to call.
+ *   Long rows are split over the SMs when there are few of them: partial
+ * results (fp32, up to 256 MB) are stream-ordered scratch as for mmq_gemm.
+ * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN, MMQ_ERR_TYPE, MMQ_ERR_OOM,
+ * MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
+ */
+int mmq_paged_attention(const mmq_paged_cache *cache, const mmq_attention *args, mmq_stream_t stream);
+
+/* Arguments of mmq_verify_draft. */
+typedef struct mmq_verification {
+  const void *target;        /* device, type: probability of token v after drafted token i (row 0: before the
+                                first) at b*target_req + i*target_row + v, k + 1 rows a request */
+  const void *draft;         /* device, type: the draft's probabilities, k rows a request; NULL: the draft
+                                gave its token probability 1 */
+  const int32_t *tokens;     /* device: drafted token i of request b at b*tokens_stride + i */
+  const int32_t *n_draft;    /* device, nreq: drafted tokens of each request, 0..k; NULL: k */
+  const float *u;            /* device: uniform in [0, 1) at b*u_stride + i */
+  const float *noise;        /* device: independent exponential variates at b*noise_stride + v */
+  int32_t *out;              /* device, nreq x (k + 1) */
+  int32_t *accepted;         /* device, nreq */
+  int64_t target_req, target_row, draft_req, draft_row, tokens_stride, u_stride, noise_stride; /* in elements */
+  int64_t nreq, vocab;
+  int32_t k;                 /* >= 0 */
+  int32_t type;              /* of target and draft: MMQ_DT_F32, MMQ_DT_F16 or MMQ_DT_BF16 */
+} mmq_verification;
+
+/*
+ * mmq_verify_draft -- verification of drafted tokens.  Drafted token x_i is
+ * kept while u_i * q_i(x_i) < p_i(x_i) (fp32); accepted[b] is the number kept
+ * before the first refusal.  Behind them comes one more token: after a refusal
+ * at row i it is argmax_v (p_i - q_i)+(v) / noise(v), or argmax_v p_i(v) /
+ * noise(v) where p_i - q_i is nowhere positive; with all kept it is
+ * argmax_v p_n(v) / noise(v).  Ties go to the lowest v; weights that are not
+ * positive (NaN among them) take no part; -1 if there are none.  With
+ * exponential noise that is a draw from the normalised weights.
+ *   out[b] = kept tokens, the drawn token, then -1.
+ * A drafted token outside [0, vocab) is refused and reported by
+ * mmq_last_device_error.  vocab in 1..2^31-1.  One kernel, no scratch.
+ * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN (elements off their own alignment),
+ * MMQ_ERR_TYPE, MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
+ */
+int mmq_verify_draft(const mmq_verification *args, mmq_stream_t stream);
+
 /* Synchronizes the current device, then returns and clears the device status
- * word: MMQ_OK, or MMQ_ERR_DEVICE_TIMEOUT if a bounded wait expired since
- * the last call. */
+ * word: MMQ_OK, MMQ_ERR_DEVICE_TIMEOUT if a bounded wait expired since
+ * the last call, or MMQ_ERR_DEVICE_INDEX if an index was out of range (the
+ * first of them, if both). */
 int mmq_last_device_error(void);
 
 /* Limit of every device-side wait, in ns (default 2e9).  Host-global. */

@@ -1,7 +1,9 @@
 """GB300 (sm_103a) k-quant x q8_0 prefill GEMM: Python binding of libmmq.so.
 
 The package holds the CUDA sources (csrc/), their build script (build.py) and
-the ctypes binding (mmq.py); the C ABI is declared in include/mmq.h.
+the ctypes binding (mmq.py; serving.py for the serving step around the GEMM:
+page tables, K/V write, paged attention, draft verification); the C ABI is
+declared in include/mmq.h.
 """
 from .mmq import (  # noqa: F401
     ARM_NAMES,
@@ -10,6 +12,10 @@ from .mmq import (  # noqa: F401
     MMQ_ARM_PAIR,
     MMQ_ARM_RAW,
     MMQ_ARM_SPLIT,
+    MMQ_DT_BF16,
+    MMQ_DT_F16,
+    MMQ_DT_F32,
+    MMQ_ERR_DEVICE_INDEX,
     MMQ_OUT_F16,
     MMQ_OUT_F32,
     MMQ_Q4_K,
@@ -35,4 +41,11 @@ from .mmq import (  # noqa: F401
     mmq_strerror,
     mmq_weights_info,
     mmq_weights_wexp,
+)
+from .serving import (  # noqa: F401
+    PageTables,
+    mmq_kv_write,
+    mmq_page_tables,
+    mmq_paged_attention,
+    mmq_verify_draft,
 )

@@ -9,6 +9,7 @@
 #include <new>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace {
 
@@ -97,6 +98,18 @@ void free_planes(mmq_weights_s *h) {
 
 }  // namespace
 
+namespace mmq {
+
+int call_context(CallContext *out) {
+  int dev;
+  DeviceState *d;
+  if (int rc = device_state(&dev, &d)) return rc;
+  *out = {dev, d->words, d->pool, next_epoch(), g_limit_ns.load()};
+  return MMQ_OK;
+}
+
+}  // namespace mmq
+
 extern "C" {
 
 const char *mmq_strerror(int code) {
@@ -112,6 +125,7 @@ const char *mmq_strerror(int code) {
     case MMQ_ERR_NO_DEVICE: return "current device is not an sm_103 GPU";
     case MMQ_ERR_SCRATCH_LIMIT:
       return "problem needs more scratch than mmq_gemm_noalloc's fixed 16 MiB buffer";
+    case MMQ_ERR_DEVICE_INDEX: return "an index in device memory (slot, page or token) was out of range";
     default: return "unknown status code";
   }
 }
@@ -392,7 +406,7 @@ int mmq_last_device_error(void) {
   const int zero = 0;
   if (cudaMemcpy(&d->words->status, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
     return cuda_rc(cudaErrorUnknown);
-  return w.status ? MMQ_ERR_DEVICE_TIMEOUT : MMQ_OK;
+  return w.status == mmq::DEVERR_INDEX ? MMQ_ERR_DEVICE_INDEX : w.status ? MMQ_ERR_DEVICE_TIMEOUT : MMQ_OK;
 }
 
 int mmq_probe_engine_rates(double *out, mmq_stream_t stream) {

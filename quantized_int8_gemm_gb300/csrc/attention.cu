@@ -1,0 +1,417 @@
+// attention.cu -- attention of new tokens over the paged cache: the general
+// kernel (warp-level MMA, any page size and head width up to 256), the join of
+// split rows, and the choice between the kernels.
+//
+//   S = scale * q . k over the keys a row sees,  out = softmax(S) . v,
+//   lse = log(sum exp(S));  a row that sees nothing: out 0, lse -inf.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "attention.cuh"
+
+namespace mmq {
+namespace {
+
+template <class T>
+struct Pair;
+template <>
+struct Pair<__half> {
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
+template <>
+struct Pair<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// 16 bytes, or (bytes == 0) 16 zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
+constexpr int kRows = 64, kKt = 64, kThreads = 128;
+
+// Byte offset of 16-byte chunk c of row r in a tile of kDp-wide rows; the
+// swizzle keeps the eight rows of an ldmatrix on different banks.
+template <int kDp>
+__device__ __forceinline__ uint32_t tile_at(int r, int c) {
+  return static_cast<uint32_t>(r * kDp * 2 + (((c & ~7) | ((c ^ r) & 7)) << 4));
+}
+
+// The general kernel.  A unit: 64 rows, 16 a warp, over K/V tiles of 64 keys,
+// double-buffered copies (cp.async, zeros for what lies past the request's
+// last key, so that what unwritten memory holds never meets the tensor core).
+// S and P stay in registers; the running maximum, sum and the output are
+// fp32, P is rounded to the cache's type for the second product.  It serves
+// the shapes the tcgen05 kernel does not take.
+template <class T, int kDp>
+__global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_constant__ AttnArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ AttnUnit s_unit;
+  __shared__ int s_more;
+  constexpr int kChunks = kDp / 8;
+  constexpr int kTile = kKt * kDp * 2;
+  const uint32_t sq = smem_addr(smem), sk = sq + kRows * kDp * 2, sv = sk + 2 * kTile;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  AttnSchedule<kKt> sched;
+  if (warp == 0) sched.plan(a, kRows, gridDim.x, 3);
+
+  for (int u = blockIdx.x;; u += gridDim.x) {
+    if (warp == 0) {
+      AttnUnit x;
+      const bool more = sched.find(a, u, x);
+      if (lane == 0) {
+        s_more = more;
+        if (more) s_unit = x;
+      }
+    }
+    __syncthreads();
+    if (!s_more) break;
+    const AttnUnit un = s_unit;
+    const int all_rows = un.n * a.rep;
+    const T *q = static_cast<const T *>(a.q);
+    for (int i = tid; i < kRows * kChunks; i += kThreads) {
+      const int r = i / kChunks, c = i % kChunks, row = un.row0 + r;
+      const bool in = row < all_rows && c * 8 < a.d;
+      const int tok = row / a.rep;
+      const T *src = in ? q + (un.q0 + tok) * a.q_token + (un.head * a.rep + row - tok * a.rep) * a.q_head + c * 8 : q;
+      cp_async16(sq + tile_at<kDp>(r, c), src, in ? 16 : 0);
+    }
+    auto load = [&](int t, int buf) {
+      const int32_t *row = a.table + un.b * a.table_stride;
+      for (int i = tid; i < kKt * kChunks; i += kThreads) {
+        const int r = i / kChunks, c = i % kChunks, key = t * kKt + r;
+        bool in = key < un.len && c * 8 < a.d;
+        int64_t page = 0;
+        int off = 0;
+        if (in) {
+          const int blk = key / a.page_size;
+          page = row[blk];
+          off = key - blk * a.page_size;
+          if (page < 0 || page >= a.pages) {
+            record_index(a.wait.status);
+            in = false;
+          }
+        }
+        const T *k = static_cast<const T *>(a.k), *v = static_cast<const T *>(a.v);
+        cp_async16(sk + buf * kTile + tile_at<kDp>(r, c),
+                   in ? k + page * a.k_page + off * a.k_token + un.head * a.k_head + c * 8 : k, in ? 16 : 0);
+        cp_async16(sv + buf * kTile + tile_at<kDp>(r, c),
+                   in ? v + page * a.v_page + off * a.v_token + un.head * a.v_head + c * 8 : v, in ? 16 : 0);
+      }
+    };
+    if (un.t_begin < un.t_end) load(un.t_begin, 0);
+    cp_async_commit();
+
+    float o[kDp / 8][4];
+#pragma unroll
+    for (int j = 0; j < kDp / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int lo[2], hi[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) attn_row_range(a, un.n, un.len, (un.row0 + warp * 16 + (lane >> 2) + 8 * h) / a.rep, lo[h], hi[h]);
+
+    for (int t = un.t_begin; t < un.t_end; ++t) {
+      const int buf = (t - un.t_begin) & 1;
+      if (t + 1 < un.t_end) load(t + 1, buf ^ 1);
+      cp_async_commit();
+      cp_async_wait<1>();
+      __syncthreads();
+      float s[kKt / 8][4];
+#pragma unroll
+      for (int j = 0; j < kKt / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < kDp / 16; ++kk) {
+        uint32_t qa[4];
+        ldmatrix_x4(qa, sq + tile_at<kDp>(warp * 16 + (lane & 15), 2 * kk + (lane >> 4)));
+#pragma unroll
+        for (int j = 0; j < kKt / 16; ++j) {
+          uint32_t kb[4];
+          ldmatrix_x4(kb, sk + buf * kTile + tile_at<kDp>(j * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)));
+          Pair<T>::mma(s[2 * j], qa, kb[0], kb[1]);
+          Pair<T>::mma(s[2 * j + 1], qa, kb[2], kb[3]);
+        }
+      }
+      const int key0 = t * kKt + 2 * (lane & 3);
+      float top[2] = {m[0], m[1]};
+#pragma unroll
+      for (int j = 0; j < kKt / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = key0 + 8 * j + (i & 1), h = i >> 1;
+          if (key < lo[h] || key >= hi[h]) s[j][i] = -INFINITY;
+          top[h] = fmaxf(top[h], s[j][i]);
+        }
+      float base[2], shrink[2], part[2] = {0.0f, 0.0f};  // the tile's sums first: fewer roundings at the size of l
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+        base[h] = top[h] == -INFINITY ? 0.0f : top[h] * a.scale_log2;
+        shrink[h] = exp2_fast(fmaf(m[h], a.scale_log2, -base[h]));
+        m[h] = top[h];
+        l[h] *= shrink[h];
+      }
+#pragma unroll
+      for (int j = 0; j < kKt / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[j][i] = exp2_fast(fmaf(s[j][i], a.scale_log2, -base[i >> 1]));
+          part[i >> 1] += s[j][i];
+        }
+      l[0] += part[0];
+      l[1] += part[1];
+#pragma unroll
+      for (int j = 0; j < kDp / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][i] *= shrink[i >> 1];
+#pragma unroll
+      for (int kk = 0; kk < kKt / 16; ++kk) {
+        const uint32_t pa[4] = {Pair<T>::pack(s[2 * kk][0], s[2 * kk][1]), Pair<T>::pack(s[2 * kk][2], s[2 * kk][3]),
+                                Pair<T>::pack(s[2 * kk + 1][0], s[2 * kk + 1][1]),
+                                Pair<T>::pack(s[2 * kk + 1][2], s[2 * kk + 1][3])};
+#pragma unroll
+        for (int j = 0; j < kDp / 16; ++j) {
+          uint32_t vb[4];
+          ldmatrix_x4_trans(vb, sv + buf * kTile + tile_at<kDp>(kk * 16 + (lane & 15), 2 * j + (lane >> 4)));
+          Pair<T>::mma(o[2 * j], pa, vb[0], vb[1]);
+          Pair<T>::mma(o[2 * j + 1], pa, vb[2], vb[3]);
+        }
+      }
+      __syncthreads();
+    }
+    cp_async_wait<0>();
+
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float sum = l[h];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const int row = un.row0 + warp * 16 + (lane >> 2) + 8 * h;
+      if (row >= all_rows) continue;
+      const int tok = row / a.rep, head = un.head * a.rep + row - tok * a.rep;
+      const int64_t at = static_cast<int64_t>(un.q0 + tok) * a.hq + head;
+      const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // (NaN stays)
+      const float lse2 = sum > 0.0f ? fmaf(m[h], a.scale_log2, log2f(sum)) : sum == 0.0f ? -INFINITY : sum;
+      if (un.pieces > 1) {
+        float *dst = a.part_o + (un.piece * a.ntok * a.hq + at) * a.d;
+#pragma unroll
+        for (int j = 0; j < kDp / 8; ++j) {
+          const int col = 8 * j + 2 * (lane & 3);
+          if (col < a.d) *reinterpret_cast<float2 *>(dst + col) = make_float2(o[j][2 * h] * inv, o[j][2 * h + 1] * inv);
+        }
+        if ((lane & 3) == 0) {
+          a.part_lse[un.piece * a.ntok * a.hq + at] = lse2;
+          if (un.piece == 0) a.part_n[at] = un.pieces;
+        }
+      } else {
+        const int64_t to = (un.q0 + tok) * a.out_token + head * a.out_head;
+#pragma unroll
+        for (int j = 0; j < kDp / 8; ++j) {
+          const int col = 8 * j + 2 * (lane & 3);
+          if (col >= a.d) continue;
+          const float x = o[j][2 * h] * inv, y = o[j][2 * h + 1] * inv;
+          if (a.out_type == MMQ_DT_F32) *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + to + col) = make_float2(x, y);
+          else *reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + to + col) = Pair<T>::pack(x, y);
+        }
+        if ((lane & 3) == 0) {
+          if (a.lse) a.lse[at] = lse2 * kLn2;
+          if (a.max_pieces > 1) a.part_n[at] = 1;
+        }
+      }
+    }
+    __syncthreads();  // the Q tile and s_unit are free
+  }
+}
+
+// Joins the pieces of split rows: with lse_p (base 2) and normalised outputs
+// o_p, out = sum 2^(lse_p - top) o_p / sum 2^(lse_p - top), in fp32 and in the
+// pieces' order.  One warp a row; each lane adds four (eight) columns.
+template <class T>
+__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a) {
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = a.ntok * a.hq, at = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (at >= rows) return;
+  const int64_t tok = at / a.hq;
+  if (tok < a.q_start[0] || tok >= a.q_start[a.nreq]) return;  // rows of no request
+  const int n = a.part_n[at];
+  if (n < 2 || n > a.max_pieces) return;  // not split
+  float top = -INFINITY, bad = 0.0f;
+  for (int p = lane; p < n; p += 32) {
+    const float x = a.part_lse[p * rows + at];
+    top = fmaxf(top, x);
+    if (x != x) bad = x;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    bad += __shfl_xor_sync(0xffffffffu, bad, d);
+  }
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  float sum = 0.0f;
+  for (int p0 = 0; p0 < n; p0 += 32) {
+    const float mine = p0 + lane < n ? a.part_lse[(p0 + lane) * rows + at] : -INFINITY;
+    const float w = mine == -INFINITY ? 0.0f : exp2f(mine - top);
+    const int here = min(32, n - p0);
+#pragma unroll 4
+    for (int i = 0; i < here; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      sum += wi;
+      if (wi == 0.0f) continue;
+      const float *src = a.part_o + ((p0 + i) * rows + at) * a.d;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int col = 4 * (lane + 32 * h);
+        if (col < a.d) {
+          const float4 x = __ldcs(reinterpret_cast<const float4 *>(src + col));
+          acc[h].x = fmaf(wi, x.x, acc[h].x);
+          acc[h].y = fmaf(wi, x.y, acc[h].y);
+          acc[h].z = fmaf(wi, x.z, acc[h].z);
+          acc[h].w = fmaf(wi, x.w, acc[h].w);
+        }
+      }
+    }
+  }
+  const float inv = (sum > 0.0f ? 1.0f / sum : 0.0f) + bad;
+  const int64_t to = tok * a.out_token + (at - tok * a.hq) * a.out_head;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int col = 4 * (lane + 32 * h);
+    if (col >= a.d) continue;
+    if (a.out_type == MMQ_DT_F32) {
+      *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to + col) =
+          make_float4(acc[h].x * inv, acc[h].y * inv, acc[h].z * inv, acc[h].w * inv);
+    } else {
+      uint2 x;
+      x.x = Pair<T>::pack(acc[h].x * inv, acc[h].y * inv);
+      x.y = Pair<T>::pack(acc[h].z * inv, acc[h].w * inv);
+      *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + to + col) = x;
+    }
+  }
+  if (lane == 0 && a.lse) a.lse[at] = (sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY) + bad;
+}
+
+template <class T, int kDp>
+cudaError_t launch_rows(const AttnArgs &a, int dev, unsigned grid, cudaStream_t s) {
+  constexpr int smem = (kRows + 4 * kKt) * kDp * 2;
+  const cudaError_t e = allow_smem<attention_rows_kernel<T, kDp>>(dev, smem);
+  if (e != cudaSuccess) return e;
+  attention_rows_kernel<T, kDp><<<grid, kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+template <class T>
+cudaError_t launch_rows_of(const AttnArgs &a, int dev, unsigned grid, cudaStream_t s) {
+  if (a.d <= 64) return launch_rows<T, 64>(a, dev, grid, s);
+  if (a.d <= 128) return launch_rows<T, 128>(a, dev, grid, s);
+  return launch_rows<T, 256>(a, dev, grid, s);
+}
+
+template <class T>
+cudaError_t launch_join(const AttnArgs &a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.ntok * a.hq + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<T>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_rows(const AttnArgs &a, int type, int dev, unsigned grid, cudaStream_t s) {
+  return type == MMQ_DT_F16 ? launch_rows_of<__half>(a, dev, grid, s) : launch_rows_of<__nv_bfloat16>(a, dev, grid, s);
+}
+
+cudaError_t launch_attention(const mmq_paged_cache &c, const mmq_attention &t, const CallContext &ctx, cudaStream_t s) {
+  AttnArgs a = {};
+  a.q = t.q, a.k = c.k, a.v = c.v, a.out = t.out, a.lse = t.lse;
+  a.table = t.table, a.seq_lens = t.seq_lens, a.q_start = t.q_start;
+  a.q_token = t.q_token, a.q_head = t.q_head, a.out_token = t.out_token, a.out_head = t.out_head;
+  a.k_page = c.k_page, a.k_token = c.k_token, a.k_head = c.k_head;
+  a.v_page = c.v_page, a.v_token = c.v_token, a.v_head = c.v_head;
+  a.table_stride = t.table_stride, a.pages = c.pages, a.ntok = t.ntok;
+  a.nreq = static_cast<int32_t>(t.nreq), a.table_width = t.table_width, a.page_size = c.page_size;
+  a.hq = t.q_heads, a.hkv = c.heads, a.rep = t.q_heads / c.heads, a.d = c.head_dim;
+  a.causal = t.causal, a.window = t.window, a.out_type = t.out_type;
+  a.scale_log2 = t.scale * 1.44269504088896341f;
+  a.wait = {&ctx.words->status, &ctx.words->abort_epoch, ctx.epoch, ctx.limit_ns};
+
+  const int slots = 2 * 152;
+  // Rows are split over the keys where that can fill the SMs: fewer than four
+  // units for each slot, and a cache row of more than two tiles.
+  const int64_t rows = t.ntok * t.q_heads, room = static_cast<int64_t>(t.table_width) * c.page_size;
+  const int64_t units = (t.ntok * a.rep + kRows - 1) / kRows * c.heads;
+  int64_t pieces = 1;
+  if (units < 4 * slots && room > 2 * kKt) {
+    pieces = std::min<int64_t>((slots + c.heads - 1) / c.heads + 1, (room + kKt - 1) / kKt);
+    pieces = std::min<int64_t>(pieces, (int64_t(256) << 20) / (rows * (a.d + 1) * 4));
+    pieces = std::max<int64_t>(pieces, 1);
+  }
+  a.max_pieces = static_cast<int32_t>(pieces);
+  void *scratch = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (pieces > 1) {
+    const size_t o_bytes = static_cast<size_t>(pieces * rows * a.d) * 4, lse_bytes = static_cast<size_t>(pieces * rows) * 4;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    e = cudaStreamIsCapturing(s, &cap);
+    if (e != cudaSuccess) return e;
+    const size_t bytes = o_bytes + lse_bytes + static_cast<size_t>(rows) * 4;
+    e = cap == cudaStreamCaptureStatusActive ? cudaMallocAsync(&scratch, bytes, s)
+                                             : cudaMallocFromPoolAsync(&scratch, bytes, ctx.pool, s);
+    if (e != cudaSuccess) return e;
+    a.part_o = static_cast<float *>(scratch);
+    a.part_lse = a.part_o + pieces * rows * a.d;
+    a.part_n = reinterpret_cast<int32_t *>(a.part_lse + pieces * rows);
+  }
+  e = launch_attention_rows(a, c.type, ctx.device, slots, s);
+  if (e == cudaSuccess && pieces > 1)
+    e = c.type == MMQ_DT_F16 ? launch_join<__half>(a, s) : launch_join<__nv_bfloat16>(a, s);
+  if (scratch) {
+    const cudaError_t ef = cudaFreeAsync(scratch, s);
+    if (e == cudaSuccess) e = ef;
+  }
+  return e;
+}
+
+}  // namespace mmq

@@ -88,8 +88,62 @@ cudaError_t launch_gemm_split(const mmq_weights_s *h, const uint8_t *Q, const fl
 cudaError_t launch_wait_selftest(DevStatus *st, unsigned epoch, uint64_t limit_ns,
                                  cudaStream_t s);
 
+// What an entry point needs to launch on the current device: its status words
+// and scratch pool, an epoch of its own and the limit of device waits.  Returns
+// an MMQ_* code.
+struct CallContext {
+  int device;
+  DevStatus *words;
+  cudaMemPool_t pool;
+  unsigned epoch;
+  uint64_t limit_ns;
+};
+int call_context(CallContext *out);
+
+// ---- paged cache and serving step (paged.cu, verify.cu, attention*.cu) ----
+constexpr int64_t kMaxRequests = 8192;  // their sums stay in shared memory
+
+struct PageTablesArgs {
+  const int32_t *cached, *fresh, *held;
+  int32_t *table;
+  const int32_t *free_pages;
+  int32_t *q_start, *seq_lens, *held_out;
+  int64_t *slots;
+  int32_t *positions, *taken;
+  int64_t table_stride, table_width, nfree, max_tokens;
+  int32_t nreq, page_size;
+};
+cudaError_t launch_page_tables(const PageTablesArgs &a, cudaStream_t s);
+
+struct KvWriteArgs {
+  mmq_paged_cache cache;
+  const void *k, *v;
+  int64_t k_token, k_head, v_token, v_head;
+  const int64_t *slots;
+  int64_t ntok;
+  int32_t heads, head_dim, src_type, tokens_per_cta;
+  int *status;
+};
+cudaError_t launch_kv_write(KvWriteArgs a, cudaStream_t s);
+
+struct VerifyArgs {
+  const void *target, *draft;
+  const int32_t *tokens, *n_draft;
+  const float *u, *noise;
+  int32_t *out, *accepted;
+  int64_t target_req, target_row, draft_req, draft_row, tokens_stride, u_stride, noise_stride;
+  int64_t nreq, vocab;
+  int32_t k, type;
+  int32_t wide;
+  int *status;
+};
+cudaError_t launch_verify(VerifyArgs a, cudaStream_t s);
+
 // Engine-rate microbenchmarks (probe.cu); out[0..4] as mmq_probe_engine_rates.
 cudaError_t launch_engine_probes(DevStatus *st, unsigned epoch, uint64_t limit_ns, cudaStream_t s, double *out);
+
+cudaError_t launch_attention(const mmq_paged_cache &cache, const mmq_attention &at, const CallContext &ctx,
+                             cudaStream_t s);
 
 // Fixed scratch of mmq_gemm_noalloc (a static device array in gemm.cu).
 constexpr size_t kNoallocScratchBytes = size_t(16) << 20;

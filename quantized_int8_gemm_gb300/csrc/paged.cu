@@ -1,0 +1,261 @@
+// paged.cu -- the bookkeeping of a paged K/V cache: page tables and slot maps
+// from request lengths, and the rows of K and V written by those slots.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace mmq {
+namespace {
+
+// ---------------------------------------------------------------- page tables
+constexpr int kTabThreads = 512;
+constexpr int kTabTokens = 2048;  // tokens of one CTA
+
+// Exclusive sums over the CTA's threads of two values; returns the totals.
+__device__ __forceinline__ void block_exclusive(int64_t &a, int64_t &b, int64_t &ta, int64_t &tb, int64_t *sm) {
+  constexpr int kWarps = kTabThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t ia = a, ib = b;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t ya = __shfl_up_sync(0xffffffffu, ia, d), yb = __shfl_up_sync(0xffffffffu, ib, d);
+    if (lane >= d) ia += ya, ib += yb;
+  }
+  if (lane == 31) sm[warp] = ia, sm[kWarps + warp] = ib;
+  __syncthreads();
+  int64_t pa = 0, pb = 0;
+  ta = tb = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int64_t xa = sm[w], xb = sm[kWarps + w];
+    if (w < warp) pa += xa, pb += xb;
+    ta += xa;
+    tb += xb;
+  }
+  a = pa + ia - a;
+  b = pb + ib - b;
+}
+
+// The largest i in [0, n) with sums[i] <= x (sums ascending, sums[0] <= x).
+__device__ __forceinline__ int last_not_above(const int *sums, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// A request's lengths and pages: `need` pages for cached + fresh tokens, of
+// which it takes `more` from the free list; `lost` are beyond its table's row.
+struct Pages {
+  int cached, fresh, held, more, lost;
+};
+__device__ __forceinline__ Pages pages_of(const PageTablesArgs &a, int b) {
+  Pages p;
+  p.cached = max(a.cached[b], 0);
+  p.fresh = max(a.fresh[b], 0);
+  p.held = max(a.held[b], 0);
+  const int64_t need = (static_cast<int64_t>(p.cached) + p.fresh + a.page_size - 1) / a.page_size;
+  const int64_t fit = need < a.table_width ? need : a.table_width;
+  p.more = fit > p.held ? static_cast<int>(fit - p.held) : 0;
+  p.lost = need > a.table_width && need > p.held ? static_cast<int>(need - max(static_cast<int64_t>(p.held), a.table_width)) : 0;
+  return p;
+}
+
+// One launch for everything.  Each CTA sums the requests' lengths by itself
+// (nreq numbers, from L2) and so needs nothing from another CTA; it then takes
+// its slice of the tokens and of the new pages and finds each one's request by
+// bisection in shared memory.  Latency bound: a few dependent reads of a few
+// KB; the 12 B a token that it writes are 0.8 MB at 65536 tokens.
+__global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const __grid_constant__ PageTablesArgs a) {
+  extern __shared__ int sums[];  // [nreq + 1] first token, [nreq + 1] first new page
+  __shared__ int64_t warp_sums[2 * kTabThreads / 32];
+  const int n = a.nreq, tid = threadIdx.x;
+  int *first_tok = sums, *first_page = sums + n + 1;
+  const int per = (n + kTabThreads - 1) / kTabThreads, b0 = min(tid * per, n), b1 = min(b0 + per, n);
+  int64_t tok = 0, page = 0, tok_all, page_all;
+  for (int b = b0; b < b1; ++b) {
+    const Pages p = pages_of(a, b);
+    tok += p.fresh;
+    page += p.more;
+  }
+  block_exclusive(tok, page, tok_all, page_all, warp_sums);
+  int64_t lost = 0;
+  auto cap = [](int64_t x) { return static_cast<int>(x < 0x7fffffff ? x : 0x7fffffff); };
+  for (int b = b0; b < b1; ++b) {
+    const Pages p = pages_of(a, b);
+    first_tok[b] = cap(tok);
+    first_page[b] = cap(page);
+    if (blockIdx.x == 0) {
+      a.q_start[b] = cap(tok);
+      a.seq_lens[b] = cap(static_cast<int64_t>(p.cached) + p.fresh);
+      const int64_t left = a.nfree - page;
+      a.held_out[b] = p.held + static_cast<int>(left < 0 ? 0 : left < p.more ? left : p.more);
+    }
+    tok += p.fresh;
+    page += p.more;
+    lost += p.lost;
+  }
+  if (tid == 0) {
+    first_tok[n] = cap(tok_all);
+    first_page[n] = cap(page_all);
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    int64_t zero = 0, lost_all, none;
+    block_exclusive(lost, zero, lost_all, none, warp_sums);
+    if (tid == 0) {
+      a.q_start[n] = cap(tok_all);
+      const int64_t short_of = page_all > a.nfree ? page_all - a.nfree : 0;
+      a.taken[0] = cap(page_all - short_of);
+      a.taken[1] = cap(short_of + lost_all);
+    }
+  }
+  // new entries of the tables
+  const int pages_n = cap(page_all), stride = gridDim.x * kTabThreads;
+  for (int j = blockIdx.x * kTabThreads + tid; j < pages_n; j += stride) {
+    const int b = last_not_above(first_page, n, j);
+    const int at = max(a.held[b], 0) + (j - first_page[b]);
+    a.table[static_cast<int64_t>(b) * a.table_stride + at] = j < a.nfree ? a.free_pages[j] : -1;
+  }
+  // tokens
+  const int tok_n = cap(tok_all);
+  const int64_t t_end = min(a.max_tokens, static_cast<int64_t>(blockIdx.x + 1) * kTabTokens);
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTabTokens + tid; t < t_end; t += kTabThreads) {
+    int64_t slot = -1;
+    int position = -1;
+    if (t < tok_n) {
+      const int b = last_not_above(first_tok, n, static_cast<int>(t));
+      const int64_t pos = static_cast<int64_t>(max(a.cached[b], 0)) + (static_cast<int>(t) - first_tok[b]);
+      const int64_t blk = pos / a.page_size;
+      const int held = max(a.held[b], 0);
+      int id = -1;
+      if (blk < a.table_width) {
+        if (blk < held) {
+          id = a.table[static_cast<int64_t>(b) * a.table_stride + blk];
+        } else {
+          const int64_t j = first_page[b] + (blk - held);
+          if (j < a.nfree) id = a.free_pages[j];
+        }
+      }
+      position = cap(pos);
+      if (id >= 0) slot = static_cast<int64_t>(id) * a.page_size + (pos - blk * a.page_size);
+    }
+    a.slots[t] = slot;
+    a.positions[t] = position;
+  }
+}
+
+// ---------------------------------------------------------------- K and V rows
+template <class T>
+__device__ __forceinline__ void load8(const void *p, int64_t at, float (&x)[8]);
+template <>
+__device__ __forceinline__ void load8<float>(const void *p, int64_t at, float (&x)[8]) {
+  const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+  const float4 a = __ldcs(s), b = __ldcs(s + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<__half>(const void *p, int64_t at, float (&x)[8]) {
+  const uint4 r = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const __half *>(p) + at));
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+  }
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const void *p, int64_t at, float (&x)[8]) {
+  const uint4 r = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + at));
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+constexpr int kWriteThreads = 256;
+
+// One thread moves 8 elements of one row: 32 B (16 B) in, 16 B out.  HBM
+// bound; the one dependent read is the token's slot.  The source is read
+// once (streaming loads), the cache rows are left in L2 for the attention
+// that follows.
+template <class S, class D>
+__global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_constant__ KvWriteArgs a) {
+  const int per_tensor = a.heads * (a.head_dim >> 3), per_tok = 2 * per_tensor;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_cta;
+  const int toks = static_cast<int>(min(static_cast<int64_t>(a.tokens_per_cta), a.ntok - t0));
+  for (int i = threadIdx.x; i < toks * per_tok; i += kWriteThreads) {
+    const int tl = i / per_tok, r = i - tl * per_tok;
+    const bool is_v = r >= per_tensor;
+    const int c = is_v ? r - per_tensor : r;
+    const int head = c / (a.head_dim >> 3), col = (c - head * (a.head_dim >> 3)) << 3;
+    const int64_t t = t0 + tl;
+    const int64_t slot = a.slots[t];
+    float x[8];
+    load8<S>(is_v ? a.v : a.k, is_v ? t * a.v_token + head * a.v_head + col : t * a.k_token + head * a.k_head + col, x);
+    if (slot < 0) continue;  // padding
+    if (slot >= a.cache.pages * a.cache.page_size) {
+      record_index(a.status);
+      continue;
+    }
+    const int64_t page = slot / a.cache.page_size;
+    const int64_t row = slot - page * a.cache.page_size;
+    uint4 o;
+    o.x = pack2(x[0], x[1], D());
+    o.y = pack2(x[2], x[3], D());
+    o.z = pack2(x[4], x[5], D());
+    o.w = pack2(x[6], x[7], D());
+    D *dst = is_v ? static_cast<D *>(a.cache.v) + page * a.cache.v_page + row * a.cache.v_token + head * a.cache.v_head
+                  : static_cast<D *>(a.cache.k) + page * a.cache.k_page + row * a.cache.k_token + head * a.cache.k_head;
+    *reinterpret_cast<uint4 *>(dst + col) = o;
+  }
+}
+
+template <class S>
+cudaError_t launch_kv_write_from(const KvWriteArgs &a, unsigned grid, cudaStream_t s) {
+  if (a.cache.type == MMQ_DT_F16) kv_write_kernel<S, __half><<<grid, kWriteThreads, 0, s>>>(a);
+  else kv_write_kernel<S, __nv_bfloat16><<<grid, kWriteThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_page_tables(const PageTablesArgs &a, cudaStream_t s) {
+  const size_t smem = 2 * (static_cast<size_t>(a.nreq) + 1) * sizeof(int);
+  if (smem > 32 * 1024) {  // (beside the static arrays, within the 48 KB that need no leave)
+    const cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * (kMaxRequests + 1) * 4);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t ctas = (a.max_tokens + kTabTokens - 1) / kTabTokens;
+  page_tables_kernel<<<static_cast<unsigned>(ctas > 0 ? ctas : 1), kTabThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_write(KvWriteArgs a, cudaStream_t s) {
+  // about four items a thread; at least one token a CTA
+  const int per_tok = 2 * a.heads * (a.head_dim >> 3);
+  a.tokens_per_cta = per_tok >= 4 * kWriteThreads ? 1 : 4 * kWriteThreads / per_tok;
+  if (a.ntok < static_cast<int64_t>(a.tokens_per_cta) * 152) a.tokens_per_cta = per_tok >= kWriteThreads ? 1 : kWriteThreads / per_tok;
+  const int64_t grid = (a.ntok + a.tokens_per_cta - 1) / a.tokens_per_cta;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  if (a.src_type == MMQ_DT_F32) return launch_kv_write_from<float>(a, static_cast<unsigned>(grid), s);
+  if (a.src_type == MMQ_DT_F16) return launch_kv_write_from<__half>(a, static_cast<unsigned>(grid), s);
+  return launch_kv_write_from<__nv_bfloat16>(a, static_cast<unsigned>(grid), s);
+}
+
+}  // namespace mmq

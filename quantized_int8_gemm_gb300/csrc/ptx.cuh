@@ -8,7 +8,11 @@
 namespace mmq {
 
 // device status codes written to the per-device status word
-enum : int { DEVERR_NONE = 0, DEVERR_TIMEOUT = 1 };
+enum : int { DEVERR_NONE = 0, DEVERR_TIMEOUT = 1, DEVERR_INDEX = 2 };
+
+// An index in device memory that is out of its range: the access is left out
+// and the host reads of it from the status word.
+__device__ __forceinline__ void record_index(int *status) { atomicCAS(status, DEVERR_NONE, DEVERR_INDEX); }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

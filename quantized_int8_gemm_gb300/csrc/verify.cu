@@ -1,0 +1,178 @@
+// verify.cu -- drafted tokens against the target's probabilities.
+//
+// Drafted token x_i of a request is kept while u_i * q_i(x_i) < p_i(x_i), i.e.
+// with probability min(1, p/q) for u uniform in [0, 1).  At the first refusal
+// the token is drawn from the normalised (p - q)+, after the last drafted
+// token from p.  With e_v independent exponential variates, argmax_v w_v / e_v
+// draws v with probability w_v / sum w: no sum over the vocabulary is needed,
+// and a maximum does not depend on the order it is taken in, so the result is
+// the same for every split of the row.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace mmq {
+namespace {
+
+constexpr int kVerThreads = 512;
+constexpr int kVerCtas = 8;  // CTAs (one cluster) of a request
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// The better of two candidates is the larger number: the weight's bits above,
+// the complement of the index below (so that ties go to the lowest index).
+// 0: no candidate.
+__device__ __forceinline__ void consider(uint64_t &best, float w, float e, int64_t v) {
+  const float key = w / e;
+  if (!(w > 0.0f && key > 0.0f)) return;
+  const uint64_t mine = static_cast<uint64_t>(__float_as_uint(key)) << 32 | (0xffffffffu - static_cast<uint32_t>(v));
+  if (mine > best) best = mine;
+}
+
+// This CTA's part of one row.  kLeft: weights (p - q)+, else p.
+template <class T, bool kLeft>
+__device__ __forceinline__ uint64_t race(const T *__restrict__ p, const T *__restrict__ q, const float *__restrict__ e,
+                                         int64_t n, bool wide, uint32_t rank) {
+  uint64_t best = 0;
+  const int64_t step = static_cast<int64_t>(kVerCtas) * kVerThreads;
+  const int64_t me = static_cast<int64_t>(rank) * kVerThreads + threadIdx.x;
+  int64_t done = 0;
+  if (wide) {  // rows on 16-byte boundaries: four elements a step
+    const int64_t groups = n >> 2;
+#pragma unroll 4
+    for (int64_t i = me; i < groups; i += step) {
+      const float4 ev = __ldcs(reinterpret_cast<const float4 *>(e) + i);
+      T pv[4], qv[4];
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<uint4 *>(pv) = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+        if (kLeft) *reinterpret_cast<uint4 *>(qv) = __ldcs(reinterpret_cast<const uint4 *>(q) + i);
+      } else {
+        *reinterpret_cast<uint2 *>(pv) = __ldcs(reinterpret_cast<const uint2 *>(p) + i);
+        if (kLeft) *reinterpret_cast<uint2 *>(qv) = __ldcs(reinterpret_cast<const uint2 *>(q) + i);
+      }
+      const float en[4] = {ev.x, ev.y, ev.z, ev.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        consider(best, kLeft ? to_f32(pv[k]) - to_f32(qv[k]) : to_f32(pv[k]), en[k], 4 * i + k);
+    }
+    done = groups << 2;
+  }
+  for (int64_t v = done + me; v < n; v += step) consider(best, kLeft ? to_f32(p[v]) - to_f32(q[v]) : to_f32(p[v]), e[v], v);
+  return best;
+}
+
+__device__ __forceinline__ uint64_t warp_max(uint64_t x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    const uint64_t y = __shfl_xor_sync(0xffffffffu, x, d);
+    x = y > x ? y : x;
+  }
+  return x;
+}
+
+// The cluster's best: each CTA reduces its own and writes it to every CTA.
+__device__ __forceinline__ uint64_t cluster_best(uint64_t mine, uint64_t *own, uint64_t *all, uint32_t rank) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  mine = warp_max(mine);
+  if (lane == 0) own[warp] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    const uint64_t b = warp_max(lane < kVerThreads / 32 ? own[lane] : 0);
+    if (lane < kVerCtas)
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_addr(all + rank), lane)), "l"(b) : "memory");
+  }
+  cluster_sync();
+  uint64_t best = 0;
+#pragma unroll
+  for (int i = 0; i < kVerCtas; ++i) best = all[i] > best ? all[i] : best;
+  return best;
+}
+
+// A cluster of 8 CTAs for each request: the row of the vocabulary is split
+// over them and joined through their shared memory, one launch, no scratch.
+// HBM bound: one row each of p, q and e (12 B an entry in fp32).
+template <class T>
+__global__ void __launch_bounds__(kVerThreads) __cluster_dims__(kVerCtas, 1, 1)
+    verify_kernel(const __grid_constant__ VerifyArgs a) {
+  __shared__ uint64_t own[kVerThreads / 32], all[2][kVerCtas];
+  __shared__ int s_kept;
+  const uint32_t rank = cluster_ctarank();
+  const int64_t b = blockIdx.x / kVerCtas;
+  const int k = a.k, lane = threadIdx.x & 31;
+  const int n = max(0, min(a.n_draft ? a.n_draft[b] : k, k));
+  const T *target = static_cast<const T *>(a.target) + b * a.target_req;
+  const T *draft = a.draft ? static_cast<const T *>(a.draft) + b * a.draft_req : nullptr;
+  const int32_t *ids = a.tokens + b * a.tokens_stride;
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  if (threadIdx.x < 32) {  // kept drafted tokens
+    int kept = n;
+    for (int i0 = 0; i0 < n && kept == n; i0 += 32) {
+      const int i = i0 + lane;
+      bool pass = true;
+      if (i < n) {
+        const int64_t x = ids[i];
+        if (x < 0 || x >= a.vocab) {
+          pass = false;
+          record_index(a.status);
+        } else {
+          const float p = to_f32(target[i * a.target_row + x]);
+          const float q = draft ? to_f32(draft[i * a.draft_row + x]) : 1.0f;
+          pass = __fmul_rn(a.u[b * a.u_stride + i], q) < p;
+        }
+      }
+      const uint32_t refused = __ballot_sync(0xffffffffu, !pass);
+      if (refused) kept = i0 + __ffs(refused) - 1;
+    }
+    if (lane == 0) s_kept = kept;
+  }
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // (also the CTA's threads: every CTA of the cluster runs)
+  __syncthreads();
+  const int kept = s_kept;
+  const T *p = target + static_cast<int64_t>(kept) * a.target_row;
+  const T *q = draft ? draft + static_cast<int64_t>(kept) * a.draft_row : nullptr;
+  const float *e = a.noise + b * a.noise_stride;
+  uint64_t best = 0;
+  if (kept < n) {
+    if (q) {
+      best = cluster_best(race<T, true>(p, q, e, a.vocab, a.wide, rank), own, all[0], rank);
+    } else {  // a draft without probabilities gave its token all of them: p without that token
+      const int64_t x = ids[kept];
+      uint64_t m = race<T, false>(p, p, e, x < 0 || x >= a.vocab ? a.vocab : x, a.wide, rank);
+      if (x >= 0 && x < a.vocab) {
+        // the entries behind the refused token; their alignment is not the row's
+        for (int64_t v = x + 1 + static_cast<int64_t>(rank) * kVerThreads + threadIdx.x; v < a.vocab;
+             v += static_cast<int64_t>(kVerCtas) * kVerThreads)
+          consider(m, to_f32(p[v]), e[v], v);
+      }
+      best = cluster_best(m, own, all[0], rank);
+    }
+  }
+  if (best == 0)  // nothing was refused, or p - q is nowhere positive
+    best = cluster_best(race<T, false>(p, p, e, a.vocab, a.wide, rank), own, all[1], rank);
+  if (rank != 0) return;
+  const int drawn = best ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
+  for (int i = threadIdx.x; i <= k; i += kVerThreads)
+    a.out[b * (k + 1) + i] = i < kept ? ids[i] : i == kept ? drawn : -1;
+  if (threadIdx.x == 0) a.accepted[b] = kept;
+}
+
+}  // namespace
+
+cudaError_t launch_verify(VerifyArgs a, cudaStream_t s) {
+  const int esz = a.type == MMQ_DT_F32 ? 4 : 2;
+  auto on16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  auto row16 = [&](int64_t stride) { return stride * esz % 16 == 0; };
+  a.wide = on16(a.target) && on16(a.draft) && on16(a.noise) && row16(a.target_req) && row16(a.target_row) &&
+           (!a.draft || (row16(a.draft_req) && row16(a.draft_row))) && a.noise_stride % 4 == 0;
+  const unsigned grid = static_cast<unsigned>(a.nreq * kVerCtas);
+  if (a.type == MMQ_DT_F32) verify_kernel<float><<<grid, kVerThreads, 0, s>>>(a);
+  else if (a.type == MMQ_DT_F16) verify_kernel<__half><<<grid, kVerThreads, 0, s>>>(a);
+  else verify_kernel<__nv_bfloat16><<<grid, kVerThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace mmq

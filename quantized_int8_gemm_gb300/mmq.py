@@ -26,6 +26,7 @@ MMQ_ERR_OOM = -6
 MMQ_ERR_UNSUPPORTED = -7
 MMQ_ERR_NO_DEVICE = -8
 MMQ_ERR_SCRATCH_LIMIT = -9
+MMQ_ERR_DEVICE_INDEX = -10
 
 MMQ_Q4_K = 12
 MMQ_Q6_K = 14
@@ -40,6 +41,9 @@ MMQ_ARM_SPLIT = 3
 MMQ_ARM_PAIR = 4
 MMQ_OUT_F16 = 1
 MMQ_OUT_F32 = 2
+MMQ_DT_F16 = 1
+MMQ_DT_F32 = 2
+MMQ_DT_BF16 = 3
 ARM_NAMES = {MMQ_ARM_F16: "f16_plane", MMQ_ARM_RAW: "raw_unpack", MMQ_ARM_SPLIT: "split_scale",
              MMQ_ARM_PAIR: "split_scale_sm_pairs"}
 
@@ -52,6 +56,7 @@ EXPORTS = [
     "mmq_gemm_noalloc", "mmq_debug_chunk_partials", "mmq_dequantize_weights",
     "mmq_last_device_error", "mmq_set_wait_timeout_ns",
     "mmq_selftest_wait_timeout", "mmq_strerror", "mmq_probe_engine_rates",
+    "mmq_page_tables", "mmq_kv_write", "mmq_paged_attention", "mmq_verify_draft",
 ]
 
 _lock = threading.Lock()
@@ -67,6 +72,8 @@ class MMQError(RuntimeError):
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load libmmq.so (built by quantized_int8_gemm_gb300.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -95,6 +102,12 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.mmq_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
         L.mmq_probe_engine_rates.argtypes = [vp, vp]
         L.mmq_strerror.argtypes = [i32]
+        # (structs go as the bytes serving.py packs)
+        cp = ctypes.c_char_p
+        L.mmq_page_tables.argtypes = [vp, vp, vp, i64, vp, i64, i64, vp, i64, i32, i64, vp, vp, vp, vp, vp, vp, vp]
+        L.mmq_kv_write.argtypes = [cp, vp, i64, i64, vp, i64, i64, i32, vp, i64, vp]
+        L.mmq_paged_attention.argtypes = [cp, cp, vp]
+        L.mmq_verify_draft.argtypes = [cp, vp]
         L.mmq_strerror.restype = ctypes.c_char_p
         for n in EXPORTS:
             f = getattr(L, n)
