@@ -66,6 +66,7 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 constexpr int kRows = 64, kKt = 64, kThreads = 128;
+constexpr int kSms = 152;
 
 // Byte offset of 16-byte chunk c of row r in a tile of kDp-wide rows; the
 // swizzle keeps the eight rows of an ldmatrix on different banks.
@@ -377,14 +378,19 @@ cudaError_t launch_attention(const mmq_paged_cache &c, const mmq_attention &t, c
   a.scale_log2 = t.scale * 1.44269504088896341f;
   a.wait = {&ctx.words->status, &ctx.words->abort_epoch, ctx.epoch, ctx.limit_ns};
 
-  const int slots = 2 * 152;
+  // The tcgen05 kernel (one CTA an SM) takes every shape it can; the general
+  // one (two CTAs an SM) the rest.
+  int tile_tok = 0, box = 0;
+  const bool umma = attention_umma_shape(c, t, &tile_tok, &box);
+  const int unit_rows = umma ? 2 * tile_tok * a.rep : kRows, kt = umma ? 128 : kKt;
+  const int64_t slots = umma ? kSms : 2 * kSms;
   // Rows are split over the keys where that can fill the SMs: fewer than four
-  // units for each slot, and a cache row of more than two tiles.
+  // units for each slot, and room for more than two tiles of keys.
   const int64_t rows = t.ntok * t.q_heads, room = static_cast<int64_t>(t.table_width) * c.page_size;
-  const int64_t units = (t.ntok * a.rep + kRows - 1) / kRows * c.heads;
+  const int64_t units = (t.ntok * a.rep + unit_rows - 1) / unit_rows * c.heads;
   int64_t pieces = 1;
-  if (units < 4 * slots && room > 2 * kKt) {
-    pieces = std::min<int64_t>((slots + c.heads - 1) / c.heads + 1, (room + kKt - 1) / kKt);
+  if (units < 4 * slots && room > 2 * kt) {
+    pieces = std::min<int64_t>((slots + c.heads - 1) / c.heads + 1, (room + kt - 1) / kt);
     pieces = std::min<int64_t>(pieces, (int64_t(256) << 20) / (rows * (a.d + 1) * 4));
     pieces = std::max<int64_t>(pieces, 1);
   }
@@ -404,7 +410,10 @@ cudaError_t launch_attention(const mmq_paged_cache &c, const mmq_attention &t, c
     a.part_lse = a.part_o + pieces * rows * a.d;
     a.part_n = reinterpret_cast<int32_t *>(a.part_lse + pieces * rows);
   }
-  e = launch_attention_rows(a, c.type, ctx.device, slots, s);
+  const unsigned grid = static_cast<unsigned>(pieces > 1 ? slots : std::min<int64_t>(slots, units + t.nreq * c.heads));
+  bool taken = false;
+  if (umma) e = launch_attention_umma(a, c, tile_tok, box, ctx.device, grid, s, &taken);
+  if (e == cudaSuccess && !taken) e = launch_attention_rows(a, c.type, ctx.device, grid, s);
   if (e == cudaSuccess && pieces > 1)
     e = c.type == MMQ_DT_F16 ? launch_join<__half>(a, s) : launch_join<__nv_bfloat16>(a, s);
   if (scratch) {

@@ -203,5 +203,8 @@ cudaError_t allow_smem(int dev, int bytes) {
 
 // The kernels' launches (attention.cu, attention_umma.cu).
 cudaError_t launch_attention_rows(const AttnArgs &a, int type, int dev, unsigned grid, cudaStream_t s);
+bool attention_umma_shape(const mmq_paged_cache &c, const mmq_attention &t, int *tile_tok, int *box);
+cudaError_t launch_attention_umma(const AttnArgs &a, const mmq_paged_cache &c, int tile_tok, int box, int dev, unsigned grid,
+                                  cudaStream_t s, bool *taken);
 
 }  // namespace mmq
