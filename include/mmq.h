@@ -436,8 +436,10 @@ typedef struct mmq_attention {
  * cache's type before they multiply V.  The results of one problem do not
  * change from call to call.
  *   Long rows are split over the SMs when there are few of them: partial
- * results (fp32, up to 256 MB) are stream-ordered scratch as for mmq_gemm.
+ * results (fp32, two for each SM, 40 MB) are stream-ordered scratch as for
+ * mmq_gemm.
  * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN, MMQ_ERR_TYPE, MMQ_ERR_OOM,
+ * MMQ_ERR_UNSUPPORTED (2^30 or more tiles of rows by keys),
  * MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
  */
 int mmq_paged_attention(const mmq_paged_cache *cache, const mmq_attention *args, mmq_stream_t stream);

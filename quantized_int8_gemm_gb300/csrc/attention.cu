@@ -90,13 +90,13 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
   constexpr int kTile = kKt * kDp * 2;
   const uint32_t sq = smem_addr(smem), sk = sq + kRows * kDp * 2, sv = sk + 2 * kTile;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  AttnSchedule<kKt> sched;
-  if (warp == 0) sched.plan(a, kRows, gridDim.x, 3);
+  AttnSchedule<kKt, kRows> sched;
+  if (warp == 0) sched.plan(a);
 
-  for (int u = blockIdx.x;; u += gridDim.x) {
+  for (;;) {
     if (warp == 0) {
       AttnUnit x;
-      const bool more = sched.find(a, u, x);
+      const bool more = sched.next(a, x);
       if (lane == 0) {
         s_more = more;
         if (more) s_unit = x;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
         int64_t page = 0;
         int off = 0;
         if (in) {
-          const int blk = key / a.page_size;
+          const int blk = a.by_page(key);
           page = row[blk];
           off = key - blk * a.page_size;
           if (page < 0 || page >= a.pages) {
@@ -230,17 +230,15 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
       const int64_t at = static_cast<int64_t>(un.q0 + tok) * a.hq + head;
       const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // (NaN stays)
       const float lse2 = sum > 0.0f ? fmaf(m[h], a.scale_log2, log2f(sum)) : sum == 0.0f ? -INFINITY : sum;
-      if (un.pieces > 1) {
-        float *dst = a.part_o + (un.piece * a.ntok * a.hq + at) * a.d;
+      if (un.slot >= 0) {
+        float *dst = reinterpret_cast<float *>(a.part_o + static_cast<int64_t>(un.slot) * (a.d / 4) * kRows) + 4 * (row - un.row0);
 #pragma unroll
         for (int j = 0; j < kDp / 8; ++j) {
           const int col = 8 * j + 2 * (lane & 3);
-          if (col < a.d) *reinterpret_cast<float2 *>(dst + col) = make_float2(o[j][2 * h] * inv, o[j][2 * h + 1] * inv);
+          if (col < a.d)
+            *reinterpret_cast<float2 *>(dst + (col >> 2) * (4 * kRows) + (col & 3)) = make_float2(o[j][2 * h] * inv, o[j][2 * h + 1] * inv);
         }
-        if ((lane & 3) == 0) {
-          a.part_lse[un.piece * a.ntok * a.hq + at] = lse2;
-          if (un.piece == 0) a.part_n[at] = un.pieces;
-        }
+        if ((lane & 3) == 0) a.part_lse[un.slot * kRows + row - un.row0] = lse2;
       } else {
         const int64_t to = (un.q0 + tok) * a.out_token + head * a.out_head;
 #pragma unroll
@@ -251,82 +249,94 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
           if (a.out_type == MMQ_DT_F32) *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + to + col) = make_float2(x, y);
           else *reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + to + col) = Pair<T>::pack(x, y);
         }
-        if ((lane & 3) == 0) {
-          if (a.lse) a.lse[at] = lse2 * kLn2;
-          if (a.max_pieces > 1) a.part_n[at] = 1;
-        }
+        if ((lane & 3) == 0 && a.lse) a.lse[at] = lse2 * kLn2;
       }
     }
     __syncthreads();  // the Q tile and s_unit are free
   }
 }
 
-// Joins the pieces of split rows: with lse_p (base 2) and normalised outputs
+// Joins the pieces of a cut unit: with lse_p (base 2) and normalised outputs
 // o_p, out = sum 2^(lse_p - top) o_p / sum 2^(lse_p - top), in fp32 and in the
-// pieces' order.  One warp a row; each lane adds four (eight) columns.
+// pieces' order.  Block (c, y): rows 16 y .. of the unit that begins in CTA c;
+// sixteen threads a row for the sums, then a thread for eight columns of a
+// row, lanes along the rows (as the partial results lie).
+constexpr int kJoinRows = 16;
 template <class T>
-__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a, int unit_rows) {
+  __shared__ float s_top[kJoinRows], s_inv[kJoinRows];
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = a.ntok * a.hq, at = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (at >= rows) return;
-  const int64_t tok = at / a.hq;
-  if (tok < a.q_start[0] || tok >= a.q_start[a.nreq]) return;  // rows of no request
-  const int n = a.part_n[at];
-  if (n < 2 || n > a.max_pieces) return;  // not split
-  float top = -INFINITY, bad = 0.0f;
-  for (int p = lane; p < n; p += 32) {
-    const float x = a.part_lse[p * rows + at];
-    top = fmaxf(top, x);
-    if (x != x) bad = x;
-  }
+  const AttnCut u = a.cuts[blockIdx.x];
+  const int r0 = blockIdx.y * kJoinRows, rows = min(min(unit_rows, u.n * a.rep - u.row0) - r0, kJoinRows);
+  if (u.last < 0 || rows <= 0) return;
+  const int c0 = blockIdx.x, pieces = u.last - c0 + 1;
+  auto slot = [&](int p) { return static_cast<int64_t>(2 * (c0 + p) + (p == 0)); };
+  auto where = [&](int r, int &tok, int &head) {
+    const int row = u.row0 + r0 + r;
+    tok = a.by_rep(row);
+    head = u.head * a.rep + row - tok * a.rep;
+    tok += u.q0;
+  };
+  {  // sixteen threads a row
+    const int r = threadIdx.x >> 4, sub = threadIdx.x & 15;
+    const float *lse = a.part_lse + r0 + min(r, rows - 1);
+    float top = -INFINITY, bad = 0.0f, sum = 0.0f;
+    for (int p = sub; p < pieces; p += 16) {
+      const float x = lse[slot(p) * unit_rows], high = fmaxf(top, x);
+      if (x != x) bad = x;
+      if (x == -INFINITY) continue;
+      sum = sum * (top == -INFINITY ? 0.0f : exp2f(top - high)) + exp2f(x - high);
+      top = high;
+    }
 #pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    bad += __shfl_xor_sync(0xffffffffu, bad, d);
+    for (int d = 8; d; d >>= 1) {
+      const float other = __shfl_xor_sync(0xffffffffu, top, d), more = __shfl_xor_sync(0xffffffffu, sum, d);
+      const float high = fmaxf(top, other);
+      sum = high == -INFINITY ? 0.0f : sum * exp2f(top - high) + more * exp2f(other - high);
+      top = high;
+      bad += __shfl_xor_sync(0xffffffffu, bad, d);
+    }
+    if (sub == 0 && r < rows) {
+      s_top[r] = top;
+      s_inv[r] = (sum > 0.0f ? 1.0f / sum : 0.0f) + bad;
+      int tok, head;
+      where(r, tok, head);
+      if (a.lse) a.lse[static_cast<int64_t>(tok) * a.hq + head] = (sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY) + bad;
+    }
   }
-  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  float sum = 0.0f;
-  for (int p0 = 0; p0 < n; p0 += 32) {
-    const float mine = p0 + lane < n ? a.part_lse[(p0 + lane) * rows + at] : -INFINITY;
-    const float w = mine == -INFINITY ? 0.0f : exp2f(mine - top);
-    const int here = min(32, n - p0);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kJoinRows * (a.d / 8); i += 256) {
+    const int c = i / kJoinRows, r = i % kJoinRows;
+    if (r >= rows) continue;
+    const float top = s_top[r], inv = s_inv[r];
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
 #pragma unroll 4
-    for (int i = 0; i < here; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      sum += wi;
-      if (wi == 0.0f) continue;
-      const float *src = a.part_o + ((p0 + i) * rows + at) * a.d;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int col = 4 * (lane + 32 * h);
-        if (col < a.d) {
-          const float4 x = __ldcs(reinterpret_cast<const float4 *>(src + col));
-          acc[h].x = fmaf(wi, x.x, acc[h].x);
-          acc[h].y = fmaf(wi, x.y, acc[h].y);
-          acc[h].z = fmaf(wi, x.z, acc[h].z);
-          acc[h].w = fmaf(wi, x.w, acc[h].w);
-        }
-      }
+    for (int p = 0; p < pieces; ++p) {
+      const int64_t s = slot(p);
+      const float l = a.part_lse[s * unit_rows + r0 + r];
+      const float4 *src = a.part_o + (s * (a.d / 4) + 2 * c) * unit_rows + r0 + r;
+      const float4 f = __ldcs(src), g = __ldcs(src + unit_rows);
+      if (l == -INFINITY) continue;
+      const float w = exp2f(l - top);
+      x.x = fmaf(w, f.x, x.x), x.y = fmaf(w, f.y, x.y), x.z = fmaf(w, f.z, x.z), x.w = fmaf(w, f.w, x.w);
+      y.x = fmaf(w, g.x, y.x), y.y = fmaf(w, g.y, y.y), y.z = fmaf(w, g.z, y.z), y.w = fmaf(w, g.w, y.w);
     }
-  }
-  const float inv = (sum > 0.0f ? 1.0f / sum : 0.0f) + bad;
-  const int64_t to = tok * a.out_token + (at - tok * a.hq) * a.out_head;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int col = 4 * (lane + 32 * h);
-    if (col >= a.d) continue;
+    int tok, head;
+    where(r, tok, head);
+    const int64_t to = tok * a.out_token + head * a.out_head + 8 * c;
     if (a.out_type == MMQ_DT_F32) {
-      *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to + col) =
-          make_float4(acc[h].x * inv, acc[h].y * inv, acc[h].z * inv, acc[h].w * inv);
+      float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to);
+      dst[0] = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+      dst[1] = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
     } else {
-      uint2 x;
-      x.x = Pair<T>::pack(acc[h].x * inv, acc[h].y * inv);
-      x.y = Pair<T>::pack(acc[h].z * inv, acc[h].w * inv);
-      *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + to + col) = x;
+      uint4 z;
+      z.x = Pair<T>::pack(x.x * inv, x.y * inv);
+      z.y = Pair<T>::pack(x.z * inv, x.w * inv);
+      z.z = Pair<T>::pack(y.x * inv, y.y * inv);
+      z.w = Pair<T>::pack(y.z * inv, y.w * inv);
+      *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + to) = z;
     }
   }
-  if (lane == 0 && a.lse) a.lse[at] = (sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY) + bad;
 }
 
 template <class T, int kDp>
@@ -345,9 +355,11 @@ cudaError_t launch_rows_of(const AttnArgs &a, int dev, unsigned grid, cudaStream
 }
 
 template <class T>
-cudaError_t launch_join(const AttnArgs &a, cudaStream_t s) {
+cudaError_t launch_join(const AttnArgs &a, int unit_rows, unsigned grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.ntok * a.hq + 7) / 8));
+  // (no unit has more rows than all tokens together)
+  const int64_t most = std::min<int64_t>(unit_rows, a.ntok * a.rep);
+  cfg.gridDim = dim3(grid, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -355,7 +367,7 @@ cudaError_t launch_join(const AttnArgs &a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<T>, a);
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<T>, a, unit_rows);
 }
 
 }  // namespace
@@ -380,42 +392,37 @@ cudaError_t launch_attention(const mmq_paged_cache &c, const mmq_attention &t, c
 
   // The tcgen05 kernel (one CTA an SM) takes every shape it can; the general
   // one (two CTAs an SM) the rest.
-  int tile_tok = 0, box = 0;
-  const bool umma = attention_umma_shape(c, t, &tile_tok, &box);
-  const int unit_rows = umma ? 2 * tile_tok * a.rep : kRows, kt = umma ? 128 : kKt;
-  const int64_t slots = umma ? kSms : 2 * kSms;
-  // Rows are split over the keys where that can fill the SMs: fewer than four
-  // units for each slot, and room for more than two tiles of keys.
-  const int64_t rows = t.ntok * t.q_heads, room = static_cast<int64_t>(t.table_width) * c.page_size;
-  const int64_t units = (t.ntok * a.rep + unit_rows - 1) / unit_rows * c.heads;
-  int64_t pieces = 1;
-  if (units < 4 * slots && room > 2 * kt) {
-    pieces = std::min<int64_t>((slots + c.heads - 1) / c.heads + 1, (room + kt - 1) / kt);
-    pieces = std::min<int64_t>(pieces, (int64_t(256) << 20) / (rows * (a.d + 1) * 4));
-    pieces = std::max<int64_t>(pieces, 1);
-  }
-  a.max_pieces = static_cast<int32_t>(pieces);
+  AttnUmma um;
+  const bool umma = attention_umma(a, c.type, &um);
+  const int unit_rows = umma ? 2 * um.tile_tok * a.rep : kRows, kt = umma ? 128 : kKt;
+  const unsigned grid = umma ? kSms : 2 * kSms;
+  a.unit_tok = umma ? 2 * um.tile_tok : 0;
+  a.by_page = FastDiv(c.page_size), a.by_rep = FastDiv(a.rep), a.by_grid = FastDiv(grid);
+  a.by_unit_tok = FastDiv(umma ? a.unit_tok : 1);
+  // The units' line (attention.cuh) is counted in 32 bits.
+  const int64_t room = static_cast<int64_t>(t.table_width) * c.page_size;
+  const int64_t units = ((t.ntok * a.rep + unit_rows - 1) / unit_rows + std::min(t.nreq, t.ntok)) * c.heads;
+  if (units >= (int64_t(1) << 30) / (std::min<int64_t>(room, 0x7fffffff) / kt + 2 + kAttnGap)) return cudaErrorNotSupported;
+  // Scratch for the pieces of cut units, unless no row can have keys for it.
+  const bool cut = room > 2 * kt;
   void *scratch = nullptr;
   cudaError_t e = cudaSuccess;
-  if (pieces > 1) {
-    const size_t o_bytes = static_cast<size_t>(pieces * rows * a.d) * 4, lse_bytes = static_cast<size_t>(pieces * rows) * 4;
+  if (cut) {
+    const size_t lse_bytes = static_cast<size_t>(2 * grid) * unit_rows * 4, o_bytes = lse_bytes * a.d;
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     e = cudaStreamIsCapturing(s, &cap);
     if (e != cudaSuccess) return e;
-    const size_t bytes = o_bytes + lse_bytes + static_cast<size_t>(rows) * 4;
+    const size_t bytes = o_bytes + lse_bytes + grid * sizeof(AttnCut);
     e = cap == cudaStreamCaptureStatusActive ? cudaMallocAsync(&scratch, bytes, s)
                                              : cudaMallocFromPoolAsync(&scratch, bytes, ctx.pool, s);
     if (e != cudaSuccess) return e;
-    a.part_o = static_cast<float *>(scratch);
-    a.part_lse = a.part_o + pieces * rows * a.d;
-    a.part_n = reinterpret_cast<int32_t *>(a.part_lse + pieces * rows);
+    a.part_o = static_cast<float4 *>(scratch);
+    a.part_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + o_bytes);
+    a.cuts = reinterpret_cast<AttnCut *>(static_cast<uint8_t *>(scratch) + o_bytes + lse_bytes);
   }
-  const unsigned grid = static_cast<unsigned>(pieces > 1 ? slots : std::min<int64_t>(slots, units + t.nreq * c.heads));
-  bool taken = false;
-  if (umma) e = launch_attention_umma(a, c, tile_tok, box, ctx.device, grid, s, &taken);
-  if (e == cudaSuccess && !taken) e = launch_attention_rows(a, c.type, ctx.device, grid, s);
-  if (e == cudaSuccess && pieces > 1)
-    e = c.type == MMQ_DT_F16 ? launch_join<__half>(a, s) : launch_join<__nv_bfloat16>(a, s);
+  e = umma ? launch_attention_umma(a, um, c.type, ctx.device, grid, s) : launch_attention_rows(a, c.type, ctx.device, grid, s);
+  if (e == cudaSuccess && cut)
+    e = c.type == MMQ_DT_F16 ? launch_join<__half>(a, unit_rows, grid, s) : launch_join<__nv_bfloat16>(a, unit_rows, grid, s);
   if (scratch) {
     const cudaError_t ef = cudaFreeAsync(scratch, s);
     if (e == cudaSuccess) e = ef;

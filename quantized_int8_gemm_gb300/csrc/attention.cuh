@@ -1,13 +1,20 @@
 // attention.cuh -- what the kernels of attention over a paged cache share: the
-// arguments, and how the work of all requests is cut into units.
+// arguments, and how the work of all requests is dealt to the CTAs.
 //
 // Rows: the query heads that share a K/V head (`rep` of them) are rows of one
 // problem, row = token * rep + head within the group, so K and V are read once
-// for the whole group.  A unit is one K/V head, a run of `rows` rows of one
-// request and a run of its K/V tiles ("piece").  Which units there are follows
-// from the lengths, which only the device knows: a warp of every CTA works
-// them out for itself and CTA c takes units c, c + grid, ...
+// for the whole group.  A unit is a K/V head and a run of `rows` rows of one
+// request, over the tiles of keys that its rows see.
+//
+// Which units there are follows from the lengths, which only the device
+// knows.  All units' tiles are laid end to end, with a gap (`kGap` tiles) in
+// front of each unit for what a unit costs beside its tiles, and each CTA
+// takes an equal stretch of that line: a few long rows and many short ones
+// then take every CTA the same time, and a CTA holds at most two pieces of
+// units that others share.  A warp of every CTA works its stretch out by
+// itself.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -17,56 +24,80 @@
 
 namespace mmq {
 
+// A unit cut into pieces: CTAs c .. last each left a partial result.
+struct AttnCut {
+  int q0, n, row0, head;
+  int last;  // -1: no unit of CTA c is cut behind it
+};
+
+// Division of 0 <= n < 2^31 by a number the host knows: with l = ceil(log2 d)
+// and m = ceil(2^(31 + l) / d), n m / 2^(31 + l) exceeds n / d by less than 1 / d.
+struct FastDiv {
+  uint32_t m = 0, shift = 0;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) {
+    uint32_t l = 0;
+    while ((uint64_t(1) << l) < d) ++l;
+    shift = 31 + l;
+    m = static_cast<uint32_t>(((uint64_t(1) << shift) + d - 1) / d);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * m >> shift);
+  }
+};
+
 struct AttnArgs {
   const void *q, *k, *v;
   void *out;
   float *lse;
   const int32_t *table, *seq_lens, *q_start;
-  float *part_o, *part_lse;  // partial results of split rows: [piece][token][q head][d], [piece][token][q head]
-  int32_t *part_n;           // pieces of a row: [token][q head]
+  // Partial results (fp32, normalised) of pieces, two slots a CTA: slot 2c + 1
+  // of the unit that begins in CTA c and goes on, slot 2c of one that began
+  // before it.  part_o [slot][d / 4][row of the unit] of 4 columns each,
+  // part_lse [slot][row of the unit] to base 2, cuts [CTA].  Null: units stay whole.
+  float4 *part_o;
+  float *part_lse;
+  AttnCut *cuts;
   int64_t q_token, q_head, out_token, out_head;
   int64_t k_page, k_token, k_head, v_page, v_token, v_head;
   int64_t table_stride, pages, ntok;
   int32_t nreq, table_width, page_size, hq, hkv, rep, d;
   int32_t causal, window, out_type;
-  int32_t max_pieces;
+  int32_t unit_tok;  // tokens of a unit (0: units are 64 rows, whatever their tokens)
+  FastDiv by_page, by_rep, by_unit_tok, by_grid;
   float scale_log2;  // scale * log2(e)
   WaitCtl wait;
 };
 
 // The part of one request that does not depend on the unit.
 struct AttnRequest {
-  int q0, n;       // first token, tokens
-  int len;         // keys
-  int tiles;       // row tiles
-  int t_lo, n_kv;  // first K/V tile that any row sees, K/V tiles from there
+  int q0, n;  // first token, tokens
+  int len;    // keys
+  int tiles;  // row tiles
 };
 
-template <int kKt>
-__device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, int b, int rows) {
+template <int kRows>
+__device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, int b) {
   AttnRequest r;
-  const int ntok = static_cast<int>(a.ntok);
-  r.q0 = max(0, min(a.q_start[b], ntok));
-  r.n = max(r.q0, min(a.q_start[b + 1], ntok)) - r.q0;
-  const int64_t room = static_cast<int64_t>(a.table_width) * a.page_size;
-  int len = max(a.seq_lens[b], 0);
-  if (len > room) {
+  const int ntok = static_cast<int>(a.ntok), from = a.q_start[b], to = a.q_start[b + 1], len = a.seq_lens[b];
+  r.q0 = max(0, min(from, ntok));
+  r.n = max(r.q0, min(to, ntok)) - r.q0;
+  // (a tile's keys are counted past the last one)
+  const int64_t room = min(static_cast<int64_t>(a.table_width) * a.page_size, static_cast<int64_t>(0x7fffff00));
+  r.len = max(len, 0);
+  if (r.len > room) {
     record_index(a.wait.status);
-    len = static_cast<int>(room);
+    r.len = static_cast<int>(room);
   }
-  r.len = len;
-  r.tiles = (r.n * a.rep + rows - 1) / rows;
-  const int64_t lo = a.window ? max(static_cast<int64_t>(0), static_cast<int64_t>(len) - r.n - a.window + 1) : 0;
-  r.t_lo = static_cast<int>(min(lo, static_cast<int64_t>(len))) / kKt;
-  r.n_kv = max(0, (len + kKt - 1) / kKt - r.t_lo);
+  r.tiles = kRows ? (r.n * a.rep + kRows - 1) / max(kRows, 1) : a.by_unit_tok(r.n + a.unit_tok - 1);
   return r;
 }
 
 struct AttnUnit {
   int q0, n, len, b, head;
-  int row0;          // first row of the unit within the request
-  int piece, pieces;
+  int row0;            // first row of the unit within the request
   int t_begin, t_end;  // K/V tiles (may be none)
+  int slot;            // of the partial result; -1: the unit is whole
 };
 
 // A row's keys: [lo, hi).
@@ -76,110 +107,189 @@ __device__ __forceinline__ void attn_row_range(const AttnArgs &a, int n, int len
   lo = a.window ? max(0, pos - a.window + 1) : 0;
 }
 
-// Deals the units out; every lane of one warp calls each function.
-template <int kKt>
+constexpr int kAttnGap = 2;
+
+// Deals the units out; every lane of one warp calls each function.  kRows: of
+// a unit, or 0 where units are whole tokens (AttnArgs::unit_tok).
+template <int kKt, int kRows>
 struct AttnSchedule {
-  int rows, cut;   // rows of a unit; K/V tiles of a piece
-  int b0, before;  // first request of the lanes' 32, units before it
-  int first;       // (lane) units of the lanes' requests before this one
-  AttnRequest r;   // (lane)
-  int pieces, each;
+  static constexpr int kGap = kAttnGap;
+  static constexpr int kLeast = 2;  // tiles a CTA takes at least
+  int b0;           // first of the 32 requests the lanes hold
+  AttnRequest r;    // (lane)
+  bool split;
+  // Places on the line: 32 bits (the host has checked its length)
+  int each;         // a CTA's stretch
+  int lo, hi;       // this CTA's
+  int pos;          // where the current unit begins
+  int b, qt, head;  // the current unit; b >= nreq: none
+  AttnRequest cur;  // its request
+  bool cut;         // this CTA has told of its cut unit
 
-  // `slots` units run at once; `fixed`: a unit's cost beside its tiles, in tiles.
-  // The cut is the one of eight with the least waves * (tiles + fixed).
-  __device__ void plan(const AttnArgs &a, int unit_rows, int slots, int fixed) {
-    rows = unit_rows;
-    cut = 1 << 28;
-    b0 = -32;
-    before = 0;
-    const int lane = threadIdx.x & 31;
-    if (a.max_pieces > 1) {
-      int64_t work = 0;
-      int longest = 0;
-      for (int b = lane; b < a.nreq; b += 32) {
-        const AttnRequest q = attn_request<kKt>(a, b, rows);
-        work += static_cast<int64_t>(q.tiles) * a.hkv * q.n_kv;
-        if (q.tiles) longest = max(longest, q.n_kv);
-      }
-      for (int d = 16; d; d >>= 1) work += __shfl_xor_sync(0xffffffffu, work, d);
-      longest = __reduce_max_sync(0xffffffffu, longest);
-      const int even = max(1, static_cast<int>(min((work + slots - 1) / slots, static_cast<int64_t>(1) << 24)));
-      int cand[8] = {even, even + (even + 7) / 8, even + (even + 3) / 4, even + (even + 1) / 2, 2 * even,
-                     max(1, (even + 1) / 2), max(1, (even + 2) / 3), max(1, longest)};
-      int units[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      for (int b = lane; b < a.nreq; b += 32) {
-        const AttnRequest q = attn_request<kKt>(a, b, rows);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          units[i] += q.tiles * a.hkv * max(1, min(a.max_pieces, (q.n_kv + cand[i] - 1) / cand[i]));
-      }
-      int64_t least = INT64_MAX;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int u = __reduce_add_sync(0xffffffffu, units[i]);
-        const int64_t cost = static_cast<int64_t>((u + slots - 1) / slots) * (min(cand[i], longest) + fixed);
-        if (cost < least) least = cost, cut = cand[i];
-      }
-    }
-    load(a, 0);
+  // K/V tiles of the rows of row tile q.
+  __device__ __forceinline__ void tiles_of(const AttnArgs &a, const AttnRequest &x, int q, int &t0, int &t1) const {
+    int from, to, none;
+    const int first = kRows ? a.by_rep(q * kRows) : q * a.unit_tok;
+    const int last = min(x.n, kRows ? a.by_rep((q + 1) * kRows - 1) + 1 : first + a.unit_tok) - 1;
+    attn_row_range(a, x.n, x.len, first, from, none);
+    attn_row_range(a, x.n, x.len, last, none, to);
+    t0 = from / kKt;
+    t1 = max(t0, (to + kKt - 1) / kKt);
   }
-
+  // Room of one unit on the line.
+  __device__ __forceinline__ int room_of(const AttnArgs &a, const AttnRequest &x, int q) const {
+    int t0, t1;
+    tiles_of(a, x, q, t0, t1);
+    return kGap + max(1, t1 - t0);
+  }
+  __device__ __forceinline__ AttnRequest lane_request(int l) const {
+    return {__shfl_sync(0xffffffffu, r.q0, l), __shfl_sync(0xffffffffu, r.n, l), __shfl_sync(0xffffffffu, r.len, l),
+            __shfl_sync(0xffffffffu, r.tiles, l)};
+  }
   __device__ __forceinline__ void load(const AttnArgs &a, int from) {
-    const int lane = threadIdx.x & 31;
     b0 = from;
-    int units = 0;
-    r = AttnRequest{0, 0, 0, 0, 0, 0};
-    pieces = each = 1;
-    if (b0 + lane < a.nreq) {
-      r = attn_request<kKt>(a, b0 + lane, rows);
-      if (r.n_kv > 0) {
-        const int want = max(1, min(a.max_pieces, (r.n_kv + cut - 1) / cut));
-        each = (r.n_kv + want - 1) / want;
-        pieces = (r.n_kv + each - 1) / each;
-      }
-      units = r.tiles * pieces * a.hkv;
-    }
-    int sum = units;
+    const int at = b0 + (threadIdx.x & 31);
+    r = AttnRequest{0, 0, 0, 0};
+    if (at < a.nreq) r = attn_request<kRows>(a, at);
+  }
+  __device__ static __forceinline__ int inclusive(int x) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, sum, d);
-      if ((threadIdx.x & 31) >= d) sum += y;
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if (static_cast<int>(threadIdx.x & 31) >= d) x += y;
     }
-    first = sum - units;
-    total = __shfl_sync(0xffffffffu, sum, 31);
+    return x;
   }
-  int total;  // units of the lanes' requests
-
-  // Unit u (ascending from call to call); false when there are fewer.
-  __device__ bool find(const AttnArgs &a, int u, AttnUnit &o) {
-    while (u - before >= total) {
-      if (b0 + 32 >= a.nreq) return false;
-      before += total;
-      load(a, b0 + 32);
+  // Room of the lane's request (all K/V heads), and the longest unit's.
+  __device__ __forceinline__ int lane_room(const AttnArgs &a, int &longest) const {
+    const int lane = threadIdx.x & 31;
+    int sum = 0;
+    if (r.tiles == 1) {
+      sum = room_of(a, r, 0);
+      longest = max(longest, sum);
     }
-    int i = u - before;
-    // the last request whose units begin at or before i (one without units begins where the next does)
-    const uint32_t here = __ballot_sync(0xffffffffu, first <= i);
-    const int l = 31 - __clz(here);
-    i -= __shfl_sync(0xffffffffu, first, l);
-    o.b = b0 + l;
-    o.q0 = __shfl_sync(0xffffffffu, r.q0, l);
-    o.n = __shfl_sync(0xffffffffu, r.n, l);
-    o.len = __shfl_sync(0xffffffffu, r.len, l);
-    o.pieces = __shfl_sync(0xffffffffu, pieces, l);
-    const int run = __shfl_sync(0xffffffffu, each, l), tiles = __shfl_sync(0xffffffffu, r.tiles, l);
-    const int t_lo = __shfl_sync(0xffffffffu, r.t_lo, l);
-    o.head = i % a.hkv;
-    i /= a.hkv;
-    o.piece = i % o.pieces;
-    o.row0 = (tiles - 1 - i / o.pieces) * rows;  // the rows that see most come first
-    int lo, hi, none;
-    attn_row_range(a, o.n, o.len, o.row0 / a.rep, lo, none);
-    attn_row_range(a, o.n, o.len, min(o.n - 1, (o.row0 + rows - 1) / a.rep), none, hi);
-    o.t_begin = max(t_lo + o.piece * run, lo / kKt);
-    o.t_end = min(t_lo + (o.piece + 1) * run, (hi + kKt - 1) / kKt);
-    if (o.t_end < o.t_begin) o.t_end = o.t_begin;
-    return true;
+    uint32_t many = __ballot_sync(0xffffffffu, r.tiles > 1);
+    while (many) {
+      const int l = __ffs(many) - 1;
+      many &= many - 1;
+      const AttnRequest x = lane_request(l);
+      int part = 0;
+#pragma unroll 1
+      for (int q = lane; q < x.tiles; q += 32) {
+        const int y = room_of(a, x, q);
+        part += y;
+        longest = max(longest, y);
+      }
+      part = __reduce_add_sync(0xffffffffu, part);
+      if (lane == l) sum = part;
+    }
+    return sum * a.hkv;
+  }
+
+  // Finds this CTA's stretch and the first unit that reaches into it.
+  __device__ __forceinline__ void plan(const AttnArgs &a) {
+    cut = false;
+    const int lane = threadIdx.x & 31;
+    int total = 0, mine = 0, longest = 0;
+#pragma unroll 1
+    for (int from = (a.nreq - 1) / 32 * 32; from >= 0; from -= 32) {  // (ends with the first 32 at hand)
+      load(a, from);
+      mine = lane_room(a, longest);
+      total += mine;
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    each = max(a.by_grid(total + static_cast<int>(gridDim.x) - 1), kLeast);
+    // Whole units where the longest is short beside a stretch: a piece costs
+    // its partial result and the join.
+    split = a.part_o && longest > kGap + kLeast && longest * 16 > each;
+    lo = each * static_cast<int>(blockIdx.x);
+    hi = lo + each;
+    pos = 0;
+    int end = inclusive(mine);
+    uint32_t past;
+    while (!(past = __ballot_sync(0xffffffffu, pos + end > lo))) {
+      pos += __shfl_sync(0xffffffffu, end, 31);
+      if (b0 + 32 >= a.nreq) {
+        b = a.nreq;
+        return;
+      }
+      load(a, b0 + 32);
+      mine = lane_room(a, longest);
+      end = inclusive(mine);
+    }
+    int l = __ffs(past) - 1;
+    pos += __shfl_sync(0xffffffffu, end - mine, l);
+    b = b0 + l;
+    cur = lane_request(l);
+    for (qt = 0;; qt += 32) {  // (the request reaches past lo, so one of its row tiles does)
+      mine = qt + lane < cur.tiles ? room_of(a, cur, qt + lane) * a.hkv : 0;
+      end = inclusive(mine);
+      past = __ballot_sync(0xffffffffu, mine && pos + end > lo);
+      if (past || qt + 32 >= cur.tiles) break;
+      pos += __shfl_sync(0xffffffffu, end, 31);
+    }
+    l = past ? __ffs(past) - 1 : 0;
+    pos += __shfl_sync(0xffffffffu, end - mine, l);
+    qt += l;
+    const int unit = room_of(a, cur, qt);
+    head = lo > pos ? (lo - pos) / unit : 0;
+    pos += head * unit;
+  }
+
+  __device__ __forceinline__ void step(const AttnArgs &a, int unit) {
+    pos += unit;
+    if (++head < a.hkv) return;
+    head = 0;
+    if (++qt < cur.tiles) return;
+    qt = 0;
+    for (;;) {  // the next request with rows
+      const int l = b + 1 - b0;
+      const uint32_t rest = __ballot_sync(0xffffffffu, r.tiles > 0 && static_cast<int>(threadIdx.x & 31) >= l);
+      if (rest) {
+        b = b0 + __ffs(rest) - 1;
+        cur = lane_request(__ffs(rest) - 1);
+        return;
+      }
+      if (b0 + 32 >= a.nreq) {
+        b = a.nreq;
+        return;
+      }
+      load(a, b0 + 32);
+      b = b0 - 1;
+    }
+  }
+
+  // This CTA's next unit, or piece of one; false when there are no more.
+  __device__ __forceinline__ bool next(const AttnArgs &a, AttnUnit &o) {
+    while (b < a.nreq) {
+      const int unit = room_of(a, cur, qt);
+      const int first = pos + kGap, end = pos + unit;  // where its tiles lie
+      if (first >= hi) break;
+      int t0, t1;
+      tiles_of(a, cur, qt, t0, t1);
+      o = {cur.q0, cur.n, cur.len, b, head, qt * (kRows ? kRows : a.unit_tok * a.rep), t0, t1, -1};
+      step(a, unit);
+      if (!split) {
+        if (first >= lo) return true;
+        continue;
+      }
+      if (end <= lo) continue;
+      const int me = blockIdx.x, c0 = first >= lo ? me : first / each, c1 = end <= hi ? me : (end - 1) / each;
+      if (c0 == c1) return true;
+      o.t_begin = t0 + max(0, lo - first);
+      o.t_end = min(t1, t0 + (hi - first));
+      const bool begins = c0 == me;
+      o.slot = 2 * me + begins;
+      if (begins) {
+        cut = true;
+        if ((threadIdx.x & 31) == 0) a.cuts[me] = {o.q0, o.n, o.row0, o.head, c1};
+      }
+      return true;
+    }
+    if (a.cuts && !cut && (threadIdx.x & 31) == 0) a.cuts[blockIdx.x].last = -1;
+    cut = true;
+    return false;
   }
 };
 
@@ -203,8 +313,13 @@ cudaError_t allow_smem(int dev, int bytes) {
 
 // The kernels' launches (attention.cu, attention_umma.cu).
 cudaError_t launch_attention_rows(const AttnArgs &a, int type, int dev, unsigned grid, cudaStream_t s);
-bool attention_umma_shape(const mmq_paged_cache &c, const mmq_attention &t, int *tile_tok, int *box);
-cudaError_t launch_attention_umma(const AttnArgs &a, const mmq_paged_cache &c, int tile_tok, int box, int dev, unsigned grid,
-                                  cudaStream_t s, bool *taken);
+// What the tcgen05 kernel needs beside the arguments; false: it does not take the problem.
+struct AttnUmma {
+  CUtensorMap q, k, v;
+  int tile_tok;  // tokens of a row tile
+  int box;       // keys of one copy
+};
+bool attention_umma(const AttnArgs &a, int type, AttnUmma *u);
+cudaError_t launch_attention_umma(const AttnArgs &a, const AttnUmma &u, int type, int dev, unsigned grid, cudaStream_t s);
 
 }  // namespace mmq

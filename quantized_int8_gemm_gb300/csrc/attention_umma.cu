@@ -2,12 +2,14 @@
 // tensor cores of sm_103a (tcgen05), for head widths up to 128.
 //
 // A unit (attention.cuh) is up to 256 rows of one K/V head, as two tiles of
-// 128, over a run of K/V tiles of 128 keys.  For each tile t and key tile j
-//   S_t = Q_t K_j^T   (TMEM, fp32)            one UMMA warp
-//   P_t = exp2(scale S_t - m), 16 bits, over S_t's columns    softmax warps of t
-//   O_t += P_t V_j    (TMEM, fp32; P read from TMEM)          the UMMA warp
-// While the softmax warps of one tile work, the tensor core runs the other
-// tile's products.
+// 128, over tiles of 128 keys.  There are two lanes t of
+//   S_t = Q K_j^T   (TMEM, fp32)                            UMMA warp t
+//   P_t = exp2(scale S_t - m), 16 bits, over S_t's columns  softmax warps of t
+//   O_t += P_t V_j  (TMEM, fp32; P read from TMEM)          UMMA warp t
+// and while the softmax warps of one lane work, the tensor core runs the other
+// lane's products.  With two row tiles lane t is row tile t and sees every key
+// tile.  With one (decode steps, short chunks) both lanes are that tile: lane t
+// takes every second key tile, and their results are joined at the end.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -22,7 +24,7 @@ namespace {
 
 constexpr int kKt = 128;        // keys of a tile
 constexpr int kThreads = 384;   // softmax warps 0-3 (tile 0) and 4-7 (tile 1), control warps 8-11
-constexpr int kUmmaWarp = 8, kLoadWarp = 9, kTailWarp = 10;
+constexpr int kUmmaWarp = 8, kLoadWarp = 10, kTailWarp = 11;  // UMMA warp of lane t: 8 + t
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 216, kRegsControl = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsControl == kThreads * kRegsLaunch,
               "the register split must add up to what the launch holds");
@@ -39,15 +41,12 @@ struct Lay {
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTile;
   static constexpr int kBars = kRing + kStages * kTile;
-  static constexpr int kNumBars = 3 * kStages + 2 + 8 + 2 * kUnits + 1;
-  static constexpr int kUnitsAt = kBars + kNumBars * 8;
+  static constexpr int kNumBars = 3 * kStages + 2 + 14 + 2 * kUnits + 1;
+  static constexpr int kStats = kBars + kNumBars * 8;  // lane 1's maximum and sum of each row
+  static constexpr int kUnitsAt = kStats + 128 * 8;
   static constexpr int kSlot = kUnitsAt + kUnits * static_cast<int>(sizeof(AttnUnit));
   static constexpr int kBytes = kSlot + 16 + 1024;  // the base is rounded up to 1024
   static_assert(kBytes <= 232448, "shared memory of a CTA");
-};
-
-struct Maps {
-  CUtensorMap q, k, v;
 };
 
 __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar) {
@@ -88,9 +87,47 @@ __device__ __forceinline__ uint32_t pack(float a, float b, __nv_bfloat16) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void parts_of(uint64_t p, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 32 lanes x 32 columns, and the largest of each lane's 32 (fp32; NaN is passed over).
+__device__ __forceinline__ void tmem_ld_max_x32(uint32_t taddr, uint32_t *r, float &top) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(top)
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <class T, int kDp>
 __global__ void __launch_bounds__(kThreads, 1)
-    attention_umma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Maps maps, int tile_tok, int box) {
+    attention_umma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnUmma um) {
   using L = Lay<kDp>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -103,40 +140,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kFix = 3 * L::kStages;
   const uint32_t q_full = bars + 8u * kFix, q_empty = bars + 8u * (kFix + 1);
   auto s_full = [&](int t) { return bars + 8u * (kFix + 2 + t); };
-  auto p_full = [&](int t) { return bars + 8u * (kFix + 4 + t); };
-  auto o_full = [&](int t) { return bars + 8u * (kFix + 6 + t); };
-  auto o_empty = [&](int t) { return bars + 8u * (kFix + 8 + t); };
-  auto u_full = [&](int i) { return bars + 8u * (kFix + 10 + i); };
-  auto u_empty = [&](int i) { return bars + 8u * (kFix + 10 + kUnits + i); };
+  auto p_full = [&](int t, int half) { return bars + 8u * (kFix + 4 + 2 * t + half); };
+  auto o_full = [&](int t) { return bars + 8u * (kFix + 8 + t); };
+  auto o_empty = [&](int t) { return bars + 8u * (kFix + 10 + t); };
+  const uint32_t stats_full = bars + 8u * (kFix + 12), stats_empty = bars + 8u * (kFix + 13);
+  auto turn = [&](int t) { return bars + 8u * (kFix + 14 + t); };
+  auto u_full = [&](int i) { return bars + 8u * (kFix + 16 + i); };
+  auto u_empty = [&](int i) { return bars + 8u * (kFix + 16 + kUnits + i); };
   const uint32_t done = bars + 8u * (L::kNumBars - 1);
   AttnUnit *units = reinterpret_cast<AttnUnit *>(smem + L::kUnitsAt);
   const WaitCtl &w = a.wait;
+  float2 *stats = reinterpret_cast<float2 *>(smem + L::kStats);
+  const int tile_tok = um.tile_tok, box = um.box;
   const int half_rows = tile_tok * a.rep;  // rows of one tile (at most 128)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(kv_full(s), 1);
-      mbar_init(kv_empty(s), 1);
+      mbar_init(kv_empty(s), 2);  // both UMMA warps
       mbar_init(tail(s), 1);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), 4);
+      mbar_init(p_full(t, 0), 4);
+      mbar_init(p_full(t, 1), 4);
       mbar_init(o_full(t), 1);
       mbar_init(o_empty(t), 4);
+      mbar_init(turn(t), 1);
     }
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(u_full(i), 1);
-      mbar_init(u_empty(i), 10);  // the UMMA warp, the tail warp and eight softmax warps
+      mbar_init(u_empty(i), 11);  // the UMMA warps, the tail warp and eight softmax warps
     }
-    mbar_init(done, 1);
+    mbar_init(stats_full, 4);
+    mbar_init(stats_empty, 4);
+    mbar_init(done, 2);
     fence_mbar_init();
   }
+  if (warp == kTailWarp && lane < 3) {
+    const CUtensorMap *m = lane == 0 ? &um.q : lane == 1 ? &um.k : &um.v;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+  }
+  griddep_launch_dependents();  // the join's CTAs come as these leave
   if (warp == kUmmaWarp) {
     tmem_alloc(base + L::kSlot, 512);
     tmem_relinquish();
+  }
+  AttnSchedule<kKt, 0> sched;
+  AttnUnit un;
+  if (warp == kLoadWarp) {  // its first unit, while the others set up
+    sched.plan(a);
+    if (!sched.next(a, un)) un.n = 0;
   }
   tc_fence_before();
   __syncthreads();
@@ -160,16 +216,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     if (warp == kLoadWarp) {
       // ---------------------------------------------------------- loads, and the units' order
-      AttnSchedule<kKt> sched;
-      sched.plan(a, 2 * half_rows, gridDim.x, 4);
       const int boxes = kKt / box;  // of a key tile, each `box` keys of one page
       uint32_t ks = 0, nu = 0, nq = 0;
       uint32_t tails = 0;           // stages whose last load was a tail
       bool ok = true;
-      for (int u = blockIdx.x; ok; u += gridDim.x, ++nu) {
-        AttnUnit un;
-        const bool more = sched.find(a, u, un);
-        if (!more) un.n = 0;
+      for (; ok; ++nu) {
+        if (nu && !sched.next(a, un)) un.n = 0;
+        const bool more = un.n > 0;
         const int e = nu % kUnits;
         ok = wait(u_empty(e), ((nu / kUnits) & 1) ^ 1);
         if (!ok) break;
@@ -188,26 +241,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane < 2 * L::kHalves) {
           const int t = lane / L::kHalves, h = lane % L::kHalves;
           if (t == 0 || two)
-            tma_load4(base + L::kQ + t * L::kTile + h * 16384, &maps.q, h * 64, 0, un.head, un.q0 + un.row0 / a.rep + t * tile_tok, q_full);
+            tma_load4(base + L::kQ + t * L::kTile + h * 16384, &um.q, h * 64, 0, un.head, un.q0 + a.by_rep(un.row0) + t * tile_tok, q_full);
         }
         const int32_t *row = a.table + un.b * a.table_stride;
         const int mine = lane / L::kHalves, h = lane % L::kHalves;  // (boxes * halves <= 32)
+        // page ids are read two tiles ahead and looked at when they are used
         auto page_of = [&](int t) {
           const int key = t * kKt + mine * box;
-          int id = 0;
-          if (mine < boxes && key < un.len && t < un.t_end) {
-            id = row[key / a.page_size];
-            if (id < 0 || id >= a.pages) {  // out of the cache: past the map's last page, zeros come
-              record_index(w.status);
-              id = static_cast<int>(a.pages);
-            }
-          }
-          return id;
+          return mine < boxes && key < un.len && t < un.t_end ? row[a.by_page(key)] : 0;
         };
-        int next = page_of(un.t_begin);
+        int ahead[2] = {page_of(un.t_begin), page_of(un.t_begin + 1)};
         for (int t = un.t_begin; t < un.t_end && ok; ++t) {
-          const int id = next, key = t * kKt + mine * box, off = key % a.page_size;
-          next = page_of(t + 1);
+          int id = ahead[0];
+          ahead[0] = ahead[1];
+          ahead[1] = page_of(t + 2);
+          const int key = t * kKt + mine * box, off = key - a.by_page(key) * a.page_size;
+          if (id < 0 || id >= a.pages) {  // out of the cache: past the map's last page, zeros come
+            record_index(w.status);
+            id = static_cast<int>(a.pages);
+          }
           const int keys = min(kKt, un.len - t * kKt), n = (keys + box - 1) / box;
           const bool load = mine < n;
 #pragma unroll
@@ -222,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(bar, n * L::kHalves * box * 128);
             __syncwarp();
             if (load)
-              tma_load4(base + L::kRing + s * L::kTile + h * 16384 + mine * box * 128, kv ? &maps.v : &maps.k, h * 64, off, un.head, id, bar);
+              tma_load4(base + L::kRing + s * L::kTile + h * 16384 + mine * box * 128, kv ? &um.v : &um.k, h * 64, off, un.head, id, bar);
           }
         }
       }
@@ -242,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // that 0 * V is 0.
       uint32_t ks = 0, nu = 0, phase = 0;
       bool ok = true;
-      AttnUnit un;
       while (take_unit(nu++, un, ok)) {
         const int tiles = un.t_end - un.t_begin;
         if (tiles == 0) continue;
@@ -263,83 +314,110 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(kv_full(s));
       }
-    } else if (warp == kUmmaWarp) {
-      // ---------------------------------------------------------- UMMAs
+    } else {
+      // ---------------------------------------------------------- UMMAs of lane t
+      // Two warps, as the tensor pipe queues little work: while one waits for
+      // its weights or a stage, the other keeps it fed.  S_t, P_t and O_t are
+      // this warp's alone, and its UMMAs run in the order they are issued in.
+      const int t = warp - kUmmaWarp;
       uint32_t elected;
       asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(elected));
       constexpr uint32_t id_qk = idesc_f16_f32(128, kKt) | kFormat<T>;
       constexpr uint32_t id_pv = idesc_f16_f32(128, kDp) | kFormat<T> | kBNMajor;
-      uint32_t ks = 0, nu = 0, nq = 0, np[2] = {0, 0}, no[2] = {0, 0};
+      const uint64_t kd0 = sdesc_kmajor_sw128(base + L::kRing), vd0 = sdesc_nmajor_sw128(base + L::kRing);
+      const uint32_t d_s = tmem + 128 * t, d_o = tmem + 256 + 128 * t;
+      uint32_t ks = 0, nu = 0, nq = 0, np = 0, no = 0, nt = 0;
       bool ok = true;
-      AttnUnit un;
-      auto qk = [&](int t, int s) {
-        if (elected) {
-          const uint64_t qd = sdesc_kmajor_sw128(base + L::kQ + t * L::kTile), kd = sdesc_kmajor_sw128(base + L::kRing + s * L::kTile);
-#pragma unroll
-          for (int k = 0; k < kDp / 16; ++k) {
-            const uint64_t at = (k >> 2) * (16384 >> 4) + (k & 3) * 2;
-            umma_f16(tmem + 128 * t, qd + at, kd + at, id_qk, k > 0);
-          }
-          umma_commit(s_full(t));
-        }
-        __syncwarp();
+      auto stage = [&](uint32_t k) { return static_cast<int>(k % L::kStages); };
+      auto landed = [&](uint32_t k) { return wait(kv_full(stage(k)), (k / L::kStages) & 1); };
+      // Both lanes pass every load of the ring in its order, also those only
+      // the other one uses: a lane that skipped a stage's load could take the
+      // load before it for its own (a phase is told by its parity).
+      auto skip = [&](uint32_t k) {
+        const bool got = landed(k);
+        if (got && lane == 0) mbar_arrive(kv_empty(stage(k)));
+        return got;
       };
-      auto pv = [&](int t, int s, int steps, bool fresh) {
-        if (elected) {
-          const uint64_t vd = sdesc_nmajor_sw128(base + L::kRing + s * L::kTile);
-          for (int k = 0; k < steps; ++k)
-            umma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, vd + k * (2048 >> 4), id_pv, !(fresh && k == 0));
+      // With two row tiles the lanes take turns (P_t V of one key tile and Q K^T
+      // of the next are one turn), so that one lane's softmax runs beside the
+      // other's UMMAs; left alone they fall into step and the tensor pipe idles
+      // while both wait for their weights (3.9 against 3.0 thousand clocks a
+      // key tile).
+      auto my_turn = [&](bool two) { return !two || wait(turn(t), (nt++ & 1) ^ (t == 0)); };
+      // S_t = Q K^T from load k
+      auto qk = [&](uint64_t qd, uint32_t k, bool two, bool known) {
+        const bool got = known || landed(k);
+        if (got) {
+          tc_fence_after();
+          if (elected) {
+            const uint64_t kd = kd0 + stage(k) * (L::kTile >> 4);
+#pragma unroll
+            for (int i = 0; i < kDp / 16; ++i) {
+              const uint64_t at = (i >> 2) * (16384 >> 4) + (i & 3) * 2;
+              umma_f16(d_s, qd + at, kd + at, id_qk, i > 0);
+            }
+            if (two) mbar_arrive(turn(t ^ 1));
+            umma_commit(s_full(t));
+            umma_commit(kv_empty(stage(k)));
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        return got;
+      };
+      // O_t (+)= P_t V from load k; the first 64 keys' weights may be there before the rest
+      auto pv = [&](uint32_t k, int steps, bool fresh, bool two, bool last) {
+        bool got = landed(k);
+        if (got && two && !last) got = landed(k + 1);  // (the next key tile's K, so that the turn does not wait for it)
+        if (got && fresh) got = wait(o_empty(t), (no++ & 1) ^ 1);
+        const uint64_t vd = vd0 + stage(k) * (L::kTile >> 4);
+        const uint32_t parity = np++ & 1;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (got) got = wait(p_full(t, half), parity);
+          if (got && half == 0) got = my_turn(two);
+          if (!got) return false;
+          tc_fence_after();
+          if (elected) {
+#pragma unroll
+            for (int i = 4 * half; i < 4 * half + 4; ++i)
+              if (i < steps) umma_ts(d_o, d_s + 8 * i, vd + i * (2048 >> 4), id_pv, !(fresh && i == 0));
+            if (half) {
+              if (two && last) mbar_arrive(turn(t ^ 1));
+              umma_commit(kv_empty(stage(k)));
+            }
+          }
+          __syncwarp();
+        }
+        return true;
       };
       while (take_unit(nu++, un, ok)) {
         const int tiles = un.t_end - un.t_begin;
         if (tiles == 0) continue;
-        const int n_t = two_tiles(un) ? 2 : 1;
-        ok = wait(q_full, nq++ & 1) && wait(kv_full(ks % L::kStages), (ks / L::kStages) & 1);
+        const bool two = two_tiles(un);
+        ok = wait(q_full, nq++ & 1);
         if (!ok) break;
-        tc_fence_after();
-        for (int t = 0; t < n_t; ++t) qk(t, ks % L::kStages);
-        if (elected) {
-          umma_commit(kv_empty(ks % L::kStages));
-          if (tiles == 1) umma_commit(q_empty);
-        }
-        __syncwarp();
-        ++ks;
-        for (int j = 0; j < tiles && ok; ++j, ks += 2) {
-          // ks: V of tile j, ks + 1: K of tile j + 1
-          const int sv = ks % L::kStages, sk = (ks + 1) % L::kStages;
-          const bool more = j + 1 < tiles;
-          const int keys = min(kKt, un.len - (un.t_begin + j) * kKt), steps = (keys + 15) >> 4;
-          ok = wait(kv_full(sv), (ks / L::kStages) & 1);
-          for (int t = 0; t < n_t && ok; ++t) {
-            if (j == 0) ok = wait(o_empty(t), (no[t]++ & 1) ^ 1);
-            ok = ok && wait(p_full(t), np[t]++ & 1);
-            if (ok && more && t == 0) ok = wait(kv_full(sk), ((ks + 1) / L::kStages) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            pv(t, sv, steps, j == 0);
-            if (t == n_t - 1) {
-              if (elected) umma_commit(kv_empty(sv));
-              __syncwarp();
-            }
-            if (more) {
-              qk(t, sk);
-            } else {
-              if (elected) umma_commit(o_full(t));
-              __syncwarp();
-            }
+        const uint64_t qd = sdesc_kmajor_sw128(base + L::kQ + (two ? t : 0) * L::kTile);
+        const int first = two ? 0 : t, dj = two ? 1 : 2;  // this lane's key tiles
+        if (first >= tiles && lane == 0) mbar_arrive(q_empty);
+        for (int j = 0; j < tiles && ok; ++j, ks += 2) {  // loads: K of tile j, then its V
+          if (!two && (j & 1) != t) {
+            ok = skip(ks) && skip(ks + 1);
+            continue;
           }
-          if (ok && more) {
-            if (elected) {
-              umma_commit(kv_empty(sk));
-              if (j + 2 == tiles) umma_commit(q_empty);  // the unit's last Q K^T
-            }
+          const bool last = j + dj >= tiles;
+          if (j == first) ok = my_turn(two);
+          ok = ok && qk(qd, ks, two, two && j != first);
+          if (ok && last) {
+            if (elected) umma_commit(q_empty);
+            __syncwarp();
+          }
+          ok = ok && pv(ks + 1, (min(kKt, un.len - (un.t_begin + j) * kKt) + 15) >> 4, j == first, two, last);
+          if (ok && last) {
+            if (elected) umma_commit(o_full(t));
             __syncwarp();
           }
         }
         if (!ok) break;
-        --ks;  // the loop counted a K past the unit's last V
       }
       if (elected) umma_commit(done);
       __syncwarp();
@@ -350,58 +428,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ softmax: one row a thread
     const int t = warp >> 2, quad = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
+    const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t, to1 = tmem + lanes + 384;
     const float sc = a.scale_log2;
-    uint32_t nu = 0, ns = 0, no = 0;
+    uint32_t nu = 0, ns = 0, no[2] = {0, 0}, nx = 0;
     bool ok = true;
-    AttnUnit un;
     while (take_unit(nu++, un, ok)) {
-      if (t == 1 && !two_tiles(un)) continue;
-      const int r = quad * 32 + lane, row = un.row0 + t * half_rows + r, tok = row / a.rep;
+      const bool two = two_tiles(un);
+      const int tiles = un.t_end - un.t_begin, q = two ? t : 0;
+      const int r = quad * 32 + lane, row = un.row0 + q * half_rows + r, tok = a.by_rep(row);
       const bool valid = r < half_rows && row < un.n * a.rep;
       const bool some = __any_sync(0xffffffffu, valid);
       int lo, hi;
       attn_row_range(a, un.n, un.len, tok, lo, hi);
       float m = -INFINITY, l = 0.0f;
-      for (int j = un.t_begin; j < un.t_end; ++j) {
+      const int j0 = un.t_begin + (two ? 0 : t), dj = two ? 1 : 2;
+      for (int j = j0; j < un.t_end; j += dj) {
         ok = wait(s_full(t), ns & 1);
         if (!ok) break;
         ++ns;
         tc_fence_after();
         if (some) {
+          // Hidden keys: S is set to -inf in TMEM first, 32 columns at a time
+          // (small code; few tiles have any).
+          const int from = lo - j * kKt, to_key = hi - j * kKt;
+          if (__any_sync(0xffffffffu, valid && (from > 0 || to_key < kKt))) {
+#pragma unroll 1
+            for (int c = 0; c < kKt; c += 32) {
+              uint32_t y[32];
+              tmem_ld_32x32b_x32(ts + c, y);
+              tmem_wait_ld(y);
+              const int y0 = from - c, y1 = to_key - c;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < y0 || i >= y1) y[i] = 0xff800000u;
+              tmem_st_32x32b_x32(ts + c, y);
+            }
+            tmem_wait_st();
+          }
           uint32_t x[2][64];
-          tmem_ld_32x32b_x64(ts, x[0]);
-          tmem_ld_32x32b_x64(ts + 64, x[1]);
+          float top[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) tmem_ld_max_x32(ts + 32 * h, x[h >> 1] + 32 * (h & 1), top[h]);
           tmem_wait_ld(x[0]);
           tmem_wait_ld(x[1]);
-          const int from = lo - j * kKt, span = hi - lo;
-          if (__any_sync(0xffffffffu, valid && (from > 0 || hi < (j + 1) * kKt))) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (span <= 0 || static_cast<uint32_t>(h * 64 + c - from) >= static_cast<uint32_t>(span)) x[h][c] = 0xff800000u;
-          }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < 64; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(x[h][c]));
-          const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          asm volatile("" : "+f"(top[0]), "+f"(top[1]), "+f"(top[2]), "+f"(top[3]));
+          const float tile_top = max3(fmaxf(top[0], top[1]), top[2], top[3]);
           // The maximum is only a guard against overflow: any m gives the same
           // quotient.  It moves when it would lag by more than 2^8, so that O
           // in TMEM is rescaled a few times a row and not in every tile; the
           // weights then stay below 2^8, within both 16-bit types.  O is at
           // rest here: S_t(j) was issued behind the last P_t V.
           const bool lags = valid && (tile_top - m) * sc > kSlack;  // (also from -inf; NaN: no)
-          if (j == un.t_begin) {
+          if (j == j0) {
             m = tile_top;
           } else if (__any_sync(0xffffffffu, lags)) {
             const float now = lags ? tile_top : m;
             const float f = lags ? exp2_fast((m - now) * sc) : 1.0f;
             m = now;
             l *= f;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kDp; c += 32) {
               uint32_t y[32];
               tmem_ld_32x32b_x32(to + c, y);
@@ -411,92 +496,166 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_32x32b_x32(to + c, y);
             }
           }
-          const float off = m == -INFINITY ? 0.0f : m * sc;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          const float off = m == -INFINITY ? 0.0f : -m * sc;
+          const uint64_t sc2 = pair_of(sc, sc), off2 = pair_of(off, off);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t p[32];
+            // Eight at a time, the exponentials of one group beside the sums and
+            // conversions of the one before: exp2 keeps its unit busy for 4
+            // clocks a warp, the packed FMA, the add and the conversion two each.
+            float e[2][8];
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-              const float e0 = exp2_fast(fmaf(__uint_as_float(x[h][c]), sc, -off));
-              const float e1 = exp2_fast(fmaf(__uint_as_float(x[h][c + 1]), sc, -off));
-              sum[c & 2] += e0;
-              sum[(c & 2) + 1] += e1;
-              p[c / 2] = pack(e0, e1, T());  // one rounding, to the type of V: the UMMA's operands have one type
-            }
+            for (int g = 0; g <= 8; ++g)
+#pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                float *now = e[g & 1] + i, *old = e[(g & 1) ^ 1] + i;
+                if (g < 8) {
+                  const int c = 8 * g + i;
+                  parts_of(fma2(pair_of(__uint_as_float(x[h][c]), __uint_as_float(x[h][c + 1])), sc2, off2), now[0], now[1]);
+                  now[0] = exp2_fast(now[0]);
+                }
+                if (g > 0) sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pair_of(old[0], old[1]));
+                if (g < 8) now[1] = exp2_fast(now[1]);
+                if (g > 0) p[4 * (g - 1) + i / 2] = pack(old[0], old[1], T());  // one rounding, to the type of V: the UMMA's operands have one type
+              }
             tmem_st_32x32b_x32(ts + 32 * h, p);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(t, h));
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_wait_st();
+          float s0, s1;
+          parts_of(add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+        } else if (lane == 0) {
+          mbar_arrive(p_full(t, 0));
+          mbar_arrive(p_full(t, 1));
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(t));
       }
       if (!ok) break;
-      // ---- the row's result
-      const int head = un.head * a.rep + row - tok * a.rep;
-      const int64_t at = static_cast<int64_t>(un.q0 + tok) * a.hq + head;
-      const bool none = un.t_begin == un.t_end;
-      if (!none) {
-        ok = wait(o_full(t), no & 1);
+      // ---- the rows' results: of lane t, or of both lanes by lane 0's warps
+      const bool both = !two && tiles > 1;
+      if (!two && t == 1) {
+        if (both) {
+          ++no[0];
+          ++no[1];
+          ok = wait(stats_empty, (nx++ & 1) ^ 1);
+          if (!ok) break;
+          stats[r] = make_float2(m, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(stats_full);
+        } else if (tiles) {
+          ++no[0];
+        }
+        continue;
+      }
+      float f0 = 1.0f, f1 = 0.0f;
+      if (tiles) {
+        ok = wait(o_full(t), no[t] & 1);
+        if (ok && both) ok = wait(o_full(1), no[1] & 1) && wait(stats_full, nx++ & 1);
         if (!ok) break;
-        ++no;
         tc_fence_after();
+        ++no[0];
+        if (two || both) ++no[1];
+        if (both) {
+          const float2 x = stats[r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(stats_empty);
+          const float top = fmaxf(m, x.x), off = top == -INFINITY ? 0.0f : top;
+          f0 = exp2_fast((m - off) * sc);
+          f1 = exp2_fast((x.x - off) * sc);
+          m = top;
+          l = l * f0 + x.y * f1;
+        }
       }
       const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // (NaN stays)
+      f0 *= inv;
+      f1 *= inv;
+      const int head = un.head * a.rep + row - tok * a.rep;
+      const int64_t at = static_cast<int64_t>(un.q0 + tok) * a.hq + head;
       if (some) {
-        const bool split = un.pieces > 1;
-        float *po = a.part_o + (un.piece * a.ntok * a.hq + at) * a.d;
+        const bool cut = un.slot >= 0;
+        float4 *po = a.part_o + static_cast<int64_t>(un.slot) * (a.d / 4) * (2 * half_rows) + (row - un.row0);
         const int64_t oat = (un.q0 + tok) * a.out_token + head * a.out_head;
-#pragma unroll
+#pragma unroll 1  // (small code: a short call runs it once, from a cold instruction cache)
         for (int c = 0; c < kDp; c += 32) {
           uint32_t y[32];
-          if (none) {
+          if (tiles == 0) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) y[i] = 0;
           } else {
             tmem_ld_32x32b_x32(to + c, y);
             tmem_wait_ld(y);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f0);
+            if (both) {
+              uint32_t z[32];
+              tmem_ld_32x32b_x32(to1 + c, z);
+              tmem_wait_ld(z);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(fmaf(__uint_as_float(z[i]), f1, __uint_as_float(y[i])));
+            }
           }
-          if (!valid) continue;
-          // a row without a key in these tiles has P = 0 throughout
+          if (cut) {
+            if (valid) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(l == 0.0f ? 0.0f : __uint_as_float(y[i]) * inv);
-          if (split || a.out_type == MMQ_DT_F32) {
-            float *dst = split ? po : static_cast<float *>(a.out) + oat;
+              for (int i = 0; i < 32; i += 4)
+                if (c + i < a.d)
+                  po[((c + i) / 4) * (2 * half_rows)] = make_float4(__uint_as_float(y[i]), __uint_as_float(y[i + 1]),
+                                                                    __uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
+            }
+          } else if (a.out_type == MMQ_DT_F32) {
+            float *dst = static_cast<float *>(a.out) + oat;
+            if (valid) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              if (c + i < a.d) *reinterpret_cast<uint4 *>(dst + c + i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+              for (int i = 0; i < 32; i += 4)
+                if (c + i < a.d) *reinterpret_cast<uint4 *>(dst + c + i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            }
           } else {
-            T *dst = static_cast<T *>(a.out) + oat;
+            // Four lanes swap their 16-byte chunks, so that they write 64
+            // bytes of one row together: a store that goes to 32 rows takes
+            // the memory pipe 32 clocks, one that goes to eight rows 8.
+            uint32_t z[4][4];  // chunk, word
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              if (c + i >= a.d) continue;
-              uint4 z;
-              z.x = pack(__uint_as_float(y[i]), __uint_as_float(y[i + 1]), T());
-              z.y = pack(__uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]), T());
-              z.z = pack(__uint_as_float(y[i + 4]), __uint_as_float(y[i + 5]), T());
-              z.w = pack(__uint_as_float(y[i + 6]), __uint_as_float(y[i + 7]), T());
-              *reinterpret_cast<uint4 *>(dst + c + i) = z;
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) z[i][k] = pack(__uint_as_float(y[8 * i + 2 * k]), __uint_as_float(y[8 * i + 2 * k + 1]), T());
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (!(i & d))
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const bool up = lane & d;
+                    const uint32_t give = up ? z[i][k] : z[i | d][k], got = __shfl_xor_sync(0xffffffffu, give, d);
+                    (up ? z[i][k] : z[i | d][k]) = got;
+                  }
+            // z[i] is now chunk lane & 3 of the row of lane (lane & ~3) + i
+            const int col = c + 8 * (lane & 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int64_t to_row = __shfl_sync(0xffffffffu, valid ? oat : -1, (lane & ~3) + i);
+              if (to_row >= 0 && col < a.d)
+                *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + to_row + col) = make_uint4(z[i][0], z[i][1], z[i][2], z[i][3]);
             }
           }
         }
         if (valid) {
           const float lse2 = l > 0.0f ? fmaf(m, sc, log2f(l)) : l == 0.0f ? -INFINITY : l;
-          if (split) {
-            a.part_lse[un.piece * a.ntok * a.hq + at] = lse2;
-            if (un.piece == 0) a.part_n[at] = un.pieces;
-          } else {
-            if (a.lse) a.lse[at] = lse2 * kLn2;
-            if (a.max_pieces > 1) a.part_n[at] = 1;
-          }
+          if (cut) a.part_lse[un.slot * (2 * half_rows) + row - un.row0] = lse2;
+          else if (a.lse) a.lse[at] = lse2 * kLn2;
         }
       }
-      if (!none) {
+      if (tiles) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(o_empty(t));
+        if (lane == 0) {
+          mbar_arrive(o_empty(t));
+          if (both) mbar_arrive(o_empty(1));
+        }
       }
     }
   }
@@ -541,7 +700,7 @@ bool encode(CUtensorMap *m, int type, const void *p, int64_t d, const int64_t (&
 }
 
 template <class T, int kDp>
-cudaError_t launch_umma(const AttnArgs &a, const Maps &maps, int tile_tok, int box, int dev, unsigned grid, cudaStream_t s) {
+cudaError_t launch_umma(const AttnArgs &a, const AttnUmma &u, int dev, unsigned grid, cudaStream_t s) {
   constexpr auto kern = attention_umma_kernel<T, kDp>;
   static std::atomic<int> ready[64];  // 0 unknown, 1 ready, 2 unusable
   int st = ready[dev].load();
@@ -554,33 +713,28 @@ cudaError_t launch_umma(const AttnArgs &a, const Maps &maps, int tile_tok, int b
     ready[dev].store(st);
   }
   if (st != 1) return cudaErrorInvalidKernelImage;
-  attention_umma_kernel<T, kDp><<<grid, kThreads, Lay<kDp>::kBytes, s>>>(a, maps, tile_tok, box);
+  attention_umma_kernel<T, kDp><<<grid, kThreads, Lay<kDp>::kBytes, s>>>(a, u);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// The tile shape of the tcgen05 kernel for this problem; false: it does not
-// take it.  Pages are copied in boxes of gcd(page_size, 128) keys, at least
-// eight, so that a box is whole swizzle groups and a warp's lanes cover a tile.
-bool attention_umma_shape(const mmq_paged_cache &c, const mmq_attention &t, int *tile_tok, int *box) {
-  const int rep = t.q_heads / c.heads;
-  *box = std::gcd(c.page_size, kKt);
-  *tile_tok = rep <= 128 ? 128 / rep : 0;
-  return c.head_dim <= 128 && rep <= 128 && *box >= 8 && encoder();
+// The tcgen05 kernel takes head widths and groups of query heads up to 128.
+// Pages are copied in boxes of gcd(page_size, 128) keys, at least eight, so
+// that a box is whole swizzle groups and a warp's lanes cover a tile.
+bool attention_umma(const AttnArgs &a, int type, AttnUmma *u) {
+  if (a.d > 128 || a.rep > 128) return false;
+  u->tile_tok = 128 / a.rep;
+  u->box = std::gcd(a.page_size, kKt);
+  return u->box >= 8 && encoder() &&
+         encode(&u->q, type, a.q, a.d, {a.rep, a.hkv, a.ntok}, {a.q_head, a.rep * a.q_head, a.q_token}, a.rep, u->tile_tok) &&
+         encode(&u->k, type, a.k, a.d, {a.page_size, a.hkv, a.pages}, {a.k_token, a.k_head, a.k_page}, u->box, 1) &&
+         encode(&u->v, type, a.v, a.d, {a.page_size, a.hkv, a.pages}, {a.v_token, a.v_head, a.v_page}, u->box, 1);
 }
 
-cudaError_t launch_attention_umma(const AttnArgs &a, const mmq_paged_cache &c, int tile_tok, int box, int dev, unsigned grid,
-                                  cudaStream_t s, bool *taken) {
-  Maps m;
-  *taken = encode(&m.q, c.type, a.q, a.d, {a.rep, a.hkv, a.ntok}, {a.q_head, a.rep * a.q_head, a.q_token}, a.rep, tile_tok) &&
-           encode(&m.k, c.type, a.k, a.d, {c.page_size, a.hkv, a.pages}, {a.k_token, a.k_head, a.k_page}, box, 1) &&
-           encode(&m.v, c.type, a.v, a.d, {c.page_size, a.hkv, a.pages}, {a.v_token, a.v_head, a.v_page}, box, 1);
-  if (!*taken) return cudaSuccess;
-  if (c.type == MMQ_DT_F16)
-    return a.d <= 64 ? launch_umma<__half, 64>(a, m, tile_tok, box, dev, grid, s) : launch_umma<__half, 128>(a, m, tile_tok, box, dev, grid, s);
-  return a.d <= 64 ? launch_umma<__nv_bfloat16, 64>(a, m, tile_tok, box, dev, grid, s)
-                   : launch_umma<__nv_bfloat16, 128>(a, m, tile_tok, box, dev, grid, s);
+cudaError_t launch_attention_umma(const AttnArgs &a, const AttnUmma &u, int type, int dev, unsigned grid, cudaStream_t s) {
+  if (type == MMQ_DT_F16) return a.d <= 64 ? launch_umma<__half, 64>(a, u, dev, grid, s) : launch_umma<__half, 128>(a, u, dev, grid, s);
+  return a.d <= 64 ? launch_umma<__nv_bfloat16, 64>(a, u, dev, grid, s) : launch_umma<__nv_bfloat16, 128>(a, u, dev, grid, s);
 }
 
 }  // namespace mmq

@@ -12,7 +12,7 @@ bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 int cuda_rc(cudaError_t e) {
   if (e == cudaSuccess) return MMQ_OK;
   cudaGetLastError();
-  return e == cudaErrorMemoryAllocation ? MMQ_ERR_OOM : MMQ_ERR_CUDA;
+  return e == cudaErrorMemoryAllocation ? MMQ_ERR_OOM : e == cudaErrorNotSupported ? MMQ_ERR_UNSUPPORTED : MMQ_ERR_CUDA;
 }
 constexpr int64_t kInt32 = 0x7fffffff;
 
