@@ -1,11 +1,14 @@
 """Builds libmmq.so in-tree: every .cu under csrc/ compiled for sm_103a only,
-in parallel, then linked into one shared library next to this file."""
+in parallel, then linked into one shared library next to this file; and
+_serving.so, the Python binding of the serving step (csrc/binding.cpp against
+torch's headers)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -13,6 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmmq.so")
+BINDING = os.path.join(PKG, "_serving.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -36,10 +40,25 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    def newer(target, deps):
+        return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
+    return newer(LIB, _deps()) and newer(BINDING, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "mmq.h")])
+
+
+def _build_binding():
+    import torch
+    home = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}", "-isystem", home, "-isystem",
+           os.path.join(home, "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+           "-I" + sysconfig.get_paths()["include"], f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -57,8 +76,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, len(_sources()))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(_sources()) + 1) as ex:
+        binding = ex.submit(_build_binding)
         results = list(ex.map(compile_one, _sources()))
+        binding.result()
     if verbose:
         for obj, log in results:
             print(f"== {os.path.basename(obj)}\n{log}")

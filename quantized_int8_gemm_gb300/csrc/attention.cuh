@@ -200,9 +200,9 @@ struct AttnSchedule {
     total = __reduce_add_sync(0xffffffffu, total);
     longest = __reduce_max_sync(0xffffffffu, longest);
     each = max(a.by_grid(total + static_cast<int>(gridDim.x) - 1), kLeast);
-    // Whole units where the longest is short beside a stretch: a piece costs
-    // its partial result and the join.
-    split = a.part_o && longest > kGap + kLeast && longest * 16 > each;
+    // Whole units cost half the longest in balance, pieces their partial
+    // results and the join (about four tiles' time).
+    split = a.part_o && max(longest, each + longest / 2) > each + 4;
     lo = each * static_cast<int>(blockIdx.x);
     hi = lo + each;
     pos = 0;

@@ -4,7 +4,7 @@
 // A unit (attention.cuh) is up to 256 rows of one K/V head, as two tiles of
 // 128, over tiles of 128 keys.  There are two lanes t of
 //   S_t = Q K_j^T   (TMEM, fp32)                            UMMA warp t
-//   P_t = exp2(scale S_t - m), 16 bits, over S_t's columns  softmax warps of t
+//   P_t = exp2(scale S_t - m), 16 bits, into TMEM           softmax warps of t
 //   O_t += P_t V_j  (TMEM, fp32; P read from TMEM)          UMMA warp t
 // and while the softmax warps of one lane work, the tensor core runs the other
 // lane's products.  With two row tiles lane t is row tile t and sees every key
@@ -36,12 +36,16 @@ constexpr float kSlack = 8.0f;  // the running maximum may lag by 2^8 (see the s
 template <int kDp>
 struct Lay {
   static constexpr int kHalves = kDp / 64;
+  // TMEM columns.  S_0, S_1; for heads of 64 there is room for P beside S, so
+  // that Q K^T of the next key tile runs while the softmax of this one does.
+  static constexpr bool kApart = kDp == 64;
+  static constexpr int kO = 256, kP = kApart ? 256 + 2 * kDp : 0, kPStep = kApart ? 64 : 128;
   static constexpr int kTile = kHalves * 16384;
   static constexpr int kStages = kDp == 64 ? 10 : 5;
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTile;
   static constexpr int kBars = kRing + kStages * kTile;
-  static constexpr int kNumBars = 3 * kStages + 2 + 14 + 2 * kUnits + 1;
+  static constexpr int kNumBars = 3 * kStages + 2 + 18 + 2 * kUnits + 1;
   static constexpr int kStats = kBars + kNumBars * 8;  // lane 1's maximum and sum of each row
   static constexpr int kUnitsAt = kStats + 128 * 8;
   static constexpr int kSlot = kUnitsAt + kUnits * static_cast<int>(sizeof(AttnUnit));
@@ -145,8 +149,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto o_empty = [&](int t) { return bars + 8u * (kFix + 10 + t); };
   const uint32_t stats_full = bars + 8u * (kFix + 12), stats_empty = bars + 8u * (kFix + 13);
   auto turn = [&](int t) { return bars + 8u * (kFix + 14 + t); };
-  auto u_full = [&](int i) { return bars + 8u * (kFix + 16 + i); };
-  auto u_empty = [&](int i) { return bars + 8u * (kFix + 16 + kUnits + i); };
+  auto s_empty = [&](int t) { return bars + 8u * (kFix + 16 + t); };
+  auto p_empty = [&](int t) { return bars + 8u * (kFix + 18 + t); };
+  auto u_full = [&](int i) { return bars + 8u * (kFix + 20 + i); };
+  auto u_empty = [&](int i) { return bars + 8u * (kFix + 20 + kUnits + i); };
   const uint32_t done = bars + 8u * (L::kNumBars - 1);
   AttnUnit *units = reinterpret_cast<AttnUnit *>(smem + L::kUnitsAt);
   const WaitCtl &w = a.wait;
@@ -169,6 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(o_full(t), 1);
       mbar_init(o_empty(t), 4);
       mbar_init(turn(t), 1);
+      mbar_init(s_empty(t), 4);
+      mbar_init(p_empty(t), 1);
     }
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(u_full(i), 1);
@@ -210,7 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     return un.n > 0;
   };
   auto two_tiles = [&](const AttnUnit &un) { return un.row0 + half_rows < un.n * a.rep; };
-  // TMEM columns: S_t (and P_t over it) at 128 t, O_t at 256 + 128 t
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
@@ -325,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_qk = idesc_f16_f32(128, kKt) | kFormat<T>;
       constexpr uint32_t id_pv = idesc_f16_f32(128, kDp) | kFormat<T> | kBNMajor;
       const uint64_t kd0 = sdesc_kmajor_sw128(base + L::kRing), vd0 = sdesc_nmajor_sw128(base + L::kRing);
-      const uint32_t d_s = tmem + 128 * t, d_o = tmem + 256 + 128 * t;
-      uint32_t ks = 0, nu = 0, nq = 0, np = 0, no = 0, nt = 0;
+      const uint32_t d_s = tmem + 128 * t, d_o = tmem + L::kO + kDp * t, d_p = tmem + L::kP + L::kPStep * t;
+      uint32_t ks = 0, nu = 0, nq = 0, np = 0, no = 0, nt = 0, ns = 0;
       bool ok = true;
       auto stage = [&](uint32_t k) { return static_cast<int>(k % L::kStages); };
       auto landed = [&](uint32_t k) { return wait(kv_full(stage(k)), (k / L::kStages) & 1); };
@@ -343,10 +350,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // other's UMMAs; left alone they fall into step and the tensor pipe idles
       // while both wait for their weights (3.9 against 3.0 thousand clocks a
       // key tile).
-      auto my_turn = [&](bool two) { return !two || wait(turn(t), (nt++ & 1) ^ (t == 0)); };
+      auto my_turn = [&](bool two) { return L::kApart || !two || wait(turn(t), (nt++ & 1) ^ (t == 0)); };
       // S_t = Q K^T from load k
       auto qk = [&](uint64_t qd, uint32_t k, bool two, bool known) {
-        const bool got = known || landed(k);
+        bool got = known || landed(k);
+        if (L::kApart && got) got = wait(s_empty(t), (ns++ & 1) ^ 1);
         if (got) {
           tc_fence_after();
           if (elected) {
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t at = (i >> 2) * (16384 >> 4) + (i & 3) * 2;
               umma_f16(d_s, qd + at, kd + at, id_qk, i > 0);
             }
-            if (two) mbar_arrive(turn(t ^ 1));
+            if (!L::kApart && two) mbar_arrive(turn(t ^ 1));
             umma_commit(s_full(t));
             umma_commit(kv_empty(stage(k)));
           }
@@ -367,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // O_t (+)= P_t V from load k; the first 64 keys' weights may be there before the rest
       auto pv = [&](uint32_t k, int steps, bool fresh, bool two, bool last) {
         bool got = landed(k);
-        if (got && two && !last) got = landed(k + 1);  // (the next key tile's K, so that the turn does not wait for it)
+        if (!L::kApart && got && two && !last) got = landed(k + 1);  // (the next key tile's K, so that the turn does not wait for it)
         if (got && fresh) got = wait(o_empty(t), (no++ & 1) ^ 1);
         const uint64_t vd = vd0 + stage(k) * (L::kTile >> 4);
         const uint32_t parity = np++ & 1;
@@ -380,10 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elected) {
 #pragma unroll
             for (int i = 4 * half; i < 4 * half + 4; ++i)
-              if (i < steps) umma_ts(d_o, d_s + 8 * i, vd + i * (2048 >> 4), id_pv, !(fresh && i == 0));
+              if (i < steps) umma_ts(d_o, d_p + 8 * i, vd + i * (2048 >> 4), id_pv, !(fresh && i == 0));
             if (half) {
-              if (two && last) mbar_arrive(turn(t ^ 1));
+              if (!L::kApart && two && last) mbar_arrive(turn(t ^ 1));
               umma_commit(kv_empty(stage(k)));
+              if (L::kApart) umma_commit(p_empty(t));
             }
           }
           __syncwarp();
@@ -398,26 +407,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const uint64_t qd = sdesc_kmajor_sw128(base + L::kQ + (two ? t : 0) * L::kTile);
         const int first = two ? 0 : t, dj = two ? 1 : 2;  // this lane's key tiles
-        if (first >= tiles && lane == 0) mbar_arrive(q_empty);
-        for (int j = 0; j < tiles && ok; ++j, ks += 2) {  // loads: K of tile j, then its V
-          if (!two && (j & 1) != t) {
-            ok = skip(ks) && skip(ks + 1);
-            continue;
-          }
-          const bool last = j + dj >= tiles;
-          if (j == first) ok = my_turn(two);
-          ok = ok && qk(qd, ks, two, two && j != first);
-          if (ok && last) {
+        const uint32_t end = ks + 2 * tiles;              // loads: K of tile j at ks + 2j, then its V
+        // the other lane's tile before key tile j, if it has one there
+        auto pass = [&](int j) { return two || j < 1 || (skip(ks + 2 * j - 2) && skip(ks + 2 * j - 1)); };
+        auto qk_of = [&](int j) {
+          ok = pass(j) && qk(qd, ks + 2 * j, two, !L::kApart && two && j != first);
+          if (ok && j + dj >= tiles) {  // the lane's last
             if (elected) umma_commit(q_empty);
             __syncwarp();
           }
-          ok = ok && pv(ks + 1, (min(kKt, un.len - (un.t_begin + j) * kKt) + 15) >> 4, j == first, two, last);
+        };
+        if (first < tiles) {
+          ok = my_turn(two);
+          if (ok) qk_of(first);
+        } else if (lane == 0) {
+          mbar_arrive(q_empty);
+        }
+        for (int j = first; j < tiles && ok; j += dj) {
+          const bool last = j + dj >= tiles;
+          if (L::kApart && !last) qk_of(j + dj);
+          ok = ok && pv(ks + 2 * j + 1, (min(kKt, un.len - (un.t_begin + j) * kKt) + 15) >> 4, j == first, two, last);
+          if (!L::kApart && ok && !last) qk_of(j + dj);
           if (ok && last) {
             if (elected) umma_commit(o_full(t));
             __syncwarp();
           }
         }
+        if (ok && !two && ((tiles - 1) & 1) != t) ok = skip(end - 2) && skip(end - 1);
         if (!ok) break;
+        ks = end;
       }
       if (elected) umma_commit(done);
       __syncwarp();
@@ -428,7 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ softmax: one row a thread
     const int t = warp >> 2, quad = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t, to1 = tmem + lanes + 384;
+    const uint32_t ts = tmem + lanes + 128 * t, tp = tmem + lanes + L::kP + L::kPStep * t;
+    const uint32_t to = tmem + lanes + L::kO + kDp * t, to1 = tmem + lanes + L::kO + kDp;
     const float sc = a.scale_log2;
     uint32_t nu = 0, ns = 0, no[2] = {0, 0}, nx = 0;
     bool ok = true;
@@ -454,10 +473,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__any_sync(0xffffffffu, valid && (from > 0 || to_key < kKt))) {
 #pragma unroll 1
             for (int c = 0; c < kKt; c += 32) {
+              const int y0 = from - c, y1 = to_key - c;
+              if (!__any_sync(0xffffffffu, valid && (y0 > 0 || y1 < 32))) continue;
               uint32_t y[32];
               tmem_ld_32x32b_x32(ts + c, y);
               tmem_wait_ld(y);
-              const int y0 = from - c, y1 = to_key - c;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (i < y0 || i >= y1) y[i] = 0xff800000u;
@@ -472,12 +492,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld(x[0]);
           tmem_wait_ld(x[1]);
           asm volatile("" : "+f"(top[0]), "+f"(top[1]), "+f"(top[2]), "+f"(top[3]));
+          if (L::kApart) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_empty(t));
+            ok = wait(p_empty(t), (ns & 1));  // P_t V of the tile before (ns counts this tile already)
+            if (!ok) break;
+            tc_fence_after();
+          }
           const float tile_top = max3(fmaxf(top[0], top[1]), top[2], top[3]);
           // The maximum is only a guard against overflow: any m gives the same
           // quotient.  It moves when it would lag by more than 2^8, so that O
           // in TMEM is rescaled a few times a row and not in every tile; the
           // weights then stay below 2^8, within both 16-bit types.  O is at
-          // rest here: S_t(j) was issued behind the last P_t V.
+          // rest here: P_t V of the tile before is done (where P lies over S,
+          // S_t(j) was issued behind it).
           const bool lags = valid && (tile_top - m) * sc > kSlack;  // (also from -inf; NaN: no)
           if (j == j0) {
             m = tile_top;
@@ -520,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (g < 8) now[1] = exp2_fast(now[1]);
                 if (g > 0) p[4 * (g - 1) + i / 2] = pack(old[0], old[1], T());  // one rounding, to the type of V: the UMMA's operands have one type
               }
-            tmem_st_32x32b_x32(ts + 32 * h, p);
+            tmem_st_32x32b_x32(tp + 32 * h, p);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -529,9 +558,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           float s0, s1;
           parts_of(add2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
-        } else if (lane == 0) {
-          mbar_arrive(p_full(t, 0));
-          mbar_arrive(p_full(t, 1));
+        } else {
+          if (L::kApart) {
+            if (lane == 0) mbar_arrive(s_empty(t));
+            ok = wait(p_empty(t), (ns & 1));
+            if (!ok) break;
+          }
+          if (lane == 0) {
+            mbar_arrive(p_full(t, 0));
+            mbar_arrive(p_full(t, 1));
+          }
         }
       }
       if (!ok) break;

@@ -16,14 +16,14 @@
 namespace mmq {
 namespace {
 
-constexpr int kVerThreads = 512;
+constexpr int kVerThreads = 256;
 constexpr int kVerCtas = 8;  // CTAs (one cluster) of a request
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// The better of two candidates is the larger number: the weight's bits above,
+// The better of two candidates is the larger number: the key's bits above,
 // the complement of the index below (so that ties go to the lowest index).
 // 0: no candidate.
 __device__ __forceinline__ void consider(uint64_t &best, float w, float e, int64_t v) {
@@ -34,6 +34,12 @@ __device__ __forceinline__ void consider(uint64_t &best, float w, float e, int64
 }
 
 // This CTA's part of one row.  kLeft: weights (p - q)+, else p.
+//
+// Few entries are worth an IEEE division: with a the product of w and the
+// approximate reciprocal (off by less than 2^-21), an entry whose a is below
+// (1 - 2^-19) of the warp's largest so far cannot win.  So a warp takes the
+// largest a of a batch first and divides where a lane is near it; entries
+// whose reciprocal leaves the normal range are always divided.
 template <class T, bool kLeft>
 __device__ __forceinline__ uint64_t race(const T *__restrict__ p, const T *__restrict__ q, const float *__restrict__ e,
                                          int64_t n, bool wide, uint32_t rank) {
@@ -41,23 +47,59 @@ __device__ __forceinline__ uint64_t race(const T *__restrict__ p, const T *__res
   const int64_t step = static_cast<int64_t>(kVerCtas) * kVerThreads;
   const int64_t me = static_cast<int64_t>(rank) * kVerThreads + threadIdx.x;
   int64_t done = 0;
-  if (wide) {  // rows on 16-byte boundaries: four elements a step
+  if (wide) {  // rows on 16-byte boundaries: four elements a load, kBatch loads a step
+    constexpr int kBatch = 4;
     const int64_t groups = n >> 2;
-#pragma unroll 4
-    for (int64_t i = me; i < groups; i += step) {
-      const float4 ev = __ldcs(reinterpret_cast<const float4 *>(e) + i);
-      T pv[4], qv[4];
-      if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<uint4 *>(pv) = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-        if (kLeft) *reinterpret_cast<uint4 *>(qv) = __ldcs(reinterpret_cast<const uint4 *>(q) + i);
-      } else {
-        *reinterpret_cast<uint2 *>(pv) = __ldcs(reinterpret_cast<const uint2 *>(p) + i);
-        if (kLeft) *reinterpret_cast<uint2 *>(qv) = __ldcs(reinterpret_cast<const uint2 *>(q) + i);
-      }
-      const float en[4] = {ev.x, ev.y, ev.z, ev.w};
+    float highest = 0.0f;
+    for (int64_t i0 = me - (threadIdx.x & 31); i0 < groups; i0 += kBatch * step) {  // (the warp as one)
+      float w[kBatch][4], ev[kBatch][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        consider(best, kLeft ? to_f32(pv[k]) - to_f32(qv[k]) : to_f32(pv[k]), en[k], 4 * i + k);
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t i = i0 + (threadIdx.x & 31) + u * step;
+        T pv[4], qv[4];
+        if (i < groups) {
+          *reinterpret_cast<float4 *>(ev[u]) = __ldcs(reinterpret_cast<const float4 *>(e) + i);
+          if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<uint4 *>(pv) = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+            if (kLeft) *reinterpret_cast<uint4 *>(qv) = __ldcs(reinterpret_cast<const uint4 *>(q) + i);
+          } else {
+            *reinterpret_cast<uint2 *>(pv) = __ldcs(reinterpret_cast<const uint2 *>(p) + i);
+            if (kLeft) *reinterpret_cast<uint2 *>(qv) = __ldcs(reinterpret_cast<const uint2 *>(q) + i);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[u][k] = kLeft ? to_f32(pv[k]) - to_f32(qv[k]) : to_f32(pv[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[u][k] = 0.0f, ev[u][k] = 1.0f;
+        }
+      }
+      // 0: no weight; negative: to be divided in any case
+      auto near_key = [](float wt, float x) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+        return !(wt > 0.0f) ? 0.0f : x >= 0x1p-125f && x <= 0x1p125f ? wt * r : -1.0f;
+      };
+      float top = 0.0f, low = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x = near_key(w[u][k], ev[u][k]);
+          top = fmaxf(top, x);
+          low = fminf(low, x);
+        }
+      highest = fmaxf(highest, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
+      const float floor = highest > 1e-30f ? highest * (1.0f - 0x1p-19f) : 0.0f;
+      if (low < 0.0f || (top >= floor && top > 0.0f)) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x = near_key(w[u][k], ev[u][k]);
+            if (x < 0.0f || (x > 0.0f && x >= floor))
+              consider(best, w[u][k], ev[u][k], 4 * (i0 + (threadIdx.x & 31) + u * step) + k);
+          }
+      }
     }
     done = groups << 2;
   }
@@ -96,7 +138,7 @@ __device__ __forceinline__ uint64_t cluster_best(uint64_t mine, uint64_t *own, u
 // over them and joined through their shared memory, one launch, no scratch.
 // HBM bound: one row each of p, q and e (12 B an entry in fp32).
 template <class T>
-__global__ void __launch_bounds__(kVerThreads) __cluster_dims__(kVerCtas, 1, 1)
+__global__ void __launch_bounds__(kVerThreads, 4) __cluster_dims__(kVerCtas, 1, 1)
     verify_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ uint64_t own[kVerThreads / 32], all[2][kVerCtas];
   __shared__ int s_kept;

@@ -102,12 +102,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.mmq_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
         L.mmq_probe_engine_rates.argtypes = [vp, vp]
         L.mmq_strerror.argtypes = [i32]
-        # (structs go as the bytes serving.py packs)
-        cp = ctypes.c_char_p
+        # (the serving step is called through csrc/binding.cpp)
         L.mmq_page_tables.argtypes = [vp, vp, vp, i64, vp, i64, i64, vp, i64, i32, i64, vp, vp, vp, vp, vp, vp, vp]
-        L.mmq_kv_write.argtypes = [cp, vp, i64, i64, vp, i64, i64, i32, vp, i64, vp]
-        L.mmq_paged_attention.argtypes = [cp, cp, vp]
-        L.mmq_verify_draft.argtypes = [cp, vp]
+        L.mmq_kv_write.argtypes = [vp, vp, i64, i64, vp, i64, i64, i32, vp, i64, vp]
+        L.mmq_paged_attention.argtypes = [vp, vp, vp]
+        L.mmq_verify_draft.argtypes = [vp, vp]
         L.mmq_strerror.restype = ctypes.c_char_p
         for n in EXPORTS:
             f = getattr(L, n)
