@@ -91,6 +91,8 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
   const uint32_t sq = smem_addr(smem), sk = sq + kRows * kDp * 2, sv = sk + 2 * kTile;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   AttnSchedule<kKt, kRows> sched;
+  griddep_wait();
+  griddep_launch_dependents();
   if (warp == 0) sched.plan(a);
 
   for (;;) {
@@ -266,6 +268,7 @@ template <class T>
 __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a, int unit_rows) {
   __shared__ float s_top[kJoinRows], s_inv[kJoinRows];
   griddep_wait();
+  griddep_launch_dependents();
   const AttnCut u = a.cuts[blockIdx.x];
   const int r0 = blockIdx.y * kJoinRows, rows = min(min(unit_rows, u.n * a.rep - u.row0) - r0, kJoinRows);
   if (u.last < 0 || rows <= 0) return;
@@ -344,8 +347,7 @@ cudaError_t launch_rows(const AttnArgs &a, int dev, unsigned grid, cudaStream_t 
   constexpr int smem = (kRows + 4 * kKt) * kDp * 2;
   const cudaError_t e = allow_smem<attention_rows_kernel<T, kDp>>(dev, smem);
   if (e != cudaSuccess) return e;
-  attention_rows_kernel<T, kDp><<<grid, kThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(attention_rows_kernel<T, kDp>, grid, 1, kThreads, smem, s, a);
 }
 template <class T>
 cudaError_t launch_rows_of(const AttnArgs &a, int dev, unsigned grid, cudaStream_t s) {
@@ -356,18 +358,9 @@ cudaError_t launch_rows_of(const AttnArgs &a, int dev, unsigned grid, cudaStream
 
 template <class T>
 cudaError_t launch_join(const AttnArgs &a, int unit_rows, unsigned grid, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
   // (no unit has more rows than all tokens together)
   const int64_t most = std::min<int64_t>(unit_rows, a.ntok * a.rep);
-  cfg.gridDim = dim3(grid, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<T>, a, unit_rows);
+  return launch_early(attention_join_kernel<T>, grid, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows), 256, 0, s, a, unit_rows);
 }
 
 }  // namespace

@@ -201,8 +201,9 @@ struct AttnSchedule {
     longest = __reduce_max_sync(0xffffffffu, longest);
     each = max(a.by_grid(total + static_cast<int>(gridDim.x) - 1), kLeast);
     // Whole units cost half the longest in balance, pieces their partial
-    // results and the join (about four tiles' time).
-    split = a.part_o && max(longest, each + longest / 2) > each + 4;
+    // results and the join (about four tiles' time, eight with two row tiles).
+    const int join = __any_sync(0xffffffffu, r.n > a.unit_tok / 2) ? 8 : 4;
+    split = a.part_o && max(longest, each + longest / 2) > each + join;
     lo = each * static_cast<int>(blockIdx.x);
     hi = lo + each;
     pos = 0;

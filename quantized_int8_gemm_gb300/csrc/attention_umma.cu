@@ -59,6 +59,15 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, 
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
+// (no branch: the warp stays together)
+__device__ __forceinline__ void mbar_arrive_if(bool yes, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"(static_cast<uint32_t>(yes))
+      : "memory");
+}
 // D[tmem] (+)= A[tmem] . B[smem], 16-bit A packed two to a column
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -123,6 +132,22 @@ __device__ __forceinline__ void tmem_ld_max_x32(uint32_t taddr, uint32_t *r, flo
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -191,19 +216,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const CUtensorMap *m = lane == 0 ? &um.q : lane == 1 ? &um.k : &um.v;
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
   }
-  griddep_launch_dependents();  // the join's CTAs come as these leave
   if (warp == kUmmaWarp) {
     tmem_alloc(base + L::kSlot, 512);
     tmem_relinquish();
   }
   AttnSchedule<kKt, 0> sched;
   AttnUnit un;
+  griddep_wait();
   if (warp == kLoadWarp) {  // its first unit, while the others set up
     sched.plan(a);
     if (!sched.next(a, un)) un.n = 0;
   }
   tc_fence_before();
   __syncthreads();
+  griddep_launch_dependents();  // the next kernel's CTAs come as these leave
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
   auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, w)) != 0; };
@@ -214,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) return false;
     un = units[e];
     __syncwarp();
-    if (lane == 0) mbar_arrive(u_empty(e));
+    mbar_arrive_if(lane == 0, u_empty(e));
     return un.n > 0;
   };
   auto two_tiles = [&](const AttnUnit &un) { return un.row0 + half_rows < un.n * a.rep; };
@@ -342,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // load before it for its own (a phase is told by its parity).
       auto skip = [&](uint32_t k) {
         const bool got = landed(k);
-        if (got && lane == 0) mbar_arrive(kv_empty(stage(k)));
+        mbar_arrive_if(got && lane == 0, kv_empty(stage(k)));
         return got;
       };
       // With two row tiles the lanes take turns (P_t V of one key tile and Q K^T
@@ -460,6 +486,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       int lo, hi;
       attn_row_range(a, un.n, un.len, tok, lo, hi);
       float m = -INFINITY, l = 0.0f;
+      // The maximum is only a guard against overflow: any m gives the same
+      // quotient.  It moves when it would lag by more than 2^8, so that O in
+      // TMEM is rescaled a few times a row and not in every tile; the weights
+      // then stay below 2^8, within both 16-bit types.  O is at rest when this
+      // is called: P_t V of the tile before is done (where P lies over S, S_t
+      // was issued behind it).
+      auto follow = [&](float tile_top, bool first) {
+        const bool lags = valid && (tile_top - m) * sc > kSlack;  // (also from -inf; NaN: no)
+        if (first) {
+          m = tile_top;
+        } else if (__any_sync(0xffffffffu, lags)) {
+          const float now = lags ? tile_top : m;
+          const float f = lags ? exp2_fast((m - now) * sc) : 1.0f;
+          m = now;
+          l *= f;
+#pragma unroll 1
+          for (int c = 0; c < kDp; c += 16) {
+            uint32_t y[16];
+            tmem_ld_x16(to + c, y);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+            tmem_st_x16(to + c, y);
+          }
+        }
+      };
       const int j0 = un.t_begin + (two ? 0 : t), dj = two ? 1 : 2;
       for (int j = j0; j < un.t_end; j += dj) {
         ok = wait(s_full(t), ns & 1);
@@ -467,107 +518,157 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ns;
         tc_fence_after();
         if (some) {
-          // Hidden keys: S is set to -inf in TMEM first, 32 columns at a time
-          // (small code; few tiles have any).
-          const int from = lo - j * kKt, to_key = hi - j * kKt;
-          if (__any_sync(0xffffffffu, valid && (from > 0 || to_key < kKt))) {
+          if constexpr (L::kApart) {
+            // Hidden keys: S is set to -inf in TMEM first, 32 columns at a time
+            // (small code; few tiles have any).
+            const int from = lo - j * kKt, to_key = hi - j * kKt;
+            if (__any_sync(0xffffffffu, valid && (from > 0 || to_key < kKt))) {
 #pragma unroll 1
-            for (int c = 0; c < kKt; c += 32) {
-              const int y0 = from - c, y1 = to_key - c;
-              if (!__any_sync(0xffffffffu, valid && (y0 > 0 || y1 < 32))) continue;
-              uint32_t y[32];
-              tmem_ld_32x32b_x32(ts + c, y);
-              tmem_wait_ld(y);
+              for (int c = 0; c < kKt; c += 32) {
+                const int y0 = from - c, y1 = to_key - c;
+                if (!__any_sync(0xffffffffu, valid && (y0 > 0 || y1 < 32))) continue;
+                uint32_t y[32];
+                tmem_ld_32x32b_x32(ts + c, y);
+                tmem_wait_ld(y);
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < y0 || i >= y1) y[i] = 0xff800000u;
-              tmem_st_32x32b_x32(ts + c, y);
+                for (int i = 0; i < 32; ++i)
+                  if (i < y0 || i >= y1) y[i] = 0xff800000u;
+                tmem_st_32x32b_x32(ts + c, y);
+              }
+              tmem_wait_st();
             }
-            tmem_wait_st();
-          }
-          uint32_t x[2][64];
-          float top[4];
+            uint32_t x[2][64];
+            float top[4];
 #pragma unroll
-          for (int h = 0; h < 4; ++h) tmem_ld_max_x32(ts + 32 * h, x[h >> 1] + 32 * (h & 1), top[h]);
-          tmem_wait_ld(x[0]);
-          tmem_wait_ld(x[1]);
-          asm volatile("" : "+f"(top[0]), "+f"(top[1]), "+f"(top[2]), "+f"(top[3]));
-          if (L::kApart) {
+            for (int h = 0; h < 4; ++h) tmem_ld_max_x32(ts + 32 * h, x[h >> 1] + 32 * (h & 1), top[h]);
+            tmem_wait_ld(x[0]);
+            tmem_wait_ld(x[1]);
+            asm volatile("" : "+f"(top[0]), "+f"(top[1]), "+f"(top[2]), "+f"(top[3]));
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(s_empty(t));
+            mbar_arrive_if(lane == 0, s_empty(t));
             ok = wait(p_empty(t), (ns & 1));  // P_t V of the tile before (ns counts this tile already)
             if (!ok) break;
             tc_fence_after();
-          }
-          const float tile_top = max3(fmaxf(top[0], top[1]), top[2], top[3]);
-          // The maximum is only a guard against overflow: any m gives the same
-          // quotient.  It moves when it would lag by more than 2^8, so that O
-          // in TMEM is rescaled a few times a row and not in every tile; the
-          // weights then stay below 2^8, within both 16-bit types.  O is at
-          // rest here: P_t V of the tile before is done (where P lies over S,
-          // S_t(j) was issued behind it).
-          const bool lags = valid && (tile_top - m) * sc > kSlack;  // (also from -inf; NaN: no)
-          if (j == j0) {
-            m = tile_top;
-          } else if (__any_sync(0xffffffffu, lags)) {
-            const float now = lags ? tile_top : m;
-            const float f = lags ? exp2_fast((m - now) * sc) : 1.0f;
-            m = now;
-            l *= f;
-#pragma unroll 1
-            for (int c = 0; c < kDp; c += 32) {
-              uint32_t y[32];
-              tmem_ld_32x32b_x32(to + c, y);
-              tmem_wait_ld(y);
+            follow(max3(fmaxf(top[0], top[1]), top[2], top[3]), j == j0);
+            const float off = m == -INFINITY ? 0.0f : -m * sc;
+            const uint64_t sc2 = pair_of(sc, sc), off2 = pair_of(off, off);
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
-              for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
-              tmem_st_32x32b_x32(to + c, y);
-            }
-          }
-          const float off = m == -INFINITY ? 0.0f : -m * sc;
-          const uint64_t sc2 = pair_of(sc, sc), off2 = pair_of(off, off);
-          uint64_t sum[2] = {0, 0};
+            for (int h = 0; h < 2; ++h) {
+              uint32_t p[32];
+              // Eight at a time, the exponentials of one group beside the sums and
+              // conversions of the one before: exp2 keeps its unit busy for 4
+              // clocks a warp, the packed FMA, the add and the conversion two each.
+              float e[2][8];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t p[32];
-            // Eight at a time, the exponentials of one group beside the sums and
-            // conversions of the one before: exp2 keeps its unit busy for 4
-            // clocks a warp, the packed FMA, the add and the conversion two each.
-            float e[2][8];
+              for (int g = 0; g <= 8; ++g)
 #pragma unroll
-            for (int g = 0; g <= 8; ++g)
-#pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                float *now = e[g & 1] + i, *old = e[(g & 1) ^ 1] + i;
-                if (g < 8) {
-                  const int c = 8 * g + i;
-                  parts_of(fma2(pair_of(__uint_as_float(x[h][c]), __uint_as_float(x[h][c + 1])), sc2, off2), now[0], now[1]);
-                  now[0] = exp2_fast(now[0]);
+                for (int i = 0; i < 8; i += 2) {
+                  float *now = e[g & 1] + i, *old = e[(g & 1) ^ 1] + i;
+                  if (g < 8) {
+                    const int c = 8 * g + i;
+                    parts_of(fma2(pair_of(__uint_as_float(x[h][c]), __uint_as_float(x[h][c + 1])), sc2, off2), now[0], now[1]);
+                    now[0] = exp2_fast(now[0]);
+                  }
+                  if (g > 0) sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pair_of(old[0], old[1]));
+                  if (g < 8) now[1] = exp2_fast(now[1]);
+                  if (g > 0) p[4 * (g - 1) + i / 2] = pack(old[0], old[1], T());  // one rounding, to the type of V: the UMMA's operands have one type
                 }
-                if (g > 0) sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pair_of(old[0], old[1]));
-                if (g < 8) now[1] = exp2_fast(now[1]);
-                if (g > 0) p[4 * (g - 1) + i / 2] = pack(old[0], old[1], T());  // one rounding, to the type of V: the UMMA's operands have one type
+              tmem_st_32x32b_x32(tp + 32 * h, p);
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              mbar_arrive_if(lane == 0, p_full(t, h));
+            }
+            float s0, s1;
+            parts_of(add2(sum[0], sum[1]), s0, s1);
+            l += s0 + s1;
+          } else {
+            // Two passes over S, both in short loops: the tile's code has to stay
+            // in the instruction caches of warps that run different parts of it
+            // (unrolled over all 128 columns, warps waited for instructions as
+            // often as they issued one).  First the maximum.
+            const int from = lo - j * kKt, to_key = hi - j * kKt;
+            const bool ends = __any_sync(0xffffffffu, valid && (from > 0 || to_key < kKt));
+            float top[4];
+            if (!ends) {
+              uint32_t x[4][32];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) tmem_ld_max_x32(ts + 32 * h, x[h], top[h]);
+              tmem_wait_ld();
+              asm volatile("" : "+f"(top[0]), "+f"(top[1]), "+f"(top[2]), "+f"(top[3]));
+            } else {  // hidden keys (the tiles at a row's ends) become -inf in TMEM
+              top[0] = top[1] = top[2] = top[3] = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < kKt; c += 32) {
+                const int y0 = from - c, y1 = to_key - c;
+                uint32_t y[32];
+                tmem_ld_32x32b_x32(ts + c, y);
+                tmem_wait_ld(y);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  if (i < y0 || i >= y1) y[i] = 0xff800000u;
+                  if (i + 1 < y0 || i + 1 >= y1) y[i + 1] = 0xff800000u;
+                  top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+                }
+                tmem_st_32x32b_x32(ts + c, y);
               }
-            tmem_st_32x32b_x32(tp + 32 * h, p);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_full(t, h));
+              tmem_wait_st();
+            }
+            follow(max3(fmaxf(top[0], top[1]), top[2], top[3]), j == j0);
+            const float off = m == -INFINITY ? 0.0f : -m * sc;
+            const uint64_t sc2 = pair_of(sc, sc), off2 = pair_of(off, off);
+            uint64_t sum[2] = {0, 0};
+            // Then the weights, 32 columns at a time; eight at a time the
+            // exponentials of one group beside the sums and conversions of the one
+            // before: exp2 keeps its unit busy for 4 clocks a warp, the packed
+            // FMA, the add and the conversion two each.
+            auto weights = [&](uint32_t (&x)[32], int c) {
+              float e[2][8];
+              uint32_t p[16];
+#pragma unroll
+              for (int g = 0; g <= 4; ++g)
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                  float *now = e[g & 1] + i, *old = e[(g & 1) ^ 1] + i;
+                  if (g < 4) {
+                    parts_of(fma2(pair_of(__uint_as_float(x[8 * g + i]), __uint_as_float(x[8 * g + i + 1])), sc2, off2), now[0], now[1]);
+                    now[0] = exp2_fast(now[0]);
+                  }
+                  if (g > 0) sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pair_of(old[0], old[1]));
+                  if (g < 4) now[1] = exp2_fast(now[1]);
+                  if (g > 0) p[4 * (g - 1) + i / 2] = pack(old[0], old[1], T());  // one rounding, to the type of V: the UMMA's operands have one type
+                }
+              tmem_st_x16(tp + c / 2, p);  // (over S: behind what has been read)
+            };
+            uint32_t x0[32], x1[32];
+            tmem_ld_32x32b_x32(ts, x0);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              tmem_wait_ld(x0);
+              tmem_ld_32x32b_x32(ts + 64 * h + 32, x1);
+              weights(x0, 64 * h);
+              tmem_wait_ld(x1);
+              if (h == 0) tmem_ld_32x32b_x32(ts + 64, x0);
+              weights(x1, 64 * h + 32);
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              mbar_arrive_if(lane == 0, p_full(t, h));
+            }
+            float s0, s1;
+            parts_of(add2(sum[0], sum[1]), s0, s1);
+            l += s0 + s1;
           }
-          float s0, s1;
-          parts_of(add2(sum[0], sum[1]), s0, s1);
-          l += s0 + s1;
         } else {
           if (L::kApart) {
-            if (lane == 0) mbar_arrive(s_empty(t));
+            mbar_arrive_if(lane == 0, s_empty(t));
             ok = wait(p_empty(t), (ns & 1));
             if (!ok) break;
           }
-          if (lane == 0) {
-            mbar_arrive(p_full(t, 0));
-            mbar_arrive(p_full(t, 1));
-          }
+          mbar_arrive_if(lane == 0, p_full(t, 0));
+          mbar_arrive_if(lane == 0, p_full(t, 1));
         }
       }
       if (!ok) break;
@@ -615,67 +716,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool cut = un.slot >= 0;
         float4 *po = a.part_o + static_cast<int64_t>(un.slot) * (a.d / 4) * (2 * half_rows) + (row - un.row0);
         const int64_t oat = (un.q0 + tok) * a.out_token + head * a.out_head;
-#pragma unroll 1  // (small code: a short call runs it once, from a cold instruction cache)
-        for (int c = 0; c < kDp; c += 32) {
-          uint32_t y[32];
+        // the row of this lane's pair of lanes that it writes to in the second store
+        const int64_t here = valid ? oat : -1, other = __shfl_xor_sync(0xffffffffu, here, 1);
+        const bool odd = lane & 1;
+        // 16 columns a turn of a short loop: run once a unit, straight code
+        // costs about five clocks an instruction, waiting to be fetched.
+#pragma unroll 1
+        for (int c = 0; c < a.d; c += 16) {
+          uint32_t y[16];
           if (tiles == 0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = 0;
+            for (int i = 0; i < 16; ++i) y[i] = 0;
           } else {
-            tmem_ld_32x32b_x32(to + c, y);
-            tmem_wait_ld(y);
+            tmem_ld_x16(to + c, y);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f0);
+            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f0);
             if (both) {
-              uint32_t z[32];
-              tmem_ld_32x32b_x32(to1 + c, z);
-              tmem_wait_ld(z);
+              uint32_t z[16];
+              tmem_ld_x16(to1 + c, z);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(fmaf(__uint_as_float(z[i]), f1, __uint_as_float(y[i])));
+              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(fmaf(__uint_as_float(z[i]), f1, __uint_as_float(y[i])));
             }
           }
+          const bool full = c + 16 <= a.d;  // (else eight columns)
           if (cut) {
             if (valid) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                if (c + i < a.d)
-                  po[((c + i) / 4) * (2 * half_rows)] = make_float4(__uint_as_float(y[i]), __uint_as_float(y[i + 1]),
-                                                                    __uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
-            }
-          } else if (a.out_type == MMQ_DT_F32) {
-            float *dst = static_cast<float *>(a.out) + oat;
-            if (valid) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                if (c + i < a.d) *reinterpret_cast<uint4 *>(dst + c + i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-            }
-          } else {
-            // Four lanes swap their 16-byte chunks, so that they write 64
-            // bytes of one row together: a store that goes to 32 rows takes
-            // the memory pipe 32 clocks, one that goes to eight rows 8.
-            uint32_t z[4][4];  // chunk, word
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) z[i][k] = pack(__uint_as_float(y[8 * i + 2 * k]), __uint_as_float(y[8 * i + 2 * k + 1]), T());
-#pragma unroll
-            for (int d = 1; d < 4; d <<= 1)
+              float4 *dst = po + (c / 4) * (2 * half_rows);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (!(i & d))
+                if (i < 2 || full)
+                  dst[i * (2 * half_rows)] = make_float4(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1]),
+                                                         __uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3]));
+            }
+          } else if (a.out_type == MMQ_DT_F32) {
+            if (valid) {
+              uint4 *dst = reinterpret_cast<uint4 *>(static_cast<float *>(a.out) + oat + c);
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const bool up = lane & d;
-                    const uint32_t give = up ? z[i][k] : z[i | d][k], got = __shfl_xor_sync(0xffffffffu, give, d);
-                    (up ? z[i][k] : z[i | d][k]) = got;
-                  }
-            // z[i] is now chunk lane & 3 of the row of lane (lane & ~3) + i
-            const int col = c + 8 * (lane & 3);
+              for (int i = 0; i < 4; ++i)
+                if (i < 2 || full) dst[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            }
+          } else {
+            // Two lanes swap 16-byte chunks, so that they write 32 bytes of one
+            // row together (a store to 32 rows takes the memory pipe 32 clocks).
+            uint32_t z[2][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int64_t to_row = __shfl_sync(0xffffffffu, valid ? oat : -1, (lane & ~3) + i);
-              if (to_row >= 0 && col < a.d)
-                *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + to_row + col) = make_uint4(z[i][0], z[i][1], z[i][2], z[i][3]);
+            for (int i = 0; i < 8; ++i) z[i >> 2][i & 3] = pack(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]), T());
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t give = odd ? z[0][k] : z[1][k], got = __shfl_xor_sync(0xffffffffu, give, 1);
+              if (odd) z[0][k] = got;
+              else z[1][k] = got;
+            }
+            // even lane: chunk 0 of its row, then of the odd lane's; odd lane: chunk 1 of the even lane's, then of its own
+            const int64_t r0 = odd ? other : here, r1 = odd ? here : other;
+            T *dst = static_cast<T *>(a.out) + c + 8 * odd;
+            if (full || !odd) {
+              if (r0 >= 0) *reinterpret_cast<uint4 *>(dst + r0) = make_uint4(z[0][0], z[0][1], z[0][2], z[0][3]);
+              if (r1 >= 0) *reinterpret_cast<uint4 *>(dst + r1) = make_uint4(z[1][0], z[1][1], z[1][2], z[1][3]);
             }
           }
         }
@@ -688,10 +785,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tiles) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(o_empty(t));
-          if (both) mbar_arrive(o_empty(1));
-        }
+        mbar_arrive_if(lane == 0, o_empty(t));
+        mbar_arrive_if(lane == 0 && both, o_empty(1));
       }
     }
   }
@@ -749,8 +844,7 @@ cudaError_t launch_umma(const AttnArgs &a, const AttnUmma &u, int dev, unsigned 
     ready[dev].store(st);
   }
   if (st != 1) return cudaErrorInvalidKernelImage;
-  attention_umma_kernel<T, kDp><<<grid, kThreads, Lay<kDp>::kBytes, s>>>(a, u);
-  return cudaGetLastError();
+  return launch_early(attention_umma_kernel<T, kDp>, grid, 1, kThreads, Lay<kDp>::kBytes, s, a, u);
 }
 
 }  // namespace

@@ -100,6 +100,24 @@ struct CallContext {
 };
 int call_context(CallContext *out);
 
+// Launches a kernel that may begin while the one before it on the stream ends
+// (it calls griddep_wait before it touches memory another kernel may use).
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), unsigned grid_x, unsigned grid_y, unsigned threads, size_t smem, cudaStream_t s,
+                         const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid_x, grid_y);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- paged cache and serving step (paged.cu, verify.cu, attention*.cu) ----
 constexpr int64_t kMaxRequests = 8192;  // their sums stay in shared memory
 

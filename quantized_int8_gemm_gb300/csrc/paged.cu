@@ -76,6 +76,8 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const __grid_c
   __shared__ int64_t warp_sums[2 * kTabThreads / 32];
   const int n = a.nreq, tid = threadIdx.x;
   int *first_tok = sums, *first_page = sums + n + 1;
+  griddep_wait();
+  griddep_launch_dependents();
   const int per = (n + kTabThreads - 1) / kTabThreads, b0 = min(tid * per, n), b1 = min(b0 + per, n);
   int64_t tok = 0, page = 0, tok_all, page_all;
   for (int b = b0; b < b1; ++b) {
@@ -196,6 +198,8 @@ constexpr int kWriteThreads = 256;
 // that follows.
 template <class S, class D>
 __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_constant__ KvWriteArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
   const int per_tensor = a.heads * (a.head_dim >> 3), per_tok = 2 * per_tensor;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_cta;
   const int toks = static_cast<int>(min(static_cast<int64_t>(a.tokens_per_cta), a.ntok - t0));
@@ -228,9 +232,7 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_co
 
 template <class S>
 cudaError_t launch_kv_write_from(const KvWriteArgs &a, unsigned grid, cudaStream_t s) {
-  if (a.cache.type == MMQ_DT_F16) kv_write_kernel<S, __half><<<grid, kWriteThreads, 0, s>>>(a);
-  else kv_write_kernel<S, __nv_bfloat16><<<grid, kWriteThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(a.cache.type == MMQ_DT_F16 ? kv_write_kernel<S, __half> : kv_write_kernel<S, __nv_bfloat16>, grid, 1, kWriteThreads, 0, s, a);
 }
 
 }  // namespace
@@ -242,8 +244,7 @@ cudaError_t launch_page_tables(const PageTablesArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   const int64_t ctas = (a.max_tokens + kTabTokens - 1) / kTabTokens;
-  page_tables_kernel<<<static_cast<unsigned>(ctas > 0 ? ctas : 1), kTabThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(page_tables_kernel, static_cast<unsigned>(ctas > 0 ? ctas : 1), 1, kTabThreads, smem, s, a);
 }
 
 cudaError_t launch_kv_write(KvWriteArgs a, cudaStream_t s) {

@@ -23,6 +23,16 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
+// Four elements.
+template <class T>
+struct Quad {
+  using type = uint2;
+};
+template <>
+struct Quad<float> {
+  using type = uint4;
+};
+
 // The better of two candidates is the larger number: the key's bits above,
 // the complement of the index below (so that ties go to the lowest index).
 // 0: no candidate.
@@ -52,26 +62,22 @@ __device__ __forceinline__ uint64_t race(const T *__restrict__ p, const T *__res
     const int64_t groups = n >> 2;
     float highest = 0.0f;
     for (int64_t i0 = me - (threadIdx.x & 31); i0 < groups; i0 += kBatch * step) {  // (the warp as one)
+      // every load of the batch before the first use (lanes past the row repeat its first group)
       float w[kBatch][4], ev[kBatch][4];
+      typename Quad<T>::type pv[kBatch], qv[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int64_t i = i0 + (threadIdx.x & 31) + u * step;
-        T pv[4], qv[4];
-        if (i < groups) {
-          *reinterpret_cast<float4 *>(ev[u]) = __ldcs(reinterpret_cast<const float4 *>(e) + i);
-          if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<uint4 *>(pv) = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-            if (kLeft) *reinterpret_cast<uint4 *>(qv) = __ldcs(reinterpret_cast<const uint4 *>(q) + i);
-          } else {
-            *reinterpret_cast<uint2 *>(pv) = __ldcs(reinterpret_cast<const uint2 *>(p) + i);
-            if (kLeft) *reinterpret_cast<uint2 *>(qv) = __ldcs(reinterpret_cast<const uint2 *>(q) + i);
-          }
+        const int64_t i = i0 + (threadIdx.x & 31) + u * step, at = i < groups ? i : 0;
+        *reinterpret_cast<float4 *>(ev[u]) = __ldcs(reinterpret_cast<const float4 *>(e) + at);
+        pv[u] = __ldcs(reinterpret_cast<const typename Quad<T>::type *>(p) + at);
+        if (kLeft) qv[u] = __ldcs(reinterpret_cast<const typename Quad<T>::type *>(q) + at);
+      }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[u][k] = kLeft ? to_f32(pv[k]) - to_f32(qv[k]) : to_f32(pv[k]);
-        } else {
+      for (int u = 0; u < kBatch; ++u) {
+        const bool in = i0 + (threadIdx.x & 31) + u * step < groups;
+        const T *pt = reinterpret_cast<const T *>(&pv[u]), *qt = reinterpret_cast<const T *>(&qv[u]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[u][k] = 0.0f, ev[u][k] = 1.0f;
-        }
+        for (int k = 0; k < 4; ++k) w[u][k] = !in ? 0.0f : kLeft ? to_f32(pt[k]) - to_f32(qt[k]) : to_f32(pt[k]);
       }
       // 0: no weight; negative: to be divided in any case
       auto near_key = [](float wt, float x) {
@@ -142,6 +148,8 @@ __global__ void __launch_bounds__(kVerThreads, 4) __cluster_dims__(kVerCtas, 1, 
     verify_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ uint64_t own[kVerThreads / 32], all[2][kVerCtas];
   __shared__ int s_kept;
+  griddep_wait();
+  griddep_launch_dependents();
   const uint32_t rank = cluster_ctarank();
   const int64_t b = blockIdx.x / kVerCtas;
   const int k = a.k, lane = threadIdx.x & 31;
@@ -211,10 +219,8 @@ cudaError_t launch_verify(VerifyArgs a, cudaStream_t s) {
   a.wide = on16(a.target) && on16(a.draft) && on16(a.noise) && row16(a.target_req) && row16(a.target_row) &&
            (!a.draft || (row16(a.draft_req) && row16(a.draft_row))) && a.noise_stride % 4 == 0;
   const unsigned grid = static_cast<unsigned>(a.nreq * kVerCtas);
-  if (a.type == MMQ_DT_F32) verify_kernel<float><<<grid, kVerThreads, 0, s>>>(a);
-  else if (a.type == MMQ_DT_F16) verify_kernel<__half><<<grid, kVerThreads, 0, s>>>(a);
-  else verify_kernel<__nv_bfloat16><<<grid, kVerThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(a.type == MMQ_DT_F32 ? verify_kernel<float> : a.type == MMQ_DT_F16 ? verify_kernel<__half> : verify_kernel<__nv_bfloat16>,
+                      grid, 1, kVerThreads, 0, s, a);
 }
 
 }  // namespace mmq
