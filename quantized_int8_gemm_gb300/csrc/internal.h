@@ -152,10 +152,9 @@ struct VerifyArgs {
   int64_t target_req, target_row, draft_req, draft_row, tokens_stride, u_stride, noise_stride;
   int64_t nreq, vocab;
   int32_t k, type;
-  int32_t wide;
   int *status;
 };
-cudaError_t launch_verify(VerifyArgs a, cudaStream_t s);
+cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s);
 
 // Engine-rate microbenchmarks (probe.cu); out[0..4] as mmq_probe_engine_rates.
 cudaError_t launch_engine_probes(DevStatus *st, unsigned epoch, uint64_t limit_ns, cudaStream_t s, double *out);

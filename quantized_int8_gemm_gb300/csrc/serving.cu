@@ -106,7 +106,7 @@ int mmq_verify_draft(const mmq_verification *args, mmq_stream_t stream) {
   a.target = t.target, a.draft = t.draft, a.tokens = t.tokens, a.n_draft = t.n_draft, a.u = t.u, a.noise = t.noise;
   a.out = t.out, a.accepted = t.accepted, a.target_req = t.target_req, a.target_row = t.target_row;
   a.draft_req = t.draft_req, a.draft_row = t.draft_row, a.tokens_stride = t.tokens_stride, a.u_stride = t.u_stride;
-  a.noise_stride = t.noise_stride, a.nreq = t.nreq, a.vocab = t.vocab, a.k = t.k, a.type = t.type, a.wide = 0;
+  a.noise_stride = t.noise_stride, a.nreq = t.nreq, a.vocab = t.vocab, a.k = t.k, a.type = t.type;
   a.status = &ctx.words->status;
   return cuda_rc(mmq::launch_verify(a, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -23,16 +23,6 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// Four elements.
-template <class T>
-struct Quad {
-  using type = uint2;
-};
-template <>
-struct Quad<float> {
-  using type = uint4;
-};
-
 // The better of two candidates is the larger number: the key's bits above,
 // the complement of the index below (so that ties go to the lowest index).
 // 0: no candidate.
@@ -43,73 +33,59 @@ __device__ __forceinline__ void consider(uint64_t &best, float w, float e, int64
   if (mine > best) best = mine;
 }
 
-// This CTA's part of one row.  kLeft: weights (p - q)+, else p.
+// This CTA's part of one row.  Weights: p, less q where there is one, and none
+// for entry `skip`.  Loads of single elements, each a whole line of a warp, and
+// a batch of them before the first use: rows of an odd vocabulary begin
+// anywhere, and three rows of one request differ in it.
 //
 // Few entries are worth an IEEE division: with a the product of w and the
 // approximate reciprocal (off by less than 2^-21), an entry whose a is below
 // (1 - 2^-19) of the warp's largest so far cannot win.  So a warp takes the
 // largest a of a batch first and divides where a lane is near it; entries
 // whose reciprocal leaves the normal range are always divided.
-template <class T, bool kLeft>
+template <class T>
 __device__ __forceinline__ uint64_t race(const T *__restrict__ p, const T *__restrict__ q, const float *__restrict__ e,
-                                         int64_t n, bool wide, uint32_t rank) {
+                                         int64_t n, int64_t skip, uint32_t rank) {
+  constexpr int kBatch = 8;
+  constexpr int64_t step = kVerCtas * kVerThreads;
+  const int lane = threadIdx.x & 31;
   uint64_t best = 0;
-  const int64_t step = static_cast<int64_t>(kVerCtas) * kVerThreads;
-  const int64_t me = static_cast<int64_t>(rank) * kVerThreads + threadIdx.x;
-  int64_t done = 0;
-  if (wide) {  // rows on 16-byte boundaries: four elements a load, kBatch loads a step
-    constexpr int kBatch = 4;
-    const int64_t groups = n >> 2;
-    float highest = 0.0f;
-    for (int64_t i0 = me - (threadIdx.x & 31); i0 < groups; i0 += kBatch * step) {  // (the warp as one)
-      // every load of the batch before the first use (lanes past the row repeat its first group)
-      float w[kBatch][4], ev[kBatch][4];
-      typename Quad<T>::type pv[kBatch], qv[kBatch];
+  float highest = 0.0f;
+  for (int64_t v0 = static_cast<int64_t>(rank) * kVerThreads + (threadIdx.x - lane); v0 < n; v0 += kBatch * step) {  // (the warp as one)
+    T pv[kBatch], qv[kBatch];
+    float w[kBatch], ev[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {  // (lanes past the row read its first entry)
+      const int64_t v = v0 + lane + u * step, at = v < n ? v : 0;
+      pv[u] = __ldcs(p + at);
+      if (q) qv[u] = __ldcs(q + at);
+      ev[u] = __ldcs(e + at);
+    }
+    // 0: no weight; negative: to be divided in any case
+    auto near_key = [](float wt, float x) {
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+      return !(wt > 0.0f) ? 0.0f : x >= 0x1p-125f && x <= 0x1p125f ? wt * r : -1.0f;
+    };
+    float top = 0.0f, low = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t v = v0 + lane + u * step;
+      w[u] = v >= n || v == skip ? 0.0f : q ? to_f32(pv[u]) - to_f32(qv[u]) : to_f32(pv[u]);
+      const float x = near_key(w[u], ev[u]);
+      top = fmaxf(top, x);
+      low = fminf(low, x);
+    }
+    highest = fmaxf(highest, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
+    const float floor = highest > 1e-30f ? highest * (1.0f - 0x1p-19f) : 0.0f;
+    if (low < 0.0f || (top >= floor && top > 0.0f)) {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int64_t i = i0 + (threadIdx.x & 31) + u * step, at = i < groups ? i : 0;
-        *reinterpret_cast<float4 *>(ev[u]) = __ldcs(reinterpret_cast<const float4 *>(e) + at);
-        pv[u] = __ldcs(reinterpret_cast<const typename Quad<T>::type *>(p) + at);
-        if (kLeft) qv[u] = __ldcs(reinterpret_cast<const typename Quad<T>::type *>(q) + at);
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const bool in = i0 + (threadIdx.x & 31) + u * step < groups;
-        const T *pt = reinterpret_cast<const T *>(&pv[u]), *qt = reinterpret_cast<const T *>(&qv[u]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[u][k] = !in ? 0.0f : kLeft ? to_f32(pt[k]) - to_f32(qt[k]) : to_f32(pt[k]);
-      }
-      // 0: no weight; negative: to be divided in any case
-      auto near_key = [](float wt, float x) {
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-        return !(wt > 0.0f) ? 0.0f : x >= 0x1p-125f && x <= 0x1p125f ? wt * r : -1.0f;
-      };
-      float top = 0.0f, low = 0.0f;
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x = near_key(w[u][k], ev[u][k]);
-          top = fmaxf(top, x);
-          low = fminf(low, x);
-        }
-      highest = fmaxf(highest, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
-      const float floor = highest > 1e-30f ? highest * (1.0f - 0x1p-19f) : 0.0f;
-      if (low < 0.0f || (top >= floor && top > 0.0f)) {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x = near_key(w[u][k], ev[u][k]);
-            if (x < 0.0f || (x > 0.0f && x >= floor))
-              consider(best, w[u][k], ev[u][k], 4 * (i0 + (threadIdx.x & 31) + u * step) + k);
-          }
+        const float x = near_key(w[u], ev[u]);
+        if (x < 0.0f || (x > 0.0f && x >= floor)) consider(best, w[u], ev[u], v0 + lane + u * step);
       }
     }
-    done = groups << 2;
   }
-  for (int64_t v = done + me; v < n; v += step) consider(best, kLeft ? to_f32(p[v]) - to_f32(q[v]) : to_f32(p[v]), e[v], v);
   return best;
 }
 
@@ -186,23 +162,10 @@ __global__ void __launch_bounds__(kVerThreads, 4) __cluster_dims__(kVerCtas, 1, 
   const T *q = draft ? draft + static_cast<int64_t>(kept) * a.draft_row : nullptr;
   const float *e = a.noise + b * a.noise_stride;
   uint64_t best = 0;
-  if (kept < n) {
-    if (q) {
-      best = cluster_best(race<T, true>(p, q, e, a.vocab, a.wide, rank), own, all[0], rank);
-    } else {  // a draft without probabilities gave its token all of them: p without that token
-      const int64_t x = ids[kept];
-      uint64_t m = race<T, false>(p, p, e, x < 0 || x >= a.vocab ? a.vocab : x, a.wide, rank);
-      if (x >= 0 && x < a.vocab) {
-        // the entries behind the refused token; their alignment is not the row's
-        for (int64_t v = x + 1 + static_cast<int64_t>(rank) * kVerThreads + threadIdx.x; v < a.vocab;
-             v += static_cast<int64_t>(kVerCtas) * kVerThreads)
-          consider(m, to_f32(p[v]), e[v], v);
-      }
-      best = cluster_best(m, own, all[0], rank);
-    }
-  }
+  // a draft without probabilities gave its token all of them: p without that token
+  if (kept < n) best = cluster_best(race(p, q, e, a.vocab, q ? -1 : static_cast<int64_t>(ids[kept]), rank), own, all[0], rank);
   if (best == 0)  // nothing was refused, or p - q is nowhere positive
-    best = cluster_best(race<T, false>(p, p, e, a.vocab, a.wide, rank), own, all[1], rank);
+    best = cluster_best(race<T>(p, nullptr, e, a.vocab, -1, rank), own, all[1], rank);
   if (rank != 0) return;
   const int drawn = best ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
   for (int i = threadIdx.x; i <= k; i += kVerThreads)
@@ -212,12 +175,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) __cluster_dims__(kVerCtas, 1, 
 
 }  // namespace
 
-cudaError_t launch_verify(VerifyArgs a, cudaStream_t s) {
-  const int esz = a.type == MMQ_DT_F32 ? 4 : 2;
-  auto on16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-  auto row16 = [&](int64_t stride) { return stride * esz % 16 == 0; };
-  a.wide = on16(a.target) && on16(a.draft) && on16(a.noise) && row16(a.target_req) && row16(a.target_row) &&
-           (!a.draft || (row16(a.draft_req) && row16(a.draft_row))) && a.noise_stride % 4 == 0;
+cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(a.nreq * kVerCtas);
   return launch_early(a.type == MMQ_DT_F32 ? verify_kernel<float> : a.type == MMQ_DT_F16 ? verify_kernel<__half> : verify_kernel<__nv_bfloat16>,
                       grid, 1, kVerThreads, 0, s, a);
