@@ -473,7 +473,8 @@ typedef struct mmq_verification {
  * exponential noise that is a draw from the normalised weights.
  *   out[b] = kept tokens, the drawn token, then -1.
  * A drafted token outside [0, vocab) is refused and reported by
- * mmq_last_device_error.  vocab in 1..2^31-1.  One kernel, no scratch.
+ * mmq_last_device_error.  nreq in 0..65535, vocab in 1..2^31-1.  One kernel,
+ * no scratch.
  * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN (elements off their own alignment),
  * MMQ_ERR_TYPE, MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
  */

@@ -10,32 +10,38 @@ namespace mmq {
 namespace {
 
 // ---------------------------------------------------------------- page tables
-constexpr int kTabThreads = 512;
-constexpr int kTabTokens = 2048;  // tokens of one CTA
+constexpr int kTabThreads = 512;  // and tokens of a CTA
+
+// Sums stop at 2^31 - 1 (for numbers that are not negative the order does not matter).
+__device__ __forceinline__ int sat_add(int a, int b) {
+  return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b), 0x7fffffffu));
+}
 
 // Exclusive sums over the CTA's threads of two values; returns the totals.
-__device__ __forceinline__ void block_exclusive(int64_t &a, int64_t &b, int64_t &ta, int64_t &tb, int64_t *sm) {
+__device__ __forceinline__ void block_exclusive(int &a, int &b, int &ta, int &tb, int *sm) {
   constexpr int kWarps = kTabThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t ia = a, ib = b;
+  int ia = a, ib = b;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t ya = __shfl_up_sync(0xffffffffu, ia, d), yb = __shfl_up_sync(0xffffffffu, ib, d);
-    if (lane >= d) ia += ya, ib += yb;
+    const int ya = __shfl_up_sync(0xffffffffu, ia, d), yb = __shfl_up_sync(0xffffffffu, ib, d);
+    if (lane >= d) ia = sat_add(ia, ya), ib = sat_add(ib, yb);
   }
   if (lane == 31) sm[warp] = ia, sm[kWarps + warp] = ib;
+  ia = __shfl_up_sync(0xffffffffu, ia, 1), ib = __shfl_up_sync(0xffffffffu, ib, 1);
+  if (lane == 0) ia = ib = 0;
   __syncthreads();
-  int64_t pa = 0, pb = 0;
+  int pa = 0, pb = 0;
   ta = tb = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const int64_t xa = sm[w], xb = sm[kWarps + w];
-    if (w < warp) pa += xa, pb += xb;
-    ta += xa;
-    tb += xb;
+    const int xa = sm[w], xb = sm[kWarps + w];
+    if (w < warp) pa = sat_add(pa, xa), pb = sat_add(pb, xb);
+    ta = sat_add(ta, xa);
+    tb = sat_add(tb, xb);
   }
-  a = pa + ia - a;
-  b = pb + ib - b;
+  a = sat_add(pa, ia);
+  b = sat_add(pb, ib);
 }
 
 // The largest i in [0, n) with sums[i] <= x (sums ascending, sums[0] <= x).
@@ -59,96 +65,108 @@ __device__ __forceinline__ Pages pages_of(const PageTablesArgs &a, int b) {
   p.cached = max(a.cached[b], 0);
   p.fresh = max(a.fresh[b], 0);
   p.held = max(a.held[b], 0);
-  const int64_t need = (static_cast<int64_t>(p.cached) + p.fresh + a.page_size - 1) / a.page_size;
-  const int64_t fit = need < a.table_width ? need : a.table_width;
-  p.more = fit > p.held ? static_cast<int>(fit - p.held) : 0;
-  p.lost = need > a.table_width && need > p.held ? static_cast<int>(need - max(static_cast<int64_t>(p.held), a.table_width)) : 0;
+  const int width = static_cast<int>(a.table_width);
+  // ceil(sum / page_size) in 32 bits: the sum is below 2^32
+  const uint32_t sum = static_cast<uint32_t>(p.cached) + static_cast<uint32_t>(p.fresh), size = a.page_size;
+  const int need = static_cast<int>(min(sum / size + (sum % size != 0), 0x7fffffffu));
+  p.more = max(min(need, width) - p.held, 0);
+  p.lost = max(need - max(p.held, width), 0);
   return p;
 }
 
 // One launch for everything.  Each CTA sums the requests' lengths by itself
 // (nreq numbers, from L2) and so needs nothing from another CTA; it then takes
-// its slice of the tokens and of the new pages and finds each one's request by
-// bisection in shared memory.  Latency bound: a few dependent reads of a few
-// KB; the 12 B a token that it writes are 0.8 MB at 65536 tokens.
+// its 512 tokens and its share of the new pages and finds each one's request by
+// bisection in shared memory.  Latency bound: two rounds of reads from L2, a
+// scan and about ten steps of bisection; the 12 B a token that it writes are
+// 0.8 MB at 65536 tokens.
 __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const __grid_constant__ PageTablesArgs a) {
   extern __shared__ int sums[];  // [nreq + 1] first token, [nreq + 1] first new page
-  __shared__ int64_t warp_sums[2 * kTabThreads / 32];
-  const int n = a.nreq, tid = threadIdx.x;
-  int *first_tok = sums, *first_page = sums + n + 1;
+  __shared__ int warp_sums[2 * kTabThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
+  const int n = a.nreq, tid = threadIdx.x;
+  int *first_tok = sums, *first_page = sums + n + 1;
+  constexpr int kKept = 2;  // requests of a thread that stay in registers
   const int per = (n + kTabThreads - 1) / kTabThreads, b0 = min(tid * per, n), b1 = min(b0 + per, n);
-  int64_t tok = 0, page = 0, tok_all, page_all;
-  for (int b = b0; b < b1; ++b) {
+  int tok = 0, page = 0, tok_all, page_all;
+  Pages kept[kKept];
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    kept[i] = Pages{0, 0, 0, 0, 0};
+    if (b0 + i < b1) kept[i] = pages_of(a, b0 + i);
+  }
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) tok = sat_add(tok, kept[i].fresh), page = sat_add(page, kept[i].more);
+  for (int b = b0 + kKept; b < b1; ++b) {
     const Pages p = pages_of(a, b);
-    tok += p.fresh;
-    page += p.more;
+    tok = sat_add(tok, p.fresh);
+    page = sat_add(page, p.more);
   }
   block_exclusive(tok, page, tok_all, page_all, warp_sums);
-  int64_t lost = 0;
-  auto cap = [](int64_t x) { return static_cast<int>(x < 0x7fffffff ? x : 0x7fffffff); };
-  for (int b = b0; b < b1; ++b) {
-    const Pages p = pages_of(a, b);
-    first_tok[b] = cap(tok);
-    first_page[b] = cap(page);
+  const int nfree = static_cast<int>(a.nfree);
+  int lost = 0;
+  auto place = [&](int b, const Pages &p) {
+    first_tok[b] = tok;
+    first_page[b] = page;
     if (blockIdx.x == 0) {
-      a.q_start[b] = cap(tok);
-      a.seq_lens[b] = cap(static_cast<int64_t>(p.cached) + p.fresh);
-      const int64_t left = a.nfree - page;
-      a.held_out[b] = p.held + static_cast<int>(left < 0 ? 0 : left < p.more ? left : p.more);
+      a.q_start[b] = tok;
+      a.seq_lens[b] = sat_add(p.cached, p.fresh);
+      a.held_out[b] = p.held + max(min(p.more, nfree - page), 0);
     }
-    tok += p.fresh;
-    page += p.more;
-    lost += p.lost;
-  }
+    tok = sat_add(tok, p.fresh);
+    page = sat_add(page, p.more);
+    lost = sat_add(lost, p.lost);
+  };
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (b0 + i < b1) place(b0 + i, kept[i]);
+  for (int b = b0 + kKept; b < b1; ++b) place(b, pages_of(a, b));
   if (tid == 0) {
-    first_tok[n] = cap(tok_all);
-    first_page[n] = cap(page_all);
+    first_tok[n] = tok_all;
+    first_page[n] = page_all;
   }
   __syncthreads();
   if (blockIdx.x == 0) {
-    int64_t zero = 0, lost_all, none;
+    int zero = 0, lost_all, none;
     block_exclusive(lost, zero, lost_all, none, warp_sums);
     if (tid == 0) {
-      a.q_start[n] = cap(tok_all);
-      const int64_t short_of = page_all > a.nfree ? page_all - a.nfree : 0;
-      a.taken[0] = cap(page_all - short_of);
-      a.taken[1] = cap(short_of + lost_all);
+      a.q_start[n] = tok_all;
+      a.taken[0] = min(page_all, nfree);
+      a.taken[1] = sat_add(max(page_all - nfree, 0), lost_all);
     }
   }
-  // new entries of the tables
-  const int pages_n = cap(page_all), stride = gridDim.x * kTabThreads;
-  for (int j = blockIdx.x * kTabThreads + tid; j < pages_n; j += stride) {
-    const int b = last_not_above(first_page, n, j);
-    const int at = max(a.held[b], 0) + (j - first_page[b]);
-    a.table[static_cast<int64_t>(b) * a.table_stride + at] = j < a.nfree ? a.free_pages[j] : -1;
-  }
   // tokens
-  const int tok_n = cap(tok_all);
-  const int64_t t_end = min(a.max_tokens, static_cast<int64_t>(blockIdx.x + 1) * kTabTokens);
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTabTokens + tid; t < t_end; t += kTabThreads) {
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTabThreads + tid;
+  if (t < a.max_tokens) {
     int64_t slot = -1;
     int position = -1;
-    if (t < tok_n) {
+    if (t < tok_all) {
       const int b = last_not_above(first_tok, n, static_cast<int>(t));
-      const int64_t pos = static_cast<int64_t>(max(a.cached[b], 0)) + (static_cast<int>(t) - first_tok[b]);
-      const int64_t blk = pos / a.page_size;
       const int held = max(a.held[b], 0);
+      const int64_t pos = static_cast<int64_t>(max(a.cached[b], 0)) + (static_cast<int>(t) - first_tok[b]);
+      const int64_t blk = static_cast<uint32_t>(pos) / static_cast<uint32_t>(a.page_size);  // (pos is below 2^32)
       int id = -1;
       if (blk < a.table_width) {
         if (blk < held) {
           id = a.table[static_cast<int64_t>(b) * a.table_stride + blk];
         } else {
           const int64_t j = first_page[b] + (blk - held);
-          if (j < a.nfree) id = a.free_pages[j];
+          if (j < nfree) id = a.free_pages[j];
         }
       }
-      position = cap(pos);
+      position = static_cast<int>(min(pos, static_cast<int64_t>(0x7fffffff)));
       if (id >= 0) slot = static_cast<int64_t>(id) * a.page_size + (pos - blk * a.page_size);
     }
     a.slots[t] = slot;
     a.positions[t] = position;
+  }
+  // new entries of the tables
+  const int stride = gridDim.x * kTabThreads;
+  for (int64_t j = static_cast<int64_t>(blockIdx.x) * kTabThreads + tid; j < page_all; j += stride) {
+    const int b = last_not_above(first_page, n, static_cast<int>(j));
+    const int at = max(a.held[b], 0) + (static_cast<int>(j) - first_page[b]);
+    a.table[static_cast<int64_t>(b) * a.table_stride + at] = j < nfree ? a.free_pages[j] : -1;
   }
 }
 
@@ -243,7 +261,7 @@ cudaError_t launch_page_tables(const PageTablesArgs &a, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * (kMaxRequests + 1) * 4);
     if (e != cudaSuccess) return e;
   }
-  const int64_t ctas = (a.max_tokens + kTabTokens - 1) / kTabTokens;
+  const int64_t ctas = (a.max_tokens + kTabThreads - 1) / kTabThreads;
   return launch_early(page_tables_kernel, static_cast<unsigned>(ctas > 0 ? ctas : 1), 1, kTabThreads, smem, s, a);
 }
 

@@ -92,7 +92,7 @@ int mmq_verify_draft(const mmq_verification *args, mmq_stream_t stream) {
   if (!args) return MMQ_ERR_ARG;
   const mmq_verification &t = *args;
   if (t.type != MMQ_DT_F32 && t.type != MMQ_DT_F16 && t.type != MMQ_DT_BF16) return MMQ_ERR_TYPE;
-  if (t.nreq < 0 || t.nreq > (1 << 24) || t.vocab < 1 || t.vocab > kInt32 || t.k < 0 || t.k == kInt32) return MMQ_ERR_ARG;
+  if (t.nreq < 0 || t.nreq > 65535 || t.vocab < 1 || t.vocab > kInt32 || t.k < 0 || t.k == kInt32) return MMQ_ERR_ARG;
   if (t.target_req < 0 || t.target_row < 0 || t.draft_req < 0 || t.draft_row < 0 || t.tokens_stride < 0 || t.u_stride < 0 ||
       t.noise_stride < 0)
     return MMQ_ERR_ARG;

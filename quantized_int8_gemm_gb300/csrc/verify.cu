@@ -10,6 +10,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -17,7 +19,6 @@ namespace mmq {
 namespace {
 
 constexpr int kVerThreads = 256;
-constexpr int kVerCtas = 8;  // CTAs (one cluster) of a request
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
@@ -43,23 +44,26 @@ __device__ __forceinline__ void consider(uint64_t &best, float w, float e, int64
 // (1 - 2^-19) of the warp's largest so far cannot win.  So a warp takes the
 // largest a of a batch first and divides where a lane is near it; entries
 // whose reciprocal leaves the normal range are always divided.
-template <class T>
+template <class T, int kCtas>
 __device__ __forceinline__ uint64_t race(const T *__restrict__ p, const T *__restrict__ q, const float *__restrict__ e,
                                          int64_t n, int64_t skip, uint32_t rank) {
-  constexpr int kBatch = 8;
-  constexpr int64_t step = kVerCtas * kVerThreads;
+  constexpr int kBatch = 8, kStep = kCtas * kVerThreads;
   const int lane = threadIdx.x & 31;
   uint64_t best = 0;
   float highest = 0.0f;
-  for (int64_t v0 = static_cast<int64_t>(rank) * kVerThreads + (threadIdx.x - lane); v0 < n; v0 += kBatch * step) {  // (the warp as one)
+  auto batch = [&](int64_t v0, auto is_whole) {  // entries v0 + lane + u * kStep (not whole: those below n)
+    constexpr bool whole = decltype(is_whole)::value;
     T pv[kBatch], qv[kBatch];
     float w[kBatch], ev[kBatch];
+    const T *pb = p + v0 + lane, *qb = q + v0 + lane;
+    const float *eb = e + v0 + lane;
+    const int64_t left = n - v0 - lane;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {  // (lanes past the row read its first entry)
-      const int64_t v = v0 + lane + u * step, at = v < n ? v : 0;
-      pv[u] = __ldcs(p + at);
-      if (q) qv[u] = __ldcs(q + at);
-      ev[u] = __ldcs(e + at);
+    for (int u = 0; u < kBatch; ++u) {
+      const bool in = whole || u * kStep < left;
+      if (in) pv[u] = __ldcs(pb + u * kStep);
+      if (in && q) qv[u] = __ldcs(qb + u * kStep);
+      if (in) ev[u] = __ldcs(eb + u * kStep);
     }
     // 0: no weight; negative: to be divided in any case
     auto near_key = [](float wt, float x) {
@@ -70,8 +74,12 @@ __device__ __forceinline__ uint64_t race(const T *__restrict__ p, const T *__res
     float top = 0.0f, low = 0.0f;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int64_t v = v0 + lane + u * step;
-      w[u] = v >= n || v == skip ? 0.0f : q ? to_f32(pv[u]) - to_f32(qv[u]) : to_f32(pv[u]);
+      if (!whole && u * kStep >= left) {
+        w[u] = 0.0f, ev[u] = 1.0f;
+        continue;
+      }
+      w[u] = q ? to_f32(pv[u]) - to_f32(qv[u]) : to_f32(pv[u]);
+      if (v0 + lane + u * kStep == skip) w[u] = 0.0f;
       const float x = near_key(w[u], ev[u]);
       top = fmaxf(top, x);
       low = fminf(low, x);
@@ -82,10 +90,13 @@ __device__ __forceinline__ uint64_t race(const T *__restrict__ p, const T *__res
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const float x = near_key(w[u], ev[u]);
-        if (x < 0.0f || (x > 0.0f && x >= floor)) consider(best, w[u], ev[u], v0 + lane + u * step);
+        if (x < 0.0f || (x > 0.0f && x >= floor)) consider(best, w[u], ev[u], v0 + lane + u * kStep);
       }
     }
-  }
+  };
+  int64_t v0 = static_cast<int64_t>(rank) * kVerThreads + (threadIdx.x - lane);  // (the warp as one)
+  for (; v0 + 31 + (kBatch - 1) * kStep < n; v0 += kBatch * kStep) batch(v0, std::true_type());
+  if (v0 < n) batch(v0, std::false_type());
   return best;
 }
 
@@ -99,6 +110,7 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t x) {
 }
 
 // The cluster's best: each CTA reduces its own and writes it to every CTA.
+template <int kCtas>
 __device__ __forceinline__ uint64_t cluster_best(uint64_t mine, uint64_t *own, uint64_t *all, uint32_t rank) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   mine = warp_max(mine);
@@ -106,28 +118,28 @@ __device__ __forceinline__ uint64_t cluster_best(uint64_t mine, uint64_t *own, u
   __syncthreads();
   if (warp == 0) {
     const uint64_t b = warp_max(lane < kVerThreads / 32 ? own[lane] : 0);
-    if (lane < kVerCtas)
+    if (lane < kCtas)
       asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_addr(all + rank), lane)), "l"(b) : "memory");
   }
   cluster_sync();
   uint64_t best = 0;
 #pragma unroll
-  for (int i = 0; i < kVerCtas; ++i) best = all[i] > best ? all[i] : best;
+  for (int i = 0; i < kCtas; ++i) best = all[i] > best ? all[i] : best;
   return best;
 }
 
 // A cluster of 8 CTAs for each request: the row of the vocabulary is split
 // over them and joined through their shared memory, one launch, no scratch.
 // HBM bound: one row each of p, q and e (12 B an entry in fp32).
-template <class T>
-__global__ void __launch_bounds__(kVerThreads, 4) __cluster_dims__(kVerCtas, 1, 1)
+template <class T, int kCtas>
+__global__ void __launch_bounds__(kVerThreads, 4) __cluster_dims__(kCtas, 1, 1)
     verify_kernel(const __grid_constant__ VerifyArgs a) {
-  __shared__ uint64_t own[kVerThreads / 32], all[2][kVerCtas];
+  __shared__ uint64_t own[kVerThreads / 32], all[2][kCtas];
   __shared__ int s_kept;
   griddep_wait();
   griddep_launch_dependents();
-  const uint32_t rank = cluster_ctarank();
-  const int64_t b = blockIdx.x / kVerCtas;
+  const uint32_t rank = blockIdx.x;  // (a cluster is a row of the grid)
+  const int64_t b = blockIdx.y;
   const int k = a.k, lane = threadIdx.x & 31;
   const int n = max(0, min(a.n_draft ? a.n_draft[b] : k, k));
   const T *target = static_cast<const T *>(a.target) + b * a.target_req;
@@ -136,19 +148,18 @@ __global__ void __launch_bounds__(kVerThreads, 4) __cluster_dims__(kVerCtas, 1, 
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   if (threadIdx.x < 32) {  // kept drafted tokens
     int kept = n;
-    for (int i0 = 0; i0 < n && kept == n; i0 += 32) {
+    for (int i0 = 0; i0 < k && kept == n; i0 += 32) {
       const int i = i0 + lane;
       bool pass = true;
-      if (i < n) {
+      if (i < k) {  // (n may still be on its way)
         const int64_t x = ids[i];
-        if (x < 0 || x >= a.vocab) {
-          pass = false;
-          record_index(a.status);
-        } else {
-          const float p = to_f32(target[i * a.target_row + x]);
-          const float q = draft ? to_f32(draft[i * a.draft_row + x]) : 1.0f;
-          pass = __fmul_rn(a.u[b * a.u_stride + i], q) < p;
-        }
+        const float u = a.u[b * a.u_stride + i];
+        const bool known = x >= 0 && x < a.vocab;
+        const int64_t at = known ? x : 0;
+        const float p = to_f32(target[i * a.target_row + at]);
+        const float q = draft ? to_f32(draft[i * a.draft_row + at]) : 1.0f;
+        pass = i >= n || (known && __fmul_rn(u, q) < p);
+        if (i < n && !known) record_index(a.status);
       }
       const uint32_t refused = __ballot_sync(0xffffffffu, !pass);
       if (refused) kept = i0 + __ffs(refused) - 1;
@@ -163,9 +174,9 @@ __global__ void __launch_bounds__(kVerThreads, 4) __cluster_dims__(kVerCtas, 1, 
   const float *e = a.noise + b * a.noise_stride;
   uint64_t best = 0;
   // a draft without probabilities gave its token all of them: p without that token
-  if (kept < n) best = cluster_best(race(p, q, e, a.vocab, q ? -1 : static_cast<int64_t>(ids[kept]), rank), own, all[0], rank);
+  if (kept < n) best = cluster_best<kCtas>(race<T, kCtas>(p, q, e, a.vocab, q ? -1 : static_cast<int64_t>(ids[kept]), rank), own, all[0], rank);
   if (best == 0)  // nothing was refused, or p - q is nowhere positive
-    best = cluster_best(race<T>(p, nullptr, e, a.vocab, -1, rank), own, all[1], rank);
+    best = cluster_best<kCtas>(race<T, kCtas>(p, nullptr, e, a.vocab, -1, rank), own, all[1], rank);
   if (rank != 0) return;
   const int drawn = best ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
   for (int i = threadIdx.x; i <= k; i += kVerThreads)
@@ -173,12 +184,18 @@ __global__ void __launch_bounds__(kVerThreads, 4) __cluster_dims__(kVerCtas, 1, 
   if (threadIdx.x == 0) a.accepted[b] = kept;
 }
 
+template <class T>
+cudaError_t launch_verify_of(const VerifyArgs &a, cudaStream_t s) {
+  const unsigned n = static_cast<unsigned>(a.nreq);
+  return launch_early(verify_kernel<T, 8>, 8, n, kVerThreads, 0, s, a);
+}
+
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(a.nreq * kVerCtas);
-  return launch_early(a.type == MMQ_DT_F32 ? verify_kernel<float> : a.type == MMQ_DT_F16 ? verify_kernel<__half> : verify_kernel<__nv_bfloat16>,
-                      grid, 1, kVerThreads, 0, s, a);
+  // Eight CTAs a request
+  if (a.type == MMQ_DT_F32) return launch_verify_of<float>(a, s);
+  return a.type == MMQ_DT_F16 ? launch_verify_of<__half>(a, s) : launch_verify_of<__nv_bfloat16>(a, s);
 }
 
 }  // namespace mmq
