@@ -264,11 +264,10 @@ struct AttnSchedule {
   // This CTA's next unit, or piece of one; false when there are no more.
   __device__ __forceinline__ bool next(const AttnArgs &a, AttnUnit &o) {
     while (b < a.nreq) {
-      const int unit = room_of(a, cur, qt);
-      const int first = pos + kGap, end = pos + unit;  // where its tiles lie
-      if (first >= hi) break;
       int t0, t1;
       tiles_of(a, cur, qt, t0, t1);
+      const int unit = kGap + max(1, t1 - t0), first = pos + kGap, end = pos + unit;  // where its tiles lie
+      if (first >= hi) break;
       o = {cur.q0, cur.n, cur.len, b, head, qt * (kRows ? kRows : a.unit_tok * a.rep), t0, t1, -1};
       step(a, unit);
       if (!split) {

@@ -24,8 +24,8 @@ namespace {
 
 constexpr int kKt = 128;        // keys of a tile
 constexpr int kThreads = 384;   // softmax warps 0-3 (tile 0) and 4-7 (tile 1), control warps 8-11
-constexpr int kUmmaWarp = 8, kLoadWarp = 10, kTailWarp = 11;  // UMMA warp of lane t: 8 + t
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 216, kRegsControl = 72;
+constexpr int kUmmaWarp = 8, kLoadWarp = 10;  // UMMA warp of lane t: 8 + t; 10: K, 11: V
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsControl = 88;
 static_assert(256 * kRegsSoftmax + 128 * kRegsControl == kThreads * kRegsLaunch,
               "the register split must add up to what the launch holds");
 constexpr int kUnits = 2;       // units handed out ahead
@@ -205,14 +205,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(u_full(i), 1);
-      mbar_init(u_empty(i), 11);  // the UMMA warps, the tail warp and eight softmax warps
+      mbar_init(u_empty(i), 11);  // the UMMA warps, the V warp and eight softmax warps
     }
     mbar_init(stats_full, 4);
     mbar_init(stats_empty, 4);
     mbar_init(done, 2);
     fence_mbar_init();
   }
-  if (warp == kTailWarp && lane < 3) {
+  if (warp == kLoadWarp + 1 && lane < 3) {
     const CUtensorMap *m = lane == 0 ? &um.q : lane == 1 ? &um.k : &um.v;
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
   }
@@ -247,105 +247,100 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    if (warp == kLoadWarp) {
-      // ---------------------------------------------------------- loads, and the units' order
-      const int boxes = kKt / box;  // of a key tile, each `box` keys of one page
-      uint32_t ks = 0, nu = 0, nq = 0;
-      uint32_t tails = 0;           // stages whose last load was a tail
+    if (warp >= kLoadWarp) {
+      // ---------------------------------------------------------- loads: one warp K, and the units' order; one Q and V
+      // (a warp issues a copy every 69 clocks whatever its size, and a tile of
+      // 16-token pages is 16 copies of 2 KB)
+      const int kv = warp - kLoadWarp;
+      const int boxes = kKt / box;                                // of a key tile, each `box` keys of one page
+      const int mine = lane / L::kHalves, h = lane % L::kHalves;  // (boxes * halves <= 32)
+      const CUtensorMap *map = kv ? &um.v : &um.k;
+      uint32_t ks = kv, nu = 0, nq = 0;  // ks: this warp's next load of the ring
+      uint32_t tails = 0, phase = 0;     // stages whose last load went to tail(), and its phases
       bool ok = true;
-      for (; ok; ++nu) {
-        if (nu && !sched.next(a, un)) un.n = 0;
-        const bool more = un.n > 0;
-        const int e = nu % kUnits;
-        ok = wait(u_empty(e), ((nu / kUnits) & 1) ^ 1);
-        if (!ok) break;
-        if (lane == 0) {
-          units[e] = un;
-          mbar_arrive(u_full(e));
+      for (;; ++nu) {
+        if (kv == 0) {
+          if (nu && !sched.next(a, un)) un.n = 0;
+          const int e = nu % kUnits;
+          ok = wait(u_empty(e), ((nu / kUnits) & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) {
+            units[e] = un;
+            mbar_arrive(u_full(e));
+          }
+          if (un.n == 0) break;
+        } else if (!take_unit(nu, un, ok)) {
+          break;
         }
-        if (!more) break;
         if (un.t_begin == un.t_end) continue;
-        const bool two = two_tiles(un);
-        ok = wait(q_empty, (nq & 1) ^ 1);
-        if (!ok) break;
-        ++nq;
-        if (lane == 0) mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * L::kHalves * half_rows * 128);
-        __syncwarp();
-        if (lane < 2 * L::kHalves) {
-          const int t = lane / L::kHalves, h = lane % L::kHalves;
-          if (t == 0 || two)
-            tma_load4(base + L::kQ + t * L::kTile + h * 16384, &um.q, h * 64, 0, un.head, un.q0 + a.by_rep(un.row0) + t * tile_tok, q_full);
-        }
-        const int32_t *row = a.table + un.b * a.table_stride;
-        const int mine = lane / L::kHalves, h = lane % L::kHalves;  // (boxes * halves <= 32)
         // page ids are read two tiles ahead and looked at when they are used
+        const int32_t *row = a.table + un.b * a.table_stride;
         auto page_of = [&](int t) {
           const int key = t * kKt + mine * box;
           return mine < boxes && key < un.len && t < un.t_end ? row[a.by_page(key)] : 0;
         };
         int ahead[2] = {page_of(un.t_begin), page_of(un.t_begin + 1)};
-        for (int t = un.t_begin; t < un.t_end && ok; ++t) {
+        if (kv) {
+          const bool two = two_tiles(un);
+          ok = wait(q_empty, (nq & 1) ^ 1);
+          if (!ok) break;
+          ++nq;
+          if (lane == 0) mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * L::kHalves * half_rows * 128);
+          __syncwarp();
+          if (lane < 2 * L::kHalves) {
+            const int t = lane / L::kHalves, g = lane % L::kHalves;
+            if (t == 0 || two)
+              tma_load4(base + L::kQ + t * L::kTile + g * 16384, &um.q, g * 64, 0, un.head, un.q0 + a.by_rep(un.row0) + t * tile_tok, q_full);
+          }
+        }
+        for (int t = un.t_begin; t < un.t_end; ++t, ks += 2) {
           int id = ahead[0];
           ahead[0] = ahead[1];
           ahead[1] = page_of(t + 2);
           const int key = t * kKt + mine * box, off = key - a.by_page(key) * a.page_size;
+          const int keys = min(kKt, un.len - t * kKt), n = (keys + box - 1) / box;
+          const int s = ks % L::kStages;
+          ok = wait(kv_empty(s), ((ks / L::kStages) & 1) ^ 1);
+          if (!ok) break;
           if (id < 0 || id >= a.pages) {  // out of the cache: past the map's last page, zeros come
             record_index(w.status);
             id = static_cast<int>(a.pages);
           }
-          const int keys = min(kKt, un.len - t * kKt), n = (keys + box - 1) / box;
-          const bool load = mine < n;
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++ks) {
-            const int s = ks % L::kStages;
-            ok = wait(kv_empty(s), ((ks / L::kStages) & 1) ^ 1);
+          const bool last = kv == 1 && keys < kKt;  // the last keys' V
+          const uint32_t bar = last ? tail(s) : kv_full(s);
+          tails = last ? tails | 1u << s : tails & ~(1u << s);
+          if (lane == 0) mbar_arrive_expect_tx(bar, n * L::kHalves * box * 128);
+          __syncwarp();
+          if (mine < n) tma_load4(base + L::kRing + s * L::kTile + h * 16384 + mine * box * 128, map, h * 64, off, un.head, id, bar);
+          if (last) {
+            // Rows past the last key, up to the next multiple of 16 (the K of
+            // one UMMA), hold what the page holds there, or an earlier tile:
+            // zeros, so that 0 * V is 0.
+            ok = wait(bar, phase >> s & 1);
             if (!ok) break;
-            // the last keys' V goes through the tail warp
-            const bool last = kv == 1 && keys < kKt;
-            const uint32_t bar = last ? tail(s) : kv_full(s);
-            tails = last ? tails | 1u << s : tails & ~(1u << s);
-            if (lane == 0) mbar_arrive_expect_tx(bar, n * L::kHalves * box * 128);
+            phase ^= 1u << s;
+            const int zero = ((keys + 15) & ~15) - keys;
+            uint8_t *v = smem + L::kRing + s * L::kTile;
+            for (int i = lane; i < zero * 8 * L::kHalves; i += 32) {
+              const int r = keys + i / (8 * L::kHalves), c = i % (8 * L::kHalves);
+              *reinterpret_cast<uint4 *>(v + (c >> 3) * 16384 + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (load)
-              tma_load4(base + L::kRing + s * L::kTile + h * 16384 + mine * box * 128, kv ? &um.v : &um.k, h * 64, off, un.head, id, bar);
+            if (lane == 0) mbar_arrive(kv_full(s));
           }
         }
+        if (!ok) break;
       }
-      if (!ok) {  // drain this CTA's copies still in flight
+      if (!ok) {  // drain this warp's copies still in flight
         if (nq) mbar_wait(q_full, (nq - 1) & 1, w, false);
-        const uint32_t from = ks > L::kStages ? ks - L::kStages : 0;
-        for (uint32_t i = from; i < ks; ++i) {
-          const int s = i % L::kStages;
-          if (!(tails >> s & 1)) mbar_wait(kv_full(s), (i / L::kStages) & 1, w, false);
+        for (int i = 1; i <= L::kStages; ++i) {
+          const int64_t k = static_cast<int64_t>(ks) - 2 * i;
+          if (k < 0 || k + L::kStages < ks) break;
+          const int s = static_cast<int>(k % L::kStages);
+          if (!(tails >> s & 1)) mbar_wait(kv_full(s), static_cast<uint32_t>(k / L::kStages) & 1, w, false);
           else for (int spin = 0; spin < 4096 && !(mbar_try_wait(tail(s), 0) && mbar_try_wait(tail(s), 1)); ++spin) {}
         }
-      }
-    } else if (warp == kTailWarp) {
-      // ---------------------------------------------------------- the last keys' V
-      // Rows past the last key, up to the next multiple of 16 (the K of one
-      // UMMA), hold what the page holds there, or an earlier tile: zeros, so
-      // that 0 * V is 0.
-      uint32_t ks = 0, nu = 0, phase = 0;
-      bool ok = true;
-      while (take_unit(nu++, un, ok)) {
-        const int tiles = un.t_end - un.t_begin;
-        if (tiles == 0) continue;
-        const int keys = un.len - (un.t_end - 1) * kKt;
-        ks += 2 * tiles;
-        if (keys >= kKt) continue;
-        const int s = (ks - 1) % L::kStages;
-        ok = wait(tail(s), phase >> s & 1);
-        if (!ok) break;
-        phase ^= 1u << s;
-        const int zero = ((keys + 15) & ~15) - keys;
-        uint8_t *v = smem + L::kRing + s * L::kTile;
-        for (int i = lane; i < zero * 8 * L::kHalves; i += 32) {
-          const int r = keys + i / (8 * L::kHalves), c = i % (8 * L::kHalves);
-          *reinterpret_cast<uint4 *>(v + (c >> 3) * 16384 + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kv_full(s));
       }
     } else {
       // ---------------------------------------------------------- UMMAs of lane t
