@@ -261,71 +261,38 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
 // Joins the pieces of a cut unit: with lse_p (base 2) and normalised outputs
 // o_p, out = sum 2^(lse_p - top) o_p / sum 2^(lse_p - top), in fp32 and in the
 // pieces' order.  Block (c, y): rows 16 y .. of the unit that begins in CTA c;
-// sixteen threads a row for the sums, then a thread for eight columns of a
-// row, lanes along the rows (as the partial results lie).
+// a thread eight columns of a row, lanes along the rows (as the partial
+// results lie).  Latency bound where few rows are cut, else L2 bound; a
+// running maximum, so that weights and outputs are read in one round.
 constexpr int kJoinRows = 16;
 template <class T>
 __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a, int unit_rows) {
-  __shared__ float s_top[kJoinRows], s_inv[kJoinRows];
   griddep_wait();
   griddep_launch_dependents();
   const AttnCut u = a.cuts[blockIdx.x];
   const int r0 = blockIdx.y * kJoinRows, rows = min(min(unit_rows, u.n * a.rep - u.row0) - r0, kJoinRows);
   if (u.last < 0 || rows <= 0) return;
-  const int c0 = blockIdx.x, pieces = u.last - c0 + 1;
-  auto slot = [&](int p) { return static_cast<int64_t>(2 * (c0 + p) + (p == 0)); };
-  auto where = [&](int r, int &tok, int &head) {
-    const int row = u.row0 + r0 + r;
-    tok = a.by_rep(row);
-    head = u.head * a.rep + row - tok * a.rep;
-    tok += u.q0;
-  };
-  {  // sixteen threads a row
-    const int r = threadIdx.x >> 4, sub = threadIdx.x & 15;
-    const float *lse = a.part_lse + r0 + min(r, rows - 1);
-    float top = -INFINITY, bad = 0.0f, sum = 0.0f;
-    for (int p = sub; p < pieces; p += 16) {
-      const float x = lse[slot(p) * unit_rows], high = fmaxf(top, x);
-      if (x != x) bad = x;
-      if (x == -INFINITY) continue;
-      sum = sum * (top == -INFINITY ? 0.0f : exp2f(top - high)) + exp2f(x - high);
-      top = high;
-    }
-#pragma unroll
-    for (int d = 8; d; d >>= 1) {
-      const float other = __shfl_xor_sync(0xffffffffu, top, d), more = __shfl_xor_sync(0xffffffffu, sum, d);
-      const float high = fmaxf(top, other);
-      sum = high == -INFINITY ? 0.0f : sum * exp2f(top - high) + more * exp2f(other - high);
-      top = high;
-      bad += __shfl_xor_sync(0xffffffffu, bad, d);
-    }
-    if (sub == 0 && r < rows) {
-      s_top[r] = top;
-      s_inv[r] = (sum > 0.0f ? 1.0f / sum : 0.0f) + bad;
-      int tok, head;
-      where(r, tok, head);
-      if (a.lse) a.lse[static_cast<int64_t>(tok) * a.hq + head] = (sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY) + bad;
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kJoinRows * (a.d / 8); i += 256) {
-    const int c = i / kJoinRows, r = i % kJoinRows;
-    if (r >= rows) continue;
-    const float top = s_top[r], inv = s_inv[r];
+  const int c0 = blockIdx.x, pieces = u.last - c0 + 1, r = threadIdx.x % kJoinRows;
+  if (r >= rows) return;
+  const int row = u.row0 + r0 + r, rtok = a.by_rep(row), head = u.head * a.rep + row - rtok * a.rep;
+  const int64_t tok = u.q0 + rtok;
+  for (int c = threadIdx.x / kJoinRows; c < a.d / 8; c += 256 / kJoinRows) {
+    float top = -INFINITY, sum = 0.0f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
 #pragma unroll 4
     for (int p = 0; p < pieces; ++p) {
-      const int64_t s = slot(p);
+      const int64_t s = 2 * (c0 + p) + (p == 0);
       const float l = a.part_lse[s * unit_rows + r0 + r];
       const float4 *src = a.part_o + (s * (a.d / 4) + 2 * c) * unit_rows + r0 + r;
       const float4 f = __ldcs(src), g = __ldcs(src + unit_rows);
       if (l == -INFINITY) continue;
-      const float w = exp2f(l - top);
-      x.x = fmaf(w, f.x, x.x), x.y = fmaf(w, f.y, x.y), x.z = fmaf(w, f.z, x.z), x.w = fmaf(w, f.w, x.w);
-      y.x = fmaf(w, g.x, y.x), y.y = fmaf(w, g.y, y.y), y.z = fmaf(w, g.z, y.z), y.w = fmaf(w, g.w, y.w);
+      const float high = fmaxf(top, l), keep = top == -INFINITY ? 0.0f : exp2f(top - high), w = exp2f(l - high);
+      top = high;
+      sum = fmaf(sum, keep, w);
+      x.x = fmaf(x.x, keep, w * f.x), x.y = fmaf(x.y, keep, w * f.y), x.z = fmaf(x.z, keep, w * f.z), x.w = fmaf(x.w, keep, w * f.w);
+      y.x = fmaf(y.x, keep, w * g.x), y.y = fmaf(y.y, keep, w * g.y), y.z = fmaf(y.z, keep, w * g.z), y.w = fmaf(y.w, keep, w * g.w);
     }
-    int tok, head;
-    where(r, tok, head);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int64_t to = tok * a.out_token + head * a.out_head + 8 * c;
     if (a.out_type == MMQ_DT_F32) {
       float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to);
@@ -339,6 +306,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
       z.w = Pair<T>::pack(y.z * inv, y.w * inv);
       *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + to) = z;
     }
+    if (c == 0 && a.lse) a.lse[tok * a.hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
   }
 }
 

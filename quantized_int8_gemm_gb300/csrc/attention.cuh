@@ -107,7 +107,7 @@ __device__ __forceinline__ void attn_row_range(const AttnArgs &a, int n, int len
   lo = a.window ? max(0, pos - a.window + 1) : 0;
 }
 
-constexpr int kAttnGap = 2;
+constexpr int kAttnGap = 3;
 
 // Deals the units out; every lane of one warp calls each function.  kRows: of
 // a unit, or 0 where units are whole tokens (AttnArgs::unit_tok).
