@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -145,7 +146,7 @@ struct CallStream {
 };
 
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, int dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+  return at::detail::empty_cuda(shape, type, c10::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
 }
 
 int64_t number(PyObject *o, const char *name) {
