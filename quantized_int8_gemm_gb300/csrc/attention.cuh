@@ -76,10 +76,13 @@ struct AttnRequest {
   int tiles;  // row tiles
 };
 
+struct AttnLengths {
+  int from, to, len;
+};
 template <int kRows>
-__device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, int b) {
+__device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, const AttnLengths &x) {
   AttnRequest r;
-  const int ntok = static_cast<int>(a.ntok), from = a.q_start[b], to = a.q_start[b + 1], len = a.seq_lens[b];
+  const int ntok = static_cast<int>(a.ntok), from = x.from, to = x.to, len = x.len;
   r.q0 = max(0, min(from, ntok));
   r.n = max(r.q0, min(to, ntok)) - r.q0;
   // (a tile's keys are counted past the last one)
@@ -146,11 +149,15 @@ struct AttnSchedule {
     return {__shfl_sync(0xffffffffu, r.q0, l), __shfl_sync(0xffffffffu, r.n, l), __shfl_sync(0xffffffffu, r.len, l),
             __shfl_sync(0xffffffffu, r.tiles, l)};
   }
+  __device__ static __forceinline__ AttnLengths lengths(const AttnArgs &a, int from) {
+    const int at = from + static_cast<int>(threadIdx.x & 31);
+    AttnLengths x{0, 0, 0};
+    if (from >= 0 && at < a.nreq) x = {a.q_start[at], a.q_start[at + 1], a.seq_lens[at]};
+    return x;
+  }
   __device__ __forceinline__ void load(const AttnArgs &a, int from) {
     b0 = from;
-    const int at = b0 + (threadIdx.x & 31);
-    r = AttnRequest{0, 0, 0, 0};
-    if (at < a.nreq) r = attn_request<kRows>(a, at);
+    r = attn_request<kRows>(a, lengths(a, from));
   }
   __device__ static __forceinline__ int inclusive(int x) {
 #pragma unroll
@@ -191,19 +198,22 @@ struct AttnSchedule {
     cut = false;
     const int lane = threadIdx.x & 31;
     int total = 0, mine = 0, longest = 0;
+    AttnLengths ahead = lengths(a, (a.nreq - 1) / 32 * 32);
 #pragma unroll 1
-    for (int from = (a.nreq - 1) / 32 * 32; from >= 0; from -= 32) {  // (ends with the first 32 at hand)
-      load(a, from);
+    for (b0 = (a.nreq - 1) / 32 * 32;; b0 -= 32) {  // (ends with the first 32 at hand)
+      const AttnLengths now = ahead;
+      ahead = lengths(a, b0 - 32);
+      r = attn_request<kRows>(a, now);
       mine = lane_room(a, longest);
       total += mine;
+      if (b0 == 0) break;
     }
     total = __reduce_add_sync(0xffffffffu, total);
     longest = __reduce_max_sync(0xffffffffu, longest);
     each = max(a.by_grid(total + static_cast<int>(gridDim.x) - 1), kLeast);
     // Whole units cost half the longest in balance, pieces their partial
-    // results and the join (about four tiles' time, eight with two row tiles).
-    const int join = __any_sync(0xffffffffu, r.n > a.unit_tok / 2) ? 8 : 4;
-    split = a.part_o && max(longest, each + longest / 2) > each + join;
+    // results and the join (about four tiles' time).
+    split = a.part_o && max(longest, each + longest / 2) > each + 4;
     lo = each * static_cast<int>(blockIdx.x);
     hi = lo + each;
     pos = 0;
@@ -223,16 +233,19 @@ struct AttnSchedule {
     pos += __shfl_sync(0xffffffffu, end - mine, l);
     b = b0 + l;
     cur = lane_request(l);
-    for (qt = 0;; qt += 32) {  // (the request reaches past lo, so one of its row tiles does)
+    qt = 0;
+    for (; cur.tiles > 1; qt += 32) {  // (the request reaches past lo, so one of its row tiles does)
       mine = qt + lane < cur.tiles ? room_of(a, cur, qt + lane) * a.hkv : 0;
       end = inclusive(mine);
       past = __ballot_sync(0xffffffffu, mine && pos + end > lo);
       if (past || qt + 32 >= cur.tiles) break;
       pos += __shfl_sync(0xffffffffu, end, 31);
     }
-    l = past ? __ffs(past) - 1 : 0;
-    pos += __shfl_sync(0xffffffffu, end - mine, l);
-    qt += l;
+    if (cur.tiles > 1) {
+      l = past ? __ffs(past) - 1 : 0;
+      pos += __shfl_sync(0xffffffffu, end - mine, l);
+      qt += l;
+    }
     const int unit = room_of(a, cur, qt);
     head = lo > pos ? (lo - pos) / unit : 0;
     pos += head * unit;
