@@ -46,10 +46,10 @@ struct Lay {
   static constexpr int kRing = 2 * kTile;
   static constexpr int kBars = kRing + kStages * kTile;
   static constexpr int kNumBars = 3 * kStages + 2 + 18 + 2 * kUnits + 1;
-  static constexpr int kStats = kBars + kNumBars * 8;  // lane 1's maximum and sum of each row
-  static constexpr int kUnitsAt = kStats + 128 * 8;
+  static constexpr int kStats = kBars + kNumBars * 8;  // [lane][row] maximum and sum
+  static constexpr int kUnitsAt = kStats + 2 * 128 * 8;
   static constexpr int kSlot = kUnitsAt + kUnits * static_cast<int>(sizeof(AttnUnit));
-  static constexpr int kBytes = kSlot + 16 + 1024;  // the base is rounded up to 1024
+  static constexpr int kBytes = kSlot + 16;
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -158,9 +158,8 @@ template <class T, int kDp>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_umma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnUmma um) {
   using L = Lay<kDp>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
-  uint8_t *smem = smem_raw + (base - raw);
+  extern __shared__ __align__(1024) uint8_t smem[];  // (swizzle groups are 1024 bytes)
+  const uint32_t base = smem_addr(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bars = base + L::kBars;
   auto kv_full = [&](int s) { return bars + 8u * s; };
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(p_full(t, 0), 4);
       mbar_init(p_full(t, 1), 4);
       mbar_init(o_full(t), 1);
-      mbar_init(o_empty(t), 4);
+      mbar_init(o_empty(t), 8);
       mbar_init(turn(t), 1);
       mbar_init(s_empty(t), 4);
       mbar_init(p_empty(t), 1);
@@ -207,8 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(u_full(i), 1);
       mbar_init(u_empty(i), 11);  // the UMMA warps, the V warp and eight softmax warps
     }
-    mbar_init(stats_full, 4);
-    mbar_init(stats_empty, 4);
+    mbar_init(stats_full, 8);
+    mbar_init(stats_empty, 8);
     mbar_init(done, 2);
     fence_mbar_init();
   }
@@ -468,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, quad = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t ts = tmem + lanes + 128 * t, tp = tmem + lanes + L::kP + L::kPStep * t;
-    const uint32_t to = tmem + lanes + L::kO + kDp * t, to1 = tmem + lanes + L::kO + kDp;
+    const uint32_t to = tmem + lanes + L::kO + kDp * t, other_o = tmem + lanes + L::kO + kDp * (t ^ 1);
     const float sc = a.scale_log2;
     uint32_t nu = 0, ns = 0, no[2] = {0, 0}, nx = 0;
     bool ok = true;
@@ -667,39 +666,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      // ---- the rows' results: of lane t, or of both lanes by lane 0's warps
+      // ---- the rows' results: of lane t, or of both lanes together, where the
+      // warps of each lane write half the columns
       const bool both = !two && tiles > 1;
-      if (!two && t == 1) {
-        if (both) {
-          ++no[0];
-          ++no[1];
-          ok = wait(stats_empty, (nx++ & 1) ^ 1);
-          if (!ok) break;
-          stats[r] = make_float2(m, l);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(stats_full);
-        } else if (tiles) {
-          ++no[0];
-        }
+      if (!two && !both && t == 1) {  // nothing of this unit came here
+        if (tiles) ++no[0];
         continue;
       }
-      float f0 = 1.0f, f1 = 0.0f;
+      float f0 = 1.0f, f1 = 0.0f;  // of O_t and of the other lane's
       if (tiles) {
+        if (both) {
+          ok = wait(stats_empty, (nx & 1) ^ 1);
+          if (!ok) break;
+          stats[128 * t + r] = make_float2(m, l);
+          __syncwarp();
+          mbar_arrive_if(lane == 0, stats_full);
+          ok = wait(stats_full, nx++ & 1) && wait(o_full(t ^ 1), no[t ^ 1] & 1);
+          if (!ok) break;
+        }
         ok = wait(o_full(t), no[t] & 1);
-        if (ok && both) ok = wait(o_full(1), no[1] & 1) && wait(stats_full, nx++ & 1);
         if (!ok) break;
         tc_fence_after();
         ++no[0];
         if (two || both) ++no[1];
         if (both) {
-          const float2 x = stats[r];
+          const float2 x = stats[128 * (t ^ 1) + r];
           __syncwarp();
-          if (lane == 0) mbar_arrive(stats_empty);
+          mbar_arrive_if(lane == 0, stats_empty);
           const float top = fmaxf(m, x.x), off = top == -INFINITY ? 0.0f : top;
           f0 = exp2_fast((m - off) * sc);
           f1 = exp2_fast((x.x - off) * sc);
           m = top;
-          l = l * f0 + x.y * f1;
+          l = __fadd_rn(__fmul_rn(l, f0), __fmul_rn(x.y, f1));  // (the same number in both lanes)
         }
       }
       const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // (NaN stays)
@@ -717,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 16 columns a turn of a short loop: run once a unit, straight code
         // costs about five clocks an instruction, waiting to be fetched.
 #pragma unroll 1
-        for (int c = 0; c < a.d; c += 16) {
+        for (int c = both ? kDp / 2 * t : 0; c < (both && t == 0 ? min(a.d, kDp / 2) : a.d); c += 16) {
           uint32_t y[16];
           if (tiles == 0) {
 #pragma unroll
@@ -728,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f0);
             if (both) {
               uint32_t z[16];
-              tmem_ld_x16(to1 + c, z);
+              tmem_ld_x16(other_o + c, z);
 #pragma unroll
               for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(fmaf(__uint_as_float(z[i]), f1, __uint_as_float(y[i])));
             }
@@ -771,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (valid) {
+        if (valid && !(both && t)) {
           const float lse2 = l > 0.0f ? fmaf(m, sc, log2f(l)) : l == 0.0f ? -INFINITY : l;
           if (cut) a.part_lse[un.slot * (2 * half_rows) + row - un.row0] = lse2;
           else if (a.lse) a.lse[at] = lse2 * kLn2;
@@ -780,8 +778,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tiles) {
         tc_fence_before();
         __syncwarp();
+        // eight arrivals a lane's O: both lanes' warps once, or its own twice
         mbar_arrive_if(lane == 0, o_empty(t));
-        mbar_arrive_if(lane == 0 && both, o_empty(1));
+        mbar_arrive_if(lane == 0, o_empty(both ? t ^ 1 : t));
       }
     }
   }
