@@ -480,6 +480,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       int lo, hi;
       attn_row_range(a, un.n, un.len, tok, lo, hi);
       float m = -INFINITY, l = 0.0f;
+      // 64 weights and their sums.  Eight at a time, the exponentials of one
+      // group beside the sums and conversions of the one before: exp2 keeps its
+      // unit busy for 4 clocks a warp, the packed FMA, the add and the
+      // conversion two each.  The one rounding is to the type of V (a UMMA's
+      // operands have one type).
+      auto weights = [](const uint32_t (&x)[64], uint32_t (&p)[32], uint64_t sc2, uint64_t off2, uint64_t (&sum)[2]) {
+        float e[2][8];
+#pragma unroll
+        for (int g = 0; g <= 8; ++g)
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            float *now = e[g & 1] + i, *old = e[(g & 1) ^ 1] + i;
+            if (g < 8) {
+              parts_of(fma2(pair_of(__uint_as_float(x[8 * g + i]), __uint_as_float(x[8 * g + i + 1])), sc2, off2), now[0], now[1]);
+              now[0] = exp2_fast(now[0]);
+            }
+            if (g > 0) sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pair_of(old[0], old[1]));
+            if (g < 8) now[1] = exp2_fast(now[1]);
+            if (g > 0) p[4 * (g - 1) + i / 2] = pack(old[0], old[1], T());
+          }
+      };
       // The maximum is only a guard against overflow: any m gives the same
       // quotient.  It moves when it would lag by more than 2^8, so that O in
       // TMEM is rescaled a few times a row and not in every tile; the weights
@@ -551,24 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t p[32];
-              // Eight at a time, the exponentials of one group beside the sums and
-              // conversions of the one before: exp2 keeps its unit busy for 4
-              // clocks a warp, the packed FMA, the add and the conversion two each.
-              float e[2][8];
-#pragma unroll
-              for (int g = 0; g <= 8; ++g)
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                  float *now = e[g & 1] + i, *old = e[(g & 1) ^ 1] + i;
-                  if (g < 8) {
-                    const int c = 8 * g + i;
-                    parts_of(fma2(pair_of(__uint_as_float(x[h][c]), __uint_as_float(x[h][c + 1])), sc2, off2), now[0], now[1]);
-                    now[0] = exp2_fast(now[0]);
-                  }
-                  if (g > 0) sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pair_of(old[0], old[1]));
-                  if (g < 8) now[1] = exp2_fast(now[1]);
-                  if (g > 0) p[4 * (g - 1) + i / 2] = pack(old[0], old[1], T());  // one rounding, to the type of V: the UMMA's operands have one type
-                }
+              weights(x[h], p, sc2, off2, sum);
               tmem_st_32x32b_x32(tp + 32 * h, p);
               tmem_wait_st();
               tc_fence_before();
@@ -614,38 +618,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float off = m == -INFINITY ? 0.0f : -m * sc;
             const uint64_t sc2 = pair_of(sc, sc), off2 = pair_of(off, off);
             uint64_t sum[2] = {0, 0};
-            // Then the weights, 32 columns at a time; eight at a time the
-            // exponentials of one group beside the sums and conversions of the one
-            // before: exp2 keeps its unit busy for 4 clocks a warp, the packed
-            // FMA, the add and the conversion two each.
-            auto weights = [&](uint32_t (&x)[32], int c) {
-              float e[2][8];
-              uint32_t p[16];
-#pragma unroll
-              for (int g = 0; g <= 4; ++g)
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                  float *now = e[g & 1] + i, *old = e[(g & 1) ^ 1] + i;
-                  if (g < 4) {
-                    parts_of(fma2(pair_of(__uint_as_float(x[8 * g + i]), __uint_as_float(x[8 * g + i + 1])), sc2, off2), now[0], now[1]);
-                    now[0] = exp2_fast(now[0]);
-                  }
-                  if (g > 0) sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pair_of(old[0], old[1]));
-                  if (g < 4) now[1] = exp2_fast(now[1]);
-                  if (g > 0) p[4 * (g - 1) + i / 2] = pack(old[0], old[1], T());  // one rounding, to the type of V: the UMMA's operands have one type
-                }
-              tmem_st_x16(tp + c / 2, p);  // (over S: behind what has been read)
-            };
-            uint32_t x0[32], x1[32];
-            tmem_ld_32x32b_x32(ts, x0);
+            // Then the weights, 64 columns at a time (over S: behind what has been read).
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-              tmem_wait_ld(x0);
-              tmem_ld_32x32b_x32(ts + 64 * h + 32, x1);
-              weights(x0, 64 * h);
-              tmem_wait_ld(x1);
-              if (h == 0) tmem_ld_32x32b_x32(ts + 64, x0);
-              weights(x1, 64 * h + 32);
+              uint32_t x[64], p[32];
+              tmem_ld_32x32b_x64(ts + 64 * h, x);
+              tmem_wait_ld(x);
+              weights(x, p, sc2, off2, sum);
+              tmem_st_32x32b_x32(tp + 32 * h, p);
               tmem_wait_st();
               tc_fence_before();
               __syncwarp();
