@@ -30,22 +30,6 @@ struct AttnCut {
   int last;  // -1: no unit of CTA c is cut behind it
 };
 
-// Division of 0 <= n < 2^31 by a number the host knows: with l = ceil(log2 d)
-// and m = ceil(2^(31 + l) / d), n m / 2^(31 + l) exceeds n / d by less than 1 / d.
-struct FastDiv {
-  uint32_t m = 0, shift = 0;
-  FastDiv() = default;
-  explicit FastDiv(uint32_t d) {
-    uint32_t l = 0;
-    while ((uint64_t(1) << l) < d) ++l;
-    shift = 31 + l;
-    m = static_cast<uint32_t>(((uint64_t(1) << shift) + d - 1) / d);
-  }
-  __device__ __forceinline__ int operator()(int n) const {
-    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * m >> shift);
-  }
-};
-
 struct AttnArgs {
   const void *q, *k, *v;
   void *out;

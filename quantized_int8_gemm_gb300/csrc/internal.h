@@ -118,6 +118,22 @@ cudaError_t launch_early(void (*kernel)(Params...), unsigned grid_x, unsigned gr
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Division of 0 <= n < 2^31 by a number the host knows: with l = ceil(log2 d)
+// and m = ceil(2^(31 + l) / d), n m / 2^(31 + l) exceeds n / d by less than 1 / d.
+struct FastDiv {
+  uint32_t m = 0, shift = 0;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) {
+    uint32_t l = 0;
+    while ((uint64_t(1) << l) < d) ++l;
+    shift = 31 + l;
+    m = static_cast<uint32_t>(((uint64_t(1) << shift) + d - 1) / d);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * m >> shift);
+  }
+};
+
 // ---- paged cache and serving step (paged.cu, verify.cu, attention*.cu) ----
 constexpr int64_t kMaxRequests = 8192;  // their sums stay in shared memory
 
@@ -140,6 +156,7 @@ struct KvWriteArgs {
   const int64_t *slots;
   int64_t ntok;
   int32_t heads, head_dim, src_type, tokens_per_cta;
+  FastDiv by_items, by_chunks, by_page;  // items of a token, 8-element chunks of a row, page_size
   int *status;
 };
 cudaError_t launch_kv_write(KvWriteArgs a, cudaStream_t s);

@@ -226,9 +226,9 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_co
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_cta;
   const int items = static_cast<int>(min(static_cast<int64_t>(a.tokens_per_cta), a.ntok - t0)) * per_tok;
   for (int i = threadIdx.x; i < items; i += kWriteThreads) {
-    const int tl = i / per_tok, r = i - tl * per_tok;
+    const int tl = a.by_items(i), r = i - tl * per_tok;
     const bool is_v = r >= per_tensor;
-    const int c = is_v ? r - per_tensor : r, head = c / chunks, col = (c - head * chunks) << 3;
+    const int c = is_v ? r - per_tensor : r, head = a.by_chunks(c), col = (c - head * chunks) << 3;
     const int64_t t = t0 + tl, slot = a.slots[t];
     float x[8];
     load8<S>(is_v ? a.v : a.k, is_v ? t * a.v_token + head * a.v_head + col : t * a.k_token + head * a.k_head + col, x);
@@ -238,9 +238,8 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_co
       continue;
     }
     int64_t page, row;
-    if (slot < 0x7fffffff) {  // (a division in 32 bits where the slot allows)
-      const uint32_t q = static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.cache.page_size);
-      page = q, row = static_cast<uint32_t>(slot) - q * static_cast<uint32_t>(a.cache.page_size);
+    if (slot <= 0x7fffffff) {
+      page = a.by_page(static_cast<int>(slot)), row = static_cast<int>(slot) - static_cast<int>(page) * a.cache.page_size;
     } else {
       page = slot / a.cache.page_size, row = slot - page * a.cache.page_size;
     }
@@ -277,6 +276,7 @@ cudaError_t launch_kv_write(KvWriteArgs a, cudaStream_t s) {
   const int per_tok = 2 * a.heads * (a.head_dim >> 3);
   const bool many = a.ntok * per_tok >= static_cast<int64_t>(2 * kWriteThreads) * 152;
   a.tokens_per_cta = std::max(1, (many ? 2 : 1) * kWriteThreads / per_tok);
+  a.by_items = FastDiv(per_tok), a.by_chunks = FastDiv(a.head_dim >> 3), a.by_page = FastDiv(a.cache.page_size);
   const int64_t grid = (a.ntok + a.tokens_per_cta - 1) / a.tokens_per_cta;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   if (a.src_type == MMQ_DT_F32) return launch_kv_write_from<float>(a, static_cast<unsigned>(grid), s);
