@@ -80,7 +80,12 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
 // last key, so that what unwritten memory holds never meets the tensor core).
 // S and P stay in registers; the running maximum, sum and the output are
 // fp32, P is rounded to the cache's type for the second product.  It serves
-// the shapes the tcgen05 kernel does not take.
+// the shapes the tcgen05 kernel does not take: heads wider than 128, pages
+// without eight keys in a row, groups of more than 128 query heads.  Bound by
+// the latency of one warp's products where few rows are at work (16 q heads
+// over 4 K/V heads of 256, 32 tokens over 4001 keys: 137 us, 3.8 TB/s) and by
+// the warp-level tensor rate beside the softmax in chunks (512 tokens over 4608
+// keys: 146 us, 250 TFLOP/s).
 template <class T, int kDp>
 __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -112,31 +117,36 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
     for (int i = tid; i < kRows * kChunks; i += kThreads) {
       const int r = i / kChunks, c = i % kChunks, row = un.row0 + r;
       const bool in = row < all_rows && c * 8 < a.d;
-      const int tok = row / a.rep;
+      const int tok = a.by_rep(row);
       const T *src = in ? q + (un.q0 + tok) * a.q_token + (un.head * a.rep + row - tok * a.rep) * a.q_head + c * 8 : q;
       cp_async16(sq + tile_at<kDp>(r, c), src, in ? 16 : 0);
     }
+    // A warp copies 16 keys of a tile: 16 lanes look their keys' rows up, then
+    // each copy takes its row's place from its lane.
     auto load = [&](int t, int buf) {
-      const int32_t *row = a.table + un.b * a.table_stride;
-      for (int i = tid; i < kKt * kChunks; i += kThreads) {
-        const int r = i / kChunks, c = i % kChunks, key = t * kKt + r;
-        bool in = key < un.len && c * 8 < a.d;
-        int64_t page = 0;
-        int off = 0;
-        if (in) {
-          const int blk = a.by_page(key);
-          page = row[blk];
-          off = key - blk * a.page_size;
-          if (page < 0 || page >= a.pages) {
-            record_index(a.wait.status);
-            in = false;
-          }
+      const int key = t * kKt + warp * 16 + (lane & 15);
+      int64_t k_at = -1, v_at = -1;
+      if (key < un.len) {
+        const int blk = a.by_page(key), off = key - blk * a.page_size;
+        const int64_t page = a.table[un.b * a.table_stride + blk];
+        if (page >= 0 && page < a.pages) {
+          k_at = page * a.k_page + off * a.k_token + un.head * a.k_head;
+          v_at = page * a.v_page + off * a.v_token + un.head * a.v_head;
+        } else {
+          record_index(a.wait.status);
         }
-        const T *k = static_cast<const T *>(a.k), *v = static_cast<const T *>(a.v);
-        cp_async16(sk + buf * kTile + tile_at<kDp>(r, c),
-                   in ? k + page * a.k_page + off * a.k_token + un.head * a.k_head + c * 8 : k, in ? 16 : 0);
-        cp_async16(sv + buf * kTile + tile_at<kDp>(r, c),
-                   in ? v + page * a.v_page + off * a.v_token + un.head * a.v_head + c * 8 : v, in ? 16 : 0);
+      }
+      constexpr int kRowsAtOnce = 32 / kChunks;
+      const int c = lane % kChunks;
+      const T *k = static_cast<const T *>(a.k) + c * 8, *v = static_cast<const T *>(a.v) + c * 8;
+#pragma unroll
+      for (int i = 0; i < 16; i += kRowsAtOnce) {
+        const int at = i + lane / kChunks;
+        const int64_t ko = __shfl_sync(0xffffffffu, k_at, at), vo = __shfl_sync(0xffffffffu, v_at, at);
+        const bool in = ko >= 0 && c * 8 < a.d;
+        const uint32_t to = buf * kTile + tile_at<kDp>(warp * 16 + at, c);
+        cp_async16(sk + to, in ? k + ko : a.k, in ? 16 : 0);
+        cp_async16(sv + to, in ? v + vo : a.v, in ? 16 : 0);
       }
     };
     if (un.t_begin < un.t_end) load(un.t_begin, 0);
@@ -148,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     int lo[2], hi[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) attn_row_range(a, un.n, un.len, (un.row0 + warp * 16 + (lane >> 2) + 8 * h) / a.rep, lo[h], hi[h]);
+    for (int h = 0; h < 2; ++h) attn_row_range(a, un.n, un.len, a.by_rep(un.row0 + warp * 16 + (lane >> 2) + 8 * h), lo[h], hi[h]);
 
     for (int t = un.t_begin; t < un.t_end; ++t) {
       const int buf = (t - un.t_begin) & 1;
@@ -228,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       const int row = un.row0 + warp * 16 + (lane >> 2) + 8 * h;
       if (row >= all_rows) continue;
-      const int tok = row / a.rep, head = un.head * a.rep + row - tok * a.rep;
+      const int tok = a.by_rep(row), head = un.head * a.rep + row - tok * a.rep;
       const int64_t at = static_cast<int64_t>(un.q0 + tok) * a.hq + head;
       const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // (NaN stays)
       const float lse2 = sum > 0.0f ? fmaf(m[h], a.scale_log2, log2f(sum)) : sum == 0.0f ? -INFINITY : sum;
@@ -351,12 +361,15 @@ cudaError_t launch_attention(const mmq_paged_cache &c, const mmq_attention &t, c
   a.scale_log2 = t.scale * 1.44269504088896341f;
   a.wait = {&ctx.words->status, &ctx.words->abort_epoch, ctx.epoch, ctx.limit_ns};
 
-  // The tcgen05 kernel (one CTA an SM) takes every shape it can; the general
-  // one (two CTAs an SM) the rest.
+  // The tcgen05 kernel (one CTA an SM) takes every shape it can, the general
+  // one (two CTAs an SM, one with heads wider than 128) the rest: 32 rows of one
+  // token over 4001 keys, 4 K/V heads of 128, take 54 us in the first (pages of 8
+  // or 16 keys) and 70 us in the second (pages of 5), 512 tokens over 4608 keys
+  // 28 and 74 us.
   AttnUmma um;
   const bool umma = attention_umma(a, c.type, &um);
   const int unit_rows = umma ? 2 * um.tile_tok * a.rep : kRows, kt = umma ? 128 : kKt;
-  const unsigned grid = umma ? kSms : 2 * kSms;
+  const unsigned grid = umma || a.d > 128 ? kSms : 2 * kSms;
   a.unit_tok = umma ? 2 * um.tile_tok : 0;
   a.by_page = FastDiv(c.page_size), a.by_rep = FastDiv(a.rep), a.by_grid = FastDiv(grid);
   a.by_unit_tok = FastDiv(umma ? a.unit_tok : 1);

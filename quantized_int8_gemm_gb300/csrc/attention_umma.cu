@@ -10,6 +10,25 @@
 // lane's products.  With two row tiles lane t is row tile t and sees every key
 // tile.  With one (decode steps, short chunks) both lanes are that tile: lane t
 // takes every second key tile, and their results are joined at the end.
+//
+// What bounds it (one GB300, calls back to back):
+//   long chunks  (4096 tokens over 32097 keys, 28 heads on 4, d 128: 1.10 ms,
+//       1.6 PFLOP/s) the chain of one lane, softmax about 1.7 thousand clocks,
+//       P V and Q K^T 0.5 each and the hand-offs: a key tile of both lanes takes
+//       about 2.6 thousand clocks, 2.05 of them UMMAs, whose operands also take
+//       all of shared memory's bandwidth;
+//   heads of 64  (prompts of 301 to 2630 tokens, window 1000: 60 us) the softmax
+//       warps, about 2.4 thousand clocks a key tile of both lanes, and what a
+//       unit of few tiles costs beside them;
+//   decode steps (64 tokens over 97 to 12002 keys, 333 MB: 64 us) HBM while the
+//       tiles run, about 51 us; the rest is the first tile's way in (5 us: plan,
+//       page ids, copies, first products, code met for the first time), the last
+//       one's way out and the join.
+// Tried and left out: two softmax threads a row on sixteen warps (77 against
+// 66 us for the decode steps, 1283 against 1150 for the chunk), four warps for
+// the copies (36 against 34 us for drafted tokens), waits that hand the warp to
+// the hardware for longer (no change), a rehearsal of the softmax code while the
+// plan is made (4 us more).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
