@@ -102,31 +102,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
   return false;
 }
 
-// mbar_wait for CTAs whose warps mostly wait: between polls the hardware may
-// hold the warp for up to 20 us (it wakes when the phase completes), so that
-// waiting warps leave the issue slots to the ones at work.
-__device__ __forceinline__ bool mbar_wait_held(uint32_t bar, uint32_t parity, const WaitCtl &w, bool bail = true) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 1; it != 0; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    if (ok) return true;
-    if ((it & 15u) == 0) {
-      if (bail && *reinterpret_cast<volatile unsigned *>(w.abort_epoch) == w.epoch) return false;
-      if (globaltimer_ns() - t0 > w.limit_ns) break;
-    }
-  }
-  record_timeout(w);
-  return false;
-}
-
 // ---------------------------------------------------------------- programmatic launch
 // In a kernel launched with programmatic stream serialization: let the next
 // kernel of the stream begin launching (issued by every CTA once it runs).
