@@ -18,8 +18,6 @@
 namespace mmq {
 namespace {
 
-constexpr int kVerThreads = 256;
-
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -44,10 +42,10 @@ __device__ __forceinline__ void consider(uint64_t &best, float w, float e, int64
 // (1 - 2^-19) of the warp's largest so far cannot win.  So a warp takes the
 // largest a of a batch first and divides where a lane is near it; entries
 // whose reciprocal leaves the normal range are always divided.
-template <class T, int kCtas>
+template <class T, int kCtas, int kThreads>
 __device__ __forceinline__ uint64_t race(const T *__restrict__ p, const T *__restrict__ q, const float *__restrict__ e,
                                          int64_t n, int64_t skip, uint32_t rank) {
-  constexpr int kBatch = 8, kStep = kCtas * kVerThreads;
+  constexpr int kBatch = kThreads == 512 ? 8 : 6, kStep = kCtas * kThreads;
   const int lane = threadIdx.x & 31;
   uint64_t best = 0;
   float highest = 0.0f;
@@ -94,7 +92,7 @@ __device__ __forceinline__ uint64_t race(const T *__restrict__ p, const T *__res
       }
     }
   };
-  int64_t v0 = static_cast<int64_t>(rank) * kVerThreads + (threadIdx.x - lane);  // (the warp as one)
+  int64_t v0 = static_cast<int64_t>(rank) * kThreads + (threadIdx.x - lane);  // (the warp as one)
   for (; v0 + 31 + (kBatch - 1) * kStep < n; v0 += kBatch * kStep) batch(v0, std::true_type());
   if (v0 < n) batch(v0, std::false_type());
   return best;
@@ -110,14 +108,14 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t x) {
 }
 
 // The cluster's best: each CTA reduces its own and writes it to every CTA.
-template <int kCtas>
+template <int kCtas, int kThreads>
 __device__ __forceinline__ uint64_t cluster_best(uint64_t mine, uint64_t *own, uint64_t *all, uint32_t rank) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   mine = warp_max(mine);
   if (lane == 0) own[warp] = mine;
   __syncthreads();
   if (warp == 0) {
-    const uint64_t b = warp_max(lane < kVerThreads / 32 ? own[lane] : 0);
+    const uint64_t b = warp_max(lane < kThreads / 32 ? own[lane] : 0);
     if (lane < kCtas)
       asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_addr(all + rank), lane)), "l"(b) : "memory");
   }
@@ -131,15 +129,21 @@ __device__ __forceinline__ uint64_t cluster_best(uint64_t mine, uint64_t *own, u
 // A cluster of 8 CTAs for each request: the row of the vocabulary is split
 // over them and joined through their shared memory, one launch, no scratch.
 // HBM bound with many requests, one row each of p, q and e (12 B an entry in
-// fp32; 160 requests, 100277 entries, 193 MB: 39 us, 4.9 TB/s); latency bound
-// with few (6 requests of 32000: 5 us), the drafted tokens' three dependent
-// reads and the join.  Eight CTAs of 256 threads and eight entries a thread in
-// flight: clusters of two or four were as fast with many requests and slower
-// with few (6.3 to 8.6 us), sixteen entries spilled (69 us).
-template <class T, int kCtas>
-__global__ void __launch_bounds__(kVerThreads, 4) __cluster_dims__(kCtas, 1, 1)
+// fp32; 160 requests, 100277 entries, 193 MB: 36 us, 5.4 TB/s); latency bound
+// with few (6 requests of 32000: 4.6 us), the drafted tokens' three dependent
+// reads and the join.
+// Up to 32 requests, whose clusters all run at once, CTAs have 512 threads, two
+// an SM, and eight entries a thread in flight (6 requests of 32000 4.6 us, 30:
+// 6.2, 10 of 151936: 10.3; the other shape 5.2, 6.8 and 15.1).  Beyond that they
+// have 256 threads, five an SM, and six entries: what a CTA waits for at its
+// start and end is hidden behind more others (36 us against 47; four an SM and
+// eight entries 40, six an SM 36.5, eight an SM and four entries 38, clusters of
+// four 37 to 44).
+constexpr unsigned kFewRequests = 32;
+template <class T, int kCtas, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 5 : 2) __cluster_dims__(kCtas, 1, 1)
     verify_kernel(const __grid_constant__ VerifyArgs a) {
-  __shared__ uint64_t own[kVerThreads / 32], all[2][kCtas];
+  __shared__ uint64_t own[kThreads / 32], all[2][kCtas];
   __shared__ int s_kept;
   griddep_wait();
   griddep_launch_dependents();
@@ -179,12 +183,12 @@ __global__ void __launch_bounds__(kVerThreads, 4) __cluster_dims__(kCtas, 1, 1)
   const float *e = a.noise + b * a.noise_stride;
   uint64_t best = 0;
   // a draft without probabilities gave its token all of them: p without that token
-  if (kept < n) best = cluster_best<kCtas>(race<T, kCtas>(p, q, e, a.vocab, q ? -1 : static_cast<int64_t>(ids[kept]), rank), own, all[0], rank);
+  if (kept < n) best = cluster_best<kCtas, kThreads>(race<T, kCtas, kThreads>(p, q, e, a.vocab, q ? -1 : static_cast<int64_t>(ids[kept]), rank), own, all[0], rank);
   if (best == 0)  // nothing was refused, or p - q is nowhere positive
-    best = cluster_best<kCtas>(race<T, kCtas>(p, nullptr, e, a.vocab, -1, rank), own, all[1], rank);
+    best = cluster_best<kCtas, kThreads>(race<T, kCtas, kThreads>(p, nullptr, e, a.vocab, -1, rank), own, all[1], rank);
   if (rank != 0) return;
   const int drawn = best ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
-  for (int i = threadIdx.x; i <= k; i += kVerThreads)
+  for (int i = threadIdx.x; i <= k; i += kThreads)
     a.out[b * (k + 1) + i] = i < kept ? ids[i] : i == kept ? drawn : -1;
   if (threadIdx.x == 0) a.accepted[b] = kept;
 }
@@ -192,7 +196,8 @@ __global__ void __launch_bounds__(kVerThreads, 4) __cluster_dims__(kCtas, 1, 1)
 template <class T>
 cudaError_t launch_verify_of(const VerifyArgs &a, cudaStream_t s) {
   const unsigned n = static_cast<unsigned>(a.nreq);
-  return launch_early(verify_kernel<T, 8>, 8, n, kVerThreads, 0, s, a);
+  if (n <= kFewRequests) return launch_early(verify_kernel<T, 8, 512>, 8, n, 512, 0, s, a);
+  return launch_early(verify_kernel<T, 8, 256>, 8, n, 256, 0, s, a);
 }
 
 }  // namespace

@@ -509,7 +509,7 @@ def _drafts(nreq, k, vocab, seed, dtype=F32, sharp=3.0):
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=["f32", "f16", "bf16"])
-@pytest.mark.parametrize("nreq,k,vocab", [(1, 0, 1), (3, 1, 5), (17, 4, 1000), (40, 7, 4097), (2, 40, 333), (5, 3, 32000)])
+@pytest.mark.parametrize("nreq,k,vocab", [(1, 0, 1), (3, 1, 5), (17, 4, 1000), (40, 7, 4097), (2, 40, 333), (5, 3, 32000), (32, 2, 40000), (33, 2, 20000)])
 def test_verify_against_the_definition(mmq, dtype, nreq, k, vocab):
     target, draft, tokens, n_draft, u, noise = _drafts(nreq, k, vocab, seed=vocab, dtype=dtype)
     for q, n in ((draft, n_draft), (None, n_draft), (draft, None)):
