@@ -428,7 +428,8 @@ typedef struct mmq_attention {
  *   Rows of q past q_start[nreq] belong to no request; their out and lse are
  * not written.  seq_lens[b] = 0 and n = 0 are allowed.  Keys past seq_lens[b]
  * are not used, whatever their memory holds, and table entries past the last
- * key's page are not read.  A non-finite V row that some row of a chunk sees
+ * key's page are not read; nor, with a window, keys and pages behind that of
+ * the request's first new token, so that such pages can be given away.  A non-finite V row that some row of a chunk sees
  * may also make rows of that chunk non-finite that do not see it.
  *   A page id outside the cache, or seq_lens[b] past table_width*page_size, is
  * reported by mmq_last_device_error; that request's rows are then unspecified.

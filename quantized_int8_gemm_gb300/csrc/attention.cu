@@ -77,7 +77,8 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
 
 // The general kernel.  A unit: 64 rows, 16 a warp, over K/V tiles of 64 keys,
 // double-buffered copies (cp.async, zeros for what lies past the request's
-// last key, so that what unwritten memory holds never meets the tensor core).
+// last key or behind the rows' windows, so that what unwritten or reused memory
+// holds never meets the tensor core).
 // S and P stay in registers; the running maximum, sum and the output are
 // fp32, P is rounded to the cache's type for the second product.  It serves
 // the shapes the tcgen05 kernel does not take: heads wider than 128, pages
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
     auto load = [&](int t, int buf) {
       const int key = t * kKt + warp * 16 + (lane & 15);
       int64_t k_at = -1, v_at = -1;
-      if (key < un.len) {
+      if (key >= un.from && key < un.len) {
         const int blk = a.by_page(key), off = key - blk * a.page_size;
         const int64_t page = a.table[un.b * a.table_stride + blk];
         if (page >= 0 && page < a.pages) {

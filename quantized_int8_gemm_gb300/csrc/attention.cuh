@@ -83,6 +83,7 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, const Att
 struct AttnUnit {
   int q0, n, len, b, head;
   int row0;            // first row of the unit within the request
+  int from;            // first key that a row of the unit sees
   int t_begin, t_end;  // K/V tiles (may be none)
   int slot;            // of the partial result; -1: the unit is whole
 };
@@ -113,9 +114,9 @@ struct AttnSchedule {
   AttnRequest cur;  // its request
   bool cut;         // this CTA has told of its cut unit
 
-  // K/V tiles of the rows of row tile q.
-  __device__ __forceinline__ void tiles_of(const AttnArgs &a, const AttnRequest &x, int q, int &t0, int &t1) const {
-    int from, to, none;
+  // K/V tiles of the rows of row tile q, and the first key that they see.
+  __device__ __forceinline__ void tiles_of(const AttnArgs &a, const AttnRequest &x, int q, int &from, int &t0, int &t1) const {
+    int to, none;
     const int first = kRows ? a.by_rep(q * kRows) : q * a.unit_tok;
     const int last = min(x.n, kRows ? a.by_rep((q + 1) * kRows - 1) + 1 : first + a.unit_tok) - 1;
     attn_row_range(a, x.n, x.len, first, from, none);
@@ -125,8 +126,8 @@ struct AttnSchedule {
   }
   // Room of one unit on the line.
   __device__ __forceinline__ int room_of(const AttnArgs &a, const AttnRequest &x, int q) const {
-    int t0, t1;
-    tiles_of(a, x, q, t0, t1);
+    int from, t0, t1;
+    tiles_of(a, x, q, from, t0, t1);
     return kGap + max(1, t1 - t0);
   }
   __device__ __forceinline__ AttnRequest lane_request(int l) const {
@@ -261,11 +262,11 @@ struct AttnSchedule {
   // This CTA's next unit, or piece of one; false when there are no more.
   __device__ __forceinline__ bool next(const AttnArgs &a, AttnUnit &o) {
     while (b < a.nreq) {
-      int t0, t1;
-      tiles_of(a, cur, qt, t0, t1);
+      int from, t0, t1;
+      tiles_of(a, cur, qt, from, t0, t1);
       const int unit = kGap + max(1, t1 - t0), first = pos + kGap, end = pos + unit;  // where its tiles lie
       if (first >= hi) break;
-      o = {cur.q0, cur.n, cur.len, b, head, qt * (kRows ? kRows : a.unit_tok * a.rep), t0, t1, -1};
+      o = {cur.q0, cur.n, cur.len, b, head, qt * (kRows ? kRows : a.unit_tok * a.rep), from, t0, t1, -1};
       step(a, unit);
       if (!split) {
         if (first >= lo) return true;

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t *row = a.table + un.b * a.table_stride;
         auto page_of = [&](int t) {
           const int key = t * kKt + mine * box;
-          return mine < boxes && key < un.len && t < un.t_end ? row[a.by_page(key)] : 0;
+          return mine < boxes && key + box > un.from && key < un.len && t < un.t_end ? row[a.by_page(key)] : 0;
         };
         int ahead[2] = {page_of(un.t_begin), page_of(un.t_begin + 1)};
         if (kv) {
@@ -311,12 +311,31 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load4(base + L::kQ + t * L::kTile + g * 16384, &um.q, g * 64, 0, un.head, un.q0 + a.by_rep(un.row0) + t * tile_tok, q_full);
           }
         }
+        // V rows before the first key that a window leaves, or past the last
+        // one up to the next multiple of 16 (the K of one UMMA), hold what the
+        // page holds there, or an earlier tile: zeros, so that 0 * V is 0.
+        auto finish = [&](int s, int skip, int keys) {
+          if (!wait(tail(s), phase >> s & 1)) return false;
+          phase ^= 1u << s;
+          const int behind = -keys & 15;
+          uint8_t *v = smem + L::kRing + s * L::kTile;
+          for (int i = lane; i < (skip + behind) * 8 * L::kHalves; i += 32) {
+            const int x = i / (8 * L::kHalves), c = i % (8 * L::kHalves), r = x < skip ? x : keys + x - skip;
+            *reinterpret_cast<uint4 *>(v + (c >> 3) * 16384 + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kv_full(s));
+          return true;
+        };
+        int held = -1;  // a first tile's V, finished when the next copy is on its way
         for (int t = un.t_begin; t < un.t_end; ++t, ks += 2) {
           int id = ahead[0];
           ahead[0] = ahead[1];
           ahead[1] = page_of(t + 2);
           const int key = t * kKt + mine * box, off = key - a.by_page(key) * a.page_size;
-          const int keys = min(kKt, un.len - t * kKt), n = (keys + box - 1) / box;
+          const int keys = min(kKt, un.len - t * kKt), skip = max(0, un.from - t * kKt);
+          const int box_log2 = 31 - __clz(box), n0 = skip >> box_log2, n = (keys + box - 1) >> box_log2;  // (a divisor of 128)
           const int s = ks % L::kStages;
           ok = wait(kv_empty(s), ((ks / L::kStages) & 1) ^ 1);
           if (!ok) break;
@@ -324,29 +343,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             record_index(w.status);
             id = static_cast<int>(a.pages);
           }
-          const bool last = kv == 1 && keys < kKt;  // the last keys' V
-          const uint32_t bar = last ? tail(s) : kv_full(s);
-          tails = last ? tails | 1u << s : tails & ~(1u << s);
-          if (lane == 0) mbar_arrive_expect_tx(bar, n * L::kHalves * box * 128);
+          const bool edge = kv == 1 && (keys < kKt || skip);  // V with rows that are no keys
+          const uint32_t bar = edge ? tail(s) : kv_full(s);
+          tails = edge ? tails | 1u << s : tails & ~(1u << s);
+          if (lane == 0) mbar_arrive_expect_tx(bar, (n - n0) * L::kHalves * box * 128);
           __syncwarp();
-          if (mine < n) tma_load4(base + L::kRing + s * L::kTile + h * 16384 + mine * box * 128, map, h * 64, off, un.head, id, bar);
-          if (last) {
-            // Rows past the last key, up to the next multiple of 16 (the K of
-            // one UMMA), hold what the page holds there, or an earlier tile:
-            // zeros, so that 0 * V is 0.
-            ok = wait(bar, phase >> s & 1);
-            if (!ok) break;
-            phase ^= 1u << s;
-            const int zero = ((keys + 15) & ~15) - keys;
-            uint8_t *v = smem + L::kRing + s * L::kTile;
-            for (int i = lane; i < zero * 8 * L::kHalves; i += 32) {
-              const int r = keys + i / (8 * L::kHalves), c = i % (8 * L::kHalves);
-              *reinterpret_cast<uint4 *>(v + (c >> 3) * 16384 + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(kv_full(s));
-          }
+          if (mine >= n0 && mine < n) tma_load4(base + L::kRing + s * L::kTile + h * 16384 + mine * box * 128, map, h * 64, off, un.head, id, bar);
+          if (held >= 0) ok = finish(held, un.from - un.t_begin * kKt, kKt);
+          held = edge && t + 1 < un.t_end ? s : -1;
+          if (ok && edge && held < 0) ok = finish(s, skip, keys);
+          if (!ok) break;
         }
         if (!ok) break;
       }

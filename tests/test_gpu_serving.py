@@ -174,6 +174,26 @@ def test_what_lies_past_the_last_key_is_not_used(mmq, d, page, poison):
     _check(p, out, lse, 1 / math.sqrt(d))
 
 
+@pytest.mark.parametrize("d,page,hq,hkv", [(64, 16, 8, 2), (128, 8, 28, 4), (128, 64, 4, 4), (128, 256, 4, 1), (256, 16, 4, 2), (64, 5, 4, 1)])
+@pytest.mark.parametrize("window", [1, 13, 100, 300])
+def test_what_lies_behind_the_window_is_not_used(mmq, d, page, hq, hkv, window):
+    """Pages and keys that no new token's window reaches may be gone: ids out of the cache, NaN in their memory."""
+    q_lens, kv_lens = [1, 1, 5, 300, 2, 1], [4097, 640, 517, 1333, 90, 7000]
+    p = _problem(F16, q_lens, kv_lens, hq, hkv, d, page, seed=window)
+    for b, (n, length) in enumerate(zip(q_lens, kv_lens)):
+        first = max(0, length - n - window + 1)
+        for j in range(first // page):
+            for x in (p["kc"], p["vc"]):
+                x[p["table"][b, j]] = math.nan
+            if (b + j) % 2:
+                p["table"][b, j] = -1 if j % 4 else 2 ** 30
+        if first % page:
+            for x in (p["kc"], p["vc"]):
+                x[p["table"][b, first // page], :first % page] = math.nan
+    out, lse = _attend(mmq, p, window=window)
+    _check(p, out, lse, 1 / math.sqrt(d), window=window)
+
+
 @pytest.mark.parametrize("d,page,q_lens", [(128, 16, [1, 1]), (128, 16, [200, 1]), (64, 5, [3, 90])])
 def test_strides_scale_and_fp32_output(mmq, d, page, q_lens):
     """q as columns of a wider tensor, an output with its own strides, fp32 output, another scale."""
