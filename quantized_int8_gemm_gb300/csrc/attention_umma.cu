@@ -17,7 +17,7 @@
 //       P V and Q K^T 0.5 each and the hand-offs: a key tile of both lanes takes
 //       about 2.6 thousand clocks, 2.05 of them UMMAs, whose operands also take
 //       all of shared memory's bandwidth;
-//   heads of 64  (prompts of 301 to 2630 tokens, window 1000: 60 us) the softmax
+//   heads of 64  (prompts of 301 to 2630 tokens, window 1000: 58 us) the softmax
 //       warps, about 2.4 thousand clocks a key tile of both lanes, and what a
 //       unit of few tiles costs beside them;
 //   decode steps (64 tokens over 97 to 12002 keys, 333 MB: 64 us) HBM while the
@@ -173,6 +173,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// Bits [from, to) of 32.
+__device__ __forceinline__ uint32_t bits_of(int from, int to) {
+  auto below = [](int n) { return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1; };
+  return below(to) & ~below(from);
+}
+
 template <class T, int kDp>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_umma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnUmma um) {
@@ -238,16 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(base + L::kSlot, 512);
     tmem_relinquish();
   }
-  AttnSchedule<kKt, 0> sched;
   AttnUnit un;
-  griddep_wait();
-  if (warp == kLoadWarp) {  // its first unit, while the others set up
-    sched.plan(a);
-    if (!sched.next(a, un)) un.n = 0;
-  }
   tc_fence_before();
   __syncthreads();
-  griddep_launch_dependents();  // the next kernel's CTAs come as these leave
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kSlot);
   auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, w)) != 0; };
@@ -265,6 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    griddep_wait();
+    griddep_launch_dependents();  // the next kernel's CTAs come as these leave
     if (warp >= kLoadWarp) {
       // ---------------------------------------------------------- loads: one warp K, and the units' order; one Q and V
       // (a warp issues a copy every 69 clocks whatever its size, and a tile of
@@ -276,9 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ks = kv, nu = 0, nq = 0;  // ks: this warp's next load of the ring
       uint32_t tails = 0, phase = 0;     // stages whose last load went to tail(), and its phases
       bool ok = true;
+      AttnSchedule<kKt, 0> sched;
+      if (kv == 0) sched.plan(a);
       for (;; ++nu) {
         if (kv == 0) {
-          if (nu && !sched.next(a, un)) un.n = 0;
+          if (!sched.next(a, un)) un.n = 0;
           const int e = nu % kUnits;
           ok = wait(u_empty(e), ((nu / kUnits) & 1) ^ 1);
           if (!ok) break;
@@ -488,6 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    griddep_wait();
+    griddep_launch_dependents();
     // ------------------------------------------------------------ softmax: one row a thread
     const int t = warp >> 2, quad = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
@@ -560,19 +565,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (some) {
           if constexpr (L::kApart) {
             // Hidden keys: S is set to -inf in TMEM first, 32 columns at a time
-            // (small code; few tiles have any).
+            // (small code; few tiles have any).  A row's keys are the bits of a
+            // word, so that a column costs one select (compared with both ends: 61
+            // against 58 us for the prompts; in registers behind the load 59.5).
             const int from = lo - j * kKt, to_key = hi - j * kKt;
             if (__any_sync(0xffffffffu, valid && (from > 0 || to_key < kKt))) {
 #pragma unroll 1
               for (int c = 0; c < kKt; c += 32) {
-                const int y0 = from - c, y1 = to_key - c;
-                if (!__any_sync(0xffffffffu, valid && (y0 > 0 || y1 < 32))) continue;
+                const uint32_t seen = bits_of(from - c, to_key - c);
+                if (!__any_sync(0xffffffffu, valid && seen != 0xffffffffu)) continue;
                 uint32_t y[32];
                 tmem_ld_32x32b_x32(ts + c, y);
                 tmem_wait_ld(y);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  if (i < y0 || i >= y1) y[i] = 0xff800000u;
+                  if (!(seen >> i & 1)) y[i] = 0xff800000u;
                 tmem_st_32x32b_x32(ts + c, y);
               }
               tmem_wait_st();
