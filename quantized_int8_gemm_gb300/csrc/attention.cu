@@ -91,7 +91,7 @@ template <class T, int kDp>
 __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ AttnUnit s_unit;
-  __shared__ int s_more;
+  __shared__ int s_more, s_sums[kAttnSums + 1];
   constexpr int kChunks = kDp / 8;
   constexpr int kTile = kKt * kDp * 2;
   const uint32_t sq = smem_addr(smem), sk = sq + kRows * kDp * 2, sv = sk + 2 * kTile;
@@ -99,7 +99,13 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
   AttnSchedule<kKt, kRows> sched;
   griddep_wait();
   griddep_launch_dependents();
-  if (warp == 0) sched.plan(a);
+  if (a.nreq > 32) {
+    if (tid == 0) s_sums[kAttnSums] = 0;
+    __syncthreads();
+    sched.add_up(a, warp, kThreads / 32, s_sums);
+    __syncthreads();
+  }
+  if (warp == 0) sched.plan(a, s_sums);
 
   for (;;) {
     if (warp == 0) {

@@ -96,6 +96,7 @@ __device__ __forceinline__ void attn_row_range(const AttnArgs &a, int n, int len
 }
 
 constexpr int kAttnGap = 3;
+constexpr int kAttnSums = 511;  // groups of requests at most
 
 // Deals the units out; every lane of one warp calls each function.  kRows: of
 // a unit, or 0 where units are whole tokens (AttnArgs::unit_tok).
@@ -178,20 +179,49 @@ struct AttnSchedule {
     return sum * a.hkv;
   }
 
-  // Finds this CTA's stretch and the first unit that reaches into it.
-  __device__ __forceinline__ void plan(const AttnArgs &a) {
-    cut = false;
-    const int lane = threadIdx.x & 31;
-    int total = 0, mine = 0, longest = 0;
-    AttnLengths ahead = lengths(a, (a.nreq - 1) / 32 * 32);
+  // Groups of requests whose rooms are added up ahead: 2^log2 requests each, 32 or more.
+  __device__ static __forceinline__ int group_log2(const AttnArgs &a) {
+    const uint32_t q = (static_cast<uint32_t>(a.nreq) - 1) / (32 * kAttnSums);  // (511 * 2^k >= nreq / 32 where 2^k > q)
+    return 5 + (32 - __clz(q));
+  }
+  // One warp's part of the rooms of all requests, in shared memory: sums[i] of
+  // group i = first, first + step, ...; sums[kAttnSums], 0 before, becomes the
+  // longest unit's.
+  __device__ __forceinline__ void add_up(const AttnArgs &a, int first, int step, int *sums) {
+    const int log2 = group_log2(a), groups = ((a.nreq - 1) >> log2) + 1;
+    int longest = 0;
+    AttnLengths ahead{0, 0, 0};
+    if (first < groups) ahead = lengths(a, first << log2);
 #pragma unroll 1
-    for (b0 = (a.nreq - 1) / 32 * 32;; b0 -= 32) {  // (ends with the first 32 at hand)
-      const AttnLengths now = ahead;
-      ahead = lengths(a, b0 - 32);
-      r = attn_request<kRows>(a, now);
-      mine = lane_room(a, longest);
-      total += mine;
-      if (b0 == 0) break;
+    for (int i = first; i < groups; i += step) {
+      int sum = 0;
+#pragma unroll 1
+      for (int j = 0; j < 1 << log2; j += 32) {
+        const AttnLengths now = ahead;
+        if (j + 32 < 1 << log2) ahead = lengths(a, (i << log2) + j + 32);
+        else if (i + step < groups) ahead = lengths(a, (i + step) << log2);
+        r = attn_request<kRows>(a, now);
+        sum += lane_room(a, longest);
+      }
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if ((threadIdx.x & 31) == 0) sums[i] = sum;
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if ((threadIdx.x & 31) == 0) atomicMax(sums + kAttnSums, longest);
+  }
+
+  // Finds this CTA's stretch and the first unit that reaches into it.  With more
+  // than 32 requests `sums` is what add_up left.
+  __device__ __forceinline__ void plan(const AttnArgs &a, const int *sums) {
+    cut = false;
+    const int lane = threadIdx.x & 31, log2 = group_log2(a), groups = ((a.nreq - 1) >> log2) + 1;
+    int total = 0, mine = 0, longest = 0;
+    if (groups > 1) {
+      for (int i = lane; i < groups; i += 32) total += sums[i];
+      longest = sums[kAttnSums];
+    } else {
+      load(a, 0);
+      total = mine = lane_room(a, longest);
     }
     total = __reduce_add_sync(0xffffffffu, total);
     longest = __reduce_max_sync(0xffffffffu, longest);
@@ -202,8 +232,28 @@ struct AttnSchedule {
     lo = each * static_cast<int>(blockIdx.x);
     hi = lo + each;
     pos = 0;
-    int end = inclusive(mine);
     uint32_t past;
+    if (groups > 1) {  // the group that reaches past lo
+      int i = 0;
+      for (;; i += 32) {
+        mine = i + lane < groups ? sums[i + lane] : 0;
+        const int end = inclusive(mine);
+        past = __ballot_sync(0xffffffffu, pos + end > lo);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          pos += __shfl_sync(0xffffffffu, end - mine, l);
+          load(a, (i + l) << log2);
+          break;
+        }
+        pos += __shfl_sync(0xffffffffu, end, 31);
+        if (i + 32 >= groups) {
+          b = a.nreq;
+          return;
+        }
+      }
+      mine = lane_room(a, longest);
+    }
+    int end = inclusive(mine);
     while (!(past = __ballot_sync(0xffffffffu, pos + end > lo))) {
       pos += __shfl_sync(0xffffffffu, end, 31);
       if (b0 + 32 >= a.nreq) {

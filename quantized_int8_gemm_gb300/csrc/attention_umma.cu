@@ -64,7 +64,7 @@ struct Lay {
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTile;
   static constexpr int kBars = kRing + kStages * kTile;
-  static constexpr int kNumBars = 3 * kStages + 2 + 18 + 2 * kUnits + 1;
+  static constexpr int kNumBars = 3 * kStages + 2 + 18 + 2 * kUnits + 2;
   static constexpr int kStats = kBars + kNumBars * 8;  // [lane][row] maximum and sum
   static constexpr int kUnitsAt = kStats + 2 * 128 * 8;
   static constexpr int kSlot = kUnitsAt + kUnits * static_cast<int>(sizeof(AttnUnit));
@@ -202,10 +202,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto p_empty = [&](int t) { return bars + 8u * (kFix + 18 + t); };
   auto u_full = [&](int i) { return bars + 8u * (kFix + 20 + i); };
   auto u_empty = [&](int i) { return bars + 8u * (kFix + 20 + kUnits + i); };
-  const uint32_t done = bars + 8u * (L::kNumBars - 1);
+  const uint32_t added = bars + 8u * (L::kNumBars - 2), done = bars + 8u * (L::kNumBars - 1);
   AttnUnit *units = reinterpret_cast<AttnUnit *>(smem + L::kUnitsAt);
   const WaitCtl &w = a.wait;
   float2 *stats = reinterpret_cast<float2 *>(smem + L::kStats);
+  // More than 32 requests: the softmax warps add up their rooms on the units'
+  // line, into the place of the statistics (4096 requests of 301 keys, 8 heads on
+  // 1: 183 us, by the planning warp alone 295; 1024, 28 heads on 4: 175 and 200).
+  int *sums = reinterpret_cast<int *>(stats);
+  static_assert((kAttnSums + 1) * sizeof(int) <= 2 * 128 * sizeof(float2));
   const int tile_tok = um.tile_tok, box = um.box;
   const int half_rows = tile_tok * a.rep;  // rows of one tile (at most 128)
 
@@ -234,6 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(stats_full, 8);
     mbar_init(stats_empty, 8);
     mbar_init(done, 2);
+    mbar_init(added, 8);
+    sums[kAttnSums] = 0;
     fence_mbar_init();
   }
   if (warp == kLoadWarp + 1 && lane < 3) {
@@ -278,8 +285,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t tails = 0, phase = 0;     // stages whose last load went to tail(), and its phases
       bool ok = true;
       AttnSchedule<kKt, 0> sched;
-      if (kv == 0) sched.plan(a);
-      for (;; ++nu) {
+      if (kv == 0) {
+        if (a.nreq > 32) ok = wait(added, 0);
+        if (ok) sched.plan(a, sums);
+      }
+      for (; ok; ++nu) {
         if (kv == 0) {
           if (!sched.next(a, un)) un.n = 0;
           const int e = nu % kUnits;
@@ -493,6 +503,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     griddep_wait();
     griddep_launch_dependents();
+    if (a.nreq > 32) {
+      AttnSchedule<kKt, 0> rooms;
+      rooms.add_up(a, warp, kUmmaWarp, sums);
+      __syncwarp();
+      mbar_arrive_if(lane == 0, added);
+    }
     // ------------------------------------------------------------ softmax: one row a thread
     const int t = warp >> 2, quad = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;

@@ -131,6 +131,9 @@ SHAPES = [
     ([1], [257], 8, 8, 128, 16),
     ([1, 1, 1], [700, 1, 129], 28, 4, 128, 16),
     ([1] * 40, [5 + 61 * i for i in range(40)], 8, 2, 64, 64),
+    ([1] * 300, [1 + (37 * i) % 290 for i in range(300)], 8, 1, 128, 16),
+    ([0, 1, 2] * 400, [(53 * i) % 200 for i in range(1200)], 2, 2, 64, 8),
+    ([1, 3] * 70, [(29 * i) % 150 for i in range(140)], 2, 1, 256, 16),
     ([5, 1, 3], [133, 640, 3], 28, 4, 128, 8),
     ([130], [130], 7, 1, 128, 32),
     ([300, 1, 77], [1000, 2049, 77], 12, 4, 64, 128),
@@ -171,6 +174,22 @@ def test_rows_that_see_nothing(mmq, d, page):
 def test_what_lies_past_the_last_key_is_not_used(mmq, d, page, poison):
     p = _problem(F16, [1, 150, 5], [100, 150, 513], 8, 2, d, page, poison=poison)
     out, lse = _attend(mmq, p)
+    _check(p, out, lse, 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("d,page", [(64, 8), (128, 5)])
+def test_very_many_requests(mmq, d, page):
+    """More groups of 32 requests than a CTA keeps sums of: few requests have tokens, the last one among them."""
+    n = 40000
+    some = {0: (1, 40), 7: (3, 130), 16351: (1, 9), 16352: (2, 300), 20011: (1, 1), n - 1: (4, 600)}
+    p = _problem(F16, [x for x, _ in some.values()], [x for _, x in some.values()], 4, 2, d, page)
+    q_lens, kv_lens = torch.zeros(n, dtype=torch.int32), torch.zeros(n, dtype=torch.int32)
+    table = torch.full((n, p["table"].shape[1]), -1, dtype=torch.int32, device="cuda")
+    for row, (at, (x, y)) in enumerate(some.items()):
+        q_lens[at], kv_lens[at] = x, y
+        table[at] = p["table"][row]
+    starts = torch.cat([torch.zeros(1, dtype=torch.int32), q_lens.cumsum(0).int()]).cuda()
+    out, lse = mmq.mmq_paged_attention(p["q"], p["kc"], p["vc"], table, kv_lens.cuda(), starts, lse=True)
     _check(p, out, lse, 1 / math.sqrt(d))
 
 
