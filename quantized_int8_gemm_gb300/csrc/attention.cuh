@@ -12,7 +12,7 @@
 // takes an equal stretch of that line: a few long rows and many short ones
 // then take every CTA the same time, and a CTA holds at most two pieces of
 // units that others share.  A warp of every CTA works its stretch out by
-// itself.
+// itself; with more than 32 requests the other warps add their room up first.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>

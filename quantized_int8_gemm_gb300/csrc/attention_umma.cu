@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float2 *stats = reinterpret_cast<float2 *>(smem + L::kStats);
   // More than 32 requests: the softmax warps add up their rooms on the units'
   // line, into the place of the statistics (4096 requests of 301 keys, 8 heads on
-  // 1: 183 us, by the planning warp alone 295; 1024, 28 heads on 4: 175 and 200).
+  // 1: 188 us, by the planning warp alone 291; 1024, 28 heads on 4: 177 and 194).
   int *sums = reinterpret_cast<int *>(stats);
   static_assert((kAttnSums + 1) * sizeof(int) <= 2 * 128 * sizeof(float2));
   const int tile_tok = um.tile_tok, box = um.box;
@@ -637,6 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // often as they issued one).  First the maximum.
             const int from = lo - j * kKt, to_key = hi - j * kKt;
             const bool ends = __any_sync(0xffffffffu, valid && (from > 0 || to_key < kKt));
+            // (P V stops at the last key: 1024 decode rows over 171 keys 118 us, 135 with both halves)
+            const int halves = un.len - j * kKt <= kKt / 2 ? 1 : 2;
             float top[4];
             if (!ends) {
               uint32_t x[4][32];
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {  // hidden keys (the tiles at a row's ends) become -inf in TMEM
               top[0] = top[1] = top[2] = top[3] = -INFINITY;
 #pragma unroll 1
-              for (int c = 0; c < kKt; c += 32) {
+              for (int c = 0; c < 64 * halves; c += 32) {
                 const int y0 = from - c, y1 = to_key - c;
                 uint32_t y[32];
                 tmem_ld_32x32b_x32(ts + c, y);
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t sum[2] = {0, 0};
             // Then the weights, 64 columns at a time (over S: behind what has been read).
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < halves; ++h) {
               uint32_t x[64], p[32];
               tmem_ld_32x32b_x64(ts + 64 * h, x);
               tmem_wait_ld(x);
@@ -679,6 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               mbar_arrive_if(lane == 0, p_full(t, h));
             }
+            if (halves == 1) mbar_arrive_if(lane == 0, p_full(t, 1));
             float s0, s1;
             parts_of(add2(sum[0], sum[1]), s0, s1);
             l += s0 + s1;
