@@ -276,20 +276,43 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
 }
 
 // Joins the pieces of a cut unit: with lse_p (base 2) and normalised outputs
-// o_p, out = sum 2^(lse_p - top) o_p / sum 2^(lse_p - top), in fp32 and in the
-// pieces' order.  Block (c, y): rows 16 y .. of the unit that begins in CTA c;
-// a thread eight columns of a row, lanes along the rows (as the partial
-// results lie).  Latency bound where few rows are cut, else L2 bound; a
-// running maximum, so that weights and outputs are read in one round.
-constexpr int kJoinRows = 16;
+// o_p, out = sum 2^(lse_p - top) o_p / sum 2^(lse_p - top), in fp32 and in an
+// order that only the pieces' number and the unit's size decide.  Block (c, y):
+// rows 16 y .. of the unit that begins in CTA c; a thread eight columns of a
+// row, lanes along the rows (as the partial results lie), with a running maximum,
+// so that weights and outputs are read in one round.  Latency bound where few
+// rows are cut, else L2 bound.
+//
+// attention_join_split_kernel, for calls of few units: where a unit has more
+// than eight pieces and fewer rows than there are blocks for, blocks also take a
+// part of its columns each and a block's threads a part of the pieces (one row
+// over 30001 keys: 8 heads on 1, 118 pieces, 19 us for the call, 53 with all
+// pieces in one thread's turn; 28 heads on 4 24 and 34).  With many units it
+// costs 0.5 us more than the other one.
+constexpr int kJoinRows = 16, kJoinLeast = 8, kJoinPieces = 8;  // (blocks a unit; pieces a thread)
+// Eight columns of a joined row, from their sums and that of the weights relative to top.
 template <class T>
-__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a, int unit_rows) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const AttnCut u = a.cuts[blockIdx.x];
-  const int r0 = blockIdx.y * kJoinRows, rows = min(min(unit_rows, u.n * a.rep - u.row0) - r0, kJoinRows);
-  if (u.last < 0 || rows <= 0) return;
-  const int c0 = blockIdx.x, pieces = u.last - c0 + 1, r = threadIdx.x % kJoinRows;
+__device__ __forceinline__ void store_joined(const AttnArgs &a, int64_t tok, int head, int c, const float4 &x, const float4 &y, float top,
+                                             float sum) {
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t to = tok * a.out_token + head * a.out_head + 8 * c;
+  if (a.out_type == MMQ_DT_F32) {
+    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to);
+    dst[0] = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    dst[1] = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+  } else {
+    uint4 z;
+    z.x = Pair<T>::pack(x.x * inv, x.y * inv);
+    z.y = Pair<T>::pack(x.z * inv, x.w * inv);
+    z.z = Pair<T>::pack(y.x * inv, y.y * inv);
+    z.w = Pair<T>::pack(y.z * inv, y.w * inv);
+    *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + to) = z;
+  }
+  if (c == 0 && a.lse) a.lse[tok * a.hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+template <class T>
+__device__ __forceinline__ void join_plain(const AttnArgs &a, const AttnCut &u, int unit_rows, int r0, int rows, int c0, int pieces) {
+  const int r = threadIdx.x % kJoinRows;
   if (r >= rows) return;
   const int row = u.row0 + r0 + r, rtok = a.by_rep(row), head = u.head * a.rep + row - rtok * a.rep;
   const int64_t tok = u.q0 + rtok;
@@ -309,21 +332,80 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
       x.x = fmaf(x.x, keep, w * f.x), x.y = fmaf(x.y, keep, w * f.y), x.z = fmaf(x.z, keep, w * f.z), x.w = fmaf(x.w, keep, w * f.w);
       y.x = fmaf(y.x, keep, w * g.x), y.y = fmaf(y.y, keep, w * g.y), y.z = fmaf(y.z, keep, w * g.z), y.w = fmaf(y.w, keep, w * g.w);
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t to = tok * a.out_token + head * a.out_head + 8 * c;
-    if (a.out_type == MMQ_DT_F32) {
-      float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to);
-      dst[0] = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-      dst[1] = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-    } else {
-      uint4 z;
-      z.x = Pair<T>::pack(x.x * inv, x.y * inv);
-      z.y = Pair<T>::pack(x.z * inv, x.w * inv);
-      z.z = Pair<T>::pack(y.x * inv, y.y * inv);
-      z.w = Pair<T>::pack(y.z * inv, y.w * inv);
-      *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + to) = z;
+    store_joined<T>(a, tok, head, c, x, y, top, sum);
+  }
+}
+template <class T>
+__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnArgs a, int unit_rows) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const AttnCut u = a.cuts[blockIdx.x];
+  const int r0 = blockIdx.y * kJoinRows, rows = min(min(unit_rows, u.n * a.rep - u.row0) - r0, kJoinRows);
+  if (u.last < 0 || rows <= 0) return;
+  join_plain<T>(a, u, unit_rows, r0, rows, blockIdx.x, u.last - static_cast<int>(blockIdx.x) + 1);
+}
+
+template <class T>
+__global__ void __launch_bounds__(256) attention_join_split_kernel(const __grid_constant__ AttnArgs a, int unit_rows) {
+  __shared__ float s_top[256], s_sum[256];
+  __shared__ float4 s_x[256], s_y[256];
+  griddep_wait();
+  griddep_launch_dependents();
+  const AttnCut u = a.cuts[blockIdx.x];
+  const int all = min(unit_rows, u.n * a.rep - u.row0);
+  if (u.last < 0 || all <= 0) return;
+  // row groups, and column groups (a power of two, up to 16)
+  const int row_groups = (all + kJoinRows - 1) / kJoinRows;
+  const int c0 = blockIdx.x, pieces = u.last - c0 + 1;
+  const int cols_log2 = pieces <= kJoinPieces ? 0 : min(min(31 - __clz(static_cast<int>(gridDim.y) / row_groups), 32 - __clz((pieces - 1) / kJoinPieces)), 4);
+  const int group = static_cast<int>(blockIdx.y) / row_groups;
+  const int r0 = (static_cast<int>(blockIdx.y) - group * row_groups) * kJoinRows, rows = min(all - r0, kJoinRows);
+  const int chunks = a.d / 8, mine = (chunks + (1 << cols_log2) - 1) >> cols_log2;
+  const int first = group * mine, end = min(chunks, first + mine);
+  if (group >> cols_log2 || first >= end) return;
+  if (cols_log2 == 0) {
+    join_plain<T>(a, u, unit_rows, r0, rows, c0, pieces);
+    return;
+  }
+  // 16 lots of threads: `par` columns' chunks at a time, and as many parts of the pieces as that leaves
+  const int par_log2 = min(32 - __clz(mine - 1), 4), par = 1 << par_log2, parts = 16 >> par_log2;
+  const int r = threadIdx.x % kJoinRows, lot = threadIdx.x / kJoinRows;
+  const int row = u.row0 + r0 + r, rtok = a.by_rep(row), head = u.head * a.rep + row - rtok * a.rep;
+  const int64_t tok = u.q0 + rtok;
+  for (int base = first; base < end; base += par) {
+    const int c = base + (lot & (par - 1)), part = lot >> par_log2;
+    const bool in = r < rows && c < end;
+    float top = -INFINITY, sum = 0.0f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    auto add = [&](float l, float w_sum, const float4 &f, const float4 &g) {  // (w_sum: of f and g's weights, relative to l)
+      const float high = fmaxf(top, l), keep = top == -INFINITY ? 0.0f : exp2f(top - high), w = exp2f(l - high);
+      top = high;
+      sum = fmaf(sum, keep, w * w_sum);
+      x.x = fmaf(x.x, keep, w * f.x), x.y = fmaf(x.y, keep, w * f.y), x.z = fmaf(x.z, keep, w * f.z), x.w = fmaf(x.w, keep, w * f.w);
+      y.x = fmaf(y.x, keep, w * g.x), y.y = fmaf(y.y, keep, w * g.y), y.z = fmaf(y.z, keep, w * g.z), y.w = fmaf(y.w, keep, w * g.w);
+    };
+    if (in) {
+#pragma unroll 4
+      for (int p = part; p < pieces; p += parts) {
+        const int64_t s = 2 * (c0 + p) + (p == 0);
+        const float l = a.part_lse[s * unit_rows + r0 + r];
+        const float4 *src = a.part_o + (s * (a.d / 4) + 2 * c) * unit_rows + r0 + r;
+        const float4 f = __ldcs(src), g = __ldcs(src + unit_rows);
+        if (l != -INFINITY) add(l, 1.0f, f, g);
+      }
     }
-    if (c == 0 && a.lse) a.lse[tok * a.hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    if (parts > 1) {
+      __syncthreads();  // (the chunk before has been read)
+      s_top[threadIdx.x] = top, s_sum[threadIdx.x] = sum, s_x[threadIdx.x] = x, s_y[threadIdx.x] = y;
+      __syncthreads();
+      if (part == 0)
+        for (int i = 1; i < parts; ++i) {
+          const int o = threadIdx.x + i * par * kJoinRows;
+          if (s_sum[o] != 0.0f) add(s_top[o], s_sum[o], s_x[o], s_y[o]);  // (NaN: added)
+        }
+    }
+    if (!in || part) continue;
+    store_joined<T>(a, tok, head, c, x, y, top, sum);
   }
 }
 
@@ -342,10 +424,12 @@ cudaError_t launch_rows_of(const AttnArgs &a, int dev, unsigned grid, cudaStream
 }
 
 template <class T>
-cudaError_t launch_join(const AttnArgs &a, int unit_rows, unsigned grid, cudaStream_t s) {
+cudaError_t launch_join(const AttnArgs &a, int unit_rows, int64_t units, unsigned grid, cudaStream_t s) {
   // (no unit has more rows than all tokens together)
-  const int64_t most = std::min<int64_t>(unit_rows, a.ntok * a.rep);
-  return launch_early(attention_join_kernel<T>, grid, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows), 256, 0, s, a, unit_rows);
+  const int64_t groups = (std::min<int64_t>(unit_rows, a.ntok * a.rep) + kJoinRows - 1) / kJoinRows;
+  if (units * 4 > grid) return launch_early(attention_join_kernel<T>, grid, static_cast<unsigned>(groups), 256, 0, s, a, unit_rows);
+  return launch_early(attention_join_split_kernel<T>, grid, static_cast<unsigned>(std::max<int64_t>(groups, kJoinLeast)), 256, 0, s, a,
+                      unit_rows);
 }
 
 }  // namespace
@@ -403,7 +487,7 @@ cudaError_t launch_attention(const mmq_paged_cache &c, const mmq_attention &t, c
   }
   e = umma ? launch_attention_umma(a, um, c.type, ctx.device, grid, s) : launch_attention_rows(a, c.type, ctx.device, grid, s);
   if (e == cudaSuccess && cut)
-    e = c.type == MMQ_DT_F16 ? launch_join<__half>(a, unit_rows, grid, s) : launch_join<__nv_bfloat16>(a, unit_rows, grid, s);
+    e = c.type == MMQ_DT_F16 ? launch_join<__half>(a, unit_rows, units, grid, s) : launch_join<__nv_bfloat16>(a, unit_rows, units, grid, s);
   if (scratch) {
     const cudaError_t ef = cudaFreeAsync(scratch, s);
     if (e == cudaSuccess) e = ef;

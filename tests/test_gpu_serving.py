@@ -146,6 +146,9 @@ SHAPES = [
     ([45, 1], [300, 333], 6, 3, 128, 5),
     ([3], [400], 160, 1, 64, 16),       # more query heads to a K/V head than rows of a tile
     ([1], [9000], 4, 1, 128, 64),       # one row, split over the keys
+    ([1], [6000], 4, 1, 256, 16),
+    ([1, 2], [20000, 3000], 4, 2, 96, 16),
+    ([20], [30000], 1, 1, 64, 256),
     ([513], [4097], 4, 1, 64, 64),
 ]
 
