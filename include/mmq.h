@@ -426,7 +426,9 @@ typedef struct mmq_attention {
  * tokens) or thousands (a prompt's chunk) go through this one call, in any
  * mixture.
  *   Rows of q past q_start[nreq] belong to no request; their out and lse are
- * not written.  seq_lens[b] = 0 and n = 0 are allowed.  Keys past seq_lens[b]
+ * not written.  Where q_start counts more tokens than q has rows (ntok), the
+ * rows that are there keep their positions and the others are left out.
+ *   seq_lens[b] = 0 and n = 0 are allowed.  Keys past seq_lens[b]
  * are not used, whatever their memory holds, and table entries past the last
  * key's page are not read; nor, with a window, keys and pages behind that of
  * the request's first new token, so that such pages can be given away.  A non-finite V row that some row of a chunk sees

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     int lo[2], hi[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) attn_row_range(a, un.n, un.len, a.by_rep(un.row0 + warp * 16 + (lane >> 2) + 8 * h), lo[h], hi[h]);
+    for (int h = 0; h < 2; ++h) attn_row_range(a, un.place, un.len, a.by_rep(un.row0 + warp * 16 + (lane >> 2) + 8 * h), lo[h], hi[h]);
 
     for (int t = un.t_begin; t < un.t_end; ++t) {
       const int buf = (t - un.t_begin) & 1;

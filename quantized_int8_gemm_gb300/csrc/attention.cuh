@@ -55,8 +55,9 @@ struct AttnArgs {
 
 // The part of one request that does not depend on the unit.
 struct AttnRequest {
-  int q0, n;  // first token, tokens
-  int len;    // keys
+  int q0, n;  // first token, tokens that q has rows for
+  int place;  // of its first token among the keys (below 0 if it has more new tokens than keys)
+  int len;    // keys that its rows see at most
   int tiles;  // row tiles
 };
 
@@ -76,12 +77,17 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, const Att
     record_index(a.wait.status);
     r.len = static_cast<int>(room);
   }
+  // Places go by all of the request's new tokens, also those past q's rows (a
+  // step whose tables counted more tokens than it has rows for); the keys end
+  // where the last row's do, since nothing wrote those of the tokens behind it.
+  r.place = r.len - (max(r.q0, to) - r.q0);
+  if (a.causal) r.len = max(0, r.place + r.n);
   r.tiles = kRows ? (r.n * a.rep + kRows - 1) / max(kRows, 1) : a.by_unit_tok(r.n + a.unit_tok - 1);
   return r;
 }
 
 struct AttnUnit {
-  int q0, n, len, b, head;
+  int q0, n, place, len, b, head;
   int row0;            // first row of the unit within the request
   int from;            // first key that a row of the unit sees
   int t_begin, t_end;  // K/V tiles (may be none)
@@ -89,8 +95,8 @@ struct AttnUnit {
 };
 
 // A row's keys: [lo, hi).
-__device__ __forceinline__ void attn_row_range(const AttnArgs &a, int n, int len, int tok, int &lo, int &hi) {
-  const int pos = len - n + tok;
+__device__ __forceinline__ void attn_row_range(const AttnArgs &a, int place, int len, int tok, int &lo, int &hi) {
+  const int pos = place + tok;
   hi = a.causal ? max(0, min(len, pos + 1)) : len;
   lo = a.window ? max(0, pos - a.window + 1) : 0;
 }
@@ -120,8 +126,8 @@ struct AttnSchedule {
     int to, none;
     const int first = kRows ? a.by_rep(q * kRows) : q * a.unit_tok;
     const int last = min(x.n, kRows ? a.by_rep((q + 1) * kRows - 1) + 1 : first + a.unit_tok) - 1;
-    attn_row_range(a, x.n, x.len, first, from, none);
-    attn_row_range(a, x.n, x.len, last, none, to);
+    attn_row_range(a, x.place, x.len, first, from, none);
+    attn_row_range(a, x.place, x.len, last, none, to);
     t0 = from / kKt;
     t1 = max(t0, (to + kKt - 1) / kKt);
   }
@@ -132,8 +138,8 @@ struct AttnSchedule {
     return kGap + max(1, t1 - t0);
   }
   __device__ __forceinline__ AttnRequest lane_request(int l) const {
-    return {__shfl_sync(0xffffffffu, r.q0, l), __shfl_sync(0xffffffffu, r.n, l), __shfl_sync(0xffffffffu, r.len, l),
-            __shfl_sync(0xffffffffu, r.tiles, l)};
+    return {__shfl_sync(0xffffffffu, r.q0, l), __shfl_sync(0xffffffffu, r.n, l), __shfl_sync(0xffffffffu, r.place, l),
+            __shfl_sync(0xffffffffu, r.len, l), __shfl_sync(0xffffffffu, r.tiles, l)};
   }
   __device__ static __forceinline__ AttnLengths lengths(const AttnArgs &a, int from) {
     const int at = from + static_cast<int>(threadIdx.x & 31);
@@ -316,7 +322,7 @@ struct AttnSchedule {
       tiles_of(a, cur, qt, from, t0, t1);
       const int unit = kGap + max(1, t1 - t0), first = pos + kGap, end = pos + unit;  // where its tiles lie
       if (first >= hi) break;
-      o = {cur.q0, cur.n, cur.len, b, head, qt * (kRows ? kRows : a.unit_tok * a.rep), from, t0, t1, -1};
+      o = {cur.q0, cur.n, cur.place, cur.len, b, head, qt * (kRows ? kRows : a.unit_tok * a.rep), from, t0, t1, -1};
       step(a, unit);
       if (!split) {
         if (first >= lo) return true;

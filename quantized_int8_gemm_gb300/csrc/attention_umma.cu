@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = r < half_rows && row < un.n * a.rep;
       const bool some = __any_sync(0xffffffffu, valid);
       int lo, hi;
-      attn_row_range(a, un.n, un.len, tok, lo, hi);
+      attn_row_range(a, un.place, un.len, tok, lo, hi);
       float m = -INFINITY, l = 0.0f;
       // 64 weights and their sums.  Eight at a time, the exponentials of one
       // group beside the sums and conversions of the one before: exp2 keeps its

@@ -1,0 +1,46 @@
+"""The serving step's operators at the limits of their arguments: rows that a step has no room for, extreme windows, waits
+that run out, buffers given by the caller.  Problems, references and tolerances are those of test_gpu_serving.py."""
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_serving import BF16, F16, _i32, _no_device_error, _problem, _reference, mmq  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _check_rows(p, out, lse, scale, causal, window):
+    """The rows that were given, against the whole problem's."""
+    n = out.shape[0]
+    ref, z, tol, z_tol = (x[:n] for x in _reference(p, scale, causal, window))
+    assert torch.isfinite(out).all()
+    assert ((out.double() - ref).abs() <= tol).all()
+    none = torch.isinf(z)
+    assert torch.equal(torch.isinf(lse) & (lse < 0), none)
+    assert (torch.where(none, 0.0, (lse.double() - torch.where(none, 0.0, z)).abs()) <= z_tol).all()
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (128, 5), (256, 16)])
+@pytest.mark.parametrize("room", [1, 3, 150, 203])
+def test_attention_of_a_step_with_more_tokens_than_rows(mmq, d, page, room):  # noqa: F811
+    """q_start counts tokens that q has no row for (the tables' new tokens past max_tokens): the rows that are there keep
+    their places, and the keys of the others, which nothing wrote, are not seen by them."""
+    q_lens, kv_lens = [3, 200, 1, 40], [700, 1500, 33, 40]
+    for causal, window in ((True, 0), (True, 70), (False, 0)):
+        p = _problem(F16, q_lens, kv_lens, 8, 2, d, page, seed=room)
+        if causal:
+            at = 0
+            for b, (n, length) in enumerate(zip(q_lens, kv_lens)):
+                for i in range(max(0, min(n, room - at)), n):
+                    key = length - n + i
+                    for x in (p["kc"], p["vc"]):
+                        x[p["table"][b, key // page], key % page] = math.nan
+                at += n
+        guard = 5
+        out = torch.full((room + guard, 8, d), 7.0, dtype=F16, device="cuda")
+        lse = torch.full((room + guard, 8), 7.0, device="cuda")
+        mmq.mmq_paged_attention(p["q"][:room], p["kc"], p["vc"], p["table"], p["seq_lens"], p["q_start"], causal=causal, window=window,
+                                out=out[:room], lse=lse[:room])
+        _check_rows(p, out[:room], lse[:room], 1 / math.sqrt(d), causal, window)
+        assert (out[room:] == 7).all() and (lse[room:] == 7).all()
