@@ -98,7 +98,7 @@ struct AttnUnit {
 __device__ __forceinline__ void attn_row_range(const AttnArgs &a, int place, int len, int tok, int &lo, int &hi) {
   const int pos = place + tok;
   hi = a.causal ? max(0, min(len, pos + 1)) : len;
-  lo = a.window ? max(0, pos - a.window + 1) : 0;
+  lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;  // (pos below 0 less a wide window would wrap)
 }
 
 constexpr int kAttnGap = 3;

@@ -44,3 +44,13 @@ def test_attention_of_a_step_with_more_tokens_than_rows(mmq, d, page, room):  # 
                                 out=out[:room], lse=lse[:room])
         _check_rows(p, out[:room], lse[:room], 1 / math.sqrt(d), causal, window)
         assert (out[room:] == 7).all() and (lse[room:] == 7).all()
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 16), (96, 3), (256, 16)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5, 2 ** 30])
+@pytest.mark.parametrize("causal", [True, False])
+def test_the_widest_windows(mmq, d, page, window, causal):  # noqa: F811
+    """Windows near the largest number, in a chunk longer than its keys (places below zero)."""
+    p = _problem(BF16, [3, 20, 300], [5, 12, 40], 4, 2, d, page)
+    out, lse = mmq.mmq_paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seq_lens"], p["q_start"], causal=causal, window=window, lse=True)
+    _check_rows(p, out, lse, 1 / math.sqrt(d), causal, window)
