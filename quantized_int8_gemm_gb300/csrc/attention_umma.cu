@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // 1: 188 us, by the planning warp alone 291; 1024, 28 heads on 4: 177 and 194).
   int *sums = reinterpret_cast<int *>(stats);
   static_assert((kAttnSums + 1) * sizeof(int) <= 2 * 128 * sizeof(float2));
+  volatile uint32_t *last = reinterpret_cast<volatile uint32_t *>(smem + L::kSlot + 8);  // the load warps' loads of the ring, at their end
   const int tile_tok = um.tile_tok, box = um.box;
   const int half_rows = tile_tok * a.rep;  // rows of one tile (at most 128)
 
@@ -282,7 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int mine = lane / L::kHalves, h = lane % L::kHalves;  // (boxes * halves <= 32)
       const CUtensorMap *map = kv ? &um.v : &um.k;
       uint32_t ks = kv, nu = 0, nq = 0;  // ks: this warp's next load of the ring
-      uint32_t tails = 0, phase = 0;     // stages whose last load went to tail(), and its phases
+      uint32_t tails = 0, phase = 0;     // stages whose last load (of this warp) went to tail(), and its phases
+      uint32_t open = 0;                 // those that it has not been waited for
       bool ok = true;
       AttnSchedule<kKt, 0> sched;
       if (kv == 0) {
@@ -330,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto finish = [&](int s, int skip, int keys) {
           if (!wait(tail(s), phase >> s & 1)) return false;
           phase ^= 1u << s;
+          open &= ~(1u << s);
           const int behind = -keys & 15;
           uint8_t *v = smem + L::kRing + s * L::kTile;
           for (int i = lane; i < (skip + behind) * 8 * L::kHalves; i += 32) {
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         int held = -1;  // a first tile's V, finished when the next copy is on its way
-        for (int t = un.t_begin; t < un.t_end; ++t, ks += 2) {
+        for (int t = un.t_begin; t < un.t_end; ++t) {
           int id = ahead[0];
           ahead[0] = ahead[1];
           ahead[1] = page_of(t + 2);
@@ -359,9 +362,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool edge = kv == 1 && (keys < kKt || skip);  // V with rows that are no keys
           const uint32_t bar = edge ? tail(s) : kv_full(s);
           tails = edge ? tails | 1u << s : tails & ~(1u << s);
+          if (edge) open |= 1u << s;
           if (lane == 0) mbar_arrive_expect_tx(bar, (n - n0) * L::kHalves * box * 128);
           __syncwarp();
           if (mine >= n0 && mine < n) tma_load4(base + L::kRing + s * L::kTile + h * 16384 + mine * box * 128, map, h * 64, off, un.head, id, bar);
+          ks += 2;  // (also where a wait below runs out: the copy is on its way)
           if (held >= 0) ok = finish(held, un.from - un.t_begin * kKt, kKt);
           held = edge && t + 1 < un.t_end ? s : -1;
           if (ok && edge && held < 0) ok = finish(s, skip, keys);
@@ -369,15 +374,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
       }
-      if (!ok) {  // drain this warp's copies still in flight
-        if (nq) mbar_wait(q_full, (nq - 1) & 1, w, false);
-        for (int i = 1; i <= L::kStages; ++i) {
-          const int64_t k = static_cast<int64_t>(ks) - 2 * i;
-          if (k < 0 || k + L::kStages < ks) break;
-          const int s = static_cast<int>(k % L::kStages);
-          if (!(tails >> s & 1)) mbar_wait(kv_full(s), static_cast<uint32_t>(k / L::kStages) & 1, w, false);
-          else for (int spin = 0; spin < 4096 && !(mbar_try_wait(tail(s), 0) && mbar_try_wait(tail(s), 1)); ++spin) {}
-        }
+      // No CTA ends with a copy in flight, whoever gave up: both warps have issued
+      // their last load here, and each waits for those of its own that may not
+      // have landed, the last of a stage.  (All have where no wait ran out.)
+      if (lane == 0) last[kv] = ks;
+      __syncwarp();
+      asm volatile("bar.sync 1, 64;" ::: "memory");  // both load warps
+      if (nq) mbar_wait(q_full, (nq - 1) & 1, w, false);
+      for (int64_t k = static_cast<int64_t>(ks) - 2; k >= 0 && k + L::kStages + 2 > ks; k -= 2) {
+        const int s = static_cast<int>(k % L::kStages);
+        // the other warp has loaded the stage again: this load was used (with an even ring it never does)
+        if ((L::kStages & 1) && k + L::kStages < last[kv ^ 1]) continue;
+        if (!(tails >> s & 1)) mbar_wait(kv_full(s), static_cast<uint32_t>(k / L::kStages) & 1, w, false);
+        else if (open >> s & 1) mbar_wait(tail(s), phase >> s & 1, w, false);
       }
     } else {
       // ---------------------------------------------------------- UMMAs of lane t

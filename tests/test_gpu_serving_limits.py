@@ -54,3 +54,44 @@ def test_the_widest_windows(mmq, d, page, window, causal):  # noqa: F811
     p = _problem(BF16, [3, 20, 300], [5, 12, 40], 4, 2, d, page)
     out, lse = mmq.mmq_paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seq_lens"], p["q_start"], causal=causal, window=window, lse=True)
     _check_rows(p, out, lse, 1 / math.sqrt(d), causal, window)
+
+
+# ---------------------------------------------------------------- waits that run out
+@pytest.fixture
+def short_waits(mmq):  # noqa: F811
+    """Waits give up as soon as they look at the clock (after 256 polls, about a millisecond)."""
+    mmq.mmq_set_wait_timeout_ns(1)
+    yield
+    mmq.mmq_set_wait_timeout_ns(2 * 10 ** 9)
+
+
+def _late_problem(n, kv_len, d):
+    """Requests of which only the last ten have tokens (the first stretches of the plan's line, then, are theirs): adding up
+    the rooms of the others takes a CTA several milliseconds."""
+    p = _problem(F16, [1] * 10, [kv_len] * 10, 4, 2, d, 16)
+    lens, starts = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    table = torch.full((n, p["table"].shape[1]), -1, dtype=torch.int32, device="cuda")
+    lens[-10:], table[-10:] = kv_len, p["table"]
+    starts[-10:] = torch.arange(1, 11, dtype=torch.int32)
+    return p, (p["kc"], p["vc"], table, lens, starts)
+
+
+def _run_out(mmq, p, args, d):  # noqa: F811
+    """A call whose waits run out, between guard rows; then the same one with time."""
+    out, lse = torch.full((30, 4, d), 7.0, dtype=F16, device="cuda"), torch.full((30, 4), 7.0, device="cuda")
+    mmq.mmq_paged_attention(p["q"], *args, out=out[10:20], lse=lse[10:20])
+    assert mmq.mmq_last_device_error() == mmq.mmq.MMQ_ERR_DEVICE_TIMEOUT
+    for guard in (out[:10], out[20:], lse[:10], lse[20:]):
+        assert (guard == 7).all()
+    assert mmq.mmq_last_device_error() == 0
+    mmq.mmq_set_wait_timeout_ns(2 * 10 ** 9)
+    mmq.mmq_paged_attention(p["q"], *args, out=out[10:20], lse=lse[10:20])
+    _check_rows(p, out[10:20], lse[10:20], 1 / math.sqrt(d), True, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_waits_that_run_out_without_pieces(mmq, short_waits, d):  # noqa: F811
+    """A table too narrow for units to be cut: no partial results and no join, only the kernel's own way out."""
+    p, args = _late_problem(3 * 10 ** 6, 250, d)
+    assert args[2].shape[1] * 16 > 256
+    _run_out(mmq, p, (args[0], args[1], args[2][:, :16], *args[3:]), d)
