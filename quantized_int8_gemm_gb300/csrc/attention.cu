@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
   AttnSchedule<kKt, kRows> sched;
   griddep_wait();
   griddep_launch_dependents();
+  if (warp == 0) sched.no_cut(a);
   if (a.nreq > 32) {
     if (tid == 0) s_sums[kAttnSums] = 0;
     __syncthreads();

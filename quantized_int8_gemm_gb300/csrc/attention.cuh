@@ -119,7 +119,6 @@ struct AttnSchedule {
   int pos;          // where the current unit begins
   int b, qt, head;  // the current unit; b >= nreq: none
   AttnRequest cur;  // its request
-  bool cut;         // this CTA has told of its cut unit
 
   // K/V tiles of the rows of row tile q, and the first key that they see.
   __device__ __forceinline__ void tiles_of(const AttnArgs &a, const AttnRequest &x, int q, int &from, int &t0, int &t1) const {
@@ -216,10 +215,16 @@ struct AttnSchedule {
     if ((threadIdx.x & 31) == 0) atomicMax(sums + kAttnSums, longest);
   }
 
+  // This CTA's cut unit is none until next() finds one.  The join reads what
+  // is told here even where this CTA gives up, so the warp that calls next()
+  // comes here first, before anything that it waits for.
+  __device__ static __forceinline__ void no_cut(const AttnArgs &a) {
+    if (a.cuts && (threadIdx.x & 31) == 0) a.cuts[blockIdx.x].last = -1;
+  }
+
   // Finds this CTA's stretch and the first unit that reaches into it.  With more
   // than 32 requests `sums` is what add_up left.
   __device__ __forceinline__ void plan(const AttnArgs &a, const int *sums) {
-    cut = false;
     const int lane = threadIdx.x & 31, log2 = group_log2(a), groups = ((a.nreq - 1) >> log2) + 1;
     int total = 0, mine = 0, longest = 0;
     if (groups > 1) {
@@ -335,14 +340,9 @@ struct AttnSchedule {
       o.t_end = min(t1, t0 + (hi - first));
       const bool begins = c0 == me;
       o.slot = 2 * me + begins;
-      if (begins) {
-        cut = true;
-        if ((threadIdx.x & 31) == 0) a.cuts[me] = {o.q0, o.n, o.row0, o.head, c1};
-      }
+      if (begins && (threadIdx.x & 31) == 0) a.cuts[me] = {o.q0, o.n, o.row0, o.head, min(c1, static_cast<int>(gridDim.x) - 1)};
       return true;
     }
-    if (a.cuts && !cut && (threadIdx.x & 31) == 0) a.cuts[blockIdx.x].last = -1;
-    cut = true;
     return false;
   }
 };

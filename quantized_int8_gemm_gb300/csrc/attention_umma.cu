@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       AttnSchedule<kKt, 0> sched;
       if (kv == 0) {
+        sched.no_cut(a);
         if (a.nreq > 32) ok = wait(added, 0);
         if (ok) sched.plan(a, sums);
       }

@@ -95,3 +95,16 @@ def test_waits_that_run_out_without_pieces(mmq, short_waits, d):  # noqa: F811
     p, args = _late_problem(3 * 10 ** 6, 250, d)
     assert args[2].shape[1] * 16 > 256
     _run_out(mmq, p, (args[0], args[1], args[2][:, :16], *args[3:]), d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_waits_that_run_out_with_pieces(mmq, short_waits, d):  # noqa: F811
+    """Long keys, so that units are cut and a second kernel joins them: it may use nothing that no CTA wrote, whatever the
+    scratch holds from a larger call before."""
+    big = _problem(F16, [300, 200], [4000, 3000], 28, 4, d, 16)
+    for _ in range(2):
+        mmq.mmq_set_wait_timeout_ns(2 * 10 ** 9)
+        mmq.mmq_paged_attention(big["q"], big["kc"], big["vc"], big["table"], big["seq_lens"], big["q_start"])
+        mmq.mmq_set_wait_timeout_ns(1)
+        p, args = _late_problem(3 * 10 ** 6, 3000, d)
+        _run_out(mmq, p, args, d)
