@@ -403,8 +403,11 @@ int mmq_last_device_error(void) {
   mmq::DevStatus w;
   if (cudaMemcpy(&w, d->words, sizeof(w), cudaMemcpyDeviceToHost) != cudaSuccess)
     return cuda_rc(cudaErrorUnknown);
-  const int zero = 0;
-  if (cudaMemcpy(&d->words->status, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
+  // Both words: a captured call has the same epoch in every replay, so that an
+  // abort left standing would stop the next replays, and with the status
+  // cleared nothing would tell of it.
+  const mmq::DevStatus none = {mmq::DEVERR_NONE, 0};
+  if (cudaMemcpy(d->words, &none, sizeof(none), cudaMemcpyHostToDevice) != cudaSuccess)
     return cuda_rc(cudaErrorUnknown);
   return w.status == mmq::DEVERR_INDEX ? MMQ_ERR_DEVICE_INDEX : w.status ? MMQ_ERR_DEVICE_TIMEOUT : MMQ_OK;
 }

@@ -70,7 +70,8 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
 // Where a bounded wait reports to: a sticky per-device status word (read and
 // cleared by the host) and a per-device abort word holding the epoch of the
 // last launch that gave up.  Each launch has its own epoch, so a stale abort
-// never stops a later launch.
+// never stops a later launch; replays of a captured launch share one, so the host
+// clears both words together.
 struct WaitCtl {
   int *status;
   unsigned *abort_epoch;

@@ -108,3 +108,17 @@ def test_waits_that_run_out_with_pieces(mmq, short_waits, d):  # noqa: F811
         mmq.mmq_set_wait_timeout_ns(1)
         p, args = _late_problem(3 * 10 ** 6, 3000, d)
         _run_out(mmq, p, args, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_every_replay_of_a_captured_call_tells_of_its_waits(mmq, short_waits, d):  # noqa: F811
+    """A captured call that gave up once is not taken for one that has given up when it is replayed."""
+    p, args = _late_problem(3 * 10 ** 6, 3000, d)
+    out = torch.full((10, 4, d), 7.0, dtype=F16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mmq.mmq_paged_attention(p["q"], *args, out=out)
+    for _ in range(3):
+        graph.replay()
+        assert mmq.mmq_last_device_error() == mmq.mmq.MMQ_ERR_DEVICE_TIMEOUT
+        assert mmq.mmq_last_device_error() == 0
