@@ -369,7 +369,9 @@ typedef struct mmq_paged_cache {
  *   taken       device, int32, 2: pages taken from the front of free_pages;
  *               pages missing (free_pages too short or need > table_width;
  *               their table entries are -1).
- * New tokens past max_tokens get no slot.  nreq in 0..8192 (more:
+ * New tokens past max_tokens get no slot.  What is written (table among it)
+ * may overlap nothing else of the call: held_out is another buffer than held,
+ * seq_lens another than cached (MMQ_ERR_ARG).  nreq in 0..8192 (more:
  * MMQ_ERR_UNSUPPORTED).  One kernel, no scratch.  Errors: MMQ_ERR_ARG,
  * MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
  */

@@ -26,6 +26,21 @@ int check_cache(const mmq_paged_cache *c) {
   return MMQ_OK;
 }
 
+// A run of bytes, or `rows` of them `pitch` apart.
+struct Run {
+  uintptr_t at;
+  uint64_t bytes, pitch, rows;
+  template <class T>
+  Run(const T *p, int64_t n, int64_t stride = 0, int64_t count = 1)
+      : at(reinterpret_cast<uintptr_t>(p)), bytes(n * sizeof(T)), pitch(stride * sizeof(T)), rows(count) {}
+};
+// Whether a (one run) and b share a byte: the first row of b that ends behind a's begin is the one to look at.
+bool meet(const Run &a, const Run &b) {
+  if (!a.bytes || !b.bytes || !b.rows) return false;
+  const uint64_t r = a.at < b.at + b.bytes ? 0 : b.pitch ? (a.at - b.at - b.bytes) / b.pitch + 1 : b.rows;
+  return r < b.rows && b.at + r * b.pitch < a.at + a.bytes;
+}
+
 }  // namespace
 
 extern "C" {
@@ -41,6 +56,19 @@ int mmq_page_tables(const int32_t *cached, const int32_t *fresh, const int32_t *
   if (!q_start || !taken) return MMQ_ERR_ARG;
   if (nreq && (!cached || !fresh || !held || !seq_lens || !held_out)) return MMQ_ERR_ARG;
   if ((nreq && table_width && !table) || (nfree && !free_pages) || (max_tokens && (!slots || !positions))) return MMQ_ERR_ARG;
+  // CTAs read the lengths and the free list again after others have written
+  // theirs, so nothing that is written may lie on anything else.
+  const Run written[] = {{q_start, nreq + 1}, {seq_lens, nreq}, {held_out, nreq}, {slots, max_tokens}, {positions, max_tokens}, {taken, 2}};
+  const Run read[] = {{cached, nreq}, {fresh, nreq}, {held, nreq}, {free_pages, nfree}}, rows(table, table_width, table_stride, nreq);
+  for (const Run &w : written) {
+    if (meet(w, rows)) return MMQ_ERR_ARG;
+    for (const Run &x : written)
+      if (&x != &w && meet(w, x)) return MMQ_ERR_ARG;
+    for (const Run &x : read)
+      if (meet(w, x)) return MMQ_ERR_ARG;
+  }
+  for (const Run &x : read)
+    if (meet(x, rows)) return MMQ_ERR_ARG;
   mmq::CallContext ctx;
   if (int rc = mmq::call_context(&ctx)) return rc;
   mmq::PageTablesArgs a;

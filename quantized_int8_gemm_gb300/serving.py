@@ -49,7 +49,8 @@ def mmq_page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, n_blocks:
                     free_pages: torch.Tensor, page_size: int, max_tokens: int, out: PageTables | None = None,
                     stream=None) -> PageTables:
     """Pages for each request's new tokens from the front of free_pages (entered into block_table in place), and the
-    slot map of the step.  Lengths and pages are int32 CUDA tensors; `out`: buffers to fill instead of new ones."""
+    slot map of the step.  Lengths and pages are int32 CUDA tensors; `out`: buffers to fill instead of new ones, which (like
+    block_table) may overlap no other tensor of the call: a step's n_blocks is not the next one's out.n_blocks."""
     got = (_binding or _load()).page_tables(cached_lens, new_lens, n_blocks, block_table, free_pages, page_size, max_tokens, out,
                                             stream)
     rc = got if out is not None else got[0]

@@ -122,3 +122,64 @@ def test_every_replay_of_a_captured_call_tells_of_its_waits(mmq, short_waits, d)
         graph.replay()
         assert mmq.mmq_last_device_error() == mmq.mmq.MMQ_ERR_DEVICE_TIMEOUT
         assert mmq.mmq_last_device_error() == 0
+
+
+# ---------------------------------------------------------------- page tables
+def _tables_problem(n, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    cached = torch.randint(0, 400, (n,), generator=g)
+    new = torch.randint(0, 9, (n,), generator=g)
+    held = (cached + 15) // 16
+    width = int(((cached + new + 15) // 16).max()) + 1
+    need = int(((cached + new + 15) // 16 - held).sum())
+    order = torch.randperm(int(held.sum()) + need + 5, generator=g).int()
+    table = torch.full((n, width), -1, dtype=torch.int32)
+    at = 0
+    for b in range(n):
+        table[b, :held[b]] = order[at:at + held[b]]
+        at += int(held[b])
+    return [x.int().cuda() for x in (cached, new, held, table, order[at:])], int(new.sum()) + 3
+
+
+@pytest.mark.parametrize("n", [1, 7, 900])
+def test_page_tables_into_buffers(mmq, n):  # noqa: F811
+    (cached, new, held, table, free), room = _tables_problem(n)
+    other = table.clone()
+    want = mmq.mmq_page_tables(cached, new, held, table, free, 16, room)
+    buffers = [torch.full_like(x, 77) for x in want]
+    for out in (tuple(buffers), mmq.PageTables(*buffers)):
+        got = mmq.mmq_page_tables(cached, new, held, other, free, 16, room, out=out)
+        assert all(x is y for x, y in zip(got, buffers))
+        assert all(torch.equal(x, y) for x, y in zip(got, want)) and torch.equal(other, table)
+    # buffers of other shapes or types, and buffers that are the call's inputs or one another's
+    for i, x in enumerate(buffers):
+        for bad in (x[:-1], x.float()):
+            with pytest.raises(ValueError):
+                mmq.mmq_page_tables(cached, new, held, other, free, 16, room, out=tuple(buffers[:i] + [bad] + buffers[i + 1:]))
+    q_start, lens, blocks, slots, positions, taken = buffers
+    for out in ((q_start, lens, held, slots, positions, taken), (q_start, cached, blocks, slots, positions, taken),
+                (q_start, new, blocks, slots, positions, taken), (q_start, lens, lens, slots, positions, taken),
+                (q_start, lens, q_start[1:], slots, positions, taken)):
+        before = [x.clone() for x in (cached, new, held, other)]
+        with pytest.raises(mmq.MMQError) as e:
+            mmq.mmq_page_tables(cached, new, held, other, free, 16, room, out=out)
+        assert e.value.code == -1
+        assert all(torch.equal(x, y) for x, y in zip(before, (cached, new, held, other)))
+
+
+def test_steps_that_hand_their_buffers_on(mmq):  # noqa: F811
+    """A captured step with two sets of buffers that take turns, on lengths that stay on the device."""
+    (cached, new, held, table, free), room = _tables_problem(40, seed=4)
+    table = torch.cat([table, torch.full_like(table, -1)], 1)
+    again, lens, blocks = table.clone(), cached.clone(), held.clone()
+    sets = [tuple(torch.empty_like(x) for x in mmq.mmq_page_tables(cached, new, held, table.clone(), free, 16, room)) for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mmq.mmq_page_tables(cached, new, held, table, free, 16, room, out=sets[0])
+        mmq.mmq_page_tables(sets[0][1], new, sets[0][2], table, free, 16, room, out=sets[1])
+    graph.replay()
+    for got in sets:
+        want = mmq.mmq_page_tables(lens, new, blocks, again, free, 16, room)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        lens, blocks = want.seq_lens, want.n_blocks
+    assert torch.equal(table, again)

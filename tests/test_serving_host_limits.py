@@ -1,0 +1,57 @@
+"""The serving step's host side at the limits of its arguments, without a GPU: what the C ABI refuses before any device
+call.  Addresses are made up, so calls that it should take are made only where there is no device to take them."""
+import ctypes
+
+import pytest
+import torch
+
+from tests.test_serving_host import ARG, i32, i64, lib, vp  # noqa: F401
+
+NO_DEVICE = -8
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up")
+
+# nine requests, 40 table columns, 100 free pages, 70 token rows; 4096 bytes for each buffer, 64 for each row of the table
+BUFFERS = {"cached": 36, "fresh": 36, "held": 36, "free": 400, "q_start": 40, "seq_lens": 36, "held_out": 36, "slots": 560, "positions": 280,
+           "taken": 8}
+READ = ["cached", "fresh", "held", "free"]
+
+
+def _tables(lib, table=1 << 20, width=8, stride=16, **moved):  # noqa: F811
+    at = {name: 4096 * (i + 1) for i, name in enumerate(BUFFERS)}
+    at.update(moved)
+    return lib.mmq_page_tables(vp(at["cached"]), vp(at["fresh"]), vp(at["held"]), i64(9), vp(table), i64(width), i64(stride), vp(at["free"]),
+                               i64(100), i32(16), i64(70), vp(at["q_start"]), vp(at["seq_lens"]), vp(at["held_out"]), vp(at["slots"]),
+                               vp(at["positions"]), vp(at["taken"]), None)
+
+
+@pytest.mark.parametrize("other", BUFFERS)
+@pytest.mark.parametrize("out", [b for b in BUFFERS if b not in READ])
+def test_page_tables_written_over_something_else(lib, out, other):  # noqa: F811
+    if out == other:
+        return
+    base = 1 << 24
+    for at in (base, base + BUFFERS[other] - 8, base - BUFFERS[out] + 8):  # all of it, its end, its begin
+        assert _tables(lib, **{other: base, out: at}) == ARG, at - base
+
+
+@pytest.mark.parametrize("name", BUFFERS)
+def test_page_tables_written_over_the_table(lib, name):  # noqa: F811
+    table, row, pitch = 1 << 24, 32, 64
+    for at in (table, table - BUFFERS[name] + 8, table + 3 * pitch + row - 8, table + 8 * pitch + row - 8):
+        assert _tables(lib, table, **{name: at}) == ARG, at - table
+
+
+@no_gpu
+def test_page_tables_beside_one_another(lib):  # noqa: F811
+    assert _tables(lib) == NO_DEVICE
+    base = 1 << 24
+    for out in BUFFERS:
+        for other in BUFFERS:
+            if out != other:
+                assert _tables(lib, **{other: base, out: base + (BUFFERS[other] + 7) // 8 * 8}) == NO_DEVICE
+        # behind the table's last row; in the gap between two of them, where it is short enough
+        assert _tables(lib, base, **{out: base + 8 * 64 + 32}) == NO_DEVICE
+        if BUFFERS[out] <= 32:
+            assert _tables(lib, base, **{out: base + 4 * 64 + 32}) == NO_DEVICE
+    for a, b in (("cached", "fresh"), ("held", "cached"), ("free", "held")):  # what is only read may be one buffer
+        assert _tables(lib, **{a: base, b: base}) == NO_DEVICE
