@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const __grid_c
     a.positions[t] = position;
   }
   // new entries of the tables
-  const int stride = gridDim.x * kTabThreads;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kTabThreads;  // (2^31 with the most token rows)
   for (int64_t j = static_cast<int64_t>(blockIdx.x) * kTabThreads + tid; j < page_all; j += stride) {
     const int b = last_not_above(first_page, n, static_cast<int>(j));
     const int at = max(a.held[b], 0) + (static_cast<int>(j) - first_page[b]);

@@ -183,3 +183,19 @@ def test_steps_that_hand_their_buffers_on(mmq):  # noqa: F811
         assert all(torch.equal(x, y) for x, y in zip(got, want))
         lens, blocks = want.seq_lens, want.n_blocks
     assert torch.equal(table, again)
+
+
+def test_page_tables_of_the_most_token_rows(mmq):  # noqa: F811
+    """2^31 - 1 rows: the CTAs' threads together are 2^31."""
+    room = 2 ** 31 - 1
+    table = torch.full((3, 9), 77, dtype=torch.int32, device="cuda")
+    table[:, 0] = _i32([5, 6, 7])
+    free = _i32(list(range(20, 40)))
+    t = mmq.mmq_page_tables(_i32([4, 0, 9]), _i32([9, 40, 0]), _i32([1, 1, 1]), table, free, 16, room)
+    assert t.q_start.tolist() == [0, 9, 49, 49] and t.taken.tolist() == [2, 0] and t.n_blocks.tolist() == [1, 3, 1]
+    assert table.tolist() == [[5] + [77] * 8, [6, 20, 21] + [77] * 6, [7] + [77] * 8]
+    want = [5 * 16 + 4 + i for i in range(9)] + [(6, 20, 21)[i // 16] * 16 + i % 16 for i in range(40)]
+    assert t.slots[:49].tolist() == want and t.positions[:49].tolist() == list(range(4, 13)) + list(range(40))
+    for x in (t.slots, t.positions):
+        for part in x[49:].split(2 ** 28):
+            assert int(part.max()) == -1 and int(part.min()) == -1
