@@ -409,7 +409,7 @@ typedef struct mmq_attention {
   int64_t q_token, q_head;   /* strides in elements, multiples of 8 */
   int64_t out_token, out_head;
   int64_t table_stride;
-  int64_t nreq, ntok;        /* requests; rows of q */
+  int64_t nreq, ntok;        /* requests; rows of q (ntok * q_heads below 2^31 - 512) */
   int32_t table_width;
   int32_t q_heads;           /* a multiple of cache->heads: q head h reads K/V head h / (q_heads / heads) */
   int32_t out_type;          /* the cache's type or MMQ_DT_F32 */

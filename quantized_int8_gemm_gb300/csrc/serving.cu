@@ -107,7 +107,7 @@ int mmq_paged_attention(const mmq_paged_cache *cache, const mmq_attention *args,
     return MMQ_ERR_ARG;
   if (!(t.scale > 0.0f) || std::isinf(t.scale)) return MMQ_ERR_ARG;
   if (t.q_token < 0 || t.q_head < 0 || t.out_token < 0 || t.out_head < 0) return MMQ_ERR_ARG;
-  if (t.ntok > kInt32 / t.q_heads) return MMQ_ERR_ARG;  // rows are counted in 32 bits
+  if (t.ntok > (kInt32 - 512) / t.q_heads) return MMQ_ERR_ARG;  // rows are counted in 32 bits, a unit's past the last one
   if (t.nreq == 0 || t.ntok == 0) return MMQ_OK;
   if (!t.q || !t.out || !t.seq_lens || !t.q_start || (t.table_width && !t.table)) return MMQ_ERR_ARG;
   if (!aligned(t.q, 16) || !aligned(t.out, 16) || (t.q_token | t.q_head | t.out_token | t.out_head) % 8) return MMQ_ERR_ALIGN;

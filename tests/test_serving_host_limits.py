@@ -55,3 +55,15 @@ def test_page_tables_beside_one_another(lib):  # noqa: F811
             assert _tables(lib, base, **{out: base + 4 * 64 + 32}) == NO_DEVICE
     for a, b in (("cached", "fresh"), ("held", "cached"), ("free", "held")):  # what is only read may be one buffer
         assert _tables(lib, **{a: base, b: base}) == NO_DEVICE
+
+
+def test_attention_rows_whose_numbers_would_wrap(lib):  # noqa: F811
+    """A row tile's rows are numbered past the last one: 2^31 less a unit's rows is the most."""
+    import tests.test_serving_host as host
+    cache = host._cache(heads=1, head_dim=8)
+    for heads in (1, 8, 160):
+        most = (2 ** 31 - 1 - 512) // heads
+        for ntok in (most + 1, (2 ** 31 - 1) // heads):
+            a = host.Attention(q=4096, out=4096, table=4096, seq_lens=4096, q_start=4096, q_token=8 * heads, q_head=8, out_token=8 * heads, out_head=8,
+                               table_stride=8, nreq=1, ntok=ntok, table_width=8, q_heads=heads, out_type=1, causal=1, scale=0.1)
+            assert lib.mmq_paged_attention(ctypes.byref(cache), ctypes.byref(a), None) == ARG
