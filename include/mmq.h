@@ -391,7 +391,8 @@ int mmq_page_tables(const int32_t *cached, const int32_t *fresh, const int32_t *
  *            the cache writes nothing and is reported by
  *            mmq_last_device_error; a slot twice leaves either row.
  *   ntok     >= 0; 0 is a no-op.
- * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN, MMQ_ERR_TYPE, MMQ_ERR_NO_DEVICE,
+ * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN, MMQ_ERR_TYPE, MMQ_ERR_UNSUPPORTED
+ * (a token's K and V of more than 2^33 elements), MMQ_ERR_NO_DEVICE,
  * MMQ_ERR_CUDA.
  */
 int mmq_kv_write(const mmq_paged_cache *cache, const void *k, int64_t k_token, int64_t k_head, const void *v,

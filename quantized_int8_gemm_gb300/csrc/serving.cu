@@ -85,6 +85,7 @@ int mmq_kv_write(const mmq_paged_cache *cache, const void *k, int64_t k_token, i
   if (int rc = check_cache(cache)) return rc;
   if (src_type != MMQ_DT_F32 && src_type != MMQ_DT_F16 && src_type != MMQ_DT_BF16) return MMQ_ERR_TYPE;
   if (ntok < 0 || ntok > kInt32 || k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0) return MMQ_ERR_ARG;
+  if (cache->heads > (int64_t(1) << 30) / (2 * (cache->head_dim / 8))) return MMQ_ERR_UNSUPPORTED;  // a token's chunks, in 32 bits
   if (ntok == 0) return MMQ_OK;
   if (!k || !v || !slots) return MMQ_ERR_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) || (k_token | k_head | v_token | v_head) % 8) return MMQ_ERR_ALIGN;

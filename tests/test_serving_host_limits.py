@@ -5,7 +5,7 @@ import ctypes
 import pytest
 import torch
 
-from tests.test_serving_host import ARG, i32, i64, lib, vp  # noqa: F401
+from tests.test_serving_host import ARG, UNSUPPORTED, i32, i64, lib, vp  # noqa: F401
 
 NO_DEVICE = -8
 no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up")
@@ -67,3 +67,10 @@ def test_attention_rows_whose_numbers_would_wrap(lib):  # noqa: F811
             a = host.Attention(q=4096, out=4096, table=4096, seq_lens=4096, q_start=4096, q_token=8 * heads, q_head=8, out_token=8 * heads, out_head=8,
                                table_stride=8, nreq=1, ntok=ntok, table_width=8, q_heads=heads, out_type=1, causal=1, scale=0.1)
             assert lib.mmq_paged_attention(ctypes.byref(cache), ctypes.byref(a), None) == ARG
+
+
+def test_kv_rows_whose_items_would_wrap(lib):  # noqa: F811
+    import tests.test_serving_host as host
+    for heads, d in ((2 ** 27, 64), (2 ** 26 + 1, 64), (2 ** 31 - 1, 8), (2 ** 25 + 1, 128)):
+        cache = host._cache(heads=heads, head_dim=d)
+        assert lib.mmq_kv_write(ctypes.byref(cache), vp(4096), i64(128), i64(64), vp(4096), i64(128), i64(64), 2, vp(4096), i64(1), None) == UNSUPPORTED
