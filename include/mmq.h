@@ -373,7 +373,8 @@ typedef struct mmq_paged_cache {
  * may overlap nothing else of the call: held_out is another buffer than held,
  * seq_lens another than cached (MMQ_ERR_ARG).  nreq in 0..8192 (more:
  * MMQ_ERR_UNSUPPORTED).  One kernel, no scratch.  Errors: MMQ_ERR_ARG,
- * MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
+ * MMQ_ERR_ALIGN (elements off their own alignment), MMQ_ERR_UNSUPPORTED,
+ * MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
  */
 int mmq_page_tables(const int32_t *cached, const int32_t *fresh, const int32_t *held, int64_t nreq,
                     int32_t *table, int64_t table_width, int64_t table_stride, const int32_t *free_pages,

@@ -9,6 +9,8 @@
 namespace {
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+template <class... T>
+bool aligned_elements(const T *...p) { return (aligned(p, alignof(T)) && ...); }
 int cuda_rc(cudaError_t e) {
   if (e == cudaSuccess) return MMQ_OK;
   cudaGetLastError();
@@ -69,6 +71,7 @@ int mmq_page_tables(const int32_t *cached, const int32_t *fresh, const int32_t *
   }
   for (const Run &x : read)
     if (meet(x, rows)) return MMQ_ERR_ARG;
+  if (!aligned_elements(cached, fresh, held, table, free_pages, q_start, seq_lens, held_out, slots, positions, taken)) return MMQ_ERR_ALIGN;
   mmq::CallContext ctx;
   if (int rc = mmq::call_context(&ctx)) return rc;
   mmq::PageTablesArgs a;
@@ -111,6 +114,7 @@ int mmq_paged_attention(const mmq_paged_cache *cache, const mmq_attention *args,
   if (t.ntok > (kInt32 - 512) / t.q_heads) return MMQ_ERR_ARG;  // rows are counted in 32 bits, a unit's past the last one
   if (t.nreq == 0 || t.ntok == 0) return MMQ_OK;
   if (!t.q || !t.out || !t.seq_lens || !t.q_start || (t.table_width && !t.table)) return MMQ_ERR_ARG;
+  if (!aligned_elements(t.lse, t.table, t.seq_lens, t.q_start)) return MMQ_ERR_ALIGN;
   if (!aligned(t.q, 16) || !aligned(t.out, 16) || (t.q_token | t.q_head | t.out_token | t.out_head) % 8) return MMQ_ERR_ALIGN;
   mmq::CallContext ctx;
   if (int rc = mmq::call_context(&ctx)) return rc;
@@ -128,7 +132,8 @@ int mmq_verify_draft(const mmq_verification *args, mmq_stream_t stream) {
   if (t.nreq == 0) return MMQ_OK;
   if (!t.target || !t.noise || !t.out || !t.accepted || (t.k && (!t.tokens || !t.u))) return MMQ_ERR_ARG;
   const uintptr_t esz = t.type == MMQ_DT_F32 ? 4 : 2;
-  if (!aligned(t.target, esz) || !aligned(t.draft, esz) || !aligned(t.noise, 4) || !aligned(t.u, 4)) return MMQ_ERR_ALIGN;
+  if (!aligned(t.target, esz) || !aligned(t.draft, esz)) return MMQ_ERR_ALIGN;
+  if (!aligned_elements(t.tokens, t.n_draft, t.u, t.noise, t.out, t.accepted)) return MMQ_ERR_ALIGN;
   mmq::CallContext ctx;
   if (int rc = mmq::call_context(&ctx)) return rc;
   mmq::VerifyArgs a;

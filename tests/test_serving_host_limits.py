@@ -5,7 +5,7 @@ import ctypes
 import pytest
 import torch
 
-from tests.test_serving_host import ARG, UNSUPPORTED, i32, i64, lib, vp  # noqa: F401
+from tests.test_serving_host import ALIGN, ARG, UNSUPPORTED, i32, i64, lib, vp  # noqa: F401
 
 NO_DEVICE = -8
 no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up")
@@ -74,3 +74,21 @@ def test_kv_rows_whose_items_would_wrap(lib):  # noqa: F811
     for heads, d in ((2 ** 27, 64), (2 ** 26 + 1, 64), (2 ** 31 - 1, 8), (2 ** 25 + 1, 128)):
         cache = host._cache(heads=heads, head_dim=d)
         assert lib.mmq_kv_write(ctypes.byref(cache), vp(4096), i64(128), i64(64), vp(4096), i64(128), i64(64), 2, vp(4096), i64(1), None) == UNSUPPORTED
+
+
+def test_pointers_off_their_elements_alignment(lib):  # noqa: F811
+    """Such an access would fault on the device."""
+    import tests.test_serving_host as host
+    for name in BUFFERS:
+        for off in (1, 2) + ((4,) if name == "slots" else ()):
+            assert _tables(lib, **{name: 4096 * 50 + off}) == ALIGN, (name, off)
+    assert _tables(lib, (1 << 20) + 2) == ALIGN
+    base = dict(q=4096, out=4096, lse=4096, table=4096, seq_lens=4096, q_start=4096, q_token=512, q_head=64, out_token=512, out_head=64, table_stride=8,
+                nreq=1, ntok=1, table_width=8, q_heads=8, out_type=1, causal=1, window=0, scale=0.1)
+    cache = host._cache()
+    for name in ("lse", "table", "seq_lens", "q_start"):
+        assert lib.mmq_paged_attention(ctypes.byref(cache), ctypes.byref(host.Attention(**{**base, name: 4098})), None) == ALIGN, name
+    base = dict(target=4096, draft=4096, tokens=4096, n_draft=4096, u=4096, noise=4096, out=4096, accepted=4096, target_req=64, target_row=32,
+                draft_req=32, draft_row=32, tokens_stride=1, u_stride=1, noise_stride=32, nreq=1, vocab=32, k=1, type=1)
+    for name in ("tokens", "n_draft", "u", "noise", "out", "accepted"):
+        assert lib.mmq_verify_draft(ctypes.byref(host.Verification(**{**base, name: 4098})), None) == ALIGN, name
