@@ -254,7 +254,8 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const mmq_paged_cache c = paged_cache(a[1], a[2], dev);
     const Rows qr = rows3(q, "q");
     const int64_t ntok = q.size(0), hq = q.size(1);
-    if (type_of(q.scalar_type()) != c.type || q.size(2) != c.head_dim || hq < 1 || hq > INT32_MAX || hq % c.heads)
+    // (a cache without heads is the library's to refuse)
+    if (type_of(q.scalar_type()) != c.type || q.size(2) != c.head_dim || hq < 1 || hq > INT32_MAX || (c.heads && hq % c.heads))
       fail(PyExc_ValueError, "q must be (tokens, a multiple of %d, %d) of the cache's type", c.heads, c.head_dim);
     mmq_attention t;
     t.scale = a[6] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.head_dim)))

@@ -199,3 +199,15 @@ def test_page_tables_of_the_most_token_rows(mmq):  # noqa: F811
     for x in (t.slots, t.positions):
         for part in x[49:].split(2 ** 28):
             assert int(part.max()) == -1 and int(part.min()) == -1
+
+
+# ---------------------------------------------------------------- the binding
+def test_a_cache_without_heads_is_refused(mmq):  # noqa: F811
+    p = _problem(F16, [2], [40], 4, 2, 64, 16)
+    none = p["kc"][:, :, :0]
+    with pytest.raises(mmq.MMQError) as e:
+        mmq.mmq_paged_attention(p["q"], none, none, p["table"], p["seq_lens"], p["q_start"])
+    assert e.value.code == -1
+    with pytest.raises(mmq.MMQError) as e:
+        mmq.mmq_kv_write(p["q"][:, :0], p["q"][:, :0], none, none, torch.zeros(2, dtype=torch.int64, device="cuda"))
+    assert e.value.code == -1
