@@ -262,6 +262,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
                               : static_cast<float>(PyFloat_AsDouble(a[6]));
     if (PyErr_Occurred()) throw PyFail{};
     t.causal = PyObject_IsTrue(a[7]);
+    if (t.causal < 0) throw PyFail{};
     t.window = small(a[8], "window");
     const at::Tensor &lens = on(a[4], "seq_lens", dev);
     if (lens.dim() != 1) fail(PyExc_ValueError, "seq_lens must have 1 dimension");

@@ -211,3 +211,11 @@ def test_a_cache_without_heads_is_refused(mmq):  # noqa: F811
     with pytest.raises(mmq.MMQError) as e:
         mmq.mmq_kv_write(p["q"][:, :0], p["q"][:, :0], none, none, torch.zeros(2, dtype=torch.int64, device="cuda"))
     assert e.value.code == -1
+
+
+def test_an_argument_without_a_truth_value_is_an_error(mmq):  # noqa: F811
+    p = _problem(F16, [2], [40], 4, 2, 64, 16)
+    out = torch.full_like(p["q"], 7.0)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        mmq.mmq_paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seq_lens"], p["q_start"], causal=torch.ones(2), out=out)
+    assert (out == 7).all()
