@@ -10,7 +10,8 @@ One step, for any mixture of requests and new tokens:
   mmq_paged_attention  the new tokens over their requests' pages, fp32 out
   mmq_gemm_f32         output projection (q6_K), then the vocabulary's (q4_K)
   mmq_verify_draft     drafted tokens against the target's probabilities; the accepted counts are the next lengths
-Lengths, page tables and accepted counts stay on the GPU.  Weights are synthetic, the block has no norm
+Lengths, page tables and accepted counts stay on the GPU; the host reads how many pages a step took (and whether any
+were missing), to cut them off its free list, and the tokens to return.  Weights are synthetic, the block has no norm
 weights and no rotation: it shows the calls, not a trained model."""
 from __future__ import annotations
 
@@ -71,9 +72,15 @@ class Block:
         return torch.stack(tokens, 1), torch.stack(probs, 1)
 
 
+def pages_of(lens, steps: int, drafted: int = 3, page_size: int = 16) -> int:
+    """Pages that serve() needs at the most for prompts of these lengths."""
+    return sum(-(-(n + steps * (drafted + 1)) // page_size) for n in lens)
+
+
 def serve(block: Block, prompts: list[torch.Tensor], steps: int = 4, drafted: int = 3, chunk: int = 64, seed: int = 1):
     """Runs the prompts through the block in chunks, then `steps` steps of `drafted` drafted tokens.  Returns the
-    requests' tokens (lists) and the last step's logits of each request's first new token."""
+    requests' tokens (lists) and the last step's logits of each request's first new token.  RuntimeError if the block's
+    cache is too small (pages_of)."""
     dev = torch.device("cuda")
     b = len(prompts)
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
@@ -86,9 +93,11 @@ def serve(block: Block, prompts: list[torch.Tensor], steps: int = 4, drafted: in
     def step(new, tokens):
         nonlocal free, held
         t = mmq.mmq_page_tables(cached, new, held, table, free, block.page, tokens.numel())
-        logits = block.forward(tokens, t, table)
-        free, held = free.roll(-int(t.taken[0])), t.n_blocks  # (a real scheduler keeps its free list on either side)
-        return t, logits
+        taken, missing = t.taken.tolist()
+        if missing:
+            raise RuntimeError(f"the cache is short of {missing} pages")
+        free, held = free[taken:], t.n_blocks
+        return t, block.forward(tokens, t, table)
 
     done = [0] * b
     while any(done[i] < len(p) for i, p in enumerate(prompts)):  # prompts, a chunk of each at a time
@@ -118,9 +127,10 @@ def main():
     ap.add_argument("--steps", type=int, default=8)
     ap.add_argument("--requests", type=int, default=5)
     a = ap.parse_args()
-    block = Block()
+    lens = [7 + 53 * i for i in range(a.requests)]
+    block = Block(pages=max(1, pages_of(lens, a.steps)))
     g = torch.Generator(device="cuda").manual_seed(0)
-    prompts = [torch.randint(0, block.vocab, (7 + 53 * i,), generator=g, device="cuda", dtype=torch.int32) for i in range(a.requests)]
+    prompts = [torch.randint(0, block.vocab, (n,), generator=g, device="cuda", dtype=torch.int32) for n in lens]
     out, _ = serve(block, prompts, a.steps)
     for p, t in zip(prompts, out):
         print(f"prompt of {len(p)} tokens, then {len(t) - len(p)}: {t[len(p):]}")
