@@ -1,7 +1,7 @@
 """Builds libmmq.so in-tree: every .cu under csrc/ compiled for sm_103a only,
 in parallel, then linked into one shared library next to this file; and
-_serving.so, the Python binding of the serving step (csrc/binding.cpp against
-torch's headers)."""
+_serving.<ABI>.so, the Python binding of the serving step (csrc/binding.cpp
+against torch's headers, so it names the Python and torch that it is for)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -16,7 +16,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmmq.so")
-BINDING = os.path.join(PKG, "_serving.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -39,10 +38,16 @@ def _deps():
         os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def binding_path() -> str:
+    """Where the binding for the running Python and torch is: their C++ layouts differ from version to version."""
+    import torch
+    return os.path.join(PKG, f"_serving.{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}.so")
+
+
 def up_to_date() -> bool:
     def newer(target, deps):
         return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
-    return newer(LIB, _deps()) and newer(BINDING, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "mmq.h")])
+    return newer(LIB, _deps()) and newer(binding_path(), [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "mmq.h")])
 
 
 def _build_binding():
@@ -50,7 +55,8 @@ def _build_binding():
     home = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = BINDING + f".tmp{os.getpid()}"
+    target = binding_path()
+    tmp = target + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}", "-isystem", home, "-isystem",
            os.path.join(home, "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
            "-I" + sysconfig.get_paths()["include"], f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -58,7 +64,7 @@ def _build_binding():
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+    os.replace(tmp, target)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

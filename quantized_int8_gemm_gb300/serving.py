@@ -13,19 +13,20 @@ from typing import NamedTuple
 
 import torch
 
-from .mmq import _PKG, MMQError, load
+from .mmq import MMQError, load
 
-BINDING_PATH = os.path.join(_PKG, "_serving.so")
 _binding = None
 
 
 def _load():
     """The compiled binding, bound to the loaded library."""
     global _binding
+    from .build import binding_path
     lib = load()
-    if not os.path.exists(BINDING_PATH):
-        raise RuntimeError(f"_serving.so not built ({BINDING_PATH}); run quantized_int8_gemm_gb300.build.build()")
-    spec = importlib.util.spec_from_file_location("quantized_int8_gemm_gb300._serving", BINDING_PATH)
+    path = binding_path()
+    if not os.path.exists(path):
+        raise RuntimeError(f"the serving binding is not built for this Python and torch ({path}); run quantized_int8_gemm_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("quantized_int8_gemm_gb300._serving", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.mmq_page_tables, lib.mmq_kv_write, lib.mmq_paged_attention,
