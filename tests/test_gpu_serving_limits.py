@@ -1,11 +1,12 @@
 """The serving step's operators at the limits of their arguments: rows that a step has no room for, extreme windows, waits
 that run out, buffers given by the caller.  Problems, references and tolerances are those of test_gpu_serving.py."""
 import math
+import threading
 
 import pytest
 import torch
 
-from tests.test_gpu_serving import BF16, F16, _i32, _no_device_error, _problem, _reference, mmq  # noqa: F401
+from tests.test_gpu_serving import BF16, F16, UNIT, _i32, _no_device_error, _problem, _reference, mmq  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -54,6 +55,102 @@ def test_the_widest_windows(mmq, d, page, window, causal):  # noqa: F811
     p = _problem(BF16, [3, 20, 300], [5, 12, 40], 4, 2, d, page)
     out, lse = mmq.mmq_paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seq_lens"], p["q_start"], causal=causal, window=window, lse=True)
     _check_rows(p, out, lse, 1 / math.sqrt(d), causal, window)
+
+
+# ---------------------------------------------------------------- infinities and NaN that rows do see
+def _put(p, which, b, key, at, value):
+    page = p["kc"].shape[1]
+    (p["keys"] if which == "kc" else p["values"])[b][key, :, at] = value
+    p[which][p["table"][b, key // page], key % page, :, at] = value
+
+
+def _reference_without(p, gone, scale):
+    """As _reference (causal), with the key gone[b] of request b left out of its rows' sums."""
+    q = p["q"].double()
+    out, tol = torch.zeros_like(q), torch.zeros_like(q)
+    lse = torch.full(q.shape[:2], -math.inf, dtype=torch.float64, device="cuda")
+    lse_tol = torch.zeros_like(lse)
+    u = UNIT[p["q"].dtype]
+    at = 0
+    for n, length, k, v, key in zip(p["q_lens"], p["kv_lens"], p["keys"], p["values"], gone):
+        rep = q.shape[1] // k.shape[1]
+        keep = [j for j in range(length) if j != key]
+        kk, vv = (x[keep].double().repeat_interleave(rep, 1).permute(1, 0, 2) for x in (k, v))
+        x = q[at:at + n].permute(1, 0, 2)
+        s = x @ kk.transpose(1, 2) * scale
+        size = (x.abs() @ kk.abs().transpose(1, 2) * scale).amax(-1)
+        hidden = torch.tensor(keep, device="cuda") > torch.arange(length - n, length, device="cuda")[:, None]
+        w = torch.softmax(s.masked_fill(hidden, -math.inf), -1)
+        o, mass = w @ vv, w @ vv.abs()
+        out[at:at + n] = o.permute(1, 0, 2)
+        tol[at:at + n] = (u * (mass + o.abs()) * 1.0625 + 1e-4 * mass).permute(1, 0, 2)
+        lse[at:at + n] = torch.logsumexp(s.masked_fill(hidden, -math.inf), -1).T
+        lse_tol[at:at + n] = (2.0 ** -20 * size + 1e-5).T
+        at += n
+    return out, lse, tol, lse_tol
+
+
+NOT_FINITE = [(64, 16, [150, 1], [900, 700]), (128, 16, [150, 1], [900, 700]), (128, 5, [70, 1], [300, 700]), (256, 16, [40, 1], [130, 700]),
+              (128, 64, [1, 2], [9000, 20000]), (64, 16, [1, 2], [9000, 20000]), (128, 3, [1, 2], [9000, 20000])]
+
+
+@pytest.mark.parametrize("d,page,q_lens,kv_lens", NOT_FINITE)
+@pytest.mark.parametrize("back", [0, 30, 600])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_a_key_that_is_not_finite(mmq, d, page, q_lens, kv_lens, back, value):  # noqa: F811
+    """One element of one key of each request, `back` places before the last.  Rows whose score of it is NaN or +inf are NaN;
+    rows whose score is -inf give it no weight; rows that do not see it are as they were.  (bf16: no smallest weight to add
+    to the tolerance.)"""
+    p = _problem(BF16, q_lens, kv_lens, 8, 2, d, page, seed=back)
+    p["q"][:, :, 1][p["q"][:, :, 1] == 0] = 1
+    gone = [max(0, length - 1 - back) for length in kv_lens]
+    for b, key in enumerate(gone):
+        _put(p, "kc", b, key, 1, value)
+    out, lse = mmq.mmq_paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seq_lens"], p["q_start"], lse=True)
+    seen = torch.cat([torch.arange(length - n, length) >= key for n, length, key in zip(q_lens, kv_lens, gone)]).cuda()[:, None]
+    spoilt = seen & (p["q"][:, :, 1] > 0) if value == math.inf else seen.expand(lse.shape)
+    assert torch.isnan(out[spoilt]).all() and torch.isnan(lse[spoilt]).all()
+    ref, z, tol, z_tol = _reference_without(p, gone, 1 / math.sqrt(d))
+    assert ((out.double() - ref).abs() <= tol)[~spoilt].all()
+    assert ((lse.double() - z).abs() <= z_tol)[~spoilt].all()
+
+
+@pytest.mark.parametrize("d,page,q_lens,kv_lens", NOT_FINITE)
+@pytest.mark.parametrize("back", [0, 30, 600])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_a_value_that_is_not_finite(mmq, d, page, q_lens, kv_lens, back, value):  # noqa: F811
+    """One element of one V row of each request: that column of the rows that see it is not finite (a row of the same chunk
+    that does not see it may be either), the other columns and every lse are as they were."""
+    p = _problem(BF16, q_lens, kv_lens, 8, 2, d, page, seed=back)
+    ref, z, tol, z_tol = _reference(p, 1 / math.sqrt(d), True, 0)
+    for b, length in enumerate(kv_lens):
+        _put(p, "vc", b, max(0, length - 1 - back), 1, value)
+    out, lse = mmq.mmq_paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seq_lens"], p["q_start"], lse=True)
+    seen = torch.cat([torch.arange(length - n, length) >= max(0, length - 1 - back) for n, length in zip(q_lens, kv_lens)]).cuda()
+    assert not torch.isfinite(out[seen][:, :, 1]).any()
+    others = [i for i in range(d) if i != 1]
+    assert ((out.double() - ref).abs() <= tol)[:, :, others].all()
+    assert ((lse.double() - z).abs() <= z_tol).all()
+
+
+def test_calls_of_two_threads_on_two_streams(mmq):  # noqa: F811
+    """Each call has scratch of its own: the bits are those of calls one after another."""
+    problems = [_problem(BF16, [300, 1, 5], [4000, 900, 3000], 28, 4, 128, 16, seed=1), _problem(F16, [1] * 6, [3000, 17, 900, 4000, 1, 250], 8, 2, 64, 16, seed=2)]
+
+    def call(p, stream=None):
+        return mmq.mmq_paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seq_lens"], p["q_start"], lse=True, stream=stream)
+
+    want = [call(p) for p in problems]
+    torch.cuda.synchronize()
+    got, streams = [[], []], [torch.cuda.Stream(), torch.cuda.Stream()]
+    threads = [threading.Thread(target=lambda i=i: got[i].extend(call(problems[i], streams[i]) for _ in range(50))) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert len(g) == 50 and all(torch.equal(x, y) for pair in g for x, y in zip(pair, w))
 
 
 # ---------------------------------------------------------------- waits that run out
