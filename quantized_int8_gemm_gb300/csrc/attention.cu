@@ -165,8 +165,10 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
     for (int j = 0; j < kDp / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     int lo[2], hi[2];
+    // (from shared memory, not from the copy in registers, of which the loop has none to spare: 119.5 against 123.2 us for
+    // 512 tokens over 4608 keys, pages of 5)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) attn_row_range(a, un.place, un.len, a.by_rep(un.row0 + warp * 16 + (lane >> 2) + 8 * h), lo[h], hi[h]);
+    for (int h = 0; h < 2; ++h) attn_row_range(a, s_unit.place, s_unit.len, a.by_rep(s_unit.row0 + warp * 16 + (lane >> 2) + 8 * h), lo[h], hi[h]);
 
     for (int t = un.t_begin; t < un.t_end; ++t) {
       const int buf = (t - un.t_begin) & 1;

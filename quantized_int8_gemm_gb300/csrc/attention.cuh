@@ -58,13 +58,11 @@ struct AttnRequest {
   int q0, n;  // first token, tokens that q has rows for
   int place;  // of its first token among the keys (below 0 if it has more new tokens than keys)
   int len;    // keys that its rows see at most
-  int tiles;  // row tiles
 };
 
 struct AttnLengths {
   int from, to, len;
 };
-template <int kRows>
 __device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, const AttnLengths &x) {
   AttnRequest r;
   const int ntok = static_cast<int>(a.ntok), from = x.from, to = x.to, len = x.len;
@@ -82,7 +80,6 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, const Att
   // where the last row's do, since nothing wrote those of the tokens behind it.
   r.place = r.len - (max(r.q0, to) - r.q0);
   if (a.causal) r.len = max(0, r.place + r.n);
-  r.tiles = kRows ? (r.n * a.rep + kRows - 1) / max(kRows, 1) : a.by_unit_tok(r.n + a.unit_tok - 1);
   return r;
 }
 
@@ -120,6 +117,11 @@ struct AttnSchedule {
   int b, qt, head;  // the current unit; b >= nreq: none
   AttnRequest cur;  // its request
 
+  // Row tiles of n tokens (worked out where they are wanted: the requests at
+  // hand stay in registers beside the attention itself).
+  __device__ static __forceinline__ int row_tiles(const AttnArgs &a, int n) {
+    return kRows ? (n * a.rep + kRows - 1) / max(kRows, 1) : a.by_unit_tok(n + a.unit_tok - 1);
+  }
   // K/V tiles of the rows of row tile q, and the first key that they see.
   __device__ __forceinline__ void tiles_of(const AttnArgs &a, const AttnRequest &x, int q, int &from, int &t0, int &t1) const {
     int to, none;
@@ -138,7 +140,7 @@ struct AttnSchedule {
   }
   __device__ __forceinline__ AttnRequest lane_request(int l) const {
     return {__shfl_sync(0xffffffffu, r.q0, l), __shfl_sync(0xffffffffu, r.n, l), __shfl_sync(0xffffffffu, r.place, l),
-            __shfl_sync(0xffffffffu, r.len, l), __shfl_sync(0xffffffffu, r.tiles, l)};
+            __shfl_sync(0xffffffffu, r.len, l)};
   }
   __device__ static __forceinline__ AttnLengths lengths(const AttnArgs &a, int from) {
     const int at = from + static_cast<int>(threadIdx.x & 31);
@@ -148,7 +150,7 @@ struct AttnSchedule {
   }
   __device__ __forceinline__ void load(const AttnArgs &a, int from) {
     b0 = from;
-    r = attn_request<kRows>(a, lengths(a, from));
+    r = attn_request(a, lengths(a, from));
   }
   __device__ static __forceinline__ int inclusive(int x) {
 #pragma unroll
@@ -162,18 +164,20 @@ struct AttnSchedule {
   __device__ __forceinline__ int lane_room(const AttnArgs &a, int &longest) const {
     const int lane = threadIdx.x & 31;
     int sum = 0;
-    if (r.tiles == 1) {
+    const int own = row_tiles(a, r.n);
+    if (own == 1) {
       sum = room_of(a, r, 0);
       longest = max(longest, sum);
     }
-    uint32_t many = __ballot_sync(0xffffffffu, r.tiles > 1);
+    uint32_t many = __ballot_sync(0xffffffffu, own > 1);
     while (many) {
       const int l = __ffs(many) - 1;
       many &= many - 1;
       const AttnRequest x = lane_request(l);
+      const int tiles = __shfl_sync(0xffffffffu, own, l);
       int part = 0;
 #pragma unroll 1
-      for (int q = lane; q < x.tiles; q += 32) {
+      for (int q = lane; q < tiles; q += 32) {
         const int y = room_of(a, x, q);
         part += y;
         longest = max(longest, y);
@@ -205,7 +209,7 @@ struct AttnSchedule {
         const AttnLengths now = ahead;
         if (j + 32 < 1 << log2) ahead = lengths(a, (i << log2) + j + 32);
         else if (i + step < groups) ahead = lengths(a, (i + step) << log2);
-        r = attn_request<kRows>(a, now);
+        r = attn_request(a, now);
         sum += lane_room(a, longest);
       }
       sum = __reduce_add_sync(0xffffffffu, sum);
@@ -280,14 +284,15 @@ struct AttnSchedule {
     b = b0 + l;
     cur = lane_request(l);
     qt = 0;
-    for (; cur.tiles > 1; qt += 32) {  // (the request reaches past lo, so one of its row tiles does)
-      mine = qt + lane < cur.tiles ? room_of(a, cur, qt + lane) * a.hkv : 0;
+    const int tiles = row_tiles(a, cur.n);
+    for (; tiles > 1; qt += 32) {  // (the request reaches past lo, so one of its row tiles does)
+      mine = qt + lane < tiles ? room_of(a, cur, qt + lane) * a.hkv : 0;
       end = inclusive(mine);
       past = __ballot_sync(0xffffffffu, mine && pos + end > lo);
-      if (past || qt + 32 >= cur.tiles) break;
+      if (past || qt + 32 >= tiles) break;
       pos += __shfl_sync(0xffffffffu, end, 31);
     }
-    if (cur.tiles > 1) {
+    if (tiles > 1) {
       l = past ? __ffs(past) - 1 : 0;
       pos += __shfl_sync(0xffffffffu, end - mine, l);
       qt += l;
@@ -301,11 +306,11 @@ struct AttnSchedule {
     pos += unit;
     if (++head < a.hkv) return;
     head = 0;
-    if (++qt < cur.tiles) return;
+    if (++qt < row_tiles(a, cur.n)) return;
     qt = 0;
     for (;;) {  // the next request with rows
       const int l = b + 1 - b0;
-      const uint32_t rest = __ballot_sync(0xffffffffu, r.tiles > 0 && static_cast<int>(threadIdx.x & 31) >= l);
+      const uint32_t rest = __ballot_sync(0xffffffffu, r.n > 0 && static_cast<int>(threadIdx.x & 31) >= l);
       if (rest) {
         b = b0 + __ffs(rest) - 1;
         cur = lane_request(__ffs(rest) - 1);
