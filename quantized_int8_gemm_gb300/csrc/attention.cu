@@ -86,7 +86,7 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
 // the latency of one warp's products where few rows are at work (16 q heads
 // over 4 K/V heads of 256, 32 tokens over 4001 keys: 137 us, 3.8 TB/s) and by
 // the warp-level tensor rate beside the softmax in chunks (512 tokens over 4608
-// keys: 146 us, 250 TFLOP/s).
+// keys: 147 us, 250 TFLOP/s).
 template <class T, int kDp>
 __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const __grid_c
 // attention_join_split_kernel, for calls of few units: where a unit has more
 // than eight pieces and fewer rows than there are blocks for, blocks also take a
 // part of its columns each and a block's threads a part of the pieces (one row
-// over 30001 keys: 8 heads on 1, 118 pieces, 19 us for the call, 53 with all
-// pieces in one thread's turn; 28 heads on 4 24 and 34).  With many units it
+// over 30001 keys: 8 heads on 1, 118 pieces, 19 us for the call, 52 with all
+// pieces in one thread's turn; 28 heads on 4 24 and 34.5).  With many units it
 // costs 0.5 us more than the other one.
 constexpr int kJoinRows = 16, kJoinLeast = 8, kJoinPieces = 8;  // (blocks a unit; pieces a thread)
 // Eight columns of a joined row, from their sums and that of the weights relative to top.
@@ -459,7 +459,7 @@ cudaError_t launch_attention(const mmq_paged_cache &c, const mmq_attention &t, c
   // one (two CTAs an SM, one with heads wider than 128) the rest: 32 rows of one
   // token over 4001 keys, 4 K/V heads of 128, take 54 us in the first (pages of 8
   // or 16 keys) and 70 us in the second (pages of 5), 512 tokens over 4608 keys
-  // 28 and 74 us.
+  // (16 heads on 4) 29 and 74 us.
   AttnUmma um;
   const bool umma = attention_umma(a, c.type, &um);
   const int unit_rows = umma ? 2 * um.tile_tok * a.rep : kRows, kt = umma ? 128 : kKt;

@@ -12,15 +12,15 @@
 // takes every second key tile, and their results are joined at the end.
 //
 // What bounds it (one GB300, calls back to back):
-//   long chunks  (4096 tokens over 32097 keys, 28 heads on 4, d 128: 1.10 ms,
-//       1.6 PFLOP/s) the chain of one lane, softmax about 1.7 thousand clocks,
-//       P V and Q K^T 0.5 each and the hand-offs: a key tile of both lanes takes
-//       about 2.6 thousand clocks, 2.05 of them UMMAs, whose operands also take
-//       all of shared memory's bandwidth;
-//   heads of 64  (prompts of 301 to 2630 tokens, window 1000: 58 us) the softmax
+//   long chunks  (4096 tokens over 32097 keys, 28 heads on 4, d 128: 1.09 to
+//       1.18 ms by clocks, 1.5 to 1.6 PFLOP/s) the chain of one lane, softmax
+//       about 1.7 thousand clocks, P V and Q K^T 0.5 each and the hand-offs: a
+//       key tile of both lanes takes about 2.6 thousand clocks, 2.05 of them
+//       UMMAs, whose operands also take all of shared memory's bandwidth;
+//   heads of 64  (prompts of 301 to 2630 tokens, window 1000: 59 us) the softmax
 //       warps, about 2.4 thousand clocks a key tile of both lanes, and what a
 //       unit of few tiles costs beside them;
-//   decode steps (64 tokens over 97 to 12002 keys, 333 MB: 64 us) HBM while the
+//   decode steps (64 tokens over 97 to 12002 keys, 333 MB: 65 us) HBM while the
 //       tiles run, about 51 us; the rest is the first tile's way in (5 us: plan,
 //       page ids, copies, first products, code met for the first time), the last
 //       one's way out and the join.
@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float2 *stats = reinterpret_cast<float2 *>(smem + L::kStats);
   // More than 32 requests: the softmax warps add up their rooms on the units'
   // line, into the place of the statistics (4096 requests of 301 keys, 8 heads on
-  // 1: 188 us, by the planning warp alone 291; 1024, 28 heads on 4: 177 and 194).
+  // 1: 187 us, 1024, 28 heads on 4: 167; 291 and 194 by the planning warp alone,
+  // when that was changed).
   int *sums = reinterpret_cast<int *>(stats);
   static_assert((kAttnSums + 1) * sizeof(int) <= 2 * 128 * sizeof(float2));
   volatile uint32_t *last = reinterpret_cast<volatile uint32_t *>(smem + L::kSlot + 8);  // the load warps' loads of the ring, at their end
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // often as they issued one).  First the maximum.
             const int from = lo - j * kKt, to_key = hi - j * kKt;
             const bool ends = __any_sync(0xffffffffu, valid && (from > 0 || to_key < kKt));
-            // (P V stops at the last key: 1024 decode rows over 171 keys 118 us, 135 with both halves)
+            // (P V stops at the last key: 1024 decode rows over 171 keys 122 us, 134 with both halves)
             const int halves = un.len - j * kKt <= kKt / 2 ? 1 : 2;
             float top[4];
             if (!ends) {
@@ -854,7 +855,8 @@ EncodeFn encoder() {
 // A map of four dimensions (row, and three with strides in elements), boxes of
 // 64 elements by b1 x 1 x b3.  128 bytes a request to memory: a head of 64 is no
 // longer, and with 256 the next head's row came with it, often for nothing (64
-// decode rows of 5001 keys, 8 heads of 64: 111 us, 155 with 256; heads of 128 alike).
+// decode rows of 5001 keys, 8 K/V heads of 64, pages of 16: 121 us, 161 with 256;
+// heads of 128 alike).
 bool encode(CUtensorMap *m, int type, const void *p, int64_t d, const int64_t (&n)[3], const int64_t (&stride)[3], int b1, int b3) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(n[0]), static_cast<cuuint64_t>(n[1]),
                               static_cast<cuuint64_t>(n[2])};

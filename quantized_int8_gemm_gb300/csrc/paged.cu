@@ -213,11 +213,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
 constexpr int kWriteThreads = 256;
 
 // One thread moves 8 elements of a row at a time: 32 B (16 B) in, 16 B out.
-// HBM bound (16384 tokens of 2 x 4 x 128 fp32 to bf16: 16.3 us, 5.5 TB/s of
-// what it reads and writes); the one dependent read is the token's slot.  Two
-// or four items of a thread in flight were slower (17.5 us): the CTAs of an SM
-// hide the latency by themselves.  The source is read once (streaming loads),
-// the cache rows are left in L2 for the attention that follows.
+// HBM bound (16384 tokens of 2 x 4 x 128 fp32 to bf16, one in nine padding: 15.8
+// us, 5.7 TB/s of what it reads and writes); the one dependent read is the
+// token's slot.  Two or four items of a thread in flight were slower (17.5 us,
+// one 16.3 then): the CTAs of an SM hide the latency by themselves.  The source
+// is read once (streaming loads), the cache rows are left in L2 for the
+// attention that follows.
 template <class S, class D>
 __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const __grid_constant__ KvWriteArgs a) {
   griddep_wait();
