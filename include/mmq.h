@@ -439,6 +439,7 @@ typedef struct mmq_attention {
  * may also make rows of that chunk non-finite that do not see it.
  *   A page id outside the cache, or seq_lens[b] past table_width*page_size, is
  * reported by mmq_last_device_error; that request's rows are then unspecified.
+ * So is a q_start that descends; every row is then unspecified.
  *   Products and sums are fp32; the softmax weights are rounded to the
  * cache's type before they multiply V.  The results of one problem do not
  * change from call to call.

@@ -68,6 +68,7 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, const Att
   const int ntok = static_cast<int>(a.ntok), from = x.from, to = x.to, len = x.len;
   r.q0 = max(0, min(from, ntok));
   r.n = max(r.q0, min(to, ntok)) - r.q0;
+  if (to < from) record_index(a.wait.status);  // (then rows may be two requests', and the line longer than the host allowed for)
   // (a tile's keys are counted past the last one)
   const int64_t room = min(static_cast<int64_t>(a.table_width) * a.page_size, static_cast<int64_t>(0x7fffff00));
   r.len = max(len, 0);
@@ -298,7 +299,7 @@ struct AttnSchedule {
       qt += l;
     }
     const int unit = room_of(a, cur, qt);
-    head = lo > pos ? (lo - pos) / unit : 0;
+    head = lo > pos ? min((lo - pos) / unit, a.hkv - 1) : 0;  // (less than hkv anyway, unless row starts descend and places wrap)
     pos += head * unit;
   }
 

@@ -316,3 +316,16 @@ def test_an_argument_without_a_truth_value_is_an_error(mmq):  # noqa: F811
     with pytest.raises(RuntimeError, match="ambiguous"):
         mmq.mmq_paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seq_lens"], p["q_start"], causal=torch.ones(2), out=out)
     assert (out == 7).all()
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 16), (128, 5)])
+def test_row_starts_that_descend_are_reported(mmq, d, page):  # noqa: F811
+    """Rows of two requests: what comes out for them is not said, but it is reported, and the rows of others stay."""
+    p = _problem(F16, [4, 3, 2], [40, 30, 300], 4, 2, d, page)
+    guard = torch.full((12, 4, d), 7.0, dtype=F16, device="cuda")
+    for starts in ([0, 4, 2, 9], [0, 4, -3, 7], [0, 9, 4, 7], [2 ** 31 - 1, 0, 2, 9]):
+        mmq.mmq_paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seq_lens"], _i32(starts), out=guard[:9])
+        assert mmq.mmq_last_device_error() == mmq.MMQ_ERR_DEVICE_INDEX
+        assert (guard[9:] == 7).all()
+    mmq.mmq_paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seq_lens"], p["q_start"], out=guard[:9])
+    assert mmq.mmq_last_device_error() == 0
