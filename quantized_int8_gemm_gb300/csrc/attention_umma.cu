@@ -855,8 +855,8 @@ EncodeFn encoder() {
 // A map of four dimensions (row, and three with strides in elements), boxes of
 // 64 elements by b1 x 1 x b3.  128 bytes a request to memory: a head of 64 is no
 // longer, and with 256 the next head's row came with it, often for nothing (64
-// decode rows of 5001 keys, 8 K/V heads of 64, pages of 16: 121 us, 161 with 256;
-// heads of 128 alike).
+// decode rows of 5001 keys, 8 K/V heads of 64, pages of 16: 111 to 121 us by
+// machine, 155 to 161 with 256; heads of 128 alike).
 bool encode(CUtensorMap *m, int type, const void *p, int64_t d, const int64_t (&n)[3], const int64_t (&stride)[3], int b1, int b3) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(n[0]), static_cast<cuuint64_t>(n[1]),
                               static_cast<cuuint64_t>(n[2])};
