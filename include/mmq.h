@@ -488,6 +488,196 @@ typedef struct mmq_verification {
  */
 int mmq_verify_draft(const mmq_verification *args, mmq_stream_t stream);
 
+/* ---- what differs from request to request in a step ---------------------
+ * The pages that requests share, give back or get copies of; the rules that a
+ * request puts on its next token; the low-rank adapter that it brings beside
+ * the shared projections.  As above nothing synchronizes or reads device
+ * memory back.
+ *
+ * mmq_page_fork -- the rows of a page table made anew from the rows that there
+ * are: row b continues old row parents[b] with its first lens[b] tokens.  One
+ * call forks a request (two rows with one parent), reorders beams, ends a
+ * request (no row continues it), and takes back the pages that refused drafted
+ * tokens left (lens[b] shorter).  With
+ *   need[b] = min(ceil(lens[b] / page_size), held[parents[b]], table_width)
+ * row b gets the first need[b] pages of its parent.  Rows may share pages that
+ * are full; the page that the next token goes into (the last one, where
+ * lens[b] is no multiple of page_size) is a row's own: of the rows that
+ * have it as that page the lowest keeps it, unless another row has it as a
+ * full one, and every other row gets a free page in its place and an entry in
+ * `pairs`, for mmq_page_copy.  Pages that no new row holds are free.
+ *   table, held  device, int32: nold rows of table_width page ids, row pitch
+ *                table_stride; pages that each row holds.
+ *   parents, lens device, int32, nnew each: old row (-1: an empty row), tokens
+ *                (negative counts as 0).
+ *   npages       pages of the cache; ids are 0..npages - 1.
+ *   new_table    device, int32, nnew rows of table_width, row pitch
+ *                new_stride; -1 behind a row's pages.
+ *   held_out     device, int32, nnew: need.
+ *   pairs        device, int32, nnew x 2: page to copy and the free page that
+ *                takes its place, -1 -1 for a row without a copy.
+ *   tokens       device, int32, nnew: tokens to copy (0 without a copy).
+ *   free_pages   device, int32, npages: ids that no new row holds, ascending,
+ *                then -1.  Copies take the lowest ids, in the rows' order.
+ *   counts       device, int32, 2: entries of free_pages; copies that found no
+ *                free page (their table entries are -1).
+ * Pages that are to stay held though no request has them are a row of their
+ * own.  An entry of parents or of a row outside its range (the page becomes
+ * -1), or lens[b] beyond what its parent holds, is reported by
+ * mmq_last_device_error.  What is written may overlap nothing else of the
+ * call (MMQ_ERR_ARG).  nold, nnew in 0..8192, npages in 0..2^20 (more:
+ * MMQ_ERR_UNSUPPORTED).  One kernel, no scratch.  Errors: MMQ_ERR_ARG,
+ * MMQ_ERR_ALIGN (elements off their own alignment), MMQ_ERR_UNSUPPORTED,
+ * MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
+ */
+typedef struct mmq_fork {
+  const int32_t *table, *held, *parents, *lens;
+  int32_t *new_table, *held_out, *pairs, *tokens, *free_pages, *counts;
+  int64_t nold, nnew, table_width, table_stride, new_stride, npages;
+  int32_t page_size;         /* >= 1 */
+} mmq_fork;
+int mmq_page_fork(const mmq_fork *args, mmq_stream_t stream);
+
+/*
+ * mmq_page_compact -- moves that bring the held pages of a cache to its front:
+ * with H pages held by any row, the j-th held id from H on moves to the j-th
+ * id below H that is not held.
+ *   table, held  device, int32, as for mmq_page_fork, nreq rows.
+ *   new_table    device, int32, nreq rows of table_width, row pitch
+ *                new_stride: the table after the moves, -1 behind a row's pages.
+ *   pairs        device, int32, (npages / 2) x 2: from, to; then -1 -1.  No
+ *                page is both.
+ *   counts       device, int32, 2: H, moves.
+ * After mmq_page_copy(pairs) pages H..npages - 1 are free.  A page id out of
+ * range in a row becomes -1 and is reported by mmq_last_device_error.  Limits,
+ * overlaps and errors as mmq_page_fork.  One kernel, no scratch.
+ */
+int mmq_page_compact(const int32_t *table, const int32_t *held, int64_t nreq, int64_t table_width, int64_t table_stride,
+                     int64_t npages, int32_t *new_table, int64_t new_stride, int32_t *pairs, int32_t *counts,
+                     mmq_stream_t stream);
+
+/*
+ * mmq_page_copy -- pages of K and V copied within a cache.
+ *   pairs   device, int32, npairs x 2: page from, page to.  A pair with a
+ *           negative id copies nothing; an id past the cache copies nothing
+ *           and is reported by mmq_last_device_error.
+ *   tokens  device, int32, npairs: leading tokens to copy (0..page_size, others
+ *           are brought into that range), or NULL: whole pages.
+ * All pairs at once: a page that one pair writes and another reads or writes
+ * holds either's rows (mmq_page_fork and mmq_page_compact give no such
+ * pairs).  npairs >= 0; 0 is a no-op.  Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN,
+ * MMQ_ERR_TYPE, MMQ_ERR_UNSUPPORTED (a page of more than 2^32 elements),
+ * MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
+ */
+int mmq_page_copy(const mmq_paged_cache *cache, const int32_t *pairs, const int32_t *tokens, int64_t npairs,
+                  mmq_stream_t stream);
+
+/* Arguments of mmq_token_probs. */
+typedef struct mmq_token_rules {
+  const void *logits;          /* device, type: token v of row i of request b at b*logits_req + i*logits_row + v */
+  void *probs;                 /* device, probs_type, or NULL: b*probs_req + i*probs_row + v */
+  void *adjusted;              /* device, adjusted_type, or NULL; may be the logits themselves (same type and strides) */
+  const float *temperature;    /* device, nreq; NULL: 1 */
+  const int32_t *tokens;       /* device: token j of request b at b*tokens_stride + j; NULL: none */
+  const int32_t *token_lens;   /* device, nreq; NULL: tokens_width */
+  const int32_t *prompt_lens;  /* device, nreq: leading tokens that are the prompt's; NULL: 0 */
+  const int32_t *draft;        /* device: drafted token j of request b at b*draft_stride + j; NULL: none */
+  const int32_t *n_draft;      /* device, nreq: rows past row n_draft[b] are not computed or written; NULL: all rows */
+  const float *repetition;     /* device, nreq; NULL: 1 */
+  const float *frequency;      /* device, nreq; NULL: 0 */
+  const float *presence;       /* device, nreq; NULL: 0 */
+  const int32_t *bias_start;   /* device, nreq + 1: first bias of each request, ascending; NULL: none */
+  const int32_t *bias_ids;     /* device, nbias */
+  const float *bias_values;    /* device, nbias */
+  const int32_t *mask;         /* device, nmasks rows of mask_stride words: bit v % 32 of word v / 32 allows token v; NULL: none */
+  const int32_t *mask_rows;    /* device, nreq x rows: row of mask, -1: no mask; NULL: row b*rows + i */
+  int64_t logits_req, logits_row, probs_req, probs_row, adjusted_req, adjusted_row;
+  int64_t tokens_stride, tokens_width, draft_stride, nbias, mask_stride, nmasks;
+  int64_t nreq, vocab;
+  int32_t rows;                /* rows of a request, >= 1: one, and one for each drafted token */
+  int32_t type, probs_type, adjusted_type; /* MMQ_DT_F32, MMQ_DT_F16 or MMQ_DT_BF16 */
+} mmq_token_rules;
+
+/*
+ * mmq_token_probs -- probabilities of the next tokens under each request's
+ * rules, as mmq_verify_draft reads them.  Row i of request b stands behind
+ * its tokens and its first i drafted ones.  With c(v) the times that token v
+ * is among the tokens behind the prompt and those drafted ones, in fp32 and in
+ * this order:
+ *   x = logits[v];  v among the tokens or drafted ones: x = x > 0 ? x / repetition : x * repetition
+ *   x -= frequency * c(v);  c(v) > 0: x -= presence;  x += the biases of v, in their order
+ *   v not allowed by the row's mask: x = -inf
+ *   adjusted[v] = x;  probs = softmax(x / temperature), over the row
+ * temperature not above 0: probability 1 for the largest x (ties: the lowest
+ * v).  A row with no token left gets probabilities of 0; a NaN that no mask
+ * hides (or, with a temperature, +inf) makes a row's probabilities NaN.
+ * Sums are fp32; probs and adjusted are rounded once.  The results
+ * of one problem do not change from call to call.
+ *   Tokens, drafted tokens and biases outside [0, vocab) are left out, a mask
+ * row past nmasks is no mask, token_lens past tokens_width, n_draft past
+ * rows - 1, bias_start past nbias are cut; all of them are reported by
+ * mmq_last_device_error.  A token counts 32767 times at the most.
+ * vocab in 1..2^18 (more: MMQ_ERR_UNSUPPORTED), nreq*rows below 2^27.  One
+ * kernel, no scratch.  Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN (elements off their
+ * own alignment), MMQ_ERR_TYPE, MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE,
+ * MMQ_ERR_CUDA.
+ */
+int mmq_token_probs(const mmq_token_rules *args, mmq_stream_t stream);
+
+/*
+ * mmq_lora_plan -- the tokens of a step in the order of their adapters, once
+ * for all its projections.
+ *   adapters  device, int32, nreq: adapter of each request's tokens, -1: none
+ *             (an id outside -1..nadapters - 1 counts as none and is reported
+ *             by mmq_last_device_error).
+ *   q_start   device, int32, nreq + 1, as for mmq_paged_attention (one that
+ *             descends is reported; the plan is then empty).
+ *   ntok      token rows; rows behind q_start[nreq] belong to no request.
+ *   plan      device, int32, mmq_lora_plan_words(ntok, nreq, nadapters) words, for
+ *             mmq_lora with the same ntok, nreq and nadapters.
+ * nreq in 0..8192, nadapters in 0..2^18 (more: MMQ_ERR_UNSUPPORTED).  One
+ * kernel, no scratch.  Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN,
+ * MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
+ */
+int mmq_lora_plan(const int32_t *adapters, const int32_t *q_start, int64_t nreq, int64_t ntok, int64_t nadapters,
+                  int32_t *plan, mmq_stream_t stream);
+/* int32 words of a plan; -1 for sizes that mmq_lora_plan refuses. */
+int64_t mmq_lora_plan_words(int64_t ntok, int64_t nreq, int64_t nadapters);
+
+/* Arguments of mmq_lora. */
+typedef struct mmq_lora_args {
+  const void *x;            /* device, 16-byte aligned, x_type: (t, i) at t*x_row + i */
+  const float *y;           /* device: (t, o) at t*y_row + o */
+  float *out;               /* device: (t, o) at t*out_row + o; y itself, or memory that overlaps nothing of the call */
+  const void *a, *b;        /* device, 16-byte aligned, type: (adapter, r, i) at (adapter*rank + r)*id + i; (adapter, o, r) at
+                               (adapter*od + o)*rank + r */
+  const float *scales;      /* device, nadapters; NULL: 1 */
+  const int32_t *ranks;     /* device, nadapters: rank of each (0..rank, others are brought into that range); NULL: rank */
+  const int32_t *plan;      /* from mmq_lora_plan */
+  int64_t x_row, y_row, out_row; /* in elements; x_row * the element's size a multiple of 16 bytes */
+  int64_t ntok, nreq, nadapters; /* as in the plan */
+  int64_t id, od;           /* id a multiple of 8 */
+  int32_t rank;             /* of the arrays a and b: a multiple of 8, at most 128 */
+  int32_t type;             /* of a and b: MMQ_DT_F16 or MMQ_DT_BF16 */
+  int32_t x_type;           /* MMQ_DT_F32, MMQ_DT_F16 or MMQ_DT_BF16 */
+} mmq_lora_args;
+
+/*
+ * mmq_lora -- low-rank adapters beside a shared projection:
+ *   out[t][o] = y[t][o] + scale * sum_r b[o][r] * (sum_i a[r][i] * x[t][i])
+ * with the adapter, and the rank, of token t's request.  Tokens of a request
+ * without an adapter get out = y; rows of no request are not written.  Where
+ * out is y (the usual call, behind mmq_gemm_f32) only rows with an adapter are
+ * touched.  Rows and columns of a and b past an adapter's rank are not used,
+ * whatever they hold.
+ *   Sums are fp32.  x and the inner sums enter the tensor cores as two 16-bit
+ * terms (an error of 2^-17 at the most).  The results of one problem do not
+ * change from call to call.  One kernel, no scratch.
+ * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN, MMQ_ERR_TYPE, MMQ_ERR_UNSUPPORTED,
+ * MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
+ */
+int mmq_lora(const mmq_lora_args *args, mmq_stream_t stream);
+
 /* Synchronizes the current device, then returns and clears the device status
  * word: MMQ_OK, MMQ_ERR_DEVICE_TIMEOUT if a bounded wait expired since
  * the last call, or MMQ_ERR_DEVICE_INDEX if an index was out of range (the

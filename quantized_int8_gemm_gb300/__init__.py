@@ -2,8 +2,9 @@
 
 The package holds the CUDA sources (csrc/), their build script (build.py) and
 the ctypes binding (mmq.py; serving.py for the serving step around the GEMM:
-page tables, K/V write, paged attention, draft verification); the C ABI is
-declared in include/mmq.h.
+page tables, K/V write, paged attention, draft verification, page forks and
+copies, token probabilities, low-rank adapters); the C ABI is declared in
+include/mmq.h.
 """
 from .mmq import (  # noqa: F401
     ARM_NAMES,
@@ -43,9 +44,18 @@ from .mmq import (  # noqa: F401
     mmq_weights_wexp,
 )
 from .serving import (  # noqa: F401
+    LoraPlan,
+    PageFork,
+    PageMoves,
     PageTables,
     mmq_kv_write,
+    mmq_lora,
+    mmq_lora_plan,
+    mmq_page_compact,
+    mmq_page_copy,
+    mmq_page_fork,
     mmq_page_tables,
     mmq_paged_attention,
+    mmq_token_probs,
     mmq_verify_draft,
 )

@@ -26,6 +26,13 @@ decltype(&mmq_page_tables) g_page_tables;
 decltype(&mmq_kv_write) g_kv_write;
 decltype(&mmq_paged_attention) g_paged_attention;
 decltype(&mmq_verify_draft) g_verify_draft;
+decltype(&mmq_page_fork) g_page_fork;
+decltype(&mmq_page_compact) g_page_compact;
+decltype(&mmq_page_copy) g_page_copy;
+decltype(&mmq_token_probs) g_token_probs;
+decltype(&mmq_lora_plan_words) g_lora_plan_words;
+decltype(&mmq_lora_plan) g_lora_plan;
+decltype(&mmq_lora) g_lora;
 
 struct PyFail {};  // a Python error is set
 [[noreturn]] void fail(PyObject *type, const char *form, ...) {
@@ -92,12 +99,12 @@ struct Table {
   int32_t *p;
   int64_t width, stride;
 };
-Table page_table(PyObject *o, int64_t nreq, int dev) {
-  const at::Tensor &t = on(o, "block_table", dev);
+Table page_table(PyObject *o, int64_t nreq, int dev, const char *name = "block_table") {
+  const at::Tensor &t = on(o, name, dev);
   if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != nreq)
-    fail(PyExc_ValueError, "block_table must be int32 of shape (%lld, width)", static_cast<long long>(nreq));
+    fail(PyExc_ValueError, "%s must be int32 of shape (%lld, width)", name, static_cast<long long>(nreq));
   const int64_t width = t.size(1);
-  if (t.stride(1) != 1 && width > 1) fail(PyExc_ValueError, "the rows of block_table must be contiguous");
+  if (t.stride(1) != 1 && width > 1) fail(PyExc_ValueError, "the rows of %s must be contiguous", name);
   return {ptr<int32_t>(t), width, nreq > 1 ? t.stride(0) : std::max(t.stride(0), width)};
 }
 
@@ -178,17 +185,18 @@ PyObject *guarded(Py_ssize_t got, Py_ssize_t want, F &&f) {
   return nullptr;
 }
 
+template <class F>
+void take(F &f, PyObject *address) {
+  void *p = PyLong_AsVoidPtr(address);
+  if (PyErr_Occurred()) throw PyFail{};
+  f = reinterpret_cast<F>(p);
+}
+// The addresses of the C ABI's functions, in the order below.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return guarded(n, 4, [&]() -> PyObject * {
-    void *p[4];
-    for (int i = 0; i < 4; ++i) {
-      p[i] = PyLong_AsVoidPtr(a[i]);
-      if (PyErr_Occurred()) throw PyFail{};
-    }
-    g_page_tables = reinterpret_cast<decltype(g_page_tables)>(p[0]);
-    g_kv_write = reinterpret_cast<decltype(g_kv_write)>(p[1]);
-    g_paged_attention = reinterpret_cast<decltype(g_paged_attention)>(p[2]);
-    g_verify_draft = reinterpret_cast<decltype(g_verify_draft)>(p[3]);
+  return guarded(n, 11, [&]() -> PyObject * {
+    take(g_page_tables, a[0]), take(g_kv_write, a[1]), take(g_paged_attention, a[2]), take(g_verify_draft, a[3]);
+    take(g_page_fork, a[4]), take(g_page_compact, a[5]), take(g_page_copy, a[6]), take(g_token_probs, a[7]);
+    take(g_lora_plan_words, a[8]), take(g_lora_plan, a[9]), take(g_lora, a[10]);
     Py_RETURN_NONE;
   });
 }
@@ -332,12 +340,242 @@ PyObject *verify_draft(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// The members of out, a tuple of n tensors.
+PyObject *item(PyObject *out, int n, int i) {
+  if (!PyTuple_Check(out) || PyTuple_GET_SIZE(out) != n) fail(PyExc_TypeError, "out must be a tuple of %d tensors", n);
+  return PyTuple_GET_ITEM(out, i);
+}
+// A vector of the call, or NULL for None.
+template <class T>
+const T *maybe(PyObject *o, const char *name, int dev, at::ScalarType type, std::initializer_list<int64_t> shape) {
+  return o == Py_None ? nullptr : ptr<T>(plain(o, name, dev, type, shape));
+}
+int64_t length_of(PyObject *o, const char *name, int dev) {
+  const at::Tensor &t = on(o, name, dev);
+  if (t.dim() != 1) fail(PyExc_ValueError, "%s must have 1 dimension", name);
+  return t.size(0);
+}
+
+// (table, n_blocks, parents, lens, page_size, n_pages, out or None, stream) -> status, or (status, out)
+PyObject *page_fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject * {
+    int dev;
+    first(a[0], "block_table", dev);
+    const int64_t nold = length_of(a[1], "n_blocks", dev), nnew = length_of(a[2], "parents", dev);
+    const Table table = page_table(a[0], nold, dev);
+    mmq_fork t;
+    t.held = ptr<int32_t>(plain(a[1], "n_blocks", dev, at::kInt, {nold})), t.parents = ptr<int32_t>(plain(a[2], "parents", dev, at::kInt, {nnew}));
+    t.lens = ptr<int32_t>(plain(a[3], "lens", dev, at::kInt, {nnew}));
+    t.page_size = small(a[4], "page_size"), t.npages = number(a[5], "n_pages");
+    if (t.npages < 0) fail(PyExc_ValueError, "n_pages is negative");
+    const CallStream s(a[7], dev);
+    at::Tensor out[6];
+    if (a[6] == Py_None) {
+      if (t.npages > INT32_MAX) fail(PyExc_ValueError, "n_pages is out of range");
+      out[0] = empty({nnew, table.width}, at::kInt, dev), out[1] = empty({nnew}, at::kInt, dev), out[2] = empty({nnew, 2}, at::kInt, dev);
+      out[3] = empty({nnew}, at::kInt, dev), out[4] = empty({t.npages}, at::kInt, dev), out[5] = empty({2}, at::kInt, dev);
+    } else {
+      out[0] = on(item(a[6], 6, 0), "out.block_table", dev), out[1] = plain(item(a[6], 6, 1), "out.n_blocks", dev, at::kInt, {nnew});
+      out[2] = plain(item(a[6], 6, 2), "out.pairs", dev, at::kInt, {nnew, 2}), out[3] = plain(item(a[6], 6, 3), "out.tokens", dev, at::kInt, {nnew});
+      out[4] = plain(item(a[6], 6, 4), "out.free_pages", dev, at::kInt, {t.npages}), out[5] = plain(item(a[6], 6, 5), "out.counts", dev, at::kInt, {2});
+    }
+    const Table fresh = a[6] == Py_None ? Table{ptr<int32_t>(out[0]), table.width, table.width} : page_table(item(a[6], 6, 0), nnew, dev, "out.block_table");
+    if (fresh.width != table.width) fail(PyExc_ValueError, "out.block_table must be as wide as block_table");
+    t.table = table.p, t.table_width = table.width, t.table_stride = table.stride, t.nold = nold, t.nnew = nnew;
+    t.new_table = fresh.p, t.new_stride = fresh.stride, t.held_out = ptr<int32_t>(out[1]), t.pairs = ptr<int32_t>(out[2]);
+    t.tokens = ptr<int32_t>(out[3]), t.free_pages = ptr<int32_t>(out[4]), t.counts = ptr<int32_t>(out[5]);
+    const int rc = g_page_fork(&t, s.handle);
+    if (a[6] != Py_None) return PyLong_FromLong(rc);
+    return Py_BuildValue("(i(NNNNNN))", rc, THPVariable_Wrap(out[0]), THPVariable_Wrap(out[1]), THPVariable_Wrap(out[2]),
+                         THPVariable_Wrap(out[3]), THPVariable_Wrap(out[4]), THPVariable_Wrap(out[5]));
+  });
+}
+
+// (table, n_blocks, n_pages, out or None, stream) -> status, or (status, out)
+PyObject *page_compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject * {
+    int dev;
+    first(a[0], "block_table", dev);
+    const int64_t nreq = length_of(a[1], "n_blocks", dev), npages = number(a[2], "n_pages");
+    const Table table = page_table(a[0], nreq, dev);
+    const at::Tensor &held = plain(a[1], "n_blocks", dev, at::kInt, {nreq});
+    if (npages < 0 || npages > INT32_MAX) fail(PyExc_ValueError, "n_pages is out of range");
+    const CallStream s(a[4], dev);
+    at::Tensor out[3];
+    if (a[3] == Py_None) {
+      out[0] = empty({nreq, table.width}, at::kInt, dev), out[1] = empty({npages / 2, 2}, at::kInt, dev), out[2] = empty({2}, at::kInt, dev);
+    } else {
+      out[0] = on(item(a[3], 3, 0), "out.block_table", dev), out[1] = plain(item(a[3], 3, 1), "out.pairs", dev, at::kInt, {npages / 2, 2});
+      out[2] = plain(item(a[3], 3, 2), "out.counts", dev, at::kInt, {2});
+    }
+    const Table fresh = a[3] == Py_None ? Table{ptr<int32_t>(out[0]), table.width, table.width} : page_table(item(a[3], 3, 0), nreq, dev, "out.block_table");
+    if (fresh.width != table.width) fail(PyExc_ValueError, "out.block_table must be as wide as block_table");
+    const int rc = g_page_compact(table.p, ptr<int32_t>(held), nreq, table.width, table.stride, npages, fresh.p, fresh.stride,
+                                  ptr<int32_t>(out[1]), ptr<int32_t>(out[2]), s.handle);
+    if (a[3] != Py_None) return PyLong_FromLong(rc);
+    return Py_BuildValue("(i(NNN))", rc, THPVariable_Wrap(out[0]), THPVariable_Wrap(out[1]), THPVariable_Wrap(out[2]));
+  });
+}
+
+// (k_cache, v_cache, pairs, tokens or None, stream) -> status
+PyObject *page_copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject * {
+    int dev;
+    first(a[0], "k_cache", dev);
+    const mmq_paged_cache c = paged_cache(a[0], a[1], dev);
+    const at::Tensor &pairs = on(a[2], "pairs", dev);
+    const int64_t npairs = pairs.dim() ? pairs.size(0) : 0;
+    plain(a[2], "pairs", dev, at::kInt, {npairs, 2});
+    const int32_t *tokens = maybe<int32_t>(a[3], "tokens", dev, at::kInt, {npairs});
+    const CallStream s(a[4], dev);
+    return PyLong_FromLong(g_page_copy(&c, ptr<int32_t>(pairs), tokens, npairs, s.handle));
+  });
+}
+
+// (logits, temperature, tokens, token_lens, prompt_lens, draft_tokens, n_draft, repetition, frequency, presence,
+//  bias: (start, ids, values), mask, mask_rows, probs: tensor or bool, adjusted: tensor or bool, stream; None where there is none)
+//  -> (status, probs or None, adjusted or None)
+PyObject *token_probs(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 16, [&]() -> PyObject * {
+    int dev;
+    const at::Tensor &logits = first(a[0], "logits", dev);
+    const Rows lr = rows3(logits, "logits");
+    mmq_token_rules t = {};
+    t.nreq = logits.size(0), t.vocab = logits.size(2), t.type = type_of(logits.scalar_type());
+    const int64_t rows = logits.size(1);
+    if (rows < 1 || rows > INT32_MAX) fail(PyExc_ValueError, "logits must have a row for each drafted token and one more");
+    if (!t.type) fail(PyExc_ValueError, "logits must be float32, float16 or bfloat16");
+    t.rows = static_cast<int32_t>(rows), t.logits = lr.p, t.logits_req = lr.s0, t.logits_row = lr.s1;
+    t.temperature = maybe<float>(a[1], "temperature", dev, at::kFloat, {t.nreq});
+    if (a[2] != Py_None) {
+      const at::Tensor &tokens = on(a[2], "tokens", dev);
+      if (tokens.scalar_type() != at::kInt || tokens.dim() != 2 || tokens.size(0) != t.nreq || (tokens.size(1) > 1 && tokens.stride(1) != 1))
+        fail(PyExc_ValueError, "tokens must be int32 of shape (%lld, width), its rows contiguous", static_cast<long long>(t.nreq));
+      t.tokens = ptr<int32_t>(tokens), t.tokens_width = tokens.size(1), t.tokens_stride = t.nreq > 1 ? tokens.stride(0) : 0;
+    } else if (a[3] != Py_None || a[4] != Py_None) {
+      fail(PyExc_ValueError, "token_lens and prompt_lens belong to tokens");
+    }
+    t.token_lens = maybe<int32_t>(a[3], "token_lens", dev, at::kInt, {t.nreq});
+    t.prompt_lens = maybe<int32_t>(a[4], "prompt_lens", dev, at::kInt, {t.nreq});
+    if (a[5] != Py_None) t.draft = ptr<int32_t>(plain(a[5], "draft_tokens", dev, at::kInt, {t.nreq, rows - 1})), t.draft_stride = rows - 1;
+    t.n_draft = maybe<int32_t>(a[6], "n_draft", dev, at::kInt, {t.nreq});
+    t.repetition = maybe<float>(a[7], "repetition", dev, at::kFloat, {t.nreq});
+    t.frequency = maybe<float>(a[8], "frequency", dev, at::kFloat, {t.nreq});
+    t.presence = maybe<float>(a[9], "presence", dev, at::kFloat, {t.nreq});
+    if (a[10] != Py_None) {
+      if (!PyTuple_Check(a[10]) || PyTuple_GET_SIZE(a[10]) != 3) fail(PyExc_TypeError, "bias must be a tuple (start, ids, values)");
+      t.nbias = length_of(PyTuple_GET_ITEM(a[10], 1), "bias ids", dev);
+      t.bias_start = ptr<int32_t>(plain(PyTuple_GET_ITEM(a[10], 0), "bias start", dev, at::kInt, {t.nreq + 1}));
+      t.bias_ids = ptr<int32_t>(plain(PyTuple_GET_ITEM(a[10], 1), "bias ids", dev, at::kInt, {t.nbias}));
+      t.bias_values = ptr<float>(plain(PyTuple_GET_ITEM(a[10], 2), "bias values", dev, at::kFloat, {t.nbias}));
+    }
+    if (a[11] != Py_None) {
+      const at::Tensor &mask = on(a[11], "mask", dev);
+      const int64_t words = (t.vocab + 31) / 32;
+      if (mask.scalar_type() != at::kInt || mask.dim() != 2 || mask.size(1) != words || (words > 1 && mask.stride(1) != 1))
+        fail(PyExc_ValueError, "mask must be int32 of shape (masks, %lld), its rows contiguous", static_cast<long long>(words));
+      t.mask = ptr<int32_t>(mask), t.nmasks = mask.size(0), t.mask_stride = t.nmasks > 1 ? mask.stride(0) : words;
+      if (t.nmasks == 0) t.mask = nullptr;
+      t.mask_rows = maybe<int32_t>(a[12], "mask_rows", dev, at::kInt, {t.nreq, rows});
+      if (!t.mask_rows && t.nmasks != t.nreq * rows) fail(PyExc_ValueError, "without mask_rows mask must have a row for each of logits'");
+    } else if (a[12] != Py_None) {
+      fail(PyExc_ValueError, "mask_rows belongs to mask");
+    }
+    const CallStream s(a[15], dev);
+    at::Tensor out[2];
+    void **p[2] = {&t.probs, &t.adjusted};
+    int64_t *req[2] = {&t.probs_req, &t.adjusted_req}, *row[2] = {&t.probs_row, &t.adjusted_row};
+    int32_t *type[2] = {&t.probs_type, &t.adjusted_type};
+    const char *name[2] = {"probs", "adjusted"};
+    for (int i = 0; i < 2; ++i) {
+      PyObject *o = a[13 + i];
+      if (o == Py_None || o == Py_False) continue;
+      out[i] = o == Py_True ? empty({t.nreq, rows, t.vocab}, at::kFloat, dev) : on(o, name[i], dev);
+      if (out[i].sizes() != logits.sizes() || !type_of(out[i].scalar_type())) fail(PyExc_ValueError, "%s must be float32, float16 or bfloat16 of logits' shape", name[i]);
+      const Rows r = rows3(out[i], name[i]);
+      *p[i] = r.p, *req[i] = r.s0, *row[i] = r.s1, *type[i] = type_of(out[i].scalar_type());
+    }
+    if (!out[0].defined() && !out[1].defined()) fail(PyExc_ValueError, "neither probs nor adjusted is wanted");
+    const int rc = g_token_probs(&t, s.handle);
+    auto wrap = [](const at::Tensor &o) {
+      if (o.defined()) return THPVariable_Wrap(o);
+      Py_INCREF(Py_None);
+      return Py_None;
+    };
+    return Py_BuildValue("(iNN)", rc, wrap(out[0]), wrap(out[1]));
+  });
+}
+
+// (adapters, q_start, max_tokens, n_adapters, out or None, stream) -> (status, words)
+PyObject *lora_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject * {
+    int dev;
+    const at::Tensor &adapters = first(a[0], "adapters", dev);
+    const int64_t nreq = length_of(a[0], "adapters", dev), ntok = number(a[2], "max_tokens"), many = number(a[3], "n_adapters");
+    plain(a[0], "adapters", dev, at::kInt, {nreq});
+    const at::Tensor &start = plain(a[1], "q_start", dev, at::kInt, {nreq + 1});
+    const int64_t words = g_lora_plan_words(ntok, nreq, many);
+    const CallStream s(a[5], dev);
+    const at::Tensor out = a[4] == Py_None ? empty({std::max<int64_t>(words, 0)}, at::kInt, dev) : plain(a[4], "out", dev, at::kInt, {words});
+    const int rc = g_lora_plan(ptr<int32_t>(adapters), ptr<int32_t>(start), nreq, ntok, many, ptr<int32_t>(out), s.handle);
+    return Py_BuildValue("(iN)", rc, THPVariable_Wrap(out));
+  });
+}
+
+struct Matrix {
+  void *p;
+  int64_t row;
+};
+Matrix rows2(const at::Tensor &t, const char *name, int64_t rows) {
+  if (t.dim() != 2 || t.size(0) != rows) fail(PyExc_ValueError, "%s must have 2 dimensions, the first the plan's %lld tokens", name, static_cast<long long>(rows));
+  if (t.size(1) > 1 && t.stride(1) != 1) fail(PyExc_ValueError, "the rows of %s must be contiguous", name);
+  return {t.data_ptr(), t.size(0) > 1 ? t.stride(0) : 0};
+}
+
+// (x, y, a, b, plan words, tokens, requests, adapters, scales or None, ranks or None, out or None, stream) -> (status, out)
+PyObject *lora(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject * {
+    int dev;
+    const at::Tensor &x = first(a[0], "x", dev), &y = on(a[1], "y", dev), &down = on(a[2], "a", dev), &up = on(a[3], "b", dev);
+    mmq_lora_args t = {};
+    t.ntok = number(a[5], "plan.tokens"), t.nreq = number(a[6], "plan.requests"), t.nadapters = number(a[7], "plan.adapters");
+    const int64_t words = g_lora_plan_words(t.ntok, t.nreq, t.nadapters);
+    t.plan = ptr<int32_t>(plain(a[4], "plan.words", dev, at::kInt, {words}));
+    const Matrix xr = rows2(x, "x", t.ntok), yr = rows2(y, "y", t.ntok);
+    t.id = x.size(1), t.od = y.size(1), t.x_type = type_of(x.scalar_type()), t.type = type_of(down.scalar_type());
+    if (!t.x_type) fail(PyExc_ValueError, "x must be float32, float16 or bfloat16");
+    if (y.scalar_type() != at::kFloat) fail(PyExc_ValueError, "y must be float32");
+    if (down.scalar_type() != up.scalar_type() || (t.type != MMQ_DT_F16 && t.type != MMQ_DT_BF16)) fail(PyExc_ValueError, "a and b must both be float16 or bfloat16");
+    if (down.dim() != 3) fail(PyExc_ValueError, "a must have 3 dimensions");
+    const int64_t rank = down.size(1);
+    if (rank > INT32_MAX) fail(PyExc_ValueError, "the rank is out of range");
+    t.a = ptr<void>(plain(a[2], "a", dev, down.scalar_type(), {t.nadapters, rank, t.id}));
+    t.b = ptr<void>(plain(a[3], "b", dev, down.scalar_type(), {t.nadapters, t.od, rank}));
+    t.rank = static_cast<int32_t>(rank);
+    t.scales = maybe<float>(a[8], "scales", dev, at::kFloat, {t.nadapters});
+    t.ranks = maybe<int32_t>(a[9], "ranks", dev, at::kInt, {t.nadapters});
+    const CallStream s(a[11], dev);
+    const at::Tensor out = a[10] == Py_None ? empty({t.ntok, t.od}, at::kFloat, dev) : on(a[10], "out", dev);
+    if (out.scalar_type() != at::kFloat || out.sizes() != y.sizes()) fail(PyExc_ValueError, "out must be float32 of y's shape");
+    const Matrix to = rows2(out, "out", t.ntok);
+    t.x = xr.p, t.x_row = xr.row, t.y = static_cast<const float *>(yr.p), t.y_row = yr.row, t.out = static_cast<float *>(to.p), t.out_row = to.row;
+    const int rc = g_lora(&t, s.handle);
+    return Py_BuildValue("(iN)", rc, THPVariable_Wrap(out));
+  });
+}
+
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL
 PyMethodDef g_methods[] = {{"bind", FAST(bind), nullptr},
                            {"page_tables", FAST(page_tables), nullptr},
                            {"kv_write", FAST(kv_write), nullptr},
                            {"paged_attention", FAST(paged_attention), nullptr},
                            {"verify_draft", FAST(verify_draft), nullptr},
+                           {"page_fork", FAST(page_fork), nullptr},
+                           {"page_compact", FAST(page_compact), nullptr},
+                           {"page_copy", FAST(page_copy), nullptr},
+                           {"token_probs", FAST(token_probs), nullptr},
+                           {"lora_plan", FAST(lora_plan), nullptr},
+                           {"lora", FAST(lora), nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -173,6 +173,59 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s);
 
+// ---- what differs from request to request (pages.cu, rules.cu, lora.cu) ----
+struct ForkArgs : mmq_fork {
+  int *status;
+};
+cudaError_t launch_page_fork(const ForkArgs &a, cudaStream_t s);
+
+struct CompactArgs {
+  const int32_t *table, *held;
+  int32_t *new_table, *pairs, *counts;
+  int64_t nreq, table_width, table_stride, new_stride, npages;
+  int *status;
+};
+cudaError_t launch_page_compact(const CompactArgs &a, cudaStream_t s);
+
+struct PageCopyArgs {
+  mmq_paged_cache cache;
+  const int32_t *pairs, *tokens;
+  int64_t npairs;
+  int *status;
+  int32_t chunks, outer_items, per_tensor, parts;  // 16-byte items: of a row, of an outer index, of a page; CTAs of a pair
+  bool token_outer;                                // the order of a page's memory
+  FastDiv by_chunks, by_outer;
+};
+cudaError_t launch_page_copy(PageCopyArgs a, cudaStream_t s);
+
+struct RulesArgs {
+  mmq_token_rules t;
+  bool penalties, many;  // tokens are counted; more of them than 15 bits hold
+  int32_t slice;         // entries of a CTA
+  FastDiv by_rows;
+  int *status;
+  unsigned *abort_epoch;
+  unsigned epoch;
+  uint64_t limit_ns;
+};
+cudaError_t launch_token_probs(RulesArgs a, cudaStream_t s);
+
+struct LoraPlanArgs {
+  const int32_t *adapters, *q_start;
+  int64_t nreq, ntok, nadapters;
+  int32_t *plan;
+  int *status;
+  int32_t tile, slots;  // tokens of a tile; keys that are sorted, a power of two
+};
+cudaError_t launch_lora_plan(LoraPlanArgs a, cudaStream_t s);
+int64_t lora_plan_words(int64_t ntok, int64_t nreq, int64_t nadapters);
+
+struct LoraArgs {
+  mmq_lora_args t;
+  bool wide;  // rows of y and out in 16-byte pieces
+};
+cudaError_t launch_lora(LoraArgs a, cudaStream_t s);
+
 // Engine-rate microbenchmarks (probe.cu); out[0..4] as mmq_probe_engine_rates.
 cudaError_t launch_engine_probes(DevStatus *st, unsigned epoch, uint64_t limit_ns, cudaStream_t s, double *out);
 

@@ -1,0 +1,424 @@
+// pages.cu -- pages of a paged K/V cache shared, given back, moved and copied:
+// the plans (which row holds which page, what is free, what has to be copied)
+// and the copies.
+//
+// The plans keep no counts from call to call: what is held is read off the
+// page table, as one bit a page.  Each CTA of a cluster sets the bits of its
+// rows' pages in its own shared memory, the bits are joined through the
+// cluster's, and ranks of pages (the j-th free one) are sums of population
+// counts.  So every result follows from the table alone, in the order of the
+// page ids and of the rows, whatever order the threads ran in.
+#include <climits>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace mmq {
+namespace {
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kGroup = 8;  // words of bits whose population is summed as one
+constexpr unsigned kAll = 0xffffffffu;
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void or_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ void sync_all() {
+  if constexpr (kCtas == 1) __syncthreads();
+  else cluster_sync();
+}
+
+// Sum of x over the threads before this one, and over all.
+__device__ __forceinline__ int block_exclusive(int x, int &total, int *sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(kAll, s, d);
+    if (lane >= d) s += y;
+  }
+  if (lane == 31) sm[warp] = s;
+  __syncthreads();
+  int mine = sm[lane], before = mine;  // (kWarps == 32)
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(kAll, before, d);
+    if (lane >= d) before += y;
+  }
+  total = __shfl_sync(kAll, before, 31);
+  const int up = __shfl_sync(kAll, before, warp > 0 ? warp - 1 : 0);
+  __syncthreads();
+  return (warp > 0 ? up : 0) + s - x;
+}
+
+// A CTA's share of table rows: `count` of them, the first `first`, `step`
+// apart.  Few rows take several warps each.  f(row's index in the share, j,
+// id), for the entries of this lane, ids loaded four at a time; load(index, j)
+// gives -1 behind a row's pages.
+template <class L, class F>
+__device__ __forceinline__ void for_entries(int count, int width, L &&load, F &&f) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int share = count > 0 && count < kWarps ? kWarps / count : 1, rows = kWarps / share;
+  if (warp >= rows * share) return;
+  for (int r = warp / share; r < count; r += rows) {
+    for (int j0 = (warp % share) * 32 + lane; j0 < width; j0 += share * 128) {
+      int id[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) id[u] = j0 + u * share * 32 < width ? load(r, j0 + u * share * 32) : -1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (j0 + u * share * 32 < width) f(r, j0 + u * share * 32, id[u]);
+    }
+  }
+}
+
+// Bits of pages: words of the whole cache, and those that one CTA of the
+// cluster joins and ranks (whole groups).
+struct Bits {
+  int words, slice;
+  __host__ __device__ Bits(int64_t pages, int ctas) {
+    words = static_cast<int>((pages + 31) / 32);
+    slice = (words + ctas - 1) / ctas;
+    slice = (slice + kGroup - 1) / kGroup * kGroup;
+  }
+};
+
+__device__ __forceinline__ void set_bit(uint32_t *words, int id) { atomicOr(&words[id >> 5], 1u << (id & 31)); }
+
+// The cluster's words of this CTA's slice, joined.
+template <int kCtas>
+__device__ __forceinline__ uint32_t joined(const uint32_t *own, int at) {
+  if constexpr (kCtas == 1) return own[at];
+  uint32_t v[kCtas], got = 0;
+#pragma unroll
+  for (int c = 0; c < kCtas; ++c) v[c] = ld_cluster(mapa_shared(smem_addr(own + at), c));
+#pragma unroll
+  for (int c = 0; c < kCtas; ++c) got |= v[c];
+  return got;
+}
+
+// Writes v to entry `rank` of every CTA's array.
+template <int kCtas>
+__device__ __forceinline__ void tell_all(int *array, int rank, int v) {
+  if (threadIdx.x < kCtas) {
+    if constexpr (kCtas == 1) array[0] = v;
+    else st_cluster(mapa_shared(smem_addr(array + rank), threadIdx.x), v);
+  }
+}
+
+// Rows of a page table made anew (see mmq.h).  A thread has one row of the new
+// table, its warps the entries.  Latency bound: the entries are read and
+// written once (2 MB for 700 rows of 9000 tokens in pages of 16), between them
+// are six joins of the cluster.
+template <int kCtas>
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) fork_kernel(const __grid_constant__ ForkArgs a) {
+  extern __shared__ uint32_t bits[];
+  __shared__ int s_parent[kThreads], s_full[kThreads], s_need[kThreads], s_target[kThreads], s_warp[kWarps];
+  __shared__ int s_copies[kCtas], s_free[kCtas];
+  const Bits n(a.npages, kCtas);
+  uint32_t *own = bits, *full = own + n.words, *held = full + n.slice;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = kCtas == 1 ? 0 : static_cast<int>(cluster_ctarank()), npages = static_cast<int>(a.npages);
+  const int width = static_cast<int>(a.table_width), nnew = static_cast<int>(a.nnew);
+  const int per = (nnew + kCtas - 1) / kCtas, b0 = min(rank * per, nnew), mine = min(per, nnew - b0), b = b0 + tid;
+  for (int i = tid; i < n.words; i += kThreads) own[i] = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  // my row: w is its writable page, -1 if it has none
+  int need = 0, nfull = 0, w = -1, left = 0;
+  if (tid < mine) {
+    const int p = a.parents[b], length = max(a.lens[b], 0);
+    if (p >= 0 && p < a.nold) {
+      const int has = min(max(a.held[p], 0), width), whole = length / a.page_size, over = length - whole * a.page_size;
+      const int want = whole + (over > 0);
+      need = min(want, has), nfull = min(whole, has);
+      if (want > has) record_index(a.status);
+      if (over > 0 && whole < need) {
+        w = a.table[p * a.table_stride + whole];
+        left = over;
+        if (w < 0 || w >= npages) record_index(a.status), w = -1;
+      }
+    } else if (p != -1) {
+      record_index(a.status);
+    }
+    if (w >= 0) a.free_pages[w] = INT_MAX;  // lowest row that has this page as its writable one
+    s_parent[tid] = p, s_full[tid] = nfull, s_need[tid] = need;
+  }
+  sync_all<kCtas>();
+  if (w >= 0) atomicMin(&a.free_pages[w], b);
+  for_entries(
+      mine, width, [&](int r, int j) { return j < s_full[r] ? a.table[s_parent[r] * a.table_stride + j] : -1; },
+      [&](int r, int j, int id) {
+        if (j < s_full[r]) {
+          if (id >= 0 && id < npages) set_bit(own, id);
+          else record_index(a.status), id = -1;
+        } else if (j < s_need[r]) {
+          return;  // the writable page: its row's thread writes it
+        }
+        a.new_table[(b0 + r) * a.new_stride + j] = id;
+      });
+  sync_all<kCtas>();
+  const int w0 = min(rank * n.slice, n.words), words = min(n.slice, n.words - w0);
+  for (int i = tid; i < n.slice; i += kThreads) full[i] = held[i] = i < words ? joined<kCtas>(own, w0 + i) : 0;
+  sync_all<kCtas>();
+  bool copy = false;
+  if (w >= 0) {
+    const int owner = (w >> 5) / n.slice, at = (w >> 5) - owner * n.slice;
+    const uint32_t bit = 1u << (w & 31);
+    const uint32_t others = kCtas == 1 ? full[at] : ld_cluster(mapa_shared(smem_addr(full + at), owner));
+    copy = (others & bit) || __ldcg(&a.free_pages[w]) != b;
+    if (!copy) {
+      if constexpr (kCtas == 1) atomicOr(&held[at], bit);
+      else or_cluster(mapa_shared(smem_addr(held + at), owner), bit);
+    }
+  }
+  int copies_here;
+  const int nth = block_exclusive(copy, copies_here, s_warp);
+  tell_all<kCtas>(s_copies, rank, copies_here);
+  sync_all<kCtas>();
+  // free pages of my slice, by groups
+  const int groups = n.slice / kGroup;
+  auto free_word = [&](int i) {
+    const int id0 = (w0 + i) * 32;
+    if (i >= words) return 0u;
+    return ~held[i] & (npages - id0 >= 32 ? kAll : (1u << (npages - id0)) - 1);
+  };
+  int free_group = 0, free_here;
+  if (tid < groups)
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) free_group += __popc(free_word(tid * kGroup + i));
+  const int before = block_exclusive(free_group, free_here, s_warp);
+  if (tid < groups) full[tid] = before;  // (nobody reads the bits there any more)
+  tell_all<kCtas>(s_free, rank, free_here);
+  sync_all<kCtas>();
+  int base = 0, total = 0, copies = 0;
+#pragma unroll
+  for (int c = 0; c < kCtas; ++c) {
+    base += c < rank ? s_free[c] : 0;
+    total += s_free[c], copies += s_copies[c];
+  }
+  // the lowest free pages go to the copies, the others to the list
+  for (int g = warp; g < groups; g += kWarps) {
+    int at = base + static_cast<int>(full[g]);
+    for (int i = g * kGroup; i < (g + 1) * kGroup; ++i) {
+      const uint32_t f = free_word(i);
+      const int k = at + __popc(f & ((1u << lane) - 1)), id = (w0 + i) * 32 + lane;
+      at += __popc(f);
+      if (!(f >> lane & 1)) continue;
+      if (k >= copies) {
+        a.free_pages[k - copies] = id;
+        continue;
+      }
+      int of = 0, first = 0;  // the CTA whose row takes it
+#pragma unroll
+      for (int c = 0; c < kCtas - 1; ++c)
+        if (k >= first + s_copies[c] && of == c) first += s_copies[c], of = c + 1;
+      if constexpr (kCtas == 1) s_target[k] = id;
+      else st_cluster(mapa_shared(smem_addr(s_target + (k - first)), of), id);
+    }
+  }
+  const int listed = max(total - copies, 0);
+  for (int i = listed + rank * kThreads + tid; i < npages; i += kCtas * kThreads) a.free_pages[i] = -1;
+  sync_all<kCtas>();
+  if (rank == 0 && tid == 0) a.counts[0] = listed, a.counts[1] = max(copies - total, 0);
+  if (tid < mine) {
+    int first = 0;
+#pragma unroll
+    for (int c = 0; c < kCtas; ++c) first += c < rank ? s_copies[c] : 0;
+    const int to = copy && first + nth < total ? s_target[nth] : -1;
+    if (nfull < need) a.new_table[b * a.new_stride + nfull] = copy ? to : w;
+    a.held_out[b] = need;
+    a.pairs[2 * b] = to >= 0 ? w : -1, a.pairs[2 * b + 1] = to;
+    a.tokens[b] = to >= 0 ? left : 0;
+  }
+}
+
+// Moves that bring the held pages to the front (see mmq.h), and the table
+// after them.  Latency bound: the entries are read twice (the second time from
+// L2) and written once.
+template <int kCtas>
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) compact_kernel(const __grid_constant__ CompactArgs a) {
+  extern __shared__ uint32_t bits[];
+  __shared__ int s_warp[kWarps], s_held[kCtas], s_below;
+  const Bits n(a.npages, kCtas);
+  const int all_groups = kCtas * n.slice / kGroup, groups = n.slice / kGroup;
+  // bits of the whole cache (first this CTA's rows', later everyone's), of my
+  // slice, pages held before each group of my slice, of the whole cache
+  uint32_t *own = bits, *held = own + kCtas * n.slice;
+  int *mine_before = reinterpret_cast<int *>(held + n.slice), *all_before = mine_before + groups;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = kCtas == 1 ? 0 : static_cast<int>(cluster_ctarank()), npages = static_cast<int>(a.npages);
+  const int width = static_cast<int>(a.table_width), nreq = static_cast<int>(a.nreq);
+  for (int i = tid; i < kCtas * n.slice; i += kThreads) own[i] = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  __syncthreads();
+  const int mine = rank < nreq ? (nreq - rank + kCtas - 1) / kCtas : 0;  // rows rank, rank + kCtas, ...
+  auto load = [&](int r, int j) {
+    const int64_t row = rank + static_cast<int64_t>(r) * kCtas;
+    return j < a.held[row] ? a.table[row * a.table_stride + j] : -1;
+  };
+  for_entries(mine, width, load, [&](int r, int j, int id) {
+    if (id >= 0 && id < npages) set_bit(own, id);
+    else if (j < a.held[rank + static_cast<int64_t>(r) * kCtas]) record_index(a.status);
+  });
+  sync_all<kCtas>();
+  for (int i = tid; i < n.slice; i += kThreads) held[i] = joined<kCtas>(own, rank * n.slice + i);
+  __syncthreads();
+  int held_group = 0, held_here;
+  if (tid < groups)
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) held_group += __popc(held[tid * kGroup + i]);
+  const int before = block_exclusive(held_group, held_here, s_warp);
+  if (tid < groups) mine_before[tid] = before;
+  tell_all<kCtas>(s_held, rank, held_here);
+  sync_all<kCtas>();
+  int base = 0, total = 0;
+#pragma unroll
+  for (int c = 0; c < kCtas; ++c) base += c < rank ? s_held[c] : 0, total += s_held[c];
+  // everyone's bits and sums
+  for (int i = tid; i < kCtas * n.slice; i += kThreads)
+    own[i] = kCtas == 1 ? held[i] : ld_cluster(mapa_shared(smem_addr(held + i % n.slice), i / n.slice));
+  for (int i = tid; i < all_groups; i += kThreads) {
+    const int c = i / groups;
+    int first = 0;
+#pragma unroll
+    for (int k = 0; k < kCtas; ++k) first += k < c ? s_held[k] : 0;
+    all_before[i] = first + (kCtas == 1 ? mine_before[i] : static_cast<int>(ld_cluster(mapa_shared(smem_addr(mine_before + i % groups), c))));
+  }
+  __syncthreads();
+  auto held_before = [&](int id) {  // pages held below id (id <= npages, within the words there are)
+    const int word = id >> 5, g = word / kGroup;
+    int s = all_before[g];
+    for (int i = g * kGroup; i < word; ++i) s += __popc(own[i]);
+    return s + __popc(own[word] & ((1u << (id & 31)) - 1));
+  };
+  if (tid == 0) s_below = total < kCtas * n.slice * 32 ? held_before(total) : total;
+  __syncthreads();
+  const int below = s_below, moves = total - below, room = npages / 2;
+  for (int g = warp; g < groups; g += kWarps) {
+    int at = base + mine_before[g];
+    for (int i = g * kGroup; i < (g + 1) * kGroup; ++i) {
+      const uint32_t h = held[i];
+      const int id = (rank * n.slice + i) * 32 + lane, k = at + __popc(h & ((1u << lane) - 1));
+      at += __popc(h);
+      if (id >= npages) continue;
+      if (h >> lane & 1) {
+        if (id >= total) a.pairs[2 * (k - below)] = id;
+      } else if (id < total) {
+        a.pairs[2 * (id - k) + 1] = id;
+      }
+    }
+  }
+  for (int i = moves + rank * kThreads + tid; i < room; i += kCtas * kThreads) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
+  if (rank == 0 && tid == 0) a.counts[0] = total, a.counts[1] = moves;
+  sync_all<kCtas>();
+  for_entries(mine, width, load, [&](int r, int j, int id) {
+    if (id < 0 || id >= npages) id = -1;
+    else if (id >= total) id = __ldcg(&a.pairs[2 * (held_before(id) - below) + 1]);
+    a.new_table[(rank + static_cast<int64_t>(r) * kCtas) * a.new_stride + j] = id;
+  });
+}
+
+// ---------------------------------------------------------------- copies
+constexpr int kCopyThreads = 256, kCopyEach = 4;
+
+// 16 B an item, four items of a thread in flight; the items of a page lie in
+// the order of its memory (K's), so that a warp's are neighbours.
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ PageCopyArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t pair = a.parts == 1 ? blockIdx.x : blockIdx.x / static_cast<unsigned>(a.parts);
+  const int part = static_cast<int>(blockIdx.x - pair * a.parts);
+  const int from = a.pairs[2 * pair], to = a.pairs[2 * pair + 1];
+  const int tokens = a.tokens ? min(max(a.tokens[pair], 0), a.cache.page_size) : a.cache.page_size;
+  if (from < 0 || to < 0) return;
+  if (from >= a.cache.pages || to >= a.cache.pages) {
+    if (threadIdx.x == 0) record_index(a.status);
+    return;
+  }
+  uint4 x[kCopyEach];
+  uint4 *dst[kCopyEach];
+#pragma unroll
+  for (int u = 0; u < kCopyEach; ++u) {
+    int i = (part * kCopyEach + u) * kCopyThreads + static_cast<int>(threadIdx.x);
+    const bool is_v = i >= a.per_tensor;
+    if (is_v) i -= a.per_tensor;
+    dst[u] = nullptr;
+    if (i >= a.per_tensor) continue;
+    const int outer = a.by_outer(i), rest = i - outer * a.outer_items, inner = a.by_chunks(rest), col = (rest - inner * a.chunks) << 3;
+    const int t = a.token_outer ? outer : inner, head = a.token_outer ? inner : outer;
+    if (t >= tokens) continue;
+    const int64_t in_page = is_v ? t * a.cache.v_token + head * a.cache.v_head + col : t * a.cache.k_token + head * a.cache.k_head + col;
+    uint16_t *p = static_cast<uint16_t *>(is_v ? a.cache.v : a.cache.k);
+    const int64_t pitch = is_v ? a.cache.v_page : a.cache.k_page;
+    x[u] = __ldcs(reinterpret_cast<const uint4 *>(p + from * pitch + in_page));
+    dst[u] = reinterpret_cast<uint4 *>(p + to * pitch + in_page);
+  }
+#pragma unroll
+  for (int u = 0; u < kCopyEach; ++u)
+    if (dst[u]) *dst[u] = x[u];
+}
+
+template <class K>
+cudaError_t allow(K kernel, size_t smem) {
+  if (smem <= 24 * 1024) return cudaSuccess;  // (beside the static arrays, within the 48 KB that need no leave)
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+}
+
+// One CTA or a cluster of eight.
+constexpr int kMany = 8;
+bool one_cta(int64_t rows, int64_t width, int64_t npages) {
+  return rows <= kThreads && rows * width <= 8192 && npages <= 32768;
+}
+
+template <int kCtas>
+cudaError_t launch_fork_with(const ForkArgs &a, cudaStream_t s) {
+  const Bits n(a.npages, kCtas);
+  const size_t smem = sizeof(uint32_t) * (n.words + 2 * static_cast<size_t>(n.slice));
+  const cudaError_t e = allow(fork_kernel<kCtas>, smem);
+  return e != cudaSuccess ? e : launch_early(fork_kernel<kCtas>, kCtas, 1, kThreads, smem, s, a);
+}
+
+template <int kCtas>
+cudaError_t launch_compact_with(const CompactArgs &a, cudaStream_t s) {
+  const Bits n(a.npages, kCtas);
+  const size_t groups = n.slice / kGroup;
+  const size_t smem = sizeof(uint32_t) * ((kCtas + 1) * static_cast<size_t>(n.slice) + (kCtas + 1) * groups);
+  const cudaError_t e = allow(compact_kernel<kCtas>, smem);
+  return e != cudaSuccess ? e : launch_early(compact_kernel<kCtas>, kCtas, 1, kThreads, smem, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_page_fork(const ForkArgs &a, cudaStream_t s) {
+  return one_cta(a.nnew, a.table_width, a.npages) ? launch_fork_with<1>(a, s) : launch_fork_with<kMany>(a, s);
+}
+
+cudaError_t launch_page_compact(const CompactArgs &a, cudaStream_t s) {
+  return one_cta(a.nreq, a.table_width, a.npages) ? launch_compact_with<1>(a, s) : launch_compact_with<kMany>(a, s);
+}
+
+cudaError_t launch_page_copy(PageCopyArgs a, cudaStream_t s) {
+  const mmq_paged_cache &c = a.cache;
+  a.chunks = c.head_dim >> 3;
+  a.token_outer = c.k_token >= c.k_head;
+  a.outer_items = (a.token_outer ? c.heads : c.page_size) * a.chunks;
+  a.per_tensor = c.page_size * c.heads * a.chunks;
+  a.by_chunks = FastDiv(a.chunks), a.by_outer = FastDiv(a.outer_items);
+  constexpr int kPer = kCopyThreads * kCopyEach;
+  a.parts = static_cast<int>((2 * static_cast<int64_t>(a.per_tensor) + kPer - 1) / kPer);
+  if (a.npairs > 0x7fffffff / a.parts) return cudaErrorNotSupported;
+  return launch_early(copy_kernel, static_cast<unsigned>(a.npairs * a.parts), 1, kCopyThreads, 0, s, a);
+}
+
+}  // namespace mmq

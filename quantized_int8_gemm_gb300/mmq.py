@@ -57,6 +57,8 @@ EXPORTS = [
     "mmq_last_device_error", "mmq_set_wait_timeout_ns",
     "mmq_selftest_wait_timeout", "mmq_strerror", "mmq_probe_engine_rates",
     "mmq_page_tables", "mmq_kv_write", "mmq_paged_attention", "mmq_verify_draft",
+    "mmq_page_fork", "mmq_page_compact", "mmq_page_copy", "mmq_token_probs",
+    "mmq_lora_plan", "mmq_lora_plan_words", "mmq_lora",
 ]
 
 _lock = threading.Lock()
@@ -107,11 +109,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.mmq_kv_write.argtypes = [vp, vp, i64, i64, vp, i64, i64, i32, vp, i64, vp]
         L.mmq_paged_attention.argtypes = [vp, vp, vp]
         L.mmq_verify_draft.argtypes = [vp, vp]
+        L.mmq_page_fork.argtypes = [vp, vp]
+        L.mmq_page_compact.argtypes = [vp, vp, i64, i64, i64, i64, vp, i64, vp, vp, vp]
+        L.mmq_page_copy.argtypes = [vp, vp, vp, i64, vp]
+        L.mmq_token_probs.argtypes = [vp, vp]
+        L.mmq_lora_plan.argtypes = [vp, vp, i64, i64, i64, vp, vp]
+        L.mmq_lora_plan_words.argtypes = [i64, i64, i64]
+        L.mmq_lora.argtypes = [vp, vp]
         L.mmq_strerror.restype = ctypes.c_char_p
         for n in EXPORTS:
             f = getattr(L, n)
             if n not in ("mmq_set_wait_timeout_ns", "mmq_strerror"):
-                f.restype = ctypes.c_int
+                f.restype = i64 if n == "mmq_lora_plan_words" else ctypes.c_int
         _lib = L
         return L
 
