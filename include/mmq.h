@@ -605,7 +605,7 @@ typedef struct mmq_token_rules {
  * is among the tokens behind the prompt and those drafted ones, in fp32 and in
  * this order:
  *   x = logits[v];  v among the tokens or drafted ones: x = x > 0 ? x / repetition : x * repetition
- *   x -= frequency * c(v);  c(v) > 0: x -= presence;  x += the biases of v, in their order
+ *   x -= frequency * c(v);  c(v) > 0: x -= presence;  x += the sum of v's biases, in their order
  *   v not allowed by the row's mask: x = -inf
  *   adjusted[v] = x;  probs = softmax(x / temperature), over the row
  * temperature not above 0: probability 1 for the largest x (ties: the lowest
@@ -616,10 +616,12 @@ typedef struct mmq_token_rules {
  *   Tokens, drafted tokens and biases outside [0, vocab) are left out, a mask
  * row past nmasks is no mask, token_lens past tokens_width, n_draft past
  * rows - 1, bias_start past nbias are cut; all of them are reported by
- * mmq_last_device_error.  A token counts 32767 times at the most.
- * vocab in 1..2^18 (more: MMQ_ERR_UNSUPPORTED), nreq*rows below 2^27.  One
- * kernel, no scratch.  Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN (elements off their
- * own alignment), MMQ_ERR_TYPE, MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE,
+ * mmq_last_device_error.
+ * vocab in 1..2^18, nreq*rows below 2^27 (more: MMQ_ERR_UNSUPPORTED).  With
+ * tokens or biases each request's are listed first, in stream-ordered scratch as for
+ * mmq_gemm (12 bytes a token and bias, a bit for each of the vocabulary).
+ * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN (elements off their own alignment),
+ * MMQ_ERR_TYPE, MMQ_ERR_OOM, MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE,
  * MMQ_ERR_CUDA.
  */
 int mmq_token_probs(const mmq_token_rules *args, mmq_stream_t stream);
@@ -670,9 +672,10 @@ typedef struct mmq_lora_args {
  * out is y (the usual call, behind mmq_gemm_f32) only rows with an adapter are
  * touched.  Rows and columns of a and b past an adapter's rank are not used,
  * whatever they hold.
- *   Sums are fp32.  x and the inner sums enter the tensor cores as two 16-bit
- * terms (an error of 2^-17 at the most).  The results of one problem do not
- * change from call to call.  One kernel, no scratch.
+ *   Sums are fp32; x and the inner sums enter the tensor cores as three 16-bit
+ * terms, which hold their 24 bits.  An x or an inner sum that is not finite makes its row NaN
+ * (infinities among them).  The results of one problem do not change from call
+ * to call.  One kernel, no scratch.
  * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN, MMQ_ERR_TYPE, MMQ_ERR_UNSUPPORTED,
  * MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
  */

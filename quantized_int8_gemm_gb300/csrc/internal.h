@@ -102,20 +102,31 @@ int call_context(CallContext *out);
 
 // Launches a kernel that may begin while the one before it on the stream ends
 // (it calls griddep_wait before it touches memory another kernel may use).
+// cluster: CTAs of a cluster, where the kernel does not say itself.
+struct Cluster {
+  unsigned ctas = 0;
+};
 template <class... Params, class... Args>
-cudaError_t launch_early(void (*kernel)(Params...), unsigned grid_x, unsigned grid_y, unsigned threads, size_t smem, cudaStream_t s,
+cudaError_t launch_early(void (*kernel)(Params...), Cluster cluster, unsigned grid_x, unsigned grid_y, unsigned threads, size_t smem, cudaStream_t s,
                          const Args &...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid_x, grid_y);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster.ctas, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster.ctas ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), unsigned grid_x, unsigned grid_y, unsigned threads, size_t smem, cudaStream_t s,
+                         const Args &...args) {
+  return launch_early(kernel, Cluster{}, grid_x, grid_y, threads, smem, s, args...);
 }
 
 // Division of 0 <= n < 2^31 by a number the host knows: with l = ceil(log2 d)
@@ -200,15 +211,21 @@ cudaError_t launch_page_copy(PageCopyArgs a, cudaStream_t s);
 
 struct RulesArgs {
   mmq_token_rules t;
-  bool penalties, many;  // tokens are counted; more of them than 15 bits hold
-  int32_t slice;         // entries of a CTA
+  bool penalties, sparse, in_place;  // tokens are counted; there are lists; adjusted is the logits
+  int32_t slice, ctas_log2;          // entries of a CTA; CTAs of a row
   FastDiv by_rows;
+  // of each request: a bit for each listed token, where each CTA's part of its
+  // list begins; of all: the listed tokens, their counts and biases
+  uint32_t *touched;
+  int32_t *starts, *list;
+  uint32_t *counts;
+  float *biases;
   int *status;
   unsigned *abort_epoch;
   unsigned epoch;
   uint64_t limit_ns;
 };
-cudaError_t launch_token_probs(RulesArgs a, cudaStream_t s);
+cudaError_t launch_token_probs(RulesArgs a, const CallContext &ctx, cudaStream_t s);
 
 struct LoraPlanArgs {
   const int32_t *adapters, *q_start;
@@ -216,6 +233,7 @@ struct LoraPlanArgs {
   int32_t *plan;
   int *status;
   int32_t tile, slots;  // tokens of a tile; keys that are sorted, a power of two
+  bool few;             // keys few enough to be compared with one another
 };
 cudaError_t launch_lora_plan(LoraPlanArgs a, cudaStream_t s);
 int64_t lora_plan_words(int64_t ntok, int64_t nreq, int64_t nadapters);

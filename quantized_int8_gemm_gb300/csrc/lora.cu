@@ -64,117 +64,143 @@ __device__ __forceinline__ int last_not_above(const int *sums, int n, int x) {
 
 // Keys (adapter, request) are sorted in shared memory, so the order does not
 // depend on the threads'.  Every CTA sorts for itself and writes its tokens.
+// Latency bound: two rounds of reads, the sort, four sums over the CTA.
 __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const __grid_constant__ LoraPlanArgs a) {
-  extern __shared__ uint32_t keys[];  // a.slots (a power of two), then the tokens and the tiles before each key
+  // a.slots (a power of two) keys, as they come and sorted, then of the sorted ones'
+  // the first row and the tokens and tiles before them; one more for the ends
+  extern __shared__ __align__(16) uint32_t loaded[];
   __shared__ int s_warp[32];
   __shared__ int s_bad;
-  int *tokens_before = reinterpret_cast<int *>(keys + a.slots), *tiles_before = tokens_before + a.slots;
+  uint32_t *keys = loaded + (a.few ? a.slots : 0);
+  int *begins = reinterpret_cast<int *>(keys + a.slots), *tokens_before = begins + a.slots, *tiles_before = tokens_before + a.slots + 1;
   const int tid = threadIdx.x, nreq = static_cast<int>(a.nreq), ntok = static_cast<int>(a.ntok);
   griddep_wait();
   griddep_launch_dependents();
   if (tid == 0) s_bad = 0;
   __syncthreads();
-  auto bounds = [&](int b, int &begin, int &end) {
-    begin = a.q_start[b], end = a.q_start[b + 1];
-    const bool descends = end < begin || begin < 0;
-    begin = min(max(begin, 0), ntok), end = min(max(end, 0), ntok);
-    return !descends;
-  };
   for (int i = tid; i < a.slots; i += kPlanThreads) {
     uint32_t key = kEmpty;
     if (i < nreq) {
-      int begin, end;
-      if (!bounds(i, begin, end)) s_bad = 1, record_index(a.status);
-      int id = a.adapters[i];
+      int begin = a.q_start[i], end = a.q_start[i + 1], id = a.adapters[i];
+      if (end < begin || begin < 0) s_bad = 1, record_index(a.status);
+      begin = min(max(begin, 0), ntok), end = min(max(end, 0), ntok);
       if (id < -1 || id >= a.nadapters) record_index(a.status), id = -1;
       if (end > begin) key = (id < 0 ? kNone : static_cast<uint32_t>(id)) << kRequestBits | static_cast<uint32_t>(i);
     }
-    keys[i] = key;
+    loaded[i] = key;
   }
   __syncthreads();
-  for (int size = 2; size <= a.slots; size <<= 1) {
-    for (int step = size >> 1; step; step >>= 1) {
-      for (int i = tid; i < a.slots >> 1; i += kPlanThreads) {
-        const int p = 2 * i - (i & (step - 1)), q = p + step;
-        const uint32_t x = keys[p], y = keys[q];
-        if ((x > y) == ((p & size) == 0)) keys[p] = y, keys[q] = x;
+  if (a.few) {
+    // a key's place is the number of smaller ones (no two are alike but empty
+    // ones, which follow in the order that they came)
+    if (tid < a.slots) {
+      const uint32_t mine = loaded[tid];
+      int place = 0;
+      if (a.slots < 4) {
+        for (int i = 0; i < a.slots; ++i) place += loaded[i] < mine || (loaded[i] == mine && i < tid);
+      } else if (mine == kEmpty) {
+        for (int i = 0; i < a.slots; ++i) place += loaded[i] < mine || i < tid;
+      } else {
+        for (int i = 0; i < a.slots; i += 4) {
+          const uint4 k = *reinterpret_cast<const uint4 *>(loaded + i);
+          place += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
+        }
       }
-      __syncthreads();
+      keys[place] = mine;
+    }
+    __syncthreads();
+  } else {
+    for (int size = 2; size <= a.slots; size <<= 1) {
+      for (int step = size >> 1; step; step >>= 1) {
+        for (int i = tid; i < a.slots >> 1; i += kPlanThreads) {
+          const int p = 2 * i - (i & (step - 1)), q = p + step;
+          const uint32_t x = keys[p], y = keys[q];
+          if ((x > y) == ((p & size) == 0)) keys[p] = y, keys[q] = x;
+        }
+        __syncthreads();
+      }
     }
   }
   // (each thread has the keys from tid * per on)
   const int per = (a.slots + kPlanThreads - 1) / kPlanThreads, i0 = min(tid * per, a.slots), i1 = min(i0 + per, a.slots);
-  auto length = [&](int i) {
-    if (keys[i] == kEmpty) return 0;
-    int begin, end;
-    bounds(static_cast<int>(keys[i] & ((1u << kRequestBits) - 1)), begin, end);
-    return end - begin;
-  };
   auto adapter = [&](int i) { return keys[i] >> kRequestBits; };
   int sum = 0, total, none;
-  for (int i = i0; i < i1; ++i) sum += length(i);
-  int at = plan_exclusive(sum, total, s_warp, false);
+  for (int i = i0; i < i1; ++i) {
+    int begin = 0, end = 0;
+    if (keys[i] != kEmpty) {
+      const int b = static_cast<int>(keys[i] & ((1u << kRequestBits) - 1));
+      begin = min(max(a.q_start[b], 0), ntok), end = min(max(a.q_start[b + 1], 0), ntok);
+    }
+    begins[i] = begin, tokens_before[i] = sum;  // (of the thread's, for now)
+    sum += end - begin;
+  }
+  const int at = plan_exclusive(sum, total, s_warp, false);
   int first = 0;  // largest begin of a group up to here
   for (int i = i0; i < i1; ++i) {
-    tokens_before[i] = at;
-    if (i == 0 || adapter(i - 1) != adapter(i)) first = at;
-    at += length(i);
+    tokens_before[i] += at;
+    if (i == 0 || adapter(i - 1) != adapter(i)) first = tokens_before[i];
   }
-  __syncthreads();
-  const int before = plan_exclusive(first, none, s_warp, true);
+  if (tid == 0) tokens_before[a.slots] = total;
+  const int before = plan_exclusive(first, none, s_warp, true);  // (and the CTA's threads meet)
   auto tiles_of = [&](int i, int &start) {  // tiles of the group that ends with key i
     if (i == 0 || adapter(i - 1) != adapter(i)) start = tokens_before[i];
-    const int end = i + 1 < a.slots ? tokens_before[i + 1] : total;
     const bool last = keys[i] != kEmpty && (i + 1 == a.slots || adapter(i + 1) != adapter(i));
-    return last ? (end - start + a.tile - 1) / a.tile : 0;
+    return last ? (tokens_before[i + 1] - start + a.tile - 1) / a.tile : 0;
   };
   int start = before, tiles = 0, all_tiles;
   for (int i = i0; i < i1; ++i) tiles += tiles_of(i, start);
   int tile = plan_exclusive(tiles, all_tiles, s_warp, false);
   start = before;
+  const bool bad = s_bad;
+  int32_t *order = a.plan + kHead, *list = order + ntok;
   for (int i = i0; i < i1; ++i) {
     tiles_before[i] = tile;
-    tile += tiles_of(i, start);
+    const int mine = tiles_of(i, start);
+    if (mine && !bad && blockIdx.x == 0) {
+      const int id = adapter(i) == kNone ? -1 : static_cast<int>(adapter(i)), end = tokens_before[i + 1];
+      if (mine <= 4) {  // (groups of many tiles: by all threads, below)
+        for (int k = 0; k < mine; ++k) {
+          int32_t *to = list + 3 * (tile + k);
+          to[0] = id, to[1] = start + k * a.tile, to[2] = min(a.tile, end - start - k * a.tile);
+        }
+      }
+      if (id < 0) a.plan[1] = tile;  // (the tiles without an adapter stand last)
+      else if (tile + mine == all_tiles) a.plan[1] = all_tiles;
+    }
+    tile += mine;
   }
+  if (tid == 0) tiles_before[a.slots] = all_tiles;
   __syncthreads();
-  if (s_bad) total = all_tiles = 0;
-  int32_t *order = a.plan + kHead, *list = order + ntok;
+  if (blockIdx.x == 0 && tid == 0) {
+    a.plan[0] = bad ? 0 : all_tiles;
+    if (bad || all_tiles == 0) a.plan[1] = 0;
+  }
+  if (bad) return;
   const int p0 = static_cast<int>(blockIdx.x) * kPlanTokens, p1 = min(p0 + kPlanTokens, total);
   for (int p = p0 + tid; p < p1; p += kPlanThreads) {
-    const int i = last_not_above(tokens_before, a.slots, p);
-    // (keys without tokens stand last, behind every token)
-    order[p] = a.q_start[keys[i] & ((1u << kRequestBits) - 1)] + (p - tokens_before[i]);
+    const int i = last_not_above(tokens_before, a.slots, p);  // (keys without tokens stand last, behind every token)
+    order[p] = begins[i] + (p - tokens_before[i]);
   }
   for (int k = static_cast<int>(blockIdx.x) * kPlanThreads + tid; k < all_tiles; k += static_cast<int>(gridDim.x) * kPlanThreads) {
-    const int i = last_not_above(tiles_before, a.slots, k);
-    int g = i;  // the group's first key
-    if (i > 0) {
-      int lo = -1, hi = i;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (adapter(mid) == adapter(i)) hi = mid;
-        else lo = mid;
-      }
-      g = hi;
+    const int i = last_not_above(tiles_before, a.slots, k);  // the group's last key
+    if (tiles_before[i + 1] - tiles_before[i] <= 4) continue;
+    int lo = -1, hi = i;  // its first one
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (adapter(mid) == adapter(i)) hi = mid;
+      else lo = mid;
     }
-    const int end = i + 1 < a.slots ? tokens_before[i + 1] : total;
-    const int begin = tokens_before[g] + (k - tiles_before[i]) * a.tile;
-    const uint32_t id = adapter(i);
-    list[3 * k] = id == kNone ? -1 : static_cast<int>(id);
+    const int begin = tokens_before[hi] + (k - tiles_before[i]) * a.tile;
+    list[3 * k] = adapter(i) == kNone ? -1 : static_cast<int>(adapter(i));
     list[3 * k + 1] = begin;
-    list[3 * k + 2] = min(a.tile, end - begin);
-    if (id != kNone && (k + 1 == all_tiles || adapter(last_not_above(tiles_before, a.slots, k + 1)) == kNone)) a.plan[1] = k + 1;
-    if (k == 0 && id == kNone) a.plan[1] = 0;
-  }
-  if (blockIdx.x == 0 && tid == 0) {
-    a.plan[0] = all_tiles;
-    if (all_tiles == 0) a.plan[1] = 0;
+    list[3 * k + 2] = min(a.tile, tokens_before[i + 1] - begin);
   }
 }
 
 // ---------------------------------------------------------------- products
 constexpr int kCtas = 8, kThreads = 256, kWarps = kThreads / 32;
 constexpr int kRankPass = 64;  // ranks whose sums a warp holds at once
+constexpr int kStages = 3;
 
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -184,6 +210,13 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+// 16 bytes to shared memory in the background, or 16 zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
 
 // D += A B, 16 x 16 by 16 x 8, bf16 in, fp32 sums.
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -199,16 +232,21 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// A pair of numbers as two bf16 terms: x = h + l, off by 2^-18 of x at the most
-// (each term is rounded to nearest, 2^-9 of what it stands for).  An infinite or
-// NaN number keeps its value in h and has l = 0 or NaN.
+// A pair of numbers as three bf16 terms: each is rounded to nearest, so that
+// what is left after it is at most 2^-9 of what it stands for, and after the
+// third nothing of an fp32 number's 24 bits.  (With two terms, 2^-18 off, the
+// outputs were 1.2 to 2.9e-6 from the 64-bit ones; fp32 sums are 2 to 8e-7 off.)
+constexpr int kTerms = 3;
 struct Terms {
-  uint32_t h, l;
+  uint32_t w[kTerms];
 };
 __device__ __forceinline__ Terms split(float x, float y) {
   Terms t;
-  t.h = pack(x, y);
-  t.l = pack(x - low(t.h), y - high(t.h));
+#pragma unroll
+  for (int i = 0; i < kTerms; ++i) {
+    t.w[i] = pack(x, y);
+    x -= low(t.w[i]), y -= high(t.w[i]);
+  }
   return t;
 }
 
@@ -217,81 +255,116 @@ template <class W>
 struct Weights8;
 template <>
 struct Weights8<__nv_bfloat16> {
-  uint32_t h[4];
-  __device__ __forceinline__ void set(uint4 r) { h[0] = r.x, h[1] = r.y, h[2] = r.z, h[3] = r.w; }
+  static constexpr int kParts = 1;
+  uint32_t w[1][4];
+  __device__ __forceinline__ void set(uint4 r) { w[0][0] = r.x, w[0][1] = r.y, w[0][2] = r.z, w[0][3] = r.w; }
 };
 template <>
 struct Weights8<__half> {
-  uint32_t h[4], l[4];
+  static constexpr int kParts = 2;
+  uint32_t w[2][4];
   __device__ __forceinline__ void set(uint4 r) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    const uint32_t v[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-      const Terms t = split(f.x, f.y);
-      h[i] = t.h, l[i] = t.l;
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v[i]));
+      w[0][i] = pack(f.x, f.y);
+      w[1][i] = pack(f.x - low(w[0][i]), f.y - high(w[0][i]));
     }
   }
 };
 
 // The lane's eight columns (two steps of 16) of rows p and q of weights by
-// those of eight rows of terms.  Which column is which within the 32 does not matter as
-// long as both sides agree: lane quarter c has columns 8c .. 8c + 7, which lie
-// together in memory.
+// those of eight rows of terms.  Which column is which within the 32 does not
+// matter as long as both sides agree: lane quarter c has columns 8c .. 8c + 7,
+// which lie together in memory.  Small products first; those of terms that
+// together are below 2^-24 are left out.
 template <class W>
 __device__ __forceinline__ void product(float (&d)[4], const Weights8<W> &p, const Weights8<W> &q, const Terms (&x)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; k += 2) {
-    mma(d, p.h[k], q.h[k], p.h[k + 1], q.h[k + 1], x[k].h, x[k + 1].h);
-    mma(d, p.h[k], q.h[k], p.h[k + 1], q.h[k + 1], x[k].l, x[k + 1].l);
-    if constexpr (sizeof(Weights8<W>) == 32) mma(d, p.l[k], q.l[k], p.l[k + 1], q.l[k + 1], x[k].h, x[k + 1].h);
+#pragma unroll
+    for (int order = kTerms - 1; order >= 0; --order) {
+#pragma unroll
+      for (int i = Weights8<W>::kParts - 1; i >= 0; --i) {
+        const int j = order - i;
+        if (j < 0) continue;
+        mma(d, p.w[i][k], q.w[i][k], p.w[i][k + 1], q.w[i][k + 1], x[k].w[j], x[k + 1].w[j]);
+      }
+    }
   }
 }
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0, 0, 0, 0); }
 
-// Eight numbers of x as terms.
-__device__ __forceinline__ void load_x(Terms (&out)[4], const void *row, int x_type, int k, bool there) {
-  float v[8] = {};
-  if (there) {
-    if (x_type == MMQ_DT_F32) {
-      const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(row) + k);
-      const float4 a = __ldg(p), b = __ldg(p + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      const uint4 r = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + k));
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// Eight numbers of x as terms, from 16 or 32 bytes (a and, if fp32, b).
+__device__ __forceinline__ void split8(Terms (&out)[4], uint4 a, uint4 b, int x_type) {
+  if (x_type == MMQ_DT_F32) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = x_type == MMQ_DT_F16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w[i])) : make_float2(low(w[i]), high(w[i]));
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
-      }
-    }
+    for (int i = 0; i < 4; ++i) out[i] = split(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    return;
   }
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) out[i] = split(v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = x_type == MMQ_DT_F16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w[i])) : make_float2(low(w[i]), high(w[i]));
+    out[i] = split(f.x, f.y);
+  }
 }
 
-// Shared memory: partial sums of the CTA's warps; of the CTA; the joined sums
-// as terms, a token's ranks together, rows 16 words from a multiple of 32
-// apart (eight lanes of a 16-byte read then touch every bank once).
+// How a CTA's warps share the first product: over groups of tokens and, within
+// a piece of x's columns, over 32 columns each.
 template <int kTile>
 struct Shape {
-  static constexpr int kTokens = kTile > 16 ? 16 : kTile;      // tokens of a warp in the first product
-  static constexpr int kGroups = kTile / kTokens;              // warps side by side over tokens
-  static constexpr int kSplit = kWarps / kGroups;              // and over the columns of x
-  static constexpr int kColumns = kTokens / 8;
+  static constexpr int kTokens = kTile == 64 ? 16 : 8, kGroups = kTile / kTokens, kSplit = kWarps / kGroups, kColumns = kTokens / 8;
+  static constexpr int kPiece = 32 * kSplit;                  // columns of a stage
+  static constexpr bool kStaged = kTile > 8;
+  static constexpr int kXStage = kTile * kPiece * 4, kStage = kXStage + kRankPass * kPiece * 2;  // bytes
+  // the terms of the joined sums: a token's ranks together, rows 16 words from
+  // a multiple of 32 apart (eight lanes of a 16-byte read then touch every
+  // bank once)
   __host__ __device__ static constexpr int pitch(int rank) { return (rank + 31) / 32 * 16 % 32 ? (rank + 31) / 32 * 16 : (rank + 31) / 32 * 16 + 16; }
-  static size_t bytes(int rank) {
-    return 4 * (static_cast<size_t>(kSplit) * kRankPass * kTile + static_cast<size_t>((rank + 15) / 16 * 16) * kTile +
-                2 * static_cast<size_t>(kTile) * pitch(rank));
+  // Shared memory: stages of the first product, then the partial sums of the
+  // warps, then the terms in one place; the CTA's sums behind it.
+  __host__ __device__ static constexpr int front(int rank) {
+    const int stages = kStaged ? kStages * kStage : 0, part = 4 * kSplit * kRankPass * kTile, terms = 4 * kTerms * kTile * pitch(rank);
+    return stages > part ? (stages > terms ? stages : terms) : (part > terms ? part : terms);
   }
+  static size_t bytes(int rank) { return front(rank) + 4 * static_cast<size_t>((rank + 15) / 16 * 16) * kTile; }
 };
 
+// Rows of a tile without an adapter: out = y over the CTA's columns.
+template <int kTile>
+__device__ __forceinline__ void copy_rows(const LoraArgs &a, const int (&s_row)[kTile], int n, int o0, int o1) {
+  const mmq_lora_args &t = a.t;
+  constexpr int kEach = 8;
+  const int width = a.wide ? (o1 - o0) / 4 : o1 - o0, items = n * width;
+  for (int i0 = threadIdx.x; i0 < items; i0 += kEach * kThreads) {
+    float4 v[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= items) continue;
+      const float *from = t.y + s_row[i / width] * t.y_row + o0 + (a.wide ? 4 : 1) * (i % width);
+      if (a.wide) v[u] = __ldcs(reinterpret_cast<const float4 *>(from));
+      else v[u].x = *from;
+    }
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= items) continue;
+      float *to = t.out + s_row[i / width] * t.out_row + o0 + (a.wide ? 4 : 1) * (i % width);
+      if (a.wide) *reinterpret_cast<float4 *>(to) = v[u];
+      else *to = v[u].x;
+    }
+  }
+}
+
 template <class W, int kTile>
-__global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lora_kernel(const __grid_constant__ LoraArgs a) {
+__global__ void __launch_bounds__(kThreads, kTile == 8 ? 3 : 2) __cluster_dims__(kCtas, 1, 1) lora_kernel(const __grid_constant__ LoraArgs a) {
   using S = Shape<kTile>;
-  extern __shared__ __align__(16) float smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_row[kTile];
   const mmq_lora_args &t = a.t;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -299,73 +372,133 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lor
   griddep_wait();
   griddep_launch_dependents();
   const bool in_place = t.y == t.out;
-  if (tile >= t.plan[in_place ? 1 : 0]) return;  // (the whole cluster)
   const int32_t *entry = t.plan + kHead + t.ntok + 3 * static_cast<int64_t>(tile);
+  if (tile >= t.plan[in_place ? 1 : 0]) return;  // (the whole cluster)
   const int adapter = entry[0], first = entry[1], n = entry[2];
   if (tid < kTile) s_row[tid] = tid < n ? t.plan[kHead + first + tid] : -1;
   const int id = static_cast<int>(t.id), od = static_cast<int>(t.od), rmax = t.rank;
+  const int units = (od + 31) / 32, per = (units + kCtas - 1) / kCtas, u0 = min(rank * per, units), u1 = min(u0 + per, units);
+  const W *up = static_cast<const W *>(t.b) + static_cast<int64_t>(max(adapter, 0)) * od * rmax;
+  if (kTile <= 16 && adapter >= 0) {
+    // few tokens: the adapter is most of what is read, so the second product's
+    // part comes to L2 during the first
+    const char *from = reinterpret_cast<const char *>(up + static_cast<int64_t>(32 * u0) * rmax);
+    const int64_t bytes = static_cast<int64_t>(min(32 * u1, od) - 32 * u0) * rmax * 2;
+    for (int64_t at = tid * 4096; at < bytes; at += kThreads * 4096)
+      bulk_prefetch_l2(from + at, static_cast<uint32_t>(min(bytes - at, static_cast<int64_t>(4096))));
+  }
   const int r = adapter < 0 ? 0 : t.ranks ? min(max(t.ranks[adapter], 0), rmax) : rmax;
-  const int units = (od + 31) / 32, per = (units + kCtas - 1) / kCtas, u1 = min((rank + 1) * per, units);
+  const float scale = t.scales && adapter >= 0 ? t.scales[adapter] : 1.0f;
   __syncthreads();
   if (r == 0) {
-    if (in_place) return;
-    for (int k = 0; k < n; ++k) {
-      const int64_t row = s_row[k];
-      for (int o = rank * per * 32 + tid; o < min(u1 * 32, od); o += kThreads) t.out[row * t.out_row + o] = t.y[row * t.y_row + o];
-    }
+    if (!in_place) copy_rows<kTile>(a, s_row, n, min(32 * u0, od), min(32 * u1, od));
     return;
   }
   const int r16 = (r + 15) / 16 * 16, r32 = (r + 31) / 32 * 32, pitch = S::pitch(rmax);
-  float *part = smem, *mine = part + S::kSplit * kRankPass * kTile;  // [split][rank of the pass][token]; [rank][token]
-  uint32_t *terms = reinterpret_cast<uint32_t *>(mine + (rmax + 15) / 16 * 16 * kTile);  // [term][token][pitch]
-  for (int k = tid; k < 2 * kTile * pitch; k += kThreads) terms[k] = 0;  // (ranks past r)
+  float *part = reinterpret_cast<float *>(smem), *mine = reinterpret_cast<float *>(smem + S::front(rmax));  // [split][rank of the pass][token]; [rank][token]
+  uint32_t *terms = reinterpret_cast<uint32_t *>(smem);                                                     // [term][token][pitch]
 
   // the first product, transposed: ranks x tokens over the CTA's columns
   {
-    const int steps = (id + 31) / 32, share = (steps + kCtas - 1) / kCtas, end = min((rank + 1) * share, steps);
+    const int pieces = (id + S::kPiece - 1) / S::kPiece, share = (pieces + kCtas - 1) / kCtas;
+    const int p0 = min(rank * share, pieces), p1 = min(p0 + share, pieces);
     const int tokens0 = warp % S::kGroups * S::kTokens, slot = warp / S::kGroups;
-    const W *weights = static_cast<const W *>(t.a) + static_cast<int64_t>(adapter) * rmax * id;
-    const size_t x_size = t.x_type == MMQ_DT_F32 ? 4 : 2;
-    const unsigned char *row[S::kColumns];
-    bool there[S::kColumns];
-#pragma unroll
-    for (int j = 0; j < S::kColumns; ++j) {
-      const int of = s_row[tokens0 + 8 * j + g];
-      there[j] = of >= 0;
-      row[j] = static_cast<const unsigned char *>(t.x) + static_cast<int64_t>(max(of, 0)) * t.x_row * x_size;
-    }
+    const W *down = static_cast<const W *>(t.a) + static_cast<int64_t>(adapter) * rmax * id;
+    const unsigned char *x = static_cast<const unsigned char *>(t.x);
+    const int x_size = t.x_type == MMQ_DT_F32 ? 4 : 2;
     for (int r0 = 0; r0 < r; r0 += kRankPass) {
+      const int ranks = min(r - r0, kRankPass);
       float acc[kRankPass / 16][S::kColumns][4] = {};
-      if (tokens0 < n) {
-        for (int step = rank * share + slot; step < end; step += S::kSplit) {
-          const int k = 32 * step + 8 * c;
-          const bool in = k < id;
-          Terms x[S::kColumns][4];
-          uint4 raw[kRankPass / 16][2];
+      if constexpr (S::kStaged) {
+        // Pieces of x and of the weights in 16-byte chunks, the chunks of odd
+        // rows half a quarter (x) or half a row of 32 columns (weights) off, so
+        // that eight lanes of a read touch every bank once.
+        const uint32_t base = smem_addr(smem);
+        const int x_chunks = S::kPiece * x_size / 16;  // of a row
+        auto x_at = [&](int row, int chunk) {
+          return static_cast<uint32_t>(row * S::kPiece * x_size) + ((chunk ^ (x_size == 4 ? row & 1 : (row & 1) * 4)) << 4);
+        };
+        auto w_at = [&](int row, int chunk) { return static_cast<uint32_t>(S::kXStage + row * S::kPiece * 2) + ((chunk ^ (row & 1) * 4) << 4); };
+        auto load = [&](int p) {
+          const uint32_t to = base + (p - p0) % kStages * S::kStage;
+          const int k0 = p * S::kPiece;
+          for (int i = tid; i < kTile * x_chunks; i += kThreads) {
+            const int row = i / x_chunks, chunk = i % x_chunks, of = s_row[row], k = k0 + chunk * 16 / x_size;
+            const bool there = of >= 0 && k < id;
+            copy16(to + x_at(row, chunk), there ? x + (of * t.x_row + k) * x_size : x, there);
+          }
+          for (int i = tid; i < min(r16 - r0, kRankPass) * (S::kPiece / 8); i += kThreads) {
+            const int row = i / (S::kPiece / 8), chunk = i % (S::kPiece / 8), k = k0 + 8 * chunk;
+            const bool there = row < ranks && k < id;
+            copy16(to + w_at(row, chunk), there ? down + static_cast<int64_t>(r0 + row) * id + k : down, there);
+          }
+        };
 #pragma unroll
-          for (int m = 0; m < kRankPass / 16; ++m) {
+        for (int p = 0; p < kStages - 1; ++p) {
+          if (p0 + p < p1) load(p0 + p);
+          copies_commit();
+        }
+        for (int p = p0; p < p1; ++p) {
+          copies_wait<kStages - 2>();
+          __syncthreads();
+          if (p + kStages - 1 < p1) load(p + kStages - 1);
+          copies_commit();
+          if (tokens0 >= n) continue;
+          const unsigned char *stage = smem + (p - p0) % kStages * S::kStage;
+          Terms xt[S::kColumns][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int of = r0 + 16 * m + 8 * h + g;
-              raw[m][h] = in && of < r ? __ldg(reinterpret_cast<const uint4 *>(weights + static_cast<int64_t>(of) * id + k)) : zero4();
-            }
+          for (int j = 0; j < S::kColumns; ++j) {
+            const int row = tokens0 + 8 * j + g, chunk = (32 * slot + 8 * c) * x_size / 16;
+            const uint4 lo = *reinterpret_cast<const uint4 *>(stage + x_at(row, chunk));
+            const uint4 hi = x_size == 4 ? *reinterpret_cast<const uint4 *>(stage + x_at(row, chunk + 1)) : zero4();
+            split8(xt[j], lo, hi, t.x_type);
           }
 #pragma unroll
-          for (int j = 0; j < S::kColumns; ++j) load_x(x[j], row[j], t.x_type, k, in && there[j]);
-#pragma unroll
           for (int m = 0; m < kRankPass / 16; ++m) {
-            if (r0 + 16 * m >= r) break;
-            Weights8<W> p, q;
-            p.set(raw[m][0]), q.set(raw[m][1]);
+            if (16 * m >= ranks) break;
+            Weights8<W> u, v;
+            u.set(*reinterpret_cast<const uint4 *>(stage + w_at(16 * m + g, 4 * slot + c)));
+            v.set(*reinterpret_cast<const uint4 *>(stage + w_at(16 * m + 8 + g, 4 * slot + c)));
 #pragma unroll
-            for (int j = 0; j < S::kColumns; ++j) product<W>(acc[m][j], p, q, x[j]);
+            for (int j = 0; j < S::kColumns; ++j) product<W>(acc[m][j], u, v, xt[j]);
           }
         }
+        copies_wait<0>();
+        __syncthreads();
+      } else {
+        const int of = s_row[tokens0 + g];
+        const unsigned char *row = x + max(of, 0) * t.x_row * x_size;
+        const int s0 = p0 * S::kSplit + slot, s1 = p1 * S::kSplit;
+        for (int step = s0; step < s1; step += S::kSplit) {
+          const int k = 32 * step + 8 * c;
+          const bool in = k < id;
+          uint4 raw[kRankPass / 16][2], lo = zero4(), hi = zero4();
+#pragma unroll
+          for (int m = 0; m < kRankPass / 16; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int at = 16 * m + 8 * h + g;
+              raw[m][h] = in && at < ranks ? __ldg(reinterpret_cast<const uint4 *>(down + static_cast<int64_t>(r0 + at) * id + k)) : zero4();
+            }
+          if (in && of >= 0) {
+            lo = __ldg(reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(k) * x_size));
+            if (x_size == 4) hi = __ldg(reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(k) * x_size) + 1);
+          }
+          Terms xt[4];
+          split8(xt, lo, hi, t.x_type);
+#pragma unroll
+          for (int m = 0; m < kRankPass / 16; ++m) {
+            if (16 * m >= ranks) break;
+            Weights8<W> u, v;
+            u.set(raw[m][0]), v.set(raw[m][1]);
+            product<W>(acc[m][0], u, v, xt);
+          }
+        }
+        if (r0) __syncthreads();
       }
-      if (r0) __syncthreads();
 #pragma unroll
       for (int m = 0; m < kRankPass / 16; ++m) {
-        if (r0 + 16 * m >= r) break;
+        if (16 * m >= ranks) break;
 #pragma unroll
         for (int j = 0; j < S::kColumns; ++j) {
           float *to = part + (slot * kRankPass + 16 * m + g) * kTile + tokens0 + 8 * j + 2 * c;
@@ -374,19 +507,19 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lor
         }
       }
       __syncthreads();
-      const int here = min(r16 - r0, kRankPass) * kTile;
-      for (int e = tid; e < here; e += kThreads) {
+      for (int e = tid; e < min(r16 - r0, kRankPass) * kTile; e += kThreads) {
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < S::kSplit; ++k) s += part[k * kRankPass * kTile + e];
         mine[r0 * kTile + e] = s;
       }
+      if (S::kStaged || r0 + kRankPass >= r) __syncthreads();  // (part makes room)
     }
   }
+  for (int k = tid; k < kTerms * kTile * pitch; k += kThreads) terms[k] = 0;  // (ranks past r)
   cluster_sync();
   // joined over the cluster: each CTA adds up a share of the pairs of ranks and
   // sends it to all
-  const float scale = t.scales ? t.scales[adapter] : 1.0f;
   for (int e = rank * kThreads + tid; e < r16 / 2 * kTile; e += kCtas * kThreads) {
     const int pair = e / kTile, token = e % kTile;
     float s0 = 0.0f, s1 = 0.0f, v0[kCtas], v1[kCtas];
@@ -401,18 +534,17 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lor
 #pragma unroll
     for (int k = 0; k < kCtas; ++k) {
       const uint32_t to = mapa_shared(smem_addr(terms + token * pitch + pair), k);
-      st_cluster(to, sum.h);
-      st_cluster(to + 4 * kTile * pitch, sum.l);
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i) st_cluster(to + 4 * i * kTile * pitch, sum.w[i]);
     }
   }
   cluster_sync();
 
   // the second product: 32 output columns of a warp at a time, of which a lane
   // has four that lie together (rows g and g + 8 of two blocks of 16)
-  const W *weights = static_cast<const W *>(t.b) + static_cast<int64_t>(adapter) * od * rmax;
   constexpr int kEach = kTile < 32 ? kTile / 8 : 4;  // columns of eight tokens at once
   const int columns = (n + 7) / 8;
-  for (int u = rank * per + warp; u < u1; u += kWarps) {
+  for (int u = u0 + warp; u < u1; u += kWarps) {
     const int o = 32 * u + 4 * g;
     for (int j0 = 0; j0 < columns; j0 += kEach) {
       float4 y[kEach][2];
@@ -425,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lor
           at[j][h] = k < n ? s_row[k] : -1;
           y[j][h] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if (at[j][h] < 0 || o >= od) continue;
-          const float *from = t.y + static_cast<int64_t>(at[j][h]) * t.y_row + o;
+          const float *from = t.y + at[j][h] * t.y_row + o;
           if (a.wide) {
             y[j][h] = __ldcs(reinterpret_cast<const float4 *>(from));
           } else {
@@ -443,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lor
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint4 raw = zero4();
-          if (k < r && o + i < od) raw = __ldg(reinterpret_cast<const uint4 *>(weights + static_cast<int64_t>(o + i) * rmax + k));
+          if (k < r && o + i < od) raw = __ldg(reinterpret_cast<const uint4 *>(up + static_cast<int64_t>(o + i) * rmax + k));
           if (k < r && k + 8 > r) {  // columns past the rank
             uint32_t *v = &raw.x;
 #pragma unroll
@@ -453,9 +585,12 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lor
         }
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
-          const uint32_t *from = terms + (8 * (j0 + j) + g) * pitch + k / 2;
-          const uint4 h = *reinterpret_cast<const uint4 *>(from), l = *reinterpret_cast<const uint4 *>(from + kTile * pitch);
-          const Terms x[4] = {{h.x, l.x}, {h.y, l.y}, {h.z, l.z}, {h.w, l.w}};
+          Terms x[4];
+#pragma unroll
+          for (int i = 0; i < kTerms; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(terms + (i * kTile + 8 * (j0 + j) + g) * pitch + k / 2);
+            x[0].w[i] = v.x, x[1].w[i] = v.y, x[2].w[i] = v.z, x[3].w[i] = v.w;
+          }
           product<W>(acc[0][j], w[0], w[1], x);
           product<W>(acc[1][j], w[2], w[3], x);
         }
@@ -466,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lor
         for (int h = 0; h < 2; ++h) {
           if (at[j][h] < 0 || o >= od) continue;
           const float4 v = make_float4(y[j][h].x + acc[0][j][h], y[j][h].y + acc[0][j][h + 2], y[j][h].z + acc[1][j][h], y[j][h].w + acc[1][j][h + 2]);
-          float *to = t.out + static_cast<int64_t>(at[j][h]) * t.out_row + o;
+          float *to = t.out + at[j][h] * t.out_row + o;
           if (a.wide) {
             *reinterpret_cast<float4 *>(to) = v;
           } else {
@@ -519,7 +654,8 @@ cudaError_t launch_lora_plan(LoraPlanArgs a, cudaStream_t s) {
   a.tile = tile_of(a.ntok, a.nreq, a.nadapters);
   a.slots = 1;
   while (a.slots < a.nreq) a.slots *= 2;
-  const size_t smem = 3 * static_cast<size_t>(a.slots) * 4;
+  a.few = a.slots <= kPlanThreads;  // (up to 1024 keys are compared with all: 256 reads; sorting them takes 55 steps with barriers)
+  const size_t smem = ((a.few ? 5 : 4) * static_cast<size_t>(a.slots) + 2) * 4;
   if (smem > 32 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;

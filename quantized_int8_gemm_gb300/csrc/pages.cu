@@ -60,24 +60,29 @@ __device__ __forceinline__ int block_exclusive(int x, int &total, int *sm) {
   return (warp > 0 ? up : 0) + s - x;
 }
 
-// A CTA's share of table rows: `count` of them, the first `first`, `step`
-// apart.  Few rows take several warps each.  f(row's index in the share, j,
-// id), for the entries of this lane, ids loaded four at a time; load(index, j)
-// gives -1 behind a row's pages.
-template <class L, class F>
-__device__ __forceinline__ void for_entries(int count, int width, L &&load, F &&f) {
+// A CTA's share of table rows, few of which take several warps each: f(row's
+// index in the share, j, entry j) for this lane's j < limit(row), entries loaded
+// eight at a time, and fill(row, j) from there to the width.
+template <class N, class L, class F, class E>
+__device__ __forceinline__ void for_entries(int count, int width, N &&limit, L &&load, F &&f, E &&fill) {
+  constexpr int kBatch = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int share = count > 0 && count < kWarps ? kWarps / count : 1, rows = kWarps / share;
   if (warp >= rows * share) return;
+  const int step = share * 32;
   for (int r = warp / share; r < count; r += rows) {
-    for (int j0 = (warp % share) * 32 + lane; j0 < width; j0 += share * 128) {
-      int id[4];
+    const int n = limit(r);
+    int j0 = (warp % share) * 32 + lane;
+    for (; j0 < n; j0 += kBatch * step) {
+      int id[kBatch];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) id[u] = j0 + u * share * 32 < width ? load(r, j0 + u * share * 32) : -1;
+      for (int u = 0; u < kBatch; ++u)
+        if (j0 + u * step < n) id[u] = load(r, j0 + u * step);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (j0 + u * share * 32 < width) f(r, j0 + u * share * 32, id[u]);
+      for (int u = 0; u < kBatch; ++u)
+        if (j0 + u * step < n) f(r, j0 + u * step, id[u]);
     }
+    for (int j = n + (warp % share) * 32 + lane; j < width; j += step) fill(r, j);
   }
 }
 
@@ -120,7 +125,7 @@ __device__ __forceinline__ void tell_all(int *array, int rank, int v) {
 // written once (2 MB for 700 rows of 9000 tokens in pages of 16), between them
 // are six joins of the cluster.
 template <int kCtas>
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) fork_kernel(const __grid_constant__ ForkArgs a) {
+__global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ ForkArgs a) {
   extern __shared__ uint32_t bits[];
   __shared__ int s_parent[kThreads], s_full[kThreads], s_need[kThreads], s_target[kThreads], s_warp[kWarps];
   __shared__ int s_copies[kCtas], s_free[kCtas];
@@ -156,15 +161,14 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) fork_k
   sync_all<kCtas>();
   if (w >= 0) atomicMin(&a.free_pages[w], b);
   for_entries(
-      mine, width, [&](int r, int j) { return j < s_full[r] ? a.table[s_parent[r] * a.table_stride + j] : -1; },
+      mine, width, [&](int r) { return s_full[r]; }, [&](int r, int j) { return a.table[s_parent[r] * a.table_stride + j]; },
       [&](int r, int j, int id) {
-        if (j < s_full[r]) {
-          if (id >= 0 && id < npages) set_bit(own, id);
-          else record_index(a.status), id = -1;
-        } else if (j < s_need[r]) {
-          return;  // the writable page: its row's thread writes it
-        }
+        if (id >= 0 && id < npages) set_bit(own, id);
+        else record_index(a.status), id = -1;
         a.new_table[(b0 + r) * a.new_stride + j] = id;
+      },
+      [&](int r, int j) {  // (the writable page: its row's thread writes it)
+        if (j >= s_need[r]) a.new_table[(b0 + r) * a.new_stride + j] = -1;
       });
   sync_all<kCtas>();
   const int w0 = min(rank * n.slice, n.words), words = min(n.slice, n.words - w0);
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) fork_k
 // after them.  Latency bound: the entries are read twice (the second time from
 // L2) and written once.
 template <int kCtas>
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) compact_kernel(const __grid_constant__ CompactArgs a) {
+__global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ CompactArgs a) {
   extern __shared__ uint32_t bits[];
   __shared__ int s_warp[kWarps], s_held[kCtas], s_below;
   const Bits n(a.npages, kCtas);
@@ -263,14 +267,16 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) compac
   griddep_launch_dependents();
   __syncthreads();
   const int mine = rank < nreq ? (nreq - rank + kCtas - 1) / kCtas : 0;  // rows rank, rank + kCtas, ...
-  auto load = [&](int r, int j) {
-    const int64_t row = rank + static_cast<int64_t>(r) * kCtas;
-    return j < a.held[row] ? a.table[row * a.table_stride + j] : -1;
-  };
-  for_entries(mine, width, load, [&](int r, int j, int id) {
-    if (id >= 0 && id < npages) set_bit(own, id);
-    else if (j < a.held[rank + static_cast<int64_t>(r) * kCtas]) record_index(a.status);
-  });
+  auto row_of = [&](int r) { return rank + static_cast<int64_t>(r) * kCtas; };
+  auto limit = [&](int r) { return min(max(a.held[row_of(r)], 0), width); };
+  auto load = [&](int r, int j) { return a.table[row_of(r) * a.table_stride + j]; };
+  for_entries(
+      mine, width, limit, load,
+      [&](int, int, int id) {
+        if (id >= 0 && id < npages) set_bit(own, id);
+        else record_index(a.status);
+      },
+      [&](int r, int j) { a.new_table[row_of(r) * a.new_stride + j] = -1; });
   sync_all<kCtas>();
   for (int i = tid; i < n.slice; i += kThreads) held[i] = joined<kCtas>(own, rank * n.slice + i);
   __syncthreads();
@@ -322,11 +328,14 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) compac
   for (int i = moves + rank * kThreads + tid; i < room; i += kCtas * kThreads) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
   if (rank == 0 && tid == 0) a.counts[0] = total, a.counts[1] = moves;
   sync_all<kCtas>();
-  for_entries(mine, width, load, [&](int r, int j, int id) {
-    if (id < 0 || id >= npages) id = -1;
-    else if (id >= total) id = __ldcg(&a.pairs[2 * (held_before(id) - below) + 1]);
-    a.new_table[(rank + static_cast<int64_t>(r) * kCtas) * a.new_stride + j] = id;
-  });
+  for_entries(
+      mine, 0, limit, load,
+      [&](int r, int j, int id) {
+        if (id < 0 || id >= npages) id = -1;
+        else if (id >= total) id = __ldcg(&a.pairs[2 * (held_before(id) - below) + 1]);
+        a.new_table[row_of(r) * a.new_stride + j] = id;
+      },
+      [&](int, int) {});
 }
 
 // ---------------------------------------------------------------- copies
@@ -369,14 +378,17 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     if (dst[u]) *dst[u] = x[u];
 }
 
-template <class K>
-cudaError_t allow(K kernel, size_t smem) {
-  if (smem <= 24 * 1024) return cudaSuccess;  // (beside the static arrays, within the 48 KB that need no leave)
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+template <class K, class A>
+cudaError_t launch_cluster(K kernel, unsigned ctas, size_t smem, cudaStream_t s, const A &a) {
+  cudaError_t e = cudaSuccess;
+  if (ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && smem > 24 * 1024)  // (beside the static arrays, within the 48 KB that need no leave)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  return e != cudaSuccess ? e : launch_early(kernel, Cluster{ctas}, ctas, 1, kThreads, smem, s, a);
 }
 
-// One CTA or a cluster of eight.
-constexpr int kMany = 8;
+// One CTA or a cluster of sixteen.
+constexpr int kMany = 16;
 bool one_cta(int64_t rows, int64_t width, int64_t npages) {
   return rows <= kThreads && rows * width <= 8192 && npages <= 32768;
 }
@@ -385,8 +397,7 @@ template <int kCtas>
 cudaError_t launch_fork_with(const ForkArgs &a, cudaStream_t s) {
   const Bits n(a.npages, kCtas);
   const size_t smem = sizeof(uint32_t) * (n.words + 2 * static_cast<size_t>(n.slice));
-  const cudaError_t e = allow(fork_kernel<kCtas>, smem);
-  return e != cudaSuccess ? e : launch_early(fork_kernel<kCtas>, kCtas, 1, kThreads, smem, s, a);
+  return launch_cluster(fork_kernel<kCtas>, kCtas, smem, s, a);
 }
 
 template <int kCtas>
@@ -394,8 +405,7 @@ cudaError_t launch_compact_with(const CompactArgs &a, cudaStream_t s) {
   const Bits n(a.npages, kCtas);
   const size_t groups = n.slice / kGroup;
   const size_t smem = sizeof(uint32_t) * ((kCtas + 1) * static_cast<size_t>(n.slice) + (kCtas + 1) * groups);
-  const cudaError_t e = allow(compact_kernel<kCtas>, smem);
-  return e != cudaSuccess ? e : launch_early(compact_kernel<kCtas>, kCtas, 1, kThreads, smem, s, a);
+  return launch_cluster(compact_kernel<kCtas>, kCtas, smem, s, a);
 }
 
 }  // namespace

@@ -143,10 +143,10 @@ int mmq_token_probs(const mmq_token_rules *args, mmq_stream_t stream) {
   a.t = t;
   if (!t.tokens) a.t.tokens_width = 0;
   if (t.nbias == 0) a.t.bias_start = nullptr;
+  a.in_place = same;
   a.penalties = (a.t.tokens_width > 0 || (t.draft && t.rows > 1)) && (t.repetition || t.frequency || t.presence);
-  a.many = a.t.tokens_width + t.rows > 0x7fff;
   a.status = &ctx.words->status, a.abort_epoch = &ctx.words->abort_epoch, a.epoch = ctx.epoch, a.limit_ns = ctx.limit_ns;
-  return cuda_rc(mmq::launch_token_probs(a, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_rc(mmq::launch_token_probs(a, ctx, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int64_t mmq_lora_plan_words(int64_t ntok, int64_t nreq, int64_t nadapters) {

@@ -1,14 +1,14 @@
-// rules.cu -- logits under each request's rules, and their probabilities.
-//
-// A row: penalties by the counts of the request's tokens, sparse biases, a
-// grammar's bits, then softmax(x / T).  A cluster of eight CTAs takes a row,
-// each an eighth of the vocabulary in shared memory, so the logits are read
-// once and the probabilities written once.
+// rules.cu -- logits under each request's rules, and their probabilities: penalties
+// by the counts of the request's tokens, sparse biases, a grammar's bits, then
+// softmax(x / T).  The softmax keeps a running maximum and sum (Milakov and
+// Gimelshein, "Online normalizer calculation for softmax", 2018).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <cstdlib>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -16,16 +16,21 @@
 namespace mmq {
 namespace {
 
-constexpr int kCtas = 8, kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMostCtas = 16, kThreads = 256, kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
-constexpr uint32_t kMet = 0x8000, kTimes = 0x7fff;  // a token's 16 bits: among the prompt's; times behind it
+// Of a listed token's count: it is among the prompt's; it has a bias.
+constexpr uint32_t kMet = 0x80000000u, kBiased = 0x40000000u;
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint64_t v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+// 8 bytes into another CTA's shared memory, counted by a barrier beside them
+// (both addresses from mapa_shared): no fence, as a store and a cluster barrier
+// would need, and so no wait for this thread's other stores.
+__device__ __forceinline__ void send(uint32_t addr, uint64_t v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u64 [%0], %1, [%2];" ::"r"(addr), "l"(v), "r"(bar) : "memory");
 }
+// (Results below 2^-126 become 0: the instruction that keeps them is four.)
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
@@ -36,58 +41,24 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ float2 unpack2(uint32_t w, __half) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
-__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
+__device__ __forceinline__ void store_low(float *p) { *p = -INFINITY; }
+__device__ __forceinline__ void store_low(__half *p) { *p = __ushort_as_half(0xfc00); }
+__device__ __forceinline__ void store_low(__nv_bfloat16 *p) { *p = __ushort_as_bfloat16(0xff80); }
+__device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// Elements [0, len) of a row's slice from x[m] on; `m` is the slice's place in
-// 16 bytes of memory, so that whole 16-byte pieces lie on 16 bytes here too.
-__device__ __forceinline__ void load_slice(const float *p, float *x, int m, int len, uint32_t bar) {
-  const int head = min((4 - m) & 3, len), body = (len - head) >> 2, tail = head + 4 * body;
-  if (threadIdx.x == 0) {
-    mbar_arrive_expect_tx(bar, body * 16);
-    if (body)
-      asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(x + m + head)),
-                   "l"(p + head), "r"(body * 16), "r"(bar)
-                   : "memory");
-  }
-  const int t = static_cast<int>(threadIdx.x);
-  if (t < head) x[m + t] = p[t];
-  else if (t >= 4 && t - 4 < len - tail) x[m + tail + t - 4] = p[tail + t - 4];
+// Four elements that begin on their own alignment.
+__device__ __forceinline__ float4 load4(const __half *p) {
+  const uint2 r = *reinterpret_cast<const uint2 *>(p);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&r.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&r.y));
+  return make_float4(a.x, a.y, b.x, b.y);
 }
-template <class T>
-__device__ __forceinline__ void load_slice(const T *p, float *x, int m, int len, uint32_t) {
-  const int head = min((8 - m) & 7, len), body = (len - head) >> 3, tail = head + 8 * body;
-  const uint4 *src = reinterpret_cast<const uint4 *>(p + head);
-  float4 *dst = reinterpret_cast<float4 *>(x + m + head);
-  for (int i0 = threadIdx.x; i0 < body; i0 += 4 * kThreads) {
-    uint4 r[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (i0 + u * kThreads < body) r[u] = __ldcs(src + i0 + u * kThreads);
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (i0 + u * kThreads < body) {
-        const float2 a = unpack2(r[u].x, T()), b = unpack2(r[u].y, T()), c = unpack2(r[u].z, T()), d = unpack2(r[u].w, T());
-        dst[2 * (i0 + u * kThreads)] = make_float4(a.x, a.y, b.x, b.y);
-        dst[2 * (i0 + u * kThreads) + 1] = make_float4(c.x, c.y, d.x, d.y);
-      }
-  }
-  const int t = static_cast<int>(threadIdx.x);
-  if (t < head) x[m + t] = to_f32(p[t]);
-  else if (t >= 8 && t - 8 < len - tail) x[m + tail + t - 8] = to_f32(p[tail + t - 8]);
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+  const uint2 r = *reinterpret_cast<const uint2 *>(p);
+  return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
 }
-
-// One element, or four that begin on their own alignment, rounded once.
-__device__ __forceinline__ void put(void *p, int type, int64_t at, float v) {
-  if (type == MMQ_DT_F32) __stcs(static_cast<float *>(p) + at, v);
-  else if (type == MMQ_DT_F16) static_cast<__half *>(p)[at] = __float2half_rn(v);
-  else static_cast<__nv_bfloat16 *>(p)[at] = __float2bfloat16_rn(v);
-}
-__device__ __forceinline__ void put4(void *p, int type, int64_t at, float4 v) {
+__device__ __forceinline__ void put4(void *p, int type, int64_t at, const float4 &v) {
   if (type == MMQ_DT_F32) {
     __stcs(reinterpret_cast<float4 *>(static_cast<float *>(p) + at), v);
     return;
@@ -97,27 +68,83 @@ __device__ __forceinline__ void put4(void *p, int type, int64_t at, float4 v) {
   else r = make_uint2(pack2(v.x, v.y, __nv_bfloat16()), pack2(v.z, v.w, __nv_bfloat16()));
   __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + at), r);
 }
-// Elements of a slice (x[m], ...) to out[at], ...; f gives what is written for
-// element e.  Four at a time where their places in memory and here agree.
-template <class F>
-__device__ __forceinline__ void write_slice(void *out, int type, int64_t at, int m, int len, F &&f) {
-  const uint32_t bytes = type == MMQ_DT_F32 ? 4 : 2;
-  const int place = static_cast<int>((reinterpret_cast<uintptr_t>(out) / bytes + at) & 3);
-  const int t = static_cast<int>(threadIdx.x);
-  if (place == (m & 3)) {
-    const int head = min((4 - place) & 3, len), body = (len - head) >> 2, tail = head + 4 * body;
-    for (int i = t; i < body; i += kThreads) {
-      const int e = head + 4 * i;
-      put4(out, type, at + e, make_float4(f(e), f(e + 1), f(e + 2), f(e + 3)));
-    }
-    if (t < head) put(out, type, at + t, f(t));
-    else if (t >= 4 && t - 4 < len - tail) put(out, type, at + tail + t - 4, f(tail + t - 4));
-    return;
-  }
-#pragma unroll 4
-  for (int e = t; e < len; e += kThreads) put(out, type, at + e, f(e));
-}
 
+// A CTA's slice of a row on its way to shared memory: whole pieces of 16 bytes by
+// bulk copies, the elements in front of and behind them by threads.  Element e
+// comes to stage[place + e], place being that of the slice in 16 bytes of memory.
+constexpr int kChunks = 5;  // copies of a slice, which are waited for one by one
+template <class T>
+struct Slice {
+  static constexpr int kPiece = 16 / sizeof(T);
+  const T *src;
+  int place, head, body, len, fours, each;  // elements; fours of them, of a chunk
+  __device__ __forceinline__ Slice(const T *p, int n) : src(p), len(n) {
+    place = static_cast<int>(reinterpret_cast<uintptr_t>(p) / sizeof(T) & (kPiece - 1));
+    head = min((kPiece - place) & (kPiece - 1), n);
+    body = (n - head) / kPiece * kPiece;
+    fours = ((place & 3) + n + 3) >> 2;
+    each = (fours + kChunks - 1) / kChunks;
+  }
+  // Where chunk k begins in the stage: a piece's begin not before its first four.
+  __device__ __forceinline__ int chunk(int k) const {
+    const int first = 4 * k * each + (place & ~3), at = k == 0 ? 0 : (first + kPiece - 1) & ~(kPiece - 1);
+    return min(max(at, place + head), place + head + body);
+  }
+  __device__ __forceinline__ void copy(T *stage, const uint64_t *bars) const {  // (one thread)
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const int from = chunk(k), to = k + 1 < kChunks ? chunk(k + 1) : place + head + body;
+      const uint32_t bytes = (to - from) * static_cast<uint32_t>(sizeof(T)), bar = smem_addr(bars + k);
+      mbar_arrive_expect_tx(bar, bytes);
+      if (bytes)
+        asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(stage + from)),
+                     "l"(src + (from - place)), "r"(bytes), "r"(bar)
+                     : "memory");
+    }
+  }
+  // The element that thread k (of 2 kPiece) brings, -1: none.
+  __device__ __forceinline__ int edge(int k) const {
+    if (k < kPiece) return k < head ? k : -1;
+    return k < 2 * kPiece && head + body + k - kPiece < len ? head + body + k - kPiece : -1;
+  }
+};
+__device__ __forceinline__ void put(void *out, int type, int64_t at, float v) {
+  if (type == MMQ_DT_F32) {
+    static_cast<float *>(out)[at] = v;
+  } else {
+    const uint16_t half = __half_as_ushort(__float2half_rn(v)), brain = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    static_cast<uint16_t *>(out)[at] = type == MMQ_DT_F16 ? half : brain;
+  }
+}
+// A slice of a row that is written, each element rounded once.
+struct Out {
+  void *p;
+  int64_t at;  // the slice's first element
+  int type;
+  bool fits;  // its fours lie in memory as the logits' do
+  __device__ __forceinline__ Out(void *out, int t, int64_t first, int m) : p(out), at(first), type(t) {
+    fits = static_cast<int>((reinterpret_cast<uintptr_t>(out) / (t == MMQ_DT_F32 ? 4 : 2) + first) & 3) == m;
+  }
+  __device__ __forceinline__ void four(int e, int len, const float4 &v) const {
+    if (fits && e >= 0 && e + 4 <= len) {
+      put4(p, type, at + e, v);
+      return;
+    }
+    const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (e + u >= 0 && e + u < len) put(p, type, at + e + u, x[u]);
+  }
+};
+
+__device__ __forceinline__ uint64_t warp_max(uint64_t x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    const uint64_t y = __shfl_xor_sync(kAll, x, d);
+    x = y > x ? y : x;
+  }
+  return x;
+}
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
@@ -128,272 +155,520 @@ __device__ __forceinline__ float warp_sum(float x) {
   for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
   return x;
 }
-__device__ __forceinline__ uint64_t warp_max(uint64_t x) {
+
+// The largest number so far and the sum of 2^((x - largest) scale); without a
+// number above -inf the sum is 0, or NaN.
+struct Part {
+  float top = -INFINITY, sum = 0.0f;
+  __device__ __forceinline__ float from() const { return top == -INFINITY ? 0.0f : top; }
+  __device__ __forceinline__ void raise(float to, float scale) {
+    if (to > top) {
+      sum *= exp2_approx((top - to) * scale);
+      top = to;
+    }
+  }
+  __device__ __forceinline__ void add(float x, float scale) { sum += exp2_approx((x - from()) * scale); }
+};
+// Joined over a warp's lanes, in each of them.
+__device__ __forceinline__ Part joined(Part p, float scale) {
+  Part all;
+  all.top = warp_max(p.top);
+  all.sum = warp_sum(p.sum * exp2_approx((p.top - all.from()) * scale));
+  return all;
+}
+__device__ __forceinline__ uint64_t as_word(Part p) { return static_cast<uint64_t>(__float_as_uint(p.top)) << 32 | __float_as_uint(p.sum); }
+__device__ __forceinline__ Part as_part(uint64_t w) {
+  Part p;
+  p.top = __uint_as_float(static_cast<uint32_t>(w >> 32)), p.sum = __uint_as_float(static_cast<uint32_t>(w));
+  return p;
+}
+// The better of two candidates for the largest logit is the larger number: the
+// logit's bits in ascending order above, the complement of the index below; all
+// ones for NaN, 0 for none.
+__device__ __forceinline__ uint64_t candidate(float x, int v) {
+  const uint32_t w = __float_as_uint(x + 0.0f);  // (-0 as 0)
+  if (x != x) return ~uint64_t(0);
+  if (x == -INFINITY) return 0;
+  return static_cast<uint64_t>(w >> 31 ? ~w : w | 0x80000000u) << 32 | (kAll - static_cast<uint32_t>(v));
+}
+
+// ---------------------------------------------------------------- the request's tokens and biases
+constexpr int kListThreads = 1024;
+constexpr int kEntries = 4096;           // listed tokens that are worked out at once
+constexpr int kStarts = kMostCtas + 2;   // numbers for a request: where each CTA's part of its list begins, the first bias
+
+// Sum of x over the threads before this one, and over all.
+__device__ __forceinline__ int block_exclusive(int x, int &total, int *sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = x;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    const uint64_t y = __shfl_xor_sync(kAll, x, d);
-    x = y > x ? y : x;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(kAll, s, d);
+    if (lane >= d) s += y;
   }
-  return x;
+  if (lane == 31) sm[warp] = s;
+  __syncthreads();
+  int all = sm[lane];  // (32 warps)
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(kAll, all, d);
+    if (lane >= d) all += y;
+  }
+  total = __shfl_sync(kAll, all, 31);
+  const int before = __shfl_sync(kAll, all, warp > 0 ? warp - 1 : 0);
+  __syncthreads();
+  return (warp > 0 ? before : 0) + s - x;
 }
 
-// Counts a token of the slice: `answered` ones up to kTimes, the prompt's once.
-__device__ __forceinline__ void count(uint32_t *counts, int at, bool answered, bool many) {
-  uint32_t *w = counts + (at >> 1);
-  const int shift = (at & 1) * 16;
-  if (!answered) {
-    atomicOr(w, kMet << shift);
-  } else if (!many) {
-    atomicAdd(w, 1u << shift);
-  } else {  // more tokens than kTimes: one of them could go over
-    uint32_t old = *w, was;
-    do {
-      was = old;
-      if ((was >> shift & kTimes) == kTimes) return;
-      old = atomicCAS(w, was, was + (1u << shift));
-    } while (old != was);
-  }
-}
-
-// HBM bound with many rows (the row in, the row out), latency bound with few.
-template <class T>
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) token_probs_kernel(const __grid_constant__ RulesArgs a) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ __align__(8) uint64_t s_bar;
-  __shared__ float s_max[kWarps], s_sum[kWarps];
-  __shared__ uint64_t s_key[kWarps], s_all[kCtas];
-  __shared__ int s_bias_id[kThreads];
-  __shared__ float s_bias[kThreads];
+// Lists a request's distinct tokens (drafted ones and those with a bias among
+// them), ascending, with the times they count before any drafted one and the sums of their
+// biases; sets a bit for each.  A CTA a request: the bits in shared memory
+// give every token its place in the list (sums of population counts), so
+// the list does not depend on the order that the threads came in.  Latency
+// bound: a round of reads, two passes over the tokens.  Every row of the
+// request goes by this list; counting in each CTA of each row took longer
+// than the rows themselves (160 requests of 6 rows of 100277: 327 us).
+__global__ void __launch_bounds__(kListThreads) token_list_kernel(const __grid_constant__ RulesArgs a) {
+  extern __shared__ __align__(16) uint32_t bits[];  // a bit for each token; listed ones before each word; counts, biases, tokens of a round
+  __shared__ int s_sums[32], s_first;
+  __shared__ bool s_twice;
   const mmq_token_rules &t = a.t;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = cluster_ctarank();
-  const int row = static_cast<int>(blockIdx.x / kCtas), b = a.by_rows(row), i = row - b * t.rows;
-  float *x = reinterpret_cast<float *>(smem);                        // a.slice + 8
-  uint32_t *counts = reinterpret_cast<uint32_t *>(x + a.slice + 8);  // 16 bits an element, if there are penalties
-  uint32_t *allowed = counts + (a.penalties ? a.slice / 2 + 4 : 0);  // a bit an element, one word in front
-  if (tid == 0) {
-    mbar_init(smem_addr(&s_bar), 1);
-    fence_mbar_init();
-  }
-  const int s0 = static_cast<int>(rank) * a.slice, vocab = static_cast<int>(t.vocab), len = max(min(a.slice, vocab - s0), 0);
-  if (a.penalties)
-    for (int e = tid; e < a.slice / 8 + 1; e += kThreads) reinterpret_cast<uint4 *>(counts)[e] = make_uint4(0, 0, 0, 0);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x, vocab = static_cast<int>(t.vocab);
+  const int words = (vocab + 31) / 32;
+  int *before = reinterpret_cast<int *>(bits + words), *list = before + words;
+  uint32_t *counts = reinterpret_cast<uint32_t *>(list + kEntries);
+  float *biases = reinterpret_cast<float *>(counts + kEntries);
+  for (int w = tid; w < words; w += kListThreads) bits[w] = 0;
+  if (tid == 0) s_twice = false, s_first = 0;
   griddep_wait();
   griddep_launch_dependents();
-  if (t.n_draft) {
-    const int n = t.n_draft[b];
-    if (tid == 0 && rank == 0 && i == 0 && (n < 0 || n >= t.rows)) record_index(a.status);
-    if (i > max(n, 0)) return;  // (the whole cluster)
-  }
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  const int width = static_cast<int>(t.tokens_width), drafted = t.draft ? t.rows - 1 : 0, nbias = static_cast<int>(t.nbias);
+  const int said = !a.penalties ? 0 : t.token_lens ? t.token_lens[b] : width, prompt = t.prompt_lens ? t.prompt_lens[b] : 0;
+  const int n = max(min(said, width), 0);
+  const int32_t *ids = t.tokens + b * t.tokens_stride, *draft = t.draft + b * t.draft_stride;
   __syncthreads();
-  constexpr int kPiece = 16 / sizeof(T);
-  const T *src = static_cast<const T *>(t.logits) + b * t.logits_req + i * t.logits_row + s0;
-  const int m = static_cast<int>(reinterpret_cast<uintptr_t>(src) / sizeof(T) & (kPiece - 1));
-  load_slice(src, x, m, len, smem_addr(&s_bar));
-  if (a.penalties) {
-    const int32_t *ids = t.tokens + b * t.tokens_stride;
-    int n = static_cast<int>(t.tokens_width);
-    if (t.token_lens) {
-      const int said = t.token_lens[b];
-      if (tid == 0 && rank == 0 && i == 0 && said > n) record_index(a.status);
-      n = max(min(said, n), 0);
-    }
-    const int prompt = t.prompt_lens ? t.prompt_lens[b] : 0;
-    auto meet = [&](int v, bool answered) {
-      const int at = v - s0;
-      if (at >= 0 && at < len) count(counts, m + at, answered, a.many);
-      else if (rank == 0 && (v < 0 || v >= vocab)) record_index(a.status);
-    };
-    for (int j0 = tid; j0 < n; j0 += 4 * kThreads) {
-      int v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (j0 + u * kThreads < n) v[u] = ids[j0 + u * kThreads];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (j0 + u * kThreads < n) meet(v[u], j0 + u * kThreads >= prompt);
-    }
-    if (t.draft)
-      for (int j = tid; j < i; j += kThreads) meet(t.draft[b * t.draft_stride + j], true);
-  }
-  bool masked = false;
-  if (t.mask) {
-    const int64_t which = t.mask_rows ? t.mask_rows[row] : row;
-    masked = which >= 0 && which < t.nmasks;
-    if (tid == 0 && rank == 0 && !masked && which != -1) record_index(a.status);
-    if (masked) {
-      const int32_t *bits = t.mask + which * t.mask_stride + (s0 >> 5);
-      const int words = (len + 31) >> 5;
-      for (int w = tid; w < words; w += kThreads) allowed[1 + w] = static_cast<uint32_t>(bits[w]);
-      if (tid == 0) allowed[0] = allowed[1 + words] = 0;
-    }
-  }
-  const float rho = t.repetition ? t.repetition[b] : 1.0f, alpha = t.frequency ? t.frequency[b] : 0.0f;
-  const float beta = t.presence ? t.presence[b] : 0.0f, temperature = t.temperature ? t.temperature[b] : 1.0f;
-  const bool greedy = !(temperature > 0.0f);
   int bias0 = 0, bias1 = 0;
   if (t.bias_start) {
-    bias0 = t.bias_start[b], bias1 = t.bias_start[b + 1];
-    const int most = static_cast<int>(t.nbias);
-    if (tid == 0 && rank == 0 && i == 0 && (bias0 < 0 || bias1 < bias0 || bias1 > most)) record_index(a.status);
-    bias0 = max(bias0, 0), bias1 = min(bias1, most);
+    // (begins that descend are raised, so that no two requests' lists overlap)
+    const int begin = t.bias_start[b], end = t.bias_start[b + 1];
+    for (int j = tid; j <= b; j += kListThreads) {
+      const int x = min(t.bias_start[j], nbias);
+      if (x > 0) atomicMax(&s_first, x);
+    }
+    if (tid == 0 && (begin < 0 || end < begin || end > nbias)) record_index(a.status);
+    __syncthreads();
+    bias0 = s_first, bias1 = max(bias0, min(end, nbias));
+  }
+  if (tid == 0 && said > width) record_index(a.status);
+  constexpr int kKept = 4;
+  int kept[kKept], bias_id = 0;
+  float bias_value = 0.0f;
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int u = 0; u < kKept; ++u)
+      if (j0 + u * kListThreads < n) kept[u] = ids[j0 + u * kListThreads];
+  };
+  load(tid);
+  if (bias0 + tid < bias1) bias_id = t.bias_ids[bias0 + tid], bias_value = t.bias_values[bias0 + tid];
+  auto known = [&](int id) { return id >= 0 && id < vocab; };
+  auto set = [&](int id) {
+    if (known(id)) atomicOr(&bits[id >> 5], 1u << (id & 31));
+    else record_index(a.status);
+  };
+  for (int j0 = tid; j0 < n; j0 += kKept * kListThreads) {
+    if (j0 != tid) load(j0);
+#pragma unroll
+    for (int u = 0; u < kKept; ++u)
+      if (j0 + u * kListThreads < n) set(kept[u]);
+  }
+  const int last = min(drafted, t.n_draft ? max(t.n_draft[b], 0) : drafted);
+  if (a.penalties)  // (all of them, so that a row does not depend on the rows behind it)
+    for (int j = tid; j < drafted; j += kListThreads)
+      if (j < last || known(draft[j])) set(draft[j]);
+  for (int j = bias0 + tid; j < bias1; j += kListThreads) set(j < bias0 + kListThreads ? bias_id : t.bias_ids[j]);
+  __syncthreads();
+  const int per = (words + kListThreads - 1) / kListThreads, w0 = min(tid * per, words), w1 = min(w0 + per, words);
+  int mine = 0, listed;
+  for (int w = w0; w < w1; ++w) mine += __popc(bits[w]);
+  int at = block_exclusive(mine, listed, s_sums);
+  for (int w = w0; w < w1; ++w) {
+    before[w] = at;
+    at += __popc(bits[w]);
   }
   __syncthreads();
-  if constexpr (sizeof(T) == 4) {
-    const WaitCtl wait = {a.status, a.abort_epoch, a.epoch, a.limit_ns};
-    mbar_wait(smem_addr(&s_bar), 0, wait, false);
+  const int all_words = a.slice / 32 << a.ctas_log2;
+  for (int w = tid; w < all_words; w += kListThreads) a.touched[static_cast<int64_t>(b) * all_words + w] = w < words ? bits[w] : 0;
+  if (tid <= 1 << a.ctas_log2) {
+    const int w = tid * (a.slice / 32);
+    a.starts[b * kStarts + tid] = w < words ? before[w] : listed;
   }
-  // elements of x in fours; place q holds those of x[4 q], ..., of which
-  // elements [0, len) are this slice's
-  const int last = (m + len + 3) >> 2;
-  auto penalized = [&](float v, uint32_t c) {
-    if (c) {
-      v = v > 0.0f ? __fdiv_rn(v, rho) : __fmul_rn(v, rho);
-      const uint32_t times = c & kTimes;
-      if (times) v = __fsub_rn(__fsub_rn(v, __fmul_rn(alpha, static_cast<float>(times))), beta);
-    }
-    return v;
-  };
-  auto penalties = [&](int q, float4 &v) {
-    const uint2 c = reinterpret_cast<const uint2 *>(counts)[q];
-    if (c.x | c.y) {
-      v.x = penalized(v.x, c.x & 0xffff), v.y = penalized(v.y, c.x >> 16);
-      v.z = penalized(v.z, c.y & 0xffff), v.w = penalized(v.w, c.y >> 16);
-    }
-  };
-  if (bias1 > bias0) {
-    if (a.penalties) {
-      for (int q = tid; q < last; q += kThreads) {
-        float4 v = reinterpret_cast<float4 *>(x)[q];
-        penalties(q, v);
-        reinterpret_cast<float4 *>(x)[q] = v;
+  if (tid == 0) a.starts[b * kStarts + kMostCtas + 1] = bias0;
+  const int64_t base = static_cast<int64_t>(b) * (width + drafted) + bias0;
+  for (int e0 = 0; e0 < listed; e0 += kEntries) {
+    const int here = min(kEntries, listed - e0);
+    for (int k = tid; k < here; k += kListThreads) counts[k] = 0, biases[k] = 0.0f;
+    __syncthreads();
+    auto place = [&](int id) {  // in the round, or -1
+      if (!known(id)) return -1;
+      const int k = before[id >> 5] + __popc(bits[id >> 5] & ((1u << (id & 31)) - 1)) - e0;
+      return k < here ? k : -1;
+    };
+    for (int j0 = tid; j0 < n; j0 += kKept * kListThreads) {
+      if (n > kKept * kListThreads) load(j0);
+#pragma unroll
+      for (int u = 0; u < kKept; ++u) {
+        const int j = j0 + u * kListThreads, k = j < n ? place(kept[u]) : -1;
+        if (k < 0) continue;
+        list[k] = kept[u];
+        if (j >= prompt) atomicAdd(&counts[k], 1u);
+        else atomicOr(&counts[k], kMet);
       }
     }
-    for (int j0 = bias0; j0 < bias1; j0 += kThreads) {
-      const int n = min(kThreads, bias1 - j0);
-      if (tid < n) s_bias_id[tid] = t.bias_ids[j0 + tid], s_bias[tid] = t.bias_values[j0 + tid];
+    if (a.penalties)
+      for (int j = tid; j < drafted; j += kListThreads)
+        if (const int k = place(draft[j]); k >= 0) list[k] = draft[j];
+    for (int j = bias0 + tid; j < bias1; j += kListThreads) {
+      const bool again = j >= bias0 + kListThreads;
+      const int id = again ? t.bias_ids[j] : bias_id, k = place(id);
+      if (k < 0) continue;
+      list[k] = id;
+      if (atomicOr(&counts[k], kBiased) & kBiased) s_twice = true;
+      else biases[k] = again ? t.bias_values[j] : bias_value;
+    }
+    __syncthreads();
+    if (s_twice) {  // a token twice: one warp adds up, in the list's order
+      for (int k = tid; k < here; k += kListThreads) biases[k] = 0.0f;
       __syncthreads();
       if (warp == 0) {
-        for (int k = 0; k < n; k += 32) {
-          const int v = k + lane < n ? s_bias_id[k + lane] : s0, at = v - s0;
-          if (rank == 0 && (v < 0 || v >= vocab)) record_index(a.status);
-          const bool here = k + lane < n && at >= 0 && at < len;
-          // the same token twice: in the list's order
-          const unsigned peers = __match_any_sync(kAll, here ? at : -1 - lane);
+        for (int j0 = bias0; j0 < bias1; j0 += 32) {
+          const int j = j0 + lane, k = j < bias1 ? place(t.bias_ids[j]) : -1;
+          const unsigned peers = __match_any_sync(kAll, k >= 0 ? k : -1 - lane);
           const int turn = __popc(peers & ((1u << lane) - 1));
           for (int r = 0; __any_sync(kAll, r <= turn); ++r) {
-            if (here && r == turn) x[m + at] = __fadd_rn(x[m + at], s_bias[k + lane]);
+            if (k >= 0 && r == turn) biases[k] += t.bias_values[j];
             __syncwarp();
           }
         }
       }
       __syncthreads();
     }
+    for (int k = tid; k < here; k += kListThreads) {
+      const int64_t to = base + e0 + k;
+      a.list[to] = list[k], a.counts[to] = counts[k], a.biases[to] = biases[k];
+    }
+    __syncthreads();
   }
-  const bool late = bias1 > bias0 || !a.penalties;  // (no penalties to be applied any more)
-  float top = -INFINITY;
-  bool nan = false;
+}
+
+// ---------------------------------------------------------------- rows
+// A cluster takes a row, each CTA of it a slice, in shared memory.  Elements
+// that are listed (above) or that a mask hides are left out of a stream that
+// all others go by in: as they come, for their exponentials against the largest
+// of the thread's in a chunk, and once the row's sum is known, to be written.
+// The listed ones, few, are worked out one a thread.
+//
+// HBM bound with many rows (the row in, the row out), latency bound with few.
+template <class T>
+__global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_constant__ RulesArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(8) uint64_t s_bars[kChunks], s_told;
+  __shared__ uint64_t s_warp[kWarps], s_all[kMostCtas];
+  __shared__ float s_from[kChunks][kThreads];  // what each thread's exponentials of a chunk are against
+  constexpr bool kWide = sizeof(T) == 4;
+  const mmq_token_rules &t = a.t;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_ctarank()), row = static_cast<int>(blockIdx.x >> a.ctas_log2), b = a.by_rows(row), i = row - b * t.rows;
+  const int words = a.slice / 32;
+  T *stage = reinterpret_cast<T *>(smem);
+  uint32_t *skip = reinterpret_cast<uint32_t *>(stage + a.slice + 16);  // a bit for each element that is left out, one word in front
+  const int s0 = rank * a.slice, vocab = static_cast<int>(t.vocab), len = max(min(a.slice, vocab - s0), 0);
+  const bool first_thread = tid == 0 && rank == 0;
+  const Slice<T> slice(static_cast<const T *>(t.logits) + b * t.logits_req + i * t.logits_row + s0, len);
+  if (tid == 0) {
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) mbar_init(smem_addr(s_bars + k), 1);
+    mbar_init(smem_addr(&s_told), 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(smem_addr(&s_told), 8u << a.ctas_log2);
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  const int drafted = t.n_draft ? t.n_draft[b] : t.rows - 1;
+  if (i > max(drafted, 0)) return;  // (the whole cluster)
+  if (tid == 0) slice.copy(stage, s_bars);
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // (the barriers are there: fence_mbar_init)
+  // everything that one number of the request says, in one round of reads
+  const float rho = t.repetition ? t.repetition[b] : 1.0f, alpha = t.frequency ? t.frequency[b] : 0.0f;
+  const float beta = t.presence ? t.presence[b] : 0.0f, temperature = t.temperature ? t.temperature[b] : 1.0f;
+  const int64_t which = !t.mask ? -1 : t.mask_rows ? t.mask_rows[row] : row;
+  int list0 = 0, list1 = 0;
+  int64_t list_base = 0;
+  if (a.sparse) {
+    const int32_t *starts = a.starts + b * kStarts;
+    list0 = starts[rank], list1 = starts[rank + 1];
+    list_base = static_cast<int64_t>(b) * (t.tokens_width + (t.draft ? t.rows - 1 : 0)) + starts[kMostCtas + 1];
+  }
+  const bool masked = which >= 0 && which < t.nmasks, any_skip = a.sparse || masked;
+  if (first_thread) {
+    if (i == 0 && (drafted < 0 || drafted >= t.rows)) record_index(a.status);
+    if (t.mask && !masked && which != -1) record_index(a.status);
+  }
+  const int32_t *mask = t.mask + which * t.mask_stride + (s0 >> 5);
+  // what is in front of the slice and behind it, in its first and last four
+  const int m = slice.place & 3;
+  if (const int e = slice.edge(tid); e >= 0) stage[slice.place + e] = slice.src[e];
+  if (tid >= 64 && tid < 64 + m) store_low(stage + slice.place - 1 - (tid - 64));
+  if (tid >= 96 && tid < 100) store_low(stage + slice.place + len + (tid - 96));
+  if (any_skip) {
+    const uint32_t *touched = a.touched + (static_cast<int64_t>(b) << a.ctas_log2) * words + rank * words;
+    for (int w = tid; w < words; w += kThreads)
+      skip[1 + w] = (masked && 32 * w < len ? ~static_cast<uint32_t>(mask[w]) : 0) | (a.sparse ? touched[w] : 0);
+    if (tid == 0) skip[0] = skip[words + 1] = 0;
+  }
+  const float scale = fmaxf(fminf(__fdiv_rn(1.44269504088896341f, temperature), FLT_MAX), 0x1p-149f);  // log2(e) / T, not 0 or inf
+  const bool greedy = !(temperature > 0.0f);
+  __syncthreads();
+  // listed element k's adjusted logit
+  auto adjusted_of = [&](int k, int &at) {
+    const int id = a.list[list_base + k];
+    const uint32_t c = a.counts[list_base + k];
+    const float bias = a.biases[list_base + k];
+    at = id - s0;
+    float y = to_f32(slice.src[at]);
+    if (a.penalties) {
+      uint32_t times = c & ~(kMet | kBiased);
+      if (t.draft)
+        for (int j = 0; j < i; ++j) times += t.draft[b * t.draft_stride + j] == id;
+      if (times || (c & kMet)) y = y > 0.0f ? __fdiv_rn(y, rho) : __fmul_rn(y, rho);
+      if (times) y = __fsub_rn(__fsub_rn(y, __fmul_rn(alpha, static_cast<float>(times))), beta);
+    }
+    if (c & kBiased) y = __fadd_rn(y, bias);
+    if (masked && !(static_cast<uint32_t>(mask[at >> 5]) >> (at & 31) & 1)) y = -INFINITY;
+    return y;
+  };
+  Part part;
   uint64_t key = 0;
-  for (int q = tid; q < last; q += kThreads) {
-    float4 v = reinterpret_cast<float4 *>(x)[q];
-    if (!late) penalties(q, v);
-    float *e = &v.x;
-    const int at = 4 * q - m;
-    uint32_t on = 15;
-    if (masked) on = __funnelshift_r(allowed[(at + 32) >> 5], allowed[((at + 32) >> 5) + 1], at + 32);
+  int kept_at = 0;  // this thread's first, for the end
+  float kept = 0.0f;
+  for (int k = list0 + tid; k < list1; k += kThreads) {
+    int at;
+    const float y = adjusted_of(k, at);
+    if (k == list0 + tid) kept_at = at, kept = y;
+    if (greedy) {
+      const uint64_t c = candidate(y, s0 + at);
+      key = c > key ? c : key;
+    } else {
+      part.raise(y, scale);
+      part.add(y, scale);
+    }
+  }
+  // four f of the slice, elements 4 f - m on: what is not the stream's is -inf
+  float4 *const fours = reinterpret_cast<float4 *>(stage + slice.place - m);
+  auto four = [&](int f) {
+    float4 v;
+    if constexpr (kWide) v = fours[f];
+    else v = load4(stage + slice.place - m + 4 * f);
+    if (any_skip) {
+      const int e = 4 * f - m + 32;
+      const uint32_t off = __funnelshift_r(skip[e >> 5], skip[(e >> 5) + 1], e);
+      if (off & 1) v.x = -INFINITY;
+      if (off & 2) v.y = -INFINITY;
+      if (off & 4) v.z = -INFINITY;
+      if (off & 8) v.w = -INFINITY;
+    }
+    return v;
+  };
+
+  // the stream, a chunk as it comes
+  const Out adjusted(t.adjusted, t.adjusted_type, b * t.adjusted_req + i * t.adjusted_row + s0, m);
+  const WaitCtl wait = {a.status, a.abort_epoch, a.epoch, a.limit_ns};
+  constexpr int kFours = 4;  // of a thread at once; with fp32 logits, of a chunk
+  float best = -INFINITY;
+#pragma unroll 1
+  for (int k = 0; k < kChunks; ++k) {
+    if (!mbar_wait(smem_addr(s_bars + k), 0, wait, false)) mbar_wait(smem_addr(s_bars + k), 0, wait, false);
+    const int end = min((k + 1) * slice.each, slice.fours);
+    s_from[k][tid] = 0.0f;
+    for (int f0 = k * slice.each + tid; f0 < end; f0 += kFours * kThreads) {
+      float4 x[kFours];
+      float top = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (!(on >> u & 1) || at + u < 0 || at + u >= len) e[u] = -INFINITY;
-      if (greedy) {
-        nan |= e[u] != e[u];
-        const uint32_t w = __float_as_uint(e[u] + 0.0f);  // (-0 as 0)
-        const uint64_t mine = static_cast<uint64_t>(w >> 31 ? ~w : w | 0x80000000u) << 32 | (kAll - static_cast<uint32_t>(s0 + at + u));
-        if (e[u] > -INFINITY && mine > key) key = mine;
+      for (int u = 0; u < kFours; ++u) {
+        const int f = f0 + u * kThreads;
+        x[u] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (f < end) {
+          x[u] = four(f);
+          if (t.adjusted && !a.in_place) adjusted.four(4 * f - m, len, x[u]);
+        }
+        top = fmaxf(top, fmaxf(fmaxf(x[u].x, x[u].y), fmaxf(x[u].z, x[u].w)));
       }
-      top = fmaxf(top, e[u]);
-    }
-    reinterpret_cast<float4 *>(x)[q] = v;
-  }
-  if (t.adjusted) {
-    __syncthreads();
-    write_slice(t.adjusted, t.adjusted_type, b * t.adjusted_req + i * t.adjusted_row + s0, m, len, [&](int e) { return x[m + e]; });
-    if (!t.probs) {
-      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-      return;
-    }
-  }
-  const int64_t at = b * t.probs_req + i * t.probs_row + s0;
-  if (greedy) {
-    key = warp_max(key);
-    if (__any_sync(kAll, nan)) key = ~uint64_t(0);
-    if (lane == 0) s_key[warp] = key;
-    __syncthreads();
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-    if (warp == 0) {
-      key = warp_max(lane < kWarps ? s_key[lane] : 0);
-      if (lane < kCtas) st_cluster(mapa_shared(smem_addr(s_all + rank), lane), key);
-    }
-    cluster_sync();
+      if (!t.probs) continue;
+      if (greedy) {
+        // only numbers as large as the largest so far
+        bool nan = false;
 #pragma unroll
-    for (int c = 0; c < kCtas; ++c) key = s_all[c] > key ? s_all[c] : key;
-    const int best = key ? static_cast<int>(kAll - static_cast<uint32_t>(key)) - s0 : -1;
-    const bool bad = key == ~uint64_t(0);
-    write_slice(t.probs, t.probs_type, at, m, len, [&](int e) { return bad ? NAN : e == best ? 1.0f : 0.0f; });
+        for (int u = 0; u < kFours; ++u) nan |= x[u].x != x[u].x || x[u].y != x[u].y || x[u].z != x[u].z || x[u].w != x[u].w;
+        if (nan) key = ~uint64_t(0);
+        if (top > best) {
+          best = top;
+#pragma unroll
+          for (int u = kFours - 1; u >= 0; --u) {
+            const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+            for (int q = 3; q >= 0; --q)
+              if (v[q] == top) {
+                const uint64_t c = candidate(top, s0 + 4 * (f0 + u * kThreads) - m + q);
+                key = c > key ? c : key;
+              }
+          }
+        }
+        continue;
+      }
+      const float low = top == -INFINITY ? 0.0f : top;
+      Part mine;
+      mine.top = top;
+#pragma unroll
+      for (int u = 0; u < kFours; ++u) {
+        float4 &v = x[u];
+        v.x = exp2_approx((v.x - low) * scale), v.y = exp2_approx((v.y - low) * scale);
+        v.z = exp2_approx((v.z - low) * scale), v.w = exp2_approx((v.w - low) * scale);
+        mine.sum += (v.x + v.y) + (v.z + v.w);
+        if constexpr (kWide)
+          if (f0 + u * kThreads < end) fours[f0 + u * kThreads] = v;
+      }
+      s_from[k][tid] = low;
+      part.raise(mine.top, scale);
+      part.sum += mine.sum * exp2_approx((low - part.from()) * scale);
+    }
+  }
+  if (t.adjusted && a.in_place && masked) {  // (listed ones stay as they are until the end)
+    for (int e = tid; e < len; e += kThreads)
+      if (!(static_cast<uint32_t>(mask[e >> 5]) >> (e & 31) & 1)) put(t.adjusted, t.adjusted_type, adjusted.at + e, -INFINITY);
+  }
+  float base = 0.0f, factor = 0.0f;
+  int first = -8;  // greedy: the element that has it all
+  bool bad = false;
+  if (t.probs) {
+    // largest number and sum, or candidate: the warp's, the CTA's, the cluster's
+    uint64_t mine = greedy ? warp_max(key) : as_word(joined(part, scale));
+    if (lane == 0) s_warp[warp] = mine;
+    __syncthreads();
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // (every CTA of the cluster runs)
+    auto join = [&](const uint64_t *words_of, int count) {
+      if (greedy) return warp_max(lane < count ? words_of[lane] : 0);
+      return as_word(joined(lane < count ? as_part(words_of[lane]) : Part{}, scale));
+    };
+    const int ctas = 1 << a.ctas_log2;
+    if (warp == 0) {
+      mine = join(s_warp, kWarps);
+      if (lane < ctas) send(mapa_shared(smem_addr(s_all + rank), lane), mine, mapa_shared(smem_addr(&s_told), lane));
+    }
+    if (!mbar_wait(smem_addr(&s_told), 0, wait, false)) mbar_wait(smem_addr(&s_told), 0, wait, false);
+    mine = join(s_all, ctas);
+    const Part all = as_part(mine);
+    bad = greedy && mine == ~uint64_t(0);
+    if (greedy && mine && !bad) first = static_cast<int>(kAll - static_cast<uint32_t>(mine)) - s0;
+    base = all.from(), factor = all.sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, all.sum);
+    const Out out(t.probs, t.probs_type, b * t.probs_req + i * t.probs_row + s0, m);
+    auto probability = [&](float y, int e) {
+      if (greedy) return bad ? NAN : e == first ? 1.0f : 0.0f;
+      return exp2_approx((y - base) * scale) * factor;
+    };
+#pragma unroll 1
+    for (int k = 0; k < kChunks; ++k) {
+      const int end = min((k + 1) * slice.each, slice.fours);
+      const float share = exp2_approx((s_from[k][tid] - base) * scale) * factor;
+#pragma unroll 4
+      for (int f = k * slice.each + tid; f < end; f += kThreads) {
+        const int e = 4 * f - m;
+        float4 v;
+        if (greedy) {
+          v = make_float4(probability(0, e), probability(0, e + 1), probability(0, e + 2), probability(0, e + 3));
+        } else if constexpr (kWide) {
+          v = fours[f];
+          v.x *= share, v.y *= share, v.z *= share, v.w *= share;
+        } else {
+          v = four(f);
+          v = make_float4(probability(v.x, e), probability(v.y, e), probability(v.z, e), probability(v.w, e));
+        }
+        out.four(e, len, v);
+      }
+    }
+    if (a.sparse) {
+      __syncthreads();  // (before the listed ones' places are written again)
+      for (int k = list0 + tid; k < list1; k += kThreads) {
+        int at = kept_at;
+        const float y = k == list0 + tid ? kept : adjusted_of(k, at);
+        put(t.probs, t.probs_type, out.at + at, probability(y, at));
+        if (t.adjusted) put(t.adjusted, t.adjusted_type, adjusted.at + at, y);
+      }
+    }
     return;
   }
-  top = warp_max(top);
-  if (lane == 0) s_max[warp] = top;
-  __syncthreads();
-  top = warp_max(lane < kWarps ? s_max[lane] : -INFINITY);
-  const float from = top == -INFINITY ? 0.0f : top;
-  const float scale = fminf(__fdiv_rn(1.44269504088896341f, temperature), FLT_MAX);  // log2(e) / T
-  float sum = 0.0f;
-  for (int q = tid; q < last; q += kThreads) {
-    float4 v = reinterpret_cast<float4 *>(x)[q];
-    v.x = exp2_approx((v.x - from) * scale), v.y = exp2_approx((v.y - from) * scale);
-    v.z = exp2_approx((v.z - from) * scale), v.w = exp2_approx((v.w - from) * scale);
-    sum += (v.x + v.y) + (v.z + v.w);
-    reinterpret_cast<float4 *>(x)[q] = v;
+  if (a.sparse) {
+    __syncthreads();
+    for (int k = list0 + tid; k < list1; k += kThreads) {
+      int at = kept_at;
+      const float y = k == list0 + tid ? kept : adjusted_of(k, at);
+      put(t.adjusted, t.adjusted_type, adjusted.at + at, y);
+    }
   }
-  sum = warp_sum(sum);
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-  if (warp == 0) {
-    sum = warp_sum(lane < kWarps ? s_sum[lane] : 0.0f);
-    const uint64_t both = static_cast<uint64_t>(__float_as_uint(top)) << 32 | __float_as_uint(sum);
-    if (lane < kCtas) st_cluster(mapa_shared(smem_addr(s_all + rank), lane), both);
-  }
-  cluster_sync();
-  float highest = -INFINITY, total = 0.0f;
-#pragma unroll
-  for (int c = 0; c < kCtas; ++c) highest = fmaxf(highest, __uint_as_float(static_cast<uint32_t>(s_all[c] >> 32)));
-  const float base = highest == -INFINITY ? 0.0f : highest;
-#pragma unroll
-  for (int c = 0; c < kCtas; ++c) {
-    const float part = __uint_as_float(static_cast<uint32_t>(s_all[c])), high = __uint_as_float(static_cast<uint32_t>(s_all[c] >> 32));
-    total += part * exp2_approx((high - base) * scale);
-  }
-  const float factor = total == 0.0f ? 0.0f : __fdiv_rn(exp2_approx((top - base) * scale), total);
-  write_slice(t.probs, t.probs_type, at, m, len, [&](int e) { return x[m + e] * factor; });
 }
 
 template <class T>
 cudaError_t launch_with(const RulesArgs &a, size_t smem, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(token_probs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = cudaSuccess;
+  if (a.ctas_log2 > 3) e = cudaFuncSetAttribute(token_probs_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && smem > 44 * 1024)  // (beside the static arrays, within the 48 KB that need no leave)
+    e = cudaFuncSetAttribute(token_probs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_early(token_probs_kernel<T>, static_cast<unsigned>(a.t.nreq * a.t.rows * kCtas), 1, kThreads, smem, s, a);
+  const unsigned ctas = 1u << a.ctas_log2;
+  return launch_early(token_probs_kernel<T>, Cluster{ctas}, static_cast<unsigned>(a.t.nreq * a.t.rows) * ctas, 1, kThreads, smem, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_token_probs(RulesArgs a, cudaStream_t s) {
-  a.slice = static_cast<int>(((a.t.vocab + kCtas - 1) / kCtas + 31) / 32 * 32);  // (masks in whole words)
+cudaError_t launch_token_probs(RulesArgs a, const CallContext &ctx, cudaStream_t s) {
+  // CTAs of a row: a slice of 50 KB at the most, so that four fit an SM
+  const int64_t rows = a.t.nreq * a.t.rows, size = a.t.type == MMQ_DT_F32 ? 4 : 2;
+  static const char *force = getenv("MMQ_RULES_CTAS");
+  a.ctas_log2 = 0;
+  while (a.ctas_log2 < 4 && ((rows << a.ctas_log2) < 4 * 152 || (a.t.vocab * size >> a.ctas_log2) > 51200) && (a.t.vocab >> a.ctas_log2) > 2048) ++a.ctas_log2;
+  if (force) a.ctas_log2 = atoi(force);
+  const int64_t ctas = int64_t(1) << a.ctas_log2;
+  a.slice = static_cast<int>(((a.t.vocab + ctas - 1) / ctas + 31) / 32 * 32);  // (masks in whole words)
   a.by_rows = FastDiv(a.t.rows);
-  const size_t smem = (a.slice + 8) * 4 + (a.penalties ? (a.slice / 2 + 4) * 4 : 0) + (a.t.mask ? (a.slice / 32 + 2) * 4 : 0);
-  if (a.t.type == MMQ_DT_F32) return launch_with<float>(a, smem, s);
-  return a.t.type == MMQ_DT_F16 ? launch_with<__half>(a, smem, s) : launch_with<__nv_bfloat16>(a, smem, s);
+  a.sparse = a.penalties || a.t.bias_start;
+  void *scratch = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (a.sparse) {
+    const size_t listed = a.t.nreq * (a.t.tokens_width + (a.t.draft ? a.t.rows - 1 : 0)) + a.t.nbias, all_words = a.t.nreq * ctas * (a.slice / 32);
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    e = cudaStreamIsCapturing(s, &cap);
+    if (e != cudaSuccess) return e;
+    const size_t bytes = 4 * (3 * listed + all_words + a.t.nreq * kStarts);
+    e = cap == cudaStreamCaptureStatusActive ? cudaMallocAsync(&scratch, bytes, s) : cudaMallocFromPoolAsync(&scratch, bytes, ctx.pool, s);
+    if (e != cudaSuccess) return e;
+    a.touched = static_cast<uint32_t *>(scratch);
+    a.starts = reinterpret_cast<int32_t *>(a.touched + all_words);
+    a.list = a.starts + a.t.nreq * kStarts;
+    a.counts = reinterpret_cast<uint32_t *>(a.list + listed);
+    a.biases = reinterpret_cast<float *>(a.counts + listed);
+    const size_t smem = 8 * ((a.t.vocab + 31) / 32) + 12 * kEntries;
+    e = cudaFuncSetAttribute(token_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = launch_early(token_list_kernel, static_cast<unsigned>(a.t.nreq), 1, kListThreads, smem, s, a);
+  }
+  const size_t smem = (a.slice + 16) * size + (a.sparse || a.t.mask ? 4 * (a.slice / 32 + 2) : 0);
+  if (e == cudaSuccess) {
+    if (a.t.type == MMQ_DT_F32) e = launch_with<float>(a, smem, s);
+    else e = a.t.type == MMQ_DT_F16 ? launch_with<__half>(a, smem, s) : launch_with<__nv_bfloat16>(a, smem, s);
+  }
+  if (scratch) {
+    const cudaError_t ef = cudaFreeAsync(scratch, s);
+    if (e == cudaSuccess) e = ef;
+  }
+  return e;
 }
 
 }  // namespace mmq
