@@ -619,7 +619,7 @@ typedef struct mmq_token_rules {
  * mmq_last_device_error.
  * vocab in 1..2^18, nreq*rows below 2^27 (more: MMQ_ERR_UNSUPPORTED).  With
  * tokens or biases each request's are listed first, in stream-ordered scratch as for
- * mmq_gemm (12 bytes a token and bias, a bit for each of the vocabulary).
+ * mmq_gemm (12 bytes for each token and bias).
  * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN (elements off their own alignment),
  * MMQ_ERR_TYPE, MMQ_ERR_OOM, MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE,
  * MMQ_ERR_CUDA.

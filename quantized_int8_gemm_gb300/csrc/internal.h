@@ -212,11 +212,10 @@ cudaError_t launch_page_copy(PageCopyArgs a, cudaStream_t s);
 struct RulesArgs {
   mmq_token_rules t;
   bool penalties, sparse, in_place;  // tokens are counted; there are lists; adjusted is the logits
-  int32_t slice, ctas_log2;          // entries of a CTA; CTAs of a row
-  FastDiv by_rows;
-  // of each request: a bit for each listed token, where each CTA's part of its
-  // list begins; of all: the listed tokens, their counts and biases
-  uint32_t *touched;
+  int32_t slice, ctas;               // entries of a CTA; CTAs of a row
+  FastDiv by_rows, by_ctas;
+  // where each CTA's part of a request's list begins; the listed tokens, their
+  // counts and biases
   int32_t *starts, *list;
   uint32_t *counts;
   float *biases;

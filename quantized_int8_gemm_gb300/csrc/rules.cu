@@ -8,7 +8,6 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
-#include <cstdlib>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -17,9 +16,12 @@ namespace mmq {
 namespace {
 
 constexpr int kMostCtas = 16, kThreads = 256, kWarps = kThreads / 32;
+// Elements of a CTA at the most: a sixteenth of 2^18, or 32 KB of 16 bits; and a
+// few for where the slice begins.
+constexpr int kMostSlice = 16384 + 40;
 constexpr unsigned kAll = 0xffffffffu;
-// Of a listed token's count: it is among the prompt's; it has a bias.
-constexpr uint32_t kMet = 0x80000000u, kBiased = 0x40000000u;
+// Of a listed token's count: it is among the prompt's; it has a bias; the row's mask hides it.
+constexpr uint32_t kMet = 0x80000000u, kBiased = 0x40000000u, kHidden = 0x20000000u;
 
 // 8 bytes into another CTA's shared memory, counted by a barrier beside them
 // (both addresses from mapa_shared): no fence, as a store and a cluster barrier
@@ -58,42 +60,31 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
   const uint2 r = *reinterpret_cast<const uint2 *>(p);
   return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
 }
-__device__ __forceinline__ void put4(void *p, int type, int64_t at, const float4 &v) {
-  if (type == MMQ_DT_F32) {
-    __stcs(reinterpret_cast<float4 *>(static_cast<float *>(p) + at), v);
-    return;
-  }
-  uint2 r;
-  if (type == MMQ_DT_F16) r = make_uint2(pack2(v.x, v.y, __half()), pack2(v.z, v.w, __half()));
-  else r = make_uint2(pack2(v.x, v.y, __nv_bfloat16()), pack2(v.z, v.w, __nv_bfloat16()));
-  __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + at), r);
-}
-
 // A CTA's slice of a row on its way to shared memory: whole pieces of 16 bytes by
 // bulk copies, the elements in front of and behind them by threads.  Element e
 // comes to stage[place + e], place being that of the slice in 16 bytes of memory.
-constexpr int kChunks = 5;  // copies of a slice, which are waited for one by one
+constexpr int kFours = 4;                   // fours of a thread at once
+constexpr int kEach = kFours * kThreads;    // and of a copy, which is waited for by itself
 template <class T>
 struct Slice {
   static constexpr int kPiece = 16 / sizeof(T);
   const T *src;
-  int place, head, body, len, fours, each;  // elements; fours of them, of a chunk
+  int place, head, body, len, fours, chunks;  // elements; fours of them; copies
   __device__ __forceinline__ Slice(const T *p, int n) : src(p), len(n) {
     place = static_cast<int>(reinterpret_cast<uintptr_t>(p) / sizeof(T) & (kPiece - 1));
     head = min((kPiece - place) & (kPiece - 1), n);
     body = (n - head) / kPiece * kPiece;
     fours = ((place & 3) + n + 3) >> 2;
-    each = (fours + kChunks - 1) / kChunks;
+    chunks = (fours + kEach - 1) / kEach;
   }
   // Where chunk k begins in the stage: a piece's begin not before its first four.
   __device__ __forceinline__ int chunk(int k) const {
-    const int first = 4 * k * each + (place & ~3), at = k == 0 ? 0 : (first + kPiece - 1) & ~(kPiece - 1);
+    const int first = 4 * k * kEach + (place & ~3), at = k == 0 ? 0 : (first + kPiece - 1) & ~(kPiece - 1);
     return min(max(at, place + head), place + head + body);
   }
   __device__ __forceinline__ void copy(T *stage, const uint64_t *bars) const {  // (one thread)
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
-      const int from = chunk(k), to = k + 1 < kChunks ? chunk(k + 1) : place + head + body;
+    for (int k = 0; k < chunks; ++k) {
+      const int from = chunk(k), to = k + 1 < chunks ? chunk(k + 1) : place + head + body;
       const uint32_t bytes = (to - from) * static_cast<uint32_t>(sizeof(T)), bar = smem_addr(bars + k);
       mbar_arrive_expect_tx(bar, bytes);
       if (bytes)
@@ -119,21 +110,31 @@ __device__ __forceinline__ void put(void *out, int type, int64_t at, float v) {
 // A slice of a row that is written, each element rounded once.
 struct Out {
   void *p;
-  int64_t at;  // the slice's first element
-  int type;
-  bool fits;  // its fours lie in memory as the logits' do
-  __device__ __forceinline__ Out(void *out, int t, int64_t first, int m) : p(out), at(first), type(t) {
-    fits = static_cast<int>((reinterpret_cast<uintptr_t>(out) / (t == MMQ_DT_F32 ? 4 : 2) + first) & 3) == m;
+  int64_t at;       // the slice's first element
+  int type, inner0, inners;  // fours that are the slice's alone and lie in memory as they do here: inners of them, from inner0 on
+  char *base;       // where four 0 would begin
+  __device__ __forceinline__ Out(void *out, int t, int64_t first, int m, int len) : p(out), at(first), type(t) {
+    const int size = t == MMQ_DT_F32 ? 4 : 2;
+    base = static_cast<char *>(out) + (first - m) * size;
+    inner0 = m > 0;
+    inners = (reinterpret_cast<uintptr_t>(base) & (4 * size - 1)) == 0 ? ((m + len) >> 2) - inner0 : 0;
   }
-  __device__ __forceinline__ void four(int e, int len, const float4 &v) const {
-    if (fits && e >= 0 && e + 4 <= len) {
-      put4(p, type, at + e, v);
+  __device__ __forceinline__ void four(int f, int m, int len, const float4 &v) const {
+    if (static_cast<unsigned>(f - inner0) < static_cast<unsigned>(max(inners, 0))) {
+      if (type == MMQ_DT_F32) {
+        __stcs(reinterpret_cast<float4 *>(base) + f, v);
+      } else {
+        const uint2 half = make_uint2(pack2(v.x, v.y, __half()), pack2(v.z, v.w, __half()));
+        const uint2 brain = make_uint2(pack2(v.x, v.y, __nv_bfloat16()), pack2(v.z, v.w, __nv_bfloat16()));
+        __stcs(reinterpret_cast<uint2 *>(base) + f, type == MMQ_DT_F16 ? half : brain);
+      }
       return;
     }
     const float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (e + u >= 0 && e + u < len) put(p, type, at + e + u, x[u]);
+    for (int u = 0; u < 4; ++u) {
+      const int e = 4 * f - m + u;
+      if (e >= 0 && e < len) put(p, type, at + e, u == 0 ? x[0] : u == 1 ? x[1] : u == 2 ? x[2] : x[3]);
+    }
   }
 };
 
@@ -195,6 +196,7 @@ __device__ __forceinline__ uint64_t candidate(float x, int v) {
 // ---------------------------------------------------------------- the request's tokens and biases
 constexpr int kListThreads = 1024;
 constexpr int kEntries = 4096;           // listed tokens that are worked out at once
+constexpr int kDrafted = 32;              // drafted tokens that a row's CTAs keep at hand
 constexpr int kStarts = kMostCtas + 2;   // numbers for a request: where each CTA's part of its list begins, the first bias
 
 // Sum of x over the threads before this one, and over all.
@@ -222,7 +224,7 @@ __device__ __forceinline__ int block_exclusive(int x, int &total, int *sm) {
 
 // Lists a request's distinct tokens (drafted ones and those with a bias among
 // them), ascending, with the times they count before any drafted one and the sums of their
-// biases; sets a bit for each.  A CTA a request: the bits in shared memory
+// biases.  A CTA a request: the bits in shared memory
 // give every token its place in the list (sums of population counts), so
 // the list does not depend on the order that the threads came in.  Latency
 // bound: a round of reads, two passes over the tokens.  Every row of the
@@ -296,9 +298,7 @@ __global__ void __launch_bounds__(kListThreads) token_list_kernel(const __grid_c
     at += __popc(bits[w]);
   }
   __syncthreads();
-  const int all_words = a.slice / 32 << a.ctas_log2;
-  for (int w = tid; w < all_words; w += kListThreads) a.touched[static_cast<int64_t>(b) * all_words + w] = w < words ? bits[w] : 0;
-  if (tid <= 1 << a.ctas_log2) {
+  if (tid <= a.ctas) {
     const int w = tid * (a.slice / 32);
     a.starts[b * kStarts + tid] = w < words ? before[w] : listed;
   }
@@ -363,24 +363,26 @@ __global__ void __launch_bounds__(kListThreads) token_list_kernel(const __grid_c
 // ---------------------------------------------------------------- rows
 // A cluster takes a row, each CTA of it a slice, in shared memory.  Elements
 // that are listed (above) or that a mask hides are left out of a stream that
-// all others go by in: as they come, for their exponentials against the largest
-// of the thread's in a chunk, and once the row's sum is known, to be written.
-// The listed ones, few, are worked out one a thread.
+// all others go by in: for their exponentials against the largest of those that
+// a thread has at once, and when the row's sum is known, to be written.  The
+// listed ones, few, are worked out one a thread.
 //
 // HBM bound with many rows (the row in, the row out), latency bound with few.
 template <class T>
 __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_constant__ RulesArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ __align__(8) uint64_t s_bars[kChunks], s_told;
-  __shared__ uint64_t s_warp[kWarps], s_all[kMostCtas];
-  __shared__ float s_from[kChunks][kThreads];  // what each thread's exponentials of a chunk are against
   constexpr bool kWide = sizeof(T) == 4;
+  constexpr int kChunks = kMostSlice / (4 * kEach) + 1;
+  __shared__ __align__(8) uint64_t s_bars[kChunks], s_told;
+  __shared__ uint64_t s_warp[kWarps], s_all[kMostCtas], s_word;
+  __shared__ int s_draft[kDrafted];
+  __shared__ float s_from[kWide ? kChunks : 1][kThreads];  // what each thread's exponentials of a copy are against
   const mmq_token_rules &t = a.t;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = static_cast<int>(cluster_ctarank()), row = static_cast<int>(blockIdx.x >> a.ctas_log2), b = a.by_rows(row), i = row - b * t.rows;
+  const int rank = static_cast<int>(cluster_ctarank()), row = a.by_ctas(static_cast<int>(blockIdx.x)), b = a.by_rows(row), i = row - b * t.rows;
   const int words = a.slice / 32;
   T *stage = reinterpret_cast<T *>(smem);
-  uint32_t *skip = reinterpret_cast<uint32_t *>(stage + a.slice + 16);  // a bit for each element that is left out, one word in front
+  uint32_t *skip = reinterpret_cast<uint32_t *>(stage + a.slice + 16);  // a bit for each element that the mask hides, one word in front
   const int s0 = rank * a.slice, vocab = static_cast<int>(t.vocab), len = max(min(a.slice, vocab - s0), 0);
   const bool first_thread = tid == 0 && rank == 0;
   const Slice<T> slice(static_cast<const T *>(t.logits) + b * t.logits_req + i * t.logits_row + s0, len);
@@ -389,10 +391,11 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
     for (int k = 0; k < kChunks; ++k) mbar_init(smem_addr(s_bars + k), 1);
     mbar_init(smem_addr(&s_told), 1);
     fence_mbar_init();
-    mbar_arrive_expect_tx(smem_addr(&s_told), 8u << a.ctas_log2);
+    mbar_arrive_expect_tx(smem_addr(&s_told), 8u * a.ctas);
   }
-  griddep_wait();
-  griddep_launch_dependents();
+  // The lists' kernel lets this one begin when everything before it is done, so
+  // what is read before the wait is there; its own lists are, behind it.
+  if (!a.sparse) griddep_wait();
   const int drafted = t.n_draft ? t.n_draft[b] : t.rows - 1;
   if (i > max(drafted, 0)) return;  // (the whole cluster)
   if (tid == 0) slice.copy(stage, s_bars);
@@ -401,6 +404,26 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
   const float rho = t.repetition ? t.repetition[b] : 1.0f, alpha = t.frequency ? t.frequency[b] : 0.0f;
   const float beta = t.presence ? t.presence[b] : 0.0f, temperature = t.temperature ? t.temperature[b] : 1.0f;
   const int64_t which = !t.mask ? -1 : t.mask_rows ? t.mask_rows[row] : row;
+  const bool masked = which >= 0 && which < t.nmasks;
+  if (first_thread) {
+    if (i == 0 && (drafted < 0 || drafted >= t.rows)) record_index(a.status);
+    if (t.mask && !masked && which != -1) record_index(a.status);
+  }
+  const int32_t *mask = t.mask + which * t.mask_stride + (s0 >> 5);
+  if (a.penalties && t.draft && tid < min(i, kDrafted)) s_draft[tid] = t.draft[b * t.draft_stride + tid];
+  // what is in front of the slice and behind it, in its first and last four
+  const int m = slice.place & 3;
+  if (const int e = slice.edge(tid); e >= 0) stage[slice.place + e] = slice.src[e];
+  if (tid >= 64 && tid < 64 + m) store_low(stage + slice.place - 1 - (tid - 64));
+  if (tid >= 96 && tid < 100) store_low(stage + slice.place + len + (tid - 96));
+  if (masked) {
+    for (int w = tid; w < words; w += kThreads) skip[1 + w] = 32 * w < len ? ~static_cast<uint32_t>(mask[w]) : 0;
+    if (tid == 0) skip[0] = skip[words + 1] = 0;
+  }
+  const float scale = fmaxf(fminf(__fdiv_rn(1.44269504088896341f, temperature), FLT_MAX), 0x1p-149f);  // log2(e) / T, not 0 or inf
+  const bool greedy = !(temperature > 0.0f);
+  if (a.sparse) griddep_wait();
+  griddep_launch_dependents();
   int list0 = 0, list1 = 0;
   int64_t list_base = 0;
   if (a.sparse) {
@@ -408,67 +431,53 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
     list0 = starts[rank], list1 = starts[rank + 1];
     list_base = static_cast<int64_t>(b) * (t.tokens_width + (t.draft ? t.rows - 1 : 0)) + starts[kMostCtas + 1];
   }
-  const bool masked = which >= 0 && which < t.nmasks, any_skip = a.sparse || masked;
-  if (first_thread) {
-    if (i == 0 && (drafted < 0 || drafted >= t.rows)) record_index(a.status);
-    if (t.mask && !masked && which != -1) record_index(a.status);
-  }
-  const int32_t *mask = t.mask + which * t.mask_stride + (s0 >> 5);
-  // what is in front of the slice and behind it, in its first and last four
-  const int m = slice.place & 3;
-  if (const int e = slice.edge(tid); e >= 0) stage[slice.place + e] = slice.src[e];
-  if (tid >= 64 && tid < 64 + m) store_low(stage + slice.place - 1 - (tid - 64));
-  if (tid >= 96 && tid < 100) store_low(stage + slice.place + len + (tid - 96));
-  if (any_skip) {
-    const uint32_t *touched = a.touched + (static_cast<int64_t>(b) << a.ctas_log2) * words + rank * words;
-    for (int w = tid; w < words; w += kThreads)
-      skip[1 + w] = (masked && 32 * w < len ? ~static_cast<uint32_t>(mask[w]) : 0) | (a.sparse ? touched[w] : 0);
-    if (tid == 0) skip[0] = skip[words + 1] = 0;
-  }
-  const float scale = fmaxf(fminf(__fdiv_rn(1.44269504088896341f, temperature), FLT_MAX), 0x1p-149f);  // log2(e) / T, not 0 or inf
-  const bool greedy = !(temperature > 0.0f);
-  __syncthreads();
-  // listed element k's adjusted logit
-  auto adjusted_of = [&](int k, int &at) {
-    const int id = a.list[list_base + k];
-    const uint32_t c = a.counts[list_base + k];
-    const float bias = a.biases[list_base + k];
-    at = id - s0;
-    float y = to_f32(slice.src[at]);
+  // The listed elements, several of a thread at once: what the list, the logits
+  // and the mask have of them, and their adjusted logits.  The reads of a
+  // thread's first ones are on their way during the stream.
+  constexpr int kListed = 2, kMore = 4;
+  struct Listed {
+    int at;  // -1: none
+    uint32_t count;
+    float bias, logit;
+  };
+  auto look_up = [&](int k0, auto &l) {
+    constexpr int kHere = sizeof(l) / sizeof(Listed);
+#pragma unroll
+    for (int u = 0; u < kHere; ++u) {
+      const int k = k0 + tid + u * kThreads;
+      l[u].at = -1;
+      if (k < list1) l[u].at = a.list[list_base + k] - s0, l[u].count = a.counts[list_base + k], l[u].bias = a.biases[list_base + k];
+    }
+#pragma unroll
+    for (int u = 0; u < kHere; ++u)
+      if (l[u].at >= 0) {
+        l[u].logit = to_f32(slice.src[l[u].at]);
+        if (masked && !(static_cast<uint32_t>(mask[l[u].at >> 5]) >> (l[u].at & 31) & 1)) l[u].count |= kHidden;
+      }
+  };
+  auto adjust = [&](const Listed &l) {
+    float y = l.logit;
     if (a.penalties) {
-      uint32_t times = c & ~(kMet | kBiased);
+      uint32_t times = l.count & ~(kMet | kBiased | kHidden);
       if (t.draft)
-        for (int j = 0; j < i; ++j) times += t.draft[b * t.draft_stride + j] == id;
-      if (times || (c & kMet)) y = y > 0.0f ? __fdiv_rn(y, rho) : __fmul_rn(y, rho);
+        for (int j = 0; j < i; ++j) times += (j < kDrafted ? s_draft[j] : t.draft[b * t.draft_stride + j]) == l.at + s0;
+      if (times || (l.count & kMet)) y = y > 0.0f ? __fdiv_rn(y, rho) : __fmul_rn(y, rho);
       if (times) y = __fsub_rn(__fsub_rn(y, __fmul_rn(alpha, static_cast<float>(times))), beta);
     }
-    if (c & kBiased) y = __fadd_rn(y, bias);
-    if (masked && !(static_cast<uint32_t>(mask[at >> 5]) >> (at & 31) & 1)) y = -INFINITY;
-    return y;
+    if (l.count & kBiased) y = __fadd_rn(y, l.bias);
+    return l.count & kHidden ? -INFINITY : y;
   };
+  Listed mine[kListed];
+  look_up(list0, mine);
   Part part;
   uint64_t key = 0;
-  int kept_at = 0;  // this thread's first, for the end
-  float kept = 0.0f;
-  for (int k = list0 + tid; k < list1; k += kThreads) {
-    int at;
-    const float y = adjusted_of(k, at);
-    if (k == list0 + tid) kept_at = at, kept = y;
-    if (greedy) {
-      const uint64_t c = candidate(y, s0 + at);
-      key = c > key ? c : key;
-    } else {
-      part.raise(y, scale);
-      part.add(y, scale);
-    }
-  }
   // four f of the slice, elements 4 f - m on: what is not the stream's is -inf
   float4 *const fours = reinterpret_cast<float4 *>(stage + slice.place - m);
   auto four = [&](int f) {
     float4 v;
     if constexpr (kWide) v = fours[f];
     else v = load4(stage + slice.place - m + 4 * f);
-    if (any_skip) {
+    if (masked) {
       const int e = 4 * f - m + 32;
       const uint32_t off = __funnelshift_r(skip[e >> 5], skip[(e >> 5) + 1], e);
       if (off & 1) v.x = -INFINITY;
@@ -479,179 +488,211 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
     return v;
   };
 
-  // the stream, a chunk as it comes
-  const Out adjusted(t.adjusted, t.adjusted_type, b * t.adjusted_req + i * t.adjusted_row + s0, m);
+  const Out adjusted(t.adjusted, t.adjusted_type, b * t.adjusted_req + i * t.adjusted_row + s0, m, len);
   const WaitCtl wait = {a.status, a.abort_epoch, a.epoch, a.limit_ns};
-  constexpr int kFours = 4;  // of a thread at once; with fp32 logits, of a chunk
-  float best = -INFINITY;
-#pragma unroll 1
-  for (int k = 0; k < kChunks; ++k) {
-    if (!mbar_wait(smem_addr(s_bars + k), 0, wait, false)) mbar_wait(smem_addr(s_bars + k), 0, wait, false);
-    const int end = min((k + 1) * slice.each, slice.fours);
-    s_from[k][tid] = 0.0f;
-    for (int f0 = k * slice.each + tid; f0 < end; f0 += kFours * kThreads) {
-      float4 x[kFours];
-      float top = -INFINITY;
+  // (one warp asks, the others are at the barrier: asking is an instruction after another)
+  if (warp == 0)
+    for (int k = 0; k < slice.chunks; ++k)
+      if (!mbar_wait(smem_addr(s_bars + k), 0, wait, false)) mbar_wait(smem_addr(s_bars + k), 0, wait, false);
+  __syncthreads();
+  if (a.sparse) {  // the listed ones leave the stream
 #pragma unroll
-      for (int u = 0; u < kFours; ++u) {
-        const int f = f0 + u * kThreads;
-        x[u] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (f < end) {
-          x[u] = four(f);
-          if (t.adjusted && !a.in_place) adjusted.four(4 * f - m, len, x[u]);
-        }
+    for (int u = 0; u < kListed; ++u)
+      if (mine[u].at >= 0) store_low(stage + slice.place + mine[u].at);
+#pragma unroll 4
+    for (int k = list0 + tid + kListed * kThreads; k < list1; k += kThreads) store_low(stage + slice.place + a.list[list_base + k] - s0);
+    __syncthreads();
+  }
+
+  // the stream, kEach fours at a time
+  float best = -INFINITY;
+  for (int k = 0; k < slice.chunks; ++k) {
+    const int f0 = k * kEach + tid;
+    if (t.adjusted && !a.in_place)
+      for (int f = f0; f < min((k + 1) * kEach, slice.fours); f += kThreads) adjusted.four(f, m, len, four(f));
+    if (!t.probs) continue;
+    float4 x[kFours];
+    float top = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kFours; ++u)
+      if (f0 + u * kThreads < slice.fours) {
+        x[u] = four(f0 + u * kThreads);
         top = fmaxf(top, fmaxf(fmaxf(x[u].x, x[u].y), fmaxf(x[u].z, x[u].w)));
       }
-      if (!t.probs) continue;
-      if (greedy) {
-        // only numbers as large as the largest so far
-        bool nan = false;
+    if (greedy) {
 #pragma unroll
-        for (int u = 0; u < kFours; ++u) nan |= x[u].x != x[u].x || x[u].y != x[u].y || x[u].z != x[u].z || x[u].w != x[u].w;
-        if (nan) key = ~uint64_t(0);
-        if (top > best) {
-          best = top;
+      for (int u = 0; u < kFours; ++u)
+        if (f0 + u * kThreads < slice.fours && (x[u].x != x[u].x || x[u].y != x[u].y || x[u].z != x[u].z || x[u].w != x[u].w)) key = ~uint64_t(0);
+      if (top > best) {  // only numbers above the largest so far
+        best = top;
+        int at = 0;
 #pragma unroll
-          for (int u = kFours - 1; u >= 0; --u) {
-            const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-            for (int q = 3; q >= 0; --q)
-              if (v[q] == top) {
-                const uint64_t c = candidate(top, s0 + 4 * (f0 + u * kThreads) - m + q);
-                key = c > key ? c : key;
-              }
+        for (int u = kFours - 1; u >= 0; --u)
+          if (f0 + u * kThreads < slice.fours) {
+            const int e = 4 * (f0 + u * kThreads) - m;
+            if (x[u].w == top) at = e + 3;
+            if (x[u].z == top) at = e + 2;
+            if (x[u].y == top) at = e + 1;
+            if (x[u].x == top) at = e;
           }
-        }
-        continue;
+        const uint64_t c = candidate(top, s0 + at);
+        key = c > key ? c : key;
       }
-      const float low = top == -INFINITY ? 0.0f : top;
-      Part mine;
-      mine.top = top;
+      continue;
+    }
+    const float low = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
 #pragma unroll
-      for (int u = 0; u < kFours; ++u) {
+    for (int u = 0; u < kFours; ++u)
+      if (f0 + u * kThreads < slice.fours) {
         float4 &v = x[u];
         v.x = exp2_approx((v.x - low) * scale), v.y = exp2_approx((v.y - low) * scale);
         v.z = exp2_approx((v.z - low) * scale), v.w = exp2_approx((v.w - low) * scale);
-        mine.sum += (v.x + v.y) + (v.z + v.w);
-        if constexpr (kWide)
-          if (f0 + u * kThreads < end) fours[f0 + u * kThreads] = v;
+        sum += (v.x + v.y) + (v.z + v.w);
+        if constexpr (kWide) fours[f0 + u * kThreads] = v;
       }
-      s_from[k][tid] = low;
-      part.raise(mine.top, scale);
-      part.sum += mine.sum * exp2_approx((low - part.from()) * scale);
-    }
+    if constexpr (kWide) s_from[k][tid] = low;
+    part.raise(top, scale);
+    part.sum += sum * exp2_approx((low - part.from()) * scale);
   }
+  // the listed ones
+  float my_y[kListed];
+#pragma unroll
+  for (int u = 0; u < kListed; ++u)
+    if (mine[u].at >= 0) my_y[u] = adjust(mine[u]);
+  auto for_listed = [&](auto &&f) {
+#pragma unroll
+    for (int u = 0; u < kListed; ++u)
+      if (mine[u].at >= 0) f(mine[u].at, my_y[u]);
+    for (int k0 = list0 + kListed * kThreads; k0 < list1; k0 += kMore * kThreads) {
+      Listed l[kMore];
+      look_up(k0, l);
+#pragma unroll
+      for (int u = 0; u < kMore; ++u)
+        if (l[u].at >= 0) f(l[u].at, adjust(l[u]));
+    }
+  };
+  if (a.sparse && t.probs)
+    for_listed([&](int at, float y) {
+      if (greedy) {
+        const uint64_t c = candidate(y, s0 + at);
+        key = c > key ? c : key;
+      } else {
+        part.raise(y, scale);
+        part.add(y, scale);
+      }
+    });
   if (t.adjusted && a.in_place && masked) {  // (listed ones stay as they are until the end)
     for (int e = tid; e < len; e += kThreads)
       if (!(static_cast<uint32_t>(mask[e >> 5]) >> (e & 31) & 1)) put(t.adjusted, t.adjusted_type, adjusted.at + e, -INFINITY);
   }
-  float base = 0.0f, factor = 0.0f;
-  int first = -8;  // greedy: the element that has it all
-  bool bad = false;
-  if (t.probs) {
-    // largest number and sum, or candidate: the warp's, the CTA's, the cluster's
-    uint64_t mine = greedy ? warp_max(key) : as_word(joined(part, scale));
-    if (lane == 0) s_warp[warp] = mine;
-    __syncthreads();
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // (every CTA of the cluster runs)
+  if (!t.probs) {
+    if (a.sparse) {
+      __syncthreads();  // (before the listed ones' places are written again)
+      for_listed([&](int at, float y) { put(t.adjusted, t.adjusted_type, adjusted.at + at, y); });
+    }
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    return;
+  }
+
+  // largest number and sum, or candidate: the warp's, the CTA's, the cluster's
+  uint64_t word = greedy ? warp_max(key) : as_word(joined(part, scale));
+  if (lane == 0) s_warp[warp] = word;
+  __syncthreads();
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // (every CTA of the cluster runs)
+  if (warp == 0) {
     auto join = [&](const uint64_t *words_of, int count) {
       if (greedy) return warp_max(lane < count ? words_of[lane] : 0);
       return as_word(joined(lane < count ? as_part(words_of[lane]) : Part{}, scale));
     };
-    const int ctas = 1 << a.ctas_log2;
-    if (warp == 0) {
-      mine = join(s_warp, kWarps);
-      if (lane < ctas) send(mapa_shared(smem_addr(s_all + rank), lane), mine, mapa_shared(smem_addr(&s_told), lane));
-    }
+    word = join(s_warp, kWarps);
+    if (lane < a.ctas) send(mapa_shared(smem_addr(s_all + rank), lane), word, mapa_shared(smem_addr(&s_told), lane));
     if (!mbar_wait(smem_addr(&s_told), 0, wait, false)) mbar_wait(smem_addr(&s_told), 0, wait, false);
-    mine = join(s_all, ctas);
-    const Part all = as_part(mine);
-    bad = greedy && mine == ~uint64_t(0);
-    if (greedy && mine && !bad) first = static_cast<int>(kAll - static_cast<uint32_t>(mine)) - s0;
-    base = all.from(), factor = all.sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, all.sum);
-    const Out out(t.probs, t.probs_type, b * t.probs_req + i * t.probs_row + s0, m);
-    auto probability = [&](float y, int e) {
-      if (greedy) return bad ? NAN : e == first ? 1.0f : 0.0f;
-      return exp2_approx((y - base) * scale) * factor;
-    };
-#pragma unroll 1
-    for (int k = 0; k < kChunks; ++k) {
-      const int end = min((k + 1) * slice.each, slice.fours);
-      const float share = exp2_approx((s_from[k][tid] - base) * scale) * factor;
-#pragma unroll 4
-      for (int f = k * slice.each + tid; f < end; f += kThreads) {
-        const int e = 4 * f - m;
+    word = join(s_all, a.ctas);
+    if (lane == 0) s_word = word;
+  }
+  __syncthreads();
+  word = s_word;
+  const Part all = as_part(word);
+  const bool bad = greedy && word == ~uint64_t(0);
+  const int first = greedy && word && !bad ? static_cast<int>(kAll - static_cast<uint32_t>(word)) - s0 : -8;  // greedy: the element that has it all
+  const float base = all.from(), factor = all.sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, all.sum);
+  auto probability = [&](float y, int e) {
+    if (greedy) return bad ? NAN : e == first ? 1.0f : 0.0f;
+    return exp2_approx((y - base) * scale) * factor;
+  };
+  const Out out(t.probs, t.probs_type, b * t.probs_req + i * t.probs_row + s0, m, len);
+  if (greedy) {
+    for (int f = tid; f < slice.fours; f += kThreads) {
+      const int e = 4 * f - m;
+      out.four(f, m, len, make_float4(probability(0, e), probability(0, e + 1), probability(0, e + 2), probability(0, e + 3)));
+    }
+  } else {
+    for (int k = 0; k < slice.chunks; ++k) {
+      float share = 0.0f;
+      if constexpr (kWide) share = exp2_approx((s_from[k][tid] - base) * scale) * factor;
+#pragma unroll
+      for (int u = 0; u < kFours; ++u) {
+        const int f = k * kEach + tid + u * kThreads;
+        if (f >= slice.fours) break;
         float4 v;
-        if (greedy) {
-          v = make_float4(probability(0, e), probability(0, e + 1), probability(0, e + 2), probability(0, e + 3));
-        } else if constexpr (kWide) {
+        if constexpr (kWide) {
           v = fours[f];
           v.x *= share, v.y *= share, v.z *= share, v.w *= share;
         } else {
           v = four(f);
-          v = make_float4(probability(v.x, e), probability(v.y, e), probability(v.z, e), probability(v.w, e));
+          v = make_float4(probability(v.x, 0), probability(v.y, 0), probability(v.z, 0), probability(v.w, 0));
         }
-        out.four(e, len, v);
+        out.four(f, m, len, v);
       }
     }
-    if (a.sparse) {
-      __syncthreads();  // (before the listed ones' places are written again)
-      for (int k = list0 + tid; k < list1; k += kThreads) {
-        int at = kept_at;
-        const float y = k == list0 + tid ? kept : adjusted_of(k, at);
-        put(t.probs, t.probs_type, out.at + at, probability(y, at));
-        if (t.adjusted) put(t.adjusted, t.adjusted_type, adjusted.at + at, y);
-      }
-    }
-    return;
   }
   if (a.sparse) {
-    __syncthreads();
-    for (int k = list0 + tid; k < list1; k += kThreads) {
-      int at = kept_at;
-      const float y = k == list0 + tid ? kept : adjusted_of(k, at);
-      put(t.adjusted, t.adjusted_type, adjusted.at + at, y);
-    }
+    __syncthreads();  // (before the listed ones' places are written again)
+    for_listed([&](int at, float y) {
+      put(t.probs, t.probs_type, out.at + at, probability(y, at));
+      if (t.adjusted) put(t.adjusted, t.adjusted_type, adjusted.at + at, y);
+    });
   }
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 template <class T>
 cudaError_t launch_with(const RulesArgs &a, size_t smem, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
-  if (a.ctas_log2 > 3) e = cudaFuncSetAttribute(token_probs_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess && smem > 44 * 1024)  // (beside the static arrays, within the 48 KB that need no leave)
+  if (a.ctas > 8) e = cudaFuncSetAttribute(token_probs_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && smem > 40 * 1024)  // (beside the static arrays, within the 48 KB that need no leave)
     e = cudaFuncSetAttribute(token_probs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const unsigned ctas = 1u << a.ctas_log2;
+  const unsigned ctas = a.ctas;
   return launch_early(token_probs_kernel<T>, Cluster{ctas}, static_cast<unsigned>(a.t.nreq * a.t.rows) * ctas, 1, kThreads, smem, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_token_probs(RulesArgs a, const CallContext &ctx, cudaStream_t s) {
-  // CTAs of a row: a slice of 50 KB at the most, so that four fit an SM
-  const int64_t rows = a.t.nreq * a.t.rows, size = a.t.type == MMQ_DT_F32 ? 4 : 2;
-  static const char *force = getenv("MMQ_RULES_CTAS");
-  a.ctas_log2 = 0;
-  while (a.ctas_log2 < 4 && ((rows << a.ctas_log2) < 4 * 152 || (a.t.vocab * size >> a.ctas_log2) > 51200) && (a.t.vocab >> a.ctas_log2) > 2048) ++a.ctas_log2;
-  if (force) a.ctas_log2 = atoi(force);
-  const int64_t ctas = int64_t(1) << a.ctas_log2;
+  // CTAs of a row: four of them fit an SM with slices of 46 KB (960 rows of 100277
+  // in fp32: 196 us, with 36 KB 216, 24 KB 277); with 32 KB of 16-bit logits (120 rows
+  // of 128256: 62 us, with 46 KB 66, 20 KB 66); with few rows more, as long as
+  // all run at once and have 2048 elements or more
+  const int64_t rows = a.t.nreq * a.t.rows, size = a.t.type == MMQ_DT_F32 ? 4 : 2, most = (size == 4 ? 46 : 32) * 1024;
+  const int64_t fit = (a.t.vocab * size + most - 1) / most, few = std::min(4 * 152 / rows, a.t.vocab / 2048);
+  const int64_t ctas = std::min<int64_t>(kMostCtas, std::max<int64_t>({fit, few, 1}));
+  a.ctas = static_cast<int>(ctas);
+  a.by_ctas = FastDiv(a.ctas);
   a.slice = static_cast<int>(((a.t.vocab + ctas - 1) / ctas + 31) / 32 * 32);  // (masks in whole words)
   a.by_rows = FastDiv(a.t.rows);
   a.sparse = a.penalties || a.t.bias_start;
   void *scratch = nullptr;
   cudaError_t e = cudaSuccess;
   if (a.sparse) {
-    const size_t listed = a.t.nreq * (a.t.tokens_width + (a.t.draft ? a.t.rows - 1 : 0)) + a.t.nbias, all_words = a.t.nreq * ctas * (a.slice / 32);
+    const size_t listed = a.t.nreq * (a.t.tokens_width + (a.t.draft ? a.t.rows - 1 : 0)) + a.t.nbias;
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     e = cudaStreamIsCapturing(s, &cap);
     if (e != cudaSuccess) return e;
-    const size_t bytes = 4 * (3 * listed + all_words + a.t.nreq * kStarts);
+    const size_t bytes = 4 * (3 * listed + a.t.nreq * kStarts);
     e = cap == cudaStreamCaptureStatusActive ? cudaMallocAsync(&scratch, bytes, s) : cudaMallocFromPoolAsync(&scratch, bytes, ctx.pool, s);
     if (e != cudaSuccess) return e;
-    a.touched = static_cast<uint32_t *>(scratch);
-    a.starts = reinterpret_cast<int32_t *>(a.touched + all_words);
+    a.starts = static_cast<int32_t *>(scratch);
     a.list = a.starts + a.t.nreq * kStarts;
     a.counts = reinterpret_cast<uint32_t *>(a.list + listed);
     a.biases = reinterpret_cast<float *>(a.counts + listed);
@@ -659,7 +700,7 @@ cudaError_t launch_token_probs(RulesArgs a, const CallContext &ctx, cudaStream_t
     e = cudaFuncSetAttribute(token_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e == cudaSuccess) e = launch_early(token_list_kernel, static_cast<unsigned>(a.t.nreq), 1, kListThreads, smem, s, a);
   }
-  const size_t smem = (a.slice + 16) * size + (a.sparse || a.t.mask ? 4 * (a.slice / 32 + 2) : 0);
+  const size_t smem = (a.slice + 16) * size + (a.t.mask ? 4 * (a.slice / 32 + 2) : 0);
   if (e == cudaSuccess) {
     if (a.t.type == MMQ_DT_F32) e = launch_with<float>(a, smem, s);
     else e = a.t.type == MMQ_DT_F16 ? launch_with<__half>(a, smem, s) : launch_with<__nv_bfloat16>(a, smem, s);
