@@ -675,9 +675,10 @@ typedef struct mmq_lora_args {
  *   Sums are fp32; x and the inner sums enter the tensor cores as three 16-bit
  * terms, which hold their 24 bits.  An x or an inner sum that is not finite makes its row NaN
  * (infinities among them).  The results of one problem do not change from call
- * to call.  One kernel, no scratch.
- * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN, MMQ_ERR_TYPE, MMQ_ERR_UNSUPPORTED,
- * MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
+ * to call.  Where adapters have more than eight tokens on the average the inner
+ * sums are stream-ordered scratch as for mmq_gemm (6 bytes a token and rank).
+ * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN, MMQ_ERR_TYPE, MMQ_ERR_OOM,
+ * MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
  */
 int mmq_lora(const mmq_lora_args *args, mmq_stream_t stream);
 

@@ -239,9 +239,12 @@ int64_t lora_plan_words(int64_t ntok, int64_t nreq, int64_t nadapters);
 
 struct LoraArgs {
   mmq_lora_args t;
-  bool wide;  // rows of y and out in 16-byte pieces
+  bool wide;              // rows of y and out in 16-byte pieces
+  int32_t front, chunks;  // bytes of the first product's stages; CTAs of a tile in the second
+  FastDiv by_chunks;
+  uint32_t *terms;        // what the first leaves for the second
 };
-cudaError_t launch_lora(LoraArgs a, cudaStream_t s);
+cudaError_t launch_lora(LoraArgs a, const CallContext &ctx, cudaStream_t s);
 
 // Engine-rate microbenchmarks (probe.cu); out[0..4] as mmq_probe_engine_rates.
 cudaError_t launch_engine_probes(DevStatus *st, unsigned epoch, uint64_t limit_ns, cudaStream_t s, double *out);

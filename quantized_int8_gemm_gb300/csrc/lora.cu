@@ -2,10 +2,8 @@
 // out[t] = y[t] + s_a (x[t] A_a^T) B_a^T with the adapter a of token t's request.
 //
 // The plan sorts a step's tokens by adapter, once for all its projections, and
-// cuts them into tiles of one adapter.  A cluster of eight CTAs takes a tile:
-// each multiplies an eighth of x's columns by A, the partial sums are joined
-// through the cluster's shared memory, and each writes an eighth of the output
-// columns.  So a tile's x, y and out go through once, in one launch.
+// cuts them into tiles of one adapter, so that x, y and out go through once and
+// an adapter's weights are read once for each tile.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -318,25 +316,37 @@ __device__ __forceinline__ void split8(Terms (&out)[4], uint4 a, uint4 b, int x_
 template <int kTile>
 struct Shape {
   static constexpr int kTokens = kTile == 64 ? 16 : 8, kGroups = kTile / kTokens, kSplit = kWarps / kGroups, kColumns = kTokens / 8;
-  static constexpr int kPiece = 32 * kSplit;                  // columns of a stage
-  static constexpr bool kStaged = kTile > 8;
-  static constexpr int kXStage = kTile * kPiece * 4, kStage = kXStage + kRankPass * kPiece * 2;  // bytes
-  // the terms of the joined sums: a token's ranks together, rows 16 words from
-  // a multiple of 32 apart (eight lanes of a 16-byte read then touch every
-  // bank once)
-  __host__ __device__ static constexpr int pitch(int rank) { return (rank + 31) / 32 * 16 % 32 ? (rank + 31) / 32 * 16 : (rank + 31) / 32 * 16 + 16; }
-  // Shared memory: stages of the first product, then the partial sums of the
-  // warps, then the terms in one place; the CTA's sums behind it.
-  __host__ __device__ static constexpr int front(int rank) {
-    const int stages = kStaged ? kStages * kStage : 0, part = 4 * kSplit * kRankPass * kTile, terms = 4 * kTerms * kTile * pitch(rank);
-    return stages > part ? (stages > terms ? stages : terms) : (part > terms ? part : terms);
-  }
-  static size_t bytes(int rank) { return front(rank) + 4 * static_cast<size_t>((rank + 15) / 16 * 16) * kTile; }
+  static constexpr int kPiece = 32 * kSplit;  // columns of a stage
 };
+// The terms of the joined sums, of a tile: [term][token][pitch] words, a token's
+// ranks together, rows 16 words from a multiple of 32 apart (eight lanes of a
+// 16-byte read then touch every bank once).
+__host__ __device__ constexpr int pitch_of(int rank) { return (rank + 31) / 32 * 16 % 32 ? (rank + 31) / 32 * 16 : (rank + 31) / 32 * 16 + 16; }
+__host__ __device__ constexpr int up16(int rank) { return (rank + 15) / 16 * 16; }
 
-// Rows of a tile without an adapter: out = y over the CTA's columns.
-template <int kTile>
-__device__ __forceinline__ void copy_rows(const LoraArgs &a, const int (&s_row)[kTile], int n, int o0, int o1) {
+__host__ __device__ constexpr int few_front(int rank) {  // bytes of the partial sums or the terms of eight tokens
+  const int part = 4 * kWarps * kRankPass * 8, terms = 4 * kTerms * 8 * pitch_of(rank);
+  return part > terms ? part : terms;
+}
+
+// A tile of the plan; n = 0 behind the last one (of those with an adapter, if
+// only they are wanted), whose entries the plan has room for but nobody wrote.
+struct Tile {
+  int adapter, first, n, rank;
+  float scale;
+};
+__device__ __forceinline__ Tile tile_at(const mmq_lora_args &t, int tile, bool adapters_only) {
+  const int32_t *entry = t.plan + kHead + t.ntok + 3 * static_cast<int64_t>(tile);
+  Tile k;
+  k.adapter = entry[0], k.first = entry[1], k.n = entry[2];
+  if (tile >= t.plan[adapters_only ? 1 : 0]) return {-1, 0, 0, 0, 1.0f};
+  k.rank = k.adapter < 0 ? 0 : t.ranks ? min(max(t.ranks[k.adapter], 0), t.rank) : t.rank;
+  k.scale = t.scales && k.adapter >= 0 ? t.scales[k.adapter] : 1.0f;
+  return k;
+}
+
+// Rows of a tile without an adapter (or of rank 0): out = y in columns [o0, o1).
+__device__ __forceinline__ void copy_rows(const LoraArgs &a, const int *s_row, int n, int o0, int o1) {
   const mmq_lora_args &t = a.t;
   constexpr int kEach = 8;
   const int width = a.wide ? (o1 - o0) / 4 : o1 - o0, items = n * width;
@@ -361,8 +371,231 @@ __device__ __forceinline__ void copy_rows(const LoraArgs &a, const int (&s_row)[
   }
 }
 
+// Partial sums of the warps of a CTA, [split][rank of the pass][token], added up
+// in their order into the CTA's, [rank][token].
+template <int kTile>
+__device__ __forceinline__ void add_up(float *mine, const float *part, int r0, int r16) {
+  using S = Shape<kTile>;
+  for (int e = threadIdx.x; e < min(r16 - r0, kRankPass) * kTile; e += kThreads) {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < S::kSplit; ++k) s += part[k * kRankPass * kTile + e];
+    mine[r0 * kTile + e] = s;
+  }
+}
+template <int kTile, int kColumns>
+__device__ __forceinline__ void put_part(float *part, const float (&acc)[kRankPass / 16][kColumns][4], int ranks, int slot, int tokens0) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int m = 0; m < kRankPass / 16; ++m) {
+    if (16 * m >= ranks) break;
+#pragma unroll
+    for (int j = 0; j < kColumns; ++j) {
+      float *to = part + (slot * kRankPass + 16 * m + g) * kTile + tokens0 + 8 * j + 2 * c;
+      *reinterpret_cast<float2 *>(to) = make_float2(acc[m][j][0], acc[m][j][1]);
+      *reinterpret_cast<float2 *>(to + 8 * kTile) = make_float2(acc[m][j][2], acc[m][j][3]);
+    }
+  }
+}
+// Ranks 2 pair and 2 pair + 1 of a token, joined over the cluster in the CTAs' order.
+template <int kTile>
+__device__ __forceinline__ Terms joined(const float *mine, int pair, int token, float scale) {
+  float s0 = 0.0f, s1 = 0.0f, v0[kCtas], v1[kCtas];
+#pragma unroll
+  for (int k = 0; k < kCtas; ++k) {
+    const uint32_t from = mapa_shared(smem_addr(mine + 2 * pair * kTile + token), k);
+    v0[k] = ld_cluster(from), v1[k] = ld_cluster(from + 4 * kTile);
+  }
+#pragma unroll
+  for (int k = 0; k < kCtas; ++k) s0 += v0[k], s1 += v1[k];
+  return split(s0 * scale, s1 * scale);
+}
+
+// Four output columns o .. o + 3 of a token.
+__device__ __forceinline__ float4 load_y(const LoraArgs &a, int row, int o) {
+  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int od = static_cast<int>(a.t.od);
+  if (row < 0 || o >= od) return y;
+  const float *from = a.t.y + row * a.t.y_row + o;
+  if (a.wide) return __ldcs(reinterpret_cast<const float4 *>(from));
+  y.x = from[0];
+  if (o + 1 < od) y.y = from[1];
+  if (o + 2 < od) y.z = from[2];
+  if (o + 3 < od) y.w = from[3];
+  return y;
+}
+__device__ __forceinline__ void store_out(const LoraArgs &a, int row, int o, float4 v) {
+  const int od = static_cast<int>(a.t.od);
+  if (row < 0 || o >= od) return;
+  float *to = a.t.out + row * a.t.out_row + o;
+  if (a.wide) {
+    *reinterpret_cast<float4 *>(to) = v;
+    return;
+  }
+  to[0] = v.x;
+  if (o + 1 < od) to[1] = v.y;
+  if (o + 2 < od) to[2] = v.z;
+  if (o + 3 < od) to[3] = v.w;
+}
+// The second product for 32 output columns (o0 on) and eight tokens of each of
+// kEach columns (k0 on): a lane has four output columns that lie together, rows
+// g and g + 8 of two blocks of 16.
+template <class W, int kEach>
+__device__ __forceinline__ void expand(float (&acc)[2][kEach][4], const LoraArgs &a, const W *up, const uint32_t *terms, int term_words, int pitch, int r,
+                                       int o, int k0) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, od = static_cast<int>(a.t.od);
+  for (int r0 = 0; r0 < r; r0 += 32) {
+    const int k = r0 + 8 * c;
+    Weights8<W> w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint4 raw = zero4();
+      if (k < r && o + i < od) raw = __ldg(reinterpret_cast<const uint4 *>(up + static_cast<int64_t>(o + i) * a.t.rank + k));
+      if (k < r && k + 8 > r) {  // columns past the rank
+        uint32_t *v = &raw.x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] &= k + 2 * e + 1 < r ? 0xffffffffu : k + 2 * e < r ? 0xffffu : 0u;
+      }
+      w[i].set(raw);
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      Terms x[4];
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(terms + i * term_words + (k0 + 8 * j + g) * pitch + k / 2);
+        x[0].w[i] = v.x, x[1].w[i] = v.y, x[2].w[i] = v.z, x[3].w[i] = v.w;
+      }
+      product<W>(acc[0][j], w[0], w[1], x);
+      product<W>(acc[1][j], w[2], w[3], x);
+    }
+  }
+}
+template <int kEach>
+__device__ __forceinline__ float4 sum_of(const float (&acc)[2][kEach][4], int j, int h, const float4 &y) {
+  return make_float4(y.x + acc[0][j][h], y.y + acc[0][j][h + 2], y.z + acc[1][j][h], y.w + acc[1][j][h + 2]);
+}
+
+// ---------------------------------------------------------------- few tokens: one kernel
+// A cluster takes a tile of eight tokens: each CTA multiplies an eighth of x's
+// columns by A, the sums are joined through the cluster's shared memory, and
+// each writes an eighth of the output columns.  HBM bound by the adapters with
+// many tiles, latency bound with few.
+constexpr int kFew = 8;
+template <class W>
+__global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCtas, 1, 1) lora_few_kernel(const __grid_constant__ LoraArgs a) {
+  using S = Shape<kFew>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int s_row[kFew];
+  const mmq_lora_args &t = a.t;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int rank = static_cast<int>(cluster_ctarank()), tile = static_cast<int>(blockIdx.x / kCtas);
+  griddep_wait();
+  griddep_launch_dependents();
+  const bool in_place = t.y == t.out;
+  const Tile k_tile = tile_at(t, tile, in_place);
+  if (k_tile.n == 0) return;  // (the whole cluster)
+  const int n = k_tile.n, r = k_tile.rank;
+  if (tid < kFew) s_row[tid] = tid < n ? t.plan[kHead + k_tile.first + tid] : -1;
+  const int id = static_cast<int>(t.id), od = static_cast<int>(t.od), rmax = t.rank;
+  const int units = (od + 31) / 32, per = (units + kCtas - 1) / kCtas, u0 = min(rank * per, units), u1 = min(u0 + per, units);
+  const W *up = static_cast<const W *>(t.b) + static_cast<int64_t>(max(k_tile.adapter, 0)) * od * rmax;
+  if (r > 0) {
+    // the adapter is most of what is read: the second product's part of it comes
+    // to L2 during the first
+    const char *from = reinterpret_cast<const char *>(up + static_cast<int64_t>(32 * u0) * rmax);
+    const int64_t bytes = static_cast<int64_t>(min(32 * u1, od) - 32 * u0) * rmax * 2;
+    for (int64_t at = tid * 4096; at < bytes; at += kThreads * 4096)
+      bulk_prefetch_l2(from + at, static_cast<uint32_t>(min(bytes - at, static_cast<int64_t>(4096))));
+  }
+  __syncthreads();
+  if (r == 0) {
+    if (!in_place) copy_rows(a, s_row, n, min(32 * u0, od), min(32 * u1, od));
+    return;
+  }
+  const int r16 = up16(r), pitch = pitch_of(rmax);
+  // partial sums of the warps, later the terms; behind them the CTA's sums
+  float *part = reinterpret_cast<float *>(smem), *mine = reinterpret_cast<float *>(smem + few_front(rmax));
+  uint32_t *terms = reinterpret_cast<uint32_t *>(smem);
+  {
+    const int pieces = (id + S::kPiece - 1) / S::kPiece, share = (pieces + kCtas - 1) / kCtas;
+    const int p0 = min(rank * share, pieces), p1 = min(p0 + share, pieces);
+    const W *down = static_cast<const W *>(t.a) + static_cast<int64_t>(k_tile.adapter) * rmax * id;
+    const int x_size = t.x_type == MMQ_DT_F32 ? 4 : 2, of = s_row[g];
+    const unsigned char *row = static_cast<const unsigned char *>(t.x) + max(of, 0) * t.x_row * x_size;
+    for (int r0 = 0; r0 < r; r0 += kRankPass) {
+      const int ranks = min(r - r0, kRankPass);
+      float acc[kRankPass / 16][S::kColumns][4] = {};
+      for (int step = p0 * S::kSplit + warp; step < p1 * S::kSplit; step += S::kSplit) {
+        const int k = 32 * step + 8 * c;
+        const bool in = k < id;
+        uint4 raw[kRankPass / 16][2], lo = zero4(), hi = zero4();
+#pragma unroll
+        for (int m = 0; m < kRankPass / 16; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int at = 16 * m + 8 * h + g;
+            raw[m][h] = in && at < ranks ? __ldg(reinterpret_cast<const uint4 *>(down + static_cast<int64_t>(r0 + at) * id + k)) : zero4();
+          }
+        if (in && of >= 0) {
+          lo = __ldg(reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(k) * x_size));
+          if (x_size == 4) hi = __ldg(reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(k) * x_size) + 1);
+        }
+        Terms xt[4];
+        split8(xt, lo, hi, t.x_type);
+#pragma unroll
+        for (int m = 0; m < kRankPass / 16; ++m) {
+          if (16 * m >= ranks) break;
+          Weights8<W> u, v;
+          u.set(raw[m][0]), v.set(raw[m][1]);
+          product<W>(acc[m][0], u, v, xt);
+        }
+      }
+      if (r0) __syncthreads();
+      put_part<kFew>(part, acc, ranks, warp, 0);
+      __syncthreads();
+      add_up<kFew>(mine, part, r0, r16);
+    }
+    __syncthreads();  // (part makes room)
+  }
+  for (int k = tid; k < kTerms * kFew * pitch; k += kThreads) terms[k] = 0;  // (ranks past r)
+  cluster_sync();
+  // each CTA adds up a share of the pairs of ranks and sends it to all
+  for (int e = rank * kThreads + tid; e < r16 / 2 * kFew; e += kCtas * kThreads) {
+    const int pair = e / kFew, token = e % kFew;
+    const Terms sum = joined<kFew>(mine, pair, token, k_tile.scale);
+#pragma unroll
+    for (int k = 0; k < kCtas; ++k) {
+      const uint32_t to = mapa_shared(smem_addr(terms + token * pitch + pair), k);
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i) st_cluster(to + 4 * i * kFew * pitch, sum.w[i]);
+    }
+  }
+  cluster_sync();
+  for (int u = u0 + warp; u < u1; u += kWarps) {
+    const int o = 32 * u + 4 * g;
+    float4 y[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) y[h] = load_y(a, s_row[2 * c + h], o);
+    float acc[2][1][4] = {};
+    expand<W, 1>(acc, a, up, terms, kFew * pitch, pitch, r, o, 0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) store_out(a, s_row[2 * c + h], o, sum_of<1>(acc, 0, h, y[h]));
+  }
+}
+
+// ---------------------------------------------------------------- more tokens: two kernels
+// With prompts the rows of x, y and out are most of what is read and written,
+// and the two products have little in common in their shares: tiles by columns
+// of x, joined; tiles by columns of out.  In one kernel (each CTA an eighth of
+// both) a tile's CTAs lived 60 us and the last, partly filled wave as long as the
+// first (2158 tokens, 3584 to 18944: 128 us).
+//
+// The first product: a cluster takes a tile, each CTA an eighth of x's columns,
+// through stages of shared memory; the sums are joined through the cluster's
+// shared memory and left as terms.
 template <class W, int kTile>
-__global__ void __launch_bounds__(kThreads, kTile == 8 ? 3 : 2) __cluster_dims__(kCtas, 1, 1) lora_kernel(const __grid_constant__ LoraArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lora_down_kernel(const __grid_constant__ LoraArgs a) {
   using S = Shape<kTile>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_row[kTile];
@@ -371,247 +604,154 @@ __global__ void __launch_bounds__(kThreads, kTile == 8 ? 3 : 2) __cluster_dims__
   const int rank = static_cast<int>(cluster_ctarank()), tile = static_cast<int>(blockIdx.x / kCtas);
   griddep_wait();
   griddep_launch_dependents();
-  const bool in_place = t.y == t.out;
-  const int32_t *entry = t.plan + kHead + t.ntok + 3 * static_cast<int64_t>(tile);
-  if (tile >= t.plan[in_place ? 1 : 0]) return;  // (the whole cluster)
-  const int adapter = entry[0], first = entry[1], n = entry[2];
-  if (tid < kTile) s_row[tid] = tid < n ? t.plan[kHead + first + tid] : -1;
-  const int id = static_cast<int>(t.id), od = static_cast<int>(t.od), rmax = t.rank;
-  const int units = (od + 31) / 32, per = (units + kCtas - 1) / kCtas, u0 = min(rank * per, units), u1 = min(u0 + per, units);
-  const W *up = static_cast<const W *>(t.b) + static_cast<int64_t>(max(adapter, 0)) * od * rmax;
-  if (kTile <= 16 && adapter >= 0) {
-    // few tokens: the adapter is most of what is read, so the second product's
-    // part comes to L2 during the first
-    const char *from = reinterpret_cast<const char *>(up + static_cast<int64_t>(32 * u0) * rmax);
-    const int64_t bytes = static_cast<int64_t>(min(32 * u1, od) - 32 * u0) * rmax * 2;
-    for (int64_t at = tid * 4096; at < bytes; at += kThreads * 4096)
-      bulk_prefetch_l2(from + at, static_cast<uint32_t>(min(bytes - at, static_cast<int64_t>(4096))));
-  }
-  const int r = adapter < 0 ? 0 : t.ranks ? min(max(t.ranks[adapter], 0), rmax) : rmax;
-  const float scale = t.scales && adapter >= 0 ? t.scales[adapter] : 1.0f;
+  const Tile k_tile = tile_at(t, tile, true);
+  if (k_tile.n == 0) return;  // (the whole cluster)
+  const int n = k_tile.n, r = k_tile.rank;
+  if (r == 0) return;
+  if (tid < kTile) s_row[tid] = tid < n ? t.plan[kHead + k_tile.first + tid] : -1;
+  const int id = static_cast<int>(t.id), rmax = t.rank, r16 = up16(r), stage_ranks = min(up16(rmax), kRankPass);
+  const int x_size = t.x_type == MMQ_DT_F32 ? 4 : 2, x_stage = kTile * S::kPiece * x_size, stage_bytes = x_stage + stage_ranks * S::kPiece * 2;
+  float *part = reinterpret_cast<float *>(smem), *mine = reinterpret_cast<float *>(smem + a.front);
+  const int pieces = (id + S::kPiece - 1) / S::kPiece, share = (pieces + kCtas - 1) / kCtas;
+  const int p0 = min(rank * share, pieces), p1 = min(p0 + share, pieces);
+  const int tokens0 = warp % S::kGroups * S::kTokens, slot = warp / S::kGroups;
+  const W *down = static_cast<const W *>(t.a) + static_cast<int64_t>(k_tile.adapter) * rmax * id;
+  const unsigned char *x = static_cast<const unsigned char *>(t.x);
+  // Pieces of x and of the weights in 16-byte chunks, the chunks of odd rows a
+  // quarter of eight (x in fp32) or half of them off, so that eight lanes of a
+  // read touch every bank once.
+  const uint32_t base = smem_addr(smem);
+  const int x_chunks_log2 = S::kPiece == 64 ? (x_size == 4 ? 4 : 3) : (x_size == 4 ? 5 : 4);  // of a row
+  auto x_at = [&](int row, int chunk) {
+    return static_cast<uint32_t>(row * S::kPiece * x_size) + ((chunk ^ (x_size == 4 ? row & 1 : (row & 1) * 4)) << 4);
+  };
+  auto w_at = [&](int row, int chunk) { return static_cast<uint32_t>(x_stage + row * S::kPiece * 2) + ((chunk ^ (row & 1) * 4) << 4); };
   __syncthreads();
-  if (r == 0) {
-    if (!in_place) copy_rows<kTile>(a, s_row, n, min(32 * u0, od), min(32 * u1, od));
-    return;
-  }
-  const int r16 = (r + 15) / 16 * 16, r32 = (r + 31) / 32 * 32, pitch = S::pitch(rmax);
-  float *part = reinterpret_cast<float *>(smem), *mine = reinterpret_cast<float *>(smem + S::front(rmax));  // [split][rank of the pass][token]; [rank][token]
-  uint32_t *terms = reinterpret_cast<uint32_t *>(smem);                                                     // [term][token][pitch]
-
-  // the first product, transposed: ranks x tokens over the CTA's columns
-  {
-    const int pieces = (id + S::kPiece - 1) / S::kPiece, share = (pieces + kCtas - 1) / kCtas;
-    const int p0 = min(rank * share, pieces), p1 = min(p0 + share, pieces);
-    const int tokens0 = warp % S::kGroups * S::kTokens, slot = warp / S::kGroups;
-    const W *down = static_cast<const W *>(t.a) + static_cast<int64_t>(adapter) * rmax * id;
-    const unsigned char *x = static_cast<const unsigned char *>(t.x);
-    const int x_size = t.x_type == MMQ_DT_F32 ? 4 : 2;
-    for (int r0 = 0; r0 < r; r0 += kRankPass) {
-      const int ranks = min(r - r0, kRankPass);
-      float acc[kRankPass / 16][S::kColumns][4] = {};
-      if constexpr (S::kStaged) {
-        // Pieces of x and of the weights in 16-byte chunks, the chunks of odd
-        // rows half a quarter (x) or half a row of 32 columns (weights) off, so
-        // that eight lanes of a read touch every bank once.
-        const uint32_t base = smem_addr(smem);
-        const int x_chunks = S::kPiece * x_size / 16;  // of a row
-        auto x_at = [&](int row, int chunk) {
-          return static_cast<uint32_t>(row * S::kPiece * x_size) + ((chunk ^ (x_size == 4 ? row & 1 : (row & 1) * 4)) << 4);
-        };
-        auto w_at = [&](int row, int chunk) { return static_cast<uint32_t>(S::kXStage + row * S::kPiece * 2) + ((chunk ^ (row & 1) * 4) << 4); };
-        auto load = [&](int p) {
-          const uint32_t to = base + (p - p0) % kStages * S::kStage;
-          const int k0 = p * S::kPiece;
-          for (int i = tid; i < kTile * x_chunks; i += kThreads) {
-            const int row = i / x_chunks, chunk = i % x_chunks, of = s_row[row], k = k0 + chunk * 16 / x_size;
-            const bool there = of >= 0 && k < id;
-            copy16(to + x_at(row, chunk), there ? x + (of * t.x_row + k) * x_size : x, there);
-          }
-          for (int i = tid; i < min(r16 - r0, kRankPass) * (S::kPiece / 8); i += kThreads) {
-            const int row = i / (S::kPiece / 8), chunk = i % (S::kPiece / 8), k = k0 + 8 * chunk;
-            const bool there = row < ranks && k < id;
-            copy16(to + w_at(row, chunk), there ? down + static_cast<int64_t>(r0 + row) * id + k : down, there);
-          }
-        };
+  for (int r0 = 0; r0 < r; r0 += kRankPass) {
+    const int ranks = min(r - r0, kRankPass);
+    float acc[kRankPass / 16][S::kColumns][4] = {};
+    auto load = [&](int p) {
+      const uint32_t to = base + (p - p0) % kStages * stage_bytes;
+      const int k0 = p * S::kPiece;
+      for (int i = tid; i < kTile << x_chunks_log2; i += kThreads) {
+        const int row = i >> x_chunks_log2, chunk = i & ((1 << x_chunks_log2) - 1), of = s_row[row], k = k0 + chunk * 16 / x_size;
+        const bool there = of >= 0 && k < id;
+        copy16(to + x_at(row, chunk), there ? x + (of * t.x_row + k) * x_size : x, there);
+      }
+      for (int i = tid; i < min(r16 - r0, kRankPass) * (S::kPiece / 8); i += kThreads) {
+        const int row = i / (S::kPiece / 8), chunk = i % (S::kPiece / 8), k = k0 + 8 * chunk;
+        const bool there = row < ranks && k < id;
+        copy16(to + w_at(row, chunk), there ? down + static_cast<int64_t>(r0 + row) * id + k : down, there);
+      }
+    };
 #pragma unroll
-        for (int p = 0; p < kStages - 1; ++p) {
-          if (p0 + p < p1) load(p0 + p);
-          copies_commit();
-        }
-        for (int p = p0; p < p1; ++p) {
-          copies_wait<kStages - 2>();
-          __syncthreads();
-          if (p + kStages - 1 < p1) load(p + kStages - 1);
-          copies_commit();
-          if (tokens0 >= n) continue;
-          const unsigned char *stage = smem + (p - p0) % kStages * S::kStage;
-          Terms xt[S::kColumns][4];
+    for (int p = 0; p < kStages - 1; ++p) {
+      if (p0 + p < p1) load(p0 + p);
+      copies_commit();
+    }
+    for (int p = p0; p < p1; ++p) {
+      copies_wait<kStages - 2>();
+      __syncthreads();
+      if (p + kStages - 1 < p1) load(p + kStages - 1);
+      copies_commit();
+      if (tokens0 >= n) continue;
+      const unsigned char *stage = smem + (p - p0) % kStages * stage_bytes;
+      Terms xt[S::kColumns][4];
 #pragma unroll
-          for (int j = 0; j < S::kColumns; ++j) {
-            const int row = tokens0 + 8 * j + g, chunk = (32 * slot + 8 * c) * x_size / 16;
-            const uint4 lo = *reinterpret_cast<const uint4 *>(stage + x_at(row, chunk));
-            const uint4 hi = x_size == 4 ? *reinterpret_cast<const uint4 *>(stage + x_at(row, chunk + 1)) : zero4();
-            split8(xt[j], lo, hi, t.x_type);
-          }
-#pragma unroll
-          for (int m = 0; m < kRankPass / 16; ++m) {
-            if (16 * m >= ranks) break;
-            Weights8<W> u, v;
-            u.set(*reinterpret_cast<const uint4 *>(stage + w_at(16 * m + g, 4 * slot + c)));
-            v.set(*reinterpret_cast<const uint4 *>(stage + w_at(16 * m + 8 + g, 4 * slot + c)));
-#pragma unroll
-            for (int j = 0; j < S::kColumns; ++j) product<W>(acc[m][j], u, v, xt[j]);
-          }
-        }
-        copies_wait<0>();
-        __syncthreads();
-      } else {
-        const int of = s_row[tokens0 + g];
-        const unsigned char *row = x + max(of, 0) * t.x_row * x_size;
-        const int s0 = p0 * S::kSplit + slot, s1 = p1 * S::kSplit;
-        for (int step = s0; step < s1; step += S::kSplit) {
-          const int k = 32 * step + 8 * c;
-          const bool in = k < id;
-          uint4 raw[kRankPass / 16][2], lo = zero4(), hi = zero4();
-#pragma unroll
-          for (int m = 0; m < kRankPass / 16; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int at = 16 * m + 8 * h + g;
-              raw[m][h] = in && at < ranks ? __ldg(reinterpret_cast<const uint4 *>(down + static_cast<int64_t>(r0 + at) * id + k)) : zero4();
-            }
-          if (in && of >= 0) {
-            lo = __ldg(reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(k) * x_size));
-            if (x_size == 4) hi = __ldg(reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(k) * x_size) + 1);
-          }
-          Terms xt[4];
-          split8(xt, lo, hi, t.x_type);
-#pragma unroll
-          for (int m = 0; m < kRankPass / 16; ++m) {
-            if (16 * m >= ranks) break;
-            Weights8<W> u, v;
-            u.set(raw[m][0]), v.set(raw[m][1]);
-            product<W>(acc[m][0], u, v, xt);
-          }
-        }
-        if (r0) __syncthreads();
+      for (int j = 0; j < S::kColumns; ++j) {
+        const int row = tokens0 + 8 * j + g, chunk = (32 * slot + 8 * c) * x_size / 16;
+        const uint4 lo = *reinterpret_cast<const uint4 *>(stage + x_at(row, chunk));
+        const uint4 hi = x_size == 4 ? *reinterpret_cast<const uint4 *>(stage + x_at(row, chunk + 1)) : zero4();
+        split8(xt[j], lo, hi, t.x_type);
       }
 #pragma unroll
       for (int m = 0; m < kRankPass / 16; ++m) {
         if (16 * m >= ranks) break;
+        Weights8<W> u, v;
+        u.set(*reinterpret_cast<const uint4 *>(stage + w_at(16 * m + g, 4 * slot + c)));
+        v.set(*reinterpret_cast<const uint4 *>(stage + w_at(16 * m + 8 + g, 4 * slot + c)));
 #pragma unroll
-        for (int j = 0; j < S::kColumns; ++j) {
-          float *to = part + (slot * kRankPass + 16 * m + g) * kTile + tokens0 + 8 * j + 2 * c;
-          *reinterpret_cast<float2 *>(to) = make_float2(acc[m][j][0], acc[m][j][1]);
-          *reinterpret_cast<float2 *>(to + 8 * kTile) = make_float2(acc[m][j][2], acc[m][j][3]);
-        }
+        for (int j = 0; j < S::kColumns; ++j) product<W>(acc[m][j], u, v, xt[j]);
       }
-      __syncthreads();
-      for (int e = tid; e < min(r16 - r0, kRankPass) * kTile; e += kThreads) {
-        float s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < S::kSplit; ++k) s += part[k * kRankPass * kTile + e];
-        mine[r0 * kTile + e] = s;
-      }
-      if (S::kStaged || r0 + kRankPass >= r) __syncthreads();  // (part makes room)
     }
-  }
-  for (int k = tid; k < kTerms * kTile * pitch; k += kThreads) terms[k] = 0;  // (ranks past r)
-  cluster_sync();
-  // joined over the cluster: each CTA adds up a share of the pairs of ranks and
-  // sends it to all
-  for (int e = rank * kThreads + tid; e < r16 / 2 * kTile; e += kCtas * kThreads) {
-    const int pair = e / kTile, token = e % kTile;
-    float s0 = 0.0f, s1 = 0.0f, v0[kCtas], v1[kCtas];
-#pragma unroll
-    for (int k = 0; k < kCtas; ++k) {
-      const uint32_t from = mapa_shared(smem_addr(mine + 2 * pair * kTile + token), k);
-      v0[k] = ld_cluster(from), v1[k] = ld_cluster(from + 4 * kTile);
-    }
-#pragma unroll
-    for (int k = 0; k < kCtas; ++k) s0 += v0[k], s1 += v1[k];
-    const Terms sum = split(s0 * scale, s1 * scale);
-#pragma unroll
-    for (int k = 0; k < kCtas; ++k) {
-      const uint32_t to = mapa_shared(smem_addr(terms + token * pitch + pair), k);
-#pragma unroll
-      for (int i = 0; i < kTerms; ++i) st_cluster(to + 4 * i * kTile * pitch, sum.w[i]);
-    }
+    copies_wait<0>();
+    __syncthreads();
+    put_part<kTile>(part, acc, ranks, slot, tokens0);
+    __syncthreads();
+    add_up<kTile>(mine, part, r0, r16);
+    __syncthreads();  // (part makes room)
   }
   cluster_sync();
+  const int pitch = pitch_of(rmax), pairs = (r + 31) / 32 * 16;  // (zeros up to whole steps of the second product)
+  uint32_t *to = a.terms + static_cast<int64_t>(tile) * kTerms * kTile * pitch;
+  for (int e = rank * kThreads + tid; e < pairs * kTile; e += kCtas * kThreads) {
+    const int pair = e % pairs, token = e / pairs;
+    Terms sum = {};
+    if (2 * pair < r16) sum = joined<kTile>(mine, pair, token, k_tile.scale);
+#pragma unroll
+    for (int i = 0; i < kTerms; ++i) to[(i * kTile + token) * pitch + pair] = sum.w[i];
+  }
+  // (a CTA stays until the others have read its sums)
+  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+}
 
-  // the second product: 32 output columns of a warp at a time, of which a lane
-  // has four that lie together (rows g and g + 8 of two blocks of 16)
+// The second product: a CTA takes 512 output columns of a tile, a warp 32 at a
+// time.  HBM bound (y in, out out).
+constexpr int kUpColumns = 512;
+template <class W, int kTile>
+__global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_constant__ LoraArgs a) {
+  extern __shared__ __align__(128) uint32_t terms[];
+  __shared__ int s_row[kTile];
+  const mmq_lora_args &t = a.t;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int tile = a.by_chunks(static_cast<int>(blockIdx.x)), chunk = static_cast<int>(blockIdx.x) - tile * a.chunks;
+  const bool in_place = t.y == t.out;
+  // (the first product's kernel lets this one begin when everything before it is
+  // done, so that all but the terms may be read before the wait)
+  const Tile k_tile = tile_at(t, tile, in_place);
+  const bool none = k_tile.n == 0;
+  const int n = k_tile.n, r = k_tile.rank, od = static_cast<int>(t.od), rmax = t.rank;
+  const int o0 = chunk * kUpColumns, o1 = min(o0 + kUpColumns, od);
+  if (!none && tid < kTile) s_row[tid] = tid < n ? t.plan[kHead + k_tile.first + tid] : -1;
+  __syncthreads();
   constexpr int kEach = kTile < 32 ? kTile / 8 : 4;  // columns of eight tokens at once
-  const int columns = (n + 7) / 8;
-  for (int u = u0 + warp; u < u1; u += kWarps) {
-    const int o = 32 * u + 4 * g;
-    for (int j0 = 0; j0 < columns; j0 += kEach) {
-      float4 y[kEach][2];
-      int at[kEach][2];
+  const W *up = static_cast<const W *>(t.b) + static_cast<int64_t>(max(k_tile.adapter, 0)) * od * rmax;
+  float4 y[kEach][2];
+  auto fetch = [&](int o, int k0) {
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) {
+    for (int j = 0; j < kEach; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = 8 * (j0 + j) + 2 * c + h;
-          at[j][h] = k < n ? s_row[k] : -1;
-          y[j][h] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (at[j][h] < 0 || o >= od) continue;
-          const float *from = t.y + at[j][h] * t.y_row + o;
-          if (a.wide) {
-            y[j][h] = __ldcs(reinterpret_cast<const float4 *>(from));
-          } else {
-            y[j][h].x = from[0];
-            if (o + 1 < od) y[j][h].y = from[1];
-            if (o + 2 < od) y[j][h].z = from[2];
-            if (o + 3 < od) y[j][h].w = from[3];
-          }
-        }
-      }
+      for (int h = 0; h < 2; ++h) y[j][h] = load_y(a, s_row[k0 + 8 * j + 2 * c + h], o);
+  };
+  const int first = o0 + 32 * warp + 4 * g;
+  if (!none && r > 0) fetch(first, 0);
+  griddep_wait();
+  griddep_launch_dependents();
+  if (none) return;
+  if (r == 0) {
+    if (!in_place) copy_rows(a, s_row, n, o0, o1);
+    return;
+  }
+  const int pitch = pitch_of(rmax), words = (r + 31) / 32 * 16;
+  const uint32_t *from = a.terms + static_cast<int64_t>(tile) * kTerms * kTile * pitch;
+  const int pieces = words / 4;  // of 16 bytes, of a row
+  for (int i = tid; i < kTerms * kTile * pieces; i += kThreads) {
+    const int row = i / pieces, at = row * pitch + 4 * (i - row * pieces);
+    copy16(smem_addr(terms + at), from + at, true);
+  }
+  copies_commit();
+  copies_wait<0>();
+  __syncthreads();
+  for (int b = o0 + 32 * warp; b < o1; b += 32 * kWarps) {
+    const int o = b + 4 * g;
+    for (int k0 = 0; k0 < n; k0 += 8 * kEach) {
+      if (o != first || k0 > 0) fetch(o, k0);
       float acc[2][kEach][4] = {};
-      for (int r0 = 0; r0 < r32; r0 += 32) {
-        const int k = r0 + 8 * c;
-        Weights8<W> w[4];
+      expand<W, kEach>(acc, a, up, terms, kTile * pitch, pitch, r, o, k0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 raw = zero4();
-          if (k < r && o + i < od) raw = __ldg(reinterpret_cast<const uint4 *>(up + static_cast<int64_t>(o + i) * rmax + k));
-          if (k < r && k + 8 > r) {  // columns past the rank
-            uint32_t *v = &raw.x;
+      for (int j = 0; j < kEach; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] &= k + 2 * e + 1 < r ? 0xffffffffu : k + 2 * e < r ? 0xffffu : 0u;
-          }
-          w[i].set(raw);
-        }
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-          Terms x[4];
-#pragma unroll
-          for (int i = 0; i < kTerms; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(terms + (i * kTile + 8 * (j0 + j) + g) * pitch + k / 2);
-            x[0].w[i] = v.x, x[1].w[i] = v.y, x[2].w[i] = v.z, x[3].w[i] = v.w;
-          }
-          product<W>(acc[0][j], w[0], w[1], x);
-          product<W>(acc[1][j], w[2], w[3], x);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (at[j][h] < 0 || o >= od) continue;
-          const float4 v = make_float4(y[j][h].x + acc[0][j][h], y[j][h].y + acc[0][j][h + 2], y[j][h].z + acc[1][j][h], y[j][h].w + acc[1][j][h + 2]);
-          float *to = t.out + at[j][h] * t.out_row + o;
-          if (a.wide) {
-            *reinterpret_cast<float4 *>(to) = v;
-          } else {
-            to[0] = v.x;
-            if (o + 1 < od) to[1] = v.y;
-            if (o + 2 < od) to[2] = v.z;
-            if (o + 3 < od) to[3] = v.w;
-          }
-        }
-      }
+        for (int h = 0; h < 2; ++h) store_out(a, s_row[k0 + 8 * j + 2 * c + h], o, sum_of<kEach>(acc, j, h, y[j][h]));
     }
   }
 }
@@ -627,22 +767,52 @@ int64_t most_tiles(int64_t ntok, int64_t nreq, int64_t nadapters) {
   return std::min(ntok, ntok / tile_of(ntok, nreq, nadapters) + std::min(nreq, nadapters + 1));
 }
 
-template <class W, int kTile>
-cudaError_t launch_with(const LoraArgs &a, cudaStream_t s) {
-  const size_t smem = Shape<kTile>::bytes(a.t.rank);
-  const cudaError_t e = cudaFuncSetAttribute(lora_kernel<W, kTile>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  const int64_t tiles = most_tiles(a.t.ntok, a.t.nreq, a.t.nadapters);
-  return launch_early(lora_kernel<W, kTile>, static_cast<unsigned>(tiles * kCtas), 1, kThreads, smem, s, a);
+template <class K>
+cudaError_t allow(K kernel, size_t smem) {
+  if (smem <= 46 * 1024) return cudaSuccess;  // (beside the static arrays, within the 48 KB that need no leave)
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
 }
 
 template <class W>
-cudaError_t launch_of(const LoraArgs &a, cudaStream_t s) {
+cudaError_t launch_few(const LoraArgs &a, cudaStream_t s) {
+  const size_t smem = few_front(a.t.rank) + 4 * static_cast<size_t>(up16(a.t.rank)) * kFew;
+  const cudaError_t e = allow(lora_few_kernel<W>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_early(lora_few_kernel<W>, static_cast<unsigned>(most_tiles(a.t.ntok, a.t.nreq, a.t.nadapters) * kCtas), 1, kThreads, smem, s, a);
+}
+
+template <class W, int kTile>
+cudaError_t launch_with(LoraArgs a, const CallContext &ctx, cudaStream_t s) {
+  using S = Shape<kTile>;
+  const int64_t tiles = most_tiles(a.t.ntok, a.t.nreq, a.t.nadapters), pitch = pitch_of(a.t.rank);
+  const int64_t chunks = (a.t.od + kUpColumns - 1) / kUpColumns;
+  if (tiles * chunks > 0x7fffffff) return cudaErrorNotSupported;
+  a.chunks = static_cast<int>(chunks), a.by_chunks = FastDiv(a.chunks);
+  const int x_size = a.t.x_type == MMQ_DT_F32 ? 4 : 2, ranks = std::min(up16(a.t.rank), kRankPass);
+  a.front = std::max(kStages * S::kPiece * (kTile * x_size + ranks * 2), 4 * S::kSplit * kRankPass * kTile);
+  const size_t down = a.front + 4 * static_cast<size_t>(up16(a.t.rank)) * kTile, up = 4 * kTerms * kTile * pitch;
+  cudaError_t e = allow(lora_down_kernel<W, kTile>, down);
+  if (e == cudaSuccess) e = allow(lora_up_kernel<W, kTile>, up);
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (e == cudaSuccess) e = cudaStreamIsCapturing(s, &cap);
+  if (e != cudaSuccess) return e;
+  void *scratch = nullptr;
+  e = cap == cudaStreamCaptureStatusActive ? cudaMallocAsync(&scratch, tiles * up, s) : cudaMallocFromPoolAsync(&scratch, tiles * up, ctx.pool, s);
+  if (e != cudaSuccess) return e;
+  a.terms = static_cast<uint32_t *>(scratch);
+  e = launch_early(lora_down_kernel<W, kTile>, static_cast<unsigned>(tiles * kCtas), 1, kThreads, down, s, a);
+  if (e == cudaSuccess) e = launch_early(lora_up_kernel<W, kTile>, static_cast<unsigned>(tiles * chunks), 1, kThreads, up, s, a);
+  const cudaError_t ef = cudaFreeAsync(scratch, s);
+  return e != cudaSuccess ? e : ef;
+}
+
+template <class W>
+cudaError_t launch_of(const LoraArgs &a, const CallContext &ctx, cudaStream_t s) {
   switch (tile_of(a.t.ntok, a.t.nreq, a.t.nadapters)) {
-    case 8: return launch_with<W, 8>(a, s);
-    case 16: return launch_with<W, 16>(a, s);
-    case 32: return launch_with<W, 32>(a, s);
-    default: return launch_with<W, 64>(a, s);
+    case 8: return launch_few<W>(a, s);
+    case 16: return launch_with<W, 16>(a, ctx, s);
+    case 32: return launch_with<W, 32>(a, ctx, s);
+    default: return launch_with<W, 64>(a, ctx, s);
   }
 }
 
@@ -664,11 +834,11 @@ cudaError_t launch_lora_plan(LoraPlanArgs a, cudaStream_t s) {
   return launch_early(lora_plan_kernel, static_cast<unsigned>(ctas), 1, kPlanThreads, smem, s, a);
 }
 
-cudaError_t launch_lora(LoraArgs a, cudaStream_t s) {
+cudaError_t launch_lora(LoraArgs a, const CallContext &ctx, cudaStream_t s) {
   const mmq_lora_args &t = a.t;
   auto whole = [](const void *p, int64_t row) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row % 4 == 0; };
   a.wide = t.od % 4 == 0 && whole(t.y, t.y_row) && whole(t.out, t.out_row);
-  return t.type == MMQ_DT_F16 ? launch_of<__half>(a, s) : launch_of<__nv_bfloat16>(a, s);
+  return t.type == MMQ_DT_F16 ? launch_of<__half>(a, ctx, s) : launch_of<__nv_bfloat16>(a, ctx, s);
 }
 
 }  // namespace mmq

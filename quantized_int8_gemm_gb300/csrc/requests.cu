@@ -206,7 +206,7 @@ int mmq_lora(const mmq_lora_args *args, mmq_stream_t stream) {
   mmq::LoraArgs a;
   a.t = t;
   if (t.ntok == 1) a.t.x_row = 0, a.t.y_row = 0, a.t.out_row = 0;
-  return cuda_rc(mmq::launch_lora(a, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_rc(mmq::launch_lora(a, ctx, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
