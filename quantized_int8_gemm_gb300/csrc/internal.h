@@ -240,7 +240,8 @@ int64_t lora_plan_words(int64_t ntok, int64_t nreq, int64_t nadapters);
 struct LoraArgs {
   mmq_lora_args t;
   bool wide;              // rows of y and out in 16-byte pieces
-  int32_t front, chunks;  // bytes of the first product's stages; CTAs of a tile in the second
+  int32_t front;          // bytes of the first product's stages
+  int32_t columns, chunks;  // of a CTA in the second product; CTAs of a tile
   FastDiv by_chunks;
   uint32_t *terms;        // what the first leaves for the second
 };

@@ -212,6 +212,9 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
@@ -621,28 +624,45 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lor
   // quarter of eight (x in fp32) or half of them off, so that eight lanes of a
   // read touch every bank once.
   const uint32_t base = smem_addr(smem);
-  const int x_chunks_log2 = S::kPiece == 64 ? (x_size == 4 ? 4 : 3) : (x_size == 4 ? 5 : 4);  // of a row
   auto x_at = [&](int row, int chunk) {
     return static_cast<uint32_t>(row * S::kPiece * x_size) + ((chunk ^ (x_size == 4 ? row & 1 : (row & 1) * 4)) << 4);
   };
   auto w_at = [&](int row, int chunk) { return static_cast<uint32_t>(x_stage + row * S::kPiece * 2) + ((chunk ^ (row & 1) * 4) << 4); };
   __syncthreads();
+  // This thread's copies of every stage: rows x_rows apart of one chunk of x,
+  // rows w_rows apart of one of the weights; k is the first column of its chunk.
+  const int x_chunks = S::kPiece * x_size / 16, x_rows = kThreads / x_chunks, x_row0 = tid / x_chunks, x_chunk = tid % x_chunks;
+  constexpr int kWChunks = S::kPiece / 8, kWRows = kThreads / kWChunks;
+  constexpr int kXCopies = kTile * S::kPiece * 4 / 16 / kThreads, kWCopies = kRankPass / kWRows;
+  const int w_row0 = tid / kWChunks, w_chunk = tid % kWChunks;
+  const unsigned char *x_from[kXCopies];
+  uint32_t x_there = 0;
+#pragma unroll
+  for (int u = 0; u < kXCopies; ++u) {
+    const int row = x_row0 + u * x_rows, of = row < kTile ? s_row[row] : -1;
+    x_from[u] = x + (max(of, 0) * t.x_row + x_chunk * 16 / x_size) * x_size;
+    x_there |= of >= 0 ? 1u << u : 0;
+  }
   for (int r0 = 0; r0 < r; r0 += kRankPass) {
     const int ranks = min(r - r0, kRankPass);
     float acc[kRankPass / 16][S::kColumns][4] = {};
+    const W *w_from = down + static_cast<int64_t>(r0 + w_row0) * id + 8 * w_chunk;
     auto load = [&](int p) {
       const uint32_t to = base + (p - p0) % kStages * stage_bytes;
       const int k0 = p * S::kPiece;
-      for (int i = tid; i < kTile << x_chunks_log2; i += kThreads) {
-        const int row = i >> x_chunks_log2, chunk = i & ((1 << x_chunks_log2) - 1), of = s_row[row], k = k0 + chunk * 16 / x_size;
-        const bool there = of >= 0 && k < id;
-        copy16(to + x_at(row, chunk), there ? x + (of * t.x_row + k) * x_size : x, there);
-      }
-      for (int i = tid; i < min(r16 - r0, kRankPass) * (S::kPiece / 8); i += kThreads) {
-        const int row = i / (S::kPiece / 8), chunk = i % (S::kPiece / 8), k = k0 + 8 * chunk;
-        const bool there = row < ranks && k < id;
-        copy16(to + w_at(row, chunk), there ? down + static_cast<int64_t>(r0 + row) * id + k : down, there);
-      }
+      const bool x_in = k0 + x_chunk * 16 / x_size < id, w_in = k0 + 8 * w_chunk < id;
+#pragma unroll
+      for (int u = 0; u < kXCopies; ++u)
+        if (x_row0 + u * x_rows < kTile) {
+          const bool there = x_in && (x_there >> u & 1);
+          copy16(to + x_at(x_row0 + u * x_rows, x_chunk), there ? x_from[u] + static_cast<int64_t>(k0) * x_size : x, there);
+        }
+#pragma unroll
+      for (int u = 0; u < kWCopies; ++u)
+        if (w_row0 + u * kWRows < min(r16 - r0, kRankPass)) {
+          const bool there = w_in && w_row0 + u * kWRows < ranks;
+          copy16(to + w_at(w_row0 + u * kWRows, w_chunk), there ? w_from + static_cast<int64_t>(u * kWRows) * id + k0 : down, there);
+        }
     };
 #pragma unroll
     for (int p = 0; p < kStages - 1; ++p) {
@@ -695,11 +715,11 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lor
   asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
-// The second product: a CTA takes 512 output columns of a tile, a warp 32 at a
-// time.  HBM bound (y in, out out).
-constexpr int kUpColumns = 512;
+// The second product: a CTA takes a.columns output columns of a tile, a warp 32 of
+// them and 16 tokens at a time, the next ones' y on its way.  HBM bound (y in, out out).
+constexpr int kYPieces = 3;
 template <class W, int kTile>
-__global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_constant__ LoraArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) lora_up_kernel(const __grid_constant__ LoraArgs a) {
   extern __shared__ __align__(128) uint32_t terms[];
   __shared__ int s_row[kTile];
   const mmq_lora_args &t = a.t;
@@ -711,20 +731,46 @@ __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_const
   const Tile k_tile = tile_at(t, tile, in_place);
   const bool none = k_tile.n == 0;
   const int n = k_tile.n, r = k_tile.rank, od = static_cast<int>(t.od), rmax = t.rank;
-  const int o0 = chunk * kUpColumns, o1 = min(o0 + kUpColumns, od);
+  const int o0 = chunk * a.columns, o1 = min(o0 + a.columns, od);
   if (!none && tid < kTile) s_row[tid] = tid < n ? t.plan[kHead + k_tile.first + tid] : -1;
   __syncthreads();
-  constexpr int kEach = kTile < 32 ? kTile / 8 : 4;  // columns of eight tokens at once
+  constexpr int kEach = 2;  // columns of eight tokens at once
+  const int pitch = pitch_of(rmax);
   const W *up = static_cast<const W *>(t.b) + static_cast<int64_t>(max(k_tile.adapter, 0)) * od * rmax;
-  float4 y[kEach][2];
-  auto fetch = [&](int o, int k0) {
+  // Piece i of the warp: columns from 32 (i / steps) kWarps on, tokens from 16
+  // (i % steps) on.  Each thread copies what it needs of y itself, some pieces
+  // ahead, to places that no other reads: [piece in flight][part][thread].
+  const int steps = (n + 8 * kEach - 1) / (8 * kEach), first = o0 + 32 * warp;
+  const int pieces = first < o1 && r > 0 ? (o1 - first + 32 * kWarps - 1) / (32 * kWarps) * steps : 0;
+  float4 *const y = reinterpret_cast<float4 *>(terms + kTerms * kTile * pitch) + tid;
+  auto fetch = [&](int i, int o, int k0) {
+    o += 4 * g;
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) y[j][h] = load_y(a, s_row[k0 + 8 * j + 2 * c + h], o);
+      for (int h = 0; h < 2; ++h) {
+        const int row = s_row[k0 + 8 * j + 2 * c + h];
+        if (row < 0 || o >= od) continue;
+        const float *src = t.y + row * t.y_row + o;
+        const uint32_t to = smem_addr(y + (i % kYPieces * 2 * kEach + 2 * j + h) * kThreads);
+        if (a.wide) {
+          copy16(to, src, true);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (o + e < od) copy4(to + 4 * e, src + e);
+        }
+      }
   };
-  const int first = o0 + 32 * warp + 4 * g;
-  if (!none && r > 0) fetch(first, 0);
+  int ahead_o = first, ahead_k = 0;
+  auto fetch_next = [&](int i) {
+    if (i < pieces) fetch(i, ahead_o, ahead_k);
+    copies_commit();
+    ahead_k += 8 * kEach;
+    if (ahead_k >= n) ahead_k = 0, ahead_o += 32 * kWarps;
+  };
+#pragma unroll
+  for (int i = 0; i < kYPieces - 1; ++i) fetch_next(i);
   griddep_wait();
   griddep_launch_dependents();
   if (none) return;
@@ -732,28 +778,31 @@ __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_const
     if (!in_place) copy_rows(a, s_row, n, o0, o1);
     return;
   }
-  const int pitch = pitch_of(rmax), words = (r + 31) / 32 * 16;
+  const int words = (r + 31) / 32 * 16;
   const uint32_t *from = a.terms + static_cast<int64_t>(tile) * kTerms * kTile * pitch;
-  const int pieces = words / 4;  // of 16 bytes, of a row
-  for (int i = tid; i < kTerms * kTile * pieces; i += kThreads) {
-    const int row = i / pieces, at = row * pitch + 4 * (i - row * pieces);
+  const int chunks = words / 4;  // of 16 bytes, of a row
+  for (int i = tid; i < kTerms * kTile * chunks; i += kThreads) {
+    const int row = i / chunks, at = row * pitch + 4 * (i - row * chunks);
     copy16(smem_addr(terms + at), from + at, true);
   }
   copies_commit();
   copies_wait<0>();
   __syncthreads();
-  for (int b = o0 + 32 * warp; b < o1; b += 32 * kWarps) {
-    const int o = b + 4 * g;
-    for (int k0 = 0; k0 < n; k0 += 8 * kEach) {
-      if (o != first || k0 > 0) fetch(o, k0);
-      float acc[2][kEach][4] = {};
-      expand<W, kEach>(acc, a, up, terms, kTile * pitch, pitch, r, o, k0);
+  int o = first, k0 = 0;
+  for (int i = 0; i < pieces; ++i) {
+    fetch_next(i + kYPieces - 1);
+    float acc[2][kEach][4] = {};
+    expand<W, kEach>(acc, a, up, terms, kTile * pitch, pitch, r, o + 4 * g, k0);
+    copies_wait<kYPieces - 1>();
 #pragma unroll
-      for (int j = 0; j < kEach; ++j)
+    for (int j = 0; j < kEach; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) store_out(a, s_row[k0 + 8 * j + 2 * c + h], o, sum_of<kEach>(acc, j, h, y[j][h]));
-    }
+      for (int h = 0; h < 2; ++h)
+        store_out(a, s_row[k0 + 8 * j + 2 * c + h], o + 4 * g, sum_of<kEach>(acc, j, h, y[(i % kYPieces * 2 * kEach + 2 * j + h) * kThreads]));
+    k0 += 8 * kEach;
+    if (k0 >= n) k0 = 0, o += 32 * kWarps;
   }
+  copies_wait<0>();
 }
 
 // Tokens of a tile: as many as an adapter has on the average, at the most 64,
@@ -785,19 +834,23 @@ template <class W, int kTile>
 cudaError_t launch_with(LoraArgs a, const CallContext &ctx, cudaStream_t s) {
   using S = Shape<kTile>;
   const int64_t tiles = most_tiles(a.t.ntok, a.t.nreq, a.t.nadapters), pitch = pitch_of(a.t.rank);
-  const int64_t chunks = (a.t.od + kUpColumns - 1) / kUpColumns;
+  // columns of a CTA in the second product: many, as what it needs beside y and
+  // out comes once, but CTAs for four rounds of the SMs
+  const int64_t want = a.t.od * tiles / (4 * 3 * 152);
+  a.columns = static_cast<int>(std::min<int64_t>(2048, std::max<int64_t>(256, want / 256 * 256)));
+  const int64_t chunks = (a.t.od + a.columns - 1) / a.columns;
   if (tiles * chunks > 0x7fffffff) return cudaErrorNotSupported;
   a.chunks = static_cast<int>(chunks), a.by_chunks = FastDiv(a.chunks);
   const int x_size = a.t.x_type == MMQ_DT_F32 ? 4 : 2, ranks = std::min(up16(a.t.rank), kRankPass);
   a.front = std::max(kStages * S::kPiece * (kTile * x_size + ranks * 2), 4 * S::kSplit * kRankPass * kTile);
-  const size_t down = a.front + 4 * static_cast<size_t>(up16(a.t.rank)) * kTile, up = 4 * kTerms * kTile * pitch;
+  const size_t down = a.front + 4 * static_cast<size_t>(up16(a.t.rank)) * kTile, left = 4 * kTerms * kTile * pitch, up = left + kYPieces * 4 * 16 * kThreads;
   cudaError_t e = allow(lora_down_kernel<W, kTile>, down);
   if (e == cudaSuccess) e = allow(lora_up_kernel<W, kTile>, up);
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (e == cudaSuccess) e = cudaStreamIsCapturing(s, &cap);
   if (e != cudaSuccess) return e;
   void *scratch = nullptr;
-  e = cap == cudaStreamCaptureStatusActive ? cudaMallocAsync(&scratch, tiles * up, s) : cudaMallocFromPoolAsync(&scratch, tiles * up, ctx.pool, s);
+  e = cap == cudaStreamCaptureStatusActive ? cudaMallocAsync(&scratch, tiles * left, s) : cudaMallocFromPoolAsync(&scratch, tiles * left, ctx.pool, s);
   if (e != cudaSuccess) return e;
   a.terms = static_cast<uint32_t *>(scratch);
   e = launch_early(lora_down_kernel<W, kTile>, static_cast<unsigned>(tiles * kCtas), 1, kThreads, down, s, a);
