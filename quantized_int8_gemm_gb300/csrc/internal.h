@@ -244,6 +244,7 @@ struct LoraArgs {
   int32_t columns, chunks;  // of a CTA in the second product; CTAs of a tile
   FastDiv by_chunks;
   uint32_t *terms;        // what the first leaves for the second
+  uint32_t zero = 0;
 };
 cudaError_t launch_lora(LoraArgs a, const CallContext &ctx, cudaStream_t s);
 

@@ -197,7 +197,6 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const __grid_co
 
 // ---------------------------------------------------------------- products
 constexpr int kCtas = 8, kThreads = 256, kWarps = kThreads / 32;
-constexpr int kRankPass = 64;  // ranks whose sums a warp holds at once
 constexpr int kStages = 3;
 
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
@@ -296,11 +295,46 @@ __device__ __forceinline__ void product(float (&d)[4], const Weights8<W> &p, con
   }
 }
 
+// An operand of 16 rows of weights by 16 columns, as the tensor cores take it: a
+// lane's pairs of columns of rows p and q, in this order, as bf16 terms.  The
+// registers of one have to lie together: where they are those that a 16-byte
+// load has filled, each product copied them first (5 moves a product), so
+// they are made once.
+template <class W>
+struct Operand {
+  static constexpr int kParts = Weights8<W>::kParts;
+  uint32_t w[kParts][4];
+  // from pairs as loaded; zero: a 0 that the compiler does not know of
+  __device__ __forceinline__ void set(uint32_t p0, uint32_t q0, uint32_t p1, uint32_t q1, uint32_t zero) {
+    const uint32_t v[4] = {p0, q0, p1, q1};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kParts == 1) {
+        w[0][i] = v[i] ^ zero;
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v[i]));
+        w[0][i] = pack(f.x, f.y);
+        w[kParts - 1][i] = pack(f.x - low(w[0][i]), f.y - high(w[0][i]));
+      }
+    }
+  }
+};
+template <class W>
+__device__ __forceinline__ void product(float (&d)[4], const Operand<W> &a, const Terms &x0, const Terms &x1) {
+#pragma unroll
+  for (int order = kTerms - 1; order >= 0; --order) {
+#pragma unroll
+    for (int i = Operand<W>::kParts - 1; i >= 0; --i)
+      if (order - i >= 0) mma(d, a.w[i][0], a.w[i][1], a.w[i][2], a.w[i][3], x0.w[order - i], x1.w[order - i]);
+  }
+}
+
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0, 0, 0, 0); }
 
 // Eight numbers of x as terms, from 16 or 32 bytes (a and, if fp32, b).
+template <bool kFp32>
 __device__ __forceinline__ void split8(Terms (&out)[4], uint4 a, uint4 b, int x_type) {
-  if (x_type == MMQ_DT_F32) {
+  if constexpr (kFp32) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) out[i] = split(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
@@ -324,11 +358,11 @@ struct Shape {
 // The terms of the joined sums, of a tile: [term][token][pitch] words, a token's
 // ranks together, rows 16 words from a multiple of 32 apart (eight lanes of a
 // 16-byte read then touch every bank once).
-__host__ __device__ constexpr int pitch_of(int rank) { return (rank + 31) / 32 * 16 % 32 ? (rank + 31) / 32 * 16 : (rank + 31) / 32 * 16 + 16; }
+__host__ __device__ constexpr int pitch_of(int rank) { return rank <= 32 ? 16 : rank <= 64 ? 48 : 80; }
 __host__ __device__ constexpr int up16(int rank) { return (rank + 15) / 16 * 16; }
 
 __host__ __device__ constexpr int few_front(int rank) {  // bytes of the partial sums or the terms of eight tokens
-  const int part = 4 * kWarps * kRankPass * 8, terms = 4 * kTerms * 8 * pitch_of(rank);
+  const int part = 4 * kWarps * 64 * 8, terms = 4 * kTerms * 8 * pitch_of(rank);
   return part > terms ? part : terms;
 }
 
@@ -376,25 +410,25 @@ __device__ __forceinline__ void copy_rows(const LoraArgs &a, const int *s_row, i
 
 // Partial sums of the warps of a CTA, [split][rank of the pass][token], added up
 // in their order into the CTA's, [rank][token].
-template <int kTile>
+template <int kTile, int kPass>
 __device__ __forceinline__ void add_up(float *mine, const float *part, int r0, int r16) {
   using S = Shape<kTile>;
-  for (int e = threadIdx.x; e < min(r16 - r0, kRankPass) * kTile; e += kThreads) {
+  for (int e = threadIdx.x; e < min(r16 - r0, kPass) * kTile; e += kThreads) {
     float s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < S::kSplit; ++k) s += part[k * kRankPass * kTile + e];
+    for (int k = 0; k < S::kSplit; ++k) s += part[k * kPass * kTile + e];
     mine[r0 * kTile + e] = s;
   }
 }
-template <int kTile, int kColumns>
-__device__ __forceinline__ void put_part(float *part, const float (&acc)[kRankPass / 16][kColumns][4], int ranks, int slot, int tokens0) {
+template <int kTile, int kPass, int kColumns>
+__device__ __forceinline__ void put_part(float *part, const float (&acc)[kPass / 16][kColumns][4], int ranks, int slot, int tokens0) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
-  for (int m = 0; m < kRankPass / 16; ++m) {
+  for (int m = 0; m < kPass / 16; ++m) {
     if (16 * m >= ranks) break;
 #pragma unroll
     for (int j = 0; j < kColumns; ++j) {
-      float *to = part + (slot * kRankPass + 16 * m + g) * kTile + tokens0 + 8 * j + 2 * c;
+      float *to = part + (slot * kPass + 16 * m + g) * kTile + tokens0 + 8 * j + 2 * c;
       *reinterpret_cast<float2 *>(to) = make_float2(acc[m][j][0], acc[m][j][1]);
       *reinterpret_cast<float2 *>(to + 8 * kTile) = make_float2(acc[m][j][2], acc[m][j][3]);
     }
@@ -484,7 +518,7 @@ __device__ __forceinline__ float4 sum_of(const float (&acc)[2][kEach][4], int j,
 // columns by A, the sums are joined through the cluster's shared memory, and
 // each writes an eighth of the output columns.  HBM bound by the adapters with
 // many tiles, latency bound with few.
-constexpr int kFew = 8;
+constexpr int kFew = 8, kFewPass = 64;  // tokens; ranks whose sums a warp holds at once
 template <class W>
 __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCtas, 1, 1) lora_few_kernel(const __grid_constant__ LoraArgs a) {
   using S = Shape<kFew>;
@@ -526,15 +560,15 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCtas, 1, 1) lor
     const W *down = static_cast<const W *>(t.a) + static_cast<int64_t>(k_tile.adapter) * rmax * id;
     const int x_size = t.x_type == MMQ_DT_F32 ? 4 : 2, of = s_row[g];
     const unsigned char *row = static_cast<const unsigned char *>(t.x) + max(of, 0) * t.x_row * x_size;
-    for (int r0 = 0; r0 < r; r0 += kRankPass) {
-      const int ranks = min(r - r0, kRankPass);
-      float acc[kRankPass / 16][S::kColumns][4] = {};
+    for (int r0 = 0; r0 < r; r0 += kFewPass) {
+      const int ranks = min(r - r0, kFewPass);
+      float acc[kFewPass / 16][S::kColumns][4] = {};
       for (int step = p0 * S::kSplit + warp; step < p1 * S::kSplit; step += S::kSplit) {
         const int k = 32 * step + 8 * c;
         const bool in = k < id;
-        uint4 raw[kRankPass / 16][2], lo = zero4(), hi = zero4();
+        uint4 raw[kFewPass / 16][2], lo = zero4(), hi = zero4();
 #pragma unroll
-        for (int m = 0; m < kRankPass / 16; ++m)
+        for (int m = 0; m < kFewPass / 16; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int at = 16 * m + 8 * h + g;
@@ -545,9 +579,10 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCtas, 1, 1) lor
           if (x_size == 4) hi = __ldg(reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(k) * x_size) + 1);
         }
         Terms xt[4];
-        split8(xt, lo, hi, t.x_type);
+        if (x_size == 4) split8<true>(xt, lo, hi, t.x_type);
+        else split8<false>(xt, lo, hi, t.x_type);
 #pragma unroll
-        for (int m = 0; m < kRankPass / 16; ++m) {
+        for (int m = 0; m < kFewPass / 16; ++m) {
           if (16 * m >= ranks) break;
           Weights8<W> u, v;
           u.set(raw[m][0]), v.set(raw[m][1]);
@@ -555,9 +590,9 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCtas, 1, 1) lor
         }
       }
       if (r0) __syncthreads();
-      put_part<kFew>(part, acc, ranks, warp, 0);
+      put_part<kFew, kFewPass>(part, acc, ranks, warp, 0);
       __syncthreads();
-      add_up<kFew>(mine, part, r0, r16);
+      add_up<kFew, kFewPass>(mine, part, r0, r16);
     }
     __syncthreads();  // (part makes room)
   }
@@ -597,8 +632,8 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCtas, 1, 1) lor
 // The first product: a cluster takes a tile, each CTA an eighth of x's columns,
 // through stages of shared memory; the sums are joined through the cluster's
 // shared memory and left as terms.
-template <class W, int kTile>
-__global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lora_down_kernel(const __grid_constant__ LoraArgs a) {
+template <class W, int kTile, bool kFp32, int kPass>
+__global__ void __launch_bounds__(kThreads, kPass == 32 ? 3 : 2) __cluster_dims__(kCtas, 1, 1) lora_down_kernel(const __grid_constant__ LoraArgs a) {
   using S = Shape<kTile>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_row[kTile];
@@ -612,93 +647,118 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lor
   const int n = k_tile.n, r = k_tile.rank;
   if (r == 0) return;
   if (tid < kTile) s_row[tid] = tid < n ? t.plan[kHead + k_tile.first + tid] : -1;
-  const int id = static_cast<int>(t.id), rmax = t.rank, r16 = up16(r), stage_ranks = min(up16(rmax), kRankPass);
-  const int x_size = t.x_type == MMQ_DT_F32 ? 4 : 2, x_stage = kTile * S::kPiece * x_size, stage_bytes = x_stage + stage_ranks * S::kPiece * 2;
+  const int id = static_cast<int>(t.id), rmax = t.rank, r16 = up16(r), stage_ranks = min(up16(rmax), kPass);
+  constexpr int kSize = kFp32 ? 4 : 2, kXRow = S::kPiece * kSize, kWRow = S::kPiece * 2, kXStage = kTile * kXRow;  // bytes
+  const uint32_t stage_bytes = kXStage + stage_ranks * kWRow;
   float *part = reinterpret_cast<float *>(smem), *mine = reinterpret_cast<float *>(smem + a.front);
   const int pieces = (id + S::kPiece - 1) / S::kPiece, share = (pieces + kCtas - 1) / kCtas;
   const int p0 = min(rank * share, pieces), p1 = min(p0 + share, pieces);
   const int tokens0 = warp % S::kGroups * S::kTokens, slot = warp / S::kGroups;
   const W *down = static_cast<const W *>(t.a) + static_cast<int64_t>(k_tile.adapter) * rmax * id;
   const unsigned char *x = static_cast<const unsigned char *>(t.x);
-  // Pieces of x and of the weights in 16-byte chunks, the chunks of odd rows a
-  // quarter of eight (x in fp32) or half of them off, so that eight lanes of a
-  // read touch every bank once.
-  const uint32_t base = smem_addr(smem);
-  auto x_at = [&](int row, int chunk) {
-    return static_cast<uint32_t>(row * S::kPiece * x_size) + ((chunk ^ (x_size == 4 ? row & 1 : (row & 1) * 4)) << 4);
-  };
-  auto w_at = [&](int row, int chunk) { return static_cast<uint32_t>(x_stage + row * S::kPiece * 2) + ((chunk ^ (row & 1) * 4) << 4); };
+  // Pieces of x and of the weights in 16-byte chunks, moved about by their row so
+  // that the rows of a read do not meet in a bank.
+  auto x_at = [](int row, int chunk) { return static_cast<uint32_t>(row * kXRow + ((chunk ^ (kFp32 ? (row & 3) << 1 : row & 7)) << 4)); };
+  auto w_at = [](int row, int chunk) { return static_cast<uint32_t>(kXStage + row * kWRow + ((chunk ^ (row & 7)) << 4)); };
   __syncthreads();
-  // This thread's copies of every stage: rows x_rows apart of one chunk of x,
-  // rows w_rows apart of one of the weights; k is the first column of its chunk.
-  const int x_chunks = S::kPiece * x_size / 16, x_rows = kThreads / x_chunks, x_row0 = tid / x_chunks, x_chunk = tid % x_chunks;
-  constexpr int kWChunks = S::kPiece / 8, kWRows = kThreads / kWChunks;
-  constexpr int kXCopies = kTile * S::kPiece * 4 / 16 / kThreads, kWCopies = kRankPass / kWRows;
-  const int w_row0 = tid / kWChunks, w_chunk = tid % kWChunks;
+  // This thread's copies of every stage: rows kXRows apart of one chunk of x,
+  // rows kWRows apart of one of the weights.
+  constexpr int kXChunks = kXRow / 16, kXRows = kThreads / kXChunks, kXCopies = kTile / kXRows;
+  constexpr int kWChunks = kWRow / 16, kWRows = kThreads / kWChunks, kWCopies = kPass / kWRows;
+  static_assert(kXCopies * kXRows == kTile && kWCopies * kWRows == kPass, "a stage is whole rounds of the threads");
+  const int x_row = tid / kXChunks, x_k = tid % kXChunks * (16 / kSize), w_row = tid / kWChunks, w_k = tid % kWChunks * 8;
   const unsigned char *x_from[kXCopies];
-  uint32_t x_there = 0;
+  bool x_there[kXCopies];
 #pragma unroll
   for (int u = 0; u < kXCopies; ++u) {
-    const int row = x_row0 + u * x_rows, of = row < kTile ? s_row[row] : -1;
-    x_from[u] = x + (max(of, 0) * t.x_row + x_chunk * 16 / x_size) * x_size;
-    x_there |= of >= 0 ? 1u << u : 0;
+    const int of = s_row[x_row + u * kXRows];
+    x_there[u] = of >= 0;
+    x_from[u] = x + (max(of, 0) * t.x_row + x_k) * kSize;
   }
-  for (int r0 = 0; r0 < r; r0 += kRankPass) {
-    const int ranks = min(r - r0, kRankPass);
-    float acc[kRankPass / 16][S::kColumns][4] = {};
-    const W *w_from = down + static_cast<int64_t>(r0 + w_row0) * id + 8 * w_chunk;
-    auto load = [&](int p) {
-      const uint32_t to = base + (p - p0) % kStages * stage_bytes;
+  const uint32_t base = smem_addr(smem), x_to = base + x_at(x_row, tid % kXChunks), w_to = base + w_at(w_row, tid % kWChunks);
+  static_assert(kXRows % (kFp32 ? 4 : 8) == 0 && kWRows % 8 == 0, "a thread's rows are moved about alike");
+  // and what it reads of one: of x the pairs of columns 2 c, 2 c + 8, 2 c + 16 and
+  // 2 c + 24 of the 32; of the weights a row for the others' operands
+  uint32_t x_read[4], w_read[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = (32 * slot + 8 * i + 2 * c) * kSize;
+    x_read[i] = base + x_at(tokens0 + g, at >> 4) + (at & 15);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) w_read[i] = base + w_at(lane & 15, 4 * slot + 2 * i + (lane >> 4));
+  for (int r0 = 0; r0 < r; r0 += kPass) {
+    const int ranks = min(r - r0, kPass), rows = min(r16 - r0, kPass);
+    float acc[kPass / 16][S::kColumns][4] = {};
+    const W *w_from = down + static_cast<int64_t>(r0 + w_row) * id + w_k;
+    auto load = [&](int p, uint32_t stage) {
       const int k0 = p * S::kPiece;
-      const bool x_in = k0 + x_chunk * 16 / x_size < id, w_in = k0 + 8 * w_chunk < id;
+      const bool x_in = k0 + x_k < id, w_in = k0 + w_k < id;
 #pragma unroll
       for (int u = 0; u < kXCopies; ++u)
-        if (x_row0 + u * x_rows < kTile) {
-          const bool there = x_in && (x_there >> u & 1);
-          copy16(to + x_at(x_row0 + u * x_rows, x_chunk), there ? x_from[u] + static_cast<int64_t>(k0) * x_size : x, there);
-        }
+        copy16(x_to + stage + u * kXRows * kXRow, x_from[u] + static_cast<int64_t>(x_in ? k0 : 0) * kSize, x_in && x_there[u]);
 #pragma unroll
-      for (int u = 0; u < kWCopies; ++u)
-        if (w_row0 + u * kWRows < min(r16 - r0, kRankPass)) {
-          const bool there = w_in && w_row0 + u * kWRows < ranks;
-          copy16(to + w_at(w_row0 + u * kWRows, w_chunk), there ? w_from + static_cast<int64_t>(u * kWRows) * id + k0 : down, there);
-        }
+      for (int u = 0; u < kWCopies; ++u) {
+        const int row = w_row + u * kWRows;
+        if (row >= rows) break;
+        const bool there = w_in && row < ranks;
+        copy16(w_to + stage + u * kWRows * kWRow, there ? w_from + static_cast<int64_t>(u * kWRows) * id + k0 : down, there);
+      }
     };
+    uint32_t to = 0, from = 0;  // stages
 #pragma unroll
     for (int p = 0; p < kStages - 1; ++p) {
-      if (p0 + p < p1) load(p0 + p);
+      if (p0 + p < p1) load(p0 + p, to);
       copies_commit();
+      to += stage_bytes;
     }
     for (int p = p0; p < p1; ++p) {
       copies_wait<kStages - 2>();
       __syncthreads();
-      if (p + kStages - 1 < p1) load(p + kStages - 1);
+      if (p + kStages - 1 < p1) load(p + kStages - 1, to);
       copies_commit();
+      to = to == (kStages - 1) * stage_bytes ? 0 : to + stage_bytes;
+      const uint32_t now = from;
+      from = from == (kStages - 1) * stage_bytes ? 0 : from + stage_bytes;
       if (tokens0 >= n) continue;
-      const unsigned char *stage = smem + (p - p0) % kStages * stage_bytes;
       Terms xt[S::kColumns][4];
 #pragma unroll
-      for (int j = 0; j < S::kColumns; ++j) {
-        const int row = tokens0 + 8 * j + g, chunk = (32 * slot + 8 * c) * x_size / 16;
-        const uint4 lo = *reinterpret_cast<const uint4 *>(stage + x_at(row, chunk));
-        const uint4 hi = x_size == 4 ? *reinterpret_cast<const uint4 *>(stage + x_at(row, chunk + 1)) : zero4();
-        split8(xt[j], lo, hi, t.x_type);
-      }
+      for (int j = 0; j < S::kColumns; ++j)
 #pragma unroll
-      for (int m = 0; m < kRankPass / 16; ++m) {
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t at = x_read[i] + now + 8 * j * kXRow;
+          float2 v;
+          if constexpr (kFp32) {
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+          } else {
+            uint32_t w;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+            v = t.x_type == MMQ_DT_F16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w)) : make_float2(low(w), high(w));
+          }
+          xt[j][i] = split(v.x, v.y);
+        }
+#pragma unroll
+      for (int m = 0; m < kPass / 16; ++m) {
         if (16 * m >= ranks) break;
-        Weights8<W> u, v;
-        u.set(*reinterpret_cast<const uint4 *>(stage + w_at(16 * m + g, 4 * slot + c)));
-        v.set(*reinterpret_cast<const uint4 *>(stage + w_at(16 * m + 8 + g, 4 * slot + c)));
 #pragma unroll
-        for (int j = 0; j < S::kColumns; ++j) product<W>(acc[m][j], u, v, xt[j]);
+        for (int i = 0; i < 2; ++i) {
+          uint32_t v[4];
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "r"(w_read[i] + now + 16 * m * kWRow)
+                       : "memory");
+          Operand<W> w;
+          w.set(v[0], v[1], v[2], v[3], 0);
+#pragma unroll
+          for (int j = 0; j < S::kColumns; ++j) product<W>(acc[m][j], w, xt[j][2 * i], xt[j][2 * i + 1]);
+        }
       }
     }
     copies_wait<0>();
     __syncthreads();
-    put_part<kTile>(part, acc, ranks, slot, tokens0);
+    put_part<kTile, kPass>(part, acc, ranks, slot, tokens0);
     __syncthreads();
-    add_up<kTile>(mine, part, r0, r16);
+    add_up<kTile, kPass>(mine, part, r0, r16);
     __syncthreads();  // (part makes room)
   }
   cluster_sync();
@@ -716,11 +776,17 @@ __global__ void __launch_bounds__(kThreads, 2) __cluster_dims__(kCtas, 1, 1) lor
 }
 
 // The second product: a CTA takes a.columns output columns of a tile, a warp 32 of
-// them and 16 tokens at a time, the next ones' y on its way.  HBM bound (y in, out out).
+// them and 16 tokens at a time, the next ones' y on its way.  The weights of 32
+// columns stay in registers for the tile's tokens, up to rank 64 (32 in fp16).
+// HBM bound (y in, out out).
 constexpr int kYPieces = 3;
-template <class W, int kTile>
-__global__ void __launch_bounds__(kThreads, 3) lora_up_kernel(const __grid_constant__ LoraArgs a) {
-  extern __shared__ __align__(128) uint32_t terms[];
+template <class W, int kTile, int kPitch>
+__global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_constant__ LoraArgs a) {
+  constexpr int kEach = 2;  // columns of eight tokens at once
+  constexpr int kHold = kPitch == 16 ? 1 : kPitch == 48 && Operand<W>::kParts == 1 ? 2 : 0;  // steps of 32 ranks whose weights stay
+  constexpr int kWords = kTerms * kTile * kPitch;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t s_y[kTile], s_out[kTile];  // a token's row, in bytes from the first; -1: none
   __shared__ int s_row[kTile];
   const mmq_lora_args &t = a.t;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -730,47 +796,89 @@ __global__ void __launch_bounds__(kThreads, 3) lora_up_kernel(const __grid_const
   // done, so that all but the terms may be read before the wait)
   const Tile k_tile = tile_at(t, tile, in_place);
   const bool none = k_tile.n == 0;
-  const int n = k_tile.n, r = k_tile.rank, od = static_cast<int>(t.od), rmax = t.rank;
+  const int n = k_tile.n, r = k_tile.rank, od = static_cast<int>(t.od), rmax = t.rank, ranks = (r + 31) / 32;
   const int o0 = chunk * a.columns, o1 = min(o0 + a.columns, od);
-  if (!none && tid < kTile) s_row[tid] = tid < n ? t.plan[kHead + k_tile.first + tid] : -1;
+  if (tid < kTile) {
+    const int row = tid < n ? t.plan[kHead + k_tile.first + tid] : -1;
+    s_row[tid] = row;
+    s_y[tid] = row < 0 ? -1 : row * t.y_row * 4, s_out[tid] = row < 0 ? -1 : row * t.out_row * 4;
+  }
   __syncthreads();
-  constexpr int kEach = 2;  // columns of eight tokens at once
-  const int pitch = pitch_of(rmax);
-  const W *up = static_cast<const W *>(t.b) + static_cast<int64_t>(max(k_tile.adapter, 0)) * od * rmax;
-  // Piece i of the warp: columns from 32 (i / steps) kWarps on, tokens from 16
-  // (i % steps) on.  Each thread copies what it needs of y itself, some pieces
-  // ahead, to places that no other reads: [piece in flight][part][thread].
-  const int steps = (n + 8 * kEach - 1) / (8 * kEach), first = o0 + 32 * warp;
+  // A warp's columns are 32 from o0 + 32 warp on, then every 32 kWarps; its pieces
+  // of them 16 tokens each.  Each thread copies what it needs of y itself, some
+  // pieces ahead, to places that no other reads: [piece in flight][part][thread].
+  const int first = o0 + 32 * warp, steps = (n + 8 * kEach - 1) / (8 * kEach);
   const int pieces = first < o1 && r > 0 ? (o1 - first + 32 * kWarps - 1) / (32 * kWarps) * steps : 0;
-  float4 *const y = reinterpret_cast<float4 *>(terms + kTerms * kTile * pitch) + tid;
-  auto fetch = [&](int i, int o, int k0) {
-    o += 4 * g;
+  constexpr uint32_t kPiece = 2 * kEach * kThreads * 16, kPart = kThreads * 16;
+  const uint32_t ring = smem_addr(smem) + 4 * kWords + tid * 16;
+  const char *y = reinterpret_cast<const char *>(t.y + 4 * g);
+  char *out = reinterpret_cast<char *>(t.out + 4 * g);
+  int ahead_o = first, ahead_k = 0, ahead = 0;
+  uint32_t ahead_at = ring;
+  auto fetch_next = [&] {
+    if (ahead < pieces) {
+      const bool inside = a.wide ? ahead_o + 4 * g < od : false;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j)
+      for (int j = 0; j < kEach; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = s_row[k0 + 8 * j + 2 * c + h];
-        if (row < 0 || o >= od) continue;
-        const float *src = t.y + row * t.y_row + o;
-        const uint32_t to = smem_addr(y + (i % kYPieces * 2 * kEach + 2 * j + h) * kThreads);
-        if (a.wide) {
-          copy16(to, src, true);
-        } else {
+        for (int h = 0; h < 2; ++h) {
+          const int64_t row = s_y[ahead_k + 8 * j + 2 * c + h];
+          const char *src = y + row + 4 * ahead_o;
+          const uint32_t to = ahead_at + (2 * j + h) * kPart;
+          if (inside) {
+            if (row >= 0) copy16(to, src, true);
+          } else if (row >= 0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (o + e < od) copy4(to + 4 * e, src + e);
+            for (int e = 0; e < 4; ++e)
+              if (ahead_o + 4 * g + e < od) copy4(to + 4 * e, src + 4 * e);
+          }
         }
-      }
-  };
-  int ahead_o = first, ahead_k = 0;
-  auto fetch_next = [&](int i) {
-    if (i < pieces) fetch(i, ahead_o, ahead_k);
+    }
     copies_commit();
+    ++ahead;
+    ahead_at = ahead_at == ring + (kYPieces - 1) * kPiece ? ring : ahead_at + kPiece;
     ahead_k += 8 * kEach;
     if (ahead_k >= n) ahead_k = 0, ahead_o += 32 * kWarps;
   };
 #pragma unroll
-  for (int i = 0; i < kYPieces - 1; ++i) fetch_next(i);
+  for (int i = 0; i < kYPieces - 1; ++i) fetch_next();
+  // rows o + 4 g + i of the weights, ranks 32 step + 8 c on
+  const W *up = static_cast<const W *>(t.b) + (static_cast<int64_t>(max(k_tile.adapter, 0)) * od + 4 * g) * rmax + 8 * c;
+  auto weights = [&](uint4 (&w)[4], int o, int step) {
+    const int k = 32 * step + 8 * c;
+    const W *from = up + static_cast<int64_t>(o) * rmax + 32 * step;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = k < r && o + 4 * g + i < od ? __ldg(reinterpret_cast<const uint4 *>(from + i * rmax)) : zero4();
+    if (k < r && k + 8 > r) {  // columns past the rank
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t *v = &w[i].x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] &= k + 2 * e + 1 < r ? 0xffffffffu : k + 2 * e < r ? 0xffffu : 0u;
+      }
+    }
+  };
+  // as operands: blocks of 16 rows (4 g, 4 g + 1; 4 g + 2, 4 g + 3), halves of a step
+  struct Step {
+    Operand<W> w[2][2];
+  };
+  auto operands = [&](Step &to, int o, int step) {
+    uint4 raw[4];
+    weights(raw, o, step);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const uint4 p = raw[2 * b], q = raw[2 * b + 1];
+      to.w[b][0].set(p.x, q.x, p.y, q.y, a.zero), to.w[b][1].set(p.z, q.z, p.w, q.w, a.zero);
+    }
+  };
+  Step hold[kHold ? kHold : 1];
+  auto take = [&](int o) {
+    if (o < o1)
+#pragma unroll
+      for (int k = 0; k < kHold; ++k)
+        if (k < ranks) operands(hold[k], o, k);
+  };
+  if (pieces) take(first);
   griddep_wait();
   griddep_launch_dependents();
   if (none) return;
@@ -778,29 +886,78 @@ __global__ void __launch_bounds__(kThreads, 3) lora_up_kernel(const __grid_const
     if (!in_place) copy_rows(a, s_row, n, o0, o1);
     return;
   }
-  const int words = (r + 31) / 32 * 16;
-  const uint32_t *from = a.terms + static_cast<int64_t>(tile) * kTerms * kTile * pitch;
-  const int chunks = words / 4;  // of 16 bytes, of a row
-  for (int i = tid; i < kTerms * kTile * chunks; i += kThreads) {
-    const int row = i / chunks, at = row * pitch + 4 * (i - row * chunks);
-    copy16(smem_addr(terms + at), from + at, true);
+  {
+    const uint32_t *from = a.terms + static_cast<int64_t>(tile) * kWords;
+    const int chunks = ranks * 4;  // of 16 bytes, of a row
+    for (int i = tid; i < kTerms * kTile * chunks; i += kThreads) {
+      const int row = i / chunks, at = row * kPitch + 4 * (i - row * chunks);
+      copy16(smem_addr(smem) + 4 * at, from + at, true);
+    }
+    copies_commit();
+    copies_wait<0>();
+    __syncthreads();
   }
-  copies_commit();
-  copies_wait<0>();
-  __syncthreads();
+  const unsigned char *terms = smem + 4 * (g * kPitch + 4 * c);
   int o = first, k0 = 0;
+  uint32_t at = ring;
   for (int i = 0; i < pieces; ++i) {
-    fetch_next(i + kYPieces - 1);
+    fetch_next();
     float acc[2][kEach][4] = {};
-    expand<W, kEach>(acc, a, up, terms, kTile * pitch, pitch, r, o + 4 * g, k0);
+    const unsigned char *mine = terms + 4 * k0 * kPitch;
+    auto step = [&](const Step &k, int s) {
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        Terms x[4];
+#pragma unroll
+        for (int q = 0; q < kTerms; ++q) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(mine + 4 * ((q * kTile + 8 * j) * kPitch + 16 * s));
+          x[0].w[q] = v.x, x[1].w[q] = v.y, x[2].w[q] = v.z, x[3].w[q] = v.w;
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) product<W>(acc[b][j], k.w[b][i], x[2 * i], x[2 * i + 1]);
+      }
+    };
+    if constexpr (kHold > 0) {
+#pragma unroll
+      for (int s = 0; s < kHold; ++s)
+        if (s < ranks) step(hold[s], s);
+    } else {
+      for (int s = 0; s < ranks; ++s) {
+        Step k;
+        operands(k, o, s);
+        step(k, s);
+      }
+    }
     copies_wait<kYPieces - 1>();
+    const bool inside = a.wide ? o + 4 * g < od : false;
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        store_out(a, s_row[k0 + 8 * j + 2 * c + h], o + 4 * g, sum_of<kEach>(acc, j, h, y[(i % kYPieces * 2 * kEach + 2 * j + h) * kThreads]));
+      for (int h = 0; h < 2; ++h) {
+        const int64_t row = s_out[k0 + 8 * j + 2 * c + h];
+        if (row < 0) continue;
+        float4 v;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at + (2 * j + h) * kPart) : "memory");
+        v = sum_of<kEach>(acc, j, h, v);
+        float *to = reinterpret_cast<float *>(out + row + 4 * o);
+        if (inside) {
+          *reinterpret_cast<float4 *>(to) = v;
+        } else {
+          const int left = od - o - 4 * g;
+          if (left > 0) to[0] = v.x;
+          if (left > 1) to[1] = v.y;
+          if (left > 2) to[2] = v.z;
+          if (left > 3) to[3] = v.w;
+        }
+      }
+    at = at == ring + (kYPieces - 1) * kPiece ? ring : at + kPiece;
     k0 += 8 * kEach;
-    if (k0 >= n) k0 = 0, o += 32 * kWarps;
+    if (k0 >= n) {
+      k0 = 0, o += 32 * kWarps;
+      take(o);
+    }
   }
   copies_wait<0>();
 }
@@ -810,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 3) lora_up_kernel(const __grid_const
 int tile_of(int64_t ntok, int64_t nreq, int64_t nadapters) {
   const int64_t groups = std::max<int64_t>(1, std::min(nreq, nadapters + 1));
   const int64_t want = std::min((ntok + groups - 1) / groups, ntok * kCtas / (2 * 152));
-  return want <= 8 ? 8 : want <= 16 ? 16 : want <= 32 ? 32 : 64;
+  return want <= 8 ? 8 : want <= 32 ? 16 : 64;
 }
 int64_t most_tiles(int64_t ntok, int64_t nreq, int64_t nadapters) {
   return std::min(ntok, ntok / tile_of(ntok, nreq, nadapters) + std::min(nreq, nadapters + 1));
@@ -841,11 +998,14 @@ cudaError_t launch_with(LoraArgs a, const CallContext &ctx, cudaStream_t s) {
   const int64_t chunks = (a.t.od + a.columns - 1) / a.columns;
   if (tiles * chunks > 0x7fffffff) return cudaErrorNotSupported;
   a.chunks = static_cast<int>(chunks), a.by_chunks = FastDiv(a.chunks);
-  const int x_size = a.t.x_type == MMQ_DT_F32 ? 4 : 2, ranks = std::min(up16(a.t.rank), kRankPass);
-  a.front = std::max(kStages * S::kPiece * (kTile * x_size + ranks * 2), 4 * S::kSplit * kRankPass * kTile);
+  const int x_size = a.t.x_type == MMQ_DT_F32 ? 4 : 2, pass = a.t.rank <= 32 ? 32 : 64, ranks = std::min(up16(a.t.rank), pass);
+  a.front = std::max(kStages * S::kPiece * (kTile * x_size + ranks * 2), 4 * S::kSplit * pass * kTile);
   const size_t down = a.front + 4 * static_cast<size_t>(up16(a.t.rank)) * kTile, left = 4 * kTerms * kTile * pitch, up = left + kYPieces * 4 * 16 * kThreads;
-  cudaError_t e = allow(lora_down_kernel<W, kTile>, down);
-  if (e == cudaSuccess) e = allow(lora_up_kernel<W, kTile>, up);
+  const auto first = pass == 32 ? (x_size == 4 ? lora_down_kernel<W, kTile, true, 32> : lora_down_kernel<W, kTile, false, 32>)
+                                : (x_size == 4 ? lora_down_kernel<W, kTile, true, 64> : lora_down_kernel<W, kTile, false, 64>);
+  const auto second = pitch == 16 ? lora_up_kernel<W, kTile, 16> : pitch == 48 ? lora_up_kernel<W, kTile, 48> : lora_up_kernel<W, kTile, 80>;
+  cudaError_t e = allow(first, down);
+  if (e == cudaSuccess) e = allow(second, up);
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (e == cudaSuccess) e = cudaStreamIsCapturing(s, &cap);
   if (e != cudaSuccess) return e;
@@ -853,8 +1013,8 @@ cudaError_t launch_with(LoraArgs a, const CallContext &ctx, cudaStream_t s) {
   e = cap == cudaStreamCaptureStatusActive ? cudaMallocAsync(&scratch, tiles * left, s) : cudaMallocFromPoolAsync(&scratch, tiles * left, ctx.pool, s);
   if (e != cudaSuccess) return e;
   a.terms = static_cast<uint32_t *>(scratch);
-  e = launch_early(lora_down_kernel<W, kTile>, static_cast<unsigned>(tiles * kCtas), 1, kThreads, down, s, a);
-  if (e == cudaSuccess) e = launch_early(lora_up_kernel<W, kTile>, static_cast<unsigned>(tiles * chunks), 1, kThreads, up, s, a);
+  e = launch_early(first, static_cast<unsigned>(tiles * kCtas), 1, kThreads, down, s, a);
+  if (e == cudaSuccess) e = launch_early(second, static_cast<unsigned>(tiles * chunks), 1, kThreads, up, s, a);
   const cudaError_t ef = cudaFreeAsync(scratch, s);
   return e != cudaSuccess ? e : ef;
 }
@@ -864,7 +1024,6 @@ cudaError_t launch_of(const LoraArgs &a, const CallContext &ctx, cudaStream_t s)
   switch (tile_of(a.t.ntok, a.t.nreq, a.t.nadapters)) {
     case 8: return launch_few<W>(a, s);
     case 16: return launch_with<W, 16>(a, ctx, s);
-    case 32: return launch_with<W, 32>(a, ctx, s);
     default: return launch_with<W, 64>(a, ctx, s);
   }
 }
