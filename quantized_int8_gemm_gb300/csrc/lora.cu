@@ -211,6 +211,14 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ float4 lds4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -232,6 +240,15 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// x -= a, y -= b, in one instruction (as a product with -1, which is exact).
+__device__ __forceinline__ void subtract(float &x, float &y, float a, float b) {
+  asm("{\n\t.reg .b64 m, v, d;\n\t"
+      "mov.b64 m, {%4, %4};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 d, {%0, %1};\n\t"
+      "fma.rn.f32x2 d, v, m, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(-1.0f));
+}
+
 // A pair of numbers as three bf16 terms: each is rounded to nearest, so that
 // what is left after it is at most 2^-9 of what it stands for, and after the
 // third nothing of an fp32 number's 24 bits.  (With two terms, 2^-18 off, the
@@ -245,7 +262,7 @@ __device__ __forceinline__ Terms split(float x, float y) {
 #pragma unroll
   for (int i = 0; i < kTerms; ++i) {
     t.w[i] = pack(x, y);
-    x -= low(t.w[i]), y -= high(t.w[i]);
+    if (i + 1 < kTerms) subtract(x, y, low(t.w[i]), high(t.w[i]));
   }
   return t;
 }
@@ -651,8 +668,7 @@ __global__ void __launch_bounds__(kThreads, kPass == 32 ? 3 : 2) __cluster_dims_
   constexpr int kSize = kFp32 ? 4 : 2, kXRow = S::kPiece * kSize, kWRow = S::kPiece * 2, kXStage = kTile * kXRow;  // bytes
   const uint32_t stage_bytes = kXStage + stage_ranks * kWRow;
   float *part = reinterpret_cast<float *>(smem), *mine = reinterpret_cast<float *>(smem + a.front);
-  const int pieces = (id + S::kPiece - 1) / S::kPiece, share = (pieces + kCtas - 1) / kCtas;
-  const int p0 = min(rank * share, pieces), p1 = min(p0 + share, pieces);
+  const int pieces = (id + S::kPiece - 1) / S::kPiece, p0 = pieces * rank / kCtas, p1 = pieces * (rank + 1) / kCtas;
   const int tokens0 = warp % S::kGroups * S::kTokens, slot = warp / S::kGroups;
   const W *down = static_cast<const W *>(t.a) + static_cast<int64_t>(k_tile.adapter) * rmax * id;
   const unsigned char *x = static_cast<const unsigned char *>(t.x);
@@ -780,13 +796,14 @@ __global__ void __launch_bounds__(kThreads, kPass == 32 ? 3 : 2) __cluster_dims_
 // columns stay in registers for the tile's tokens, up to rank 64 (32 in fp16).
 // HBM bound (y in, out out).
 constexpr int kYPieces = 3;
+constexpr int kEach = 2;  // columns of eight tokens at once (four gained nothing, and spilled)
 template <class W, int kTile, int kPitch>
 __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_constant__ LoraArgs a) {
-  constexpr int kEach = 2;  // columns of eight tokens at once
   constexpr int kHold = kPitch == 16 ? 1 : kPitch == 48 && Operand<W>::kParts == 1 ? 2 : 0;  // steps of 32 ranks whose weights stay
   constexpr int kWords = kTerms * kTile * kPitch;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int64_t s_y[kTile], s_out[kTile];  // a token's row, in bytes from the first; -1: none
+  __shared__ const char *s_y[kTile];  // a token's row; null: none
+  __shared__ char *s_out[kTile];
   __shared__ int s_row[kTile];
   const mmq_lora_args &t = a.t;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -801,38 +818,42 @@ __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_const
   if (tid < kTile) {
     const int row = tid < n ? t.plan[kHead + k_tile.first + tid] : -1;
     s_row[tid] = row;
-    s_y[tid] = row < 0 ? -1 : row * t.y_row * 4, s_out[tid] = row < 0 ? -1 : row * t.out_row * 4;
+    s_y[tid] = row < 0 ? nullptr : reinterpret_cast<const char *>(t.y + row * t.y_row);
+    s_out[tid] = row < 0 ? nullptr : reinterpret_cast<char *>(t.out + row * t.out_row);
   }
   __syncthreads();
   // A warp's columns are 32 from o0 + 32 warp on, then every 32 kWarps; its pieces
-  // of them 16 tokens each.  Each thread copies what it needs of y itself, some
+  // of them 8 kEach tokens.  Each thread copies what it needs of y itself, some
   // pieces ahead, to places that no other reads: [piece in flight][part][thread].
   const int first = o0 + 32 * warp, steps = (n + 8 * kEach - 1) / (8 * kEach);
   const int pieces = first < o1 && r > 0 ? (o1 - first + 32 * kWarps - 1) / (32 * kWarps) * steps : 0;
   constexpr uint32_t kPiece = 2 * kEach * kThreads * 16, kPart = kThreads * 16;
   const uint32_t ring = smem_addr(smem) + 4 * kWords + tid * 16;
-  const char *y = reinterpret_cast<const char *>(t.y + 4 * g);
-  char *out = reinterpret_cast<char *>(t.out + 4 * g);
+  // A piece within the tile and the columns, in 16-byte pieces, needs no checks.
+  auto whole = [&](int o, int k0) { return a.wide && k0 + 8 * kEach <= n && o + 32 <= od; };
   int ahead_o = first, ahead_k = 0, ahead = 0;
   uint32_t ahead_at = ring;
   auto fetch_next = [&] {
     if (ahead < pieces) {
-      const bool inside = a.wide ? ahead_o + 4 * g < od : false;
+      const char *const *rows = s_y + ahead_k + 2 * c;
+      const uint32_t column = 4 * (ahead_o + 4 * g);
+      if (whole(ahead_o, ahead_k)) {
 #pragma unroll
-      for (int j = 0; j < kEach; ++j)
+        for (int j = 0; j < kEach; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t row = s_y[ahead_k + 8 * j + 2 * c + h];
-          const char *src = y + row + 4 * ahead_o;
-          const uint32_t to = ahead_at + (2 * j + h) * kPart;
-          if (inside) {
-            if (row >= 0) copy16(to, src, true);
-          } else if (row >= 0) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (ahead_o + 4 * g + e < od) copy4(to + 4 * e, src + 4 * e);
+          for (int h = 0; h < 2; ++h) copy16(ahead_at + (2 * j + h) * kPart, rows[8 * j + h] + column);
+      } else {
+#pragma unroll 1
+        for (int q = 0; q < 2 * kEach; ++q) {
+          const char *row = rows[q / 2 * 8 + q % 2];
+          const int left = row ? od - ahead_o - 4 * g : 0;
+          if (a.wide) {
+            if (left > 0) copy16(ahead_at + q * kPart, row + column);
+          } else {
+            for (int e = 0; e < min(left, 4); ++e) copy4(ahead_at + q * kPart + 4 * e, row + column + 4 * e);
           }
         }
+      }
     }
     copies_commit();
     ++ahead;
@@ -891,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_const
     const int chunks = ranks * 4;  // of 16 bytes, of a row
     for (int i = tid; i < kTerms * kTile * chunks; i += kThreads) {
       const int row = i / chunks, at = row * kPitch + 4 * (i - row * chunks);
-      copy16(smem_addr(smem) + 4 * at, from + at, true);
+      copy16(smem_addr(smem) + 4 * at, from + at);
     }
     copies_commit();
     copies_wait<0>();
@@ -931,27 +952,32 @@ __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_const
       }
     }
     copies_wait<kYPieces - 1>();
-    const bool inside = a.wide ? o + 4 * g < od : false;
+    char *const *rows = s_out + k0 + 2 * c;
+    const uint32_t column = 4 * (o + 4 * g);
+    if (whole(o, k0)) {
 #pragma unroll
-    for (int j = 0; j < kEach; ++j)
+      for (int j = 0; j < kEach; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t row = s_out[k0 + 8 * j + 2 * c + h];
-        if (row < 0) continue;
-        float4 v;
-        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at + (2 * j + h) * kPart) : "memory");
-        v = sum_of<kEach>(acc, j, h, v);
-        float *to = reinterpret_cast<float *>(out + row + 4 * o);
-        if (inside) {
-          *reinterpret_cast<float4 *>(to) = v;
-        } else {
-          const int left = od - o - 4 * g;
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float4 *>(rows[8 * j + h] + column) = sum_of<kEach>(acc, j, h, lds4(at + (2 * j + h) * kPart));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kEach; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 v = sum_of<kEach>(acc, j, h, lds4(at + (2 * j + h) * kPart));
+          float *to = reinterpret_cast<float *>(rows[8 * j + h] + column);
+          const int left = rows[8 * j + h] ? od - o - 4 * g : 0;
+          if (a.wide) {
+            if (left > 0) *reinterpret_cast<float4 *>(to) = v;
+            continue;
+          }
           if (left > 0) to[0] = v.x;
           if (left > 1) to[1] = v.y;
           if (left > 2) to[2] = v.z;
           if (left > 3) to[3] = v.w;
         }
-      }
+    }
     at = at == ring + (kYPieces - 1) * kPiece ? ring : at + kPiece;
     k0 += 8 * kEach;
     if (k0 >= n) {
@@ -992,15 +1018,17 @@ cudaError_t launch_with(LoraArgs a, const CallContext &ctx, cudaStream_t s) {
   using S = Shape<kTile>;
   const int64_t tiles = most_tiles(a.t.ntok, a.t.nreq, a.t.nadapters), pitch = pitch_of(a.t.rank);
   // columns of a CTA in the second product: many, as what it needs beside y and
-  // out comes once, but CTAs for four rounds of the SMs
-  const int64_t want = a.t.od * tiles / (4 * 3 * 152);
+  // out comes once, but CTAs for five rounds of the SMs (64 tiles of 18944 columns:
+  // 512 columns 250 us for both products, 768 240, 1024 247, 2048 275; equal
+  // stretches of all tiles' columns for one round of CTAs 253)
+  const int64_t want = a.t.od * tiles / (5 * 2 * 152) + 128;
   a.columns = static_cast<int>(std::min<int64_t>(2048, std::max<int64_t>(256, want / 256 * 256)));
   const int64_t chunks = (a.t.od + a.columns - 1) / a.columns;
   if (tiles * chunks > 0x7fffffff) return cudaErrorNotSupported;
   a.chunks = static_cast<int>(chunks), a.by_chunks = FastDiv(a.chunks);
   const int x_size = a.t.x_type == MMQ_DT_F32 ? 4 : 2, pass = a.t.rank <= 32 ? 32 : 64, ranks = std::min(up16(a.t.rank), pass);
   a.front = std::max(kStages * S::kPiece * (kTile * x_size + ranks * 2), 4 * S::kSplit * pass * kTile);
-  const size_t down = a.front + 4 * static_cast<size_t>(up16(a.t.rank)) * kTile, left = 4 * kTerms * kTile * pitch, up = left + kYPieces * 4 * 16 * kThreads;
+  const size_t down = a.front + 4 * static_cast<size_t>(up16(a.t.rank)) * kTile, left = 4 * kTerms * kTile * pitch, up = left + kYPieces * 2 * kEach * 16 * kThreads;
   const auto first = pass == 32 ? (x_size == 4 ? lora_down_kernel<W, kTile, true, 32> : lora_down_kernel<W, kTile, false, 32>)
                                 : (x_size == 4 ? lora_down_kernel<W, kTile, true, 64> : lora_down_kernel<W, kTile, false, 64>);
   const auto second = pitch == 16 ? lora_up_kernel<W, kTile, 16> : pitch == 48 ? lora_up_kernel<W, kTile, 48> : lora_up_kernel<W, kTile, 80>;
