@@ -617,6 +617,8 @@ typedef struct mmq_token_rules {
  * row past nmasks is no mask, token_lens past tokens_width, n_draft past
  * rows - 1, bias_start past nbias are cut; all of them are reported by
  * mmq_last_device_error.
+ * What is written may overlap nothing else of the call (MMQ_ERR_ARG), but for
+ * adjusted in the logits' place.
  * vocab in 1..2^18, nreq*rows below 2^27 (more: MMQ_ERR_UNSUPPORTED).  With
  * tokens or biases each request's are listed first, in stream-ordered scratch as for
  * mmq_gemm (12 bytes for each token and bias).

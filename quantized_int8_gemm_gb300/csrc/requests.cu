@@ -39,6 +39,9 @@ bool table_fits(int64_t nreq, int64_t width, int64_t stride) {
   return nreq >= 0 && width >= 0 && width <= kInt32 && stride >= width && stride <= (int64_t(1) << 40);
 }
 
+// Whether n strides stay below any memory there is.
+bool spans(int64_t n, int64_t stride) { return stride >= 0 && stride <= (int64_t(1) << 48) / (n > 0 ? n : 1); }
+
 // The elements of (blocks, rows, n) in strides end on this one.
 int64_t extent(int64_t blocks, int64_t rows, int64_t n, int64_t block, int64_t row) { return (blocks - 1) * block + (rows - 1) * row + n; }
 
@@ -108,9 +111,11 @@ int mmq_token_probs(const mmq_token_rules *args, mmq_stream_t stream) {
   if (t.nreq < 0 || t.rows < 1 || t.vocab < 1 || t.tokens_width < 0 || t.tokens_width > kInt32 || t.nbias < 0 || t.nbias > kInt32 ||
       t.nmasks < 0 || t.nmasks > kInt32)
     return MMQ_ERR_ARG;
-  if (t.logits_req < 0 || t.logits_row < 0 || t.probs_req < 0 || t.probs_row < 0 || t.adjusted_req < 0 || t.adjusted_row < 0 ||
-      t.tokens_stride < 0 || t.draft_stride < 0 || t.mask_stride < 0)
-    return MMQ_ERR_ARG;
+  for (int64_t stride : {t.logits_req, t.probs_req, t.adjusted_req, t.tokens_stride, t.draft_stride})
+    if (!spans(t.nreq, stride)) return MMQ_ERR_ARG;
+  for (int64_t stride : {t.logits_row, t.probs_row, t.adjusted_row})
+    if (!spans(t.rows, stride)) return MMQ_ERR_ARG;
+  if (!spans(t.nmasks, t.mask_stride)) return MMQ_ERR_ARG;
   if (t.vocab > kMaxVocab) return MMQ_ERR_UNSUPPORTED;
   if (t.nreq > ((int64_t(1) << 27) - 1) / t.rows) return MMQ_ERR_UNSUPPORTED;
   if (t.nreq == 0) return MMQ_OK;
@@ -136,6 +141,18 @@ int mmq_token_probs(const mmq_token_rules *args, mmq_stream_t stream) {
   }
   if (t.adjusted) {
     if (!rows_apart(t.adjusted_req, t.adjusted_row) || (!same && meet(run(t.adjusted, t.adjusted_type, t.adjusted_req, t.adjusted_row), logits))) return MMQ_ERR_ARG;
+  }
+  const int64_t words = (t.vocab + 31) / 32, width = t.tokens ? t.tokens_width : 0;
+  auto vector = [&](const auto *p, int64_t n) { return Run(p, p ? n : 0); };
+  const Run read[] = {vector(t.temperature, t.nreq), vector(t.token_lens, t.nreq), vector(t.prompt_lens, t.nreq), vector(t.n_draft, t.nreq),
+                      vector(t.repetition, t.nreq), vector(t.frequency, t.nreq), vector(t.presence, t.nreq), vector(t.bias_start, t.nreq + 1),
+                      vector(t.bias_ids, t.nbias), vector(t.bias_values, t.nbias), vector(t.mask_rows, t.nreq * t.rows),
+                      vector(t.tokens, width ? extent(1, t.nreq, width, 0, t.tokens_stride) : 0),
+                      vector(t.draft, t.rows > 1 ? extent(1, t.nreq, t.rows - 1, 0, t.draft_stride) : 0),
+                      vector(t.mask, t.nmasks ? extent(1, t.nmasks, words, 0, t.mask_stride) : 0)};
+  for (const Run &r : read) {
+    if (t.probs && meet(run(t.probs, t.probs_type, t.probs_req, t.probs_row), r)) return MMQ_ERR_ARG;
+    if (t.adjusted && meet(run(t.adjusted, t.adjusted_type, t.adjusted_req, t.adjusted_row), r)) return MMQ_ERR_ARG;
   }
   mmq::CallContext ctx;
   if (int rc = mmq::call_context(&ctx)) return rc;
@@ -175,7 +192,8 @@ int mmq_lora(const mmq_lora_args *args, mmq_stream_t stream) {
   const mmq_lora_args &t = *args;
   if ((t.type != MMQ_DT_F16 && t.type != MMQ_DT_BF16) || !is_type(t.x_type)) return MMQ_ERR_TYPE;
   if (t.ntok < 0 || t.nreq < 0 || t.nadapters < 0 || t.id < 8 || t.id % 8 || t.od < 1 || t.rank < 8 || t.rank % 8 || t.rank > 128) return MMQ_ERR_ARG;
-  if (t.x_row < 0 || t.y_row < 0 || t.out_row < 0) return MMQ_ERR_ARG;
+  for (int64_t stride : {t.x_row, t.y_row, t.out_row})
+    if (!spans(t.ntok, stride)) return MMQ_ERR_ARG;
   if (t.id > kInt32 - 64 || t.od > kInt32 - 64 * 1024 || mmq_lora_plan_words(t.ntok, t.nreq, t.nadapters) < 0) return MMQ_ERR_UNSUPPORTED;
   if (t.ntok == 0 || t.nreq == 0) return MMQ_OK;
   if (!t.x || !t.y || !t.out || !t.plan || (t.nadapters && (!t.a || !t.b))) return MMQ_ERR_ARG;

@@ -4,9 +4,9 @@ probabilities and adapters in 64 bits.
 Tolerances, derived before any run.  Adjusted logits: four fp32 operations and one for each bias, each half a step
 (2^-24) of what has been added up to there.  Probabilities: those errors over the temperature, twice (the largest logit has
 them too); the exponent's argument carries 2^-23 of itself; exp2, the sum, the division and the joins stay within 2^-20.
-Adapters: x and the inner sums as two bf16 terms, 2^-18 each, fp16 weights as two terms of which the product of the small
-ones is left out, 2^-18 each; fp32 sums in chains of at most 128 steps of 2^-23: 2^-15 of the sum of magnitudes in all; the
-last addition rounds to fp32."""
+Adapters: x and the inner sums as three bf16 terms, 2^-27 each, fp16 weights as two terms of which the products of the
+smallest ones are left out, 2^-26; fp32 sums in chains of at most 128 steps of 2^-23: 2^-15 of the sum of magnitudes in all;
+the last addition rounds to fp32."""
 import math
 import random
 
@@ -16,6 +16,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+ARG, ALIGN, UNSUPPORTED = -1, -2, -7
 HALF_STEP = {F32: 2.0 ** -24, F16: 2.0 ** -11, BF16: 2.0 ** -8}
 
 
@@ -668,6 +669,89 @@ def test_lora_faults(mmq):
     got = mmq.mmq_lora(**p, plan=plan)
     want, tol = _lora_reference(p, [2, 3], [0, 1])
     assert ((got.double() - want).abs() <= tol).all()
+
+
+# ---------------------------------------------------------------- refusals
+def test_refused_pages(mmq):
+    table, held, parents, lens = _table([[1, 2], [3]], 4), _i32([2, 1]), _i32([0, 1]), _i32([20, 3])
+    kc, vc = (torch.zeros((8, 16, 2, 64), dtype=F16, device="cuda") for _ in range(2))
+    f, m = mmq.mmq_page_fork(table, held, parents, lens, 16, 8), mmq.mmq_page_compact(table, held, 8)
+    fork = lambda **kw: mmq.mmq_page_fork(**{**dict(block_table=table, n_blocks=held, parents=parents, lens=lens, page_size=16, n_pages=8), **kw})  # noqa: E731
+    compact = lambda **kw: mmq.mmq_page_compact(**{**dict(block_table=table, n_blocks=held, n_pages=8), **kw})  # noqa: E731
+    copy = lambda **kw: mmq.mmq_page_copy(**{**dict(k_cache=kc, v_cache=vc, pairs=f.pairs, tokens=f.tokens), **kw})  # noqa: E731
+    for call, bad in [(fork, dict(block_table=table.long())), (fork, dict(block_table=table[0])), (fork, dict(block_table=table.t())),
+                      (fork, dict(n_blocks=held[:1])), (fork, dict(n_blocks=held.float())), (fork, dict(parents=parents[:1])),
+                      (fork, dict(lens=lens.long())), (fork, dict(lens=lens[:, None])), (fork, dict(n_pages=-1)), (fork, dict(n_pages=2 ** 31)),
+                      (fork, dict(out=f._replace(counts=f.counts[:1]))), (fork, dict(out=f._replace(block_table=f.block_table[:, :3]))),
+                      (fork, dict(out=f._replace(free_pages=f.free_pages[:7]))), (fork, dict(out=f._replace(pairs=f.pairs.float()))),
+                      (compact, dict(block_table=table[:1])), (compact, dict(n_pages=-1)), (compact, dict(out=m._replace(pairs=m.pairs[:2]))),
+                      (copy, dict(pairs=f.pairs.long())), (copy, dict(pairs=f.tokens)), (copy, dict(tokens=f.tokens[:1])),
+                      (copy, dict(v_cache=vc[:4])), (copy, dict(v_cache=vc.bfloat16())), (copy, dict(k_cache=kc.float(), v_cache=vc.float()))]:
+        with pytest.raises(ValueError):
+            call(**bad)
+    for call, bad in [(fork, dict(parents=parents.cpu())), (fork, dict(out=(f.pairs,))), (fork, dict(lens=None)), (compact, dict(out=m.counts)),
+                      (copy, dict(pairs=None)), (copy, dict(tokens=[1, 2]))]:
+        with pytest.raises(TypeError):
+            call(**bad)
+    for call, bad, code in [(fork, dict(page_size=0), ARG), (fork, dict(out=f._replace(block_table=table)), ARG),
+                            (fork, dict(out=f._replace(n_blocks=held)), ARG), (fork, dict(n_pages=2 ** 20 + 1), UNSUPPORTED),
+                            (compact, dict(out=m._replace(block_table=table)), ARG)]:
+        with pytest.raises(mmq.MMQError) as e:
+            call(**bad)
+        assert e.value.code == code, bad.keys()
+    _same_fork(f, _fork_reference([[1, 2], [3]], [0, 1], [20, 3], 16, 8, 4))
+
+
+def test_refused_rules(mmq):
+    p = _rules_problem(2, 1, 320, F32, seed=1)
+    one, ids = torch.ones(2, device="cuda"), _i32([0, 1])
+    for bad in (dict(logits=p["logits"].double()), dict(logits=p["logits"][0]), dict(logits=p["logits"].transpose(1, 2)), dict(temperature=one[:1]),
+                dict(temperature=one.half()), dict(tokens=p["tokens"][:1]), dict(tokens=p["tokens"].long()), dict(tokens=None), dict(token_lens=ids[:1]),
+                dict(prompt_lens=one), dict(draft_tokens=p["draft_tokens"][:, :0]), dict(n_draft=one), dict(repetition=one[:1]), dict(frequency=ids),
+                dict(presence=one[:1]), dict(bias=(ids, *p["bias"][1:])), dict(bias=(p["bias"][0], p["bias"][1], p["bias"][2][:-1])),
+                dict(mask=p["mask"][:, :-1]), dict(mask=p["mask"].long()), dict(mask=None), dict(mask_rows=ids), dict(probs=None), dict(probs=False),
+                dict(probs=p["logits"][:, :1].clone()), dict(probs=p["logits"].double()), dict(adjusted=p["logits"][..., :-1])):
+        with pytest.raises(ValueError):
+            mmq.mmq_token_probs(**{**p, **bad})
+    for bad in (dict(temperature=one.cpu()), dict(bias=p["bias"][0]), dict(bias=p["bias"][:2]), dict(tokens=[1]), dict(probs=3)):
+        with pytest.raises(TypeError):
+            mmq.mmq_token_probs(**{**p, **bad})
+    for bad in (dict(probs=p["logits"]), dict(adjusted=torch.empty(320, device="cuda").expand(2, 2, 320))):
+        with pytest.raises(mmq.MMQError) as e:
+            mmq.mmq_token_probs(**{**p, **bad})
+        assert e.value.code == ARG
+
+
+def test_refused_adapters(mmq):
+    p, adapters, start, t = _lora_problem([2, 3], [0, 1], 2, 64, 96, 8, BF16)
+    plan = mmq.mmq_lora_plan(adapters, start, t, 2)
+    for bad in ((adapters[:1], start, t, 2), (adapters.long(), start, t, 2), (adapters, start[:2], t, 2), (adapters, start.float(), t, 2),
+                (adapters, start, t, 2, plan.words[:-1])):
+        with pytest.raises(ValueError):
+            mmq.mmq_lora_plan(*bad)
+    for bad, code in (((adapters, start, -1, 2), ARG), ((adapters, start, t, -1), ARG),
+                      ((adapters, start, 2 ** 30, 2), UNSUPPORTED), ((adapters, start, t, 2 ** 19), UNSUPPORTED)):
+        with pytest.raises(mmq.MMQError) as e:
+            mmq.mmq_lora_plan(*bad)
+        assert e.value.code == code, bad
+    lora = lambda **kw: mmq.mmq_lora(**{**p, "plan": plan, **kw})  # noqa: E731
+    for bad in (dict(x=p["x"][:-1]), dict(x=p["x"].double()), dict(x=p["x"].t()), dict(y=p["y"].half()), dict(y=p["y"][:, :-1]), dict(a=p["a"].half()),
+                dict(a=p["a"].float(), b=p["b"].float()), dict(a=p["a"][:1]), dict(b=p["b"][:, :, :4]), dict(b=p["b"].transpose(1, 2)),
+                dict(scales=p["scales"].half()), dict(ranks=_i32([1])), dict(out=p["y"][:-1]), dict(out=p["y"].half()),
+                dict(plan=plan._replace(words=plan.words[:-1])), dict(plan=plan._replace(tokens=4)), dict(plan=plan._replace(requests=1)),
+                dict(plan=plan._replace(adapters=1))):
+        with pytest.raises(ValueError):
+            lora(**bad)
+    wide, flat = torch.zeros((t, 70), device="cuda"), torch.zeros(t * 96 + 4, device="cuda")
+    for bad, code in ((dict(x=wide[:, 1:65]), ALIGN), (dict(x=wide[:, :64]), ALIGN),
+                      (dict(a=p["a"][:, :4].contiguous(), b=p["b"][..., :4].contiguous()), ARG),
+                      (dict(out=p["y"].new_empty(96).expand(t, 96)), ARG),
+                      (dict(y=flat[4:].view(t, 96), out=flat[:-4].view(t, 96)), ARG)):  # four further on in one buffer
+        with pytest.raises(mmq.MMQError) as e:
+            lora(**bad)
+        assert e.value.code == code, bad.keys()
+    with pytest.raises(TypeError):
+        lora(x=p["x"].cpu())
 
 
 # ---------------------------------------------------------------- together, streams, graphs
