@@ -491,40 +491,6 @@ __device__ __forceinline__ void store_out(const LoraArgs &a, int row, int o, flo
   if (o + 2 < od) to[2] = v.z;
   if (o + 3 < od) to[3] = v.w;
 }
-// The second product for 32 output columns (o0 on) and eight tokens of each of
-// kEach columns (k0 on): a lane has four output columns that lie together, rows
-// g and g + 8 of two blocks of 16.
-template <class W, int kEach>
-__device__ __forceinline__ void expand(float (&acc)[2][kEach][4], const LoraArgs &a, const W *up, const uint32_t *terms, int term_words, int pitch, int r,
-                                       int o, int k0) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, od = static_cast<int>(a.t.od);
-  for (int r0 = 0; r0 < r; r0 += 32) {
-    const int k = r0 + 8 * c;
-    Weights8<W> w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint4 raw = zero4();
-      if (k < r && o + i < od) raw = __ldg(reinterpret_cast<const uint4 *>(up + static_cast<int64_t>(o + i) * a.t.rank + k));
-      if (k < r && k + 8 > r) {  // columns past the rank
-        uint32_t *v = &raw.x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] &= k + 2 * e + 1 < r ? 0xffffffffu : k + 2 * e < r ? 0xffffu : 0u;
-      }
-      w[i].set(raw);
-    }
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      Terms x[4];
-#pragma unroll
-      for (int i = 0; i < kTerms; ++i) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(terms + i * term_words + (k0 + 8 * j + g) * pitch + k / 2);
-        x[0].w[i] = v.x, x[1].w[i] = v.y, x[2].w[i] = v.z, x[3].w[i] = v.w;
-      }
-      product<W>(acc[0][j], w[0], w[1], x);
-      product<W>(acc[1][j], w[2], w[3], x);
-    }
-  }
-}
 template <int kEach>
 __device__ __forceinline__ float4 sum_of(const float (&acc)[2][kEach][4], int j, int h, const float4 &y) {
   return make_float4(y.x + acc[0][j][h], y.y + acc[0][j][h + 2], y.z + acc[1][j][h], y.w + acc[1][j][h + 2]);
@@ -532,13 +498,18 @@ __device__ __forceinline__ float4 sum_of(const float (&acc)[2][kEach][4], int j,
 
 // ---------------------------------------------------------------- few tokens: one kernel
 // A cluster takes a tile of eight tokens: each CTA multiplies an eighth of x's
-// columns by A, the sums are joined through the cluster's shared memory, and
-// each writes an eighth of the output columns.  HBM bound by the adapters with
-// many tiles, latency bound with few.
-constexpr int kFew = 8, kFewPass = 64;  // tokens; ranks whose sums a warp holds at once
-template <class W>
-__global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCtas, 1, 1) lora_few_kernel(const __grid_constant__ LoraArgs a) {
-  using S = Shape<kFew>;
+// columns by A, every CTA adds up the eight sums in their order, and each writes
+// an eighth of the output columns.  HBM bound by the adapters with many tiles,
+// latency bound with few.  Up to rank 32 two pieces of A and what the second
+// product needs first are asked for ahead, in 116 registers (one token, 3584 ->
+// 4608, rank 16: 8.4 -> 6.4 us); beyond, three CTAs an SM hide more than reads
+// ahead in two do (96 tokens of 50 adapters of rank 64: 21.1 against 24.6 us), and
+// B comes to L2 during the first product.
+constexpr int kFew = 8;  // tokens
+template <class W, int kPass>  // ranks whose sums a warp holds at once
+__global__ void __launch_bounds__(kThreads, kPass == 32 ? 2 : 3) __cluster_dims__(kCtas, 1, 1) lora_few_kernel(const __grid_constant__ LoraArgs a) {
+  constexpr int kHold = kPass / 32;  // steps of 32 ranks of the second product
+  constexpr bool kAhead = kPass == 32;  // (registers for two)
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_row[kFew];
   const mmq_lora_args &t = a.t;
@@ -552,91 +523,154 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCtas, 1, 1) lor
   const int n = k_tile.n, r = k_tile.rank;
   if (tid < kFew) s_row[tid] = tid < n ? t.plan[kHead + k_tile.first + tid] : -1;
   const int id = static_cast<int>(t.id), od = static_cast<int>(t.od), rmax = t.rank;
-  const int units = (od + 31) / 32, per = (units + kCtas - 1) / kCtas, u0 = min(rank * per, units), u1 = min(u0 + per, units);
-  const W *up = static_cast<const W *>(t.b) + static_cast<int64_t>(max(k_tile.adapter, 0)) * od * rmax;
-  if (r > 0) {
-    // the adapter is most of what is read: the second product's part of it comes
-    // to L2 during the first
-    const char *from = reinterpret_cast<const char *>(up + static_cast<int64_t>(32 * u0) * rmax);
-    const int64_t bytes = static_cast<int64_t>(min(32 * u1, od) - 32 * u0) * rmax * 2;
-    for (int64_t at = tid * 4096; at < bytes; at += kThreads * 4096)
-      bulk_prefetch_l2(from + at, static_cast<uint32_t>(min(bytes - at, static_cast<int64_t>(4096))));
-  }
-  __syncthreads();
+  const int units = (od + 31) / 32, u0 = units * rank / kCtas, u1 = units * (rank + 1) / kCtas;
   if (r == 0) {
+    __syncthreads();
     if (!in_place) copy_rows(a, s_row, n, min(32 * u0, od), min(32 * u1, od));
     return;
   }
+  const W *down = static_cast<const W *>(t.a) + static_cast<int64_t>(k_tile.adapter) * rmax * id;
+  const W *up = static_cast<const W *>(t.b) + static_cast<int64_t>(k_tile.adapter) * od * rmax;
   const int r16 = up16(r), pitch = pitch_of(rmax);
   // partial sums of the warps, later the terms; behind them the CTA's sums
   float *part = reinterpret_cast<float *>(smem), *mine = reinterpret_cast<float *>(smem + few_front(rmax));
   uint32_t *terms = reinterpret_cast<uint32_t *>(smem);
-  {
-    const int pieces = (id + S::kPiece - 1) / S::kPiece, share = (pieces + kCtas - 1) / kCtas;
-    const int p0 = min(rank * share, pieces), p1 = min(p0 + share, pieces);
-    const W *down = static_cast<const W *>(t.a) + static_cast<int64_t>(k_tile.adapter) * rmax * id;
-    const int x_size = t.x_type == MMQ_DT_F32 ? 4 : 2, of = s_row[g];
-    const unsigned char *row = static_cast<const unsigned char *>(t.x) + max(of, 0) * t.x_row * x_size;
-    for (int r0 = 0; r0 < r; r0 += kFewPass) {
-      const int ranks = min(r - r0, kFewPass);
-      float acc[kFewPass / 16][S::kColumns][4] = {};
-      for (int step = p0 * S::kSplit + warp; step < p1 * S::kSplit; step += S::kSplit) {
-        const int k = 32 * step + 8 * c;
-        const bool in = k < id;
-        uint4 raw[kFewPass / 16][2], lo = zero4(), hi = zero4();
+  // The first product: the warps take 32 columns at a time.
+  const int steps = (id + 31) / 32, s0 = steps * rank / kCtas + warp, s1 = steps * (rank + 1) / kCtas;
+  const int x_size = t.x_type == MMQ_DT_F32 ? 4 : 2;
+  struct Piece {
+    uint4 w[kPass / 16][2], lo, hi;
+  };
+  auto fetch_w = [&](Piece &p, int step, int r0) {
+    const int k = 32 * step + 8 * c;
 #pragma unroll
-        for (int m = 0; m < kFewPass / 16; ++m)
+    for (int m = 0; m < kPass / 16; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int at = 16 * m + 8 * h + g;
-            raw[m][h] = in && at < ranks ? __ldg(reinterpret_cast<const uint4 *>(down + static_cast<int64_t>(r0 + at) * id + k)) : zero4();
-          }
-        if (in && of >= 0) {
-          lo = __ldg(reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(k) * x_size));
-          if (x_size == 4) hi = __ldg(reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(k) * x_size) + 1);
-        }
-        Terms xt[4];
-        if (x_size == 4) split8<true>(xt, lo, hi, t.x_type);
-        else split8<false>(xt, lo, hi, t.x_type);
-#pragma unroll
-        for (int m = 0; m < kFewPass / 16; ++m) {
-          if (16 * m >= ranks) break;
-          Weights8<W> u, v;
-          u.set(raw[m][0]), v.set(raw[m][1]);
-          product<W>(acc[m][0], u, v, xt);
-        }
+      for (int h = 0; h < 2; ++h) {
+        const int at = r0 + 16 * m + 8 * h + g;
+        p.w[m][h] = k < id && at < r ? __ldg(reinterpret_cast<const uint4 *>(down + static_cast<int64_t>(at) * id + k)) : zero4();
       }
-      if (r0) __syncthreads();
-      put_part<kFew, kFewPass>(part, acc, ranks, warp, 0);
-      __syncthreads();
-      add_up<kFew, kFewPass>(mine, part, r0, r16);
-    }
-    __syncthreads();  // (part makes room)
+  };
+  Piece now;
+  if (kAhead && s0 < s1) fetch_w(now, s0, 0);
+  if (tid < 32) {
+    // the adapter is most of what is read: the second product's part of it comes
+    // to L2 during the first
+    const char *from = reinterpret_cast<const char *>(up + static_cast<int64_t>(32 * u0) * rmax);
+    const int64_t bytes = static_cast<int64_t>(min(32 * u1, od) - 32 * u0) * rmax * 2;
+    for (int64_t at = tid * 4096; at < bytes; at += 32 * 4096)
+      bulk_prefetch_l2(from + at, static_cast<uint32_t>(min(bytes - at, static_cast<int64_t>(4096))));
   }
-  for (int k = tid; k < kTerms * kFew * pitch; k += kThreads) terms[k] = 0;  // (ranks past r)
-  cluster_sync();
-  // each CTA adds up a share of the pairs of ranks and sends it to all
-  for (int e = rank * kThreads + tid; e < r16 / 2 * kFew; e += kCtas * kThreads) {
+  __syncthreads();
+  const int of = s_row[g];
+  const unsigned char *row = static_cast<const unsigned char *>(t.x) + max(of, 0) * t.x_row * x_size;
+  auto fetch_x = [&](Piece &p, int step) {
+    const int k = 32 * step + 8 * c;
+    p.lo = p.hi = zero4();
+    if (k >= id || of < 0) return;
+    p.lo = __ldg(reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(k) * x_size));
+    if (x_size == 4) p.hi = __ldg(reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(k) * x_size) + 1);
+  };
+  if (kAhead && s0 < s1) fetch_x(now, s0);
+  uint4 ahead[kHold][4];  // of the second product: the weights, and y
+  float4 y[2];
+  auto fetch_up = [&](uint4 (&w)[4], int u, int r0) {
+    const int k = r0 + 8 * c, o = 32 * u + 4 * g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = k < r && o + i < od ? __ldg(reinterpret_cast<const uint4 *>(up + static_cast<int64_t>(o + i) * rmax + k)) : zero4();
+  };
+  auto fetch_unit = [&](int u) {
+    if (u >= u1) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) y[h] = load_y(a, s_row[2 * c + h], 32 * u + 4 * g);
+#pragma unroll
+    for (int s = 0; s < kHold; ++s) fetch_up(ahead[s], u, 32 * s);
+  };
+  for (int r0 = 0; r0 < r; r0 += kPass) {
+    const int ranks = min(r - r0, kPass);
+    float acc[kPass / 16][1][4] = {};
+    auto multiply = [&](const Piece &p) {
+      Terms xt[4];
+      if (x_size == 4) split8<true>(xt, p.lo, p.hi, t.x_type);
+      else split8<false>(xt, p.lo, p.hi, t.x_type);
+#pragma unroll
+      for (int m = 0; m < kPass / 16; ++m) {
+        if (16 * m >= ranks) break;
+        Weights8<W> u, v;
+        u.set(p.w[m][0]), v.set(p.w[m][1]);
+        product<W>(acc[m][0], u, v, xt);
+      }
+    };
+    for (int step = s0; step < s1; step += kWarps) {
+      if constexpr (kAhead) {
+        Piece next;
+        const bool more = step + kWarps < s1;
+        if (more) fetch_w(next, step + kWarps, r0), fetch_x(next, step + kWarps);
+        multiply(now);
+        if (more) now = next;
+      } else {
+        fetch_w(now, step, r0), fetch_x(now, step);
+        multiply(now);
+      }
+    }
+    if (kAhead && r0 + kPass >= r) fetch_unit(u0 + warp);
+    if (r0) __syncthreads();
+    put_part<kFew, kPass>(part, acc, ranks, warp, 0);
+    __syncthreads();
+    add_up<kFew, kPass>(mine, part, r0, r16);
+  }
+  cluster_sync();  // (part makes room, too)
+  for (int e = tid; e < r16 / 2 * kFew; e += kThreads) {
     const int pair = e / kFew, token = e % kFew;
     const Terms sum = joined<kFew>(mine, pair, token, k_tile.scale);
 #pragma unroll
-    for (int k = 0; k < kCtas; ++k) {
-      const uint32_t to = mapa_shared(smem_addr(terms + token * pitch + pair), k);
-#pragma unroll
-      for (int i = 0; i < kTerms; ++i) st_cluster(to + 4 * i * kFew * pitch, sum.w[i]);
-    }
+    for (int i = 0; i < kTerms; ++i) terms[(i * kFew + token) * pitch + pair] = sum.w[i];
   }
-  cluster_sync();
+  const int left = ((r + 31) / 32 * 32 - r16) / 2;  // pairs of ranks past r, of the last step: 0 or 8
+  for (int e = tid; e < kTerms * kFew * left; e += kThreads) terms[e / left * pitch + r16 / 2 + e % left] = 0;
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // (a CTA stays until the others have read its sums)
+  __syncthreads();
   for (int u = u0 + warp; u < u1; u += kWarps) {
     const int o = 32 * u + 4 * g;
-    float4 y[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) y[h] = load_y(a, s_row[2 * c + h], o);
+    if (!kAhead) fetch_unit(u);
     float acc[2][1][4] = {};
-    expand<W, 1>(acc, a, up, terms, kFew * pitch, pitch, r, o, 0);
+    auto multiply = [&](uint4 (&raw)[4], int r0) {
+      const int k = r0 + 8 * c;
+      Weights8<W> w[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) store_out(a, s_row[2 * c + h], o, sum_of<1>(acc, 0, h, y[h]));
+      for (int i = 0; i < 4; ++i) {
+        if (k < r && k + 8 > r) {  // columns past the rank
+          uint32_t *v = &raw[i].x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] &= k + 2 * e + 1 < r ? 0xffffffffu : k + 2 * e < r ? 0xffffu : 0u;
+        }
+        w[i].set(raw[i]);
+      }
+      Terms x[4];
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(terms + (i * kFew + g) * pitch + k / 2);
+        x[0].w[i] = v.x, x[1].w[i] = v.y, x[2].w[i] = v.z, x[3].w[i] = v.w;
+      }
+      product<W>(acc[0][0], w[0], w[1], x);
+      product<W>(acc[1][0], w[2], w[3], x);
+    };
+#pragma unroll
+    for (int s = 0; s < kHold; ++s)
+      if (32 * s < r) multiply(ahead[s], 32 * s);
+    for (int r0 = 32 * kHold; r0 < r; r0 += 32) {
+      uint4 raw[4];
+      fetch_up(raw, u, r0);
+      multiply(raw, r0);
+    }
+    float4 out[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) out[h] = sum_of<1>(acc, 0, h, y[h]);
+    if (kAhead) fetch_unit(u + kWarps);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) store_out(a, s_row[2 * c + h], o, out[h]);
   }
+  asm volatile("barrier.cluster.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- more tokens: two kernels
@@ -1008,9 +1042,10 @@ cudaError_t allow(K kernel, size_t smem) {
 template <class W>
 cudaError_t launch_few(const LoraArgs &a, cudaStream_t s) {
   const size_t smem = few_front(a.t.rank) + 4 * static_cast<size_t>(up16(a.t.rank)) * kFew;
-  const cudaError_t e = allow(lora_few_kernel<W>, smem);
+  const auto kernel = a.t.rank <= 32 ? lora_few_kernel<W, 32> : lora_few_kernel<W, 64>;
+  const cudaError_t e = allow(kernel, smem);
   if (e != cudaSuccess) return e;
-  return launch_early(lora_few_kernel<W>, static_cast<unsigned>(most_tiles(a.t.ntok, a.t.nreq, a.t.nadapters) * kCtas), 1, kThreads, smem, s, a);
+  return launch_early(kernel, static_cast<unsigned>(most_tiles(a.t.ntok, a.t.nreq, a.t.nadapters) * kCtas), 1, kThreads, smem, s, a);
 }
 
 template <class W, int kTile>

@@ -28,6 +28,11 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ uint4 ld_cluster4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ void or_cluster(uint32_t addr, uint32_t v) {
   asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -126,7 +131,7 @@ __device__ __forceinline__ void tell_all(int *array, int rank, int v) {
 // are six joins of the cluster.
 template <int kCtas>
 __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ ForkArgs a) {
-  extern __shared__ uint32_t bits[];
+  extern __shared__ __align__(16) uint32_t bits[];
   __shared__ int s_parent[kThreads], s_full[kThreads], s_need[kThreads], s_target[kThreads], s_warp[kWarps];
   __shared__ int s_copies[kCtas], s_free[kCtas];
   const Bits n(a.npages, kCtas);
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
 // L2) and written once.
 template <int kCtas>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ CompactArgs a) {
-  extern __shared__ uint32_t bits[];
+  extern __shared__ __align__(16) uint32_t bits[];
   __shared__ int s_warp[kWarps], s_held[kCtas], s_below;
   const Bits n(a.npages, kCtas);
   const int all_groups = kCtas * n.slice / kGroup, groups = n.slice / kGroup;
@@ -291,15 +296,21 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
   int base = 0, total = 0;
 #pragma unroll
   for (int c = 0; c < kCtas; ++c) base += c < rank ? s_held[c] : 0, total += s_held[c];
-  // everyone's bits and sums
-  for (int i = tid; i < kCtas * n.slice; i += kThreads)
-    own[i] = kCtas == 1 ? held[i] : ld_cluster(mapa_shared(smem_addr(held + i % n.slice), i / n.slice));
-  for (int i = tid; i < all_groups; i += kThreads) {
-    const int c = i / groups;
-    int first = 0;
+  // everyone's bits and sums: two warps take each CTA's
+  if constexpr (kCtas == 1) {
+    for (int i = tid; i < n.slice; i += kThreads) own[i] = held[i];
+    for (int i = tid; i < groups; i += kThreads) all_before[i] = mine_before[i];
+  } else {
+    constexpr int kEach = kThreads / kCtas;
+    const int c = tid / kEach, first = tid % kEach;
+    const uint32_t words_of = mapa_shared(smem_addr(held), c), sums_of = mapa_shared(smem_addr(mine_before), c);
+    int sum = 0;
 #pragma unroll
-    for (int k = 0; k < kCtas; ++k) first += k < c ? s_held[k] : 0;
-    all_before[i] = first + (kCtas == 1 ? mine_before[i] : static_cast<int>(ld_cluster(mapa_shared(smem_addr(mine_before + i % groups), c))));
+    for (int k = 0; k < kCtas; ++k) sum += k < c ? s_held[k] : 0;
+#pragma unroll 4
+    for (int i = first; i < n.slice / 4; i += kEach) reinterpret_cast<uint4 *>(own + c * n.slice)[i] = ld_cluster4(words_of + 16 * i);
+#pragma unroll 4
+    for (int i = first; i < groups; i += kEach) all_before[c * groups + i] = sum + static_cast<int>(ld_cluster(sums_of + 4 * i));
   }
   __syncthreads();
   auto held_before = [&](int id) {  // pages held below id (id <= npages, within the words there are)
