@@ -246,8 +246,18 @@ __global__ void __launch_bounds__(kListThreads) token_list_kernel(const __grid_c
   griddep_launch_dependents();
   const int width = static_cast<int>(t.tokens_width), drafted = t.draft ? t.rows - 1 : 0, nbias = static_cast<int>(t.nbias);
   const int said = !a.penalties ? 0 : t.token_lens ? t.token_lens[b] : width, prompt = t.prompt_lens ? t.prompt_lens[b] : 0;
-  const int n = max(min(said, width), 0);
   const int32_t *ids = t.tokens + b * t.tokens_stride, *draft = t.draft + b * t.draft_stride;
+  // (the first tokens of the row's width, while their number is on its way)
+  constexpr int kKept = 4;
+  int kept[kKept], bias_id = 0;
+  float bias_value = 0.0f;
+  auto load = [&](int j0, int end) {
+#pragma unroll
+    for (int u = 0; u < kKept; ++u)
+      if (j0 + u * kListThreads < end) kept[u] = ids[j0 + u * kListThreads];
+  };
+  load(tid, a.penalties ? width : 0);
+  const int n = max(min(said, width), 0);
   __syncthreads();
   int bias0 = 0, bias1 = 0;
   if (t.bias_start) {
@@ -262,15 +272,6 @@ __global__ void __launch_bounds__(kListThreads) token_list_kernel(const __grid_c
     bias0 = s_first, bias1 = max(bias0, min(end, nbias));
   }
   if (tid == 0 && said > width) record_index(a.status);
-  constexpr int kKept = 4;
-  int kept[kKept], bias_id = 0;
-  float bias_value = 0.0f;
-  auto load = [&](int j0) {
-#pragma unroll
-    for (int u = 0; u < kKept; ++u)
-      if (j0 + u * kListThreads < n) kept[u] = ids[j0 + u * kListThreads];
-  };
-  load(tid);
   if (bias0 + tid < bias1) bias_id = t.bias_ids[bias0 + tid], bias_value = t.bias_values[bias0 + tid];
   auto known = [&](int id) { return id >= 0 && id < vocab; };
   auto set = [&](int id) {
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kListThreads) token_list_kernel(const __grid_c
     else record_index(a.status);
   };
   for (int j0 = tid; j0 < n; j0 += kKept * kListThreads) {
-    if (j0 != tid) load(j0);
+    if (j0 != tid) load(j0, n);
 #pragma unroll
     for (int u = 0; u < kKept; ++u)
       if (j0 + u * kListThreads < n) set(kept[u]);
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kListThreads) token_list_kernel(const __grid_c
       return k < here ? k : -1;
     };
     for (int j0 = tid; j0 < n; j0 += kKept * kListThreads) {
-      if (n > kKept * kListThreads) load(j0);
+      if (n > kKept * kListThreads) load(j0, n);
 #pragma unroll
       for (int u = 0; u < kKept; ++u) {
         const int j = j0 + u * kListThreads, k = j < n ? place(kept[u]) : -1;
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
   }
   // The listed elements, several of a thread at once: what the list, the logits
   // and the mask have of them, and their adjusted logits.  The reads of a
-  // thread's first ones are on their way during the stream.
+  // thread's first ones are on their way during the copies, which bring their logits.
   constexpr int kListed = 2, kMore = 4;
   struct Listed {
     int at;  // -1: none
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
 #pragma unroll
     for (int u = 0; u < kHere; ++u)
       if (l[u].at >= 0) {
-        l[u].logit = to_f32(slice.src[l[u].at]);
+        if (k0 != list0) l[u].logit = to_f32(slice.src[l[u].at]);
         if (masked && !(static_cast<uint32_t>(mask[l[u].at >> 5]) >> (l[u].at & 31) & 1)) l[u].count |= kHidden;
       }
   };
@@ -498,7 +499,11 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
   if (a.sparse) {  // the listed ones leave the stream
 #pragma unroll
     for (int u = 0; u < kListed; ++u)
-      if (mine[u].at >= 0) store_low(stage + slice.place + mine[u].at);
+      if (mine[u].at >= 0) {
+        T *at = stage + slice.place + mine[u].at;
+        mine[u].logit = to_f32(*at);
+        store_low(at);
+      }
 #pragma unroll 4
     for (int k = list0 + tid + kListed * kThreads; k < list1; k += kThreads) store_low(stage + slice.place + a.list[list_base + k] - s0);
     __syncthreads();
@@ -670,11 +675,11 @@ cudaError_t launch_with(const RulesArgs &a, size_t smem, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_token_probs(RulesArgs a, const CallContext &ctx, cudaStream_t s) {
-  // CTAs of a row: four of them fit an SM with slices of 46 KB (960 rows of 100277
-  // in fp32: 196 us, with 36 KB 216, 24 KB 277); with 32 KB of 16-bit logits (120 rows
-  // of 128256: 62 us, with 46 KB 66, 20 KB 66); with few rows more, as long as
+  // CTAs of a row: slices of up to 50 KB (960 rows of 100277
+  // in fp32: 8 CTAs of a row 189 us, 9 196, 10 201, 17 277); with 32 KB of 16-bit logits (120 rows
+  // of 128256: 8 CTAs 62 us, 5 77, 6 72, 10 64, 16 70); with few rows more, as long as
   // all run at once and have 2048 elements or more
-  const int64_t rows = a.t.nreq * a.t.rows, size = a.t.type == MMQ_DT_F32 ? 4 : 2, most = (size == 4 ? 46 : 32) * 1024;
+  const int64_t rows = a.t.nreq * a.t.rows, size = a.t.type == MMQ_DT_F32 ? 4 : 2, most = (size == 4 ? 50 : 32) * 1024;
   const int64_t fit = (a.t.vocab * size + most - 1) / most, few = std::min(4 * 152 / rows, a.t.vocab / 2048);
   const int64_t ctas = std::min<int64_t>(kMostCtas, std::max<int64_t>({fit, few, 1}));
   a.ctas = static_cast<int>(ctas);
