@@ -233,6 +233,14 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The tensor cores cut what they add up off at the last bit of the largest: long
+// sums go on in fp32 proper, from sums of 32 columns (18944 columns at rank 32:
+// 1.6e-6 off in one chain, 2.3e-7 so; fp32 products by a library 6e-7).
+__device__ __forceinline__ void add(float (&sum)[4], const float (&x)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum[e] += x[e];
+}
+
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
@@ -503,7 +511,7 @@ __device__ __forceinline__ float4 sum_of(const float (&acc)[2][kEach][4], int j,
 // latency bound with few.  Up to rank 32 two pieces of A and what the second
 // product needs first are asked for ahead, in 116 registers (one token, 3584 ->
 // 4608, rank 16: 8.4 -> 6.4 us); beyond, three CTAs an SM hide more than reads
-// ahead in two do (96 tokens of 50 adapters of rank 64: 21.1 against 24.6 us), and
+// ahead in two do (96 tokens of 50 adapters of rank 64: 22.1 against 24.6 us), and
 // B comes to L2 during the first product.
 constexpr int kFew = 8;  // tokens
 template <class W, int kPass>  // ranks whose sums a warp holds at once
@@ -598,7 +606,9 @@ __global__ void __launch_bounds__(kThreads, kPass == 32 ? 2 : 3) __cluster_dims_
         if (16 * m >= ranks) break;
         Weights8<W> u, v;
         u.set(p.w[m][0]), v.set(p.w[m][1]);
-        product<W>(acc[m][0], u, v, xt);
+        float here[4] = {};
+        product<W>(here, u, v, xt);
+        add(acc[m][0], here);
       }
     };
     for (int step = s0; step < s1; step += kWarps) {
@@ -790,6 +800,7 @@ __global__ void __launch_bounds__(kThreads, kPass == 32 ? 3 : 2) __cluster_dims_
 #pragma unroll
       for (int m = 0; m < kPass / 16; ++m) {
         if (16 * m >= ranks) break;
+        float here[S::kColumns][4] = {};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           uint32_t v[4];
@@ -800,8 +811,10 @@ __global__ void __launch_bounds__(kThreads, kPass == 32 ? 3 : 2) __cluster_dims_
           Operand<W> w;
           w.set(v[0], v[1], v[2], v[3], 0);
 #pragma unroll
-          for (int j = 0; j < S::kColumns; ++j) product<W>(acc[m][j], w, xt[j][2 * i], xt[j][2 * i + 1]);
+          for (int j = 0; j < S::kColumns; ++j) product<W>(here[j], w, xt[j][2 * i], xt[j][2 * i + 1]);
         }
+#pragma unroll
+        for (int j = 0; j < S::kColumns; ++j) add(acc[m][j], here[j]);
       }
     }
     copies_wait<0>();

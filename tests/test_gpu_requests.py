@@ -624,6 +624,20 @@ def test_lora_large_values(mmq):
         _check_lora(mmq, p, start, adapters, [30], [0], 1, t)
 
 
+@pytest.mark.parametrize("lens", [[1], [30, 25], [700, 600]], ids=str)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_lora_long_sums_of_one_sign(mmq, lens, dtype):
+    """Numbers of one sign, so that every rounding counts in full and a sum cut off always errs to one side: at most 37 sums
+    of 32 columns a warp (18944 / 8 CTAs / 2 warps / 32), each of 6 steps of the tensor cores (8 more products with fp16
+    weights) of 2^-23, added up with 2^-24 each, then 2 warps and 8 CTAs; the second product's 6 steps (10); the splits 2^-26."""
+    p, _, start, t = _lora_problem(lens, [0] * len(lens), 1, 18944, 256, 32, dtype)
+    p = {**p, "x": p["x"].abs() + 1, "a": p["a"].abs() + 2.0 ** -6, "b": p["b"].abs() + 1, "y": torch.zeros_like(p["y"])}
+    got = mmq.mmq_lora(**p, plan=mmq.mmq_lora_plan(_i32([0] * len(lens)), start, t, 1))
+    want, _ = _lora_reference(p, lens, [0] * len(lens))
+    steps = (6 + 6 if dtype == BF16 else 10 + 10)
+    assert ((got.double() - want).abs() / want).max() <= (2 * steps + 37 + 10 + 2) * 2.0 ** -24
+
+
 @pytest.mark.parametrize("nreq", [1, 2, 31, 300, 1025, 8192])
 def test_lora_plan(mmq, nreq):
     """Every token of a request once, tiles of one adapter, adapters ascending and none last."""
