@@ -660,7 +660,7 @@ typedef struct mmq_lora_args {
   const int32_t *plan;      /* from mmq_lora_plan */
   int64_t x_row, y_row, out_row; /* in elements; x_row * the element's size a multiple of 16 bytes */
   int64_t ntok, nreq, nadapters; /* as in the plan */
-  int64_t id, od;           /* id a multiple of 8 */
+  int64_t id, od;           /* id a multiple of 8; both at most 2^28 (more: MMQ_ERR_UNSUPPORTED) */
   int32_t rank;             /* of the arrays a and b: a multiple of 8, at most 128 */
   int32_t type;             /* of a and b: MMQ_DT_F16 or MMQ_DT_BF16 */
   int32_t x_type;           /* MMQ_DT_F32, MMQ_DT_F16 or MMQ_DT_BF16 */
@@ -675,9 +675,9 @@ typedef struct mmq_lora_args {
  * touched.  Rows and columns of a and b past an adapter's rank are not used,
  * whatever they hold.
  *   Sums are fp32; x and the inner sums enter the tensor cores as three 16-bit
- * terms, which hold their 24 bits.  An x or an inner sum that is not finite makes its row NaN
- * (infinities among them).  The results of one problem do not change from call
- * to call.  Where adapters have more than eight tokens on the average the inner
+ * terms, which hold their 24 bits.  An x or an inner sum that is not finite
+ * (or that the first term rounds to infinity, from 3.39e38 on) makes its row
+ * NaN.  The results of one problem do not change from call to call.  Where adapters have more than eight tokens on the average the inner
  * sums are stream-ordered scratch as for mmq_gemm (6 bytes a token and rank).
  * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN, MMQ_ERR_TYPE, MMQ_ERR_OOM,
  * MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.

@@ -10,6 +10,7 @@ using mmq::aligned, mmq::aligned_elements, mmq::check_cache, mmq::cuda_rc, mmq::
 namespace {
 
 constexpr int64_t kMaxPages = int64_t(1) << 20, kMaxVocab = int64_t(1) << 18, kMaxAdapters = int64_t(1) << 18;
+constexpr int64_t kMostColumns = int64_t(1) << 28;  // of x and out: bytes in a row stay below 2^31
 
 bool is_type(int t) { return t == MMQ_DT_F32 || t == MMQ_DT_F16 || t == MMQ_DT_BF16; }
 int64_t size_of(int t) { return t == MMQ_DT_F32 ? 4 : 2; }
@@ -194,7 +195,7 @@ int mmq_lora(const mmq_lora_args *args, mmq_stream_t stream) {
   if (t.ntok < 0 || t.nreq < 0 || t.nadapters < 0 || t.id < 8 || t.id % 8 || t.od < 1 || t.rank < 8 || t.rank % 8 || t.rank > 128) return MMQ_ERR_ARG;
   for (int64_t stride : {t.x_row, t.y_row, t.out_row})
     if (!spans(t.ntok, stride)) return MMQ_ERR_ARG;
-  if (t.id > kInt32 - 64 || t.od > kInt32 - 64 * 1024 || mmq_lora_plan_words(t.ntok, t.nreq, t.nadapters) < 0) return MMQ_ERR_UNSUPPORTED;
+  if (t.id > kMostColumns || t.od > kMostColumns || mmq_lora_plan_words(t.ntok, t.nreq, t.nadapters) < 0) return MMQ_ERR_UNSUPPORTED;
   if (t.ntok == 0 || t.nreq == 0) return MMQ_OK;
   if (!t.x || !t.y || !t.out || !t.plan || (t.nadapters && (!t.a || !t.b))) return MMQ_ERR_ARG;
   if (!aligned(t.x, 16) || !aligned(t.a, 16) || !aligned(t.b, 16) || t.x_row * size_of(t.x_type) % 16) return MMQ_ERR_ALIGN;

@@ -243,7 +243,7 @@ def test_lora_checks(lib):  # noqa: F811
     for bad in (dict(x=(1 << 20) + 8), dict(a=(1 << 22) + 8), dict(b=(1 << 23) + 2), dict(x_row=66), dict(y=(1 << 21) + 2, out=(1 << 21) + 2),
                 dict(scales=4098), dict(ranks=4097), dict(plan=BASE + 1), dict(x_row=68, x_type=1)):
         assert _lora(lib, **bad) == ALIGN, bad
-    for bad in (dict(ntok=2 ** 31 // 64, x_row=0), dict(nreq=8193), dict(nadapters=2 ** 18 + 1), dict(id=2 ** 31 - 8), dict(od=2 ** 31 - 8)):
+    for bad in (dict(ntok=2 ** 31 // 64, x_row=0), dict(nreq=8193), dict(nadapters=2 ** 18 + 1), dict(id=2 ** 28 + 8), dict(od=2 ** 28 + 1)):
         assert _lora(lib, **bad) == UNSUPPORTED, bad
     assert _lora(lib, ntok=0) == 0 and _lora(lib, nreq=0) == 0
 
