@@ -35,6 +35,38 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Two numbers at once.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+// 2^((v - low) scale) of each.
+__device__ __forceinline__ float4 exponentials(const float4 &v, float low, float scale) {
+  const uint64_t l = pair(-low, -low), s = pair(scale, scale);
+  float4 e;
+  unpair(mul2(add2(pair(v.x, v.y), l), s), e.x, e.y);
+  unpair(mul2(add2(pair(v.z, v.w), l), s), e.z, e.w);
+  return make_float4(exp2_approx(e.x), exp2_approx(e.y), exp2_approx(e.z), exp2_approx(e.w));
+}
+__device__ __forceinline__ float4 times(const float4 &v, float factor) {
+  const uint64_t f = pair(factor, factor);
+  float4 p;
+  unpair(mul2(pair(v.x, v.y), f), p.x, p.y);
+  unpair(mul2(pair(v.z, v.w), f), p.z, p.w);
+  return p;
+}
 __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
@@ -474,17 +506,21 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
   uint64_t key = 0;
   // four f of the slice, elements 4 f - m on: what is not the stream's is -inf
   float4 *const fours = reinterpret_cast<float4 *>(stage + slice.place - m);
-  auto four = [&](int f) {
-    float4 v;
-    if constexpr (kWide) v = fours[f];
-    else v = load4(stage + slice.place - m + 4 * f);
+  auto plain_four = [&](int f) {
+    if constexpr (kWide) return fours[f];
+    else return load4(stage + slice.place - m + 4 * f);
+  };
+  auto four = [&](int f) {  // (what the mask hides is -inf in the slice, too, from then on)
+    float4 v = plain_four(f);
     if (masked) {
       const int e = 4 * f - m + 32;
-      const uint32_t off = __funnelshift_r(skip[e >> 5], skip[(e >> 5) + 1], e);
+      const uint32_t off = __funnelshift_r(skip[e >> 5], skip[(e >> 5) + 1], e) & 15;
       if (off & 1) v.x = -INFINITY;
       if (off & 2) v.y = -INFINITY;
       if (off & 4) v.z = -INFINITY;
       if (off & 8) v.w = -INFINITY;
+      if constexpr (!kWide)
+        if (off) *reinterpret_cast<uint2 *>(stage + slice.place - m + 4 * f) = make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
     }
     return v;
   };
@@ -513,17 +549,16 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
   float best = -INFINITY;
   for (int k = 0; k < slice.chunks; ++k) {
     const int f0 = k * kEach + tid;
-    if (t.adjusted && !a.in_place)
-      for (int f = f0; f < min((k + 1) * kEach, slice.fours); f += kThreads) adjusted.four(f, m, len, four(f));
-    if (!t.probs) continue;
     float4 x[kFours];
     float top = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kFours; ++u)
       if (f0 + u * kThreads < slice.fours) {
         x[u] = four(f0 + u * kThreads);
+        if (t.adjusted && !a.in_place) adjusted.four(f0 + u * kThreads, m, len, x[u]);
         top = fmaxf(top, fmaxf(fmaxf(x[u].x, x[u].y), fmaxf(x[u].z, x[u].w)));
       }
+    if (!t.probs) continue;
     if (greedy) {
 #pragma unroll
       for (int u = 0; u < kFours; ++u)
@@ -550,9 +585,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
 #pragma unroll
     for (int u = 0; u < kFours; ++u)
       if (f0 + u * kThreads < slice.fours) {
-        float4 &v = x[u];
-        v.x = exp2_approx((v.x - low) * scale), v.y = exp2_approx((v.y - low) * scale);
-        v.z = exp2_approx((v.z - low) * scale), v.w = exp2_approx((v.w - low) * scale);
+        const float4 v = exponentials(x[u], low, scale);
         sum += (v.x + v.y) + (v.z + v.w);
         if constexpr (kWide) fours[f0 + u * kThreads] = v;
       }
@@ -642,11 +675,9 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
         if (f >= slice.fours) break;
         float4 v;
         if constexpr (kWide) {
-          v = fours[f];
-          v.x *= share, v.y *= share, v.z *= share, v.w *= share;
+          v = times(fours[f], share);
         } else {
-          v = four(f);
-          v = make_float4(probability(v.x, 0), probability(v.y, 0), probability(v.z, 0), probability(v.w, 0));
+          v = times(exponentials(plain_four(f), base, scale), factor);
         }
         out.four(f, m, len, v);
       }
