@@ -67,9 +67,10 @@ __device__ __forceinline__ int block_exclusive(int x, int &total, int *sm) {
 
 // A CTA's share of table rows, few of which take several warps each: f(row's
 // index in the share, j, entry j) for this lane's j < limit(row), entries loaded
-// eight at a time, and fill(row, j) from there to the width.
-template <class N, class L, class F, class E>
-__device__ __forceinline__ void for_entries(int count, int width, N &&limit, L &&load, F &&f, E &&fill) {
+// eight at a time, and fill(row, j) from there to the width.  Where instead(entry)
+// points to a number, that takes the entry's place (again eight loads at a time).
+template <class N, class L, class I, class F, class E>
+__device__ __forceinline__ void for_entries(int count, int width, N &&limit, L &&load, I &&instead, F &&f, E &&fill) {
   constexpr int kBatch = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int share = count > 0 && count < kWarps ? kWarps / count : 1, rows = kWarps / share;
@@ -83,6 +84,12 @@ __device__ __forceinline__ void for_entries(int count, int width, N &&limit, L &
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
         if (j0 + u * step < n) id[u] = load(r, j0 + u * step);
+      const int *from[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) from[u] = j0 + u * step < n ? instead(id[u]) : nullptr;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (from[u]) id[u] = __ldcg(from[u]);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
         if (j0 + u * step < n) f(r, j0 + u * step, id[u]);
@@ -167,6 +174,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
   if (w >= 0) atomicMin(&a.free_pages[w], b);
   for_entries(
       mine, width, [&](int r) { return s_full[r]; }, [&](int r, int j) { return a.table[s_parent[r] * a.table_stride + j]; },
+      [](int) -> const int * { return nullptr; },
       [&](int r, int j, int id) {
         if (id >= 0 && id < npages) set_bit(own, id);
         else record_index(a.status), id = -1;
@@ -261,9 +269,11 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
   const Bits n(a.npages, kCtas);
   const int all_groups = kCtas * n.slice / kGroup, groups = n.slice / kGroup;
   // bits of the whole cache (first this CTA's rows', later everyone's), of my
-  // slice, pages held before each group of my slice, of the whole cache
+  // slice, pages held before each word within its group (up to 224), before each group of my
+  // slice, of the whole cache
   uint32_t *own = bits, *held = own + kCtas * n.slice;
-  int *mine_before = reinterpret_cast<int *>(held + n.slice), *all_before = mine_before + groups;
+  uint8_t *word_before = reinterpret_cast<uint8_t *>(held + n.slice);
+  int *mine_before = reinterpret_cast<int *>(word_before + kCtas * n.slice), *all_before = mine_before + groups;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = kCtas == 1 ? 0 : static_cast<int>(cluster_ctarank()), npages = static_cast<int>(a.npages);
   const int width = static_cast<int>(a.table_width), nreq = static_cast<int>(a.nreq);
@@ -276,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
   auto limit = [&](int r) { return min(max(a.held[row_of(r)], 0), width); };
   auto load = [&](int r, int j) { return a.table[row_of(r) * a.table_stride + j]; };
   for_entries(
-      mine, width, limit, load,
+      mine, width, limit, load, [](int) -> const int * { return nullptr; },
       [&](int, int, int id) {
         if (id >= 0 && id < npages) set_bit(own, id);
         else record_index(a.status);
@@ -297,27 +307,41 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
 #pragma unroll
   for (int c = 0; c < kCtas; ++c) base += c < rank ? s_held[c] : 0, total += s_held[c];
   // everyone's bits and sums: two warps take each CTA's
-  if constexpr (kCtas == 1) {
-    for (int i = tid; i < n.slice; i += kThreads) own[i] = held[i];
-    for (int i = tid; i < groups; i += kThreads) all_before[i] = mine_before[i];
-  } else {
-    constexpr int kEach = kThreads / kCtas;
-    const int c = tid / kEach, first = tid % kEach;
-    const uint32_t words_of = mapa_shared(smem_addr(held), c), sums_of = mapa_shared(smem_addr(mine_before), c);
+  {
+    constexpr int kThreadsEach = kThreads / kCtas;
+    const int c = tid / kThreadsEach;
+    const uint32_t words_of = kCtas == 1 ? smem_addr(held) : mapa_shared(smem_addr(held), c);
+    const uint32_t sums_of = kCtas == 1 ? smem_addr(mine_before) : mapa_shared(smem_addr(mine_before), c);
     int sum = 0;
 #pragma unroll
     for (int k = 0; k < kCtas; ++k) sum += k < c ? s_held[k] : 0;
-#pragma unroll 4
-    for (int i = first; i < n.slice / 4; i += kEach) reinterpret_cast<uint4 *>(own + c * n.slice)[i] = ld_cluster4(words_of + 16 * i);
-#pragma unroll 4
-    for (int i = first; i < groups; i += kEach) all_before[c * groups + i] = sum + static_cast<int>(ld_cluster(sums_of + 4 * i));
+#pragma unroll 2
+    for (int g = tid % kThreadsEach; g < groups; g += kThreadsEach) {
+      uint4 half[2];
+      int first;
+      if constexpr (kCtas == 1) {
+        half[0] = reinterpret_cast<const uint4 *>(held)[2 * g], half[1] = reinterpret_cast<const uint4 *>(held)[2 * g + 1], first = mine_before[g];
+      } else {
+        half[0] = ld_cluster4(words_of + 32 * g), half[1] = ld_cluster4(words_of + 32 * g + 16), first = static_cast<int>(ld_cluster(sums_of + 4 * g));
+      }
+      const int at = c * groups + g;
+      uint32_t in_group[2], here = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w[4] = {half[h].x, half[h].y, half[h].z, half[h].w};
+        in_group[h] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) in_group[h] |= here << (8 * i), here += __popc(w[i]);
+        reinterpret_cast<uint4 *>(own)[2 * at + h] = half[h];
+      }
+      reinterpret_cast<uint2 *>(word_before)[at] = make_uint2(in_group[0], in_group[1]);
+      all_before[at] = sum + first;
+    }
   }
   __syncthreads();
   auto held_before = [&](int id) {  // pages held below id (id <= npages, within the words there are)
     const int word = id >> 5, g = word / kGroup;
-    int s = all_before[g];
-    for (int i = g * kGroup; i < word; ++i) s += __popc(own[i]);
-    return s + __popc(own[word] & ((1u << (id & 31)) - 1));
+    return all_before[g] + word_before[word] + __popc(own[word] & ((1u << (id & 31)) - 1));
   };
   if (tid == 0) s_below = total < kCtas * n.slice * 32 ? held_before(total) : total;
   __syncthreads();
@@ -341,11 +365,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
   sync_all<kCtas>();
   for_entries(
       mine, 0, limit, load,
-      [&](int r, int j, int id) {
-        if (id < 0 || id >= npages) id = -1;
-        else if (id >= total) id = __ldcg(&a.pairs[2 * (held_before(id) - below) + 1]);
-        a.new_table[row_of(r) * a.new_stride + j] = id;
-      },
+      [&](int id) -> const int * { return id >= total && id < npages ? &a.pairs[2 * (held_before(id) - below) + 1] : nullptr; },
+      [&](int r, int j, int id) { a.new_table[row_of(r) * a.new_stride + j] = id < 0 || id >= npages ? -1 : id; },
       [&](int, int) {});
 }
 
@@ -419,7 +440,7 @@ template <int kCtas>
 cudaError_t launch_compact_with(const CompactArgs &a, cudaStream_t s) {
   const Bits n(a.npages, kCtas);
   const size_t groups = n.slice / kGroup;
-  const size_t smem = sizeof(uint32_t) * ((kCtas + 1) * static_cast<size_t>(n.slice) + (kCtas + 1) * groups);
+  const size_t smem = sizeof(uint32_t) * ((kCtas + 1) * static_cast<size_t>(n.slice) + (kCtas + 1) * groups) + kCtas * static_cast<size_t>(n.slice);
   return launch_cluster(compact_kernel<kCtas>, kCtas, smem, s, a);
 }
 
