@@ -65,36 +65,41 @@ __device__ __forceinline__ int block_exclusive(int x, int &total, int *sm) {
   return (warp > 0 ? up : 0) + s - x;
 }
 
-// A CTA's share of table rows, few of which take several warps each: f(row's
-// index in the share, j, entry j) for this lane's j < limit(row), entries loaded
-// eight at a time, and fill(row, j) from there to the width.  Where instead(entry)
-// points to a number, that takes the entry's place (again eight loads at a time).
-template <class N, class L, class I, class F, class E>
+// A CTA's share of table rows, by pieces of 32 kBatch entries, the rows' first ones
+// first (with a warp a row the others waited for those with long rows: 500 rows
+// compacted 18.4 us, so 16.1; 8 rows 6.1 and 4.5): f(row's index in the share, j,
+// entry j) for this lane's j < limit(row), loaded kBatch at a time, and fill(row, j)
+// from there to the width.  Where instead(entry) points to a number, that takes the
+// entry's place (again kBatch loads at a time).  Few rows go by pieces of 128 (8 rows
+// 4.5 us against 4.8), many by 256 (500 rows 16.1 against 18.2).
+template <int kBatch, class N, class L, class I, class F, class E>
 __device__ __forceinline__ void for_entries(int count, int width, N &&limit, L &&load, I &&instead, F &&f, E &&fill) {
-  constexpr int kBatch = 8;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int share = count > 0 && count < kWarps ? kWarps / count : 1, rows = kWarps / share;
-  if (warp >= rows * share) return;
-  const int step = share * 32;
-  for (int r = warp / share; r < count; r += rows) {
-    const int n = limit(r);
-    int j0 = (warp % share) * 32 + lane;
-    for (; j0 < n; j0 += kBatch * step) {
-      int id[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (j0 + u * step < n) id[u] = load(r, j0 + u * step);
-      const int *from[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) from[u] = j0 + u * step < n ? instead(id[u]) : nullptr;
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (from[u]) id[u] = __ldcg(from[u]);
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (j0 + u * step < n) f(r, j0 + u * step, id[u]);
+  constexpr int kPiece = 32 * kBatch;
+  const int lane = threadIdx.x & 31, pieces = (width + kPiece - 1) / kPiece;
+  int r = threadIdx.x >> 5, j0 = lane;
+  for (int k = 0; k < pieces * count; ++k) {
+    while (r >= count) {
+      r -= count, j0 += kPiece;
+      if (j0 - lane >= width || count == 0) return;
     }
-    for (int j = n + (warp % share) * 32 + lane; j < width; j += step) fill(r, j);
+    const int n = limit(r);
+    int id[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (j0 + 32 * u < n) id[u] = load(r, j0 + 32 * u);
+    const int *from[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) from[u] = j0 + 32 * u < n ? instead(id[u]) : nullptr;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (from[u]) id[u] = __ldcg(from[u]);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int j = j0 + 32 * u;
+      if (j < n) f(r, j, id[u]);
+      else if (j < width) fill(r, j);
+    }
+    r += kWarps;
   }
 }
 
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
   }
   sync_all<kCtas>();
   if (w >= 0) atomicMin(&a.free_pages[w], b);
-  for_entries(
+  for_entries<kCtas == 1 ? 4 : 8>(
       mine, width, [&](int r) { return s_full[r]; }, [&](int r, int j) { return a.table[s_parent[r] * a.table_stride + j]; },
       [](int) -> const int * { return nullptr; },
       [&](int r, int j, int id) {
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
   auto row_of = [&](int r) { return rank + static_cast<int64_t>(r) * kCtas; };
   auto limit = [&](int r) { return min(max(a.held[row_of(r)], 0), width); };
   auto load = [&](int r, int j) { return a.table[row_of(r) * a.table_stride + j]; };
-  for_entries(
+  for_entries<kCtas == 1 ? 4 : 8>(
       mine, width, limit, load, [](int) -> const int * { return nullptr; },
       [&](int, int, int id) {
         if (id >= 0 && id < npages) set_bit(own, id);
@@ -363,8 +368,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
   for (int i = moves + rank * kThreads + tid; i < room; i += kCtas * kThreads) reinterpret_cast<int2 *>(a.pairs)[i] = make_int2(-1, -1);
   if (rank == 0 && tid == 0) a.counts[0] = total, a.counts[1] = moves;
   sync_all<kCtas>();
-  for_entries(
-      mine, 0, limit, load,
+  for_entries<kCtas == 1 ? 4 : 8>(
+      mine, width, limit, load,
       [&](int id) -> const int * { return id >= total && id < npages ? &a.pairs[2 * (held_before(id) - below) + 1] : nullptr; },
       [&](int r, int j, int id) { a.new_table[row_of(r) * a.new_stride + j] = id < 0 || id >= npages ? -1 : id; },
       [&](int, int) {});
@@ -419,12 +424,12 @@ cudaError_t launch_cluster(K kernel, unsigned ctas, size_t smem, cudaStream_t s,
   return e != cudaSuccess ? e : launch_early(kernel, Cluster{ctas}, ctas, 1, kThreads, smem, s, a);
 }
 
-// One CTA for few entries of the table, or a cluster of sixteen.  Forks of 32 rows of
-// 128 pages take 7.4 us by one and 9.6 by sixteen, of 64 rows 10.1 and 9.9;
-// compactions, which go over the entries twice, of 8 rows of 200 7.5 and 8.3, of 32
-// rows of 128 9.0 and 8.4.
+// One CTA for few entries of the table, or a cluster of sixteen.  Forks of 64 rows of
+// 128 pages take 8.6 us by one and 9.5 by sixteen, of 64 rows of 256 11.2 and 9.8;
+// compactions, which go over the entries twice, of 32 rows of 128 6.0 and 7.1, of 64
+// rows of 128 9.9 and 7.2.
 constexpr int kMany = 16;
-constexpr int64_t kForked = 8192, kMoved = 2048;
+constexpr int64_t kForked = 8192, kMoved = 4096;
 bool one_cta(int64_t rows, int64_t width, int64_t npages, int64_t entries) {
   return rows <= kThreads && rows * width <= entries && npages <= 32768;
 }
