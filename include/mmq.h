@@ -611,8 +611,9 @@ typedef struct mmq_token_rules {
  * temperature not above 0: probability 1 for the largest x (ties: the lowest
  * v).  A row with no token left gets probabilities of 0; a NaN that no mask
  * hides (or, with a temperature, +inf) makes a row's probabilities NaN.
- * Sums are fp32; probs and adjusted are rounded once.  The results
- * of one problem do not change from call to call.
+ * Sums are fp32; probs and adjusted are rounded once.  The results of one
+ * problem do not change from call to call; a row that begins elsewhere in 16
+ * bytes of memory is added up in other groups.
  *   Tokens, drafted tokens and biases outside [0, vocab) are left out, a mask
  * row past nmasks is no mask, token_lens past tokens_width, n_draft past
  * rows - 1, bias_start past nbias are cut; all of them are reported by

@@ -793,6 +793,79 @@ def test_other_stream_and_current_device(mmq):
     assert torch.equal(got, want)
 
 
+def test_two_threads_on_two_streams(mmq):
+    """Calls with scratch at the same time: each its own."""
+    import threading
+    jobs = []
+    for seed in range(2):
+        probs = _rules_problem(5, 3, 30011, (F32, BF16)[seed], seed=seed, hist=900, bias=20)
+        lora, adapters, start, t = _lora_problem([200, 3, 90 + seed], [0, 1, 0], 2, 768, 1024, (32, 64)[seed], BF16, seed=seed)
+        plan = mmq.mmq_lora_plan(adapters, start, t, 2)
+        jobs.append((probs, lora, plan, [*mmq.mmq_token_probs(**probs, adjusted=True), mmq.mmq_lora(**lora, plan=plan)]))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(probs, lora, plan, want):
+        s = torch.cuda.Stream()
+        for _ in range(40):
+            with torch.cuda.stream(s):
+                got = [*mmq.mmq_token_probs(**probs, adjusted=True), mmq.mmq_lora(**lora, plan=plan)]
+            s.synchronize()
+            wrong.extend(k for k, (a, b) in enumerate(zip(got, want)) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=run, args=job) for job in jobs]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not wrong
+
+
+def test_a_row_for_all(mmq):
+    """Inputs that are one row seen many times (stride 0): logits, tokens, x and y."""
+    v, b = 3001, 4
+    g = torch.Generator(device="cuda").manual_seed(2)
+    logits = torch.randn((1, 1, v), generator=g, device="cuda")
+    tokens = torch.randint(0, v, (1, 50), generator=g, device="cuda", dtype=torch.int32)
+    rho = _f32([1.3] * b)
+    got, adjusted = mmq.mmq_token_probs(logits.expand(b, 1, v), tokens=tokens.expand(b, 50), repetition=rho, adjusted=True)
+    want = mmq.mmq_token_probs(logits.repeat(b, 1, 1), tokens=tokens.repeat(b, 1), repetition=rho, adjusted=True)
+    # 3001 elements: the repeated rows begin anywhere in 16 bytes of memory, so that their sums go by other groups and their
+    # exponentials against other maxima; each is within 2^-20 and 2^-23 of an exponent below 16: 2 (1 + 2) 2^-20 in all
+    assert ((got - want[0]).abs() <= 6 * 2.0 ** -20 * want[0]).all() and torch.equal(adjusted, want[1])
+    for n in (5, 300):
+        p, adapters, start, t = _lora_problem([n - 1, 1], [0, 1], 2, 256, 512, 16, BF16)
+        plan = mmq.mmq_lora_plan(adapters, start, t, 2)
+        x, y = p["x"][:1], p["y"][:1]
+        got = mmq.mmq_lora(**{**p, "x": x.expand(t, 256), "y": y.expand(t, 512)}, plan=plan)
+        assert torch.equal(got, mmq.mmq_lora(**{**p, "x": x.repeat(t, 1), "y": y.repeat(t, 1)}, plan=plan))
+
+
+@pytest.mark.parametrize("old,new,width,pages", [(3, 5, 40, 2 ** 20), (8192, 8192, 3, 30000), (40, 70, 300, 2 ** 20)])
+def test_fork_and_compact_at_the_limits(mmq, old, new, width, pages):
+    """The largest caches and the most rows: what is held, what is free and what moves, by sets."""
+    r, page = random.Random(old), 16
+    g = torch.Generator(device="cuda").manual_seed(old)
+    table = torch.randperm(pages, generator=g, device="cuda")[: old * width].view(old, width).int()
+    n = [r.randint(0, width * page) for _ in range(old)]
+    held = [-(-x // page) for x in n]
+    parents = [r.randrange(old) for _ in range(new)]
+    lens = [max(0, n[p] - r.choice([0, 0, 1, 40])) for p in parents]
+    rows = [row[:h] for row, h in zip(table.tolist(), held)]
+    f = mmq.mmq_page_fork(table, _i32(held), _i32(parents), _i32(lens), page, pages)
+    _same_fork(f, _fork_reference(rows, parents, lens, page, pages, width))
+    m = mmq.mmq_page_compact(f.block_table, f.n_blocks, pages)
+    used = sorted({x for row, k in zip(f.block_table.tolist(), f.n_blocks.tolist()) for x in row[:k]})
+    h = len(used)
+    moved = [x for x in used if x >= h]
+    to = sorted(set(range(h)) - set(used))
+    assert m.counts.tolist() == [h, len(moved)] and m.pairs[: len(moved)].tolist() == [list(x) for x in zip(moved, to)]
+    assert (m.pairs[len(moved):] == -1).all()
+    place = dict(zip(moved, to))
+    want = [[place.get(x, x) for x in row[:k]] + [-1] * (width - k) for row, k in zip(f.block_table.tolist(), f.n_blocks.tolist())]
+    assert m.block_table.tolist() == want
+
+
 def test_graphs_on_other_inputs(mmq):
     """Two captured graphs, replayed in turn on other tables, lengths, tokens and adapters."""
     page, pages, width = 8, 300, 30
