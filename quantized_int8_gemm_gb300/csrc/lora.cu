@@ -842,10 +842,17 @@ __global__ void __launch_bounds__(kThreads, kPass == 32 ? 3 : 2) __cluster_dims_
 // them and 16 tokens at a time, the next ones' y on its way.  The weights of 32
 // columns stay in registers for the tile's tokens, up to rank 64 (32 in fp16).
 // HBM bound (y in, out out).
-constexpr int kYPieces = 3;
+// Weights of up to 32 ranks in bf16 leave registers for four CTAs an SM, which hide
+// more of each other than longer stretches of a row save (64 tiles of 18944 columns,
+// both products: four CTAs with 256 columns 234 us, 512 240, 768 259; two with
+// 512 250, 768 239, 1024 247; three with 512 241).
+template <class W>
+__host__ __device__ constexpr int up_ctas(int pitch) { return pitch == 16 && Weights8<W>::kParts == 1 ? 4 : 2; }
+__host__ __device__ constexpr int y_pieces(int ctas) { return ctas == 4 ? 2 : 3; }  // of y, on their way or in use
 constexpr int kEach = 2;  // columns of eight tokens at once (four gained nothing, and spilled)
 template <class W, int kTile, int kPitch>
-__global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_constant__ LoraArgs a) {
+__global__ void __launch_bounds__(kThreads, up_ctas<W>(kPitch)) lora_up_kernel(const __grid_constant__ LoraArgs a) {
+  constexpr int kYPieces = y_pieces(up_ctas<W>(kPitch));
   constexpr int kHold = kPitch == 16 ? 1 : kPitch == 48 && Operand<W>::kParts == 1 ? 2 : 0;  // steps of 32 ranks whose weights stay
   constexpr int kWords = kTerms * kTile * kPitch;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -1006,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_const
       for (int j = 0; j < kEach; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float4 *>(rows[8 * j + h] + column) = sum_of<kEach>(acc, j, h, lds4(at + (2 * j + h) * kPart));
+          __stcs(reinterpret_cast<float4 *>(rows[8 * j + h] + column), sum_of<kEach>(acc, j, h, lds4(at + (2 * j + h) * kPart)));
     } else {
 #pragma unroll
       for (int j = 0; j < kEach; ++j)
@@ -1065,18 +1072,17 @@ template <class W, int kTile>
 cudaError_t launch_with(LoraArgs a, const CallContext &ctx, cudaStream_t s) {
   using S = Shape<kTile>;
   const int64_t tiles = most_tiles(a.t.ntok, a.t.nreq, a.t.nadapters), pitch = pitch_of(a.t.rank);
-  // columns of a CTA in the second product: many, as what it needs beside y and
-  // out comes once, but CTAs for five rounds of the SMs (64 tiles of 18944 columns:
-  // 512 columns 250 us for both products, 768 240, 1024 247, 2048 275; equal
-  // stretches of all tiles' columns for one round of CTAs 253)
-  const int64_t want = a.t.od * tiles / (5 * 2 * 152) + 128;
+  // columns of a CTA in the second product: 256 with four CTAs an SM; with two more, as
+  // what it needs beside y and out comes once, but CTAs for five rounds of the SMs
+  const int ctas = up_ctas<W>(static_cast<int>(pitch)), y_copies = y_pieces(ctas);
+  const int64_t want = ctas == 4 ? 256 : a.t.od * tiles / (5 * 2 * 152) + 128;
   a.columns = static_cast<int>(std::min<int64_t>(2048, std::max<int64_t>(256, want / 256 * 256)));
   const int64_t chunks = (a.t.od + a.columns - 1) / a.columns;
   if (tiles * chunks > 0x7fffffff) return cudaErrorNotSupported;
   a.chunks = static_cast<int>(chunks), a.by_chunks = FastDiv(a.chunks);
   const int x_size = a.t.x_type == MMQ_DT_F32 ? 4 : 2, pass = a.t.rank <= 32 ? 32 : 64, ranks = std::min(up16(a.t.rank), pass);
   a.front = std::max(kStages * S::kPiece * (kTile * x_size + ranks * 2), 4 * S::kSplit * pass * kTile);
-  const size_t down = a.front + 4 * static_cast<size_t>(up16(a.t.rank)) * kTile, left = 4 * kTerms * kTile * pitch, up = left + kYPieces * 2 * kEach * 16 * kThreads;
+  const size_t down = a.front + 4 * static_cast<size_t>(up16(a.t.rank)) * kTile, left = 4 * kTerms * kTile * pitch, up = left + y_copies * 2 * kEach * 16 * kThreads;
   const auto first = pass == 32 ? (x_size == 4 ? lora_down_kernel<W, kTile, true, 32> : lora_down_kernel<W, kTile, false, 32>)
                                 : (x_size == 4 ? lora_down_kernel<W, kTile, true, 64> : lora_down_kernel<W, kTile, false, 64>);
   const auto second = pitch == 16 ? lora_up_kernel<W, kTile, 16> : pitch == 48 ? lora_up_kernel<W, kTile, 48> : lora_up_kernel<W, kTile, 80>;
