@@ -28,6 +28,9 @@ bool apart(const Run (&written)[kWritten], const Run (&read)[kRead], const Run &
   }
   for (const Run &x : read)
     if (meet(x, new_rows)) return false;
+  Run whole = new_rows;  // (rows by rows only where the whole stretches meet: halves of wider rows do)
+  whole.bytes += new_rows.rows ? (new_rows.rows - 1) * new_rows.pitch : 0, whole.rows = 1;
+  if (!meet(whole, old_rows)) return true;
   for (uint64_t r = 0; r < new_rows.rows; ++r) {
     Run row = new_rows;
     row.at += r * row.pitch, row.rows = 1;
