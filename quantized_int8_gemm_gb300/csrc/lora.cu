@@ -201,9 +201,6 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const __grid_co
 constexpr int kCtas = 8, kThreads = 256, kWarps = kThreads / 32;
 constexpr int kStages = 3;
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
