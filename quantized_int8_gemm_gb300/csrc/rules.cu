@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
       }
       continue;
     }
-    const float low = top == -INFINITY ? 0.0f : top;
+    const float low = top == -INFINITY ? 0.0f : top;  // (-inf less -inf is no number)
     float sum = 0.0f;
 #pragma unroll
     for (int u = 0; u < kFours; ++u)
@@ -590,8 +590,10 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
         if constexpr (kWide) fours[f0 + u * kThreads] = v;
       }
     if constexpr (kWide) s_from[k][tid] = low;
+    // (against top, not low: where there is nothing, 0 or NaN times 2^-inf = 0; 2^(0 - largest)
+    // may be infinite)
     part.raise(top, scale);
-    part.sum += sum * exp2_approx((low - part.from()) * scale);
+    part.sum += sum * exp2_approx((top - part.from()) * scale);
   }
   // the listed ones
   float my_y[kListed];
