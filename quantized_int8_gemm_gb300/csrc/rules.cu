@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
   __shared__ __align__(8) uint64_t s_bars[kChunks], s_told;
   __shared__ uint64_t s_warp[kWarps], s_all[kMostCtas], s_word;
   __shared__ int s_draft[kDrafted];
-  __shared__ float s_from[kWide ? kChunks : 1][kThreads];  // what each thread's exponentials of a copy are against
+  __shared__ float s_from[kWide ? kChunks : 1][kThreads];  // what each thread's exponentials of a copy are against; -inf where all are 0 (or NaN)
   const mmq_token_rules &t = a.t;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank()), row = a.by_ctas(static_cast<int>(blockIdx.x)), b = a.by_rows(row), i = row - b * t.rows;
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
         sum += (v.x + v.y) + (v.z + v.w);
         if constexpr (kWide) fours[f0 + u * kThreads] = v;
       }
-    if constexpr (kWide) s_from[k][tid] = low;
+    if constexpr (kWide) s_from[k][tid] = top;
     // (against top, not low: where there is nothing, 0 or NaN times 2^-inf = 0; 2^(0 - largest)
     // may be infinite)
     part.raise(top, scale);
