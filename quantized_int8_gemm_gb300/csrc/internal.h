@@ -209,6 +209,8 @@ struct PageCopyArgs {
 };
 cudaError_t launch_page_copy(PageCopyArgs a, cudaStream_t s);
 
+constexpr int64_t kMaxListed = 0x7fffffff / 18;  // requests with lists, whose `starts` are counted in 32 bits
+
 struct RulesArgs {
   mmq_token_rules t;
   bool penalties, sparse, in_place;  // tokens are counted; there are lists; adjusted is the logits

@@ -158,14 +158,15 @@ int mmq_token_probs(const mmq_token_rules *args, mmq_stream_t stream) {
     if (t.probs && meet(run(t.probs, t.probs_type, t.probs_req, t.probs_row), r)) return MMQ_ERR_ARG;
     if (t.adjusted && meet(run(t.adjusted, t.adjusted_type, t.adjusted_req, t.adjusted_row), r)) return MMQ_ERR_ARG;
   }
-  mmq::CallContext ctx;
-  if (int rc = mmq::call_context(&ctx)) return rc;
   mmq::RulesArgs a;
   a.t = t;
   if (!t.tokens) a.t.tokens_width = 0;
   if (t.nbias == 0) a.t.bias_start = nullptr;
   a.in_place = same;
   a.penalties = (a.t.tokens_width > 0 || (t.draft && t.rows > 1)) && (t.repetition || t.frequency || t.presence);
+  if ((a.penalties || a.t.bias_start) && t.nreq > mmq::kMaxListed) return MMQ_ERR_UNSUPPORTED;
+  mmq::CallContext ctx;
+  if (int rc = mmq::call_context(&ctx)) return rc;
   a.status = &ctx.words->status, a.abort_epoch = &ctx.words->abort_epoch, a.epoch = ctx.epoch, a.limit_ns = ctx.limit_ns;
   return cuda_rc(mmq::launch_token_probs(a, ctx, reinterpret_cast<cudaStream_t>(stream)));
 }

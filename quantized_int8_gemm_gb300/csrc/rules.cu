@@ -230,6 +230,7 @@ constexpr int kListThreads = 1024;
 constexpr int kEntries = 4096;           // listed tokens that are worked out at once
 constexpr int kDrafted = 32;              // drafted tokens that a row's CTAs keep at hand
 constexpr int kStarts = kMostCtas + 2;   // numbers for a request: where each CTA's part of its list begins, the first bias
+static_assert(kMaxListed * kStarts <= 0x7fffffff, "b * kStarts is an int");
 
 // Sum of x over the threads before this one, and over all.
 __device__ __forceinline__ int block_exclusive(int x, int &total, int *sm) {
