@@ -22,6 +22,7 @@ constexpr int kMostSlice = 16384 + 40;
 constexpr unsigned kAll = 0xffffffffu;
 // Of a listed token's count: it is among the prompt's; it has a bias; the row's mask hides it.
 constexpr uint32_t kMet = 0x80000000u, kBiased = 0x40000000u, kHidden = 0x20000000u;
+static_assert(kMaxSaid < kHidden, "a count does not reach the flags");
 
 // 8 bytes into another CTA's shared memory, counted by a barrier beside them
 // (both addresses from mapa_shared): no fence, as a store and a cluster barrier
