@@ -620,10 +620,12 @@ typedef struct mmq_token_rules {
  * mmq_last_device_error.
  * What is written may overlap nothing else of the call (MMQ_ERR_ARG), but for
  * adjusted in the logits' place.
- * vocab in 1..2^18, tokens_width below 2^29, nreq*rows below 2^27, nreq with penalized tokens or with
- * biases at most 119304647 (more: MMQ_ERR_UNSUPPORTED).  With such
- * tokens or biases each request's are listed first, in stream-ordered scratch as for
- * mmq_gemm (12 bytes for each token and bias).
+ * vocab in 1..2^18, tokens_width below 2^29, nbias at most 2^31 - 2048,
+ * nreq*rows below 2^27, nreq with penalized tokens or with biases at most
+ * 119304647 (more: MMQ_ERR_UNSUPPORTED).  With such tokens or biases each
+ * request's are listed first, in stream-ordered scratch as for mmq_gemm (12
+ * bytes for each token of the rows' width, drafted token and bias, 72 a
+ * request).
  * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN (elements off their own alignment),
  * MMQ_ERR_TYPE, MMQ_ERR_OOM, MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE,
  * MMQ_ERR_CUDA.

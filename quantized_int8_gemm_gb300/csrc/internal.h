@@ -210,6 +210,7 @@ struct PageCopyArgs {
 cudaError_t launch_page_copy(PageCopyArgs a, cudaStream_t s);
 
 constexpr int64_t kMaxSaid = (int64_t(1) << 29) - 1;  // tokens of a request, so that a count of them lies below its flags
+constexpr int64_t kMaxBiases = 0x7fffffff - 2047;     // so that rounds of 1024 behind the last one stay in 32 bits
 constexpr int64_t kMaxListed = 0x7fffffff / 18;  // requests with lists, whose `starts` are counted in 32 bits
 
 struct RulesArgs {

@@ -120,7 +120,7 @@ int mmq_token_probs(const mmq_token_rules *args, mmq_stream_t stream) {
   for (int64_t stride : {t.logits_row, t.probs_row, t.adjusted_row})
     if (!spans(t.rows, stride)) return MMQ_ERR_ARG;
   if (!spans(t.nmasks, t.mask_stride)) return MMQ_ERR_ARG;
-  if (t.vocab > kMaxVocab || t.tokens_width > mmq::kMaxSaid) return MMQ_ERR_UNSUPPORTED;
+  if (t.vocab > kMaxVocab || t.tokens_width > mmq::kMaxSaid || t.nbias > mmq::kMaxBiases) return MMQ_ERR_UNSUPPORTED;
   if (t.nreq > ((int64_t(1) << 27) - 1) / t.rows) return MMQ_ERR_UNSUPPORTED;
   if (t.nreq == 0) return MMQ_OK;
   if (!t.logits || (!t.probs && !t.adjusted) || (t.tokens_width && !t.tokens) || (t.nbias && (!t.bias_ids || !t.bias_values))) return MMQ_ERR_ARG;

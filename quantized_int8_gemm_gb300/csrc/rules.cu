@@ -228,6 +228,7 @@ __device__ __forceinline__ uint64_t candidate(float x, int v) {
 
 // ---------------------------------------------------------------- the request's tokens and biases
 constexpr int kListThreads = 1024;
+static_assert(kMaxBiases + 2 * kListThreads - 1 <= 0x7fffffff, "numbers of biases are ints");
 constexpr int kEntries = 4096;           // listed tokens that are worked out at once
 constexpr int kDrafted = 32;              // drafted tokens that a row's CTAs keep at hand
 constexpr int kStarts = kMostCtas + 2;   // numbers for a request: where each CTA's part of its list begins, the first bias

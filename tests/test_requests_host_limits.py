@@ -22,9 +22,16 @@ def test_the_most_requests(lib):  # noqa: F811
     assert _probs(lib, MANY, nreq=2 ** 27 - 1) == NO_DEVICE  # no lists
     assert _probs(lib, MANY, nreq=2 ** 27 - 1, tokens=4096, tokens_width=1) == NO_DEVICE  # no penalties, so that no tokens are counted
     assert _probs(lib, MANY, nreq=1, **{**LISTS, "tokens_width": 2 ** 29 - 1}) == NO_DEVICE
+    assert _probs(lib, MANY, nreq=1, bias_start=4096, bias_ids=1 << 41, bias_values=1 << 42, nbias=2 ** 31 - 2048) == NO_DEVICE
 
 
 def test_tokens_that_a_count_has_no_bits_for(lib):  # noqa: F811
     """A listed token's count lies in the 29 bits below its flags: said 2^29 times it would be a hidden one."""
     for width in (2 ** 29, 2 ** 31 - 1):
         assert _probs(lib, MANY, nreq=1, **{**LISTS, "tokens_width": width}) == UNSUPPORTED
+
+
+def test_biases_whose_numbers_would_wrap(lib):  # noqa: F811
+    """A CTA's threads go over the biases 1024 at a time, in 32 bits."""
+    for n in (2 ** 31 - 2047, 2 ** 31 - 1):
+        assert _probs(lib, MANY, nreq=1, bias_start=4096, bias_ids=1 << 41, bias_values=1 << 42, nbias=n) == UNSUPPORTED
