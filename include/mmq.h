@@ -525,10 +525,10 @@ int mmq_verify_draft(const mmq_verification *args, mmq_stream_t stream);
  * own.  An entry of parents or of a row outside its range (the page becomes
  * -1), or lens[b] beyond what its parent holds, is reported by
  * mmq_last_device_error.  What is written may overlap nothing else of the
- * call (MMQ_ERR_ARG).  nold, nnew in 0..8192, npages in 0..2^20 (more:
- * MMQ_ERR_UNSUPPORTED).  One kernel, no scratch.  Errors: MMQ_ERR_ARG,
- * MMQ_ERR_ALIGN (elements off their own alignment), MMQ_ERR_UNSUPPORTED,
- * MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
+ * call (MMQ_ERR_ARG).  nold, nnew in 0..8192, npages in 0..2^20, table_width
+ * at most 2^31 - 1024 (more: MMQ_ERR_UNSUPPORTED).  One kernel, no scratch.
+ * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN (elements off their own alignment),
+ * MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
  */
 typedef struct mmq_fork {
   const int32_t *table, *held, *parents, *lens;

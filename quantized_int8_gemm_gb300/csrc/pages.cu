@@ -74,7 +74,7 @@ __device__ __forceinline__ int block_exclusive(int x, int &total, int *sm) {
 // 4.5 us against 4.8), many by 256 (500 rows 16.1 against 18.2).
 template <int kBatch, class N, class L, class I, class F, class E>
 __device__ __forceinline__ void for_entries(int count, int width, N &&limit, L &&load, I &&instead, F &&f, E &&fill) {
-  constexpr int kPiece = 32 * kBatch;
+  constexpr int kPiece = 32 * kBatch;  // (a width is 1023 below 2^31 - 1 at the most, so that j0 + kPiece does not wrap)
   const int lane = threadIdx.x & 31, pieces = (width + kPiece - 1) / kPiece;
   int r = threadIdx.x >> 5, j0 = lane;
   for (int k = 0; k < pieces * count; ++k) {

@@ -10,6 +10,7 @@ using mmq::aligned, mmq::aligned_elements, mmq::check_cache, mmq::cuda_rc, mmq::
 namespace {
 
 constexpr int64_t kMaxPages = int64_t(1) << 20, kMaxVocab = int64_t(1) << 18, kMaxAdapters = int64_t(1) << 18;
+constexpr int64_t kMaxWidth = kInt32 - 1023;  // of page tables: columns of a round of warps behind the last one stay in 32 bits
 constexpr int64_t kMostColumns = int64_t(1) << 28;  // of x and out: bytes in a row stay below 2^31
 
 bool is_type(int t) { return t == MMQ_DT_F32 || t == MMQ_DT_F16 || t == MMQ_DT_BF16; }
@@ -59,7 +60,7 @@ int mmq_page_fork(const mmq_fork *args, mmq_stream_t stream) {
   if (!table_fits(t.nold, t.table_width, t.table_stride) || !table_fits(t.nnew, t.table_width, t.new_stride) || t.npages < 0 ||
       t.page_size < 1)
     return MMQ_ERR_ARG;
-  if (t.nold > kMaxRequests || t.nnew > kMaxRequests || t.npages > kMaxPages) return MMQ_ERR_UNSUPPORTED;
+  if (t.nold > kMaxRequests || t.nnew > kMaxRequests || t.npages > kMaxPages || t.table_width > kMaxWidth) return MMQ_ERR_UNSUPPORTED;
   if (!t.counts || (t.npages && !t.free_pages)) return MMQ_ERR_ARG;
   if (t.nold && (!t.held || (t.table_width && !t.table))) return MMQ_ERR_ARG;
   if (t.nnew && (!t.parents || !t.lens || !t.held_out || !t.pairs || !t.tokens || (t.table_width && !t.new_table))) return MMQ_ERR_ARG;
@@ -80,7 +81,7 @@ int mmq_page_compact(const int32_t *table, const int32_t *held, int64_t nreq, in
                      int64_t npages, int32_t *new_table, int64_t new_stride, int32_t *pairs, int32_t *counts,
                      mmq_stream_t stream) {
   if (!table_fits(nreq, table_width, table_stride) || !table_fits(nreq, table_width, new_stride) || npages < 0) return MMQ_ERR_ARG;
-  if (nreq > kMaxRequests || npages > kMaxPages) return MMQ_ERR_UNSUPPORTED;
+  if (nreq > kMaxRequests || npages > kMaxPages || table_width > kMaxWidth) return MMQ_ERR_UNSUPPORTED;
   if (!counts || (npages > 1 && !pairs) || (nreq && (!held || (table_width && (!table || !new_table))))) return MMQ_ERR_ARG;
   if (!aligned_elements(table, held, new_table, counts) || !aligned(pairs, 8)) return MMQ_ERR_ALIGN;
   const Run written[] = {{pairs, npages / 2 * 2}, {counts, 2}};
