@@ -185,6 +185,13 @@ struct VerifyArgs {
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s);
 
 // ---- what differs from request to request (pages.cu, rules.cu, lora.cu) ----
+// The most of each that the entry points take.  How much shared memory a kernel may
+// have is a setting of the kernel on its device, not of a call, so it is always that
+// of the most, whatever a call needs: set to a call's own, a small call of one thread
+// between another's setting and launch made that launch fail.
+constexpr int64_t kMaxPages = int64_t(1) << 20, kMaxVocab = int64_t(1) << 18, kMaxAdapters = int64_t(1) << 18;
+constexpr int kMaxRank = 128;
+
 struct ForkArgs : mmq_fork {
   int *status;
 };

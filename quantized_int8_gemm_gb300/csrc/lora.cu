@@ -1054,18 +1054,18 @@ int64_t most_tiles(int64_t ntok, int64_t nreq, int64_t nadapters) {
   return std::min(ntok, ntok / tile_of(ntok, nreq, nadapters) + std::min(nreq, nadapters + 1));
 }
 
+// most: bytes of shared memory of the kernel's largest rank, for every call.
 template <class K>
-cudaError_t allow(K kernel, size_t smem) {
+cudaError_t allow(K kernel, size_t smem, size_t most) {
   if (smem <= 46 * 1024) return cudaSuccess;  // (beside the static arrays, within the 48 KB that need no leave)
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
 }
 
 template <class W>
 cudaError_t launch_few(const LoraArgs &a, cudaStream_t s) {
   const size_t smem = few_front(a.t.rank) + 4 * static_cast<size_t>(up16(a.t.rank)) * kFew;
+  static_assert(few_front(kMaxRank) + 4 * up16(kMaxRank) * kFew <= 46 * 1024, "within what needs no leave");
   const auto kernel = a.t.rank <= 32 ? lora_few_kernel<W, 32> : lora_few_kernel<W, 64>;
-  const cudaError_t e = allow(kernel, smem);
-  if (e != cudaSuccess) return e;
   return launch_early(kernel, static_cast<unsigned>(most_tiles(a.t.ntok, a.t.nreq, a.t.nadapters) * kCtas), 1, kThreads, smem, s, a);
 }
 
@@ -1081,14 +1081,16 @@ cudaError_t launch_with(LoraArgs a, const CallContext &ctx, cudaStream_t s) {
   const int64_t chunks = (a.t.od + a.columns - 1) / a.columns;
   if (tiles * chunks > 0x7fffffff) return cudaErrorNotSupported;
   a.chunks = static_cast<int>(chunks), a.by_chunks = FastDiv(a.chunks);
-  const int x_size = a.t.x_type == MMQ_DT_F32 ? 4 : 2, pass = a.t.rank <= 32 ? 32 : 64, ranks = std::min(up16(a.t.rank), pass);
-  a.front = std::max(kStages * S::kPiece * (kTile * x_size + ranks * 2), 4 * S::kSplit * pass * kTile);
-  const size_t down = a.front + 4 * static_cast<size_t>(up16(a.t.rank)) * kTile, left = 4 * kTerms * kTile * pitch, up = left + y_copies * 2 * kEach * 16 * kThreads;
+  const int x_size = a.t.x_type == MMQ_DT_F32 ? 4 : 2, pass = a.t.rank <= 32 ? 32 : 64;
+  auto front = [&](int rank) { return std::max(kStages * S::kPiece * (kTile * x_size + std::min(up16(rank), pass) * 2), 4 * S::kSplit * pass * kTile); };
+  auto down_bytes = [&](int rank) { return front(rank) + 4 * static_cast<size_t>(up16(rank)) * kTile; };
+  a.front = front(a.t.rank);
+  const size_t down = down_bytes(a.t.rank), left = 4 * kTerms * kTile * pitch, up = left + y_copies * 2 * kEach * 16 * kThreads;
   const auto first = pass == 32 ? (x_size == 4 ? lora_down_kernel<W, kTile, true, 32> : lora_down_kernel<W, kTile, false, 32>)
                                 : (x_size == 4 ? lora_down_kernel<W, kTile, true, 64> : lora_down_kernel<W, kTile, false, 64>);
   const auto second = pitch == 16 ? lora_up_kernel<W, kTile, 16> : pitch == 48 ? lora_up_kernel<W, kTile, 48> : lora_up_kernel<W, kTile, 80>;
-  cudaError_t e = allow(first, down);
-  if (e == cudaSuccess) e = allow(second, up);
+  cudaError_t e = allow(first, down, down_bytes(pass == 32 ? 32 : kMaxRank));
+  if (e == cudaSuccess) e = allow(second, up, up);  // (the kernel's own, for every rank that it takes)
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (e == cudaSuccess) e = cudaStreamIsCapturing(s, &cap);
   if (e != cudaSuccess) return e;
@@ -1121,11 +1123,13 @@ cudaError_t launch_lora_plan(LoraPlanArgs a, cudaStream_t s) {
   while (a.slots < a.nreq) a.slots *= 2;
   a.few = a.slots <= 1024;  // (up to 1024 keys are compared with all: 256 reads; sorting them takes 55 steps with barriers)
   const size_t smem = ((a.few ? 5 : 4) * static_cast<size_t>(a.slots) + 2) * 4;
+  constexpr int kMost = (4 * kMaxRequests + 2) * 4;
+  static_assert((kMaxRequests & (kMaxRequests - 1)) == 0 && kMaxRequests == 1 << kRequestBits, "the slots of the most requests");
   // (few requests of few tokens: fewer warps to meet, one request 3.1 instead of 3.7 us, 96 4.9
   // instead of 5.4)
   if (a.slots <= 128 && a.ntok <= 512) return launch_early(lora_plan_kernel<128>, 1, 1, 128, smem, s, a);
   if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(lora_plan_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = cudaFuncSetAttribute(lora_plan_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
   const int64_t ctas = std::max<int64_t>(1, (a.ntok + kPlanTokens - 1) / kPlanTokens);

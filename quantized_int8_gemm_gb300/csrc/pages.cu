@@ -415,12 +415,13 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     if (dst[u]) *dst[u] = x[u];
 }
 
+// most: bytes of shared memory of the largest cache, for every call.
 template <class K, class A>
-cudaError_t launch_cluster(K kernel, unsigned ctas, size_t smem, cudaStream_t s, const A &a) {
+cudaError_t launch_cluster(K kernel, unsigned ctas, size_t smem, size_t most, cudaStream_t s, const A &a) {
   cudaError_t e = cudaSuccess;
   if (ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && smem > 24 * 1024)  // (beside the static arrays, within the 48 KB that need no leave)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
   return e != cudaSuccess ? e : launch_early(kernel, Cluster{ctas}, ctas, 1, kThreads, smem, s, a);
 }
 
@@ -430,23 +431,29 @@ cudaError_t launch_cluster(K kernel, unsigned ctas, size_t smem, cudaStream_t s,
 // rows of 128 9.9 and 7.2.
 constexpr int kMany = 16;
 constexpr int64_t kForked = 8192, kMoved = 4096;
+constexpr int64_t kFewPages = 32768;
 bool one_cta(int64_t rows, int64_t width, int64_t npages, int64_t entries) {
-  return rows <= kThreads && rows * width <= entries && npages <= 32768;
+  return rows <= kThreads && rows * width <= entries && npages <= kFewPages;
 }
+constexpr int64_t most_pages(int ctas) { return ctas == 1 ? kFewPages : kMaxPages; }
 
+size_t fork_bytes(int64_t pages, int ctas) {
+  const Bits n(pages, ctas);
+  return sizeof(uint32_t) * (n.words + 2 * static_cast<size_t>(n.slice));
+}
 template <int kCtas>
 cudaError_t launch_fork_with(const ForkArgs &a, cudaStream_t s) {
-  const Bits n(a.npages, kCtas);
-  const size_t smem = sizeof(uint32_t) * (n.words + 2 * static_cast<size_t>(n.slice));
-  return launch_cluster(fork_kernel<kCtas>, kCtas, smem, s, a);
+  return launch_cluster(fork_kernel<kCtas>, kCtas, fork_bytes(a.npages, kCtas), fork_bytes(most_pages(kCtas), kCtas), s, a);
 }
 
+size_t compact_bytes(int64_t pages, int ctas) {
+  const Bits n(pages, ctas);
+  const size_t groups = n.slice / kGroup;
+  return sizeof(uint32_t) * ((ctas + 1) * static_cast<size_t>(n.slice) + (ctas + 1) * groups) + ctas * static_cast<size_t>(n.slice);
+}
 template <int kCtas>
 cudaError_t launch_compact_with(const CompactArgs &a, cudaStream_t s) {
-  const Bits n(a.npages, kCtas);
-  const size_t groups = n.slice / kGroup;
-  const size_t smem = sizeof(uint32_t) * ((kCtas + 1) * static_cast<size_t>(n.slice) + (kCtas + 1) * groups) + kCtas * static_cast<size_t>(n.slice);
-  return launch_cluster(compact_kernel<kCtas>, kCtas, smem, s, a);
+  return launch_cluster(compact_kernel<kCtas>, kCtas, compact_bytes(a.npages, kCtas), compact_bytes(most_pages(kCtas), kCtas), s, a);
 }
 
 }  // namespace

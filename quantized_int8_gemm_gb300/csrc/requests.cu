@@ -5,11 +5,11 @@
 #include "checks.h"
 #include "internal.h"
 
-using mmq::aligned, mmq::aligned_elements, mmq::check_cache, mmq::cuda_rc, mmq::kInt32, mmq::kMaxRequests, mmq::meet, mmq::Run;
+using mmq::aligned, mmq::aligned_elements, mmq::check_cache, mmq::cuda_rc, mmq::kInt32, mmq::kMaxAdapters, mmq::kMaxPages, mmq::kMaxRequests,
+    mmq::kMaxVocab, mmq::meet, mmq::Run;
 
 namespace {
 
-constexpr int64_t kMaxPages = int64_t(1) << 20, kMaxVocab = int64_t(1) << 18, kMaxAdapters = int64_t(1) << 18;
 constexpr int64_t kMaxWidth = kInt32 - 1023;  // of page tables: columns of a round of warps behind the last one stay in 32 bits
 constexpr int64_t kMostColumns = int64_t(1) << 28;  // of x and out: bytes in a row stay below 2^31
 
@@ -197,7 +197,7 @@ int mmq_lora(const mmq_lora_args *args, mmq_stream_t stream) {
   if (!args) return MMQ_ERR_ARG;
   const mmq_lora_args &t = *args;
   if ((t.type != MMQ_DT_F16 && t.type != MMQ_DT_BF16) || !is_type(t.x_type)) return MMQ_ERR_TYPE;
-  if (t.ntok < 0 || t.nreq < 0 || t.nadapters < 0 || t.id < 8 || t.id % 8 || t.od < 1 || t.rank < 8 || t.rank % 8 || t.rank > 128) return MMQ_ERR_ARG;
+  if (t.ntok < 0 || t.nreq < 0 || t.nadapters < 0 || t.id < 8 || t.id % 8 || t.od < 1 || t.rank < 8 || t.rank % 8 || t.rank > mmq::kMaxRank) return MMQ_ERR_ARG;
   for (int64_t stride : {t.x_row, t.y_row, t.out_row})
     if (!spans(t.ntok, stride)) return MMQ_ERR_ARG;
   if (t.id > kMostColumns || t.od > kMostColumns || mmq_lora_plan_words(t.ntok, t.nreq, t.nadapters) < 0) return MMQ_ERR_UNSUPPORTED;

@@ -697,12 +697,16 @@ __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_c
   }
 }
 
+// Bytes of shared memory: of a row's CTA with that many elements, of a request's list.
+size_t row_bytes(size_t slice, size_t size, bool mask) { return (slice + 16) * size + (mask ? 4 * (slice / 32 + 2) : 0); }
+size_t list_bytes(size_t vocab) { return 8 * ((vocab + 31) / 32) + 12 * kEntries; }
+
 template <class T>
 cudaError_t launch_with(const RulesArgs &a, size_t smem, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (a.ctas > 8) e = cudaFuncSetAttribute(token_probs_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && smem > 40 * 1024)  // (beside the static arrays, within the 48 KB that need no leave)
-    e = cudaFuncSetAttribute(token_probs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    e = cudaFuncSetAttribute(token_probs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(row_bytes(kMostSlice, sizeof(T), true)));
   if (e != cudaSuccess) return e;
   const unsigned ctas = a.ctas;
   return launch_early(token_probs_kernel<T>, Cluster{ctas}, static_cast<unsigned>(a.t.nreq * a.t.rows) * ctas, 1, kThreads, smem, s, a);
@@ -737,11 +741,10 @@ cudaError_t launch_token_probs(RulesArgs a, const CallContext &ctx, cudaStream_t
     a.list = a.starts + a.t.nreq * kStarts;
     a.counts = reinterpret_cast<uint32_t *>(a.list + listed);
     a.biases = reinterpret_cast<float *>(a.counts + listed);
-    const size_t smem = 8 * ((a.t.vocab + 31) / 32) + 12 * kEntries;
-    e = cudaFuncSetAttribute(token_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e == cudaSuccess) e = launch_early(token_list_kernel, static_cast<unsigned>(a.t.nreq), 1, kListThreads, smem, s, a);
+    e = cudaFuncSetAttribute(token_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(list_bytes(kMaxVocab)));
+    if (e == cudaSuccess) e = launch_early(token_list_kernel, static_cast<unsigned>(a.t.nreq), 1, kListThreads, list_bytes(a.t.vocab), s, a);
   }
-  const size_t smem = (a.slice + 16) * size + (a.t.mask ? 4 * (a.slice / 32 + 2) : 0);
+  const size_t smem = row_bytes(a.slice, size, a.t.mask);
   if (e == cudaSuccess) {
     if (a.t.type == MMQ_DT_F32) e = launch_with<float>(a, smem, s);
     else e = a.t.type == MMQ_DT_F16 ? launch_with<__half>(a, smem, s) : launch_with<__nv_bfloat16>(a, smem, s);
