@@ -2,6 +2,8 @@
 // request in a serving step (declared in mmq.h): argument checks and launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "checks.h"
 #include "internal.h"
 
@@ -47,8 +49,42 @@ bool table_fits(int64_t nreq, int64_t width, int64_t stride) {
 // Whether n strides stay below any memory there is.
 bool spans(int64_t n, int64_t stride) { return stride >= 0 && stride <= (int64_t(1) << 48) / (n > 0 ? n : 1); }
 
-// The elements of (blocks, rows, n) in strides end on this one.
-int64_t extent(int64_t blocks, int64_t rows, int64_t n, int64_t block, int64_t row) { return (blocks - 1) * block + (rows - 1) * row + n; }
+// Rows of n elements in two strides: blocks of rows, the larger stride between blocks.
+struct Rows {
+  Run block;  // the first one's
+  uint64_t pitch, blocks;
+  template <class T>
+  Rows(const T *p, int64_t n, int64_t s0, int64_t n0, int64_t s1 = 0, int64_t n1 = 1)
+      : block(p, p ? n : 0, std::min(s0, s1), s0 < s1 ? n0 : n1), pitch(std::max(s0, s1) * sizeof(T)), blocks(s0 < s1 ? n1 : n0) {}
+  uint64_t block_bytes() const { return (block.rows - 1) * block.pitch + block.bytes; }
+};
+bool meet(const Run &a, const Rows &b) {
+  if (!a.bytes || !b.block.bytes || !b.block.rows || !b.blocks) return false;
+  // from the first block that ends behind a's begin to the last that begins in front of its end
+  const uint64_t bytes = b.block_bytes(), blocks = b.pitch ? b.blocks : 1;
+  Run block = b.block;
+  uint64_t k = a.at < block.at + bytes ? 0 : b.pitch ? (a.at - block.at - bytes) / b.pitch + 1 : 1;
+  for (block.at += k * b.pitch; k < blocks && block.at < a.at + a.bytes; ++k, block.at += b.pitch)
+    if (mmq::meet(a, block)) return true;
+  return false;
+}
+// Row by row only where the whole stretches meet (halves of wider rows do).
+bool meet(const Rows &a, const Rows &b) {
+  auto whole = [](const Rows &r) {
+    Run w = r.block;
+    if (w.bytes && r.block.rows && r.blocks) w.bytes = (r.blocks - 1) * r.pitch + r.block_bytes();
+    w.rows = 1;
+    return w;
+  };
+  if (!mmq::meet(whole(a), whole(b))) return false;
+  for (uint64_t k = 0; k < a.blocks; ++k)
+    for (uint64_t i = 0; i < a.block.rows; ++i) {
+      Run row = a.block;
+      row.at += k * a.pitch + i * a.block.pitch, row.rows = 1;
+      if (meet(row, b)) return true;
+    }
+  return false;
+}
 
 }  // namespace
 
@@ -131,34 +167,26 @@ int mmq_token_probs(const mmq_token_rules *args, mmq_stream_t stream) {
                         t.bias_start, t.bias_ids, t.bias_values, t.mask, t.mask_rows))
     return MMQ_ERR_ALIGN;
   // what is written overlaps no row that another cluster reads or writes
-  auto run = [&](const void *p, int type, int64_t req, int64_t row) {
-    return Run(static_cast<const char *>(p), size_of(type) * extent(t.nreq, t.rows, t.vocab, req, row));
+  auto rows_of = [&](const void *p, int type, int64_t req, int64_t row) {
+    if (type == MMQ_DT_F32) return Rows(static_cast<const float *>(p), t.vocab, req, t.nreq, row, t.rows);
+    return Rows(static_cast<const uint16_t *>(p), t.vocab, req, t.nreq, row, t.rows);
   };
   auto rows_apart = [&](int64_t req, int64_t row) {  // rows do not lie on one another
     return (t.rows == 1 || row >= t.vocab) && (t.nreq == 1 || req >= (t.rows - 1) * row + t.vocab || (t.rows > 1 && row >= (t.nreq - 1) * req + t.vocab && req >= t.vocab));
   };
-  const Run logits = run(t.logits, t.type, t.logits_req, t.logits_row);
+  const Rows logits = rows_of(t.logits, t.type, t.logits_req, t.logits_row), probs = rows_of(t.probs, t.probs_type, t.probs_req, t.probs_row);
+  const Rows adjusted = rows_of(t.adjusted, t.adjusted_type, t.adjusted_req, t.adjusted_row);
   const bool same = t.adjusted == t.logits && t.adjusted_type == t.type && t.adjusted_req == t.logits_req && t.adjusted_row == t.logits_row;
-  if (t.probs) {
-    const Run probs = run(t.probs, t.probs_type, t.probs_req, t.probs_row);
-    if (!rows_apart(t.probs_req, t.probs_row) || meet(probs, logits)) return MMQ_ERR_ARG;
-    if (t.adjusted && meet(probs, run(t.adjusted, t.adjusted_type, t.adjusted_req, t.adjusted_row))) return MMQ_ERR_ARG;
-  }
-  if (t.adjusted) {
-    if (!rows_apart(t.adjusted_req, t.adjusted_row) || (!same && meet(run(t.adjusted, t.adjusted_type, t.adjusted_req, t.adjusted_row), logits))) return MMQ_ERR_ARG;
-  }
-  const int64_t words = (t.vocab + 31) / 32, width = t.tokens ? t.tokens_width : 0;
-  auto vector = [&](const auto *p, int64_t n) { return Run(p, p ? n : 0); };
-  const Run read[] = {vector(t.temperature, t.nreq), vector(t.token_lens, t.nreq), vector(t.prompt_lens, t.nreq), vector(t.n_draft, t.nreq),
-                      vector(t.repetition, t.nreq), vector(t.frequency, t.nreq), vector(t.presence, t.nreq), vector(t.bias_start, t.nreq + 1),
-                      vector(t.bias_ids, t.nbias), vector(t.bias_values, t.nbias), vector(t.mask_rows, t.nreq * t.rows),
-                      vector(t.tokens, width ? extent(1, t.nreq, width, 0, t.tokens_stride) : 0),
-                      vector(t.draft, t.rows > 1 ? extent(1, t.nreq, t.rows - 1, 0, t.draft_stride) : 0),
-                      vector(t.mask, t.nmasks ? extent(1, t.nmasks, words, 0, t.mask_stride) : 0)};
-  for (const Run &r : read) {
-    if (t.probs && meet(run(t.probs, t.probs_type, t.probs_req, t.probs_row), r)) return MMQ_ERR_ARG;
-    if (t.adjusted && meet(run(t.adjusted, t.adjusted_type, t.adjusted_req, t.adjusted_row), r)) return MMQ_ERR_ARG;
-  }
+  if (t.probs && (!rows_apart(t.probs_req, t.probs_row) || meet(probs, logits) || meet(probs, adjusted))) return MMQ_ERR_ARG;
+  if (t.adjusted && (!rows_apart(t.adjusted_req, t.adjusted_row) || (!same && meet(adjusted, logits)))) return MMQ_ERR_ARG;
+  auto vector = [](const auto *p, int64_t n) { return Rows(p, n, 0, 1); };
+  const Rows read[] = {vector(t.temperature, t.nreq), vector(t.token_lens, t.nreq), vector(t.prompt_lens, t.nreq), vector(t.n_draft, t.nreq),
+                       vector(t.repetition, t.nreq), vector(t.frequency, t.nreq), vector(t.presence, t.nreq), vector(t.bias_start, t.nreq + 1),
+                       vector(t.bias_ids, t.nbias), vector(t.bias_values, t.nbias), vector(t.mask_rows, t.nreq * t.rows),
+                       Rows(t.tokens, t.tokens_width, t.tokens_stride, t.nreq), Rows(t.draft, t.rows - 1, t.draft_stride, t.nreq),
+                       Rows(t.mask, (t.vocab + 31) / 32, t.mask_stride, t.nmasks)};
+  for (const Rows &r : read)
+    if (meet(probs, r) || meet(adjusted, r)) return MMQ_ERR_ARG;
   mmq::RulesArgs a;
   a.t = t;
   if (!t.tokens) a.t.tokens_width = 0;

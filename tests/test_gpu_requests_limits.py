@@ -122,3 +122,21 @@ def test_calls_of_two_sizes_at_the_same_time(mmq, what):  # noqa: F811
         x.join()
     torch.cuda.synchronize()
     assert all(len(c) == 3000 for c in codes) and {x for c in codes for x in c} == {0}
+
+
+# ---------------------------------------------------------------- rows between rows
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_probs_and_adjusted_in_halves_of_one_array(mmq, dtype):  # noqa: F811
+    """Outputs side by side in one array, or beside the logits: the same bits as in arrays of their own with rows that begin
+    alike in 16 bytes of memory."""
+    v = 1504  # (whole pieces of 16 bytes)
+    p = _rules_problem(4, 2, v, dtype, seed=11)
+    want = mmq.mmq_token_probs(**p, probs=torch.empty_like(p["logits"]), adjusted=torch.empty_like(p["logits"]))
+    both = torch.empty((4, 3, 2 * v), dtype=dtype, device="cuda")
+    got = mmq.mmq_token_probs(**p, probs=both[..., v:], adjusted=both[..., :v])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    both[..., :v] = p["logits"]
+    got = mmq.mmq_token_probs(**{**p, "logits": both[..., :v]}, probs=both[..., v:], adjusted=both[..., :v])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with pytest.raises(mmq.MMQError):
+        mmq.mmq_token_probs(**p, probs=both[..., v - 1:-1], adjusted=both[..., :v])
