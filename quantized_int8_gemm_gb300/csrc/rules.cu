@@ -16,9 +16,10 @@ namespace mmq {
 namespace {
 
 constexpr int kMostCtas = 16, kThreads = 256, kWarps = kThreads / 32;
-// Elements of a CTA at the most: a sixteenth of 2^18, or 32 KB of 16 bits; and a
-// few for where the slice begins.
-constexpr int kMostSlice = 16384 + 40;
+// Elements of a CTA at the most, for which the kernel has barriers: a sixteenth of
+// 2^18, or 32 KB of 16 bits.
+constexpr int kMostSlice = 16384;
+static_assert(kMaxVocab <= kMostSlice * kMostCtas, "the largest vocabulary in as many slices");
 constexpr unsigned kAll = 0xffffffffu;
 // Of a listed token's count: it is among the prompt's; it has a bias; the row's mask hides it.
 constexpr uint32_t kMet = 0x80000000u, kBiased = 0x40000000u, kHidden = 0x20000000u;
@@ -408,7 +409,7 @@ template <class T>
 __global__ void __launch_bounds__(kThreads, 4) token_probs_kernel(const __grid_constant__ RulesArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr bool kWide = sizeof(T) == 4;
-  constexpr int kChunks = kMostSlice / (4 * kEach) + 1;
+  constexpr int kChunks = kMostSlice / (4 * kEach) + 1;  // (one more for where the slice begins)
   __shared__ __align__(8) uint64_t s_bars[kChunks], s_told;
   __shared__ uint64_t s_warp[kWarps], s_all[kMostCtas], s_word;
   __shared__ int s_draft[kDrafted];
@@ -725,6 +726,7 @@ cudaError_t launch_token_probs(RulesArgs a, const CallContext &ctx, cudaStream_t
   a.ctas = static_cast<int>(ctas);
   a.by_ctas = FastDiv(a.ctas);
   a.slice = static_cast<int>(((a.t.vocab + ctas - 1) / ctas + 31) / 32 * 32);  // (masks in whole words)
+  if (a.slice > kMostSlice) return cudaErrorNotSupported;  // (the rule above gives none such; the kernel would pass its barriers' end)
   a.by_rows = FastDiv(a.t.rows);
   a.sparse = a.penalties || a.t.bias_start;
   void *scratch = nullptr;
