@@ -1,5 +1,5 @@
 """What differs from request to request in a step, on the GPU, at the limits of its arguments: logits far from 0, calls of
-several threads.  Tolerances are those of tests/test_gpu_requests.py, derived there, unless a test says others."""
+several threads; and all bits of the adapters' inputs.  Tolerances are those of tests/test_gpu_requests.py, derived there, unless a test says others."""
 import ctypes
 import math
 import threading
@@ -46,6 +46,34 @@ def test_probs_of_masked_logits_far_below_zero(mmq, b, k, v, dtype, shift):  # n
     p["bias"] = (_i32([40 * i for i in range(b + 1)]), _i32(ids), _f32(values))
     for temperature in (None, 0.05):
         _check_rules(mmq, _far(p, 0.0, temperature))
+
+
+# ---------------------------------------------------------------- terms of the adapters' operands
+def _terms(x, n):  # the sum of n bf16 terms, each what rounding to nearest leaves of those before
+    left, got = x.clone(), torch.zeros_like(x, dtype=torch.float64)
+    for _ in range(n):
+        term = left.to(BF16).float()
+        got, left = got + term.double(), left - term
+    return got
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("rank", [8, 32, 72])
+@pytest.mark.parametrize("tokens", [5, 700, 3000])  # (the kernels of few tokens, of tiles of 16 and of 64)
+def test_lora_holds_all_bits_of_x(mmq, tokens, rank, dtype):  # noqa: F811
+    """Weights of one 1 a row: out is x's columns, through both products.  Three terms hold an fp32 number's 24 bits, so each
+    product's sum is the number itself, cut off at most at the last bit of its first term, 2^-23 of up to twice the number
+    (2^-22), twice: 2^-21.  Two terms would leave up to 2^-18."""
+    g = torch.Generator(device="cuda").manual_seed(rank)
+    x = torch.randn((tokens, 520), generator=g, device="cuda")
+    a, b = torch.zeros((1, rank, 520), dtype=dtype, device="cuda"), torch.eye(rank, device="cuda").to(dtype)[None].contiguous()
+    columns = torch.arange(rank, device="cuda") * 7
+    a[0, torch.arange(rank, device="cuda"), columns] = 1
+    want = x[:, columns].double()
+    assert torch.equal(_terms(x[:, columns], 3), want)
+    assert ((_terms(x[:, columns], 2) - want).abs() > 2.0 ** -20 * want.abs()).any()
+    got = mmq.mmq_lora(x, torch.zeros((tokens, rank), device="cuda"), a, b, mmq.mmq_lora_plan(_i32([0]), _i32([0, tokens]), tokens, 1))
+    assert ((got.double() - want).abs() <= 2.0 ** -21 * want.abs()).all()
 
 
 # ---------------------------------------------------------------- threads
