@@ -611,9 +611,12 @@ typedef struct mmq_token_rules {
  * temperature not above 0: probability 1 for the largest x (ties: the lowest
  * v).  A row with no token left gets probabilities of 0; a NaN that no mask
  * hides (or, with a temperature, +inf) makes a row's probabilities NaN.
- * Sums are fp32; probs and adjusted are rounded once.  The results of one
- * problem do not change from call to call; a row that begins elsewhere in 16
- * bytes of memory is added up in other groups.
+ * Sums are fp32; probs and adjusted are rounded once.  Exponentials are within
+ * 2^-20, and 2^-23 times the size of their exponent, of themselves;
+ * probabilities below 2^-126 may become 0.  The results of one problem do not
+ * change from call to call; a row that begins elsewhere in 16 bytes of memory,
+ * or is one of another number of rows, is added up in other groups, so that a
+ * request alone and in a batch may differ in the last bits.
  *   Tokens, drafted tokens and biases outside [0, vocab) are left out, a mask
  * row past nmasks is no mask, token_lens past tokens_width, n_draft past
  * rows - 1, bias_start past nbias are cut; all of them are reported by
@@ -681,8 +684,13 @@ typedef struct mmq_lora_args {
  *   Sums are fp32; x and the inner sums enter the tensor cores as three 16-bit
  * terms, which hold their 24 bits.  An x or an inner sum that is not finite
  * (or that the first term rounds to infinity, from 3.39e38 on) makes its row
- * NaN.  The results of one problem do not change from call to call.  Where adapters have more than eight tokens on the average the inner
- * sums are stream-ordered scratch as for mmq_gemm (6 bytes a token and rank).
+ * NaN.  The results of one problem do not change from call to call.
+ *   With g = min(nreq, nadapters + 1) groups of tokens (at least one),
+ * ceil(ntok / g) above 8 and ntok above 341 the inner sums are stream-ordered
+ * scratch as for mmq_gemm: for tiles of 64 tokens (of 16, where ceil(ntok / g)
+ * or ntok * 8 / 304 is at most 32), min(ntok, ntok / tile + g) of them, 192
+ * bytes a token's place up to rank 32, 576 up to 64, else 960.  Other calls
+ * have none.
  * Errors: MMQ_ERR_ARG, MMQ_ERR_ALIGN, MMQ_ERR_TYPE, MMQ_ERR_OOM,
  * MMQ_ERR_UNSUPPORTED, MMQ_ERR_NO_DEVICE, MMQ_ERR_CUDA.
  */

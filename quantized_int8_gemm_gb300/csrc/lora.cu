@@ -259,7 +259,7 @@ __device__ __forceinline__ void subtract(float &x, float &y, float a, float b) {
 // A pair of numbers as three bf16 terms: each is rounded to nearest, so that
 // what is left after it is at most 2^-9 of what it stands for, and after the
 // third nothing of an fp32 number's 24 bits.  (With two terms, 2^-18 off, the
-// outputs were 1.2 to 2.9e-6 from the 64-bit ones; fp32 sums are 2 to 8e-7 off.)
+// outputs were 1.2 to 2.9e-6 from the 64-bit ones; fp32 sums are 2 to 10e-7 off.)
 constexpr int kTerms = 3;
 struct Terms {
   uint32_t w[kTerms];
@@ -508,10 +508,11 @@ __device__ __forceinline__ float4 sum_of(const float (&acc)[2][kEach][4], int j,
 // columns by A, every CTA adds up the eight sums in their order, and each writes
 // an eighth of the output columns.  HBM bound by the adapters with many tiles,
 // latency bound with few.  Up to rank 32 two pieces of A and what the second
-// product needs first are asked for ahead, in 116 registers (one token, 3584 ->
+// product needs first are asked for ahead, in 118 registers (127 with fp16 weights; one token, 3584 ->
 // 4608, rank 16: 8.4 -> 6.4 us); beyond, three CTAs an SM hide more than reads
 // ahead in two do (96 tokens of 50 adapters of rank 64: 22.1 against 24.6 us), and
-// B comes to L2 during the first product.
+// B comes to L2 during the first product.  The 80 registers of three CTAs an SM do not
+// hold everything: 68 bytes a thread are spilled (36 with fp16 weights).
 constexpr int kFew = 8;  // tokens
 template <class W, int kPass>  // ranks whose sums a warp holds at once
 __global__ void __launch_bounds__(kThreads, kPass == 32 ? 2 : 3) __cluster_dims__(kCtas, 1, 1) lora_few_kernel(const __grid_constant__ LoraArgs a) {
@@ -691,7 +692,8 @@ __global__ void __launch_bounds__(kThreads, kPass == 32 ? 2 : 3) __cluster_dims_
 //
 // The first product: a cluster takes a tile, each CTA an eighth of x's columns,
 // through stages of shared memory; the sums are joined through the cluster's
-// shared memory and left as terms.
+// shared memory and left as terms.  (Tiles of 64 with fp32 x up to rank 32 spill 16 bytes a
+// thread into 80 registers, 32 with fp16 weights.)
 template <class W, int kTile, bool kFp32, int kPass>
 __global__ void __launch_bounds__(kThreads, kPass == 32 ? 3 : 2) __cluster_dims__(kCtas, 1, 1) lora_down_kernel(const __grid_constant__ LoraArgs a) {
   using S = Shape<kTile>;
@@ -844,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, kPass == 32 ? 3 : 2) __cluster_dims_
 // Weights of up to 32 ranks in bf16 leave registers for four CTAs an SM, which hide
 // more of each other than longer stretches of a row save (64 tiles of 18944 columns,
 // both projections: four CTAs with 256 columns 234 us, 512 240, 768 259; two with
-// 512 250, 768 239, 1024 247; three with 512 241).
+// 512 250, 768 239, 1024 247; three with 512 241); 4 bytes a thread are spilled for it.
 template <class W>
 __host__ __device__ constexpr int up_ctas(int pitch) { return pitch == 16 && Weights8<W>::kParts == 1 ? 4 : 2; }
 __host__ __device__ constexpr int y_pieces(int ctas) { return ctas == 4 ? 2 : 3; }  // of y, on their way or in use

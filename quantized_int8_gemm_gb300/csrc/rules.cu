@@ -98,7 +98,7 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
 // bulk copies, the elements in front of and behind them by threads.  Element e
 // comes to stage[place + e], place being that of the slice in 16 bytes of memory.
 constexpr int kFours = 4;                   // fours of a thread at once
-constexpr int kEach = kFours * kThreads;    // and of a copy, which is waited for by itself
+constexpr int kEach = kFours * kThreads;    // and of a copy (each has a barrier; all are waited for before the first four)
 template <class T>
 struct Slice {
   static constexpr int kPiece = 16 / sizeof(T);
@@ -716,10 +716,11 @@ cudaError_t launch_with(const RulesArgs &a, size_t smem, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_token_probs(RulesArgs a, const CallContext &ctx, cudaStream_t s) {
-  // CTAs of a row: slices of up to 50 KB (960 rows of 100277
-  // in fp32: 8 CTAs of a row 189 us, 9 196, 10 201, 17 277); with 32 KB of 16-bit logits (120 rows
-  // of 128256: 8 CTAs 62 us, 5 77, 6 72, 10 64, 16 70); with few rows more, as long as
-  // all run at once and have 2048 elements or more
+  // CTAs of a row: slices of up to 50 KB in fp32 (960 rows of 100277: 8 CTAs of a row 189 us,
+  // 7 208, 9 196, 10 200, 12 225, 16 275) and of up to 32 KB, the most that the kernel takes,
+  // in 16 bits (120 rows of 128256: 8 CTAs 56.3 us, 9 56.8, 10 58.2, 12 58.8, 16 61.8); with few
+  // rows more, as long as all run at once and have 2048 elements or more (one row of 32000:
+  // 2 CTAs 11.2 us, 4 9.2, 8 8.4, 12 8.3, 15 8.5, 16 8.4)
   const int64_t rows = a.t.nreq * a.t.rows, size = a.t.type == MMQ_DT_F32 ? 4 : 2, most = (size == 4 ? 50 : 32) * 1024;
   const int64_t fit = (a.t.vocab * size + most - 1) / most, few = std::min(4 * 152 / rows, a.t.vocab / 2048);
   const int64_t ctas = std::min<int64_t>(kMostCtas, std::max<int64_t>({fit, few, 1}));
